@@ -1,0 +1,607 @@
+"""The 4-bit key/value cache operators as a user calls them, in plain form and
+through this package, over the sizes they are used at.
+
+  insert   new keys and values quantised into the paged 4-bit cache, and read
+           back as the values they stand for (kv4_insert, kv4_gather)
+  attend   decode attention over the cache, every key (kv4_attention)
+  select   decode attention over the columns an indexer chose
+           (kv4_attention_topk)
+  evict    the tokens a budget keeps, by accumulated attention weight, moved
+           to fresh pages (kv_evict_select, kv_compact)
+
+``own`` chooses the side ``run`` takes: False computes in elementary torch
+operations in 32 bits, rounded once at the end; True calls the package.
+``exact`` computes the definitions in 64 bits, apart from both.
+
+Cache layout (what kv4_insert writes): ``cache`` [num_blocks, Hkv, block, D]
+bytes, a token's record being D/2 bytes of packed E2M1 keys, then D/2 bytes of
+packed E2M1 values; ``scales`` [num_blocks, Hkv, block, D/16] E8M0 bytes, D/32
+of the key's blocks of 32 elements, then D/32 of the value's.  Element order
+within a record: key bytes are [t = 4][g = D/32][4 bytes], the eight elements
+32 g + 8 t ...; value bytes are [r = 8][g = D/32][2 bytes], the four elements
+32 g + 4 r ...; the lower element of a byte is its low nibble.
+"""
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda"
+BLOCK = 32                     # elements that share a scale
+LOG2E = 1.4426950408889634
+
+# ------------------------------------------------------------------- the cases
+
+# 64 query heads, D = 128, 64-token blocks, 2048 selected keys, 64 requests of
+# two tokens with context lengths log-uniform in [4096, 131072]: the paged
+# decode workload of this package's benchmark.
+
+
+def listed():
+    return [
+        # the keys and values of one decode step: 64 requests of two tokens
+        dict(name="insert_step", op="insert", T=128, Hkv=8, D=128, block=64),
+        # a whole prompt's keys and values after its prefill
+        dict(name="insert_prompt", op="insert", T=32768, Hkv=8, D=128, block=64),
+        # one request with a short context: what one call costs at least
+        dict(name="attend_one_short", op="attend", B=1, nn=1, lo=777, hi=777, Hq=64, Hkv=8,
+             D=128, block=64, weights=False),
+        # one request with a long context: few rows, one long axis to split
+        dict(name="attend_one_long", op="attend", B=1, nn=1, lo=131071, hi=131071, Hq=64, Hkv=8,
+             D=128, block=64, weights=False),
+        # a full decode batch with two tokens a request, ragged contexts
+        dict(name="attend_batch", op="attend", B=64, nn=2, lo=4096, hi=131072, Hq=64, Hkv=8,
+             D=128, block=64, weights=False),
+        # all query heads on one key/value head
+        dict(name="attend_shared_head", op="attend", B=64, nn=1, lo=1024, hi=16384, Hq=64, Hkv=1,
+             D=128, block=64, weights=False),
+        # the attention weight of every key accumulated for eviction
+        dict(name="attend_weights", op="attend", B=16, nn=1, lo=8192, hi=32768, Hq=32, Hkv=8,
+             D=128, block=64, weights=True),
+        # one key/value head a query head, D = 64, small blocks, lengths from
+        # one token up
+        dict(name="attend_heads_d64", op="attend", B=32, nn=1, lo=1, hi=4096, Hq=16, Hkv=16,
+             D=64, block=16, weights=False),
+        # one request's 2048 selected keys of a long context
+        dict(name="select_one", op="select", B=1, nn=1, lo=131072, hi=131072, k=2048, Hq=64,
+             Hkv=8, D=128, block=64, weights=False),
+        # the decode batch on the indexer's selection, with each selected
+        # key's weight
+        dict(name="select_batch", op="select", B=64, nn=2, lo=4096, hi=131072, k=2048, Hq=64,
+             Hkv=8, D=128, block=64, weights=True),
+        # one request cut down to an eighth
+        dict(name="evict_one", op="evict", B=1, lo=32768, hi=32768, budget=4096, sink=4,
+             recent=512, Hkv=8, D=128, block=64),
+        # a batch brought back to 4096 tokens a request
+        dict(name="evict_batch", op="evict", B=64, lo=4096, hi=131072, budget=4096, sink=4,
+             recent=512, Hkv=8, D=128, block=64),
+    ]
+
+
+def _logu(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["insert", "attend", "attend", "select", "select", "evict"])
+    D = rng.choice([64, 128, 128])
+    block = rng.choice([8, 16, 32, 64, 128])
+    if op == "insert":
+        return dict(op=op, T=_logu(rng, 1, 32768), Hkv=_logu(rng, 1, 8), D=D, block=block)
+    if op == "evict":
+        B = _logu(rng, 1, 64)
+        hi = _logu(rng, 64, 131072)
+        lo = _logu(rng, 1, hi)
+        budget = _logu(rng, 16, 4096)
+        sink = rng.randrange(0, min(8, budget // 2) + 1)
+        return dict(op=op, B=B, lo=lo, hi=hi, budget=budget, sink=sink,
+                    recent=rng.randrange(0, budget // 2), Hkv=_logu(rng, 1, 8), D=D, block=block)
+    Hkv = _logu(rng, 1, 16)
+    G = rng.choice([1, 2, 3, 4, 5, 7, 8, 8, 12, 16])
+    if rng.random() < 0.2:
+        Hkv, G = 1, rng.choice([24, 32, 64])
+    nn = rng.choice([1, 1, 2, 3, 4])
+    if G * nn > 64 or Hkv * G > 64:
+        nn, G = 1, max(1, min(G, 64 // Hkv))
+    B = _logu(rng, 1, 64)
+    hi = _logu(rng, 64, 131072)
+    if op == "attend":                                     # no more than attend_batch reads
+        hi = max(64, min(hi, (64 << 17) // (B * max(1, Hkv * nn // 8))))
+    lo = _logu(rng, 1, hi)
+    case = dict(op=op, B=B, nn=nn, lo=lo, hi=hi, Hq=Hkv * G, Hkv=Hkv, D=D, block=block,
+                weights=rng.random() < 0.4 and B * hi * Hkv * G * nn < 1 << 29)
+    if op == "select":
+        case["k"] = _logu(rng, 1, 2048)
+        case["weights"] = rng.random() < 0.5
+    return case
+
+
+def _lens(case):
+    """Context lengths spread evenly over the logarithm of [lo, hi]."""
+    B, lo, hi = case["B"], case["lo"], case["hi"]
+    return [int(round(lo * (hi / lo) ** ((i + 0.5) / B))) for i in range(B)]
+
+
+def work(case):
+    D, Hkv = case["D"], case["Hkv"]
+    rec = D + D // 16                                      # bytes of a token and head
+    if case["op"] == "insert":
+        n = case["T"] * Hkv
+        # read k and v, write the records; read them, write k and v
+        return dict(bytes=2 * n * (4 * D + rec) + 16 * case["T"], flops=8 * n * D)
+    lens = _lens(case)
+    if case["op"] == "evict":
+        keep = [min(case["budget"], L) for L in lens]
+        row = Hkv * rec + 2 * D                            # and the indexer's bf16 key
+        width = -(-max(lens) // case["block"]) * case["block"]
+        return dict(bytes=sum(4 * L for L in lens) + 4 * case["B"] * width
+                    + sum(k * (2 * row + 4) for k in keep), flops=sum(lens))
+    nn, Hq = case["nn"], case["Hq"]
+    rows = case["B"] * nn
+    io = rows * Hq * (4 * D + 4)                           # q, the output and its lse
+    if case["op"] == "attend":
+        keys = sum(lens)
+        seen = sum(max(L - nn + j + 1, 0) for L in lens for j in range(nn))
+        w = 8 * keys if case["weights"] else 0
+        return dict(bytes=keys * Hkv * rec + io + w, flops=4 * seen * Hq * D)
+    keys = sum(min(case["k"], max(L - nn + j + 1, 0)) for L in lens for j in range(nn))
+    w = 4 * rows * case["k"] if case["weights"] else 0
+    return dict(bytes=keys * (Hkv * rec + 4) + io + w, flops=4 * keys * Hq * D)
+
+
+# ------------------------------------------------------------------ the format
+
+
+def _pow2(e):
+    """2^e in float32 for whole e in [-126, 127], exactly (by its bits)."""
+    return ((e.int() + 127) << 23).view(torch.float32)
+
+
+def _quantise(x):
+    """[..., D] float32 -> E2M1 codes [..., D] and E8M0 codes [..., D/32].
+
+    A block's scale is the smallest power of two s, no less than 2^-126, with
+    max|x| <= 6 s (1 for a block of zeros); elements go to the nearest E2M1
+    value, ties to the even code; a block with a NaN or an infinity is all NaN
+    (scale code 255).
+    """
+    x = x.reshape(*x.shape[:-1], -1, BLOCK)
+    amax = x.abs().amax(-1)
+    bad = ~torch.isfinite(amax)
+    m, e = torch.frexp(torch.where(bad, 1.0, amax))
+    e = torch.where(m <= 0.75, e - 3, e - 2)               # 6 * 2^e = 0.75 * 2^(e + 3)
+    e = torch.where(amax > 0, e, 0).clamp_(min=-126)
+    y = x * _pow2(-e)[..., None]
+    a = y.abs()
+    code = (y.signbit().to(torch.uint8) << 3)
+    for i, edge in enumerate((0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0)):
+        code += (a >= edge) if i & 1 else (a > edge)
+    code = torch.where(bad[..., None], 0, code)
+    scale = torch.where(bad, 255, e + 127).to(torch.uint8)
+    return code.flatten(-2), scale
+
+
+def _pack(kc, vc):
+    """Key and value codes [..., D] -> records [..., D] bytes."""
+    lead, D = kc.shape[:-1], kc.shape[-1]
+    G = D // BLOCK
+    kb = (kc[..., 0::2] | (kc[..., 1::2] << 4)).reshape(*lead, G, 4, 4)
+    vb = (vc[..., 0::2] | (vc[..., 1::2] << 4)).reshape(*lead, G, 8, 2)
+    return torch.cat([kb.transpose(-3, -2).reshape(*lead, D // 2),
+                      vb.transpose(-3, -2).reshape(*lead, D // 2)], -1)
+
+
+def _unpack(rec, sc):
+    """Records and scales of [..., D] bytes -> keys and values [..., D] float32."""
+    lead, D = rec.shape[:-1], rec.shape[-1]
+    G = D // BLOCK
+    kb = rec[..., :D // 2].reshape(*lead, 4, G, 4).transpose(-3, -2)
+    vb = rec[..., D // 2:].reshape(*lead, 8, G, 2).transpose(-3, -2)
+    out = []
+    for b, s in ((kb, sc[..., :G]), (vb, sc[..., G:])):
+        b = b.reshape(*lead, G, 16)
+        c = torch.stack([b & 15, b >> 4], -1).reshape(*lead, G, BLOCK)
+        m = (c & 7).float()
+        x = torch.where(m < 4, m * 0.5, torch.where(m < 6, m - 2, 2 * m - 8))
+        x = torch.where(c > 7, -x, x)
+        f = torch.where((s == 0) | (s == 255), torch.nan, _pow2(s.int() - 127))
+        out.append((x * f[..., None]).reshape(*lead, D))
+    return out
+
+
+# ---------------------------------------------------------------------- inputs
+
+
+def _gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def _randn(g, *shape):
+    return torch.randn(*shape, generator=g, device=DEV)
+
+
+def _pages(g, lens, block, spare=0):
+    """A block table whose blocks lie in random order, and the block count."""
+    n = [-(-L // block) for L in lens]
+    total = sum(n)
+    perm = torch.randperm(max(total, 1), generator=g, device=DEV, dtype=torch.int32)
+    table = torch.zeros(len(lens), max(max(n), 1), dtype=torch.int32, device=DEV)
+    at = 0
+    for b, c in enumerate(n):
+        table[b, :c] = perm[at:at + c]
+        at += c
+    return table, max(total, 1) + spare
+
+
+def _fill_cache(g, nblk, Hkv, block, D):
+    """A cache of normal keys and values, whose heads and blocks differ in size."""
+    cache = torch.empty(nblk, Hkv, block, D, dtype=torch.uint8, device=DEV)
+    scales = torch.empty(nblk, Hkv, block, D // 16, dtype=torch.uint8, device=DEV)
+    step = max(1, (1 << 27) // (Hkv * block * D))
+    kmag = torch.exp2(0.5 * _randn(g, Hkv, 1, D))
+    vmag = torch.exp2(1.0 * _randn(g, Hkv, 1, D))
+    for at in range(0, nblk, step):
+        n = min(step, nblk - at)
+        kc, ks = _quantise(_randn(g, n, Hkv, block, D) * kmag)
+        vc, vs = _quantise(_randn(g, n, Hkv, block, D) * vmag)
+        cache[at:at + n] = _pack(kc, vc)
+        scales[at:at + n] = torch.cat([ks, vs], -1)
+    return cache, scales
+
+
+def _host_perm(seed, n):
+    return torch.randperm(n, generator=torch.Generator().manual_seed(seed)).tolist()
+
+
+def prepare(case, seed):
+    g = _gen(seed)
+    D, Hkv, block = case["D"], case["Hkv"], case["block"]
+    s = dict(case)
+    if own:
+        from top_selection_dsa_gb300 import api
+        s["api"] = api
+    if case["op"] == "insert":
+        T = case["T"]
+        # keys and values as one projection writes them, token by token
+        kv = (_randn(g, T, 2 * Hkv, D) * torch.exp2(_randn(g, T, 2 * Hkv, 1))).bfloat16()
+        s["k"], s["v"] = kv[:, :Hkv], kv[:, Hkv:]
+        nblk = -(-T // block) * 2
+        s["slots"] = torch.randperm(nblk * block, generator=g, device=DEV)[:T].contiguous()
+        s["cache"] = torch.zeros(nblk, Hkv, block, D, dtype=torch.uint8, device=DEV)
+        s["scales"] = torch.zeros(nblk, Hkv, block, D // 16, dtype=torch.uint8, device=DEV)
+        if own:
+            s["out"] = [torch.empty(T, Hkv, D, dtype=torch.bfloat16, device=DEV)
+                        for _ in range(2)]
+        return s
+    lens = _lens(case)
+    lens = [lens[i] for i in _host_perm(seed, len(lens))]
+    B = case["B"]
+    s["lens_host"] = lens
+    s["lens"] = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    if case["op"] == "evict":
+        kept = [min(case["budget"], L) for L in lens]
+        new = [-(-k // block) for k in kept]
+        s["table"], nsrc = _pages(g, lens, block)
+        nblk = nsrc + sum(new)
+        nt = torch.zeros(B, max(new), dtype=torch.int32, device=DEV)
+        at = nsrc
+        for b, c in enumerate(new):
+            nt[b, :c] = torch.arange(at, at + c, dtype=torch.int32, device=DEV)
+            at += c
+        s["new_table"], s["nsrc"], s["kept_host"] = nt, nsrc, kept
+        s["cache"] = torch.randint(0, 256, (nblk, Hkv, block, D), generator=g, device=DEV,
+                                   dtype=torch.uint8)
+        s["scales"] = torch.randint(110, 135, (nblk, Hkv, block, D // 16), generator=g,
+                                    device=DEV, dtype=torch.uint8)
+        s["index_k"] = torch.randint(0, 30000, (nblk, block, D), generator=g, device=DEV,
+                                     dtype=torch.int16).view(torch.bfloat16)
+        for t in (s["cache"], s["scales"], s["index_k"]):
+            t[nsrc:] = 0
+        # accumulated weight: long-tailed, with ties
+        width = s["table"].shape[1] * block
+        w = torch.exp2(3 * _randn(g, B, width))
+        w = torch.where(torch.rand(B, width, generator=g, device=DEV) < 0.05, 0.0, w)
+        inside = torch.arange(width, device=DEV) < s["lens"][:, None]
+        s["weights"] = torch.where(inside, w, 0.0)
+        if own:
+            s["ws"] = torch.empty(max(s["api"].kv_evict_workspace_bytes(
+                B, width, case["budget"]), 256), dtype=torch.uint8, device=DEV)
+            s["moved_weights"] = torch.empty_like(s["weights"])
+        return s
+    nn, Hq = case["nn"], case["Hq"]
+    s["table"], nblk = _pages(g, lens, block)
+    s["cache"], s["scales"] = _fill_cache(g, nblk, Hkv, block, D)
+    s["q"] = (1.5 * _randn(g, B * nn, Hq, D)).bfloat16()
+    s["scale"] = D ** -0.5
+    width = s["table"].shape[1] * block
+    if case["op"] == "select":
+        k = case["k"]
+        s["sel"] = torch.full((B * nn, k), -1, dtype=torch.int32, device=DEV)
+        for b, L in enumerate(lens):
+            for j in range(nn):
+                n = max(L - nn + j + 1, 0)
+                if n == 0:
+                    continue
+                c = torch.randperm(n, generator=g, device=DEV)[:k].sort().values
+                s["sel"][b * nn + j, :c.numel()] = c.int()
+    elif case["weights"]:
+        s["weights_in"] = torch.rand(B, width, generator=g, device=DEV)
+    if own:
+        s["out"] = torch.empty(B * nn, Hq, D, dtype=torch.bfloat16, device=DEV)
+        s["lse"] = torch.empty(B * nn, Hq, dtype=torch.float32, device=DEV)
+        cols = case["k"] if case["op"] == "select" else width
+        s["ws"] = torch.empty(max(s["api"].kv4_attention_workspace_bytes(
+            B, nn, Hq, Hkv, D, cols, selected=case["op"] == "select",
+            weights=case["weights"]), 256), dtype=torch.uint8, device=DEV)
+        if case["op"] == "select" and case["weights"]:
+            s["sel_weights"] = torch.empty(B * nn, case["k"], dtype=torch.float32, device=DEV)
+    return s
+
+
+# ------------------------------------------------------------------- one pass
+
+
+def run(state):
+    return (_run_own if own else _run_plain)(state)
+
+
+def _run_own(s):
+    api = s["api"]
+    if s["op"] == "insert":
+        api.kv4_insert(s["k"], s["v"], s["slots"], s["cache"], s["scales"])
+        k, v = api.kv4_gather(s["cache"], s["scales"], s["slots"], k=s["out"][0], v=s["out"][1])
+        return dict(k=k, v=v)
+    if s["op"] == "evict":
+        keep, lens = api.kv_evict_select(s["weights"], s["lens"], s["budget"], sink=s["sink"],
+                                         recent=s["recent"], workspace=s["ws"])
+        api.kv_compact([s["cache"], s["scales"], s["index_k"]], keep, s["lens"], s["table"],
+                       s["new_table"], key_weights=s["weights"],
+                       key_weights_out=s["moved_weights"])
+        n = s["nsrc"]
+        return dict(keep=keep, lens=lens, cache=s["cache"][n:], scales=s["scales"][n:],
+                    index_k=s["index_k"][n:], weights=s["moved_weights"])
+    args = (s["q"], s["cache"], s["scales"], s["table"], s["lens"])
+    opts = dict(next_n=s["nn"], softmax_scale=s["scale"], out=s["out"], lse=s["lse"],
+                workspace=s["ws"])
+    if s["op"] == "attend":
+        if not s["weights"]:
+            out, lse = api.kv4_attention(*args, **opts)
+            return dict(out=out, lse=lse)
+        w = s["weights_in"].clone()
+        out, lse = api.kv4_attention(*args, key_weights=w, **opts)
+        return dict(out=out, lse=lse, weights=w)
+    if not s["weights"]:
+        out, lse = api.kv4_attention_topk(*args, s["sel"], **opts)
+        return dict(out=out, lse=lse)
+    out, lse = api.kv4_attention_topk(*args, s["sel"], sel_weights=s["sel_weights"], **opts)
+    return dict(out=out, lse=lse, weights=s["sel_weights"])
+
+
+def _softmax_pv(S, V):
+    """Logits [h, g, n] and values [n, h, D] -> output, natural-log lse, weights."""
+    m = S.amax(-1, keepdim=True)
+    m = torch.where(m == -torch.inf, 0.0, m)
+    p = torch.exp(S - m)
+    l = p.sum(-1, keepdim=True)
+    o = torch.matmul(p, V.transpose(0, 1)) / torch.where(l == 0, 1.0, l)
+    return o, (m + torch.log(l)).squeeze(-1), p / torch.where(l == 0, 1.0, l)
+
+
+def _run_plain(s):
+    D, Hkv, block = s["D"], s["Hkv"], s["block"]
+    if s["op"] == "insert":
+        kc, ks = _quantise(s["k"].float())
+        vc, vs = _quantise(s["v"].float())
+        blk, at = s["slots"] // block, s["slots"] % block
+        s["cache"][blk, :, at] = _pack(kc, vc)
+        s["scales"][blk, :, at] = torch.cat([ks, vs], -1)
+        k, v = _unpack(s["cache"][blk, :, at], s["scales"][blk, :, at])
+        return dict(k=k.bfloat16(), v=v.bfloat16())
+    if s["op"] == "evict":
+        return _evict_plain(s)
+    nn, Hq = s["nn"], s["Hq"]
+    G = Hq // Hkv
+    B = s["B"]
+    out = torch.zeros(B * nn, Hq, D, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((B * nn, Hq), -torch.inf, device=DEV)
+    weights = None
+    if s["weights"]:
+        weights = s["weights_in"].clone() if s["op"] == "attend" else \
+            torch.zeros(B * nn, s["k"], device=DEV)
+    for b, L in enumerate(s["lens_host"]):
+        if s["op"] == "attend":
+            if L == 0:
+                continue
+            blocks = s["table"][b, :-(-L // block)].long()
+            rec = s["cache"][blocks].transpose(1, 2).reshape(-1, Hkv, D)[:L]
+            sc = s["scales"][blocks].transpose(1, 2).reshape(-1, Hkv, D // 16)[:L]
+            K, V = _unpack(rec, sc)
+            q = s["q"][b * nn:(b + 1) * nn].float().reshape(nn, Hkv, G, D)
+            q = q.transpose(0, 1).reshape(Hkv, nn * G, D)
+            S = torch.matmul(q, K.permute(1, 2, 0)) * s["scale"]
+            if nn > 1:
+                seen = L - nn + 1 + torch.arange(nn, device=DEV).repeat_interleave(G)
+                S.masked_fill_(torch.arange(L, device=DEV) >= seen[:, None], -torch.inf)
+            o, ls, p = _softmax_pv(S, V)
+            o = o.reshape(Hkv, nn, G, D).transpose(0, 1).reshape(nn, Hq, D)
+            out[b * nn:(b + 1) * nn] = o.bfloat16()
+            lse[b * nn:(b + 1) * nn] = ls.reshape(Hkv, nn, G).transpose(0, 1).reshape(nn, Hq)
+            if weights is not None:
+                weights[b, :L] += p.sum((0, 1))
+            continue
+        idx = s["sel"][b * nn:(b + 1) * nn].long()
+        pos = idx.clamp(min=0)
+        blk, at = s["table"][b].long()[pos // block], pos % block
+        for j in range(nn):
+            r = b * nn + j
+            K, V = _unpack(s["cache"][blk[j], :, at[j]], s["scales"][blk[j], :, at[j]])
+            q = s["q"][r].float().reshape(Hkv, G, D)
+            S = torch.matmul(q, K.permute(1, 2, 0)) * s["scale"]
+            S.masked_fill_(idx[j] < 0, -torch.inf)
+            o, ls, p = _softmax_pv(S, torch.where(idx[j][:, None, None] < 0, 0.0, V))
+            out[r], lse[r] = o.reshape(Hq, D).bfloat16(), ls.reshape(Hq)
+            if weights is not None:
+                weights[r] = p.sum((0, 1))
+    res = dict(out=out, lse=lse)
+    if weights is not None:
+        res["weights"] = weights
+    return res
+
+
+def _evict_plain(s):
+    B, block, budget = s["B"], s["block"], s["budget"]
+    w = s["weights"]
+    keep = torch.full((B, budget), -1, dtype=torch.int32, device=DEV)
+    moved = torch.zeros_like(w)
+    for b, L in enumerate(s["lens_host"]):
+        lo = min(s["sink"], L)
+        hi = max(lo, L - s["recent"])
+        room = budget - s["sink"] - s["recent"]
+        mid = torch.sort(w[b, lo:hi], descending=True, stable=True).indices[:room] + lo
+        mid = torch.sort(mid).values
+        pos = torch.cat([torch.arange(lo, device=DEV), mid, torch.arange(hi, L, device=DEV)])
+        n = pos.numel()
+        keep[b, :n] = pos.int()
+        moved[b, :n] = w[b, pos]
+        src, dst = s["table"][b].long()[pos // block], torch.arange(n, device=DEV)
+        new = s["new_table"][b].long()[dst // block]
+        for t in (s["cache"], s["scales"]):
+            t[new, :, dst % block] = t[src, :, pos % block]
+        s["index_k"][new, dst % block] = s["index_k"][src, pos % block]
+    n = s["nsrc"]
+    return dict(keep=keep, lens=(keep >= 0).sum(1).int(), cache=s["cache"][n:],
+                scales=s["scales"][n:], index_k=s["index_k"][n:], weights=moved)
+
+
+# ------------------------------------------------------------------ definitions
+
+_E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+def _two64(e):
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
+def _decode64(rec, sc, key):
+    """The keys (or values) of records [n, D], one head, by the format's table."""
+    n, D = rec.shape
+    G = D // BLOCK
+    table = torch.tensor([v for v in _E2M1] + [-v for v in _E2M1], dtype=torch.float64,
+                         device=rec.device)
+    e = torch.arange(D, device=rec.device)
+    g = e // 32
+    if key:
+        t = e % 32 // 8
+        byte = (t * G + g) * 4 + e % 8 // 2
+        s = sc[:, :G]
+    else:
+        r = e % 32 // 4
+        byte = D // 2 + (r * G + g) * 2 + e % 4 // 2
+        s = sc[:, G:]
+    nib = (rec[:, byte].int() >> (4 * (e % 2)).int()) & 15
+    return table[nib.long()] * _two64(s.int() - 127)[:, g]
+
+
+def exact(case, seed):
+    global own
+    was, own = own, False
+    try:
+        s = prepare(case, seed)
+    finally:
+        own = was
+    if case["op"] == "insert":
+        return dict(k=_nearest64(s["k"]), v=_nearest64(s["v"]))
+    if case["op"] == "evict":
+        return _evict64(s)
+    nn, Hq, Hkv, D, block = s["nn"], s["Hq"], s["Hkv"], s["D"], s["block"]
+    if sum(s["lens_host"]) * Hq * nn * D > 1 << 40:
+        return None
+    G = Hq // Hkv
+    B = s["B"]
+    out = torch.zeros(B * nn, Hq, D, dtype=torch.float64, device=DEV)
+    lse = torch.full((B * nn, Hq), -torch.inf, dtype=torch.float64, device=DEV)
+    weights = None
+    if s["weights"]:
+        weights = s["weights_in"].double() if s["op"] == "attend" else \
+            torch.zeros(B * nn, s["k"], dtype=torch.float64, device=DEV)
+    for b, L in enumerate(s["lens_host"]):
+        for h in range(Hkv):
+            base = torch.arange(L, device=DEV)
+            row0 = b * nn
+            if s["op"] == "attend":
+                sets = [(base, range(nn))]
+            else:
+                sets = [(s["sel"][row0 + j][s["sel"][row0 + j] >= 0].long(), [j])
+                        for j in range(nn)]
+            for pos, js in sets:
+                if pos.numel() == 0:
+                    continue
+                page, at = s["table"][b].long()[pos // block], pos % block
+                rec, sc = s["cache"][page, h, at], s["scales"][page, h, at]
+                K, V = _decode64(rec, sc, True), _decode64(rec, sc, False)
+                for j in js:
+                    n = L - nn + j + 1
+                    ok = pos < n
+                    if not bool(ok.any()):
+                        continue
+                    q = s["q"][row0 + j, h * G:(h + 1) * G].double()
+                    S = (q @ K[ok].T) * s["scale"]
+                    z = torch.logsumexp(S, -1, keepdim=True)
+                    p = torch.exp(S - z)
+                    out[row0 + j, h * G:(h + 1) * G] = p @ V[ok]
+                    lse[row0 + j, h * G:(h + 1) * G] = z[:, 0]
+                    if weights is not None and s["op"] == "attend":
+                        weights[b, :L][ok] += p.sum(0)
+                    elif weights is not None:
+                        weights[row0 + j, :pos.numel()] += p.sum(0)
+    res = dict(out=out, lse=lse)
+    if weights is not None:
+        res["weights"] = weights
+    return res
+
+
+def _nearest64(x):
+    """Every element as the value its block's format gives it, by distances."""
+    shape = x.shape
+    x = x.double().reshape(-1, BLOCK)
+    grid = torch.tensor(_E2M1, dtype=torch.float64, device=x.device)
+    amax = x.abs().amax(1)
+    e = torch.full_like(amax, -126)
+    for step in (128, 64, 32, 16, 8, 4, 2, 1):             # the largest e with 6 * 2^e < amax
+        up = e + step
+        e = torch.where(6 * _two64(up) < amax, up, e)
+    e = torch.where(6 * _two64(e) < amax, e + 1, e)
+    e = torch.where(amax > 0, e, 0)
+    s = _two64(e)[:, None]
+    y = torch.empty_like(x)
+    step = 1 << 20
+    for at in range(0, x.shape[0], step):
+        a = x[at:at + step].abs() / s[at:at + step]
+        d = (a[..., None] - grid).abs()
+        near = d.amin(-1, keepdim=True)
+        tie = d == near
+        odd = torch.arange(8, device=x.device) % 2
+        pick = torch.where(tie, odd, 2).argmin(-1)
+        y[at:at + step] = grid[pick]
+    return (torch.copysign(y, x) * s).reshape(shape)
+
+
+def _evict64(s):
+    """Kept positions and weights by a full sort on the host; bytes only move."""
+    B, budget = s["B"], s["budget"]
+    w = s["weights"].double().cpu()
+    keep = torch.full((B, budget), -1, dtype=torch.int32)
+    moved = torch.zeros_like(w)
+    lens = []
+    for b, L in enumerate(s["lens_host"]):
+        row = w[b, :L].tolist()
+        lo, hi = min(s["sink"], L), max(min(s["sink"], L), L - s["recent"])
+        best = sorted(range(lo, hi), key=lambda i: (-row[i], i))
+        best = best[:budget - s["sink"] - s["recent"]]
+        pos = sorted(list(range(lo)) + best + list(range(hi, L)))
+        keep[b, :len(pos)] = torch.tensor(pos, dtype=torch.int32)
+        moved[b, :len(pos)] = w[b, pos]
+        lens.append(len(pos))
+    return dict(keep=keep.to(DEV), lens=torch.tensor(lens, dtype=torch.int32, device=DEV),
+                cache=None, scales=None, index_k=None, weights=moved.to(DEV))
