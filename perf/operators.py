@@ -356,7 +356,7 @@ def _run_own(s):
         keep, lens = api.kv_evict_select(s["weights"], s["lens"], s["budget"], sink=s["sink"],
                                          recent=s["recent"], workspace=s["ws"])
         api.kv_compact([s["cache"], s["scales"], s["index_k"]], keep, s["lens"], s["table"],
-                       s["new_table"], key_weights=s["weights"],
+                       s["new_table"], new_lens=lens, key_weights=s["weights"],
                        key_weights_out=s["moved_weights"])
         n = s["nsrc"]
         return dict(keep=keep, lens=lens, cache=s["cache"][n:], scales=s["scales"][n:],
