@@ -447,6 +447,182 @@ dsa_status_t dsa_k_norm_quant_insert(const void* k, const float* ln_weight, cons
                                      int num_blocks, int block_size, dsa_stream_t stream);
 
 /*
+ * --------------------------------------------------------------------------
+ * The 4-bit key/value cache: what the attention over the selected columns
+ * reads.  Keys and values are MXFP4 (the element format of
+ * dsa_indexer_logits_mxfp4: E2M1 codes, one E8M0 scale per 32 consecutive
+ * elements of a head's row), paged like the indexer's key cache.
+ *
+ *   cache   [num_blocks, Hkv, block_size, D] bytes: a token's record of one
+ *           key/value head is D/2 bytes of key codes, then D/2 of value codes
+ *   scales  [num_blocks, Hkv, block_size, D/16] bytes: D/32 of the key's
+ *           scales, then D/32 of the value's
+ * Order of the codes in a record (that of the attention kernel's matrix
+ * fragments), with G = D/32: the key's 4-byte word t*G + g (t < 4, g < G)
+ * holds elements 32g + 8t .. + 7, the value's 2-byte unit r*G + g (r < 8)
+ * elements 32g + 4r .. + 3, the lower element of a byte in its low nibble.
+ * dsa_kv4_insert writes this layout, dsa_kv4_gather reads it back.
+ *
+ * Shared by the calls below: D is 64 or 128, block_size a power of two in
+ * [8, 128] (else DSA_ERR_UNSUPPORTED), cache and scales 16-byte aligned;
+ * num_blocks * block_size * Hkv < 2^32.  Slots are block * block_size + row,
+ * as in dsa_k_norm_quant_insert; the index cache and this one can share a
+ * block table.  Once a call has run on a device its calls can be captured
+ * into a CUDA graph.
+ * --------------------------------------------------------------------------
+ */
+
+/*
+ * Writes new keys and values into their slots.  Per block of 32 elements: the
+ * scale is the smallest power of two s >= 2^-126 with max|x| <= 6 s (1 for a
+ * block of zeros), codes = x / s rounded to nearest, ties to the even code
+ * (nothing saturates).  A block with a NaN or an infinity becomes all NaN
+ * (scale code 255).
+ *
+ *   k, v          [T, Hkv, D] bf16, 16-byte aligned; tokens k_stride (v_stride)
+ *                 elements apart (a multiple of 8, at least Hkv * D)
+ *   slot_mapping  [T] int64, distinct: a slot below 0 is skipped; one past the
+ *                 cache is skipped and reported by dsa_get_last_device_error
+ *                 as DSA_ERR_INVALID_ARG
+ */
+dsa_status_t dsa_kv4_insert(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                            const int64_t* slot_mapping, int T, int Hkv, int D, void* cache,
+                            uint8_t* scales, int num_blocks, int block_size,
+                            dsa_stream_t stream);
+
+/*
+ * Reads slots back as the values they stand for: k, v [T, Hkv, D] bf16 out,
+ * dense, 16-byte aligned (exact: two significant bits times a power of two;
+ * scale code 255 reads as NaN).  Slots as dsa_kv4_insert; a skipped one gives
+ * zeros.
+ */
+dsa_status_t dsa_kv4_gather(const void* cache, const uint8_t* scales, int num_blocks,
+                            int block_size, const int64_t* slots, int T, int Hkv, int D, void* k,
+                            void* v, dsa_stream_t stream);
+
+/*
+ * Decode attention over the cache.  Query row r = b*next_n + j (token j of
+ * request b) sees the keys [0, L_b - next_n + j + 1):
+ *   S[r,h,c] = softmax_scale * q[r,h] . K[c, h / (Hq/Hkv)]
+ *   lse[r,h] = log sum_c exp S[r,h,c]
+ *   out[r,h] = sum_c exp(S[r,h,c] - lse[r,h]) V[c, h / (Hq/Hkv)]
+ * A row that sees nothing gives out = 0 and lse = -inf.  Values of keys that
+ * a row does not see never reach it, whatever they hold.
+ *
+ *   q             [B*next_n, Hq, D] bf16, 16-byte aligned; Hq a multiple of Hkv
+ *   block_table   [B, max_blocks] int32; context_lens [B] int32, counting the
+ *                 request's next_n new tokens: bad entries as in
+ *                 dsa_indexer_logits_paged (block 0 in their place, lengths
+ *                 clamped, both recorded)
+ *   softmax_scale finite
+ *   out           [B*next_n, Hq, D] bf16, 8-byte aligned
+ *   lse           [B*next_n, Hq] fp32 (natural logarithm) or NULL
+ *   key_weights   NULL, or [B, ldw] fp32, ldw >= max_blocks*block_size: the
+ *                 weight sum_{j,h} exp(S - lse) of every key below L_b is
+ *                 ADDED at its position (other positions are untouched)
+ *   workspace     dsa_kv4_attention_workspace_bytes(B, next_n, Hq, Hkv, D,
+ *                 max_blocks*block_size, 0, key_weights != NULL) bytes, 256-byte
+ *                 aligned; NULL where that is 0.  It is sized for the current
+ *                 device.
+ * Products run on the tensor cores in fp16 with fp32 accumulation: keys and
+ * values enter exactly, q after division by a power of two per row (its
+ * elements below 2^-24 of the row's largest vanish), the weights rounded to
+ * fp16 (2^-12 relative; contributions below 2^-24 of the largest value scale
+ * vanish).  Sums, the softmax's maximum and sum, and the weights are fp32.
+ * Every sum runs in one fixed order: results are the same from call to call.
+ */
+dsa_status_t dsa_kv4_attention(const void* q, const void* cache, const uint8_t* scales,
+                               int num_blocks, const int32_t* block_table, int max_blocks,
+                               const int32_t* context_lens, int B, int next_n, int block_size,
+                               int Hq, int Hkv, int D, float softmax_scale, void* out, float* lse,
+                               float* key_weights, int64_t ldw, void* workspace, size_t ws_bytes,
+                               dsa_stream_t stream);
+
+/*
+ * The same over the columns an indexer selected: row r attends to the
+ * positions topk[r, 0 .. k) alone.
+ *
+ *   topk          [B*next_n, k] int32 logical positions, in any order, distinct
+ *                 within a row (dsa_indexer_topk_paged's output); -1 is an
+ *                 empty entry, wherever it stands; any other entry that the
+ *                 row does not see is left out and reported by
+ *                 dsa_get_last_device_error as DSA_ERR_INVALID_ARG
+ *   topk_weights  NULL, or [B*next_n, k] fp32: the weight sum_h exp(S - lse)
+ *                 of every entry is written (0 for an empty one)
+ *   key_weights   NULL, or [B, ldw] fp32 as above: the entries' weights are
+ *                 added at their positions
+ *   workspace     dsa_kv4_attention_workspace_bytes(B, next_n, Hq, Hkv, D, k, 1,
+ *                 topk_weights != NULL || key_weights != NULL) bytes
+ */
+dsa_status_t dsa_kv4_attention_topk(const void* q, const void* cache, const uint8_t* scales,
+                                    int num_blocks, const int32_t* block_table, int max_blocks,
+                                    const int32_t* context_lens, const int32_t* topk, int k, int B,
+                                    int next_n, int block_size, int Hq, int Hkv, int D,
+                                    float softmax_scale, void* out, float* lse,
+                                    float* topk_weights, float* key_weights, int64_t ldw,
+                                    void* workspace, size_t ws_bytes, dsa_stream_t stream);
+
+/*
+ * Scratch bytes of the two attention calls on the current device; cols is
+ * max_blocks*block_size, or k with selected != 0.  (size_t)-1 for bad
+ * arguments.
+ */
+size_t dsa_kv4_attention_workspace_bytes(int B, int next_n, int Hq, int Hkv, int D, int64_t cols,
+                                         int selected, int weights);
+
+/*
+ * Which tokens of every request a budget keeps: its first `sink` positions,
+ * its last `recent`, and of those between the budget - sink - recent with the
+ * largest accumulated weight (ties to the lower position; -inf and NaN are
+ * never kept).  A request no longer than the budget keeps everything (but
+ * such weights).
+ *
+ *   key_weights   [B, ldw] fp32, ldw >= max_ctx; only positions below L_b are read
+ *   context_lens  [B] int32 in [0, max_ctx] (others are clamped and recorded)
+ *   keep          [B, budget] int32 out: kept positions ascending, then -1
+ *   new_lens      [B] int32 out: how many
+ *   workspace     dsa_kv_evict_workspace_bytes(B, max_ctx, budget) bytes,
+ *                 256-byte aligned
+ * sink + recent <= budget.
+ */
+dsa_status_t dsa_kv_evict_select(const float* key_weights, int64_t ldw,
+                                 const int32_t* context_lens, int B, int max_ctx, int budget,
+                                 int sink, int recent, int32_t* keep, int32_t* new_lens,
+                                 void* workspace, size_t ws_bytes, dsa_stream_t stream);
+size_t dsa_kv_evict_workspace_bytes(int B, int64_t max_ctx, int budget);
+
+/* One paged array of a compaction: [num_blocks, planes, block_size, row_bytes]
+ * (planes = 1 for the indexer's keys, Hkv for the 4-bit cache). */
+typedef struct {
+    void* base;    /* 16-byte aligned */
+    int planes;    /* >= 1 */
+    int row_bytes; /* bytes of a token's row of one plane, a multiple of 4 */
+} dsa_paged_rows_t;
+
+/*
+ * Moves every request's kept rows together: row keep[b, i] becomes row i, in
+ * all `caches` (at most 8, all with the same blocks) at once.
+ *
+ *   new_block_table  [B, new_max_blocks] int32: pages to move to, none of them
+ *                    a page that block_table names; or NULL: in place (the
+ *                    pages past new_lens are then free).  A page in place must
+ *                    belong to one request only.
+ *   context_lens     [B] lengths before, new_lens [B] after (at most budget)
+ *   keep             [B, budget] int32, ascending; entries outside
+ *                    [0, context_lens[b]) below new_lens[b], and pages outside
+ *                    the cache, are skipped and recorded
+ *   key_weights      NULL, or [B, ldw] fp32: moved alike into key_weights_out
+ *                    (which may be key_weights), whose rest up to
+ *                    max_blocks*block_size becomes 0
+ */
+dsa_status_t dsa_kv_compact(const dsa_paged_rows_t* caches, int n_caches, int num_blocks,
+                            int block_size, const int32_t* block_table, int max_blocks,
+                            const int32_t* new_block_table, int new_max_blocks,
+                            const int32_t* context_lens, const int32_t* keep,
+                            const int32_t* new_lens, int B, int budget, const float* key_weights,
+                            float* key_weights_out, int64_t ldw, dsa_stream_t stream);
+
+/*
  * Scratch bytes an operation needs.  rows/cols are T/S for the prefill ops and
  * B*next_n / max_blocks*block_size for the paged ones; k is index_topk.  The
  * composed calls need the fp32 logits (rows * round_up(cols, 4) floats, padded
@@ -465,7 +641,8 @@ const char* dsa_status_string(dsa_status_t status);
  * kernel's bounded wait gave up since the last call, DSA_ERR_INVALID_ARG when
  * a paged call met a block id or context length out of range (or
  * dsa_topk_sort_by_score an index outside its row, or
- * dsa_k_norm_quant_insert a slot past the cache), DSA_ERR_CUDA
+ * dsa_k_norm_quant_insert a slot past the cache; the key/value cache's calls
+ * likewise), DSA_ERR_CUDA
  * when the synchronisation itself failed, else DSA_OK.
  */
 dsa_status_t dsa_get_last_device_error(void);

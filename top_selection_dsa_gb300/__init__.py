@@ -14,6 +14,8 @@ from __future__ import annotations
 __all__ = [
     "indexer_logits", "topk", "indexer_topk", "indexer_logits_paged",
     "indexer_topk_paged", "workspace_bytes", "DSAError",
+    "kv4_cache", "kv4_insert", "kv4_gather", "kv4_attention", "kv4_attention_topk",
+    "kv_evict_select", "kv_compact",
 ]
 
 

@@ -32,8 +32,15 @@ EXPORTS = (
     "dsa_topk_sort_by_score", "dsa_q_quant_fold_weights", "dsa_k_norm_quant_insert",
     "dsa_topk_merge", "dsa_indexer_topk_host_bytes", "dsa_indexer_topk_host",
     "dsa_indexer_logits_mxfp4", "dsa_indexer_topk_mxfp4", "dsa_topk_merge_ranks",
-    "dsa_topk_dcp_candidates",
+    "dsa_topk_dcp_candidates", "dsa_kv4_insert", "dsa_kv4_gather", "dsa_kv4_attention",
+    "dsa_kv4_attention_topk", "dsa_kv4_attention_workspace_bytes", "dsa_kv_evict_select",
+    "dsa_kv_evict_workspace_bytes", "dsa_kv_compact",
 )
+
+
+class PagedRows(ctypes.Structure):
+    """Mirror of dsa_paged_rows_t."""
+    _fields_ = [("base", ctypes.c_void_p), ("planes", ctypes.c_int), ("row_bytes", ctypes.c_int)]
 
 
 class DSAError(RuntimeError):
@@ -75,6 +82,22 @@ def _load():
     lib.dsa_indexer_topk_host.argtypes = [P, P, P, P, I, P, P, P, I, I, I, I, I, P, P, SZ, P]
     lib.dsa_indexer_logits_mxfp4.argtypes = [P, P, P, P, P, P, P, I, I, I, I, P, I64, U32, P]
     lib.dsa_indexer_topk_mxfp4.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, P, P, SZ, P]
+    lib.dsa_kv4_insert.argtypes = [P, I64, P, I64, P, I, I, I, P, P, I, I, P]
+    lib.dsa_kv4_gather.argtypes = [P, P, I, I, P, I, I, I, P, P, P]
+    lib.dsa_kv4_attention.argtypes = [P, P, P, I, P, I, P, I, I, I, I, I, I, F, P, P, P, I64, P, SZ,
+                                      P]
+    lib.dsa_kv4_attention_topk.argtypes = [P, P, P, I, P, I, P, P, I, I, I, I, I, I, I, F, P, P, P,
+                                           P, I64, P, SZ, P]
+    lib.dsa_kv4_attention_workspace_bytes.argtypes = [I, I, I, I, I, I64, I, I]
+    lib.dsa_kv4_attention_workspace_bytes.restype = SZ
+    lib.dsa_kv_evict_select.argtypes = [P, I64, P, I, I, I, I, I, P, P, P, SZ, P]
+    lib.dsa_kv_evict_workspace_bytes.argtypes = [I, I64, I]
+    lib.dsa_kv_evict_workspace_bytes.restype = SZ
+    lib.dsa_kv_compact.argtypes = [ctypes.POINTER(PagedRows), I, I, I, P, I, P, I, P, P, P, I, I,
+                                   P, P, I64, P]
+    for name in ("dsa_kv4_insert", "dsa_kv4_gather", "dsa_kv4_attention",
+                 "dsa_kv4_attention_topk", "dsa_kv_evict_select", "dsa_kv_compact"):
+        getattr(lib, name).restype = I
     for name in ("dsa_indexer_logits_mxfp4", "dsa_indexer_topk_mxfp4"):
         getattr(lib, name).restype = I
     for name in ("dsa_indexer_logits", "dsa_topk", "dsa_indexer_topk",
@@ -492,6 +515,279 @@ def k_norm_quant_insert(k, ln_weight, ln_bias, eps, slot_mapping, k_cache, k_sca
                                          num_blocks, block_size, _stream(dev))
     _check(st, "dsa_k_norm_quant_insert")
     return k_cache, k_scale
+
+
+def kv4_cache(num_blocks, num_kv_heads, block_size, head_dim, device="cuda"):
+    """An empty 4-bit key/value cache: (cache [num_blocks, Hkv, block_size, D],
+    scales [num_blocks, Hkv, block_size, D/16]), both uint8."""
+    return (torch.zeros((num_blocks, num_kv_heads, block_size, head_dim), dtype=torch.uint8,
+                        device=device),
+            torch.zeros((num_blocks, num_kv_heads, block_size, head_dim // 16), dtype=torch.uint8,
+                        device=device))
+
+
+def _kv4_shape(cache, scales, dev):
+    _need(cache, "cache", (torch.uint8,), dev)
+    _need(scales, "scales", (torch.uint8,), dev)
+    if cache.dim() != 4 or scales.dim() != 4:
+        raise ValueError("cache [num_blocks, Hkv, block_size, D] and scales "
+                         "[num_blocks, Hkv, block_size, D/16] expected")
+    nb, hkv, bs, D = cache.shape
+    if tuple(scales.shape) != (nb, hkv, bs, D // 16):
+        raise ValueError(f"scales must be {(nb, hkv, bs, D // 16)}, got {tuple(scales.shape)}")
+    return nb, hkv, bs, D
+
+
+def _shape(t, name, shape):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _token_rows(t, name, dev, shape):
+    """Element stride between tokens of a [T, Hkv, D] bf16 tensor whose heads
+    and elements are dense."""
+    if not t.is_cuda or t.device != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on {dev}")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be bf16, got {t.dtype}")
+    _shape(t, name, shape)
+    T, H, D = shape
+    if t.numel() and ((D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D)):
+        raise ValueError(f"{name}: heads and elements of a token must be dense")
+    return t.stride(0) if T > 1 else H * D
+
+
+def kv4_insert(k, v, slot_mapping, cache, scales):
+    """Quantise new keys and values [T, Hkv, D] (bf16; tokens may be strided,
+    as slices of one projection are) into their slots of the 4-bit cache.  In
+    place."""
+    dev = cache.device
+    nb, hkv, bs, D = _kv4_shape(cache, scales, dev)
+    _need(slot_mapping, "slot_mapping", (torch.int64,), dev)
+    T = slot_mapping.numel()
+    ks = _token_rows(k, "k", dev, (T, hkv, D))
+    vs = _token_rows(v, "v", dev, (T, hkv, D))
+    if T == 0:
+        return cache, scales
+    with torch.cuda.device(dev):
+        st = lib.dsa_kv4_insert(_ptr(k), ks, _ptr(v), vs, _ptr(slot_mapping), T, hkv, D,
+                                _ptr(cache), _ptr(scales), nb, bs, _stream(dev))
+    _check(st, "dsa_kv4_insert")
+    return cache, scales
+
+
+def kv4_gather(cache, scales, slots, *, k=None, v=None):
+    """The keys and values at `slots` of the 4-bit cache: two [T, Hkv, D] bf16
+    tensors (zeros for a slot below 0)."""
+    dev = cache.device
+    nb, hkv, bs, D = _kv4_shape(cache, scales, dev)
+    _need(slots, "slots", (torch.int64,), dev)
+    T = slots.numel()
+    k = torch.empty((T, hkv, D), dtype=torch.bfloat16, device=dev) if k is None else k
+    v = torch.empty((T, hkv, D), dtype=torch.bfloat16, device=dev) if v is None else v
+    for t, n in ((k, "k"), (v, "v")):
+        _need(t, n, (torch.bfloat16,), dev)
+        _shape(t, n, (T, hkv, D))
+    if T == 0:
+        return k, v
+    with torch.cuda.device(dev):
+        st = lib.dsa_kv4_gather(_ptr(cache), _ptr(scales), nb, bs, _ptr(slots), T, hkv, D, _ptr(k),
+                                _ptr(v), _stream(dev))
+    _check(st, "dsa_kv4_gather")
+    return k, v
+
+
+def kv4_attention_workspace_bytes(B, next_n, Hq, Hkv, D, cols, *, selected=False,
+                                  weights=False) -> int:
+    """Workspace of kv4_attention (cols = max_blocks * block_size) or, with
+    `selected`, of kv4_attention_topk (cols = k), on the current device."""
+    n = lib.dsa_kv4_attention_workspace_bytes(B, next_n, Hq, Hkv, D, cols, int(selected),
+                                              int(weights))
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("dsa_kv4_attention_workspace_bytes: bad arguments")
+    return int(n)
+
+
+def _kv4_attention(q, cache, scales, block_table, context_lens, topk_idx, next_n, softmax_scale,
+                   out, lse, topk_weights, key_weights, workspace):
+    dev = q.device
+    nb, hkv, bs, D = _kv4_shape(cache, scales, dev)
+    _need(q, "q", (torch.bfloat16,), dev)
+    _need(block_table, "block_table", (torch.int32,), dev)
+    _need(context_lens, "context_lens", (torch.int32,), dev)
+    _need(topk_idx, "topk_idx", (torch.int32,), dev)
+    _need(topk_weights, "topk_weights", (torch.float32,), dev)
+    _need(key_weights, "key_weights", (torch.float32,), dev)
+    B, max_blocks = block_table.shape
+    R, Hq, Dq = q.shape
+    if R != B * next_n or Dq != D:
+        raise ValueError(f"q must be [{B * next_n}, Hq, {D}], got {tuple(q.shape)}")
+    _shape(context_lens, "context_lens", (B,))
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((R, Hq), dtype=torch.float32, device=dev)
+    _need(out, "out", (torch.bfloat16,), dev)
+    _need(lse, "lse", (torch.float32,), dev)
+    _shape(out, "out", (R, Hq, D))
+    _shape(lse, "lse", (R, Hq))
+    ldw = 0
+    if key_weights is not None:
+        if key_weights.dim() != 2 or key_weights.shape[0] != B or \
+                key_weights.shape[1] < max_blocks * bs:
+            raise ValueError(f"key_weights must be [{B}, >= {max_blocks * bs}], got "
+                             f"{tuple(key_weights.shape)}")
+        ldw = key_weights.shape[1]
+    scale = D ** -0.5 if softmax_scale is None else float(softmax_scale)
+    with torch.cuda.device(dev):
+        if topk_idx is None:
+            nbytes = kv4_attention_workspace_bytes(B, next_n, Hq, hkv, D, max_blocks * bs,
+                                                   weights=key_weights is not None)
+            ws = _workspace(nbytes, dev, workspace)
+            st = lib.dsa_kv4_attention(_ptr(q), _ptr(cache), _ptr(scales), nb, _ptr(block_table),
+                                       max_blocks, _ptr(context_lens), B, next_n, bs, Hq, hkv, D,
+                                       scale, _ptr(out), _ptr(lse), _ptr(key_weights), ldw,
+                                       _ptr(ws) if nbytes else None, nbytes, _stream(dev))
+            _check(st, "dsa_kv4_attention")
+        else:
+            k = topk_idx.shape[-1]
+            _shape(topk_idx, "topk_idx", (R, k))
+            _shape(topk_weights, "topk_weights", (R, k))
+            nbytes = kv4_attention_workspace_bytes(
+                B, next_n, Hq, hkv, D, k, selected=True,
+                weights=key_weights is not None or topk_weights is not None)
+            ws = _workspace(nbytes, dev, workspace)
+            st = lib.dsa_kv4_attention_topk(
+                _ptr(q), _ptr(cache), _ptr(scales), nb, _ptr(block_table), max_blocks,
+                _ptr(context_lens), _ptr(topk_idx), k, B, next_n, bs, Hq, hkv, D, scale, _ptr(out),
+                _ptr(lse), _ptr(topk_weights), _ptr(key_weights), ldw,
+                _ptr(ws) if nbytes else None, nbytes, _stream(dev))
+            _check(st, "dsa_kv4_attention_topk")
+    return out, lse
+
+
+def kv4_attention(q, cache, scales, block_table, context_lens, *, next_n, softmax_scale=None,
+                  out=None, lse=None, key_weights=None, workspace=None):
+    """Decode attention of q [B*next_n, Hq, D] (bf16) over the 4-bit paged
+    cache: (out like q, lse [B*next_n, Hq] fp32).  softmax_scale defaults to
+    D^-0.5; key_weights [B, >= max_blocks*block_size] fp32 has every key's
+    attention weight, summed over heads and rows, added to it."""
+    return _kv4_attention(q, cache, scales, block_table, context_lens, None, next_n,
+                          softmax_scale, out, lse, None, key_weights, workspace)
+
+
+def kv4_attention_topk(q, cache, scales, block_table, context_lens, topk_idx, *, next_n,
+                       softmax_scale=None, out=None, lse=None, sel_weights=None,
+                       key_weights=None, workspace=None):
+    """kv4_attention over the selected columns topk_idx [B*next_n, k] (logical
+    positions, -1 empty: indexer_topk_paged's output).  sel_weights
+    [B*next_n, k] fp32 receives every entry's attention weight, summed over
+    heads; key_weights has them added at their positions."""
+    if topk_idx is None:
+        raise ValueError("topk_idx [B*next_n, k] expected")
+    return _kv4_attention(q, cache, scales, block_table, context_lens, topk_idx, next_n,
+                          softmax_scale, out, lse, sel_weights, key_weights, workspace)
+
+
+def kv_evict_workspace_bytes(B, max_ctx, budget) -> int:
+    n = lib.dsa_kv_evict_workspace_bytes(B, max_ctx, budget)
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("dsa_kv_evict_workspace_bytes: bad arguments")
+    return int(n)
+
+
+def kv_evict_select(key_weights, context_lens, budget, *, sink=0, recent=0, keep=None,
+                    new_lens=None, workspace=None):
+    """The positions every request keeps under `budget`: its first `sink`, its
+    last `recent` and the heaviest between, by key_weights [B, ldw].  Returns
+    (keep [B, budget] int32 ascending, -1 padded; new_lens [B] int32)."""
+    dev = key_weights.device
+    _need(key_weights, "key_weights", (torch.float32,), dev)
+    _need(context_lens, "context_lens", (torch.int32,), dev)
+    B, ldw = key_weights.shape
+    _shape(context_lens, "context_lens", (B,))
+    if keep is None:
+        keep = torch.empty((B, budget), dtype=torch.int32, device=dev)
+    if new_lens is None:
+        new_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+    _need(keep, "keep", (torch.int32,), dev)
+    _need(new_lens, "new_lens", (torch.int32,), dev)
+    _shape(keep, "keep", (B, budget))
+    _shape(new_lens, "new_lens", (B,))
+    nbytes = kv_evict_workspace_bytes(B, ldw, budget)
+    with torch.cuda.device(dev):
+        ws = _workspace(nbytes, dev, workspace)
+        st = lib.dsa_kv_evict_select(_ptr(key_weights), ldw, _ptr(context_lens), B, ldw,
+                                     int(budget), int(sink), int(recent), _ptr(keep),
+                                     _ptr(new_lens), _ptr(ws), nbytes, _stream(dev))
+    _check(st, "dsa_kv_evict_select")
+    return keep, new_lens
+
+
+def _paged_rows(t, block_size, dev):
+    """A paged cache as (planes, row bytes): [num_blocks, planes, block_size,
+    ...] or [num_blocks, block_size, ...] with one plane."""
+    if not t.is_cuda or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"every cache must be a contiguous CUDA tensor on {dev}")
+    if t.dim() == 4 and t.shape[2] == block_size:
+        planes, row = t.shape[1], t.shape[3]
+    elif t.dim() in (2, 3) and t.shape[1] == block_size:
+        planes, row = 1, t.shape[2] if t.dim() == 3 else 1
+    else:
+        raise ValueError("caches are [num_blocks, planes, block_size, row], [num_blocks, "
+                         f"block_size, row] or [num_blocks, block_size]; got {tuple(t.shape)} "
+                         f"with block_size {block_size}")
+    return PagedRows(t.data_ptr(), planes, row * t.element_size())
+
+
+def kv_compact(caches, keep, context_lens, block_table, new_block_table=None, *, new_lens=None,
+               block_size=None, key_weights=None, key_weights_out=None):
+    """Move the kept rows of every request together (row keep[b, i] becomes row
+    i), in all paged `caches` at once: to the pages of new_block_table, or in
+    place.  new_lens defaults to the entries of keep before its -1 padding;
+    block_size to the first cache's.  key_weights moves alike, into
+    key_weights_out (default: in place), zeros after."""
+    caches = list(caches)
+    dev = keep.device
+    _need(keep, "keep", (torch.int32,), dev)
+    _need(context_lens, "context_lens", (torch.int32,), dev)
+    _need(block_table, "block_table", (torch.int32,), dev)
+    _need(new_block_table, "new_block_table", (torch.int32,), dev)
+    _need(new_lens, "new_lens", (torch.int32,), dev)
+    _need(key_weights, "key_weights", (torch.float32,), dev)
+    _need(key_weights_out, "key_weights_out", (torch.float32,), dev)
+    B, budget = keep.shape
+    max_blocks = block_table.shape[1]
+    _shape(context_lens, "context_lens", (B,))
+    _shape(block_table, "block_table", (B, max_blocks))
+    if new_block_table is not None:
+        _shape(new_block_table, "new_block_table", (B, new_block_table.shape[-1]))
+    if not caches and block_size is None:
+        raise ValueError("block_size is needed without caches")
+    if block_size is None:
+        block_size = caches[0].shape[2] if caches[0].dim() == 4 else caches[0].shape[1]
+    num_blocks = caches[0].shape[0] if caches else 1
+    if any(c.shape[0] != num_blocks for c in caches):
+        raise ValueError("every cache must have the same number of blocks")
+    rows = (PagedRows * max(len(caches), 1))(*[_paged_rows(c, block_size, dev) for c in caches])
+    if new_lens is None:
+        new_lens = (keep >= 0).sum(1, dtype=torch.int32)
+    _shape(new_lens, "new_lens", (B,))
+    ldw = 0
+    if key_weights is not None:
+        if key_weights_out is None:
+            key_weights_out = key_weights
+        ldw = key_weights.shape[1]
+        _shape(key_weights, "key_weights", (B, ldw))
+        _shape(key_weights_out, "key_weights_out", (B, ldw))
+    with torch.cuda.device(dev):
+        st = lib.dsa_kv_compact(rows, len(caches), num_blocks, block_size, _ptr(block_table),
+                                max_blocks, _ptr(new_block_table),
+                                0 if new_block_table is None else new_block_table.shape[1],
+                                _ptr(context_lens), _ptr(keep), _ptr(new_lens), B, budget,
+                                _ptr(key_weights), _ptr(key_weights_out), ldw, _stream(dev))
+    _check(st, "dsa_kv_compact")
+    return caches
 
 
 def last_device_error() -> int:

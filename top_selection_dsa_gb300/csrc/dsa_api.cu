@@ -11,10 +11,9 @@
 
 #include "dsa.h"
 
-#include <nvtx3/nvToolsExt.h>
-
 #include <algorithm>
 #include <vector>
+#include "dsa_abi.h"
 #include "dsa_common.cuh"
 #include "dsa_internal.h"
 
@@ -46,6 +45,8 @@ EncodeTiledFn encode_fn() {
 
 constexpr int kMaxDevices = 64;
 
+}  // namespace
+
 // Device address of g_error_word on the current device (looked up once per
 // device), or null.
 uint32_t* error_word() {
@@ -62,8 +63,6 @@ uint32_t* error_word() {
   return addr[dev];
 }
 
-}  // namespace
-
 // SM count of the current device (queried once per device).
 int device_sm_count() {
   int dev = 0;
@@ -78,22 +77,6 @@ int device_sm_count() {
 }
 
 namespace {
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
-cudaStream_t as_stream(dsa_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
-
-dsa_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA; }
-
-// An NVTX range named after the entry point around each call, so that a
-// profiler's timeline shows which library call queued which kernels.  (With
-// no tool attached an NVTX call returns at once.)
-struct CallRange {
-  explicit CallRange(const char* name) { nvtxRangePushA(name); }
-  ~CallRange() { nvtxRangePop(); }
-  CallRange(const CallRange&) = delete;
-  CallRange& operator=(const CallRange&) = delete;
-};
 
 // 128-byte-swizzled tiled map over a row-major [rows, D] matrix (2-D) or a
 // [blocks, block_rows, D] cache (3-D), box = 128 bytes of D x box_rows rows.

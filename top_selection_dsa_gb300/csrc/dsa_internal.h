@@ -119,4 +119,84 @@ cudaError_t launch_k_norm_insert(const void* k, const float* gamma, const float*
                                  const int64_t* slots, int T, bool fp8, int64_t capacity,
                                  void* cache, float* cache_scale, uint32_t* err, cudaStream_t s);
 
+// ------------------------------------------------ the 4-bit key/value cache
+// Device address of the current device's error word, or null.
+uint32_t* error_word();
+
+// Writing and reading back (dsa_kv4_cache.cu); D is 64 or 128, block_size a
+// power of two.
+cudaError_t launch_kv4_insert(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                              const int64_t* slots, int T, int Hkv, int D, void* cache,
+                              void* scales, int num_blocks, int block_size, uint32_t* err,
+                              cudaStream_t s);
+cudaError_t launch_kv4_gather(const void* cache, const void* scales, const int64_t* slots, int T,
+                              int Hkv, int D, int num_blocks, int block_size, void* k, void* v,
+                              uint32_t* err, cudaStream_t s);
+
+// Decode attention (dsa_kv4_attn.cu).  A group is what shares its columns: a
+// request (every key), or a query row (selected keys).
+struct Kv4AttnParams {
+  const uint16_t* q;       // [B*next_n, Hq, D] bf16
+  const uint8_t* cache;    // [num_blocks, Hkv, block_size, D]
+  const uint8_t* scales;   // [num_blocks, Hkv, block_size, D/16]
+  const int32_t* block_table;
+  const int32_t* context_lens;
+  const int32_t* sel;      // [B*next_n, sel_k] or null
+  int sel_k;
+  int groups, next_n, heads, Hkv, Hq, row_tiles;  // heads: query heads per key/value head
+  int max_blocks, num_blocks, log_bs;
+  float scale_log2e;       // softmax scale times log2(e)
+  int chunk, nsplit;       // columns per CTA, CTAs per group, head and row tile
+  int cols;                // columns at most (max context, or sel_k)
+  uint16_t* out;           // [B*next_n, Hq, D] bf16
+  float* lse;              // [B*next_n, Hq] or null
+  float* part_o;           // [groups, nsplit, Hkv*row_tiles, rows, D] when nsplit > 1
+  float* part_ml;          // [.., rows, 2]
+  float* scores;           // [groups, Hkv*row_tiles, cols, rows]: base-2 logits, for the weights
+  float* lse2;             // [groups, Hkv*row_tiles, rows]
+  float* sel_weights;      // [B*next_n, sel_k] or null
+  float* key_weights;      // [B, ldw] or null
+  int64_t ldw;
+  uint32_t* err;
+};
+// How a call is cut up, and the byte offsets of its workspace.
+struct Kv4AttnPlan {
+  int64_t groups;
+  int heads, nt, row_tiles, chunk, nsplit;
+  int64_t part_o, part_ml, scores, lse2, sel_weights, bytes;
+};
+Kv4AttnPlan kv4_attn_plan(int B, int next_n, int Hq, int Hkv, int D, int64_t cols, bool selected,
+                          bool weights);
+cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int D, int nt, bool scores,
+                                 cudaStream_t s);
+
+// Eviction (dsa_kv_evict.cu).
+cudaError_t launch_evict_ranges(const int32_t* lens, int B, int max_ctx, int sink, int recent,
+                                int32_t* starts, int32_t* ends, uint32_t* err, cudaStream_t s);
+cudaError_t launch_evict_keep(const int32_t* lens, const int32_t* starts, const int32_t* ends,
+                              const int32_t* mid, int B, int max_ctx, int room, int budget,
+                              int32_t* keep, int32_t* new_lens, cudaStream_t s);
+constexpr int kMaxCompact = 8;  // caches one compaction moves
+struct CompactParams {
+  struct Cache {
+    uint8_t* base;       // [num_blocks, planes, block_size, row_bytes]
+    int planes, row_bytes;
+  } cache[kMaxCompact];
+  int first_unit[kMaxCompact + 1];  // units (plane, column of bytes) before each cache
+  int ncaches, units;
+  const int32_t* keep;       // [B, budget]
+  const int32_t* new_lens;   // [B]
+  const int32_t* block_table;      // [B, max_blocks]
+  const int32_t* new_block_table;  // [B, new_max_blocks], or null: in place
+  int B, budget, max_blocks, new_max_blocks, num_blocks, log_bs;
+  const float* weights;   // [B, ldw] or null
+  float* weights_out;     // [B, ldw], may be weights
+  int64_t ldw;
+  const int32_t* old_lens;
+  uint32_t* err;
+};
+cudaError_t launch_kv_compact(const CompactParams& p, cudaStream_t s);
+// Units (plane, slice of bytes) of a cache.
+int compact_units(const CompactParams::Cache& c);
+
 }  // namespace dsa

@@ -1,0 +1,869 @@
+// dsa_kv4_attn.cu -- decode attention over the paged 4-bit key/value cache
+// (layout in dsa_kv4.cuh), over every key of a request or over the columns an
+// indexer selected.
+//
+//   S[n,c] = scale * q[n] . K[c]       for the columns c that row n sees
+//   lse[n] = log sum_c exp S[n,c]      out[n] = sum_c exp(S[n,c] - lse[n]) V[c]
+//
+// One warp walks tiles of 64 columns of one key/value head for up to 16 query
+// rows (the rows of the head's group, all tokens of the request): cp.async
+// brings the tile's records and scales into the warp's own two-stage ring,
+// and everything after that stays in registers.
+//   S^T = K q^T   mma m16n8k16 with the keys as the 16-row operand: its fp16
+//                 elements are the E2M1 codes' values themselves (exact); the
+//                 four blocks of 32 elements accumulate apart and are summed
+//                 in fp32 with their power-of-two scales.  q is divided by a
+//                 power of two per row so that its largest element is in
+//                 [1, 2): bf16's eight bits fit fp16 exactly, and elements
+//                 below 2^-24 of the row's largest vanish.
+//   softmax       one pass: running maximum m and sum l per row (base 2, in
+//                 fp32), the accumulated output rescaled when m rises.
+//   O^T += V^T P  keys as the contraction: V's elements again the codes'
+//                 values, one 16-row tile per half block of channels, and the
+//                 value scales multiplied into P (fp16) once per block of 32
+//                 channels, relative to the largest scale met so far, 2^x:
+//                 P 2^(e - x) <= 1, and terms below 2^-24 of that vanish.
+// Rounding P to fp16 costs 2^-12 of each term (the output's bf16 rounding is
+// 2^-9); l sums the unrounded weights.
+//
+// Rows of the m16 operand are permuted within each group of eight (odd rows
+// exchange halves, row i holds key i ^ 4): with the records' 16-byte chunks
+// XOR-swizzled by the key's index in its group of eight, the 16-byte key
+// loads and the 8-byte value loads are then both free of bank conflicts.
+//
+// The columns of a request are cut into chunks, one CTA (four warps, tiles
+// dealt round) per chunk, head and 16 rows; a CTA that covers all of a row's
+// columns writes the result, otherwise partial sums that a second kernel
+// joins.
+#include <math.h>
+
+#include "dsa_internal.h"
+#include "dsa_kv4.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kTile = 64;       // columns a warp takes at a time
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 2;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+template <int kBytes>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 r;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"(a)
+               : "memory");
+  return r;
+}
+__device__ __forceinline__ void sts16(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"(static_cast<uint16_t>(v)) : "memory");
+}
+
+// fp16 bits of 2^(e - top), e <= top (0 below 2^-24).
+__device__ __forceinline__ uint32_t scale_f16(uint32_t e, int top) {
+  const int t = static_cast<int>(e) - top + 15;
+  return t > 0 ? static_cast<uint32_t>(t) << 10 : (t > -10 ? 0x200u >> -t : 0u);
+}
+
+// Non-zero when a byte of w is 255.
+__device__ __forceinline__ uint32_t has_ff(uint32_t w) {
+  return (~w - 0x01010101u) & w & 0x80808080u;
+}
+
+template <int D>
+struct Layout {
+  static constexpr int G = D / kMxBlock;        // scale blocks of a row
+  static constexpr int kChunks = D / 16;        // 16-byte chunks of a record
+  static constexpr int kSc = D / 16;            // scale bytes of a record
+  static constexpr int kTileBytes = kTile * D;
+  static constexpr int kStageBytes = kTileBytes + kTile * kSc;
+  static constexpr int kFactorBytes = kTile * G * 2;
+  static constexpr int kWarpBytes = kStages * kStageBytes + kFactorBytes;
+  // Chunk c of key `row` of a tile.
+  __device__ static __forceinline__ uint32_t chunk_at(int row, int c) {
+    const int f = D == 128 ? (row & 7) : ((row >> 1) & 3);
+    return row * D + ((c ^ f) << 4);
+  }
+};
+
+// The group (request, or selected row) a CTA works for.
+struct Group {
+  int b;       // request
+  int L;       // tokens in its cache
+  int cols;    // columns: cached tokens, or entries of the selection
+  int limit;   // selected row: columns it may see
+};
+
+template <bool kSel>
+__device__ __forceinline__ Group group_of(const Kv4AttnParams& p, int g, bool report) {
+  Group r;
+  r.b = kSel ? g / p.next_n : g;
+  const int cap = p.max_blocks << p.log_bs;
+  const int raw = __ldg(p.context_lens + r.b);
+  if (report && (raw < 0 || raw > cap)) record_error(p.err, kErrBadIndex);
+  r.L = raw < 0 ? 0 : (raw > cap ? cap : raw);
+  r.cols = kSel ? p.sel_k : r.L;
+  r.limit = kSel ? max(r.L - p.next_n + (g - r.b * p.next_n) + 1, 0) : r.L;
+  return r;
+}
+
+// Where query row n (of a group's rows for one key/value head) lies: the row
+// of q, out and lse as [rows, Hq].
+template <bool kSel>
+__device__ __forceinline__ int64_t head_row(const Kv4AttnParams& p, int g, int head, int n) {
+  const int j = kSel ? 0 : n / p.heads;
+  const int64_t row = kSel ? g : static_cast<int64_t>(g) * p.next_n + j;
+  return row * p.Hq + head * p.heads + (n - j * p.heads);
+}
+
+template <int D, int NT, bool kSel, bool kScores>
+__global__ void __launch_bounds__(kThreads, 3)
+    kv4_attn_kernel(const __grid_constant__ Kv4AttnParams p) {
+  using Lay = Layout<D>;
+  constexpr int G = Lay::G;
+  constexpr int kRows = 8 * NT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = lane >> 2, t = lane & 3;
+
+  // head and row tile fastest: neighbouring CTAs read neighbouring heads of
+  // the same pages.
+  const int per_split = p.Hkv * p.row_tiles;
+  int64_t id = blockIdx.x;
+  const int ht = static_cast<int>(id % per_split);
+  id /= per_split;
+  const int split = static_cast<int>(id % p.nsplit);
+  const int grp = static_cast<int>(id / p.nsplit);
+  const int head = ht / p.row_tiles;
+  const int row0 = (ht % p.row_tiles) * kRows;
+  const int nrows = kSel ? p.heads : p.heads * p.next_n;
+
+  const Group gr = group_of<kSel>(p, grp, split == 0 && ht == 0 && threadIdx.x == 0);
+  const int c0 = split * p.chunk;
+  if (c0 >= gr.cols && split > 0) return;
+  const int c1 = min(gr.cols, c0 + p.chunk);
+  const bool whole = gr.cols <= p.chunk;
+
+  const uint32_t ring = smem_u32(smem) + warp * Lay::kWarpBytes;
+  const uint32_t factors = ring + kStages * Lay::kStageBytes;
+
+  // ---------------------------------------------------------------- queries
+  // B fragments: lane (r, t) holds row r's elements 32 g + 8 t .. + 7.
+  uint32_t qf[NT][G][4];
+  float f_scale[NT][2];  // S = f_scale * accumulator, for rows 2t and 2t + 1
+  int limit[NT][2];      // columns those rows see
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int n = row0 + nt * 8 + r;
+    uint4 raw[G];
+    uint32_t amax = 0;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      raw[g] = make_uint4(0u, 0u, 0u, 0u);
+      if (n < nrows)
+        raw[g] = __ldg(reinterpret_cast<const uint4*>(
+            p.q + head_row<kSel>(p, grp, head, n) * D + g * 32 + t * 8));
+      const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        amax = max(amax, max((w[i] << 16) & 0x7FFF0000u, w[i] & 0x7FFF0000u));
+    }
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    // Exponent of the largest element; rows with none (all zero, or an
+    // infinity or NaN somewhere) keep their values.
+    const int E = amax == 0 || amax >= 0x7F800000u ? 0
+                                                   : max(static_cast<int>(amax >> 23), 1) - 127;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        qf[nt][g][i] = pack_f16(ldexpf(bf16_lo(w[i]), -E), ldexpf(bf16_hi(w[i]), -E));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = __shfl_sync(0xffffffffu, E, (2 * t + i) * 4);
+      f_scale[nt][i] = ldexpf(p.scale_log2e, e);
+      const int nn = row0 + nt * 8 + 2 * t + i;
+      limit[nt][i] = kSel ? gr.cols : gr.L - p.next_n + min(nn / p.heads, p.next_n - 1) + 1;
+    }
+  }
+  const int all_see = kSel ? gr.cols : gr.L - p.next_n + 1;  // columns every row sees
+
+  // ------------------------------------------------------------------ loads
+  // Tiles of this warp: columns c0 + 64 (warp + 4 i).  A lane finds the
+  // records of the tile's columns `lane` and `lane + 32`.
+  const int tiles = (c1 - c0 + kTile - 1) / kTile;
+  const int bs_mask = (1 << p.log_bs) - 1;
+  uint32_t rec[2];
+  bool has[2];
+  auto locate = [&](int tile) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int col = c0 + tile * kTile + lane + 32 * i;
+      int pos = -1;
+      if (tile < tiles && col < c1) {
+        pos = col;
+        if (kSel) {
+          pos = __ldg(p.sel + static_cast<int64_t>(grp) * p.sel_k + col);
+          if (pos < -1 || pos >= gr.limit) {
+            record_error(p.err, kErrBadIndex);
+            pos = -1;
+          }
+        }
+      }
+      has[i] = pos >= 0;
+      rec[i] = 0;
+      if (has[i]) {
+        int block = __ldg(p.block_table + static_cast<int64_t>(gr.b) * p.max_blocks +
+                          (pos >> p.log_bs));
+        if (block < 0 || block >= p.num_blocks) {
+          record_error(p.err, kErrBadIndex);
+          block = 0;
+        }
+        rec[i] = ((static_cast<uint32_t>(block) * p.Hkv + head) << p.log_bs) + (pos & bs_mask);
+      }
+    }
+  };
+  // Copies of the located tile into stage s; absent columns become zeros.
+  auto fetch = [&](int s, uint32_t mask0, uint32_t mask1) {
+    const uint32_t base = ring + s * Lay::kStageBytes;
+    constexpr int kPer = 32 / Lay::kChunks;  // records per instruction
+    const int c = lane % Lay::kChunks;
+#pragma unroll
+    for (int i = 0; i < kTile / kPer; ++i) {
+      const int row = i * kPer + lane / Lay::kChunks;
+      const bool upper = i >= kTile / kPer / 2;
+      const uint32_t rc = __shfl_sync(0xffffffffu, upper ? rec[1] : rec[0], row & 31);
+      const bool ok = ((upper ? mask1 : mask0) >> (row & 31)) & 1;
+      cp_async16(base + Lay::chunk_at(row, c), p.cache + static_cast<int64_t>(rc) * D + c * 16,
+                 ok ? 16u : 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      cp_async_small<Lay::kSc>(base + Lay::kTileBytes + (lane + 32 * i) * Lay::kSc,
+                               p.scales + static_cast<int64_t>(rec[i]) * Lay::kSc,
+                               has[i] ? Lay::kSc : 0);
+  };
+
+  float o[NT][2 * G][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 2 * G; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
+  int top = 0;  // o is in units of 2^(top - 127)
+
+  uint32_t mask[kStages][2];
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) {
+    locate(warp + s * kWarps);
+    mask[s][0] = __ballot_sync(0xffffffffu, has[0]);
+    mask[s][1] = __ballot_sync(0xffffffffu, has[1]);
+    if (mask[s][0] | mask[s][1]) fetch(s, mask[s][0], mask[s][1]);
+    cp_async_commit();
+  }
+
+  // Lane addresses that do not change from tile to tile: the key chunk of
+  // rows pi(r) (+ 8, + 16 ..), the value units of rows 2t and (2t+1)^4.
+  const int prow = r ^ ((r & 1) << 2);
+  const uint32_t k_at = D == 128 ? Lay::chunk_at(prow, t) : Lay::chunk_at(prow, t >> 1) + (t & 1) * 8;
+  const int v_row[2] = {2 * t, (2 * t + 1) ^ 4};
+  uint32_t v_at[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    v_at[i] = D == 128 ? Lay::chunk_at(v_row[i], 4 + (r >> 1)) + (r & 1) * 8
+                       : Lay::chunk_at(v_row[i], 2 + (r >> 2)) + (r & 3) * 4;
+
+  int s = 0;
+  for (int tile = warp; tile < tiles; tile += kWarps, s ^= 1) {
+    locate(tile + kStages * kWarps);  // two tiles on: its loads return under this tile's work
+    cp_async_wait<kStages - 1>();
+    __syncwarp();
+    const uint32_t base = ring + s * Lay::kStageBytes;
+    const uint32_t m0 = s ? mask[1][0] : mask[0][0], m1 = s ? mask[1][1] : mask[0][1];
+    if (m0 | m1) {
+      // -------------------------------------------------- value scale factors
+      const uint32_t sc_base = base + Lay::kTileBytes;
+      uint32_t nan0 = 0, nan1 = 0;  // keys with a NaN scale
+      {
+        uint32_t ks[2], vs[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // absent columns are zero
+          if constexpr (D == 128) {
+            const uint2 u = lds64(sc_base + (lane + 32 * i) * 8);
+            ks[i] = u.x, vs[i] = u.y;
+          } else {
+            const uint32_t u = lds32(sc_base + (lane + 32 * i) * 4);
+            ks[i] = u & 0xFFFFu, vs[i] = u >> 16;
+          }
+        }
+        if (__any_sync(0xffffffffu, has_ff(ks[0]) | has_ff(ks[1]) | has_ff(vs[0]) | has_ff(vs[1]))) {
+          // NaN scales (rare).  A key's makes its logits NaN below; a value's
+          // makes its 32 channels of every row that sees the column NaN, here,
+          // and takes no part in the products.
+          nan0 = __ballot_sync(0xffffffffu, has_ff(ks[0]) != 0);
+          nan1 = __ballot_sync(0xffffffffu, has_ff(ks[1]) != 0);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t keys = __ballot_sync(0xffffffffu, has_ff(vs[i]) != 0);
+            while (keys) {
+              const int src = __ffs(keys) - 1;
+              keys &= keys - 1;
+              const uint32_t w = __shfl_sync(0xffffffffu, vs[i], src);
+              const int col = c0 + tile * kTile + 32 * i + src;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                  for (int g = 0; g < G; ++g)
+                    if (((w >> (8 * g)) & 255u) == 255u && col < limit[nt][h]) {
+                      o[nt][2 * g][h] = o[nt][2 * g][2 + h] = __uint_as_float(0x7FC00000u);
+                      o[nt][2 * g + 1][h] = o[nt][2 * g + 1][2 + h] = __uint_as_float(0x7FC00000u);
+                    }
+            }
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+              if (((vs[i] >> (8 * g)) & 255u) == 255u) vs[i] &= ~(255u << (8 * g));
+          }
+        }
+        uint32_t mx = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int g = 0; g < G; ++g) mx = max(mx, (vs[i] >> (8 * g)) & 255u);
+        mx = __reduce_max_sync(0xffffffffu, mx);
+        if (static_cast<int>(mx) > top) {
+          const float down = exp2f(static_cast<float>(top - static_cast<int>(mx)));
+          top = static_cast<int>(mx);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2 * G; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[nt][i][j] *= down;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          // Key `lane + 32 i` is row i8 ^ (odd: 4) of its group of eight.
+          const int key = lane + 32 * i;
+          const int row = (key & 7) ^ ((key & 1) << 2);
+          const uint32_t at = factors + ((key >> 3) * 4 + (row >> 1)) * (4 * G) + (row & 1) * 2;
+          const bool ok = i ? (m1 >> lane) & 1 : (m0 >> lane) & 1;
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+            sts16(at + 4 * g, ok ? scale_f16((vs[i] >> (8 * g)) & 255u, top) : 0u);
+        }
+        __syncwarp();
+      }
+      // ------------------------------------------------------------ S^T = K q^T
+      float sacc[4][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        uint32_t kw[2][G];
+        uint32_t ks[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t at = base + (mt * 16 + h * 8) * D + k_at;
+          if constexpr (D == 128) {
+            const uint4 u = lds128(at);
+            kw[h][0] = u.x, kw[h][1] = u.y, kw[h][2] = u.z, kw[h][3] = u.w;
+          } else {
+            const uint2 u = lds64(at);
+            kw[h][0] = u.x, kw[h][1] = u.y;
+          }
+          ks[h] = lds32(sc_base + (mt * 16 + h * 8 + prow) * Lay::kSc);
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const float s0 = __uint_as_float(((ks[0] >> (8 * g)) & 255u) << 23);
+          const float s1 = __uint_as_float(((ks[1] >> (8 * g)) & 255u) << 23);
+          const uint32_t a0 = e2m1x2_to_f16x2<0>(kw[0][g]), a1 = e2m1x2_to_f16x2<0>(kw[1][g]);
+          const uint32_t a2 = e2m1x2_to_f16x2<1>(kw[0][g]), a3 = e2m1x2_to_f16x2<1>(kw[1][g]);
+          const uint32_t b0 = e2m1x2_to_f16x2<2>(kw[0][g]), b1 = e2m1x2_to_f16x2<2>(kw[1][g]);
+          const uint32_t b2 = e2m1x2_to_f16x2<3>(kw[0][g]), b3 = e2m1x2_to_f16x2<3>(kw[1][g]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16816(c, a0, a1, a2, a3, qf[nt][g][0], qf[nt][g][1]);
+            mma16816(c, b0, b1, b2, b3, qf[nt][g][2], qf[nt][g][3]);
+            if (g == 0) {
+              sacc[mt][nt][0] = c[0] * s0, sacc[mt][nt][1] = c[1] * s0;
+              sacc[mt][nt][2] = c[2] * s1, sacc[mt][nt][3] = c[3] * s1;
+            } else {
+              sacc[mt][nt][0] = fmaf(c[0], s0, sacc[mt][nt][0]);
+              sacc[mt][nt][1] = fmaf(c[1], s0, sacc[mt][nt][1]);
+              sacc[mt][nt][2] = fmaf(c[2], s1, sacc[mt][nt][2]);
+              sacc[mt][nt][3] = fmaf(c[3], s1, sacc[mt][nt][3]);
+            }
+          }
+        }
+      }
+      // --------------------------------------------------------------- softmax
+      const int col0 = c0 + tile * kTile;
+      const bool clean = (nan0 | nan1) == 0 && (kSel ? (m0 & m1) == 0xffffffffu
+                                                     : col0 + kTile <= min(c1, all_see));
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sacc[mt][nt][j] *= f_scale[nt][j & 1];
+      if (!clean) {
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int key = mt * 16 + h * 8 + prow;
+            const bool here = ((mt >= 2 ? m1 : m0) >> (key & 31)) & 1;
+            const bool nan = ((mt >= 2 ? nan1 : nan0) >> (key & 31)) & 1;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                if (nan) sacc[mt][nt][2 * h + i] = __uint_as_float(0x7FC00000u);
+                if (!here || (!kSel && col0 + key >= limit[nt][i]))
+                  sacc[mt][nt][2 * h + i] = -INFINITY;
+              }
+          }
+      }
+      if constexpr (kScores) {
+        float* dst = p.scores + (static_cast<int64_t>(grp) * per_split + ht) * p.cols * kRows;
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int col = col0 + mt * 16 + h * 8 + prow;
+            if (col < c1) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                *reinterpret_cast<float2*>(dst + static_cast<int64_t>(col) * kRows + nt * 8 +
+                                           2 * t) =
+                    make_float2(sacc[mt][nt][2 * h], sacc[mt][nt][2 * h + 1]);
+            }
+          }
+      }
+      float mn[NT][2];
+      bool up = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float x = m[nt][i];
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt)
+            x = fmaxf(x, fmaxf(sacc[mt][nt][i], sacc[mt][nt][2 + i]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          mn[nt][i] = x;
+          up |= x > m[nt][i];
+        }
+      if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            // m = -inf: nothing accumulated yet (l and o are zero).
+            const float a = m[nt][i] == -INFINITY ? 0.f : ex2(m[nt][i] - mn[nt][i]);
+            m[nt][i] = mn[nt][i];
+            l[nt][i] *= a;
+#pragma unroll
+            for (int j = 0; j < 2 * G; ++j) o[nt][j][i] *= a, o[nt][j][2 + i] *= a;
+          }
+      }
+      uint32_t pf[4][NT][2];  // P as B fragments: row r, keys 2t, 2t+1 (+ 8)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        // A row that has seen no column yet: every exponent is -inf.
+        const float z0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+        const float z1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+          const float p0 = ex2(sacc[mt][nt][0] - z0), p1 = ex2(sacc[mt][nt][1] - z1);
+          const float p2 = ex2(sacc[mt][nt][2] - z0), p3 = ex2(sacc[mt][nt][3] - z1);
+          l[nt][0] += p0 + p2;
+          l[nt][1] += p1 + p3;
+          pf[mt][nt][0] = transpose8x8(pack_f16(p0, p1));
+          pf[mt][nt][1] = transpose8x8(pack_f16(p2, p3));
+        }
+      }
+      // ------------------------------------------------------------ O^T += V^T P
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        // lo/hi: the even/odd codes of this lane's units for the key pairs
+        // (2t, 2t+1) and (2t+8, 2t+9), one pair per byte.
+        uint32_t lo[2][G / 2], hi[2][G / 2];
+        uint32_t fac[2][G];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t va[G / 2], vb[G / 2];
+          const uint32_t at = base + (mt * 16 + h * 8) * D;
+          if constexpr (D == 128) {
+            const uint2 ua = lds64(at + v_at[0]), ub = lds64(at + v_at[1]);
+            va[0] = ua.x, va[1] = ua.y, vb[0] = ub.x, vb[1] = ub.y;
+            const uint4 u = lds128(factors + ((mt * 2 + h) * 4 + t) * 16);
+            fac[h][0] = u.x, fac[h][1] = u.y, fac[h][2] = u.z, fac[h][3] = u.w;
+          } else {
+            va[0] = lds32(at + v_at[0]), vb[0] = lds32(at + v_at[1]);
+            const uint2 u = lds64(factors + ((mt * 2 + h) * 4 + t) * 8);
+            fac[h][0] = u.x, fac[h][1] = u.y;
+          }
+#pragma unroll
+          for (int i = 0; i < G / 2; ++i) {
+            lo[h][i] = (va[i] & 0x0F0F0F0Fu) | ((vb[i] << 4) & 0xF0F0F0F0u);
+            hi[h][i] = ((va[i] >> 4) & 0x0F0F0F0Fu) | (vb[i] & 0xF0F0F0F0u);
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          // Channels 32 g + 4 r + {0, 1} (first tile) and + {2, 3} (second).
+          const uint32_t l0 = lo[0][g / 2], h0 = hi[0][g / 2], l1 = lo[1][g / 2], h1 = hi[1][g / 2];
+          uint32_t a[2][4];
+          if (g % 2 == 0) {
+            a[0][0] = e2m1x2_to_f16x2<0>(l0), a[0][1] = e2m1x2_to_f16x2<0>(h0);
+            a[0][2] = e2m1x2_to_f16x2<0>(l1), a[0][3] = e2m1x2_to_f16x2<0>(h1);
+            a[1][0] = e2m1x2_to_f16x2<1>(l0), a[1][1] = e2m1x2_to_f16x2<1>(h0);
+            a[1][2] = e2m1x2_to_f16x2<1>(l1), a[1][3] = e2m1x2_to_f16x2<1>(h1);
+          } else {
+            a[0][0] = e2m1x2_to_f16x2<2>(l0), a[0][1] = e2m1x2_to_f16x2<2>(h0);
+            a[0][2] = e2m1x2_to_f16x2<2>(l1), a[0][3] = e2m1x2_to_f16x2<2>(h1);
+            a[1][0] = e2m1x2_to_f16x2<3>(l0), a[1][1] = e2m1x2_to_f16x2<3>(h0);
+            a[1][2] = e2m1x2_to_f16x2<3>(l1), a[1][3] = e2m1x2_to_f16x2<3>(h1);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint32_t b0 = mul_f16x2(pf[mt][nt][0], fac[0][g]);
+            const uint32_t b1 = mul_f16x2(pf[mt][nt][1], fac[1][g]);
+            mma16816(o[nt][2 * g], a[0][0], a[0][1], a[0][2], a[0][3], b0, b1);
+            mma16816(o[nt][2 * g + 1], a[1][0], a[1][1], a[1][2], a[1][3], b0, b1);
+          }
+        }
+      }
+    }
+    __syncwarp();
+    const uint32_t n0 = __ballot_sync(0xffffffffu, has[0]);
+    const uint32_t n1 = __ballot_sync(0xffffffffu, has[1]);
+    if (n0 | n1) fetch(s, n0, n1);
+    cp_async_commit();
+    if (s) mask[1][0] = n0, mask[1][1] = n1;
+    else mask[0][0] = n0, mask[0][1] = n1;
+  }
+
+  // ------------------------------------------- join the four warps, write out
+  cp_async_wait<0>();
+  __syncthreads();
+  float* so = reinterpret_cast<float*>(smem);              // [warp][row][D]
+  float* sml = so + kWarps * kRows * D;                    // [warp][row][2]
+  const float unit = exp2f(static_cast<float>(top - 127));
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float x = l[nt][i];
+      x += __shfl_xor_sync(0xffffffffu, x, 4);
+      x += __shfl_xor_sync(0xffffffffu, x, 8);
+      x += __shfl_xor_sync(0xffffffffu, x, 16);
+      const int row = nt * 8 + 2 * t + i;
+      if (r == 0) {
+        sml[(warp * kRows + row) * 2] = m[nt][i];
+        sml[(warp * kRows + row) * 2 + 1] = x;
+      }
+      float* dst = so + (warp * kRows + row) * D;
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        *reinterpret_cast<float4*>(dst + 32 * g + 4 * r) =
+            make_float4(o[nt][2 * g][i] * unit, o[nt][2 * g][2 + i] * unit,
+                        o[nt][2 * g + 1][i] * unit, o[nt][2 * g + 1][2 + i] * unit);
+    }
+  __syncthreads();
+  const int64_t part = (static_cast<int64_t>(grp) * p.nsplit + split) * per_split + ht;
+  for (int e = threadIdx.x; e < kRows * D / 4; e += kThreads) {
+    const int row = e / (D / 4), d = (e % (D / 4)) * 4;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sml[(w * kRows + row) * 2]);
+    const float z = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = ex2(sml[(w * kRows + row) * 2] - z);
+      L = fmaf(sml[(w * kRows + row) * 2 + 1], f, L);
+      const float4 x = *reinterpret_cast<const float4*>(so + (w * kRows + row) * D + d);
+      a.x = fmaf(x.x, f, a.x), a.y = fmaf(x.y, f, a.y);
+      a.z = fmaf(x.z, f, a.z), a.w = fmaf(x.w, f, a.w);
+    }
+    const int n = row0 + row;
+    if (whole) {
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      const float lse2 = M + log2f(L);
+      if (n < nrows) {
+        const int64_t hr = head_row<kSel>(p, grp, head, n);
+        *reinterpret_cast<uint2*>(p.out + hr * D + d) =
+            make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+        if (d == 0 && p.lse) p.lse[hr] = L == 0.f ? -INFINITY : lse2 * 0.69314718055994531f;
+      }
+      if (kScores && d == 0)
+        p.lse2[(static_cast<int64_t>(grp) * per_split + ht) * kRows + row] =
+            n >= nrows || L == 0.f ? INFINITY : lse2;
+    } else {
+      *reinterpret_cast<float4*>(p.part_o + (part * kRows + row) * D + d) = a;
+      if (d == 0)
+        *reinterpret_cast<float2*>(p.part_ml + (part * kRows + row) * 2) = make_float2(M, L);
+    }
+  }
+}
+
+// Joins the partial sums of a group's chunks: one CTA per group, head and row
+// tile, D/4 threads a row.
+template <int D, int NT, bool kSel, bool kScores>
+__global__ void __launch_bounds__(kThreads)
+    kv4_join_kernel(const __grid_constant__ Kv4AttnParams p) {
+  constexpr int kRows = 8 * NT;
+  const int per_split = p.Hkv * p.row_tiles;
+  const int ht = static_cast<int>(blockIdx.x % per_split);
+  const int grp = static_cast<int>(blockIdx.x / per_split);
+  const int head = ht / p.row_tiles;
+  const int row0 = (ht % p.row_tiles) * kRows;
+  const int nrows = kSel ? p.heads : p.heads * p.next_n;
+  const Group gr = group_of<kSel>(p, grp, false);
+  if (gr.cols <= p.chunk) return;
+  const int ns = (gr.cols + p.chunk - 1) / p.chunk;
+  for (int e = threadIdx.x; e < kRows * D / 4; e += kThreads) {
+    const int row = e / (D / 4), d = (e % (D / 4)) * 4;
+    float M = -INFINITY, L = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int sp = 0; sp < ns; ++sp) {
+      const int64_t part = (static_cast<int64_t>(grp) * p.nsplit + sp) * per_split + ht;
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (part * kRows + row) * 2);
+      const float4 x = *reinterpret_cast<const float4*>(p.part_o + (part * kRows + row) * D + d);
+      const float Mn = fmaxf(M, ml.x);
+      const float z = Mn == -INFINITY ? 0.f : Mn;
+      const float fo = ex2(M - z), fn = ex2(ml.x - z);
+      M = Mn;
+      L = L * fo + ml.y * fn;
+      a.x = a.x * fo + x.x * fn, a.y = a.y * fo + x.y * fn;
+      a.z = a.z * fo + x.z * fn, a.w = a.w * fo + x.w * fn;
+    }
+    const int n = row0 + row;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const float lse2 = M + log2f(L);
+    if (n < nrows) {
+      const int64_t hr = head_row<kSel>(p, grp, head, n);
+      *reinterpret_cast<uint2*>(p.out + hr * D + d) =
+          make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+      if (d == 0 && p.lse) p.lse[hr] = L == 0.f ? -INFINITY : lse2 * 0.69314718055994531f;
+    }
+    if (kScores && d == 0)
+      p.lse2[(static_cast<int64_t>(grp) * per_split + ht) * kRows + row] =
+          n >= nrows || L == 0.f ? INFINITY : lse2;
+  }
+}
+
+// A column's attention weight, summed over heads and rows in one fixed order:
+// w = sum exp2(S - lse).  Dense: added to key_weights.  Selected: written to
+// sel_weights, and (one token a request) added to key_weights at the column's
+// position.
+template <int NT, bool kSel>
+__global__ void __launch_bounds__(256) kv4_weight_kernel(const __grid_constant__ Kv4AttnParams p) {
+  constexpr int kRows = 8 * NT;
+  const int per_split = p.Hkv * p.row_tiles;
+  const int per_grp = (p.cols + 255) / 256;
+  const int grp = static_cast<int>(blockIdx.x / per_grp);
+  const int col = static_cast<int>(blockIdx.x % per_grp) * 256 + threadIdx.x;
+  const Group gr = group_of<kSel>(p, grp, false);
+  if (static_cast<int>(blockIdx.x % per_grp) * 256 >= gr.cols) return;
+  extern __shared__ float lse_s[];
+  for (int i = threadIdx.x; i < per_split * kRows; i += 256)
+    lse_s[i] = p.lse2[static_cast<int64_t>(grp) * per_split * kRows + i];
+  __syncthreads();
+  if (col >= gr.cols) return;
+  float w = 0.f;
+  int pos = col;
+  if (kSel) {
+    pos = __ldg(p.sel + static_cast<int64_t>(grp) * p.sel_k + col);
+    if (pos < 0 || pos >= gr.limit) pos = -1;
+  }
+  if (pos >= 0) {
+    for (int ht = 0; ht < per_split; ++ht) {
+      const float4* src = reinterpret_cast<const float4*>(
+          p.scores + ((static_cast<int64_t>(grp) * per_split + ht) * p.cols + col) * kRows);
+      const float4* z = reinterpret_cast<const float4*>(lse_s + ht * kRows);
+#pragma unroll
+      for (int i = 0; i < kRows / 4; ++i) {
+        const float4 x = __ldg(src + i), y = z[i];
+        w += ex2(x.x - y.x) + ex2(x.y - y.y) + ex2(x.z - y.z) + ex2(x.w - y.w);
+      }
+    }
+  }
+  if (kSel) {
+    if (p.sel_weights) p.sel_weights[static_cast<int64_t>(grp) * p.sel_k + col] = w;
+    if (p.key_weights && p.next_n == 1 && pos >= 0)
+      atomicAdd(p.key_weights + static_cast<int64_t>(gr.b) * p.ldw + pos, w);
+  } else {
+    p.key_weights[static_cast<int64_t>(gr.b) * p.ldw + col] += w;
+  }
+}
+
+// Several tokens a request: their rows may select the same column, so one CTA
+// per request adds row after row (a row's columns are distinct, so the sums
+// do not depend on the order the threads run in).
+__global__ void __launch_bounds__(1024)
+    kv4_weight_scatter_kernel(const __grid_constant__ Kv4AttnParams p) {
+  const int b = blockIdx.x;
+  for (int j = 0; j < p.next_n; ++j) {
+    const int64_t row = static_cast<int64_t>(b) * p.next_n + j;
+    const Group gr = group_of<true>(p, static_cast<int>(row), false);
+    for (int c = threadIdx.x; c < p.sel_k; c += blockDim.x) {
+      const int pos = __ldg(p.sel + row * p.sel_k + c);
+      if (pos >= 0 && pos < gr.limit)
+        atomicAdd(p.key_weights + static_cast<int64_t>(b) * p.ldw + pos,
+                  p.sel_weights[row * p.sel_k + c]);
+    }
+    __syncthreads();
+  }
+}
+
+template <int D, int NT, bool kSel, bool kScores>
+cudaError_t launch_one(const Kv4AttnParams& p, cudaStream_t s) {
+  using Lay = Layout<D>;
+  constexpr int kRing = kWarps * Lay::kWarpBytes;
+  constexpr int kJoin = kWarps * 8 * NT * (D + 2) * 4;
+  constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
+  auto* fn = kv4_attn_kernel<D, NT, kSel, kScores>;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = static_cast<int64_t>(p.groups) * p.Hkv * p.row_tiles;
+  fn<<<static_cast<unsigned>(tiles * p.nsplit), kThreads, kSmem, s>>>(p);
+  e = cudaGetLastError();
+  if (e == cudaSuccess && p.nsplit > 1) {
+    kv4_join_kernel<D, NT, kSel, kScores><<<static_cast<unsigned>(tiles), kThreads, 0, s>>>(p);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess && kScores) {
+    const int64_t grid = static_cast<int64_t>(p.groups) * ((p.cols + 255) / 256);
+    const size_t sm = static_cast<size_t>(p.Hkv) * p.row_tiles * 8 * NT * sizeof(float);
+    kv4_weight_kernel<NT, kSel><<<static_cast<unsigned>(grid), 256, sm, s>>>(p);
+    e = cudaGetLastError();
+    if (e == cudaSuccess && kSel && p.key_weights && p.next_n > 1) {
+      kv4_weight_scatter_kernel<<<static_cast<unsigned>(p.groups / p.next_n), 1024, 0, s>>>(p);
+      e = cudaGetLastError();
+    }
+  }
+  return e;
+}
+
+template <int D, int NT>
+cudaError_t launch_nt(const Kv4AttnParams& p, bool scores, cudaStream_t s) {
+  if (p.sel) return scores ? launch_one<D, NT, true, true>(p, s) : launch_one<D, NT, true, false>(p, s);
+  return scores ? launch_one<D, NT, false, true>(p, s) : launch_one<D, NT, false, false>(p, s);
+}
+
+int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+Kv4AttnPlan kv4_attn_plan(int B, int next_n, int Hq, int Hkv, int D, int64_t cols, bool selected,
+                          bool weights) {
+  Kv4AttnPlan pl = {};
+  pl.heads = Hq / Hkv;
+  pl.groups = selected ? static_cast<int64_t>(B) * next_n : B;
+  const int rows = selected ? pl.heads : pl.heads * next_n;
+  pl.nt = rows <= 8 ? 1 : 2;
+  pl.row_tiles = (rows + 8 * pl.nt - 1) / (8 * pl.nt);
+  // Chunks: enough CTAs for every SM's three places, at least one tile a
+  // warp, and no more than 64 tiles so that requests of unequal length spread.
+  const int64_t tiles = (cols + kTile - 1) / kTile;
+  const int64_t lanes = pl.groups * Hkv * pl.row_tiles;
+  const int64_t places = static_cast<int64_t>(device_sm_count() > 0 ? device_sm_count() : 152) * 3;
+  int64_t per = (tiles * lanes + places - 1) / (places > 0 ? places : 1);
+  per = per < kWarps ? kWarps : (per > 64 ? 64 : per);
+  per = (per + kWarps - 1) / kWarps * kWarps;
+  pl.chunk = static_cast<int>(per) * kTile;
+  pl.nsplit = static_cast<int>((cols + pl.chunk - 1) / pl.chunk);
+  if (pl.nsplit < 1) pl.nsplit = 1;
+  const int64_t parts = lanes * pl.nsplit * 8 * pl.nt;
+  int64_t off = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t at = off;
+    off += up256(bytes);
+    return at;
+  };
+  pl.part_o = take(pl.nsplit > 1 ? parts * D * 4 : 0);
+  pl.part_ml = take(pl.nsplit > 1 ? parts * 8 : 0);
+  pl.scores = take(weights ? lanes * cols * 8 * pl.nt * 4 : 0);
+  pl.lse2 = take(weights ? lanes * 8 * pl.nt * 4 : 0);
+  pl.sel_weights = take(weights && selected && next_n > 1 ? pl.groups * cols * 4 : 0);
+  pl.bytes = off;
+  return pl;
+}
+
+cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int D, int nt, bool scores,
+                                 cudaStream_t s) {
+  if (D == 128) return nt == 1 ? launch_nt<128, 1>(p, scores, s) : launch_nt<128, 2>(p, scores, s);
+  return nt == 1 ? launch_nt<64, 1>(p, scores, s) : launch_nt<64, 2>(p, scores, s);
+}
+
+}  // namespace dsa

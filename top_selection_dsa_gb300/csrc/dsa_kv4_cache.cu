@@ -1,0 +1,237 @@
+// dsa_kv4_cache.cu -- writing bf16 keys and values into the paged 4-bit cache
+// and reading them back as bf16.
+//
+// Quantisation, per block of 32 elements of a head's row: s = 2^e with e the
+// smallest exponent, no less than -126, for which max|x| <= 6 * 2^e (e = 0 for
+// a block of zeros), codes = x / s rounded to the nearest E2M1 value, ties to
+// the even code (nothing saturates).  A block that holds a NaN or an infinity
+// is written as scale code 255 (NaN) with zero codes: all of it reads back as
+// NaN.  Reading back is exact in bf16 (two significant bits times a power of
+// two).
+//
+// Both are memory-bound: one lane moves eight elements (16 bytes of bf16), a
+// record takes D/4 lanes (the key's, then the value's), and a lane has
+// kRecords records in flight.
+#include "dsa_internal.h"
+#include "dsa_kv4.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRecords = 4;
+
+struct CacheParams {
+  const uint16_t* k;  // insert: [T, Hkv, D], rows k_stride / v_stride elements apart
+  const uint16_t* v;
+  int64_t k_stride, v_stride;
+  uint16_t* k_out;    // gather: [T, Hkv, D], dense
+  uint16_t* v_out;
+  const int64_t* slots;
+  int64_t items;      // T * Hkv
+  int Hkv, log_bs;
+  int64_t capacity;
+  uint8_t* cache;
+  uint8_t* scales;
+  uint32_t* err;
+};
+
+// Record number of (slot, head): ((slot / bs) * Hkv + head) * bs + slot % bs.
+__device__ __forceinline__ int64_t record_of(const CacheParams& p, int64_t slot, int head) {
+  const int64_t block = slot >> p.log_bs;
+  const int64_t at = slot & ((int64_t(1) << p.log_bs) - 1);
+  return ((block * p.Hkv + head) << p.log_bs) + at;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) kv4_insert_kernel(const __grid_constant__ CacheParams p) {
+  constexpr int G = D / kMxBlock;
+  constexpr int kLanes = D / 4;  // D/8 for the key row, D/8 for the value row
+  constexpr int kPerCta = kThreads / kLanes;
+  const int sub = threadIdx.x % kLanes;
+  const bool is_v = sub >= kLanes / 2;
+  const int e8 = sub % (kLanes / 2);  // this lane's eight elements: 8 e8 ..
+  const int g = e8 / 4, t = e8 % 4;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kPerCta;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * kPerCta + threadIdx.x / kLanes;
+       base - threadIdx.x / kLanes < p.items; base += step * kRecords) {
+    uint4 raw[kRecords];
+    int64_t rec[kRecords];
+#pragma unroll
+    for (int i = 0; i < kRecords; ++i) {
+      const int64_t item = base + i * step;
+      rec[i] = -1;
+      raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (item < p.items) {
+        const int64_t tok = item / p.Hkv;
+        const int head = static_cast<int>(item - tok * p.Hkv);
+        const int64_t slot = __ldg(p.slots + tok);
+        if (slot >= p.capacity) {
+          if (sub == 0 && head == 0) record_error(p.err, kErrBadIndex);
+        } else if (slot >= 0) {
+          rec[i] = record_of(p, slot, head);
+          const uint16_t* src = is_v ? p.v + tok * p.v_stride : p.k + tok * p.k_stride;
+          raw[i] = __ldg(reinterpret_cast<const uint4*>(src + head * D) + e8);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRecords; ++i) {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      // The largest magnitude as bits: a NaN's or an infinity's are above
+      // every finite value's, so one integer maximum finds either.
+      uint32_t amax = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        amax = max(amax, max((w[j] << 16) & 0x7FFF0000u, w[j] & 0x7FFF0000u));
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      // 6 * 2^e = 1.5 * 2^(e+2): compare the mantissa with 1.5.
+      const int E = static_cast<int>(amax >> 23);
+      int e = E - 127 - 2 + ((amax & 0x7FFFFFu) > 0x400000u ? 1 : 0);
+      e = amax == 0 ? 0 : (e < -126 ? -126 : e);
+      const bool bad = amax >= 0x7F800000u;
+      const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      uint32_t codes = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        codes |= f32x2_to_e2m1x2(bf16_lo(w[j]) * inv, bf16_hi(w[j]) * inv) << (8 * j);
+      if (bad) codes = 0;
+      if (rec[i] < 0) continue;
+      uint8_t* dst = p.cache + rec[i] * D;
+      if (!is_v) {
+        *reinterpret_cast<uint32_t*>(dst + (t * G + g) * 4) = codes;
+      } else {
+        uint16_t* half = reinterpret_cast<uint16_t*>(dst + D / 2);
+        half[(2 * t) * G + g] = static_cast<uint16_t>(codes);
+        half[(2 * t + 1) * G + g] = static_cast<uint16_t>(codes >> 16);
+      }
+      if (t == 0)
+        p.scales[rec[i] * (D / 16) + (is_v ? G : 0) + g] =
+            bad ? 255 : static_cast<uint8_t>(e + 127);
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const __grid_constant__ CacheParams p) {
+  constexpr int G = D / kMxBlock;
+  constexpr int kLanes = D / 4;
+  constexpr int kPerCta = kThreads / kLanes;
+  const int sub = threadIdx.x % kLanes;
+  const bool is_v = sub >= kLanes / 2;
+  const int e8 = sub % (kLanes / 2);
+  const int g = e8 / 4, t = e8 % 4;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kPerCta;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * kPerCta + threadIdx.x / kLanes;
+       base < p.items; base += step * kRecords) {
+    uint32_t codes[kRecords];
+    uint32_t sc[kRecords];
+#pragma unroll
+    for (int i = 0; i < kRecords; ++i) {
+      const int64_t item = base + i * step;
+      codes[i] = 0;
+      sc[i] = 127;
+      if (item < p.items) {
+        const int64_t tok = item / p.Hkv;
+        const int head = static_cast<int>(item - tok * p.Hkv);
+        const int64_t slot = __ldg(p.slots + tok);
+        if (slot >= p.capacity) {
+          if (sub == 0 && head == 0) record_error(p.err, kErrBadIndex);
+        } else if (slot >= 0) {
+          const int64_t rec = record_of(p, slot, head);
+          const uint8_t* src = p.cache + rec * D;
+          if (!is_v) {
+            codes[i] = *reinterpret_cast<const uint32_t*>(src + (t * G + g) * 4);
+          } else {
+            const uint16_t* half = reinterpret_cast<const uint16_t*>(src + D / 2);
+            codes[i] = half[(2 * t) * G + g] |
+                       (static_cast<uint32_t>(half[(2 * t + 1) * G + g]) << 16);
+          }
+          sc[i] = p.scales[rec * (D / 16) + (is_v ? G : 0) + g];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRecords; ++i) {
+      const int64_t item = base + i * step;
+      if (item >= p.items) break;
+      const float s = sc[i] == 255 ? __uint_as_float(0x7FC00000u)
+                                   : ldexpf(1.f, static_cast<int>(sc[i]) - 127);
+      const uint32_t h[4] = {e2m1x2_to_f16x2<0>(codes[i]), e2m1x2_to_f16x2<1>(codes[i]),
+                             e2m1x2_to_f16x2<2>(codes[i]), e2m1x2_to_f16x2<3>(codes[i])};
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+        o[j] = pack_bf16(f.x * s, f.y * s);
+      }
+      uint16_t* dst = (is_v ? p.v_out : p.k_out) + item * D;
+      *(reinterpret_cast<uint4*>(dst) + e8) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+}
+
+int cache_grid(int64_t items, int D) {
+  const int64_t per = static_cast<int64_t>(kThreads / (D / 4)) * kRecords;
+  const int64_t need = (items + per - 1) / per;
+  const int64_t cap = static_cast<int64_t>(device_sm_count() > 0 ? device_sm_count() : 1) * 16;
+  return static_cast<int>(need < cap ? need : cap);
+}
+
+int log2_of(int x) {
+  int l = 0;
+  while ((1 << l) < x) ++l;
+  return l;
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_insert(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                              const int64_t* slots, int T, int Hkv, int D, void* cache,
+                              void* scales, int num_blocks, int block_size, uint32_t* err,
+                              cudaStream_t s) {
+  CacheParams p = {};
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.slots = slots;
+  p.items = static_cast<int64_t>(T) * Hkv;
+  p.Hkv = Hkv;
+  p.log_bs = log2_of(block_size);
+  p.capacity = static_cast<int64_t>(num_blocks) * block_size;
+  p.cache = static_cast<uint8_t*>(cache);
+  p.scales = static_cast<uint8_t*>(scales);
+  p.err = err;
+  if (p.items <= 0) return cudaSuccess;
+  if (D == 128)
+    kv4_insert_kernel<128><<<cache_grid(p.items, D), kThreads, 0, s>>>(p);
+  else
+    kv4_insert_kernel<64><<<cache_grid(p.items, D), kThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv4_gather(const void* cache, const void* scales, const int64_t* slots, int T,
+                              int Hkv, int D, int num_blocks, int block_size, void* k, void* v,
+                              uint32_t* err, cudaStream_t s) {
+  CacheParams p = {};
+  p.k_out = static_cast<uint16_t*>(k);
+  p.v_out = static_cast<uint16_t*>(v);
+  p.slots = slots;
+  p.items = static_cast<int64_t>(T) * Hkv;
+  p.Hkv = Hkv;
+  p.log_bs = log2_of(block_size);
+  p.capacity = static_cast<int64_t>(num_blocks) * block_size;
+  p.cache = static_cast<uint8_t*>(const_cast<void*>(cache));
+  p.scales = static_cast<uint8_t*>(const_cast<void*>(scales));
+  p.err = err;
+  if (p.items <= 0) return cudaSuccess;
+  if (D == 128)
+    kv4_gather_kernel<128><<<cache_grid(p.items, D), kThreads, 0, s>>>(p);
+  else
+    kv4_gather_kernel<64><<<cache_grid(p.items, D), kThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace dsa
