@@ -76,6 +76,23 @@ int device_sm_count() {
   return count[dev];
 }
 
+bool encode_rows_map(CUtensorMap* map, const void* base, int row_bytes, int64_t rows,
+                     int box_rows, int64_t planes) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn || (row_bytes != 64 && row_bytes != 128)) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(planes)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes),
+                                 static_cast<cuuint64_t>(row_bytes) * rows};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(row_bytes),
+                             static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 // 128-byte-swizzled tiled map over a row-major [rows, D] matrix (2-D) or a

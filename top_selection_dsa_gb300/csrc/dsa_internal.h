@@ -123,6 +123,11 @@ cudaError_t launch_k_norm_insert(const void* k, const float* gamma, const float*
 // Device address of the current device's error word, or null.
 uint32_t* error_word();
 
+// Tiled map over row-major bytes [planes, rows, row_bytes], box = one row's
+// bytes x box_rows rows x 1, swizzled over row_bytes (64 or 128).
+bool encode_rows_map(CUtensorMap* map, const void* base, int row_bytes, int64_t rows,
+                     int box_rows, int64_t planes);
+
 // Writing and reading back (dsa_kv4_cache.cu); D is 64 or 128, block_size a
 // power of two.
 cudaError_t launch_kv4_insert(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
@@ -136,6 +141,7 @@ cudaError_t launch_kv4_gather(const void* cache, const void* scales, const int64
 // Decode attention (dsa_kv4_attn.cu).  A group is what shares its columns: a
 // request (every key), or a query row (selected keys).
 struct Kv4AttnParams {
+  CUtensorMap tmap;        // the records, [num_blocks*Hkv, block_size, D bytes] (every key)
   const uint16_t* q;       // [B*next_n, Hq, D] bf16
   const uint8_t* cache;    // [num_blocks, Hkv, block_size, D]
   const uint8_t* scales;   // [num_blocks, Hkv, block_size, D/16]

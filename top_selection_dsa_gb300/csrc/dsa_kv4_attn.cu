@@ -110,36 +110,62 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
                : "memory");
   return r;
 }
-__device__ __forceinline__ void sts16(uint32_t a, uint32_t v) {
-  asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"(static_cast<uint16_t>(v)) : "memory");
-}
-
-// fp16 bits of 2^(e - top), e <= top (0 below 2^-24).
-__device__ __forceinline__ uint32_t scale_f16(uint32_t e, int top) {
-  const int t = static_cast<int>(e) - top + 15;
-  return t > 0 ? static_cast<uint32_t>(t) << 10 : (t > -10 ? 0x200u >> -t : 0u);
-}
-
 // Non-zero when a byte of w is 255.
 __device__ __forceinline__ uint32_t has_ff(uint32_t w) {
   return (~w - 0x01010101u) & w & 0x80808080u;
 }
 
+// Shared memory of a CTA: all warps' rings of tiles first (1024-byte aligned,
+// the swizzle is a function of the address; there is no static shared memory,
+// so the block begins so aligned), then by warp the tiles' scales, what the
+// tile in work needs of them -- 2^e of every key's blocks (fp32), and the
+// value factors as fp16 pairs in the order of P's fragments -- and the ring's
+// barriers.
 template <int D>
 struct Layout {
   static constexpr int G = D / kMxBlock;        // scale blocks of a row
   static constexpr int kChunks = D / 16;        // 16-byte chunks of a record
   static constexpr int kSc = D / 16;            // scale bytes of a record
   static constexpr int kTileBytes = kTile * D;
-  static constexpr int kStageBytes = kTileBytes + kTile * kSc;
-  static constexpr int kFactorBytes = kTile * G * 2;
-  static constexpr int kWarpBytes = kStages * kStageBytes + kFactorBytes;
-  // Chunk c of key `row` of a tile.
+  static constexpr int kScaleBytes = kTile * kSc;
+  static constexpr int kWarpTiles = kStages * kTileBytes;
+  // Per warp, after all warps' tiles:
+  static constexpr int kScales = 0;
+  static constexpr int kKeyScales = kScales + kStages * kScaleBytes;
+  static constexpr int kFactors = kKeyScales + kTile * G * 4;
+  static constexpr int kBarriers = kFactors + kTile * G * 2;
+  static constexpr int kWarpRest = kBarriers + 16 * ((kStages + 1) / 2);
+  static constexpr int kBytes = kWarps * (kWarpTiles + kWarpRest);
+  // Byte address of chunk c of key `row` of a tile: the 128- (64-) byte
+  // swizzle of a tensor map whose rows are the records.
   __device__ static __forceinline__ uint32_t chunk_at(int row, int c) {
     const int f = D == 128 ? (row & 7) : ((row >> 1) & 3);
     return row * D + ((c ^ f) << 4);
   }
 };
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+__device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
+
+// Byte g of w as the fp32 number 2^(byte - 127) (0 for byte 0).
+template <int kByte>
+__device__ __forceinline__ uint32_t e8m0_bits(uint32_t w) {
+  return (kByte == 3 ? w >> 1 : w << (23 - 8 * kByte)) & 0x7F800000u;
+}
 
 // The group (request, or selected row) a CTA works for.
 struct Group {
@@ -177,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   using Lay = Layout<D>;
   constexpr int G = Lay::G;
   constexpr int kRows = 8 * NT;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, t = lane & 3;
 
@@ -199,14 +225,120 @@ __global__ void __launch_bounds__(kThreads, 3)
   const int c1 = min(gr.cols, c0 + p.chunk);
   const bool whole = gr.cols <= p.chunk;
 
-  const uint32_t ring = smem_u32(smem) + warp * Lay::kWarpBytes;
-  const uint32_t factors = ring + kStages * Lay::kStageBytes;
+  uint8_t* const tiles_p = smem + warp * Lay::kWarpTiles;
+  uint8_t* const rest_p = smem + kWarps * Lay::kWarpTiles + warp * Lay::kWarpRest;
+  const uint32_t ring = smem_u32(tiles_p), rest = smem_u32(rest_p);
+  uint64_t* const bar = reinterpret_cast<uint64_t*>(rest_p + Lay::kBarriers);
+  if (!kSel) {
+    if (lane == 0) {
+#pragma unroll
+      for (int s = 0; s < kStages; ++s) mbar_init(&bar[s], 1);
+      fence_barrier_init();
+    }
+    __syncwarp();
+  }
+
+  // ------------------------------------------------------------------ loads
+  // Tiles of this warp: columns c0 + 64 (warp + 4 i), in stage i % kStages.
+  const int tiles = (c1 - c0 + kTile - 1) / kTile;
+  const int bs_mask = (1 << p.log_bs) - 1;
+  const int32_t* table = p.block_table + static_cast<int64_t>(gr.b) * p.max_blocks;
+  auto page_of = [&](int pos) {
+    int block = __ldg(table + (pos >> p.log_bs));
+    if (block < 0 || block >= p.num_blocks) {
+      record_error(p.err, kErrBadIndex);
+      block = 0;
+    }
+    return block * p.Hkv + head;  // records of this page and head: page << log_bs ..
+  };
+  // What a tile's loads need, found two tiles ahead.  Dense: lane i < 64 /
+  // rows holds the page of the tile's i-th run of `rows` tokens.  Selected: a
+  // lane holds the records of the columns `lane` and `lane + 32`.
+  const int rows = min(1 << p.log_bs, kTile);
+  uint32_t rec[2] = {0u, 0u};
+  bool has[2] = {false, false};
+  auto locate = [&](int tile) {
+    if constexpr (kSel) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int col = c0 + tile * kTile + lane + 32 * i;
+        int pos = -1;
+        if (col < c1) {
+          pos = __ldg(p.sel + static_cast<int64_t>(grp) * p.sel_k + col);
+          if (pos < -1 || pos >= gr.limit) {
+            record_error(p.err, kErrBadIndex);
+            pos = -1;
+          }
+        }
+        has[i] = pos >= 0;
+        rec[i] = has[i] ? (static_cast<uint32_t>(page_of(pos)) << p.log_bs) + (pos & bs_mask) : 0u;
+      }
+    } else {
+      const int pos = c0 + tile * kTile + lane * rows;
+      has[0] = lane * rows < kTile && pos < c1;
+      if (has[0]) rec[0] = page_of(pos);
+    }
+  };
+  // Starts the copies of the located tile into stage s; returns the columns
+  // (bit i of .x: column i, of .y: column 32 + i) of a selected tile.
+  auto fetch = [&](int s, int tile) {
+    uint2 cols = make_uint2(0u, 0u);
+    const uint32_t base = ring + s * Lay::kTileBytes;
+    const uint32_t sbase = rest + Lay::kScales + s * Lay::kScaleBytes;
+    if constexpr (kSel) {
+      cols.x = __ballot_sync(0xffffffffu, has[0]);
+      cols.y = __ballot_sync(0xffffffffu, has[1]);
+      if (cols.x | cols.y) {  // absent columns become zeros
+        constexpr int kPer = 32 / Lay::kChunks;  // records per instruction
+        const int c = lane % Lay::kChunks;
+#pragma unroll
+        for (int i = 0; i < kTile / kPer; ++i) {
+          const int row = i * kPer + lane / Lay::kChunks;
+          const bool upper = i >= kTile / kPer / 2;
+          const uint32_t rc = __shfl_sync(0xffffffffu, upper ? rec[1] : rec[0], row & 31);
+          const bool ok = ((upper ? cols.y : cols.x) >> (row & 31)) & 1;
+          cp_async16(base + Lay::chunk_at(row, c), p.cache + static_cast<int64_t>(rc) * D + c * 16,
+                     ok ? 16u : 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          cp_async_small<Lay::kSc>(sbase + (lane + 32 * i) * Lay::kSc,
+                                   p.scales + static_cast<int64_t>(rec[i]) * Lay::kSc,
+                                   has[i] ? Lay::kSc : 0);
+      }
+      cp_async_commit();
+    } else if (tile < tiles) {
+      // Whole runs of a page: what lies past the last column is masked.
+      const int n = __popc(__ballot_sync(0xffffffffu, has[0]));
+      if (lane == 0) mbar_arrive_expect_tx(&bar[s], n * rows * (D + Lay::kSc));
+      __syncwarp();
+      if (has[0]) {
+        const int at = (c0 + tile * kTile + lane * rows) & bs_mask;
+        tma_load_3d(tiles_p + s * Lay::kTileBytes + lane * rows * D, &p.tmap, &bar[s], 0, at,
+                    static_cast<int>(rec[0]));
+        bulk_load(sbase + lane * rows * Lay::kSc,
+                  p.scales + ((static_cast<int64_t>(rec[0]) << p.log_bs) + at) * Lay::kSc,
+                  rows * Lay::kSc, &bar[s]);
+      }
+    }
+    return cols;
+  };
+
+  uint2 cols[kStages];
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) {
+    locate(warp + s * kWarps);
+    cols[s] = fetch(s, warp + s * kWarps);
+  }
 
   // ---------------------------------------------------------------- queries
-  // B fragments: lane (r, t) holds row r's elements 32 g + 8 t .. + 7.
+  // B fragments: lane (r, t) holds row r's elements 32 g + 8 t .. + 7, times
+  // the softmax scale's sign.
   uint32_t qf[NT][G][4];
-  float f_scale[NT][2];  // S = f_scale * accumulator, for rows 2t and 2t + 1
-  int limit[NT][2];      // columns those rows see
+  float f[NT][2];    // base-2 logit = f * accumulator (f > 0), rows 2t and 2t + 1
+  int limit[NT][2];  // columns those rows see
+  const bool zero = p.scale_log2e == 0.f;
+  const float sign = zero ? 0.f : (p.scale_log2e < 0.f ? -1.f : 1.f);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int n = row0 + nt * 8 + r;
@@ -234,73 +366,18 @@ __global__ void __launch_bounds__(kThreads, 3)
       const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        qf[nt][g][i] = pack_f16(ldexpf(bf16_lo(w[i]), -E), ldexpf(bf16_hi(w[i]), -E));
+        qf[nt][g][i] =
+            pack_f16(ldexpf(bf16_lo(w[i]), -E) * sign, ldexpf(bf16_hi(w[i]), -E) * sign);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int e = __shfl_sync(0xffffffffu, E, (2 * t + i) * 4);
-      f_scale[nt][i] = ldexpf(p.scale_log2e, e);
+      f[nt][i] = zero ? 1.f : ldexpf(fabsf(p.scale_log2e), e);
       const int nn = row0 + nt * 8 + 2 * t + i;
       limit[nt][i] = kSel ? gr.cols : gr.L - p.next_n + min(nn / p.heads, p.next_n - 1) + 1;
     }
   }
   const int all_see = kSel ? gr.cols : gr.L - p.next_n + 1;  // columns every row sees
-
-  // ------------------------------------------------------------------ loads
-  // Tiles of this warp: columns c0 + 64 (warp + 4 i).  A lane finds the
-  // records of the tile's columns `lane` and `lane + 32`.
-  const int tiles = (c1 - c0 + kTile - 1) / kTile;
-  const int bs_mask = (1 << p.log_bs) - 1;
-  uint32_t rec[2];
-  bool has[2];
-  auto locate = [&](int tile) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int col = c0 + tile * kTile + lane + 32 * i;
-      int pos = -1;
-      if (tile < tiles && col < c1) {
-        pos = col;
-        if (kSel) {
-          pos = __ldg(p.sel + static_cast<int64_t>(grp) * p.sel_k + col);
-          if (pos < -1 || pos >= gr.limit) {
-            record_error(p.err, kErrBadIndex);
-            pos = -1;
-          }
-        }
-      }
-      has[i] = pos >= 0;
-      rec[i] = 0;
-      if (has[i]) {
-        int block = __ldg(p.block_table + static_cast<int64_t>(gr.b) * p.max_blocks +
-                          (pos >> p.log_bs));
-        if (block < 0 || block >= p.num_blocks) {
-          record_error(p.err, kErrBadIndex);
-          block = 0;
-        }
-        rec[i] = ((static_cast<uint32_t>(block) * p.Hkv + head) << p.log_bs) + (pos & bs_mask);
-      }
-    }
-  };
-  // Copies of the located tile into stage s; absent columns become zeros.
-  auto fetch = [&](int s, uint32_t mask0, uint32_t mask1) {
-    const uint32_t base = ring + s * Lay::kStageBytes;
-    constexpr int kPer = 32 / Lay::kChunks;  // records per instruction
-    const int c = lane % Lay::kChunks;
-#pragma unroll
-    for (int i = 0; i < kTile / kPer; ++i) {
-      const int row = i * kPer + lane / Lay::kChunks;
-      const bool upper = i >= kTile / kPer / 2;
-      const uint32_t rc = __shfl_sync(0xffffffffu, upper ? rec[1] : rec[0], row & 31);
-      const bool ok = ((upper ? mask1 : mask0) >> (row & 31)) & 1;
-      cp_async16(base + Lay::chunk_at(row, c), p.cache + static_cast<int64_t>(rc) * D + c * 16,
-                 ok ? 16u : 0u);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      cp_async_small<Lay::kSc>(base + Lay::kTileBytes + (lane + 32 * i) * Lay::kSc,
-                               p.scales + static_cast<int64_t>(rec[i]) * Lay::kSc,
-                               has[i] ? Lay::kSc : 0);
-  };
 
   float o[NT][2 * G][4];
 #pragma unroll
@@ -309,69 +386,96 @@ __global__ void __launch_bounds__(kThreads, 3)
     for (int i = 0; i < 2 * G; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
-  float m[NT][2], l[NT][2];
+  // m: reference of the exponents, as an accumulator value.  It is raised to
+  // the running maximum only when a logit passes it by kSlack (base 2), so
+  // most tiles need no maximum across lanes and no rescaling; weights are then
+  // at most 2^kSlack, which fp16 and fp32 hold as well as 1.
+  constexpr float kSlack = 8.f;
+  float m[NT][2], thr[NT][2], z[NT][2], l[NT][2];  // thr = m + kSlack / f, z = f m
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
-  int top = 0;  // o is in units of 2^(top - 127)
-
-  uint32_t mask[kStages][2];
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-  for (int s = 0; s < kStages; ++s) {
-    locate(warp + s * kWarps);
-    mask[s][0] = __ballot_sync(0xffffffffu, has[0]);
-    mask[s][1] = __ballot_sync(0xffffffffu, has[1]);
-    if (mask[s][0] | mask[s][1]) fetch(s, mask[s][0], mask[s][1]);
-    cp_async_commit();
-  }
+    for (int i = 0; i < 2; ++i)
+      m[nt][i] = thr[nt][i] = -INFINITY, z[nt][i] = l[nt][i] = 0.f;
+  float unit = 0.f, inv_unit = 0.f;  // o is in units of the largest value scale so far
 
   // Lane addresses that do not change from tile to tile: the key chunk of
   // rows pi(r) (+ 8, + 16 ..), the value units of rows 2t and (2t+1)^4.
   const int prow = r ^ ((r & 1) << 2);
-  const uint32_t k_at = D == 128 ? Lay::chunk_at(prow, t) : Lay::chunk_at(prow, t >> 1) + (t & 1) * 8;
+  const uint32_t k_at =
+      D == 128 ? Lay::chunk_at(prow, t) : Lay::chunk_at(prow, t >> 1) + (t & 1) * 8;
   const int v_row[2] = {2 * t, (2 * t + 1) ^ 4};
   uint32_t v_at[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
     v_at[i] = D == 128 ? Lay::chunk_at(v_row[i], 4 + (r >> 1)) + (r & 1) * 8
                        : Lay::chunk_at(v_row[i], 2 + (r >> 2)) + (r & 3) * 4;
+  const uint32_t ks_at = rest + Lay::kKeyScales, fac_at = rest + Lay::kFactors;
 
   int s = 0;
-  for (int tile = warp; tile < tiles; tile += kWarps, s ^= 1) {
+  uint32_t phase = 0;
+  bool ok = true;
+  for (int tile = warp; tile < tiles; tile += kWarps) {
     locate(tile + kStages * kWarps);  // two tiles on: its loads return under this tile's work
-    cp_async_wait<kStages - 1>();
-    __syncwarp();
-    const uint32_t base = ring + s * Lay::kStageBytes;
-    const uint32_t m0 = s ? mask[1][0] : mask[0][0], m1 = s ? mask[1][1] : mask[0][1];
-    if (m0 | m1) {
-      // -------------------------------------------------- value scale factors
-      const uint32_t sc_base = base + Lay::kTileBytes;
-      uint32_t nan0 = 0, nan1 = 0;  // keys with a NaN scale
+    const int col0 = c0 + tile * kTile;
+    uint2 live;  // columns of this tile
+    if constexpr (kSel) {
+      cp_async_wait<kStages - 1>();
+      __syncwarp();
+      live = s ? cols[1] : cols[0];
+    } else {
+      ok = mbar_wait_bounded(&bar[s], phase, nullptr);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      const int n = c1 - col0;
+      live.x = n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+      live.y = n >= 64 ? 0xffffffffu : (n > 32 ? (1u << (n - 32)) - 1u : 0u);
+    }
+    const uint32_t base = ring + s * Lay::kTileBytes;
+    if (live.x | live.y) {
+      uint32_t nan_x = 0, nan_y = 0;  // keys with a NaN scale
+      // ---------------------------------------------------------------- scales
+      // Lane (q8, t) takes the keys of rows 2t and 2t + 1 of the q8-th group
+      // of eight: one fragment pair.
       {
+        const uint32_t sbase = rest + Lay::kScales + s * Lay::kScaleBytes;
         uint32_t ks[2], vs[2];
+        int key[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {  // absent columns are zero
+        for (int i = 0; i < 2; ++i) {
+          key[i] = r * 8 + v_row[i];
           if constexpr (D == 128) {
-            const uint2 u = lds64(sc_base + (lane + 32 * i) * 8);
+            const uint2 u = lds64(sbase + key[i] * 8);
             ks[i] = u.x, vs[i] = u.y;
           } else {
-            const uint32_t u = lds32(sc_base + (lane + 32 * i) * 4);
+            const uint32_t u = lds32(sbase + key[i] * 4);
             ks[i] = u & 0xFFFFu, vs[i] = u >> 16;
           }
+          if (!(((r >= 4 ? live.y : live.x) >> (key[i] & 31)) & 1)) ks[i] = vs[i] = 0u;
         }
-        if (__any_sync(0xffffffffu, has_ff(ks[0]) | has_ff(ks[1]) | has_ff(vs[0]) | has_ff(vs[1]))) {
+        if (__any_sync(0xffffffffu,
+                       has_ff(ks[0]) | has_ff(ks[1]) | has_ff(vs[0]) | has_ff(vs[1]))) {
           // NaN scales (rare).  A key's makes its logits NaN below; a value's
           // makes its 32 channels of every row that sees the column NaN, here,
           // and takes no part in the products.
-          nan0 = __ballot_sync(0xffffffffu, has_ff(ks[0]) != 0);
-          nan1 = __ballot_sync(0xffffffffu, has_ff(ks[1]) != 0);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            uint32_t keys = __ballot_sync(0xffffffffu, has_ff(vs[i]) != 0);
-            while (keys) {
-              const int src = __ffs(keys) - 1;
-              keys &= keys - 1;
+            uint32_t from = __ballot_sync(0xffffffffu, has_ff(ks[i]) != 0);
+            while (from) {
+              const int src = __ffs(from) - 1;
+              from &= from - 1;
+              const int k = __shfl_sync(0xffffffffu, key[i], src);
+              if (k < 32) nan_x |= 1u << k;
+              else nan_y |= 1u << (k - 32);
+            }
+            from = __ballot_sync(0xffffffffu, has_ff(vs[i]) != 0);
+            while (from) {
+              const int src = __ffs(from) - 1;
+              from &= from - 1;
               const uint32_t w = __shfl_sync(0xffffffffu, vs[i], src);
-              const int col = c0 + tile * kTile + 32 * i + src;
+              const int col = col0 + __shfl_sync(0xffffffffu, key[i], src);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -388,15 +492,29 @@ __global__ void __launch_bounds__(kThreads, 3)
               if (((vs[i] >> (8 * g)) & 255u) == 255u) vs[i] &= ~(255u << (8 * g));
           }
         }
-        uint32_t mx = 0;
+        uint32_t vf[2][G];
+        uint32_t top = 0;  // scales order as their bits
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i) {
+          uint32_t kf[G];
+          kf[0] = e8m0_bits<0>(ks[i]), kf[1] = e8m0_bits<1>(ks[i]);
+          vf[i][0] = e8m0_bits<0>(vs[i]), vf[i][1] = e8m0_bits<1>(vs[i]);
+          if constexpr (D == 128) {
+            kf[2] = e8m0_bits<2>(ks[i]), kf[3] = e8m0_bits<3>(ks[i]);
+            vf[i][2] = e8m0_bits<2>(vs[i]), vf[i][3] = e8m0_bits<3>(vs[i]);
+            sts128(ks_at + key[i] * 16, kf[0], kf[1], kf[2], kf[3]);
+          } else {
+            sts64(ks_at + key[i] * 8, kf[0], kf[1]);
+          }
 #pragma unroll
-          for (int g = 0; g < G; ++g) mx = max(mx, (vs[i] >> (8 * g)) & 255u);
-        mx = __reduce_max_sync(0xffffffffu, mx);
-        if (static_cast<int>(mx) > top) {
-          const float down = exp2f(static_cast<float>(top - static_cast<int>(mx)));
-          top = static_cast<int>(mx);
+          for (int g = 0; g < G; ++g) top = max(top, vf[i][g]);
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (top > __float_as_uint(unit)) {
+          const float up = __uint_as_float(top);
+          const float down = unit == 0.f ? 0.f : unit / up;
+          unit = up;
+          inv_unit = 1.f / up;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -404,211 +522,208 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll
               for (int j = 0; j < 4; ++j) o[nt][i][j] *= down;
         }
+        uint32_t fac[G];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          // Key `lane + 32 i` is row i8 ^ (odd: 4) of its group of eight.
-          const int key = lane + 32 * i;
-          const int row = (key & 7) ^ ((key & 1) << 2);
-          const uint32_t at = factors + ((key >> 3) * 4 + (row >> 1)) * (4 * G) + (row & 1) * 2;
-          const bool ok = i ? (m1 >> lane) & 1 : (m0 >> lane) & 1;
-#pragma unroll
-          for (int g = 0; g < G; ++g)
-            sts16(at + 4 * g, ok ? scale_f16((vs[i] >> (8 * g)) & 255u, top) : 0u);
-        }
+        for (int g = 0; g < G; ++g)
+          fac[g] = pack_f16(__uint_as_float(vf[0][g]) * inv_unit,
+                            __uint_as_float(vf[1][g]) * inv_unit);
+        if constexpr (D == 128) sts128(fac_at + lane * 16, fac[0], fac[1], fac[2], fac[3]);
+        else sts64(fac_at + lane * 8, fac[0], fac[1]);
         __syncwarp();
       }
-      // ------------------------------------------------------------ S^T = K q^T
-      float sacc[4][NT][4];
+      const bool clean =
+          (nan_x | nan_y) == 0 && (kSel ? (live.x & live.y) == 0xffffffffu
+                                        : col0 + kTile <= min(c1, all_see));
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        // ---------------------------------------------------------- S^T = K q^T
+        const uint32_t hbase = base + half * 32 * D;
+        float sacc[2][NT][4];
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        uint32_t kw[2][G];
-        uint32_t ks[2];
+        for (int mt = 0; mt < 2; ++mt) {
+          uint32_t kw[2][G];
+          float ks[2][G];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t at = base + (mt * 16 + h * 8) * D + k_at;
-          if constexpr (D == 128) {
-            const uint4 u = lds128(at);
-            kw[h][0] = u.x, kw[h][1] = u.y, kw[h][2] = u.z, kw[h][3] = u.w;
-          } else {
-            const uint2 u = lds64(at);
-            kw[h][0] = u.x, kw[h][1] = u.y;
-          }
-          ks[h] = lds32(sc_base + (mt * 16 + h * 8 + prow) * Lay::kSc);
-        }
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          const float s0 = __uint_as_float(((ks[0] >> (8 * g)) & 255u) << 23);
-          const float s1 = __uint_as_float(((ks[1] >> (8 * g)) & 255u) << 23);
-          const uint32_t a0 = e2m1x2_to_f16x2<0>(kw[0][g]), a1 = e2m1x2_to_f16x2<0>(kw[1][g]);
-          const uint32_t a2 = e2m1x2_to_f16x2<1>(kw[0][g]), a3 = e2m1x2_to_f16x2<1>(kw[1][g]);
-          const uint32_t b0 = e2m1x2_to_f16x2<2>(kw[0][g]), b1 = e2m1x2_to_f16x2<2>(kw[1][g]);
-          const uint32_t b2 = e2m1x2_to_f16x2<3>(kw[0][g]), b3 = e2m1x2_to_f16x2<3>(kw[1][g]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816(c, a0, a1, a2, a3, qf[nt][g][0], qf[nt][g][1]);
-            mma16816(c, b0, b1, b2, b3, qf[nt][g][2], qf[nt][g][3]);
-            if (g == 0) {
-              sacc[mt][nt][0] = c[0] * s0, sacc[mt][nt][1] = c[1] * s0;
-              sacc[mt][nt][2] = c[2] * s1, sacc[mt][nt][3] = c[3] * s1;
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t at = hbase + (mt * 16 + h * 8) * D + k_at;
+            const uint32_t sat = ks_at + (half * 32 + mt * 16 + h * 8 + prow) * (4 * G);
+            if constexpr (D == 128) {
+              const uint4 u = lds128(at), v = lds128(sat);
+              kw[h][0] = u.x, kw[h][1] = u.y, kw[h][2] = u.z, kw[h][3] = u.w;
+              ks[h][0] = __uint_as_float(v.x), ks[h][1] = __uint_as_float(v.y);
+              ks[h][2] = __uint_as_float(v.z), ks[h][3] = __uint_as_float(v.w);
             } else {
-              sacc[mt][nt][0] = fmaf(c[0], s0, sacc[mt][nt][0]);
-              sacc[mt][nt][1] = fmaf(c[1], s0, sacc[mt][nt][1]);
-              sacc[mt][nt][2] = fmaf(c[2], s1, sacc[mt][nt][2]);
-              sacc[mt][nt][3] = fmaf(c[3], s1, sacc[mt][nt][3]);
+              const uint2 u = lds64(at), v = lds64(sat);
+              kw[h][0] = u.x, kw[h][1] = u.y;
+              ks[h][0] = __uint_as_float(v.x), ks[h][1] = __uint_as_float(v.y);
+            }
+          }
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const uint32_t a0 = e2m1x2_to_f16x2<0>(kw[0][g]), a1 = e2m1x2_to_f16x2<0>(kw[1][g]);
+            const uint32_t a2 = e2m1x2_to_f16x2<1>(kw[0][g]), a3 = e2m1x2_to_f16x2<1>(kw[1][g]);
+            const uint32_t b0 = e2m1x2_to_f16x2<2>(kw[0][g]), b1 = e2m1x2_to_f16x2<2>(kw[1][g]);
+            const uint32_t b2 = e2m1x2_to_f16x2<3>(kw[0][g]), b3 = e2m1x2_to_f16x2<3>(kw[1][g]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float c[4] = {0.f, 0.f, 0.f, 0.f};
+              mma16816(c, a0, a1, a2, a3, qf[nt][g][0], qf[nt][g][1]);
+              mma16816(c, b0, b1, b2, b3, qf[nt][g][2], qf[nt][g][3]);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                sacc[mt][nt][j] =
+                    g == 0 ? c[j] * ks[j >> 1][g] : fmaf(c[j], ks[j >> 1][g], sacc[mt][nt][j]);
             }
           }
         }
-      }
-      // --------------------------------------------------------------- softmax
-      const int col0 = c0 + tile * kTile;
-      const bool clean = (nan0 | nan1) == 0 && (kSel ? (m0 & m1) == 0xffffffffu
-                                                     : col0 + kTile <= min(c1, all_see));
+        // ------------------------------------------------------------- softmax
+        const uint32_t hlive = half ? live.y : live.x;
+        if (!clean) {
+          const uint32_t hnan = half ? nan_y : nan_x;
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt)
+          for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sacc[mt][nt][j] *= f_scale[nt][j & 1];
-      if (!clean) {
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int key = mt * 16 + h * 8 + prow;
-            const bool here = ((mt >= 2 ? m1 : m0) >> (key & 31)) & 1;
-            const bool nan = ((mt >= 2 ? nan1 : nan0) >> (key & 31)) & 1;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                if (nan) sacc[mt][nt][2 * h + i] = __uint_as_float(0x7FC00000u);
-                if (!here || (!kSel && col0 + key >= limit[nt][i]))
-                  sacc[mt][nt][2 * h + i] = -INFINITY;
-              }
-          }
-      }
-      if constexpr (kScores) {
-        float* dst = p.scores + (static_cast<int64_t>(grp) * per_split + ht) * p.cols * kRows;
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int col = col0 + mt * 16 + h * 8 + prow;
-            if (col < c1) {
+            for (int h = 0; h < 2; ++h) {
+              const int key = mt * 16 + h * 8 + prow;
+              const bool here = (hlive >> key) & 1, nan = (hnan >> key) & 1;
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
-                *reinterpret_cast<float2*>(dst + static_cast<int64_t>(col) * kRows + nt * 8 +
-                                           2 * t) =
-                    make_float2(sacc[mt][nt][2 * h], sacc[mt][nt][2 * h + 1]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  if (nan) sacc[mt][nt][2 * h + i] = __uint_as_float(0x7FC00000u);
+                  if (!here || (!kSel && col0 + half * 32 + key >= limit[nt][i]))
+                    sacc[mt][nt][2 * h + i] = -INFINITY;
+                }
             }
-          }
-      }
-      float mn[NT][2];
-      bool up = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float x = m[nt][i];
-#pragma unroll
-          for (int mt = 0; mt < 4; ++mt)
-            x = fmaxf(x, fmaxf(sacc[mt][nt][i], sacc[mt][nt][2 + i]));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          mn[nt][i] = x;
-          up |= x > m[nt][i];
         }
-      if (__any_sync(0xffffffffu, up)) {
+        if constexpr (kScores) {
+          float* dst = p.scores + (static_cast<int64_t>(grp) * per_split + ht) * p.cols * kRows;
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int col = col0 + half * 32 + mt * 16 + h * 8 + prow;
+              if (col < c1) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  *reinterpret_cast<float2*>(dst + static_cast<int64_t>(col) * kRows + nt * 8 +
+                                             2 * t) =
+                      make_float2(sacc[mt][nt][2 * h] * f[nt][0],
+                                  sacc[mt][nt][2 * h + 1] * f[nt][1]);
+              }
+            }
+        }
+        float x[NT][2];
+        bool up = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            // m = -inf: nothing accumulated yet (l and o are zero).
-            const float a = m[nt][i] == -INFINITY ? 0.f : ex2(m[nt][i] - mn[nt][i]);
-            m[nt][i] = mn[nt][i];
-            l[nt][i] *= a;
-#pragma unroll
-            for (int j = 0; j < 2 * G; ++j) o[nt][j][i] *= a, o[nt][j][2 + i] *= a;
+            x[nt][i] = fmaxf(fmaxf(sacc[0][nt][i], sacc[0][nt][2 + i]),
+                             fmaxf(sacc[1][nt][i], sacc[1][nt][2 + i]));
+            up |= x[nt][i] > thr[nt][i];
           }
-      }
-      uint32_t pf[4][NT][2];  // P as B fragments: row r, keys 2t, 2t+1 (+ 8)
+        if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        // A row that has seen no column yet: every exponent is -inf.
-        const float z0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
-        const float z1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
-          const float p0 = ex2(sacc[mt][nt][0] - z0), p1 = ex2(sacc[mt][nt][1] - z1);
-          const float p2 = ex2(sacc[mt][nt][2] - z0), p3 = ex2(sacc[mt][nt][3] - z1);
-          l[nt][0] += p0 + p2;
-          l[nt][1] += p1 + p3;
-          pf[mt][nt][0] = transpose8x8(pack_f16(p0, p1));
-          pf[mt][nt][1] = transpose8x8(pack_f16(p2, p3));
+            for (int i = 0; i < 2; ++i) {
+              float v = fmaxf(x[nt][i], __shfl_xor_sync(0xffffffffu, x[nt][i], 4));
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+              v = fmaxf(v, m[nt][i]);
+              // m = -inf: nothing accumulated yet (l and o are zero).
+              const float a = m[nt][i] == -INFINITY ? 0.f : ex2((m[nt][i] - v) * f[nt][i]);
+              m[nt][i] = v;
+              thr[nt][i] = v + kSlack / f[nt][i];
+              // A row that has seen no column: every exponent is -inf.
+              z[nt][i] = v == -INFINITY ? 0.f : v * f[nt][i];
+              l[nt][i] *= a;
+#pragma unroll
+              for (int j = 0; j < 2 * G; ++j) o[nt][j][i] *= a, o[nt][j][2 + i] *= a;
+            }
         }
-      }
-      // ------------------------------------------------------------ O^T += V^T P
+        uint32_t pf[2][NT][2];  // P as B fragments: row r, keys 2t, 2t+1 (+ 8)
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        // lo/hi: the even/odd codes of this lane's units for the key pairs
-        // (2t, 2t+1) and (2t+8, 2t+9), one pair per byte.
-        uint32_t lo[2][G / 2], hi[2][G / 2];
-        uint32_t fac[2][G];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t va[G / 2], vb[G / 2];
-          const uint32_t at = base + (mt * 16 + h * 8) * D;
-          if constexpr (D == 128) {
-            const uint2 ua = lds64(at + v_at[0]), ub = lds64(at + v_at[1]);
-            va[0] = ua.x, va[1] = ua.y, vb[0] = ub.x, vb[1] = ub.y;
-            const uint4 u = lds128(factors + ((mt * 2 + h) * 4 + t) * 16);
-            fac[h][0] = u.x, fac[h][1] = u.y, fac[h][2] = u.z, fac[h][3] = u.w;
-          } else {
-            va[0] = lds32(at + v_at[0]), vb[0] = lds32(at + v_at[1]);
-            const uint2 u = lds64(factors + ((mt * 2 + h) * 4 + t) * 8);
-            fac[h][0] = u.x, fac[h][1] = u.y;
+          for (int mt = 0; mt < 2; ++mt) {
+            const float p0 = ex2(fmaf(sacc[mt][nt][0], f[nt][0], -z[nt][0]));
+            const float p1 = ex2(fmaf(sacc[mt][nt][1], f[nt][1], -z[nt][1]));
+            const float p2 = ex2(fmaf(sacc[mt][nt][2], f[nt][0], -z[nt][0]));
+            const float p3 = ex2(fmaf(sacc[mt][nt][3], f[nt][1], -z[nt][1]));
+            l[nt][0] += p0 + p2;
+            l[nt][1] += p1 + p3;
+            pf[mt][nt][0] = transpose8x8(pack_f16(p0, p1));
+            pf[mt][nt][1] = transpose8x8(pack_f16(p2, p3));
+          }
+        // ---------------------------------------------------------- O^T += V^T P
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          // lo/hi: the even/odd codes of this lane's units for the key pairs
+          // (2t, 2t+1) and (2t+8, 2t+9), one pair per byte.
+          uint32_t lo[2][G / 2], hi[2][G / 2];
+          uint32_t fac[2][G];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t va[G / 2], vb[G / 2];
+            const uint32_t at = hbase + (mt * 16 + h * 8) * D;
+            const uint32_t fat = fac_at + ((half * 4 + mt * 2 + h) * 4 + t) * (4 * G);
+            if constexpr (D == 128) {
+              const uint2 ua = lds64(at + v_at[0]), ub = lds64(at + v_at[1]);
+              va[0] = ua.x, va[1] = ua.y, vb[0] = ub.x, vb[1] = ub.y;
+              const uint4 u = lds128(fat);
+              fac[h][0] = u.x, fac[h][1] = u.y, fac[h][2] = u.z, fac[h][3] = u.w;
+            } else {
+              va[0] = lds32(at + v_at[0]), vb[0] = lds32(at + v_at[1]);
+              const uint2 u = lds64(fat);
+              fac[h][0] = u.x, fac[h][1] = u.y;
+            }
+#pragma unroll
+            for (int i = 0; i < G / 2; ++i) {
+              lo[h][i] = (va[i] & 0x0F0F0F0Fu) | ((vb[i] << 4) & 0xF0F0F0F0u);
+              hi[h][i] = ((va[i] >> 4) & 0x0F0F0F0Fu) | (vb[i] & 0xF0F0F0F0u);
+            }
           }
 #pragma unroll
-          for (int i = 0; i < G / 2; ++i) {
-            lo[h][i] = (va[i] & 0x0F0F0F0Fu) | ((vb[i] << 4) & 0xF0F0F0F0u);
-            hi[h][i] = ((va[i] >> 4) & 0x0F0F0F0Fu) | (vb[i] & 0xF0F0F0F0u);
-          }
-        }
+          for (int g = 0; g < G; ++g) {
+            // Channels 32 g + 4 r + {0, 1} (first tile) and + {2, 3} (second).
+            const uint32_t l0 = lo[0][g / 2], h0 = hi[0][g / 2];
+            const uint32_t l1 = lo[1][g / 2], h1 = hi[1][g / 2];
+            uint32_t a[2][4];
+            if (g % 2 == 0) {
+              a[0][0] = e2m1x2_to_f16x2<0>(l0), a[0][1] = e2m1x2_to_f16x2<0>(h0);
+              a[0][2] = e2m1x2_to_f16x2<0>(l1), a[0][3] = e2m1x2_to_f16x2<0>(h1);
+              a[1][0] = e2m1x2_to_f16x2<1>(l0), a[1][1] = e2m1x2_to_f16x2<1>(h0);
+              a[1][2] = e2m1x2_to_f16x2<1>(l1), a[1][3] = e2m1x2_to_f16x2<1>(h1);
+            } else {
+              a[0][0] = e2m1x2_to_f16x2<2>(l0), a[0][1] = e2m1x2_to_f16x2<2>(h0);
+              a[0][2] = e2m1x2_to_f16x2<2>(l1), a[0][3] = e2m1x2_to_f16x2<2>(h1);
+              a[1][0] = e2m1x2_to_f16x2<3>(l0), a[1][1] = e2m1x2_to_f16x2<3>(h0);
+              a[1][2] = e2m1x2_to_f16x2<3>(l1), a[1][3] = e2m1x2_to_f16x2<3>(h1);
+            }
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          // Channels 32 g + 4 r + {0, 1} (first tile) and + {2, 3} (second).
-          const uint32_t l0 = lo[0][g / 2], h0 = hi[0][g / 2], l1 = lo[1][g / 2], h1 = hi[1][g / 2];
-          uint32_t a[2][4];
-          if (g % 2 == 0) {
-            a[0][0] = e2m1x2_to_f16x2<0>(l0), a[0][1] = e2m1x2_to_f16x2<0>(h0);
-            a[0][2] = e2m1x2_to_f16x2<0>(l1), a[0][3] = e2m1x2_to_f16x2<0>(h1);
-            a[1][0] = e2m1x2_to_f16x2<1>(l0), a[1][1] = e2m1x2_to_f16x2<1>(h0);
-            a[1][2] = e2m1x2_to_f16x2<1>(l1), a[1][3] = e2m1x2_to_f16x2<1>(h1);
-          } else {
-            a[0][0] = e2m1x2_to_f16x2<2>(l0), a[0][1] = e2m1x2_to_f16x2<2>(h0);
-            a[0][2] = e2m1x2_to_f16x2<2>(l1), a[0][3] = e2m1x2_to_f16x2<2>(h1);
-            a[1][0] = e2m1x2_to_f16x2<3>(l0), a[1][1] = e2m1x2_to_f16x2<3>(h0);
-            a[1][2] = e2m1x2_to_f16x2<3>(l1), a[1][3] = e2m1x2_to_f16x2<3>(h1);
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint32_t b0 = mul_f16x2(pf[mt][nt][0], fac[0][g]);
-            const uint32_t b1 = mul_f16x2(pf[mt][nt][1], fac[1][g]);
-            mma16816(o[nt][2 * g], a[0][0], a[0][1], a[0][2], a[0][3], b0, b1);
-            mma16816(o[nt][2 * g + 1], a[1][0], a[1][1], a[1][2], a[1][3], b0, b1);
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint32_t b0 = mul_f16x2(pf[mt][nt][0], fac[0][g]);
+              const uint32_t b1 = mul_f16x2(pf[mt][nt][1], fac[1][g]);
+              mma16816(o[nt][2 * g], a[0][0], a[0][1], a[0][2], a[0][3], b0, b1);
+              mma16816(o[nt][2 * g + 1], a[1][0], a[1][1], a[1][2], a[1][3], b0, b1);
+            }
           }
         }
       }
     }
     __syncwarp();
-    const uint32_t n0 = __ballot_sync(0xffffffffu, has[0]);
-    const uint32_t n1 = __ballot_sync(0xffffffffu, has[1]);
-    if (n0 | n1) fetch(s, n0, n1);
-    cp_async_commit();
-    if (s) mask[1][0] = n0, mask[1][1] = n1;
-    else mask[0][0] = n0, mask[0][1] = n1;
+    const uint2 c = fetch(s, tile + kStages * kWarps);
+    if (s) cols[1] = c;
+    else cols[0] = c;
+    s = s + 1 == kStages ? 0 : s + 1;
+    phase ^= s == 0;
+  }
+  if (!kSel && !ok) {
+    // A copy never came: report, and give the others their time to land.
+    if (lane == 0) record_error(p.err, kErrTimeout);
+    for (int i = 0; i < kStages; ++i) mbar_wait_bounded(&bar[i], i < s ? phase ^ 1u : phase, nullptr);
   }
 
   // ------------------------------------------- join the four warps, write out
@@ -616,7 +731,6 @@ __global__ void __launch_bounds__(kThreads, 3)
   __syncthreads();
   float* so = reinterpret_cast<float*>(smem);              // [warp][row][D]
   float* sml = so + kWarps * kRows * D;                    // [warp][row][2]
-  const float unit = exp2f(static_cast<float>(top - 127));
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -627,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 3)
       x += __shfl_xor_sync(0xffffffffu, x, 16);
       const int row = nt * 8 + 2 * t + i;
       if (r == 0) {
-        sml[(warp * kRows + row) * 2] = m[nt][i];
+        sml[(warp * kRows + row) * 2] = m[nt][i] == -INFINITY ? -INFINITY : z[nt][i];
         sml[(warp * kRows + row) * 2 + 1] = x;
       }
       float* dst = so + (warp * kRows + row) * D;
@@ -644,12 +758,12 @@ __global__ void __launch_bounds__(kThreads, 3)
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sml[(w * kRows + row) * 2]);
-    const float z = M == -INFINITY ? 0.f : M;
+    const float z0 = M == -INFINITY ? 0.f : M;
     float L = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = ex2(sml[(w * kRows + row) * 2] - z);
+      const float f = ex2(sml[(w * kRows + row) * 2] - z0);
       L = fmaf(sml[(w * kRows + row) * 2 + 1], f, L);
       const float4 x = *reinterpret_cast<const float4*>(so + (w * kRows + row) * D + d);
       a.x = fmaf(x.x, f, a.x), a.y = fmaf(x.y, f, a.y);
@@ -789,7 +903,7 @@ __global__ void __launch_bounds__(1024)
 template <int D, int NT, bool kSel, bool kScores>
 cudaError_t launch_one(const Kv4AttnParams& p, cudaStream_t s) {
   using Lay = Layout<D>;
-  constexpr int kRing = kWarps * Lay::kWarpBytes;
+  constexpr int kRing = Lay::kBytes;
   constexpr int kJoin = kWarps * 8 * NT * (D + 2) * 4;
   constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
   auto* fn = kv4_attn_kernel<D, NT, kSel, kScores>;
