@@ -138,7 +138,10 @@ cudaError_t launch_kv4_gather(const void* cache, const void* scales, const int64
                               int Hkv, int D, int num_blocks, int block_size, void* k, void* v,
                               uint32_t* err, cudaStream_t s);
 
-// Decode attention (dsa_kv4_attn.cu).  A group is what shares its columns: a
+// Decode attention (dsa_kv4_attn.cu).  Columns a warp takes at a time: the
+// height of the records' tensor-map box is the smaller of this and a page.
+constexpr int kKv4Tile = 64;
+// A group is what shares its columns: a
 // request (every key), or a query row (selected keys).
 struct Kv4AttnParams {
   CUtensorMap tmap;        // the records, [num_blocks*Hkv, block_size, D bytes] (every key)

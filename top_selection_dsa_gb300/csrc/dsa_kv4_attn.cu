@@ -43,10 +43,11 @@
 namespace dsa {
 namespace {
 
-constexpr int kTile = 64;       // columns a warp takes at a time
+constexpr int kTile = kKv4Tile;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 2;
+constexpr int kCtasPerSm = 3;   // registers (168 a thread) and shared memory
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
@@ -72,6 +73,15 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same from zero.
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -121,7 +131,7 @@ __device__ __forceinline__ uint32_t has_ff(uint32_t w) {
 // tile in work needs of them -- 2^e of every key's blocks (fp32), and the
 // value factors as fp16 pairs in the order of P's fragments -- and the ring's
 // barriers.
-template <int D>
+template <int D, int NT>
 struct Layout {
   static constexpr int G = D / kMxBlock;        // scale blocks of a row
   static constexpr int kChunks = D / 16;        // 16-byte chunks of a record
@@ -132,10 +142,13 @@ struct Layout {
   // Per warp, after all warps' tiles:
   static constexpr int kScales = 0;
   static constexpr int kKeyScales = kScales + kStages * kScaleBytes;
-  static constexpr int kFactors = kKeyScales + kTile * G * 4;
+  static constexpr int kFactors = kKeyScales + (NT > 1 ? 0 : kTile * G * 4);
   static constexpr int kBarriers = kFactors + kTile * G * 2;
-  static constexpr int kWarpRest = kBarriers + 16 * ((kStages + 1) / 2);
-  static constexpr int kBytes = kWarps * (kWarpTiles + kWarpRest);
+  static constexpr int kWarpRest = (kBarriers + 8 * kStages + 15) / 16 * 16;
+  // Then, with two row tiles, the query fragments and their factors.
+  static constexpr int kQueries = kWarps * (kWarpTiles + kWarpRest);
+  static constexpr int kFactorF = kQueries + (NT > 1 ? NT * G * 32 * 16 : 0);
+  static constexpr int kBytes = kFactorF + (NT > 1 ? NT * 8 * 4 : 0);
   // Byte address of chunk c of key `row` of a tile: the 128- (64-) byte
   // swizzle of a tensor map whose rows are the records.
   __device__ static __forceinline__ uint32_t chunk_at(int row, int c) {
@@ -198,9 +211,9 @@ __device__ __forceinline__ int64_t head_row(const Kv4AttnParams& p, int g, int h
 }
 
 template <int D, int NT, bool kSel, bool kScores>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     kv4_attn_kernel(const __grid_constant__ Kv4AttnParams p) {
-  using Lay = Layout<D>;
+  using Lay = Layout<D, NT>;
   constexpr int G = Lay::G;
   constexpr int kRows = 8 * NT;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -243,52 +256,59 @@ __global__ void __launch_bounds__(kThreads, 3)
   const int tiles = (c1 - c0 + kTile - 1) / kTile;
   const int bs_mask = (1 << p.log_bs) - 1;
   const int32_t* table = p.block_table + static_cast<int64_t>(gr.b) * p.max_blocks;
-  auto page_of = [&](int pos) {
-    int block = __ldg(table + (pos >> p.log_bs));
+  // Records of a page and head: result << log_bs ..
+  auto page_of = [&](int block) {
     if (block < 0 || block >= p.num_blocks) {
       record_error(p.err, kErrBadIndex);
       block = 0;
     }
-    return block * p.Hkv + head;  // records of this page and head: page << log_bs ..
+    return static_cast<uint32_t>(block) * p.Hkv + head;
   };
-  // What a tile's loads need, found two tiles ahead.  Dense: lane i < 64 /
-  // rows holds the page of the tile's i-th run of `rows` tokens.  Selected: a
-  // lane holds the records of the columns `lane` and `lane + 32`.
+  // What a tile's loads need is read ahead of them, and looked at only when
+  // they are issued.  Dense: lane i < 64 / rows reads the page of the tile's
+  // i-th run of `rows` tokens.  Selected: a lane has the columns `lane` and
+  // `lane + 32`, their positions read one tile before their pages.
   const int rows = min(1 << p.log_bs, kTile);
-  uint32_t rec[2] = {0u, 0u};
-  bool has[2] = {false, false};
+  int pos[2] = {-1, -1}, next_pos[2] = {-1, -1}, block[2] = {0, 0};
+  auto read_columns = [&](int tile) {  // selected: this lane's positions of `tile`
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int col = c0 + tile * kTile + lane + 32 * i;
+      next_pos[i] = col < c1 ? __ldg(p.sel + static_cast<int64_t>(grp) * p.sel_k + col) : -1;
+    }
+  };
   auto locate = [&](int tile) {
     if constexpr (kSel) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int col = c0 + tile * kTile + lane + 32 * i;
-        int pos = -1;
-        if (col < c1) {
-          pos = __ldg(p.sel + static_cast<int64_t>(grp) * p.sel_k + col);
-          if (pos < -1 || pos >= gr.limit) {
-            record_error(p.err, kErrBadIndex);
-            pos = -1;
-          }
+        pos[i] = next_pos[i];
+        if (pos[i] < -1 || pos[i] >= gr.limit) {
+          record_error(p.err, kErrBadIndex);
+          pos[i] = -1;
         }
-        has[i] = pos >= 0;
-        rec[i] = has[i] ? (static_cast<uint32_t>(page_of(pos)) << p.log_bs) + (pos & bs_mask) : 0u;
+        if (pos[i] >= 0) block[i] = __ldg(table + (pos[i] >> p.log_bs));
       }
+      read_columns(tile + kWarps);
     } else {
-      const int pos = c0 + tile * kTile + lane * rows;
-      has[0] = lane * rows < kTile && pos < c1;
-      if (has[0]) rec[0] = page_of(pos);
+      pos[0] = c0 + tile * kTile + lane * rows;
+      if (lane * rows >= kTile || pos[0] >= c1) pos[0] = -1;
+      else block[0] = __ldg(table + (pos[0] >> p.log_bs));
     }
   };
-  // Starts the copies of the located tile into stage s; returns the columns
-  // (bit i of .x: column i, of .y: column 32 + i) of a selected tile.
+  // Starts the copies of the located tile into stage s; returns which columns
+  // of a selected tile there are (.x: columns 0 .. 31).
   auto fetch = [&](int s, int tile) {
     uint2 cols = make_uint2(0u, 0u);
     const uint32_t base = ring + s * Lay::kTileBytes;
     const uint32_t sbase = rest + Lay::kScales + s * Lay::kScaleBytes;
     if constexpr (kSel) {
-      cols.x = __ballot_sync(0xffffffffu, has[0]);
-      cols.y = __ballot_sync(0xffffffffu, has[1]);
+      cols.x = __ballot_sync(0xffffffffu, pos[0] >= 0);
+      cols.y = __ballot_sync(0xffffffffu, pos[1] >= 0);
       if (cols.x | cols.y) {  // absent columns become zeros
+        uint32_t rec[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          rec[i] = pos[i] >= 0 ? (page_of(block[i]) << p.log_bs) + (pos[i] & bs_mask) : 0u;
         constexpr int kPer = 32 / Lay::kChunks;  // records per instruction
         const int c = lane % Lay::kChunks;
 #pragma unroll
@@ -296,35 +316,36 @@ __global__ void __launch_bounds__(kThreads, 3)
           const int row = i * kPer + lane / Lay::kChunks;
           const bool upper = i >= kTile / kPer / 2;
           const uint32_t rc = __shfl_sync(0xffffffffu, upper ? rec[1] : rec[0], row & 31);
-          const bool ok = ((upper ? cols.y : cols.x) >> (row & 31)) & 1;
           cp_async16(base + Lay::chunk_at(row, c), p.cache + static_cast<int64_t>(rc) * D + c * 16,
-                     ok ? 16u : 0u);
+                     ((upper ? cols.y : cols.x) >> (row & 31)) & 1 ? 16u : 0u);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           cp_async_small<Lay::kSc>(sbase + (lane + 32 * i) * Lay::kSc,
                                    p.scales + static_cast<int64_t>(rec[i]) * Lay::kSc,
-                                   has[i] ? Lay::kSc : 0);
+                                   pos[i] >= 0 ? Lay::kSc : 0);
       }
       cp_async_commit();
     } else if (tile < tiles) {
       // Whole runs of a page: what lies past the last column is masked.
-      const int n = __popc(__ballot_sync(0xffffffffu, has[0]));
+      const int n = __popc(__ballot_sync(0xffffffffu, pos[0] >= 0));
       if (lane == 0) mbar_arrive_expect_tx(&bar[s], n * rows * (D + Lay::kSc));
       __syncwarp();
-      if (has[0]) {
-        const int at = (c0 + tile * kTile + lane * rows) & bs_mask;
+      if (pos[0] >= 0) {
+        const uint32_t page = page_of(block[0]);
+        const int at = pos[0] & bs_mask;
         tma_load_3d(tiles_p + s * Lay::kTileBytes + lane * rows * D, &p.tmap, &bar[s], 0, at,
-                    static_cast<int>(rec[0]));
+                    static_cast<int>(page));
         bulk_load(sbase + lane * rows * Lay::kSc,
-                  p.scales + ((static_cast<int64_t>(rec[0]) << p.log_bs) + at) * Lay::kSc,
+                  p.scales + ((static_cast<int64_t>(page) << p.log_bs) + at) * Lay::kSc,
                   rows * Lay::kSc, &bar[s]);
       }
     }
     return cols;
   };
 
-  uint2 cols[kStages];
+  uint2 cols[kStages];  // oldest first
+  if (kSel) read_columns(warp);
 #pragma unroll
   for (int s = 0; s < kStages; ++s) {
     locate(warp + s * kWarps);
@@ -334,13 +355,16 @@ __global__ void __launch_bounds__(kThreads, 3)
   // ---------------------------------------------------------------- queries
   // B fragments: lane (r, t) holds row r's elements 32 g + 8 t .. + 7, times
   // the softmax scale's sign.
-  uint32_t qf[NT][G][4];
+  // One row tile: every warp keeps the fragments in registers.  Two: warps 0
+  // and 1 prepare one each, and all read them from shared memory.
+  uint32_t qf[NT == 1 ? G : 1][4];
   float f[NT][2];    // base-2 logit = f * accumulator (f > 0), rows 2t and 2t + 1
-  int limit[NT][2];  // columns those rows see
   const bool zero = p.scale_log2e == 0.f;
   const float sign = zero ? 0.f : (p.scale_log2e < 0.f ? -1.f : 1.f);
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
+  const uint32_t q_at = smem_u32(smem) + Lay::kQueries + lane * 16;
+  float* const f_s = reinterpret_cast<float*>(smem + Lay::kFactorF);
+  if (NT == 1 || warp < NT) {
+    const int nt = NT == 1 ? 0 : warp;
     const int n = row0 + nt * 8 + r;
     uint4 raw[G];
     uint32_t amax = 0;
@@ -361,22 +385,42 @@ __global__ void __launch_bounds__(kThreads, 3)
     // infinity or NaN somewhere) keep their values.
     const int E = amax == 0 || amax >= 0x7F800000u ? 0
                                                    : max(static_cast<int>(amax >> 23), 1) - 127;
+    const float down = ldexpf(sign, -E);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
+      uint32_t h[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        qf[nt][g][i] =
-            pack_f16(ldexpf(bf16_lo(w[i]), -E) * sign, ldexpf(bf16_hi(w[i]), -E) * sign);
+      for (int i = 0; i < 4; ++i) h[i] = pack_f16(bf16_lo(w[i]) * down, bf16_hi(w[i]) * down);
+      if constexpr (NT == 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qf[g][i] = h[i];
+      } else {
+        sts128(q_at + (nt * G + g) * 512, h[0], h[1], h[2], h[3]);
+      }
     }
+    const float fr = zero ? 1.f : ldexpf(fabsf(p.scale_log2e), E);
+    if constexpr (NT == 1) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int e = __shfl_sync(0xffffffffu, E, (2 * t + i) * 4);
-      f[nt][i] = zero ? 1.f : ldexpf(fabsf(p.scale_log2e), e);
-      const int nn = row0 + nt * 8 + 2 * t + i;
-      limit[nt][i] = kSel ? gr.cols : gr.L - p.next_n + min(nn / p.heads, p.next_n - 1) + 1;
+      for (int i = 0; i < 2; ++i) f[0][i] = __shfl_sync(0xffffffffu, fr, (2 * t + i) * 4);
+    } else if (t == 0) {
+      f_s[nt * 8 + r] = fr;
     }
   }
+  if constexpr (NT > 1) {
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) f[nt][i] = f_s[nt * 8 + 2 * t + i];
+  }
+  // Columns that query row 2t + i of row tile nt sees (asked for in the tiles
+  // where some row does not see all of them).
+  auto limit = [&](int nt, int i) {
+    if (kSel) return gr.cols;
+    const int j = (row0 + nt * 8 + 2 * t + i) / p.heads;
+    return gr.L - p.next_n + min(j, p.next_n - 1) + 1;
+  };
   const int all_see = kSel ? gr.cols : gr.L - p.next_n + 1;  // columns every row sees
 
   float o[NT][2 * G][4];
@@ -386,17 +430,17 @@ __global__ void __launch_bounds__(kThreads, 3)
     for (int i = 0; i < 2 * G; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
-  // m: reference of the exponents, as an accumulator value.  It is raised to
-  // the running maximum only when a logit passes it by kSlack (base 2), so
-  // most tiles need no maximum across lanes and no rescaling; weights are then
-  // at most 2^kSlack, which fp16 and fp32 hold as well as 1.
+  // z: reference of a row's exponents (base 2).  It is raised to the running
+  // maximum only when a logit passes it by kSlack, that is when an accumulator
+  // passes thr, so most tiles need no maximum across lanes and no rescaling;
+  // weights are then at most 2^kSlack, which fp16 and fp32 hold as well as 1.
+  // thr = -inf: the row has seen no column.
   constexpr float kSlack = 8.f;
-  float m[NT][2], thr[NT][2], z[NT][2], l[NT][2];  // thr = m + kSlack / f, z = f m
+  float thr[NT][2], z[NT][2], l[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      m[nt][i] = thr[nt][i] = -INFINITY, z[nt][i] = l[nt][i] = 0.f;
+    for (int i = 0; i < 2; ++i) thr[nt][i] = -INFINITY, z[nt][i] = l[nt][i] = 0.f;
   float unit = 0.f, inv_unit = 0.f;  // o is in units of the largest value scale so far
 
   // Lane addresses that do not change from tile to tile: the key chunk of
@@ -416,13 +460,13 @@ __global__ void __launch_bounds__(kThreads, 3)
   uint32_t phase = 0;
   bool ok = true;
   for (int tile = warp; tile < tiles; tile += kWarps) {
-    locate(tile + kStages * kWarps);  // two tiles on: its loads return under this tile's work
+    locate(tile + kStages * kWarps);  // what it reads returns under this tile's work
     const int col0 = c0 + tile * kTile;
     uint2 live;  // columns of this tile
     if constexpr (kSel) {
       cp_async_wait<kStages - 1>();
       __syncwarp();
-      live = s ? cols[1] : cols[0];
+      live = cols[0];
     } else {
       ok = mbar_wait_bounded(&bar[s], phase, nullptr);
       if (!__all_sync(0xffffffffu, ok)) {
@@ -434,47 +478,53 @@ __global__ void __launch_bounds__(kThreads, 3)
       live.y = n >= 64 ? 0xffffffffu : (n > 32 ? (1u << (n - 32)) - 1u : 0u);
     }
     const uint32_t base = ring + s * Lay::kTileBytes;
+    const uint32_t sbase = rest + Lay::kScales + s * Lay::kScaleBytes;
     if (live.x | live.y) {
-      uint32_t nan_x = 0, nan_y = 0;  // keys with a NaN scale
+      uint2 nan = make_uint2(0u, 0u);  // keys with a NaN scale
       // ---------------------------------------------------------------- scales
-      // Lane (q8, t) takes the keys of rows 2t and 2t + 1 of the q8-th group
+      // Lane 4 q8 + t takes the keys of rows 2t and 2t + 1 of the q8-th group
       // of eight: one fragment pair.
       {
-        const uint32_t sbase = rest + Lay::kScales + s * Lay::kScaleBytes;
-        uint32_t ks[2], vs[2];
+        uint32_t kw[2], vw[2], vf[2][G];
         int key[2];
+        uint32_t top = 0;  // scales order as their bits
+        bool bad = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           key[i] = r * 8 + v_row[i];
           if constexpr (D == 128) {
             const uint2 u = lds64(sbase + key[i] * 8);
-            ks[i] = u.x, vs[i] = u.y;
+            kw[i] = u.x, vw[i] = u.y;
           } else {
             const uint32_t u = lds32(sbase + key[i] * 4);
-            ks[i] = u & 0xFFFFu, vs[i] = u >> 16;
+            kw[i] = u & 0xFFFFu, vw[i] = u >> 16;
           }
-          if (!(((r >= 4 ? live.y : live.x) >> (key[i] & 31)) & 1)) ks[i] = vs[i] = 0u;
+          if (!(((r >= 4 ? live.y : live.x) >> (key[i] & 31)) & 1)) kw[i] = vw[i] = 0u;
+          bad |= has_ff(kw[i]) != 0;
+          vf[i][0] = e8m0_bits<0>(vw[i]), vf[i][1] = e8m0_bits<1>(vw[i]);
+          if constexpr (D == 128) vf[i][2] = e8m0_bits<2>(vw[i]), vf[i][3] = e8m0_bits<3>(vw[i]);
+#pragma unroll
+          for (int g = 0; g < G; ++g) top = max(top, vf[i][g]);
         }
-        if (__any_sync(0xffffffffu,
-                       has_ff(ks[0]) | has_ff(ks[1]) | has_ff(vs[0]) | has_ff(vs[1]))) {
-          // NaN scales (rare).  A key's makes its logits NaN below; a value's
-          // makes its 32 channels of every row that sees the column NaN, here,
-          // and takes no part in the products.
+        if (__any_sync(0xffffffffu, bad || top == 0x7F800000u)) {
+          // NaN scales (code 255; rare).  A key's makes its logits NaN below;
+          // a value's makes its 32 channels of every row that sees the column
+          // NaN, here, and takes no part in the products.
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            uint32_t from = __ballot_sync(0xffffffffu, has_ff(ks[i]) != 0);
+            uint32_t from = __ballot_sync(0xffffffffu, has_ff(kw[i]) != 0);
             while (from) {
               const int src = __ffs(from) - 1;
               from &= from - 1;
               const int k = __shfl_sync(0xffffffffu, key[i], src);
-              if (k < 32) nan_x |= 1u << k;
-              else nan_y |= 1u << (k - 32);
+              if (k < 32) nan.x |= 1u << k;
+              else nan.y |= 1u << (k - 32);
             }
-            from = __ballot_sync(0xffffffffu, has_ff(vs[i]) != 0);
+            from = __ballot_sync(0xffffffffu, has_ff(vw[i]) != 0);
             while (from) {
               const int src = __ffs(from) - 1;
               from &= from - 1;
-              const uint32_t w = __shfl_sync(0xffffffffu, vs[i], src);
+              const uint32_t word = __shfl_sync(0xffffffffu, vw[i], src);
               const int col = col0 + __shfl_sync(0xffffffffu, key[i], src);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
@@ -482,32 +532,20 @@ __global__ void __launch_bounds__(kThreads, 3)
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                   for (int g = 0; g < G; ++g)
-                    if (((w >> (8 * g)) & 255u) == 255u && col < limit[nt][h]) {
+                    if (((word >> (8 * g)) & 255u) == 255u && col < limit(nt, h)) {
                       o[nt][2 * g][h] = o[nt][2 * g][2 + h] = __uint_as_float(0x7FC00000u);
                       o[nt][2 * g + 1][h] = o[nt][2 * g + 1][2 + h] = __uint_as_float(0x7FC00000u);
                     }
             }
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-              if (((vs[i] >> (8 * g)) & 255u) == 255u) vs[i] &= ~(255u << (8 * g));
           }
-        }
-        uint32_t vf[2][G];
-        uint32_t top = 0;  // scales order as their bits
+          top = 0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t kf[G];
-          kf[0] = e8m0_bits<0>(ks[i]), kf[1] = e8m0_bits<1>(ks[i]);
-          vf[i][0] = e8m0_bits<0>(vs[i]), vf[i][1] = e8m0_bits<1>(vs[i]);
-          if constexpr (D == 128) {
-            kf[2] = e8m0_bits<2>(ks[i]), kf[3] = e8m0_bits<3>(ks[i]);
-            vf[i][2] = e8m0_bits<2>(vs[i]), vf[i][3] = e8m0_bits<3>(vs[i]);
-            sts128(ks_at + key[i] * 16, kf[0], kf[1], kf[2], kf[3]);
-          } else {
-            sts64(ks_at + key[i] * 8, kf[0], kf[1]);
-          }
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int g = 0; g < G; ++g) top = max(top, vf[i][g]);
+            for (int g = 0; g < G; ++g) {
+              if (vf[i][g] == 0x7F800000u) vf[i][g] = 0u;
+              top = max(top, vf[i][g]);
+            }
         }
         top = __reduce_max_sync(0xffffffffu, top);
         if (top > __float_as_uint(unit)) {
@@ -522,6 +560,20 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll
               for (int j = 0; j < 4; ++j) o[nt][i][j] *= down;
         }
+        if constexpr (NT == 1) {
+          // The key scales as fp32, where rows r of a group of eight find
+          // them side by side.  (With two row tiles there is no room for
+          // them: the scale words are unpacked where they are used.)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t at = ks_at + (r * 8 + 2 * t + i) * (4 * G);
+            if constexpr (D == 128)
+              sts128(at, e8m0_bits<0>(kw[i]), e8m0_bits<1>(kw[i]), e8m0_bits<2>(kw[i]),
+                     e8m0_bits<3>(kw[i]));
+            else
+              sts64(at, e8m0_bits<0>(kw[i]), e8m0_bits<1>(kw[i]));
+          }
+        }
         uint32_t fac[G];
 #pragma unroll
         for (int g = 0; g < G; ++g)
@@ -532,12 +584,12 @@ __global__ void __launch_bounds__(kThreads, 3)
         __syncwarp();
       }
       const bool clean =
-          (nan_x | nan_y) == 0 && (kSel ? (live.x & live.y) == 0xffffffffu
+          (nan.x | nan.y) == 0 && (kSel ? (live.x & live.y) == 0xffffffffu
                                         : col0 + kTile <= min(c1, all_see));
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
-        // ---------------------------------------------------------- S^T = K q^T
         const uint32_t hbase = base + half * 32 * D;
+        // ---------------------------------------------------------- S^T = K q^T
         float sacc[2][NT][4];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
@@ -546,16 +598,31 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t at = hbase + (mt * 16 + h * 8) * D + k_at;
-            const uint32_t sat = ks_at + (half * 32 + mt * 16 + h * 8 + prow) * (4 * G);
             if constexpr (D == 128) {
-              const uint4 u = lds128(at), v = lds128(sat);
+              const uint4 u = lds128(at);
               kw[h][0] = u.x, kw[h][1] = u.y, kw[h][2] = u.z, kw[h][3] = u.w;
-              ks[h][0] = __uint_as_float(v.x), ks[h][1] = __uint_as_float(v.y);
-              ks[h][2] = __uint_as_float(v.z), ks[h][3] = __uint_as_float(v.w);
             } else {
-              const uint2 u = lds64(at), v = lds64(sat);
+              const uint2 u = lds64(at);
               kw[h][0] = u.x, kw[h][1] = u.y;
-              ks[h][0] = __uint_as_float(v.x), ks[h][1] = __uint_as_float(v.y);
+            }
+            if constexpr (NT == 1) {
+              const uint32_t sat = ks_at + (half * 32 + mt * 16 + h * 8 + r) * (4 * G);
+              if constexpr (D == 128) {
+                const uint4 v = lds128(sat);
+                ks[h][0] = __uint_as_float(v.x), ks[h][1] = __uint_as_float(v.y);
+                ks[h][2] = __uint_as_float(v.z), ks[h][3] = __uint_as_float(v.w);
+              } else {
+                const uint2 v = lds64(sat);
+                ks[h][0] = __uint_as_float(v.x), ks[h][1] = __uint_as_float(v.y);
+              }
+            } else {
+              const uint32_t w = lds32(sbase + (half * 32 + mt * 16 + h * 8 + prow) * Lay::kSc);
+              ks[h][0] = __uint_as_float(e8m0_bits<0>(w));
+              ks[h][1] = __uint_as_float(e8m0_bits<1>(w));
+              if constexpr (D == 128) {
+                ks[h][2] = __uint_as_float(e8m0_bits<2>(w));
+                ks[h][3] = __uint_as_float(e8m0_bits<3>(w));
+              }
             }
           }
 #pragma unroll
@@ -566,9 +633,12 @@ __global__ void __launch_bounds__(kThreads, 3)
             const uint32_t b2 = e2m1x2_to_f16x2<3>(kw[0][g]), b3 = e2m1x2_to_f16x2<3>(kw[1][g]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              float c[4] = {0.f, 0.f, 0.f, 0.f};
-              mma16816(c, a0, a1, a2, a3, qf[nt][g][0], qf[nt][g][1]);
-              mma16816(c, b0, b1, b2, b3, qf[nt][g][2], qf[nt][g][3]);
+              float c[4];
+              uint4 q;
+              if constexpr (NT == 1) q = make_uint4(qf[g][0], qf[g][1], qf[g][2], qf[g][3]);
+              else q = lds128(q_at + (nt * G + g) * 512);
+              mma16816_zero(c, a0, a1, a2, a3, q.x, q.y);
+              mma16816(c, b0, b1, b2, b3, q.z, q.w);
 #pragma unroll
               for (int j = 0; j < 4; ++j)
                 sacc[mt][nt][j] =
@@ -577,21 +647,20 @@ __global__ void __launch_bounds__(kThreads, 3)
           }
         }
         // ------------------------------------------------------------- softmax
-        const uint32_t hlive = half ? live.y : live.x;
         if (!clean) {
-          const uint32_t hnan = half ? nan_y : nan_x;
+          const uint32_t hlive = half ? live.y : live.x, hnan = half ? nan.y : nan.x;
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int key = mt * 16 + h * 8 + prow;
-              const bool here = (hlive >> key) & 1, nan = (hnan >> key) & 1;
+              const bool here = (hlive >> key) & 1, bad = (hnan >> key) & 1;
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                  if (nan) sacc[mt][nt][2 * h + i] = __uint_as_float(0x7FC00000u);
-                  if (!here || (!kSel && col0 + half * 32 + key >= limit[nt][i]))
+                  if (bad) sacc[mt][nt][2 * h + i] = __uint_as_float(0x7FC00000u);
+                  if (!here || (!kSel && col0 + half * 32 + key >= limit(nt, i)))
                     sacc[mt][nt][2 * h + i] = -INFINITY;
                 }
             }
@@ -631,16 +700,15 @@ __global__ void __launch_bounds__(kThreads, 3)
               float v = fmaxf(x[nt][i], __shfl_xor_sync(0xffffffffu, x[nt][i], 4));
               v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
               v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-              v = fmaxf(v, m[nt][i]);
-              // m = -inf: nothing accumulated yet (l and o are zero).
-              const float a = m[nt][i] == -INFINITY ? 0.f : ex2((m[nt][i] - v) * f[nt][i]);
-              m[nt][i] = v;
-              thr[nt][i] = v + kSlack / f[nt][i];
-              // A row that has seen no column: every exponent is -inf.
-              z[nt][i] = v == -INFINITY ? 0.f : v * f[nt][i];
-              l[nt][i] *= a;
+              if (v > thr[nt][i]) {
+                const float zn = v * f[nt][i];
+                const float a = thr[nt][i] == -INFINITY ? 0.f : ex2(z[nt][i] - zn);
+                z[nt][i] = zn;
+                thr[nt][i] = v + kSlack / f[nt][i];
+                l[nt][i] *= a;
 #pragma unroll
-              for (int j = 0; j < 2 * G; ++j) o[nt][j][i] *= a, o[nt][j][2 + i] *= a;
+                for (int j = 0; j < 2 * G; ++j) o[nt][j][i] *= a, o[nt][j][2 + i] *= a;
+              }
             }
         }
         uint32_t pf[2][NT][2];  // P as B fragments: row r, keys 2t, 2t+1 (+ 8)
@@ -715,8 +783,9 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
     __syncwarp();
     const uint2 c = fetch(s, tile + kStages * kWarps);
-    if (s) cols[1] = c;
-    else cols[0] = c;
+#pragma unroll
+    for (int i = 0; i + 1 < kStages; ++i) cols[i] = cols[i + 1];
+    cols[kStages - 1] = c;
     s = s + 1 == kStages ? 0 : s + 1;
     phase ^= s == 0;
   }
@@ -741,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 3)
       x += __shfl_xor_sync(0xffffffffu, x, 16);
       const int row = nt * 8 + 2 * t + i;
       if (r == 0) {
-        sml[(warp * kRows + row) * 2] = m[nt][i] == -INFINITY ? -INFINITY : z[nt][i];
+        sml[(warp * kRows + row) * 2] = thr[nt][i] == -INFINITY ? -INFINITY : z[nt][i];
         sml[(warp * kRows + row) * 2 + 1] = x;
       }
       float* dst = so + (warp * kRows + row) * D;
@@ -902,7 +971,7 @@ __global__ void __launch_bounds__(1024)
 
 template <int D, int NT, bool kSel, bool kScores>
 cudaError_t launch_one(const Kv4AttnParams& p, cudaStream_t s) {
-  using Lay = Layout<D>;
+  using Lay = Layout<D, NT>;
   constexpr int kRing = Lay::kBytes;
   constexpr int kJoin = kWarps * 8 * NT * (D + 2) * 4;
   constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
@@ -951,7 +1020,8 @@ Kv4AttnPlan kv4_attn_plan(int B, int next_n, int Hq, int Hkv, int D, int64_t col
   // warp, and no more than 64 tiles so that requests of unequal length spread.
   const int64_t tiles = (cols + kTile - 1) / kTile;
   const int64_t lanes = pl.groups * Hkv * pl.row_tiles;
-  const int64_t places = static_cast<int64_t>(device_sm_count() > 0 ? device_sm_count() : 152) * 3;
+  const int64_t places =
+      static_cast<int64_t>(device_sm_count() > 0 ? device_sm_count() : 152) * kCtasPerSm;
   int64_t per = (tiles * lanes + places - 1) / (places > 0 ? places : 1);
   per = per < kWarps ? kWarps : (per > 64 ? 64 : per);
   per = (per + kWarps - 1) / kWarps * kWarps;

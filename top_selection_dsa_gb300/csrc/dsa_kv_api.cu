@@ -87,7 +87,7 @@ dsa_status_t run_attention(const AttnArgs& a, bool selected, dsa_stream_t stream
     return DSA_ERR_INVALID_ARG;
   Kv4AttnParams p = {};
   if (!selected && !encode_rows_map(&p.tmap, a.cache, a.D, a.block_size,
-                                    a.block_size < 64 ? a.block_size : 64,
+                                    a.block_size < kKv4Tile ? a.block_size : kKv4Tile,
                                     static_cast<int64_t>(a.num_blocks) * a.Hkv))
     return DSA_ERR_CUDA;
   p.q = static_cast<const uint16_t*>(a.q);
