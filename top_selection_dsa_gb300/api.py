@@ -9,7 +9,9 @@ not been built -- there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -526,20 +528,52 @@ def kv4_cache(num_blocks, num_kv_heads, block_size, head_dim, device="cuda"):
                         device=device))
 
 
+# The decode calls run once a layer and step, on kernels of a few microseconds:
+# their checks compare each tensor once, and go through the ones above only to
+# name what is wrong.
+def _need_all(dev, specs):
+    if dev.type != "cuda":
+        raise ValueError(f"{specs[0][1]} must be a CUDA tensor")
+    for t, name, dtype in specs:
+        if t is not None and (t.dtype is not dtype or t.device != dev or not t.is_contiguous()):
+            _need(t, name, (dtype,), dev)
+
+
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _on(dev):
+    """The device of a call made current (a no-op when it is)."""
+    return _NO_GUARD if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+# The current stream's handle without a Stream object around it, where torch
+# offers that.
+_raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(dev):
+    if _raw_stream_of is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return _raw_stream_of(dev.index)
+
+
 def _kv4_shape(cache, scales, dev):
-    _need(cache, "cache", (torch.uint8,), dev)
-    _need(scales, "scales", (torch.uint8,), dev)
     if cache.dim() != 4 or scales.dim() != 4:
         raise ValueError("cache [num_blocks, Hkv, block_size, D] and scales "
                          "[num_blocks, Hkv, block_size, D/16] expected")
     nb, hkv, bs, D = cache.shape
-    if tuple(scales.shape) != (nb, hkv, bs, D // 16):
+    if scales.shape != (nb, hkv, bs, D // 16):
         raise ValueError(f"scales must be {(nb, hkv, bs, D // 16)}, got {tuple(scales.shape)}")
     return nb, hkv, bs, D
 
 
 def _shape(t, name, shape):
-    if t is not None and tuple(t.shape) != shape:
+    if t is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
 
 
@@ -562,16 +596,17 @@ def kv4_insert(k, v, slot_mapping, cache, scales):
     as slices of one projection are) into their slots of the 4-bit cache.  In
     place."""
     dev = cache.device
+    _need_all(dev, ((cache, "cache", torch.uint8), (scales, "scales", torch.uint8),
+                    (slot_mapping, "slot_mapping", torch.int64)))
     nb, hkv, bs, D = _kv4_shape(cache, scales, dev)
-    _need(slot_mapping, "slot_mapping", (torch.int64,), dev)
     T = slot_mapping.numel()
     ks = _token_rows(k, "k", dev, (T, hkv, D))
     vs = _token_rows(v, "v", dev, (T, hkv, D))
     if T == 0:
         return cache, scales
-    with torch.cuda.device(dev):
-        st = lib.dsa_kv4_insert(_ptr(k), ks, _ptr(v), vs, _ptr(slot_mapping), T, hkv, D,
-                                _ptr(cache), _ptr(scales), nb, bs, _stream(dev))
+    with _on(dev):
+        st = lib.dsa_kv4_insert(_addr(k), ks, _addr(v), vs, _addr(slot_mapping), T, hkv, D,
+                                _addr(cache), _addr(scales), nb, bs, _raw_stream(dev))
     _check(st, "dsa_kv4_insert")
     return cache, scales
 
@@ -581,18 +616,19 @@ def kv4_gather(cache, scales, slots, *, k=None, v=None):
     tensors (zeros for a slot below 0)."""
     dev = cache.device
     nb, hkv, bs, D = _kv4_shape(cache, scales, dev)
-    _need(slots, "slots", (torch.int64,), dev)
     T = slots.numel()
     k = torch.empty((T, hkv, D), dtype=torch.bfloat16, device=dev) if k is None else k
     v = torch.empty((T, hkv, D), dtype=torch.bfloat16, device=dev) if v is None else v
-    for t, n in ((k, "k"), (v, "v")):
-        _need(t, n, (torch.bfloat16,), dev)
-        _shape(t, n, (T, hkv, D))
+    _need_all(dev, ((cache, "cache", torch.uint8), (scales, "scales", torch.uint8),
+                    (slots, "slots", torch.int64), (k, "k", torch.bfloat16),
+                    (v, "v", torch.bfloat16)))
+    _shape(k, "k", (T, hkv, D))
+    _shape(v, "v", (T, hkv, D))
     if T == 0:
         return k, v
-    with torch.cuda.device(dev):
-        st = lib.dsa_kv4_gather(_ptr(cache), _ptr(scales), nb, bs, _ptr(slots), T, hkv, D, _ptr(k),
-                                _ptr(v), _stream(dev))
+    with _on(dev):
+        st = lib.dsa_kv4_gather(_addr(cache), _addr(scales), nb, bs, _addr(slots), T, hkv, D,
+                                _addr(k), _addr(v), _raw_stream(dev))
     _check(st, "dsa_kv4_gather")
     return k, v
 
@@ -601,8 +637,13 @@ def kv4_attention_workspace_bytes(B, next_n, Hq, Hkv, D, cols, *, selected=False
                                   weights=False) -> int:
     """Workspace of kv4_attention (cols = max_blocks * block_size) or, with
     `selected`, of kv4_attention_topk (cols = k), on the current device."""
-    n = lib.dsa_kv4_attention_workspace_bytes(B, next_n, Hq, Hkv, D, cols, int(selected),
-                                              int(weights))
+    return _kv4_workspace(torch.cuda.current_device() if torch.cuda.is_available() else -1,
+                          B, next_n, Hq, Hkv, D, cols, bool(selected), bool(weights))
+
+
+@functools.lru_cache(maxsize=4096)
+def _kv4_workspace(device, B, next_n, Hq, Hkv, D, cols, selected, weights):
+    n = lib.dsa_kv4_attention_workspace_bytes(B, next_n, Hq, Hkv, D, cols, selected, weights)
     if n == ctypes.c_size_t(-1).value:
         raise ValueError("dsa_kv4_attention_workspace_bytes: bad arguments")
     return int(n)
@@ -612,23 +653,21 @@ def _kv4_attention(q, cache, scales, block_table, context_lens, topk_idx, next_n
                    out, lse, topk_weights, key_weights, workspace):
     dev = q.device
     nb, hkv, bs, D = _kv4_shape(cache, scales, dev)
-    _need(q, "q", (torch.bfloat16,), dev)
-    _need(block_table, "block_table", (torch.int32,), dev)
-    _need(context_lens, "context_lens", (torch.int32,), dev)
-    _need(topk_idx, "topk_idx", (torch.int32,), dev)
-    _need(topk_weights, "topk_weights", (torch.float32,), dev)
-    _need(key_weights, "key_weights", (torch.float32,), dev)
     B, max_blocks = block_table.shape
     R, Hq, Dq = q.shape
     if R != B * next_n or Dq != D:
         raise ValueError(f"q must be [{B * next_n}, Hq, {D}], got {tuple(q.shape)}")
-    _shape(context_lens, "context_lens", (B,))
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
         lse = torch.empty((R, Hq), dtype=torch.float32, device=dev)
-    _need(out, "out", (torch.bfloat16,), dev)
-    _need(lse, "lse", (torch.float32,), dev)
+    _need_all(dev, ((q, "q", torch.bfloat16), (cache, "cache", torch.uint8),
+                    (scales, "scales", torch.uint8), (block_table, "block_table", torch.int32),
+                    (context_lens, "context_lens", torch.int32), (out, "out", torch.bfloat16),
+                    (lse, "lse", torch.float32), (topk_idx, "topk_idx", torch.int32),
+                    (topk_weights, "topk_weights", torch.float32),
+                    (key_weights, "key_weights", torch.float32)))
+    _shape(context_lens, "context_lens", (B,))
     _shape(out, "out", (R, Hq, D))
     _shape(lse, "lse", (R, Hq))
     ldw = 0
@@ -638,30 +677,29 @@ def _kv4_attention(q, cache, scales, block_table, context_lens, topk_idx, next_n
             raise ValueError(f"key_weights must be [{B}, >= {max_blocks * bs}], got "
                              f"{tuple(key_weights.shape)}")
         ldw = key_weights.shape[1]
-    scale = D ** -0.5 if softmax_scale is None else float(softmax_scale)
-    with torch.cuda.device(dev):
+    scale = D ** -0.5 if softmax_scale is None else softmax_scale
+    with _on(dev):
         if topk_idx is None:
-            nbytes = kv4_attention_workspace_bytes(B, next_n, Hq, hkv, D, max_blocks * bs,
-                                                   weights=key_weights is not None)
+            nbytes = _kv4_workspace(dev.index, B, next_n, Hq, hkv, D, max_blocks * bs, False,
+                                    key_weights is not None)
             ws = _workspace(nbytes, dev, workspace)
-            st = lib.dsa_kv4_attention(_ptr(q), _ptr(cache), _ptr(scales), nb, _ptr(block_table),
-                                       max_blocks, _ptr(context_lens), B, next_n, bs, Hq, hkv, D,
-                                       scale, _ptr(out), _ptr(lse), _ptr(key_weights), ldw,
-                                       _ptr(ws) if nbytes else None, nbytes, _stream(dev))
+            st = lib.dsa_kv4_attention(
+                _addr(q), _addr(cache), _addr(scales), nb, _addr(block_table), max_blocks,
+                _addr(context_lens), B, next_n, bs, Hq, hkv, D, scale, _addr(out), _addr(lse),
+                _addr(key_weights), ldw, _addr(ws) if nbytes else None, nbytes, _raw_stream(dev))
             _check(st, "dsa_kv4_attention")
         else:
             k = topk_idx.shape[-1]
             _shape(topk_idx, "topk_idx", (R, k))
             _shape(topk_weights, "topk_weights", (R, k))
-            nbytes = kv4_attention_workspace_bytes(
-                B, next_n, Hq, hkv, D, k, selected=True,
-                weights=key_weights is not None or topk_weights is not None)
+            nbytes = _kv4_workspace(dev.index, B, next_n, Hq, hkv, D, k, True,
+                                    key_weights is not None or topk_weights is not None)
             ws = _workspace(nbytes, dev, workspace)
             st = lib.dsa_kv4_attention_topk(
-                _ptr(q), _ptr(cache), _ptr(scales), nb, _ptr(block_table), max_blocks,
-                _ptr(context_lens), _ptr(topk_idx), k, B, next_n, bs, Hq, hkv, D, scale, _ptr(out),
-                _ptr(lse), _ptr(topk_weights), _ptr(key_weights), ldw,
-                _ptr(ws) if nbytes else None, nbytes, _stream(dev))
+                _addr(q), _addr(cache), _addr(scales), nb, _addr(block_table), max_blocks,
+                _addr(context_lens), _addr(topk_idx), k, B, next_n, bs, Hq, hkv, D, scale,
+                _addr(out), _addr(lse), _addr(topk_weights), _addr(key_weights), ldw,
+                _addr(ws) if nbytes else None, nbytes, _raw_stream(dev))
             _check(st, "dsa_kv4_attention_topk")
     return out, lse
 
@@ -689,6 +727,7 @@ def kv4_attention_topk(q, cache, scales, block_table, context_lens, topk_idx, *,
                           softmax_scale, out, lse, sel_weights, key_weights, workspace)
 
 
+@functools.lru_cache(maxsize=4096)
 def kv_evict_workspace_bytes(B, max_ctx, budget) -> int:
     n = lib.dsa_kv_evict_workspace_bytes(B, max_ctx, budget)
     if n == ctypes.c_size_t(-1).value:
@@ -702,24 +741,23 @@ def kv_evict_select(key_weights, context_lens, budget, *, sink=0, recent=0, keep
     last `recent` and the heaviest between, by key_weights [B, ldw].  Returns
     (keep [B, budget] int32 ascending, -1 padded; new_lens [B] int32)."""
     dev = key_weights.device
-    _need(key_weights, "key_weights", (torch.float32,), dev)
-    _need(context_lens, "context_lens", (torch.int32,), dev)
     B, ldw = key_weights.shape
-    _shape(context_lens, "context_lens", (B,))
     if keep is None:
         keep = torch.empty((B, budget), dtype=torch.int32, device=dev)
     if new_lens is None:
         new_lens = torch.empty((B,), dtype=torch.int32, device=dev)
-    _need(keep, "keep", (torch.int32,), dev)
-    _need(new_lens, "new_lens", (torch.int32,), dev)
+    _need_all(dev, ((key_weights, "key_weights", torch.float32),
+                    (context_lens, "context_lens", torch.int32), (keep, "keep", torch.int32),
+                    (new_lens, "new_lens", torch.int32)))
+    _shape(context_lens, "context_lens", (B,))
     _shape(keep, "keep", (B, budget))
     _shape(new_lens, "new_lens", (B,))
     nbytes = kv_evict_workspace_bytes(B, ldw, budget)
-    with torch.cuda.device(dev):
+    with _on(dev):
         ws = _workspace(nbytes, dev, workspace)
-        st = lib.dsa_kv_evict_select(_ptr(key_weights), ldw, _ptr(context_lens), B, ldw,
-                                     int(budget), int(sink), int(recent), _ptr(keep),
-                                     _ptr(new_lens), _ptr(ws), nbytes, _stream(dev))
+        st = lib.dsa_kv_evict_select(_addr(key_weights), ldw, _addr(context_lens), B, ldw, budget,
+                                     sink, recent, _addr(keep), _addr(new_lens), _addr(ws), nbytes,
+                                     _raw_stream(dev))
     _check(st, "dsa_kv_evict_select")
     return keep, new_lens
 
@@ -727,7 +765,7 @@ def kv_evict_select(key_weights, context_lens, budget, *, sink=0, recent=0, keep
 def _paged_rows(t, block_size, dev):
     """A paged cache as (planes, row bytes): [num_blocks, planes, block_size,
     ...] or [num_blocks, block_size, ...] with one plane."""
-    if not t.is_cuda or t.device != dev or not t.is_contiguous():
+    if t.device != dev or not t.is_contiguous():
         raise ValueError(f"every cache must be a contiguous CUDA tensor on {dev}")
     if t.dim() == 4 and t.shape[2] == block_size:
         planes, row = t.shape[1], t.shape[3]
@@ -737,7 +775,7 @@ def _paged_rows(t, block_size, dev):
         raise ValueError("caches are [num_blocks, planes, block_size, row], [num_blocks, "
                          f"block_size, row] or [num_blocks, block_size]; got {tuple(t.shape)} "
                          f"with block_size {block_size}")
-    return PagedRows(t.data_ptr(), planes, row * t.element_size())
+    return t.data_ptr(), planes, row * t.element_size()
 
 
 def kv_compact(caches, keep, context_lens, block_table, new_block_table=None, *, new_lens=None,
@@ -749,13 +787,12 @@ def kv_compact(caches, keep, context_lens, block_table, new_block_table=None, *,
     key_weights_out (default: in place), zeros after."""
     caches = list(caches)
     dev = keep.device
-    _need(keep, "keep", (torch.int32,), dev)
-    _need(context_lens, "context_lens", (torch.int32,), dev)
-    _need(block_table, "block_table", (torch.int32,), dev)
-    _need(new_block_table, "new_block_table", (torch.int32,), dev)
-    _need(new_lens, "new_lens", (torch.int32,), dev)
-    _need(key_weights, "key_weights", (torch.float32,), dev)
-    _need(key_weights_out, "key_weights_out", (torch.float32,), dev)
+    _need_all(dev, ((keep, "keep", torch.int32), (context_lens, "context_lens", torch.int32),
+                    (block_table, "block_table", torch.int32),
+                    (new_block_table, "new_block_table", torch.int32),
+                    (new_lens, "new_lens", torch.int32),
+                    (key_weights, "key_weights", torch.float32),
+                    (key_weights_out, "key_weights_out", torch.float32)))
     B, budget = keep.shape
     max_blocks = block_table.shape[1]
     _shape(context_lens, "context_lens", (B,))
@@ -780,12 +817,12 @@ def kv_compact(caches, keep, context_lens, block_table, new_block_table=None, *,
         ldw = key_weights.shape[1]
         _shape(key_weights, "key_weights", (B, ldw))
         _shape(key_weights_out, "key_weights_out", (B, ldw))
-    with torch.cuda.device(dev):
-        st = lib.dsa_kv_compact(rows, len(caches), num_blocks, block_size, _ptr(block_table),
-                                max_blocks, _ptr(new_block_table),
+    with _on(dev):
+        st = lib.dsa_kv_compact(rows, len(caches), num_blocks, block_size, _addr(block_table),
+                                max_blocks, _addr(new_block_table),
                                 0 if new_block_table is None else new_block_table.shape[1],
-                                _ptr(context_lens), _ptr(keep), _ptr(new_lens), B, budget,
-                                _ptr(key_weights), _ptr(key_weights_out), ldw, _stream(dev))
+                                _addr(context_lens), _addr(keep), _addr(new_lens), B, budget,
+                                _addr(key_weights), _addr(key_weights_out), ldw, _raw_stream(dev))
     _check(st, "dsa_kv_compact")
     return caches
 

@@ -138,10 +138,7 @@ cudaError_t launch_kv4_gather(const void* cache, const void* scales, const int64
                               int Hkv, int D, int num_blocks, int block_size, void* k, void* v,
                               uint32_t* err, cudaStream_t s);
 
-// Decode attention (dsa_kv4_attn.cu).  Columns a warp takes at a time: the
-// height of the records' tensor-map box is the smaller of this and a page.
-constexpr int kKv4Tile = 64;
-// A group is what shares its columns: a
+// Decode attention (dsa_kv4_attn.cu).  A group is what shares its columns: a
 // request (every key), or a query row (selected keys).
 struct Kv4AttnParams {
   CUtensorMap tmap;        // the records, [num_blocks*Hkv, block_size, D bytes] (every key)
@@ -155,12 +152,13 @@ struct Kv4AttnParams {
   int groups, next_n, heads, Hkv, Hq, row_tiles;  // heads: query heads per key/value head
   int max_blocks, num_blocks, log_bs;
   float scale_log2e;       // softmax scale times log2(e)
-  int chunk, nsplit;       // columns per CTA, CTAs per group, head and row tile
+  int ctas;                // that share the work
   int cols;                // columns at most (max context, or sel_k)
   uint16_t* out;           // [B*next_n, Hq, D] bf16
   float* lse;              // [B*next_n, Hq] or null
-  float* part_o;           // [groups, nsplit, Hkv*row_tiles, rows, D] when nsplit > 1
-  float* part_ml;          // [.., rows, 2]
+  float* part_o;           // [ctas, 2, rows, D]: partial results
+  float* part_ml;          // [ctas, 2, rows, 2]
+  int4* spans;             // [ctas]: what to join, or null when nothing can be split
   float* scores;           // [groups, Hkv*row_tiles, cols, rows]: base-2 logits, for the weights
   float* lse2;             // [groups, Hkv*row_tiles, rows]
   float* sel_weights;      // [B*next_n, sel_k] or null
@@ -171,12 +169,13 @@ struct Kv4AttnParams {
 // How a call is cut up, and the byte offsets of its workspace.
 struct Kv4AttnPlan {
   int64_t groups;
-  int heads, nt, row_tiles, chunk, nsplit;
-  int64_t part_o, part_ml, scores, lse2, sel_weights, bytes;
+  int heads, rows, row_tiles, tile, ctas;  // rows of a CTA; columns of a tile
+  bool split;
+  int64_t part_o, part_ml, spans, scores, lse2, sel_weights, bytes;
 };
 Kv4AttnPlan kv4_attn_plan(int B, int next_n, int Hq, int Hkv, int D, int64_t cols, bool selected,
                           bool weights);
-cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int D, int nt, bool scores,
+cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int D, int rows, bool scores,
                                  cudaStream_t s);
 
 // Eviction (dsa_kv_evict.cu).

@@ -31,11 +31,12 @@
 // XOR-swizzled by the key's index in its group of eight, the 16-byte key
 // loads and the 8-byte value loads are then both free of bank conflicts.
 //
-// The columns of a request are cut into chunks, one CTA (four warps, tiles
-// dealt round) per chunk, head and 16 rows; a CTA that covers all of a row's
-// columns writes the result, otherwise partial sums that a second kernel
-// joins.
+// The work is cut into equal shares, one per resident CTA, whatever the
+// requests' lengths (Walk below); a CTA that has all of a row's columns writes
+// the result, otherwise partial sums that a second kernel joins.
 #include <math.h>
+
+#include <atomic>
 
 #include "dsa_internal.h"
 #include "dsa_kv4.cuh"
@@ -43,7 +44,7 @@
 namespace dsa {
 namespace {
 
-constexpr int kTile = kKv4Tile;
+constexpr int kTile = 64;       // columns a warp takes at a time
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 2;
@@ -93,6 +94,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The low nibbles of a's bytes with the high nibbles of b's: one three-input
+// logic operation.
+__device__ __forceinline__ uint32_t low_nibbles_of(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, 0x0F0F0F0F, 0xE4;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
@@ -188,17 +197,140 @@ struct Group {
   int limit;   // selected row: columns it may see
 };
 
+__device__ __forceinline__ int context_len(const Kv4AttnParams& p, int b, bool report = false) {
+  const int cap = p.max_blocks << p.log_bs;
+  const int raw = __ldg(p.context_lens + b);
+  if (report && (raw < 0 || raw > cap)) record_error(p.err, kErrBadIndex);
+  return raw < 0 ? 0 : (raw > cap ? cap : raw);
+}
+
 template <bool kSel>
-__device__ __forceinline__ Group group_of(const Kv4AttnParams& p, int g, bool report) {
+__device__ __forceinline__ Group group_of(const Kv4AttnParams& p, int g) {
   Group r;
   r.b = kSel ? g / p.next_n : g;
-  const int cap = p.max_blocks << p.log_bs;
-  const int raw = __ldg(p.context_lens + r.b);
-  if (report && (raw < 0 || raw > cap)) record_error(p.err, kErrBadIndex);
-  r.L = raw < 0 ? 0 : (raw > cap ? cap : raw);
+  r.L = context_len(p, r.b);
   r.cols = kSel ? p.sel_k : r.L;
   r.limit = kSel ? max(r.L - p.next_n + (g - r.b * p.next_n) + 1, 0) : r.L;
   return r;
+}
+
+// The work of a call is a list of units of kUnit columns, by group, then head
+// and row tile, then column (a group without columns has one empty unit); CTA
+// i of P takes the units [T i / P, T (i + 1) / P) of the T there are, whatever
+// the requests' lengths.  A run of units of one group, head and row tile is a
+// span; a CTA's spans are whole, but for its first and its last, which may be
+// shared with its neighbours.
+struct Span {
+  int g, ht;       // group; head and row tile
+  int u0, u1;      // units of it
+  int units;       // that there are
+  bool first;      // of the CTA
+  __device__ bool whole() const { return u0 == 0 && u1 == units; }
+};
+
+template <bool kSel, int kUnit>
+struct Walk {
+  int64_t t, t1, total;
+  int64_t P;       // CTAs that have work
+  int64_t base;    // units before group g
+  int g;
+  bool first;
+
+  __device__ static int units_of(int cols) { return cols > 0 ? (cols + kUnit - 1) / kUnit : 1; }
+
+  // Executed by whole warps.
+  __device__ __forceinline__ explicit Walk(const Kv4AttnParams& p) {
+    const int per = p.Hkv * p.row_tiles;
+    const int lane = threadIdx.x & 31;
+    const int64_t i = blockIdx.x;
+    first = true;
+    if constexpr (kSel) {
+      const int64_t upg = static_cast<int64_t>(units_of(p.sel_k)) * per;
+      total = upg * p.groups;
+      share(i);
+      g = static_cast<int>(t / upg);
+      base = g * upg;
+      if (blockIdx.x == 0)
+        for (int b = threadIdx.x; b < p.groups / p.next_n; b += blockDim.x) context_len(p, b, true);
+    } else {
+      const bool report = blockIdx.x == 0 && threadIdx.x < 32;
+      int64_t mine = 0;
+      for (int b = lane; b < p.groups; b += 32)
+        mine += units_of(context_len(p, b, report));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+      total = mine * per;
+      share(i);
+      base = 0;
+      g = 0;
+      for (int b0 = 0; b0 < p.groups; b0 += 32) {
+        const int64_t v =
+            b0 + lane < p.groups
+                ? static_cast<int64_t>(units_of(context_len(p, b0 + lane))) * per : 0;
+        int64_t incl = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, t < base + incl);
+        if (past) {
+          const int src = __ffs(past) - 1;
+          g = b0 + src;
+          base += __shfl_sync(0xffffffffu, incl - v, src);
+          break;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+  }
+  __device__ __forceinline__ void share(int64_t i) {
+    P = total < gridDim.x ? total : gridDim.x;
+    t = i < P ? total * i / P : total;
+    t1 = i < P ? total * (i + 1) / P : total;
+  }
+  __device__ __forceinline__ bool more() const { return t < t1; }
+  __device__ __forceinline__ Span next(const Kv4AttnParams& p, int cols) {
+    Span s;
+    s.g = g;
+    s.units = units_of(cols);
+    const int64_t at = t - base;
+    s.ht = static_cast<int>(at / s.units);
+    s.u0 = static_cast<int>(at - static_cast<int64_t>(s.ht) * s.units);
+    const int64_t left = t1 - t;
+    s.u1 = left < s.units - s.u0 ? s.u0 + static_cast<int>(left) : s.units;
+    s.first = first;
+    first = false;
+    t += s.u1 - s.u0;
+    if (s.u1 == s.units && s.ht == p.Hkv * p.row_tiles - 1) {
+      ++g;
+      base = t;
+    }
+    return s;
+  }
+  // The CTA that takes unit x.
+  __device__ __forceinline__ int cta_of(int64_t x) const {
+    return static_cast<int>(((x + 1) * P - 1) / total);
+  }
+};
+
+// What a CTA leaves for the join: the span it begins and does not end.
+//   .x group, or -1; .y head and row tile; .z the last CTA of that span;
+//   .w which of this CTA's two partial results it is (the others' are their
+//   first)
+template <bool kSel, int kUnit>
+__device__ __forceinline__ void note_span(const Kv4AttnParams& p, const Walk<kSel, kUnit>& w,
+                                          const Span& s) {
+  if (threadIdx.x != 0 || s.u0 != 0 || s.u1 == s.units) return;
+  const int64_t last = w.t - s.u1 + s.units - 1;
+  p.spans[blockIdx.x] = make_int4(s.g, s.ht, w.cta_of(last), s.first ? 0 : 1);
+}
+
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Where query row n (of a group's rows for one key/value head) lies: the row
@@ -210,6 +342,37 @@ __device__ __forceinline__ int64_t head_row(const Kv4AttnParams& p, int g, int h
   return row * p.Hq + head * p.heads + (n - j * p.heads);
 }
 
+// Which kernel takes a CTA's rows (padded to 8, 16, 32 or 64).
+constexpr bool uses_tc(int rows) { return rows > 16; }
+
+// One row's four channels d .. d + 3: the result, when the columns summed are
+// all of the row's, else the partial sums `part` (M: reference of the weights,
+// base 2; L: their sum; a: the weighted values).
+template <int D, int kRows, bool kSel, bool kScores>
+__device__ __forceinline__ void write_row(const Kv4AttnParams& p, int grp, int ht, int row0,
+                                          int nrows, int row, int d, bool whole, int64_t part,
+                                          float M, float L, float4 a) {
+  const int per_split = p.Hkv * p.row_tiles;
+  const int head = ht / p.row_tiles;
+  const int n = row0 + row;
+  if (whole) {
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const float lse2 = M + log2f(L);
+    if (n < nrows) {
+      const int64_t hr = head_row<kSel>(p, grp, head, n);
+      *reinterpret_cast<uint2*>(p.out + hr * D + d) =
+          make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+      if (d == 0 && p.lse) p.lse[hr] = L == 0.f ? -INFINITY : lse2 * 0.69314718055994531f;
+    }
+    if (kScores && d == 0)
+      p.lse2[(static_cast<int64_t>(grp) * per_split + ht) * kRows + row] =
+          n >= nrows || L == 0.f ? INFINITY : lse2;
+  } else {
+    *reinterpret_cast<float4*>(p.part_o + (part * kRows + row) * D + d) = a;
+    if (d == 0) *reinterpret_cast<float2*>(p.part_ml + (part * kRows + row) * 2) = make_float2(M, L);
+  }
+}
+
 template <int D, int NT, bool kSel, bool kScores>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     kv4_attn_kernel(const __grid_constant__ Kv4AttnParams p) {
@@ -219,24 +382,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, t = lane & 3;
-
-  // head and row tile fastest: neighbouring CTAs read neighbouring heads of
-  // the same pages.
-  const int per_split = p.Hkv * p.row_tiles;
-  int64_t id = blockIdx.x;
-  const int ht = static_cast<int>(id % per_split);
-  id /= per_split;
-  const int split = static_cast<int>(id % p.nsplit);
-  const int grp = static_cast<int>(id / p.nsplit);
-  const int head = ht / p.row_tiles;
-  const int row0 = (ht % p.row_tiles) * kRows;
-  const int nrows = kSel ? p.heads : p.heads * p.next_n;
-
-  const Group gr = group_of<kSel>(p, grp, split == 0 && ht == 0 && threadIdx.x == 0);
-  const int c0 = split * p.chunk;
-  if (c0 >= gr.cols && split > 0) return;
-  const int c1 = min(gr.cols, c0 + p.chunk);
-  const bool whole = gr.cols <= p.chunk;
 
   uint8_t* const tiles_p = smem + warp * Lay::kWarpTiles;
   uint8_t* const rest_p = smem + kWarps * Lay::kWarpTiles + warp * Lay::kWarpRest;
@@ -250,6 +395,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
     __syncwarp();
   }
+  const int per_split = p.Hkv * p.row_tiles;
+  const int nrows = kSel ? p.heads : p.heads * p.next_n;
+  Walk<kSel, kTile * kWarps> walk(p);
+  launch_dependents();
+  if (threadIdx.x == 0 && p.spans) p.spans[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  int s = 0;           // stage and phase of this warp's next tile
+  uint32_t phase = 0;
+  bool ok = true;
+  while (walk.more() && __syncthreads_and(ok)) {
+  const Group gr = group_of<kSel>(p, walk.g);
+  const Span span = walk.next(p, gr.cols);
+  note_span(p, walk, span);
+  const int grp = span.g, ht = span.ht;
+  const int head = ht / p.row_tiles;
+  const int row0 = (ht % p.row_tiles) * kRows;
+  const int c0 = span.u0 * (kTile * kWarps);
+  const int c1 = min(gr.cols, span.u1 * (kTile * kWarps));
 
   // ------------------------------------------------------------------ loads
   // Tiles of this warp: columns c0 + 64 (warp + 4 i), in stage i % kStages.
@@ -347,9 +509,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   uint2 cols[kStages];  // oldest first
   if (kSel) read_columns(warp);
 #pragma unroll
-  for (int s = 0; s < kStages; ++s) {
-    locate(warp + s * kWarps);
-    cols[s] = fetch(s, warp + s * kWarps);
+  for (int i = 0; i < kStages; ++i) {
+    locate(warp + i * kWarps);
+    cols[i] = fetch((s + i) % kStages, warp + i * kWarps);
   }
 
   // ---------------------------------------------------------------- queries
@@ -456,9 +618,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                        : Lay::chunk_at(v_row[i], 2 + (r >> 2)) + (r & 3) * 4;
   const uint32_t ks_at = rest + Lay::kKeyScales, fac_at = rest + Lay::kFactors;
 
-  int s = 0;
-  uint32_t phase = 0;
-  bool ok = true;
   for (int tile = warp; tile < tiles; tile += kWarps) {
     locate(tile + kStages * kWarps);  // what it reads returns under this tile's work
     const int col0 = c0 + tile * kTile;
@@ -749,8 +908,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             }
 #pragma unroll
             for (int i = 0; i < G / 2; ++i) {
-              lo[h][i] = (va[i] & 0x0F0F0F0Fu) | ((vb[i] << 4) & 0xF0F0F0F0u);
-              hi[h][i] = ((va[i] >> 4) & 0x0F0F0F0Fu) | (vb[i] & 0xF0F0F0F0u);
+              lo[h][i] = low_nibbles_of(va[i], vb[i] << 4);
+              hi[h][i] = low_nibbles_of(va[i] >> 4, vb[i]);
             }
           }
 #pragma unroll
@@ -821,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         o[nt][2 * g + 1][i] * unit, o[nt][2 * g + 1][2 + i] * unit);
     }
   __syncthreads();
-  const int64_t part = (static_cast<int64_t>(grp) * p.nsplit + split) * per_split + ht;
+  const int64_t part = static_cast<int64_t>(blockIdx.x) * 2 + (span.first ? 0 : 1);
   for (int e = threadIdx.x; e < kRows * D / 4; e += kThreads) {
     const int row = e / (D / 4), d = (e % (D / 4)) * 4;
     float M = -INFINITY;
@@ -838,71 +997,732 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       a.x = fmaf(x.x, f, a.x), a.y = fmaf(x.y, f, a.y);
       a.z = fmaf(x.z, f, a.z), a.w = fmaf(x.w, f, a.w);
     }
-    const int n = row0 + row;
-    if (whole) {
-      const float inv = L == 0.f ? 0.f : 1.f / L;
-      const float lse2 = M + log2f(L);
-      if (n < nrows) {
-        const int64_t hr = head_row<kSel>(p, grp, head, n);
-        *reinterpret_cast<uint2*>(p.out + hr * D + d) =
-            make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
-        if (d == 0 && p.lse) p.lse[hr] = L == 0.f ? -INFINITY : lse2 * 0.69314718055994531f;
-      }
-      if (kScores && d == 0)
-        p.lse2[(static_cast<int64_t>(grp) * per_split + ht) * kRows + row] =
-            n >= nrows || L == 0.f ? INFINITY : lse2;
-    } else {
-      *reinterpret_cast<float4*>(p.part_o + (part * kRows + row) * D + d) = a;
-      if (d == 0)
-        *reinterpret_cast<float2*>(p.part_ml + (part * kRows + row) * 2) = make_float2(M, L);
-    }
+    write_row<D, kRows, kSel, kScores>(p, grp, ht, row0, nrows, row, d, span.whole(), part, M, L,
+                                       a);
+  }
+  // The next span's copies overwrite what was read and written here.
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
 }
 
-// Joins the partial sums of a group's chunks: one CTA per group, head and row
-// tile, D/4 threads a row.
-template <int D, int NT, bool kSel, bool kScores>
+constexpr int kTcTile = 128;    // columns of a tile: one TMEM lane each
+constexpr int kTcThreads = 128;
+constexpr int kTcStages = 2;
+constexpr float kUnseen = -1e30f;  // exponent reference of a row that has seen no column
+
+// Shared memory of a CTA (1024-byte aligned).
+template <int D, int N>
+struct TcLayout {
+  static constexpr int G = D / kMxBlock;
+  static constexpr int kTileBytes = kTcTile * D;
+  static constexpr int kSc = D / 16;
+  static constexpr int kTiles = 0;
+  static constexpr int kValues = kTiles + kTcStages * kTileBytes;  // fp16 [key][D], and at the end
+  static constexpr int kValueBytes = kTcTile * D * 2;              // fp32 [row][D]
+  static constexpr int kQ = kValues + kValueBytes;                 // fp16 [row][D]
+  static constexpr int kP = kQ + N * D * 2;                        // fp16 [key][row]
+  static constexpr int kScales = kP + kTcTile * N * 2;
+  static constexpr int kFz = kScales + kTcStages * kTcTile * kSc;  // float2 [row]: F, z
+  static constexpr int kRowF = kFz + N * 8;
+  static constexpr int kLimit = kRowF + N * 4;
+  static constexpr int kAlpha = kLimit + N * 4;
+  static constexpr int kNan = kAlpha + N * 4;
+  static constexpr int kPart = kNan + N * 4;       // [4][row] of a reduction over warps
+  static constexpr int kRed = kPart + 4 * N * 4;   // [2][4]
+  static constexpr int kBars = (kRed + 32 + 7) / 8 * 8;
+  static constexpr int kSlot = kBars + 8 * (kTcStages + 2);
+  static constexpr int kBytes = kSlot + 16;
+  static constexpr int kTmemK = 0;                 // columns: K', S, O
+  static constexpr int kTmemS = D / 2;
+  static constexpr int kTmemO = kTmemS + N;
+  static constexpr int kTmemCols = kTmemO + N <= 128 ? 128 : 256;
+  static constexpr int kCtas = N == 16 ? 3 : 2;    // an SM holds
+};
+
+__device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
+      "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_load_row(uint32_t taddr, float (&v)[N]) {
+  if constexpr (N == 16) tmem_load16(taddr, v);
+  else if constexpr (N == 32) tmem_load32(taddr, v);
+  else tmem_load64(taddr, v);
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_store_row(uint32_t taddr, const float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 16) {
+    uint32_t r[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(v[i + j]);
+    tmem_store16(taddr + i, r);
+  }
+}
+
+// D (+)= A B^T with A [128 x 16] fp16 in TMEM, B from shared memory.
+__device__ __forceinline__ void mma_ts_f16(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Shared-memory descriptor of an operand stored M- (or N-) major: rows of 2^s
+// bytes along M, one row per k, swizzled over the row (mode 2: 128 bytes, 4:
+// 64, 6: 32); `lead` bytes between row-wide blocks along M, eight k rows `row8`
+// bytes apart.
+__device__ __forceinline__ uint64_t mn_major_desc(uint32_t saddr, uint32_t lead, uint32_t row8,
+                                                  uint32_t mode) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>((lead >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>((row8 >> 4) & 0x3FFFu) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(mode) << 61;
+  return d;
+}
+
+// K-major, rows of 2^s bytes (128 or 64: the swizzle), eight rows `row8` apart.
+__device__ __forceinline__ uint64_t k_major_desc(uint32_t saddr, uint32_t row8, uint32_t mode) {
+  return mn_major_desc(saddr, 16, row8, mode);
+}
+
+__device__ __forceinline__ uint32_t order_f32(float x) {  // order of floats as unsigned
+  const uint32_t u = __float_as_uint(x);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float unorder_f32(uint32_t u) {
+  return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
+}
+
+template <int D, int N, bool kSel, bool kScores>
+__global__ void __launch_bounds__(kTcThreads, TcLayout<D, N>::kCtas)
+    kv4_attn_tc_kernel(const __grid_constant__ Kv4AttnParams p) {
+  using Lay = TcLayout<D, N>;
+  constexpr int G = Lay::G;
+  constexpr int kChunks = D / 16;
+  constexpr float kSlack = 8.f;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  const int per_split = p.Hkv * p.row_tiles;
+  const int nrows = kSel ? p.heads : p.heads * p.next_n;
+  const uint32_t sb = smem_u32(smem);
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + Lay::kBars);
+  uint64_t* const s_done = full + kTcStages;
+  uint64_t* const o_done = s_done + 1;
+  volatile uint32_t* const slot = reinterpret_cast<volatile uint32_t*>(smem + Lay::kSlot);
+  volatile uint32_t* const abort_flag = slot + 1;
+  float2* const fz = reinterpret_cast<float2*>(smem + Lay::kFz);
+  float* const row_f = reinterpret_cast<float*>(smem + Lay::kRowF);
+  int* const limit = reinterpret_cast<int*>(smem + Lay::kLimit);
+  float* const alpha = reinterpret_cast<float*>(smem + Lay::kAlpha);
+  uint32_t* const nan_rows = reinterpret_cast<uint32_t*>(smem + Lay::kNan);
+  uint32_t* const part = reinterpret_cast<uint32_t*>(smem + Lay::kPart);
+  uint32_t* const red = reinterpret_cast<uint32_t*>(smem + Lay::kRed);
+
+  if (tid == 0) {
+    for (int s = 0; s < kTcStages; ++s) mbar_init(&full[s], 1);
+    mbar_init(s_done, 1);
+    mbar_init(o_done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncwarp();
+  if (warp == 0) tmem_alloc(const_cast<uint32_t*>(reinterpret_cast<volatile uint32_t*>(slot)),
+                            Lay::kTmemCols);
+  Walk<kSel, kTcTile> walk(p);
+  launch_dependents();
+  if (tid == 0 && p.spans) p.spans[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *slot;
+  const uint32_t lanes = tmem + (static_cast<uint32_t>(warp) << 21);  // this warp's 32 lanes
+  uint32_t done = 0;  // tiles so far: their stages and phases
+  bool ok = true;
+  while (walk.more() && __syncthreads_and(ok)) {
+  const Group gr = group_of<kSel>(p, walk.g);
+  const Span span = walk.next(p, gr.cols);
+  note_span(p, walk, span);
+  const int grp = span.g, ht = span.ht;
+  const int head = ht / p.row_tiles;
+  const int row0 = (ht % p.row_tiles) * N;
+  const int c0 = span.u0 * kTcTile;
+  const int c1 = min(gr.cols, span.u1 * kTcTile);
+  const int tiles = (c1 - c0 + kTcTile - 1) / kTcTile;
+
+  // ------------------------------------------------------------------ loads
+  const int bs_mask = (1 << p.log_bs) - 1;
+  const int32_t* table = p.block_table + static_cast<int64_t>(gr.b) * p.max_blocks;
+  auto page_of = [&](int block) {
+    if (block < 0 || block >= p.num_blocks) {
+      record_error(p.err, kErrBadIndex);
+      block = 0;
+    }
+    return static_cast<uint32_t>(block) * p.Hkv + head;
+  };
+  // Dense: lane i of warp 0 reads the page of the tile's i-th run of `rows`
+  // tokens.  Selected: thread i has column i, read a tile before its page.
+  const int rows = min(1 << p.log_bs, kTcTile);
+  int pos = -1, next_pos = -1, block = 0;
+  auto read_column = [&](int tile) {
+    const int col = c0 + tile * kTcTile + tid;
+    next_pos = col < c1 ? __ldg(p.sel + static_cast<int64_t>(grp) * p.sel_k + col) : -1;
+  };
+  auto locate = [&](int tile) {
+    if constexpr (kSel) {
+      pos = next_pos;
+      if (pos < -1 || pos >= gr.limit) {
+        record_error(p.err, kErrBadIndex);
+        pos = -1;
+      }
+      if (pos >= 0) block = __ldg(table + (pos >> p.log_bs));
+      read_column(tile + 1);
+    } else if (warp == 0) {
+      pos = c0 + tile * kTcTile + lane * rows;
+      if (lane * rows >= kTcTile || pos >= c1) pos = -1;
+      else block = __ldg(table + (pos >> p.log_bs));
+    }
+  };
+  // Starts the copies of the located tile into stage s; returns whether this
+  // thread's column (selected) is there.  Warp w copies columns 32 w .. + 31.
+  auto fetch = [&](int s, int tile) {
+    bool here = false;
+    if constexpr (kSel) {
+      here = pos >= 0;
+      const uint32_t cols = __ballot_sync(0xffffffffu, here);
+      const uint32_t rec = here ? (page_of(block) << p.log_bs) + (pos & bs_mask) : 0u;
+      const uint32_t base = sb + Lay::kTiles + s * Lay::kTileBytes;
+      constexpr int kPer = 32 / kChunks;
+      const int c = lane % kChunks;
+      if (cols) {
+#pragma unroll
+        for (int i = 0; i < 32 / kPer; ++i) {
+          const int row = i * kPer + lane / kChunks;
+          const uint32_t rc = __shfl_sync(0xffffffffu, rec, row);
+          cp_async16(base + Layout<D, 1>::chunk_at(warp * 32 + row, c),
+                     p.cache + static_cast<int64_t>(rc) * D + c * 16,
+                     (cols >> row) & 1 ? 16u : 0u);
+        }
+        cp_async_small<Lay::kSc>(sb + Lay::kScales + (s * kTcTile + tid) * Lay::kSc,
+                                 p.scales + static_cast<int64_t>(rec) * Lay::kSc,
+                                 here ? Lay::kSc : 0);
+      }
+      cp_async_commit();
+    } else if (warp == 0 && tile < tiles) {
+      const int n = __popc(__ballot_sync(0xffffffffu, pos >= 0));
+      if (lane == 0) mbar_arrive_expect_tx(&full[s], n * rows * (D + Lay::kSc));
+      __syncwarp();
+      if (pos >= 0) {
+        const uint32_t page = page_of(block);
+        const int at = pos & bs_mask;
+        tma_load_3d(smem + Lay::kTiles + s * Lay::kTileBytes + lane * rows * D, &p.tmap, &full[s],
+                    0, at, static_cast<int>(page));
+        bulk_load(sb + Lay::kScales + (s * kTcTile + lane * rows) * Lay::kSc,
+                  p.scales + ((static_cast<int64_t>(page) << p.log_bs) + at) * Lay::kSc,
+                  rows * Lay::kSc, &full[s]);
+      }
+    }
+    return here;
+  };
+  bool here[kTcStages];
+  if (kSel) read_column(0);
+#pragma unroll
+  for (int i = 0; i < kTcStages; ++i) {
+    locate(i);
+    here[i] = fetch((done + i) % kTcStages, i);
+  }
+
+  // ---------------------------------------------------------------- queries
+  // Row n as fp16 in the keys' order of codes, K-major, swizzled over 128
+  // bytes (64 elements); D/16 threads a row, 16 elements each.
+  const bool zero = p.scale_log2e == 0.f;
+  const float sign = zero ? 0.f : (p.scale_log2e < 0.f ? -1.f : 1.f);
+  {
+    constexpr int kPer = D / 16;
+    const int sub = tid % kPer;
+#pragma unroll
+    for (int it = 0; it < (N * kPer + kTcThreads - 1) / kTcThreads; ++it) {
+      const int n = it * (kTcThreads / kPer) + tid / kPer;
+      if (n >= N) break;  // whole warps
+      uint4 raw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+      if (row0 + n < nrows) {
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.q + head_row<kSel>(p, grp, head, row0 + n) * D + sub * 16);
+        raw[0] = __ldg(src), raw[1] = __ldg(src + 1);
+      }
+      uint32_t amax = 0;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          amax = max(amax, max((w[i] << 16) & 0x7FFF0000u, w[i] & 0x7FFF0000u));
+      }
+#pragma unroll
+      for (int x = 1; x < kPer; x <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, x));
+      const int E = amax == 0 || amax >= 0x7F800000u
+                        ? 0
+                        : max(static_cast<int>(amax >> 23), 1) - 127;
+      const float down = ldexpf(sign, -E);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+        const int lc = sub * 2 + j;                       // elements 8 lc ..: block lc / 4
+        const int kc = (lc % 4) * G + lc / 4;             // their place in a record
+        const uint32_t at = sb + Lay::kQ + (kc / 8) * (N * 128) + n * 128 +
+                            (((kc % 8) ^ (n & 7)) << 4);
+        sts128(at, pack_f16(bf16_lo(w[0]) * down, bf16_hi(w[0]) * down),
+               pack_f16(bf16_lo(w[1]) * down, bf16_hi(w[1]) * down),
+               pack_f16(bf16_lo(w[2]) * down, bf16_hi(w[2]) * down),
+               pack_f16(bf16_lo(w[3]) * down, bf16_hi(w[3]) * down));
+      }
+      if (sub == 0) {
+        row_f[n] = zero ? 1.f : ldexpf(fabsf(p.scale_log2e), E);
+        fz[n] = make_float2(0.f, kUnseen);
+        limit[n] = kSel ? gr.cols
+                        : gr.L - p.next_n + min((row0 + n) / p.heads, p.next_n - 1) + 1;
+        nan_rows[n] = 0;
+      }
+    }
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncthreads();
+  const int all_see = kSel ? gr.cols : gr.L - p.next_n + 1;
+
+  float l[N];  // this key lane's share of every row's sum
+#pragma unroll
+  for (int n = 0; n < N; ++n) l[n] = 0.f;
+  // References of the key and value scales (E8M0 bits as fp32): raised to the
+  // largest scale so far when one passes them by 2^kSlack.
+  float k_ref = 0.f, v_ref = 0.f, k_inv = 0.f, v_inv = 0.f;
+
+  constexpr uint32_t kIdescS = mma_idesc(0, 128, N);
+  constexpr uint32_t kIdescO = mma_idesc(0, 128, N) | (1u << 15) | (1u << 16);
+  constexpr uint32_t kModeP = N == 16 ? 6 : (N == 32 ? 4 : 2);
+  for (int tile = 0; tile < tiles; ++tile, ++done) {
+    const int s = done % kTcStages;
+    locate(tile + kTcStages);
+    const int col = c0 + tile * kTcTile + tid;
+    bool valid, fail = false;  // fail: a wait gave up (votes carry it to every thread)
+    if constexpr (kSel) {
+      cp_async_wait<kTcStages - 1>();
+      __syncwarp();
+      valid = here[0];
+    } else {
+      if (!mbar_wait_bounded(&full[s], (done / kTcStages) & 1, abort_flag)) fail = true;
+      valid = col < c1;
+    }
+    const uint32_t base = sb + Lay::kTiles + s * Lay::kTileBytes;
+    // ---------------------------------------------------------------- scales
+    uint32_t kw, vw;
+    {
+      const uint32_t at = sb + Lay::kScales + (s * kTcTile + tid) * Lay::kSc;
+      if constexpr (D == 128) {
+        const uint2 u = lds64(at);
+        kw = u.x, vw = u.y;
+      } else {
+        const uint32_t u = lds32(at);
+        kw = u & 0xFFFFu, vw = u >> 16;
+      }
+      if (!valid) kw = vw = 0u;
+    }
+    uint32_t kf[G], vf[G];
+    auto unpack_scales = [&](uint32_t w, uint32_t (&f)[G]) {
+      f[0] = e8m0_bits<0>(w), f[1] = e8m0_bits<1>(w);
+      if constexpr (D == 128) f[2] = e8m0_bits<2>(w), f[3] = e8m0_bits<3>(w);
+    };
+    unpack_scales(kw, kf);
+    unpack_scales(vw, vf);
+    bool k_nan = false;
+    if (has_ff(kw) | has_ff(vw)) {
+      // NaN scales (rare): a key's makes its logits NaN, a value's makes its
+      // 32 channels of every row that sees the column NaN at the end.
+      k_nan = has_ff(kw) != 0;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        if (kf[g] == 0x7F800000u) kf[g] = 0u;
+        if (vf[g] == 0x7F800000u) {
+          vf[g] = 0u;
+          for (int n = 0; n < N; ++n)
+            if (col < limit[n]) atomicOr(&nan_rows[n], 1u << g);
+        }
+      }
+    }
+    uint32_t k_top = kf[0], v_top = vf[0];
+#pragma unroll
+    for (int g = 1; g < G; ++g) k_top = max(k_top, kf[g]), v_top = max(v_top, vf[g]);
+    const bool passes = __uint_as_float(k_top) > k_ref * 256.f ||
+                        __uint_as_float(v_top) > v_ref * 256.f;
+    // ------------------------------------------------------ K' = K 2^-ref to TMEM
+    auto put_keys = [&]() {
+      uint32_t fac[G];
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const float x = __uint_as_float(kf[g]) * k_inv;
+        fac[g] = pack_f16(x, x);
+      }
+      if (k_nan) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) fac[g] = 0x7E007E00u;
+      }
+      uint32_t r[32];
+#pragma unroll
+      for (int c = 0; c < kChunks / 2; ++c) {
+        const uint4 u = lds128(base + Layout<D, 1>::chunk_at(tid, c));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int g = i % G, at = (c % 2) * 16 + i * 4;
+          r[at] = mul_f16x2(e2m1x2_to_f16x2<0>(w[i]), fac[g]);
+          r[at + 1] = mul_f16x2(e2m1x2_to_f16x2<1>(w[i]), fac[g]);
+          r[at + 2] = mul_f16x2(e2m1x2_to_f16x2<2>(w[i]), fac[g]);
+          r[at + 3] = mul_f16x2(e2m1x2_to_f16x2<3>(w[i]), fac[g]);
+        }
+        if (c % 2 == 1) tmem_store32(lanes + Lay::kTmemK + (c / 2) * 32, r);
+      }
+      tmem_wait_st();
+    };
+    put_keys();
+    tc_fence_before_sync();
+    if (fail) *abort_flag = 1;
+    if (__syncthreads_or(passes || fail)) {
+      // Rare: larger scales than the references allow for.  New references,
+      // the keys once more, and what is accumulated in the new unit.
+      tc_fence_after_sync();
+      const uint32_t kt = __reduce_max_sync(0xffffffffu, k_top);
+      const uint32_t vt = __reduce_max_sync(0xffffffffu, v_top);
+      if (lane == 0) red[warp] = kt, red[4 + warp] = vt;
+      if (tile > 0 && !mbar_wait_bounded(o_done, (done - 1) & 1, abort_flag)) *abort_flag = 1;
+      __syncthreads();
+      if (*abort_flag) {
+        ok = false;
+        break;
+      }
+      const float kn = fmaxf(k_ref, __uint_as_float(max(max(red[0], red[1]), max(red[2], red[3]))));
+      const float vn = fmaxf(v_ref, __uint_as_float(max(max(red[4], red[5]), max(red[6], red[7]))));
+      if (kn != k_ref) {
+        k_ref = kn;
+        k_inv = 1.f / kn;
+        if (tid < N) fz[tid].x = row_f[tid] * kn;
+      }
+      if (vn != v_ref) {
+        if (tile > 0) {
+          const float down = v_ref / vn;
+          float o[N];
+          tc_fence_after_sync();
+          tmem_load_row<N>(lanes + Lay::kTmemO, o);
+#pragma unroll
+          for (int n = 0; n < N; ++n) o[n] *= down;
+          tmem_store_row<N>(lanes + Lay::kTmemO, o);
+          tmem_wait_st();
+        }
+        v_ref = vn;
+        v_inv = 1.f / vn;
+      }
+      put_keys();
+      tc_fence_before_sync();
+      __syncthreads();
+    }
+    // ------------------------------------------------------------- S = K' q^T
+    if (tid == 0) {
+      tc_fence_after_sync();
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        mma_ts_f16(tmem + Lay::kTmemS, tmem + Lay::kTmemK + k * 8,
+                   k_major_desc(sb + Lay::kQ + (k / 4) * (N * 128) + (k % 4) * 32, 1024, 2),
+                   kIdescS, k > 0);
+      mma_commit(s_done);
+    }
+    // ------------------------------------ V' = V 2^-ref, when the last tile's is used
+    if (tile > 0 && !mbar_wait_bounded(o_done, (done - 1) & 1, abort_flag)) fail = true;
+    {
+      uint32_t fac[G];
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const float x = __uint_as_float(vf[g]) * v_inv;
+        fac[g] = pack_f16(x, x);
+      }
+#pragma unroll
+      for (int c = 0; c < kChunks / 2; ++c) {
+        const uint4 u = lds128(base + Layout<D, 1>::chunk_at(tid, kChunks / 2 + c));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int g = (2 * i) % G;  // blocks of the word's two units
+          const int m8 = c * 4 + i;   // its eight channels' place
+          sts128(sb + Lay::kValues + (m8 / 8) * (kTcTile * 128) + tid * 128 +
+                     (((m8 % 8) ^ (tid & 7)) << 4),
+                 mul_f16x2(e2m1x2_to_f16x2<0>(w[i]), fac[g]),
+                 mul_f16x2(e2m1x2_to_f16x2<1>(w[i]), fac[g]),
+                 mul_f16x2(e2m1x2_to_f16x2<2>(w[i]), fac[g + 1]),
+                 mul_f16x2(e2m1x2_to_f16x2<3>(w[i]), fac[g + 1]));
+        }
+      }
+    }
+    // ---------------------------------------------------------------- softmax
+    if (!mbar_wait_bounded(s_done, done & 1, abort_flag)) fail = true;
+    tc_fence_after_sync();
+    float x[N];
+    tmem_load_row<N>(lanes + Lay::kTmemS, x);
+    const bool clean = c0 + (tile + 1) * kTcTile <= min(c1, all_see) && (!kSel || valid);
+    if constexpr (kScores) {
+      if (col < c1) {
+        float* dst = p.scores +
+                     ((static_cast<int64_t>(grp) * per_split + ht) * p.cols + col) * N;
+#pragma unroll
+        for (int n = 0; n < N; n += 4) {
+          float v[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            v[j] = valid && (kSel || col < limit[n + j]) ? x[n + j] * fz[n + j].x : -INFINITY;
+          *reinterpret_cast<float4*>(dst + n) = make_float4(v[0], v[1], v[2], v[3]);
+        }
+      }
+    }
+    float mx = -INFINITY;
+    auto weights = [&]() {
+      float pr[N];
+#pragma unroll
+      for (int n = 0; n < N; n += 2) {
+        const float4 c = *reinterpret_cast<const float4*>(&fz[n]);
+        float e0 = fmaf(x[n], c.x, -c.y), e1 = fmaf(x[n + 1], c.z, -c.w);
+        if (!clean) {
+          if (!valid || (!kSel && col >= limit[n])) e0 = -INFINITY;
+          if (!valid || (!kSel && col >= limit[n + 1])) e1 = -INFINITY;
+        }
+        mx = fmaxf(mx, fmaxf(e0, e1));
+        pr[n] = ex2(e0), pr[n + 1] = ex2(e1);
+      }
+#pragma unroll
+      for (int c = 0; c < N / 8; ++c) {
+        const int f = N == 16 ? (tid >> 2) & 1 : (N == 32 ? (tid >> 1) & 3 : tid & 7);
+        sts128(sb + Lay::kP + tid * (2 * N) + ((c ^ f) << 4),
+               pack_f16(pr[8 * c], pr[8 * c + 1]), pack_f16(pr[8 * c + 2], pr[8 * c + 3]),
+               pack_f16(pr[8 * c + 4], pr[8 * c + 5]), pack_f16(pr[8 * c + 6], pr[8 * c + 7]));
+      }
+      return [&l, pr]() {
+#pragma unroll
+        for (int n = 0; n < N; ++n) l[n] += pr[n];
+      };
+    };
+    auto add = weights();
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    tc_fence_before_sync();
+    if (fail) *abort_flag = 1;
+    if (__syncthreads_or(mx > kSlack || fail)) {
+      // Rare: a logit far above its row's reference.  Rows' maxima over the
+      // tile, new references, and what is accumulated (sums here, O in TMEM).
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        float v = valid && (kSel || col < limit[n]) ? x[n] * fz[n].x : -INFINITY;
+        if (!(v == v)) v = -INFINITY;  // a NaN stays one without a reference
+        const uint32_t w = __reduce_max_sync(0xffffffffu, order_f32(v));
+        if (lane == 0) part[warp * N + n] = w;
+      }
+      __syncthreads();
+      if (*abort_flag) {
+        ok = false;
+        break;
+      }
+      if (tid < N) {
+        const float z = fz[tid].y;
+        const float top = unorder_f32(max(max(part[tid], part[N + tid]),
+                                          max(part[2 * N + tid], part[3 * N + tid])));
+        float a = 1.f;
+        if (top > z + kSlack) {
+          a = z == kUnseen ? 0.f : ex2(z - top);
+          fz[tid].y = top;
+        }
+        alpha[tid] = a;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < N; ++n) l[n] *= alpha[n];
+      if (tile > 0) {
+        float o[N];
+        tc_fence_after_sync();
+        tmem_load_row<N>(lanes + Lay::kTmemO, o);
+#pragma unroll
+        for (int n = 0; n < N; ++n) o[n] *= alpha[n];
+        tmem_store_row<N>(lanes + Lay::kTmemO, o);
+        tmem_wait_st();
+      }
+      auto again = weights();
+      again();
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      tc_fence_before_sync();
+      __syncthreads();
+    } else {
+      add();
+    }
+    // --------------------------------------------------------------- O += V'^T P
+    if (tid == 0) {
+      tc_fence_after_sync();
+#pragma unroll
+      for (int k = 0; k < kTcTile / 16; ++k)
+        mma_ss<false>(tmem + Lay::kTmemO,
+                      mn_major_desc(sb + Lay::kValues + k * 2048, D == 128 ? kTcTile * 128 : 0,
+                                    1024, 2),
+                      mn_major_desc(sb + Lay::kP + k * (32 * N), 16, 16 * N, kModeP), kIdescO,
+                      tile > 0 || k > 0);
+      mma_commit(o_done);
+    }
+    const bool h = fetch(s, tile + kTcStages);
+#pragma unroll
+    for (int i = 0; i + 1 < kTcStages; ++i) here[i] = here[i + 1];
+    here[kTcStages - 1] = h;
+  }
+  if (ok && tiles > 0) {
+    if (!mbar_wait_bounded(o_done, (done - 1) & 1, abort_flag)) ok = false;
+  } else if (!ok) {
+    // A copy or a product never came: report, and give what is in flight its
+    // time.
+    if (tid == 0) record_error(p.err, kErrTimeout);
+    if (!kSel)
+      for (int i = 0; i < kTcStages; ++i)
+        mbar_wait_bounded(&full[(done + i) % kTcStages], ((done + i) / kTcStages) & 1, nullptr);
+    mbar_wait_bounded(s_done, done & 1, nullptr, 1000000);
+    mbar_wait_bounded(o_done, done & 1, nullptr, 1000000);
+  }
+  cp_async_wait<0>();
+  tc_fence_after_sync();
+
+  // -------------------------------------------------------------- write out
+  // O^T's lane m holds channel 32 g + 4 r + i, m = (r G + g) 4 + i.
+  float* const so = reinterpret_cast<float*>(smem + Lay::kValues);  // [row][D]
+  if (tiles > 0) {
+    float o[N];
+    tmem_load_row<N>(lanes + Lay::kTmemO, o);
+    tc_fence_before_sync();
+    if (tid < D) {
+      const int g = (tid / 4) % G, r = tid / (4 * G), d = 32 * g + 4 * r + tid % 4;
+#pragma unroll
+      for (int n = 0; n < N; ++n) so[n * D + d] = o[n] * v_ref;
+    }
+    float* const lp = reinterpret_cast<float*>(part);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      float v = l[n];
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+      if (lane == 0) lp[warp * N + n] = v;
+    }
+  }
+  __syncthreads();
+  const int64_t pt = static_cast<int64_t>(blockIdx.x) * 2 + (span.first ? 0 : 1);
+  for (int e = tid; e < N * D / 4; e += kTcThreads) {
+    const int row = e / (D / 4), d = (e % (D / 4)) * 4;
+    const float* lp = reinterpret_cast<const float*>(part);
+    float L = 0.f, M = -INFINITY;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (tiles > 0) {
+      L = (lp[row] + lp[N + row]) + (lp[2 * N + row] + lp[3 * N + row]);
+      a = *reinterpret_cast<const float4*>(so + row * D + d);
+      if (fz[row].y != kUnseen) M = fz[row].y;
+      if ((nan_rows[row] >> (d / 32)) & 1)
+        a.x = a.y = a.z = a.w = __uint_as_float(0x7FC00000u);
+    }
+    write_row<D, N, kSel, kScores>(p, grp, ht, row0, nrows, row, d, span.whole(), pt, M, L, a);
+  }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, Lay::kTmemCols);
+  }
+}
+
+// Joins the partial results of the spans that CTAs share: one CTA for every
+// CTA of the attention kernel (which had to begin the span) and row.  The
+// references first, then the channels, dealt over the partial results.
+constexpr int kMaxCtas = 1024;  // of the attention kernel (their factors fit shared memory)
+
+template <int D, int kRows, bool kSel, bool kScores>
 __global__ void __launch_bounds__(kThreads)
     kv4_join_kernel(const __grid_constant__ Kv4AttnParams p) {
-  constexpr int kRows = 8 * NT;
-  const int per_split = p.Hkv * p.row_tiles;
-  const int ht = static_cast<int>(blockIdx.x % per_split);
-  const int grp = static_cast<int>(blockIdx.x / per_split);
-  const int head = ht / p.row_tiles;
+  __shared__ float factor[kMaxCtas];
+  __shared__ float red[kWarps * 2];
+  __shared__ float4 sums[kThreads];
+  grid_dependency_wait();
+  const int cta = blockIdx.x / kRows, row = blockIdx.x % kRows;
+  const int4 sp = p.spans[cta];
+  if (sp.x < 0) return;
+  const int grp = sp.x, ht = sp.y, n = sp.z - cta + 1;
   const int row0 = (ht % p.row_tiles) * kRows;
   const int nrows = kSel ? p.heads : p.heads * p.next_n;
-  const Group gr = group_of<kSel>(p, grp, false);
-  if (gr.cols <= p.chunk) return;
-  const int ns = (gr.cols + p.chunk - 1) / p.chunk;
-  for (int e = threadIdx.x; e < kRows * D / 4; e += kThreads) {
-    const int row = e / (D / 4), d = (e % (D / 4)) * 4;
-    float M = -INFINITY, L = 0.f;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int sp = 0; sp < ns; ++sp) {
-      const int64_t part = (static_cast<int64_t>(grp) * p.nsplit + sp) * per_split + ht;
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (part * kRows + row) * 2);
-      const float4 x = *reinterpret_cast<const float4*>(p.part_o + (part * kRows + row) * D + d);
-      const float Mn = fmaxf(M, ml.x);
-      const float z = Mn == -INFINITY ? 0.f : Mn;
-      const float fo = ex2(M - z), fn = ex2(ml.x - z);
-      M = Mn;
-      L = L * fo + ml.y * fn;
-      a.x = a.x * fo + x.x * fn, a.y = a.y * fo + x.y * fn;
-      a.z = a.z * fo + x.z * fn, a.w = a.w * fo + x.w * fn;
-    }
-    const int n = row0 + row;
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    const float lse2 = M + log2f(L);
-    if (n < nrows) {
-      const int64_t hr = head_row<kSel>(p, grp, head, n);
-      *reinterpret_cast<uint2*>(p.out + hr * D + d) =
-          make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
-      if (d == 0 && p.lse) p.lse[hr] = L == 0.f ? -INFINITY : lse2 * 0.69314718055994531f;
-    }
-    if (kScores && d == 0)
-      p.lse2[(static_cast<int64_t>(grp) * per_split + ht) * kRows + row] =
-          n >= nrows || L == 0.f ? INFINITY : lse2;
+  if (!kScores && row0 + row >= nrows) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto part_of = [&](int i) {
+    return static_cast<int64_t>(cta + i) * 2 + (i == 0 ? sp.w : 0);
+  };
+  float M = -INFINITY;
+  for (int i = threadIdx.x; i < n; i += kThreads)
+    M = fmaxf(M, p.part_ml[(part_of(i) * kRows + row) * 2]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) red[warp] = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const float z = M == -INFINITY ? 0.f : M;
+  float L = 0.f;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (part_of(i) * kRows + row) * 2);
+    const float f = ex2(ml.x - z);
+    factor[i] = f;
+    L = fmaf(ml.y, f, L);
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  if (lane == 0) red[kWarps + warp] = L;
+  __syncthreads();
+  L = (red[kWarps] + red[kWarps + 1]) + (red[kWarps + 2] + red[kWarps + 3]);
+  constexpr int kQuads = D / 4, kDeal = kThreads / kQuads;
+  const int q = threadIdx.x % kQuads;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = threadIdx.x / kQuads; i < n; i += kDeal) {
+    const float4 x =
+        *reinterpret_cast<const float4*>(p.part_o + (part_of(i) * kRows + row) * D + q * 4);
+    const float f = factor[i];
+    a.x = fmaf(x.x, f, a.x), a.y = fmaf(x.y, f, a.y);
+    a.z = fmaf(x.z, f, a.z), a.w = fmaf(x.w, f, a.w);
+  }
+  sums[threadIdx.x] = a;
+  __syncthreads();
+  if (threadIdx.x >= kQuads) return;
+#pragma unroll
+  for (int i = 1; i < kDeal; ++i) {
+    const float4 x = sums[i * kQuads + q];
+    a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+  }
+  write_row<D, kRows, kSel, kScores>(p, grp, ht, row0, nrows, row, q * 4, true, 0, M, L, a);
 }
 
 // A column's attention weight, summed over heads and rows in one fixed order:
@@ -916,7 +1736,7 @@ __global__ void __launch_bounds__(256) kv4_weight_kernel(const __grid_constant__
   const int per_grp = (p.cols + 255) / 256;
   const int grp = static_cast<int>(blockIdx.x / per_grp);
   const int col = static_cast<int>(blockIdx.x % per_grp) * 256 + threadIdx.x;
-  const Group gr = group_of<kSel>(p, grp, false);
+  const Group gr = group_of<kSel>(p, grp);
   if (static_cast<int>(blockIdx.x % per_grp) * 256 >= gr.cols) return;
   extern __shared__ float lse_s[];
   for (int i = threadIdx.x; i < per_split * kRows; i += 256)
@@ -958,7 +1778,7 @@ __global__ void __launch_bounds__(1024)
   const int b = blockIdx.x;
   for (int j = 0; j < p.next_n; ++j) {
     const int64_t row = static_cast<int64_t>(b) * p.next_n + j;
-    const Group gr = group_of<true>(p, static_cast<int>(row), false);
+    const Group gr = group_of<true>(p, static_cast<int>(row));
     for (int c = threadIdx.x; c < p.sel_k; c += blockDim.x) {
       const int pos = __ldg(p.sel + row * p.sel_k + c);
       if (pos >= 0 && pos < gr.limit)
@@ -969,26 +1789,50 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-template <int D, int NT, bool kSel, bool kScores>
-cudaError_t launch_one(const Kv4AttnParams& p, cudaStream_t s) {
-  using Lay = Layout<D, NT>;
-  constexpr int kRing = Lay::kBytes;
-  constexpr int kJoin = kWarps * 8 * NT * (D + 2) * 4;
-  constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
-  auto* fn = kv4_attn_kernel<D, NT, kSel, kScores>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
-  const int64_t tiles = static_cast<int64_t>(p.groups) * p.Hkv * p.row_tiles;
-  fn<<<static_cast<unsigned>(tiles * p.nsplit), kThreads, kSmem, s>>>(p);
-  e = cudaGetLastError();
-  if (e == cudaSuccess && p.nsplit > 1) {
-    kv4_join_kernel<D, NT, kSel, kScores><<<static_cast<unsigned>(tiles), kThreads, 0, s>>>(p);
-    e = cudaGetLastError();
+// Rows of a CTA (padded), its kernel and what that takes.
+template <int D, int kRows, bool kSel, bool kScores>
+cudaError_t launch_rows(const Kv4AttnParams& p, cudaStream_t s) {
+  cudaError_t e;
+  auto launch = [&](auto* fn, int threads, int smem) {
+    static std::atomic<uint64_t> ready{0};  // devices this kernel's limit is set on
+    int dev = 0;
+    cudaError_t r = cudaGetDevice(&dev);
+    if (r != cudaSuccess) return r;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+      r = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (r != cudaSuccess) return r;
+      ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    fn<<<p.ctas, threads, smem, s>>>(p);
+    return cudaGetLastError();
+  };
+  if constexpr (!uses_tc(kRows)) {
+    using Lay = Layout<D, kRows / 8>;
+    constexpr int kJoin = kWarps * kRows * (D + 2) * 4;
+    e = launch(kv4_attn_kernel<D, kRows / 8, kSel, kScores>, kThreads,
+               Lay::kBytes > kJoin ? Lay::kBytes : kJoin);
+  } else {
+    e = launch(kv4_attn_tc_kernel<D, kRows, kSel, kScores>, kTcThreads,
+               TcLayout<D, kRows>::kBytes);
+  }
+  if (e == cudaSuccess && p.spans) {
+    // Launched while the attention kernel still runs (it waits inside).
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.ctas) * kRows);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, kRows, kSel, kScores>, p);
   }
   if (e == cudaSuccess && kScores) {
     const int64_t grid = static_cast<int64_t>(p.groups) * ((p.cols + 255) / 256);
-    const size_t sm = static_cast<size_t>(p.Hkv) * p.row_tiles * 8 * NT * sizeof(float);
-    kv4_weight_kernel<NT, kSel><<<static_cast<unsigned>(grid), 256, sm, s>>>(p);
+    const size_t sm = static_cast<size_t>(p.Hkv) * p.row_tiles * kRows * sizeof(float);
+    kv4_weight_kernel<kRows / 8, kSel><<<static_cast<unsigned>(grid), 256, sm, s>>>(p);
     e = cudaGetLastError();
     if (e == cudaSuccess && kSel && p.key_weights && p.next_n > 1) {
       kv4_weight_scatter_kernel<<<static_cast<unsigned>(p.groups / p.next_n), 1024, 0, s>>>(p);
@@ -998,10 +1842,21 @@ cudaError_t launch_one(const Kv4AttnParams& p, cudaStream_t s) {
   return e;
 }
 
-template <int D, int NT>
-cudaError_t launch_nt(const Kv4AttnParams& p, bool scores, cudaStream_t s) {
-  if (p.sel) return scores ? launch_one<D, NT, true, true>(p, s) : launch_one<D, NT, true, false>(p, s);
-  return scores ? launch_one<D, NT, false, true>(p, s) : launch_one<D, NT, false, false>(p, s);
+template <int D, int kRows>
+cudaError_t launch_kind(const Kv4AttnParams& p, bool scores, cudaStream_t s) {
+  if (p.sel)
+    return scores ? launch_rows<D, kRows, true, true>(p, s) : launch_rows<D, kRows, true, false>(p, s);
+  return scores ? launch_rows<D, kRows, false, true>(p, s) : launch_rows<D, kRows, false, false>(p, s);
+}
+
+template <int D>
+cudaError_t launch_d(const Kv4AttnParams& p, int rows, bool scores, cudaStream_t s) {
+  switch (rows) {
+    case 8: return launch_kind<D, 8>(p, scores, s);
+    case 16: return launch_kind<D, 16>(p, scores, s);
+    case 32: return launch_kind<D, 32>(p, scores, s);
+    default: return launch_kind<D, 64>(p, scores, s);
+  }
 }
 
 int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
@@ -1014,40 +1869,38 @@ Kv4AttnPlan kv4_attn_plan(int B, int next_n, int Hq, int Hkv, int D, int64_t col
   pl.heads = Hq / Hkv;
   pl.groups = selected ? static_cast<int64_t>(B) * next_n : B;
   const int rows = selected ? pl.heads : pl.heads * next_n;
-  pl.nt = rows <= 8 ? 1 : 2;
-  pl.row_tiles = (rows + 8 * pl.nt - 1) / (8 * pl.nt);
-  // Chunks: enough CTAs for every SM's three places, at least one tile a
-  // warp, and no more than 64 tiles so that requests of unequal length spread.
-  const int64_t tiles = (cols + kTile - 1) / kTile;
+  pl.rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows <= 32 ? 32 : 64));
+  pl.row_tiles = (rows + pl.rows - 1) / pl.rows;
+  pl.tile = uses_tc(pl.rows) ? kTcTile : kTile;
+  // As many CTAs as the device holds, or as there can be units of work.
+  const int64_t unit = uses_tc(pl.rows) ? kTcTile : kTile * kWarps;
+  const int64_t units = cols > 0 ? (cols + unit - 1) / unit : 1;
   const int64_t lanes = pl.groups * Hkv * pl.row_tiles;
-  const int64_t places =
-      static_cast<int64_t>(device_sm_count() > 0 ? device_sm_count() : 152) * kCtasPerSm;
-  int64_t per = (tiles * lanes + places - 1) / (places > 0 ? places : 1);
-  per = per < kWarps ? kWarps : (per > 64 ? 64 : per);
-  per = (per + kWarps - 1) / kWarps * kWarps;
-  pl.chunk = static_cast<int>(per) * kTile;
-  pl.nsplit = static_cast<int>((cols + pl.chunk - 1) / pl.chunk);
-  if (pl.nsplit < 1) pl.nsplit = 1;
-  const int64_t parts = lanes * pl.nsplit * 8 * pl.nt;
+  const int64_t places = static_cast<int64_t>(device_sm_count() > 0 ? device_sm_count() : 152) *
+                         (pl.rows <= 16 ? 3 : 2);
+  pl.ctas = static_cast<int>(units * lanes < places ? units * lanes : places);
+  if (pl.ctas > kMaxCtas) pl.ctas = kMaxCtas;
+  pl.split = units > 1;
   int64_t off = 0;
   auto take = [&](int64_t bytes) {
     const int64_t at = off;
     off += up256(bytes);
     return at;
   };
-  pl.part_o = take(pl.nsplit > 1 ? parts * D * 4 : 0);
-  pl.part_ml = take(pl.nsplit > 1 ? parts * 8 : 0);
-  pl.scores = take(weights ? lanes * cols * 8 * pl.nt * 4 : 0);
-  pl.lse2 = take(weights ? lanes * 8 * pl.nt * 4 : 0);
+  const int64_t parts = pl.split ? static_cast<int64_t>(pl.ctas) * 2 * pl.rows : 0;
+  pl.part_o = take(parts * D * 4);
+  pl.part_ml = take(parts * 8);
+  pl.spans = take(pl.split ? static_cast<int64_t>(pl.ctas) * 16 : 0);
+  pl.scores = take(weights ? lanes * cols * pl.rows * 4 : 0);
+  pl.lse2 = take(weights ? lanes * pl.rows * 4 : 0);
   pl.sel_weights = take(weights && selected && next_n > 1 ? pl.groups * cols * 4 : 0);
   pl.bytes = off;
   return pl;
 }
 
-cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int D, int nt, bool scores,
+cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int D, int rows, bool scores,
                                  cudaStream_t s) {
-  if (D == 128) return nt == 1 ? launch_nt<128, 1>(p, scores, s) : launch_nt<128, 2>(p, scores, s);
-  return nt == 1 ? launch_nt<64, 1>(p, scores, s) : launch_nt<64, 2>(p, scores, s);
+  return D == 128 ? launch_d<128>(p, rows, scores, s) : launch_d<64>(p, rows, scores, s);
 }
 
 }  // namespace dsa

@@ -78,16 +78,15 @@ dsa_status_t run_attention(const AttnArgs& a, bool selected, dsa_stream_t stream
   const Kv4AttnPlan pl =
       kv4_attn_plan(a.B, a.next_n, a.Hq, a.Hkv, a.D, cols, selected, weights);
   const int64_t lanes = static_cast<int64_t>(a.Hkv) * pl.row_tiles;
-  if (pl.groups * lanes * pl.nsplit >= (int64_t(1) << 31) ||
-      pl.groups * ((cols + 255) / 256) >= (int64_t(1) << 31) ||
-      (weights && lanes * 8 * pl.nt * 4 > 48 * 1024))
+  if (pl.groups * lanes >= (int64_t(1) << 31) || pl.groups * ((cols + 255) / 256) >= (int64_t(1) << 31) ||
+      (weights && lanes * pl.rows * 4 > 48 * 1024))
     return DSA_ERR_UNSUPPORTED;
   if (pl.bytes > 0 && (!a.workspace || !aligned(a.workspace, 256) ||
                        a.ws_bytes < static_cast<size_t>(pl.bytes)))
     return DSA_ERR_INVALID_ARG;
   Kv4AttnParams p = {};
   if (!selected && !encode_rows_map(&p.tmap, a.cache, a.D, a.block_size,
-                                    a.block_size < kKv4Tile ? a.block_size : kKv4Tile,
+                                    a.block_size < pl.tile ? a.block_size : pl.tile,
                                     static_cast<int64_t>(a.num_blocks) * a.Hkv))
     return DSA_ERR_CUDA;
   p.q = static_cast<const uint16_t*>(a.q);
@@ -107,14 +106,14 @@ dsa_status_t run_attention(const AttnArgs& a, bool selected, dsa_stream_t stream
   p.num_blocks = a.num_blocks;
   p.log_bs = log2_of(a.block_size);
   p.scale_log2e = static_cast<float>(static_cast<double>(a.softmax_scale) * 1.4426950408889634);
-  p.chunk = pl.chunk;
-  p.nsplit = pl.nsplit;
+  p.ctas = pl.ctas;
   p.cols = static_cast<int>(cols);
   p.out = static_cast<uint16_t*>(a.out);
   p.lse = a.lse;
   char* ws = static_cast<char*>(a.workspace);
   p.part_o = reinterpret_cast<float*>(ws + pl.part_o);
   p.part_ml = reinterpret_cast<float*>(ws + pl.part_ml);
+  p.spans = pl.split ? reinterpret_cast<int4*>(ws + pl.spans) : nullptr;
   p.scores = reinterpret_cast<float*>(ws + pl.scores);
   p.lse2 = reinterpret_cast<float*>(ws + pl.lse2);
   // Several tokens a request: the scatter reads the rows' weights, so they
@@ -127,7 +126,7 @@ dsa_status_t run_attention(const AttnArgs& a, bool selected, dsa_stream_t stream
   p.ldw = a.ldw;
   p.err = error_word();
   if (!p.err) return DSA_ERR_CUDA;
-  return from_cuda(launch_kv4_attention(p, a.D, pl.nt, weights, as_stream(stream)));
+  return from_cuda(launch_kv4_attention(p, a.D, pl.rows, weights, as_stream(stream)));
 }
 
 // Workspace of the eviction: row ranges, the middle's selection, and the
