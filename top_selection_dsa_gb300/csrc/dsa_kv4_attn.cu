@@ -157,7 +157,9 @@ struct Layout {
   // Then, with two row tiles, the query fragments and their factors.
   static constexpr int kQueries = kWarps * (kWarpTiles + kWarpRest);
   static constexpr int kFactorF = kQueries + (NT > 1 ? NT * G * 32 * 16 : 0);
-  static constexpr int kBytes = kFactorF + (NT > 1 ? NT * 8 * 4 : 0);
+  static constexpr int kLimits = kFactorF + (NT > 1 ? NT * 8 * 4 : 0);
+  static constexpr int kWalk = kLimits + NT * 8 * 4;
+  static constexpr int kBytes = kWalk + 128;
   // Byte address of chunk c of key `row` of a tile: the 128- (64-) byte
   // swizzle of a tensor map whose rows are the records.
   __device__ static __forceinline__ uint32_t chunk_at(int row, int c) {
@@ -220,11 +222,14 @@ __device__ __forceinline__ Group group_of(const Kv4AttnParams& p, int g) {
 // the requests' lengths.  A run of units of one group, head and row tile is a
 // span; a CTA's spans are whole, but for its first and its last, which may be
 // shared with its neighbours.
+// The walk lives in shared memory (its state would cost every thread a dozen
+// registers): warp 0 begins it, thread 0 takes the next span.
 struct Span {
-  int g, ht;       // group; head and row tile
+  int g, ht;       // group (-1: no more); head and row tile
   int u0, u1;      // units of it
   int units;       // that there are
-  bool first;      // of the CTA
+  int first;       // of the CTA
+  Group gr;
   __device__ bool whole() const { return u0 == 0 && u1 == units; }
 };
 
@@ -235,9 +240,11 @@ struct Walk {
   int64_t base;    // units before group g
   int g;
   bool first;
+  Span span;       // the one in work
 
   __device__ static int units_of(int cols) { return cols > 0 ? (cols + kUnit - 1) / kUnit : 1; }
 
+  __device__ Walk() {}
   // Executed by whole warps.
   __device__ __forceinline__ explicit Walk(const Kv4AttnParams& p) {
     const int per = p.Hkv * p.row_tiles;
@@ -251,9 +258,9 @@ struct Walk {
       g = static_cast<int>(t / upg);
       base = g * upg;
       if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b < p.groups / p.next_n; b += blockDim.x) context_len(p, b, true);
+        for (int b = lane; b < p.groups / p.next_n; b += 32) context_len(p, b, true);
     } else {
-      const bool report = blockIdx.x == 0 && threadIdx.x < 32;
+      const bool report = blockIdx.x == 0;
       int64_t mine = 0;
       for (int b = lane; b < p.groups; b += 32)
         mine += units_of(context_len(p, b, report));
@@ -289,11 +296,19 @@ struct Walk {
     t = i < P ? total * i / P : total;
     t1 = i < P ? total * (i + 1) / P : total;
   }
-  __device__ __forceinline__ bool more() const { return t < t1; }
-  __device__ __forceinline__ Span next(const Kv4AttnParams& p, int cols) {
+  // Thread 0: the next span; the one it begins and does not end is noted for
+  // the join: .x group; .y head and row tile; .z the last CTA of the span; .w
+  // which of this CTA's two partial results it is (the others' are their
+  // first).
+  __device__ __forceinline__ void next(const Kv4AttnParams& p) {
+    if (t >= t1) {
+      span.g = -1;
+      return;
+    }
     Span s;
+    s.gr = group_of<kSel>(p, g);
     s.g = g;
-    s.units = units_of(cols);
+    s.units = units_of(s.gr.cols);
     const int64_t at = t - base;
     s.ht = static_cast<int>(at / s.units);
     s.u0 = static_cast<int>(at - static_cast<int64_t>(s.ht) * s.units);
@@ -302,11 +317,13 @@ struct Walk {
     s.first = first;
     first = false;
     t += s.u1 - s.u0;
+    if (s.u0 == 0 && s.u1 < s.units)
+      p.spans[blockIdx.x] = make_int4(s.g, s.ht, cta_of(t + s.units - s.u1 - 1), s.first ? 0 : 1);
     if (s.u1 == s.units && s.ht == p.Hkv * p.row_tiles - 1) {
       ++g;
       base = t;
     }
-    return s;
+    span = s;
   }
   // The CTA that takes unit x.
   __device__ __forceinline__ int cta_of(int64_t x) const {
@@ -314,16 +331,14 @@ struct Walk {
   }
 };
 
-// What a CTA leaves for the join: the span it begins and does not end.
-//   .x group, or -1; .y head and row tile; .z the last CTA of that span;
-//   .w which of this CTA's two partial results it is (the others' are their
-//   first)
-template <bool kSel, int kUnit>
-__device__ __forceinline__ void note_span(const Kv4AttnParams& p, const Walk<kSel, kUnit>& w,
-                                          const Span& s) {
-  if (threadIdx.x != 0 || s.u0 != 0 || s.u1 == s.units) return;
-  const int64_t last = w.t - s.u1 + s.units - 1;
-  p.spans[blockIdx.x] = make_int4(s.g, s.ht, w.cta_of(last), s.first ? 0 : 1);
+// Warp 0 of a CTA: begins the walk.
+template <class W>
+__device__ __forceinline__ void begin_walk(W* walk, const Kv4AttnParams& p) {
+  const W w(p);
+  if (threadIdx.x == 0) {
+    *walk = w;
+    if (p.spans) p.spans[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  }
 }
 
 __device__ __forceinline__ void launch_dependents() {
@@ -397,16 +412,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   }
   const int per_split = p.Hkv * p.row_tiles;
   const int nrows = kSel ? p.heads : p.heads * p.next_n;
-  Walk<kSel, kTile * kWarps> walk(p);
+  auto* const walk = reinterpret_cast<Walk<kSel, kTile * kWarps>*>(smem + Lay::kWalk);
+  if (warp == 0) begin_walk(walk, p);
   launch_dependents();
-  if (threadIdx.x == 0 && p.spans) p.spans[blockIdx.x] = make_int4(-1, 0, 0, 0);
   int s = 0;           // stage and phase of this warp's next tile
   uint32_t phase = 0;
   bool ok = true;
-  while (walk.more() && __syncthreads_and(ok)) {
-  const Group gr = group_of<kSel>(p, walk.g);
-  const Span span = walk.next(p, gr.cols);
-  note_span(p, walk, span);
+  for (;;) {
+  if (threadIdx.x == 0) walk->next(p);
+  if (!__syncthreads_and(ok)) break;  // and the last span's shared memory is free
+  const Span span = walk->span;
+  if (span.g < 0) break;
+  const Group& gr = span.gr;
   const int grp = span.g, ht = span.ht;
   const int head = ht / p.row_tiles;
   const int row0 = (ht % p.row_tiles) * kRows;
@@ -524,6 +541,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   const bool zero = p.scale_log2e == 0.f;
   const float sign = zero ? 0.f : (p.scale_log2e < 0.f ? -1.f : 1.f);
   const uint32_t q_at = smem_u32(smem) + Lay::kQueries + lane * 16;
+  int* const limit_s = reinterpret_cast<int*>(smem + Lay::kLimits);
+  if (threadIdx.x < kRows)
+    limit_s[threadIdx.x] =
+        kSel ? gr.cols
+             : gr.L - p.next_n +
+                   min((row0 + static_cast<int>(threadIdx.x)) / p.heads, p.next_n - 1) + 1;
   float* const f_s = reinterpret_cast<float*>(smem + Lay::kFactorF);
   if (NT == 1 || warp < NT) {
     const int nt = NT == 1 ? 0 : warp;
@@ -569,8 +592,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       f_s[nt * 8 + r] = fr;
     }
   }
+  __syncthreads();
   if constexpr (NT > 1) {
-    __syncthreads();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -578,11 +601,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   }
   // Columns that query row 2t + i of row tile nt sees (asked for in the tiles
   // where some row does not see all of them).
-  auto limit = [&](int nt, int i) {
-    if (kSel) return gr.cols;
-    const int j = (row0 + nt * 8 + 2 * t + i) / p.heads;
-    return gr.L - p.next_n + min(j, p.next_n - 1) + 1;
-  };
+  auto limit = [&](int nt, int i) { return limit_s[nt * 8 + 2 * t + i]; };
   const int all_see = kSel ? gr.cols : gr.L - p.next_n + 1;  // columns every row sees
 
   float o[NT][2 * G][4];
@@ -1031,7 +1050,8 @@ struct TcLayout {
   static constexpr int kRed = kPart + 4 * N * 4;   // [2][4]
   static constexpr int kBars = (kRed + 32 + 7) / 8 * 8;
   static constexpr int kSlot = kBars + 8 * (kTcStages + 2);
-  static constexpr int kBytes = kSlot + 16;
+  static constexpr int kWalk = kSlot + 16;
+  static constexpr int kBytes = kWalk + 128;
   static constexpr int kTmemK = 0;                 // columns: K', S, O
   static constexpr int kTmemS = D / 2;
   static constexpr int kTmemO = kTmemS + N;
@@ -1155,9 +1175,9 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<D, N>::kCtas)
   __syncwarp();
   if (warp == 0) tmem_alloc(const_cast<uint32_t*>(reinterpret_cast<volatile uint32_t*>(slot)),
                             Lay::kTmemCols);
-  Walk<kSel, kTcTile> walk(p);
+  auto* const walk = reinterpret_cast<Walk<kSel, kTcTile>*>(smem + Lay::kWalk);
+  if (warp == 0) begin_walk(walk, p);
   launch_dependents();
-  if (tid == 0 && p.spans) p.spans[blockIdx.x] = make_int4(-1, 0, 0, 0);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -1165,10 +1185,12 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<D, N>::kCtas)
   const uint32_t lanes = tmem + (static_cast<uint32_t>(warp) << 21);  // this warp's 32 lanes
   uint32_t done = 0;  // tiles so far: their stages and phases
   bool ok = true;
-  while (walk.more() && __syncthreads_and(ok)) {
-  const Group gr = group_of<kSel>(p, walk.g);
-  const Span span = walk.next(p, gr.cols);
-  note_span(p, walk, span);
+  for (;;) {
+  if (tid == 0) walk->next(p);
+  if (!__syncthreads_and(ok)) break;
+  const Span span = walk->span;
+  if (span.g < 0) break;
+  const Group& gr = span.gr;
   const int grp = span.g, ht = span.ht;
   const int head = ht / p.row_tiles;
   const int row0 = (ht % p.row_tiles) * N;
@@ -1810,8 +1832,8 @@ cudaError_t launch_rows(const Kv4AttnParams& p, cudaStream_t s) {
   if constexpr (!uses_tc(kRows)) {
     using Lay = Layout<D, kRows / 8>;
     constexpr int kJoin = kWarps * kRows * (D + 2) * 4;
-    e = launch(kv4_attn_kernel<D, kRows / 8, kSel, kScores>, kThreads,
-               Lay::kBytes > kJoin ? Lay::kBytes : kJoin);
+    static_assert(kJoin <= Lay::kWalk && sizeof(Walk<kSel, kTile * kWarps>) <= 128, "");
+    e = launch(kv4_attn_kernel<D, kRows / 8, kSel, kScores>, kThreads, Lay::kBytes);
   } else {
     e = launch(kv4_attn_tc_kernel<D, kRows, kSel, kScores>, kTcThreads,
                TcLayout<D, kRows>::kBytes);
