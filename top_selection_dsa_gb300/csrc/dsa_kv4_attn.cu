@@ -611,17 +611,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     for (int i = 0; i < 2 * G; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
-  // z: reference of a row's exponents (base 2).  It is raised to the running
-  // maximum only when a logit passes it by kSlack, that is when an accumulator
-  // passes thr, so most tiles need no maximum across lanes and no rescaling;
-  // weights are then at most 2^kSlack, which fp16 and fp32 hold as well as 1.
-  // thr = -inf: the row has seen no column.
+  // m: reference of a row's accumulators, weight = 2^(f (accumulator - m)).  It
+  // is raised to the running maximum only when a logit passes it by kSlack
+  // (base 2), that is when an accumulator passes thr, so most tiles need no
+  // maximum across lanes and no rescaling; weights are then at most 2^kSlack,
+  // which fp16 and fp32 hold as well as 1.  thr = -inf: the row has seen no
+  // column.
   constexpr float kSlack = 8.f;
-  float thr[NT][2], z[NT][2], l[NT][2];
+  float thr[NT][2], m[NT][2], l[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) thr[nt][i] = -INFINITY, z[nt][i] = l[nt][i] = 0.f;
+    for (int i = 0; i < 2; ++i) thr[nt][i] = -INFINITY, m[nt][i] = l[nt][i] = 0.f;
   float unit = 0.f, inv_unit = 0.f;  // o is in units of the largest value scale so far
 
   // Lane addresses that do not change from tile to tile: the key chunk of
@@ -879,9 +880,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
               v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
               v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
               if (v > thr[nt][i]) {
-                const float zn = v * f[nt][i];
-                const float a = thr[nt][i] == -INFINITY ? 0.f : ex2(z[nt][i] - zn);
-                z[nt][i] = zn;
+                const float a = thr[nt][i] == -INFINITY ? 0.f : ex2((m[nt][i] - v) * f[nt][i]);
+                m[nt][i] = v;
                 thr[nt][i] = v + kSlack / f[nt][i];
                 l[nt][i] *= a;
 #pragma unroll
@@ -894,10 +894,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt) {
-            const float p0 = ex2(fmaf(sacc[mt][nt][0], f[nt][0], -z[nt][0]));
-            const float p1 = ex2(fmaf(sacc[mt][nt][1], f[nt][1], -z[nt][1]));
-            const float p2 = ex2(fmaf(sacc[mt][nt][2], f[nt][0], -z[nt][0]));
-            const float p3 = ex2(fmaf(sacc[mt][nt][3], f[nt][1], -z[nt][1]));
+            const float p0 = ex2((sacc[mt][nt][0] - m[nt][0]) * f[nt][0]);
+            const float p1 = ex2((sacc[mt][nt][1] - m[nt][1]) * f[nt][1]);
+            const float p2 = ex2((sacc[mt][nt][2] - m[nt][0]) * f[nt][0]);
+            const float p3 = ex2((sacc[mt][nt][3] - m[nt][1]) * f[nt][1]);
             l[nt][0] += p0 + p2;
             l[nt][1] += p1 + p3;
             pf[mt][nt][0] = transpose8x8(pack_f16(p0, p1));
@@ -988,7 +988,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       x += __shfl_xor_sync(0xffffffffu, x, 16);
       const int row = nt * 8 + 2 * t + i;
       if (r == 0) {
-        sml[(warp * kRows + row) * 2] = thr[nt][i] == -INFINITY ? -INFINITY : z[nt][i];
+        sml[(warp * kRows + row) * 2] = thr[nt][i] == -INFINITY ? -INFINITY : m[nt][i] * f[nt][i];
         sml[(warp * kRows + row) * 2 + 1] = x;
       }
       float* dst = so + (warp * kRows + row) * D;
@@ -1025,9 +1025,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 }
 
 constexpr int kTcTile = 128;    // columns of a tile: one TMEM lane each
-constexpr int kTcThreads = 128;
+constexpr int kTcThreads = 256; // warps 0-3: keys; warps 4-7: values; both: softmax
 constexpr int kTcStages = 2;
-constexpr float kUnseen = -1e30f;  // exponent reference of a row that has seen no column
+constexpr int kTcCtas = 2;      // an SM holds
+constexpr float kUnseen = -3e38f;  // reference of a row that has seen no column
 
 // Shared memory of a CTA (1024-byte aligned).
 template <int D, int N>
@@ -1041,13 +1042,14 @@ struct TcLayout {
   static constexpr int kQ = kValues + kValueBytes;                 // fp16 [row][D]
   static constexpr int kP = kQ + N * D * 2;                        // fp16 [key][row]
   static constexpr int kScales = kP + kTcTile * N * 2;
-  static constexpr int kFz = kScales + kTcStages * kTcTile * kSc;  // float2 [row]: F, z
+  // float2 [row]: F and m, weight = 2^(F (accumulator - m))
+  static constexpr int kFz = kScales + kTcStages * kTcTile * kSc;
   static constexpr int kRowF = kFz + N * 8;
   static constexpr int kLimit = kRowF + N * 4;
   static constexpr int kAlpha = kLimit + N * 4;
   static constexpr int kNan = kAlpha + N * 4;
   static constexpr int kPart = kNan + N * 4;       // [4][row] of a reduction over warps
-  static constexpr int kRed = kPart + 4 * N * 4;   // [2][4]
+  static constexpr int kRed = kPart + 4 * N * 4;   // [4]: maxima of the warps of one kind, twice
   static constexpr int kBars = (kRed + 32 + 7) / 8 * 8;
   static constexpr int kSlot = kBars + 8 * (kTcStages + 2);
   static constexpr int kWalk = kSlot + 16;
@@ -1056,19 +1058,12 @@ struct TcLayout {
   static constexpr int kTmemS = D / 2;
   static constexpr int kTmemO = kTmemS + N;
   static constexpr int kTmemCols = kTmemO + N <= 128 ? 128 : 256;
-  static constexpr int kCtas = N == 16 ? 3 : 2;    // an SM holds
 };
 
-__device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_store8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
-      "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
 }
 __device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -1081,24 +1076,6 @@ __device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&r)
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-template <int N>
-__device__ __forceinline__ void tmem_load_row(uint32_t taddr, float (&v)[N]) {
-  if constexpr (N == 16) tmem_load16(taddr, v);
-  else if constexpr (N == 32) tmem_load32(taddr, v);
-  else tmem_load64(taddr, v);
-}
-
-template <int N>
-__device__ __forceinline__ void tmem_store_row(uint32_t taddr, const float (&v)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; i += 16) {
-    uint32_t r[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(v[i + j]);
-    tmem_store16(taddr + i, r);
-  }
 }
 
 // D (+)= A B^T with A [128 x 16] fp16 in TMEM, B from shared memory.
@@ -1139,15 +1116,33 @@ __device__ __forceinline__ float unorder_f32(uint32_t u) {
   return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
 }
 
+// Barrier of the four warps of one kind, with an OR of their votes.
+__device__ __forceinline__ bool kind_barrier_or(int id, bool vote) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(static_cast<uint32_t>(vote))
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void kind_barrier(int id) {
+  asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory");
+}
+
 template <int D, int N, bool kSel, bool kScores>
-__global__ void __launch_bounds__(kTcThreads, TcLayout<D, N>::kCtas)
+__global__ void __launch_bounds__(kTcThreads, kTcCtas)
     kv4_attn_tc_kernel(const __grid_constant__ Kv4AttnParams p) {
   using Lay = TcLayout<D, N>;
   constexpr int G = Lay::G;
   constexpr int kChunks = D / 16;
+  constexpr int kHalf = N / 2;  // rows of a warp's share of the softmax
   constexpr float kSlack = 8.f;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool is_v = warp >= 4;   // value warps
+  const int key = tid & 127;     // of a tile: this thread's, and its TMEM lane
 
   const int per_split = p.Hkv * p.row_tiles;
   const int nrows = kSel ? p.heads : p.heads * p.next_n;
@@ -1172,17 +1167,15 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<D, N>::kCtas)
     *abort_flag = 0;
     fence_barrier_init();
   }
-  __syncwarp();
-  if (warp == 0) tmem_alloc(const_cast<uint32_t*>(reinterpret_cast<volatile uint32_t*>(slot)),
-                            Lay::kTmemCols);
   auto* const walk = reinterpret_cast<Walk<kSel, kTcTile>*>(smem + Lay::kWalk);
   if (warp == 0) begin_walk(walk, p);
+  if (warp == 1) tmem_alloc(const_cast<uint32_t*>(slot), Lay::kTmemCols);
   launch_dependents();
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *slot;
-  const uint32_t lanes = tmem + (static_cast<uint32_t>(warp) << 21);  // this warp's 32 lanes
+  const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);  // this warp's 32 lanes
   uint32_t done = 0;  // tiles so far: their stages and phases
   bool ok = true;
   for (;;) {
@@ -1209,11 +1202,13 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<D, N>::kCtas)
     return static_cast<uint32_t>(block) * p.Hkv + head;
   };
   // Dense: lane i of warp 0 reads the page of the tile's i-th run of `rows`
-  // tokens.  Selected: thread i has column i, read a tile before its page.
+  // tokens.  Selected: thread i of either kind has column i, read a tile
+  // before its page; the key warps copy the keys' half of the record and its
+  // scales, the value warps the values' half.
   const int rows = min(1 << p.log_bs, kTcTile);
   int pos = -1, next_pos = -1, block = 0;
   auto read_column = [&](int tile) {
-    const int col = c0 + tile * kTcTile + tid;
+    const int col = c0 + tile * kTcTile + key;
     next_pos = col < c1 ? __ldg(p.sel + static_cast<int64_t>(grp) * p.sel_k + col) : -1;
   };
   auto locate = [&](int tile) {
@@ -1232,7 +1227,8 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<D, N>::kCtas)
     }
   };
   // Starts the copies of the located tile into stage s; returns whether this
-  // thread's column (selected) is there.  Warp w copies columns 32 w .. + 31.
+  // thread's column (selected) is there.  Warp w copies columns 32 (w % 4) ..,
+  // what its own threads read.
   auto fetch = [&](int s, int tile) {
     bool here = false;
     if constexpr (kSel) {
@@ -1240,20 +1236,21 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<D, N>::kCtas)
       const uint32_t cols = __ballot_sync(0xffffffffu, here);
       const uint32_t rec = here ? (page_of(block) << p.log_bs) + (pos & bs_mask) : 0u;
       const uint32_t base = sb + Lay::kTiles + s * Lay::kTileBytes;
-      constexpr int kPer = 32 / kChunks;
-      const int c = lane % kChunks;
+      constexpr int kPer = 64 / kChunks;  // records per instruction, half of each
+      const int c = lane % (kChunks / 2) + (is_v ? kChunks / 2 : 0);
       if (cols) {
 #pragma unroll
         for (int i = 0; i < 32 / kPer; ++i) {
-          const int row = i * kPer + lane / kChunks;
+          const int row = i * kPer + lane / (kChunks / 2);
           const uint32_t rc = __shfl_sync(0xffffffffu, rec, row);
-          cp_async16(base + Layout<D, 1>::chunk_at(warp * 32 + row, c),
+          cp_async16(base + Layout<D, 1>::chunk_at((warp & 3) * 32 + row, c),
                      p.cache + static_cast<int64_t>(rc) * D + c * 16,
                      (cols >> row) & 1 ? 16u : 0u);
         }
-        cp_async_small<Lay::kSc>(sb + Lay::kScales + (s * kTcTile + tid) * Lay::kSc,
-                                 p.scales + static_cast<int64_t>(rec) * Lay::kSc,
-                                 here ? Lay::kSc : 0);
+        if (!is_v)
+          cp_async_small<Lay::kSc>(sb + Lay::kScales + (s * kTcTile + key) * Lay::kSc,
+                                   p.scales + static_cast<int64_t>(rec) * Lay::kSc,
+                                   here ? Lay::kSc : 0);
       }
       cp_async_commit();
     } else if (warp == 0 && tile < tiles) {
@@ -1288,10 +1285,8 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<D, N>::kCtas)
   {
     constexpr int kPer = D / 16;
     const int sub = tid % kPer;
-#pragma unroll
-    for (int it = 0; it < (N * kPer + kTcThreads - 1) / kTcThreads; ++it) {
-      const int n = it * (kTcThreads / kPer) + tid / kPer;
-      if (n >= N) break;  // whole warps
+#pragma unroll 1
+    for (int n = tid / kPer; n < N; n += kTcThreads / kPer) {  // whole warps
       uint4 raw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
       if (row0 + n < nrows) {
         const uint4* src = reinterpret_cast<const uint4*>(
@@ -1337,12 +1332,14 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<D, N>::kCtas)
   __syncthreads();
   const int all_see = kSel ? gr.cols : gr.L - p.next_n + 1;
 
-  float l[N];  // this key lane's share of every row's sum
+  // This thread's rows of the softmax: n0 .. n0 + kHalf - 1, of its key lane.
+  const int n0 = is_v ? kHalf : 0;
+  float l[kHalf];  // the key lane's share of their sums
 #pragma unroll
-  for (int n = 0; n < N; ++n) l[n] = 0.f;
-  // References of the key and value scales (E8M0 bits as fp32): raised to the
-  // largest scale so far when one passes them by 2^kSlack.
-  float k_ref = 0.f, v_ref = 0.f, k_inv = 0.f, v_inv = 0.f;
+  for (int n = 0; n < kHalf; ++n) l[n] = 0.f;
+  // Reference of this kind's scales (E8M0 bits as fp32): raised to the largest
+  // so far when one passes it by 2^kSlack.
+  float ref = -1.f, ref_inv = 0.f;
 
   constexpr uint32_t kIdescS = mma_idesc(0, 128, N);
   constexpr uint32_t kIdescO = mma_idesc(0, 128, N) | (1u << 15) | (1u << 16);
@@ -1350,11 +1347,12 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<D, N>::kCtas)
   for (int tile = 0; tile < tiles; ++tile, ++done) {
     const int s = done % kTcStages;
     locate(tile + kTcStages);
-    const int col = c0 + tile * kTcTile + tid;
+    const int col = c0 + tile * kTcTile + key;
     bool valid, fail = false;  // fail: a wait gave up (votes carry it to every thread)
     if constexpr (kSel) {
       cp_async_wait<kTcStages - 1>();
-      __syncwarp();
+      // The value warps read scales that the key warps copied.
+      __syncthreads();
       valid = here[0];
     } else {
       if (!mbar_wait_bounded(&full[s], (done / kTcStages) & 1, abort_flag)) fail = true;
@@ -1362,247 +1360,244 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<D, N>::kCtas)
     }
     const uint32_t base = sb + Lay::kTiles + s * Lay::kTileBytes;
     // ---------------------------------------------------------------- scales
-    uint32_t kw, vw;
+    uint32_t sw;  // of the key, or of the value
     {
-      const uint32_t at = sb + Lay::kScales + (s * kTcTile + tid) * Lay::kSc;
+      const uint32_t at = sb + Lay::kScales + (s * kTcTile + key) * Lay::kSc;
       if constexpr (D == 128) {
-        const uint2 u = lds64(at);
-        kw = u.x, vw = u.y;
+        sw = lds32(at + (is_v ? 4 : 0));
       } else {
         const uint32_t u = lds32(at);
-        kw = u & 0xFFFFu, vw = u >> 16;
+        sw = is_v ? u >> 16 : u & 0xFFFFu;
       }
-      if (!valid) kw = vw = 0u;
+      if (!valid) sw = 0u;
     }
-    uint32_t kf[G], vf[G];
-    auto unpack_scales = [&](uint32_t w, uint32_t (&f)[G]) {
-      f[0] = e8m0_bits<0>(w), f[1] = e8m0_bits<1>(w);
-      if constexpr (D == 128) f[2] = e8m0_bits<2>(w), f[3] = e8m0_bits<3>(w);
-    };
-    unpack_scales(kw, kf);
-    unpack_scales(vw, vf);
+    uint32_t sf[G];
+    sf[0] = e8m0_bits<0>(sw), sf[1] = e8m0_bits<1>(sw);
+    if constexpr (D == 128) sf[2] = e8m0_bits<2>(sw), sf[3] = e8m0_bits<3>(sw);
     bool k_nan = false;
-    if (has_ff(kw) | has_ff(vw)) {
+    if (has_ff(sw)) {
       // NaN scales (rare): a key's makes its logits NaN, a value's makes its
       // 32 channels of every row that sees the column NaN at the end.
-      k_nan = has_ff(kw) != 0;
+      k_nan = !is_v;
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        if (kf[g] == 0x7F800000u) kf[g] = 0u;
-        if (vf[g] == 0x7F800000u) {
-          vf[g] = 0u;
-          for (int n = 0; n < N; ++n)
-            if (col < limit[n]) atomicOr(&nan_rows[n], 1u << g);
+      for (int g = 0; g < G; ++g)
+        if (sf[g] == 0x7F800000u) {
+          sf[g] = 0u;
+          if (is_v)
+            for (int n = 0; n < N; ++n)
+              if (col < limit[n]) atomicOr(&nan_rows[n], 1u << g);
         }
-      }
     }
-    uint32_t k_top = kf[0], v_top = vf[0];
+    uint32_t top = sf[0];
 #pragma unroll
-    for (int g = 1; g < G; ++g) k_top = max(k_top, kf[g]), v_top = max(v_top, vf[g]);
-    const bool passes = __uint_as_float(k_top) > k_ref * 256.f ||
-                        __uint_as_float(v_top) > v_ref * 256.f;
-    // ------------------------------------------------------ K' = K 2^-ref to TMEM
-    auto put_keys = [&]() {
-      uint32_t fac[G];
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const float x = __uint_as_float(kf[g]) * k_inv;
-        fac[g] = pack_f16(x, x);
-      }
-      if (k_nan) {
-#pragma unroll
-        for (int g = 0; g < G; ++g) fac[g] = 0x7E007E00u;
-      }
-      uint32_t r[32];
-#pragma unroll
-      for (int c = 0; c < kChunks / 2; ++c) {
-        const uint4 u = lds128(base + Layout<D, 1>::chunk_at(tid, c));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int g = i % G, at = (c % 2) * 16 + i * 4;
-          r[at] = mul_f16x2(e2m1x2_to_f16x2<0>(w[i]), fac[g]);
-          r[at + 1] = mul_f16x2(e2m1x2_to_f16x2<1>(w[i]), fac[g]);
-          r[at + 2] = mul_f16x2(e2m1x2_to_f16x2<2>(w[i]), fac[g]);
-          r[at + 3] = mul_f16x2(e2m1x2_to_f16x2<3>(w[i]), fac[g]);
-        }
-        if (c % 2 == 1) tmem_store32(lanes + Lay::kTmemK + (c / 2) * 32, r);
-      }
-      tmem_wait_st();
+    for (int g = 1; g < G; ++g) top = max(top, sf[g]);
+    const bool passes = valid && __uint_as_float(top) > ref * 256.f;
+    // The largest scale of this kind in the tile (rare: a new reference).
+    auto new_ref = [&]() {
+      const uint32_t t = __reduce_max_sync(0xffffffffu, top);
+      if (lane == 0) red[warp] = t;
+      kind_barrier(is_v ? 2 : 1);
+      const uint32_t* r = red + (is_v ? 4 : 0);
+      return fmaxf(fmaxf(ref, 1.17549435e-38f),
+                   __uint_as_float(max(max(r[0], r[1]), max(r[2], r[3]))));
     };
-    put_keys();
-    tc_fence_before_sync();
-    if (fail) *abort_flag = 1;
-    if (__syncthreads_or(passes || fail)) {
-      // Rare: larger scales than the references allow for.  New references,
-      // the keys once more, and what is accumulated in the new unit.
-      tc_fence_after_sync();
-      const uint32_t kt = __reduce_max_sync(0xffffffffu, k_top);
-      const uint32_t vt = __reduce_max_sync(0xffffffffu, v_top);
-      if (lane == 0) red[warp] = kt, red[4 + warp] = vt;
-      if (tile > 0 && !mbar_wait_bounded(o_done, (done - 1) & 1, abort_flag)) *abort_flag = 1;
-      __syncthreads();
-      if (*abort_flag) {
-        ok = false;
-        break;
-      }
-      const float kn = fmaxf(k_ref, __uint_as_float(max(max(red[0], red[1]), max(red[2], red[3]))));
-      const float vn = fmaxf(v_ref, __uint_as_float(max(max(red[4], red[5]), max(red[6], red[7]))));
-      if (kn != k_ref) {
-        k_ref = kn;
-        k_inv = 1.f / kn;
-        if (tid < N) fz[tid].x = row_f[tid] * kn;
-      }
-      if (vn != v_ref) {
-        if (tile > 0) {
-          const float down = v_ref / vn;
-          float o[N];
-          tc_fence_after_sync();
-          tmem_load_row<N>(lanes + Lay::kTmemO, o);
-#pragma unroll
-          for (int n = 0; n < N; ++n) o[n] *= down;
-          tmem_store_row<N>(lanes + Lay::kTmemO, o);
-          tmem_wait_st();
-        }
-        v_ref = vn;
-        v_inv = 1.f / vn;
-      }
-      put_keys();
-      tc_fence_before_sync();
-      __syncthreads();
-    }
-    // ------------------------------------------------------------- S = K' q^T
-    if (tid == 0) {
-      tc_fence_after_sync();
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        mma_ts_f16(tmem + Lay::kTmemS, tmem + Lay::kTmemK + k * 8,
-                   k_major_desc(sb + Lay::kQ + (k / 4) * (N * 128) + (k % 4) * 32, 1024, 2),
-                   kIdescS, k > 0);
-      mma_commit(s_done);
-    }
-    // ------------------------------------ V' = V 2^-ref, when the last tile's is used
-    if (tile > 0 && !mbar_wait_bounded(o_done, (done - 1) & 1, abort_flag)) fail = true;
-    {
-      uint32_t fac[G];
+    uint32_t fac[G];
+    auto factors = [&]() {
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const float x = __uint_as_float(vf[g]) * v_inv;
-        fac[g] = pack_f16(x, x);
+        const float x = __uint_as_float(sf[g]) * ref_inv;
+        fac[g] = k_nan ? 0x7E007E00u : pack_f16(x, x);
       }
+    };
+    // V' = V 2^-ref, one channel-major row per key.
+    auto put_values = [&]() {
+      factors();
 #pragma unroll
       for (int c = 0; c < kChunks / 2; ++c) {
-        const uint4 u = lds128(base + Layout<D, 1>::chunk_at(tid, kChunks / 2 + c));
+        const uint4 u = lds128(base + Layout<D, 1>::chunk_at(key, kChunks / 2 + c));
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int g = (2 * i) % G;  // blocks of the word's two units
           const int m8 = c * 4 + i;   // its eight channels' place
-          sts128(sb + Lay::kValues + (m8 / 8) * (kTcTile * 128) + tid * 128 +
-                     (((m8 % 8) ^ (tid & 7)) << 4),
+          sts128(sb + Lay::kValues + (m8 / 8) * (kTcTile * 128) + key * 128 +
+                     (((m8 % 8) ^ (key & 7)) << 4),
                  mul_f16x2(e2m1x2_to_f16x2<0>(w[i]), fac[g]),
                  mul_f16x2(e2m1x2_to_f16x2<1>(w[i]), fac[g]),
                  mul_f16x2(e2m1x2_to_f16x2<2>(w[i]), fac[g + 1]),
                  mul_f16x2(e2m1x2_to_f16x2<3>(w[i]), fac[g + 1]));
         }
       }
+    };
+    bool again = false;  // this kind's reference is new: what it went into is done once more
+    if (!is_v) {
+      // ------------------------------------------- K' = K 2^-ref to TMEM, S = K' q^T
+      if (kind_barrier_or(1, passes)) {
+        const float r = new_ref();
+        if (tid < N) {
+          const float m = fz[tid].y;  // an accumulator value: in the new unit
+          fz[tid] = make_float2(row_f[tid] * r, m == kUnseen ? m : m * (ref / r));
+        }
+        ref = r;
+        ref_inv = 1.f / r;
+        again = true;
+      }
+      factors();
+#pragma unroll
+      for (int c = 0; c < kChunks / 2; ++c) {
+        const uint4 u = lds128(base + Layout<D, 1>::chunk_at(key, c));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        uint32_t r[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int g = i % G;
+          r[4 * i] = mul_f16x2(e2m1x2_to_f16x2<0>(w[i]), fac[g]);
+          r[4 * i + 1] = mul_f16x2(e2m1x2_to_f16x2<1>(w[i]), fac[g]);
+          r[4 * i + 2] = mul_f16x2(e2m1x2_to_f16x2<2>(w[i]), fac[g]);
+          r[4 * i + 3] = mul_f16x2(e2m1x2_to_f16x2<3>(w[i]), fac[g]);
+        }
+        tmem_store16(lanes + Lay::kTmemK + c * 16, r);
+      }
+      tmem_wait_st();
+      tc_fence_before_sync();
+      kind_barrier(1);
+      if (tid == 0) {
+        tc_fence_after_sync();
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma_ts_f16(tmem + Lay::kTmemS, tmem + Lay::kTmemK + k * 8,
+                     k_major_desc(sb + Lay::kQ + (k / 4) * (N * 128) + (k % 4) * 32, 1024, 2),
+                     kIdescS, k > 0);
+        mma_commit(s_done);
+      }
+      __syncwarp();
+      // P's buffer is free once the last tile's products are done.
+      if (tile > 0 && !mbar_wait_bounded(o_done, (done - 1) & 1, abort_flag)) fail = true;
+    } else {
+      if (tile > 0 && !mbar_wait_bounded(o_done, (done - 1) & 1, abort_flag)) fail = true;
+      again = passes;
+      put_values();
     }
-    // ---------------------------------------------------------------- softmax
     if (!mbar_wait_bounded(s_done, done & 1, abort_flag)) fail = true;
     tc_fence_after_sync();
-    float x[N];
-    tmem_load_row<N>(lanes + Lay::kTmemS, x);
+    // ---------------------------------------------------------------- softmax
     const bool clean = c0 + (tile + 1) * kTcTile <= min(c1, all_see) && (!kSel || valid);
-    if constexpr (kScores) {
-      if (col < c1) {
-        float* dst = p.scores +
-                     ((static_cast<int64_t>(grp) * per_split + ht) * p.cols + col) * N;
+    const bool dirty = __any_sync(0xffffffffu, !clean);
+    float pr[kHalf];
+    // Once, but for the rare cases below, which need one round more.
+    for (int round = 0;; ++round) {
+      float mx = -INFINITY;
 #pragma unroll
-        for (int n = 0; n < N; n += 4) {
-          float v[4];
+      for (int c = 0; c < kHalf; c += 8) {
+        float x[8];
+        tmem_load8(lanes + Lay::kTmemS + n0 + c, x);
+        if (dirty) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            v[j] = valid && (kSel || col < limit[n + j]) ? x[n + j] * fz[n + j].x : -INFINITY;
-          *reinterpret_cast<float4*>(dst + n) = make_float4(v[0], v[1], v[2], v[3]);
+          for (int j = 0; j < 8; ++j)
+            if (!valid || (!kSel && col >= limit[n0 + c + j])) x[j] = -INFINITY;
         }
-      }
-    }
-    float mx = -INFINITY;
-    auto weights = [&]() {
-      float pr[N];
 #pragma unroll
-      for (int n = 0; n < N; n += 2) {
-        const float4 c = *reinterpret_cast<const float4*>(&fz[n]);
-        float e0 = fmaf(x[n], c.x, -c.y), e1 = fmaf(x[n + 1], c.z, -c.w);
-        if (!clean) {
-          if (!valid || (!kSel && col >= limit[n])) e0 = -INFINITY;
-          if (!valid || (!kSel && col >= limit[n + 1])) e1 = -INFINITY;
+        for (int j = 0; j < 8; j += 2) {
+          const float4 f = *reinterpret_cast<const float4*>(&fz[n0 + c + j]);
+          float e0 = (x[j] - f.y) * f.x, e1 = (x[j + 1] - f.w) * f.z;
+          if (dirty) {  // no reference makes an absent column's weight other than zero
+            if (x[j] == -INFINITY) e0 = -INFINITY;
+            if (x[j + 1] == -INFINITY) e1 = -INFINITY;
+          }
+          mx = fmaxf(mx, fmaxf(e0, e1));
+          pr[c + j] = ex2(e0), pr[c + j + 1] = ex2(e1);
         }
-        mx = fmaxf(mx, fmaxf(e0, e1));
-        pr[n] = ex2(e0), pr[n + 1] = ex2(e1);
+        const int ch = (n0 + c) / 8;
+        const int fl = N == 16 ? (key >> 2) & 1 : (N == 32 ? (key >> 1) & 3 : key & 7);
+        sts128(sb + Lay::kP + key * (2 * N) + ((ch ^ fl) << 4), pack_f16(pr[c], pr[c + 1]),
+               pack_f16(pr[c + 2], pr[c + 3]), pack_f16(pr[c + 4], pr[c + 5]),
+               pack_f16(pr[c + 6], pr[c + 7]));
       }
-#pragma unroll
-      for (int c = 0; c < N / 8; ++c) {
-        const int f = N == 16 ? (tid >> 2) & 1 : (N == 32 ? (tid >> 1) & 3 : tid & 7);
-        sts128(sb + Lay::kP + tid * (2 * N) + ((c ^ f) << 4),
-               pack_f16(pr[8 * c], pr[8 * c + 1]), pack_f16(pr[8 * c + 2], pr[8 * c + 3]),
-               pack_f16(pr[8 * c + 4], pr[8 * c + 5]), pack_f16(pr[8 * c + 6], pr[8 * c + 7]));
-      }
-      return [&l, pr]() {
-#pragma unroll
-        for (int n = 0; n < N; ++n) l[n] += pr[n];
-      };
-    };
-    auto add = weights();
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    tc_fence_before_sync();
-    if (fail) *abort_flag = 1;
-    if (__syncthreads_or(mx > kSlack || fail)) {
-      // Rare: a logit far above its row's reference.  Rows' maxima over the
-      // tile, new references, and what is accumulated (sums here, O in TMEM).
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        float v = valid && (kSel || col < limit[n]) ? x[n] * fz[n].x : -INFINITY;
-        if (!(v == v)) v = -INFINITY;  // a NaN stays one without a reference
-        const uint32_t w = __reduce_max_sync(0xffffffffu, order_f32(v));
-        if (lane == 0) part[warp * N + n] = w;
-      }
-      __syncthreads();
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      tc_fence_before_sync();
+      if (fail) *abort_flag = 1;
+      if (!__syncthreads_or(mx > kSlack || again || fail) || round == 3) break;
+      // Rare.  A larger value scale than the reference allows for: a new
+      // reference, the values once more, O in the new unit.  A logit far above
+      // its row's reference: rows' maxima over the tile, new references, sums
+      // and O by what that takes off.
       if (*abort_flag) {
         ok = false;
         break;
       }
+      tc_fence_after_sync();
+      if (is_v) {
+        const float r = new_ref();
+        if (tid == 128) red[0] = __float_as_uint(r == ref ? 1.f : ref / r);
+        if (r != ref) {
+          ref = r;
+          ref_inv = 1.f / r;
+          put_values();
+        }
+      }
+      again = false;
+#pragma unroll 1
+      for (int c = 0; c < kHalf; c += 8) {
+        float x[8];
+        tmem_load8(lanes + Lay::kTmemS + n0 + c, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int n = n0 + c + j;
+          float v = valid && (kSel || col < limit[n]) ? x[j] : -INFINITY;
+          if (!(v == v)) v = -INFINITY;  // a NaN stays one without a reference
+          const uint32_t w = __reduce_max_sync(0xffffffffu, order_f32(v));
+          if (lane == 0) part[(warp & 3) * N + n] = w;
+        }
+      }
+      __syncthreads();
+      const float down = __uint_as_float(red[0]);
       if (tid < N) {
-        const float z = fz[tid].y;
-        const float top = unorder_f32(max(max(part[tid], part[N + tid]),
-                                          max(part[2 * N + tid], part[3 * N + tid])));
+        const float2 f = fz[tid];
+        const float m = unorder_f32(max(max(part[tid], part[N + tid]),
+                                        max(part[2 * N + tid], part[3 * N + tid])));
         float a = 1.f;
-        if (top > z + kSlack) {
-          a = z == kUnseen ? 0.f : ex2(z - top);
-          fz[tid].y = top;
+        if (m > f.y && (f.y == kUnseen || (m - f.y) * f.x > kSlack)) {
+          a = f.y == kUnseen ? 0.f : ex2((f.y - m) * f.x);
+          fz[tid].y = m;
         }
         alpha[tid] = a;
       }
       __syncthreads();
 #pragma unroll
-      for (int n = 0; n < N; ++n) l[n] *= alpha[n];
+      for (int n = 0; n < kHalf; ++n) l[n] *= alpha[n0 + n];
       if (tile > 0) {
-        float o[N];
-        tc_fence_after_sync();
-        tmem_load_row<N>(lanes + Lay::kTmemO, o);
+#pragma unroll 1
+        for (int c = 0; c < kHalf; c += 8) {
+          float o[8];
+          tmem_load8(lanes + Lay::kTmemO + n0 + c, o);
+          uint32_t r[8];
 #pragma unroll
-        for (int n = 0; n < N; ++n) o[n] *= alpha[n];
-        tmem_store_row<N>(lanes + Lay::kTmemO, o);
+          for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(o[j] * (alpha[n0 + c + j] * down));
+          tmem_store8(lanes + Lay::kTmemO + n0 + c, r);
+        }
         tmem_wait_st();
       }
-      auto again = weights();
-      again();
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      tc_fence_before_sync();
-      __syncthreads();
-    } else {
-      add();
     }
+    if (!ok) break;
+    if constexpr (kScores) {
+      float* dst = p.scores +
+                   ((static_cast<int64_t>(grp) * per_split + ht) * p.cols + col) * N + n0;
+#pragma unroll 1
+      for (int c = 0; c < kHalf; c += 8) {
+        float v[8];
+        tmem_load8(lanes + Lay::kTmemS + n0 + c, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[j] = valid && (kSel || col < limit[n0 + c + j]) ? v[j] * fz[n0 + c + j].x : -INFINITY;
+        if (col < c1) {
+          *reinterpret_cast<float4*>(dst + c) = make_float4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<float4*>(dst + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        }
+        __syncwarp();
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < kHalf; ++n) l[n] += pr[n];
     // --------------------------------------------------------------- O += V'^T P
     if (tid == 0) {
       tc_fence_after_sync();
@@ -1615,6 +1610,7 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<D, N>::kCtas)
                       tile > 0 || k > 0);
       mma_commit(o_done);
     }
+    __syncwarp();
     const bool h = fetch(s, tile + kTcStages);
 #pragma unroll
     for (int i = 0; i + 1 < kTcStages; ++i) here[i] = here[i + 1];
@@ -1638,22 +1634,29 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<D, N>::kCtas)
   // -------------------------------------------------------------- write out
   // O^T's lane m holds channel 32 g + 4 r + i, m = (r G + g) 4 + i.
   float* const so = reinterpret_cast<float*>(smem + Lay::kValues);  // [row][D]
+  if (tid == 128) alpha[0] = ref;                                  // the values' unit
+  __syncthreads();
   if (tiles > 0) {
-    float o[N];
-    tmem_load_row<N>(lanes + Lay::kTmemO, o);
-    tc_fence_before_sync();
-    if (tid < D) {
-      const int g = (tid / 4) % G, r = tid / (4 * G), d = 32 * g + 4 * r + tid % 4;
+    const float unit = alpha[0];
+    const int g = (key / 4) % G, r = key / (4 * G), d = 32 * g + 4 * r + key % 4;
+#pragma unroll 1
+    for (int c = 0; c < kHalf; c += 8) {
+      float o[8];
+      tmem_load8(lanes + Lay::kTmemO + n0 + c, o);
+      if (key < D) {
 #pragma unroll
-      for (int n = 0; n < N; ++n) so[n * D + d] = o[n] * v_ref;
+        for (int j = 0; j < 8; ++j) so[(n0 + c + j) * D + d] = o[j] * unit;
+      }
+      __syncwarp();
     }
+    tc_fence_before_sync();
     float* const lp = reinterpret_cast<float*>(part);
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
+    for (int n = 0; n < kHalf; ++n) {
       float v = l[n];
 #pragma unroll
       for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
-      if (lane == 0) lp[warp * N + n] = v;
+      if (lane == 0) lp[(warp & 3) * N + n0 + n] = v;
     }
   }
   __syncthreads();
@@ -1666,7 +1669,7 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<D, N>::kCtas)
     if (tiles > 0) {
       L = (lp[row] + lp[N + row]) + (lp[2 * N + row] + lp[3 * N + row]);
       a = *reinterpret_cast<const float4*>(so + row * D + d);
-      if (fz[row].y != kUnseen) M = fz[row].y;
+      if (fz[row].y != kUnseen) M = fz[row].y * fz[row].x;
       if ((nan_rows[row] >> (d / 32)) & 1)
         a.x = a.y = a.z = a.w = __uint_as_float(0x7FC00000u);
     }
@@ -1675,76 +1678,79 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<D, N>::kCtas)
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 1) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, Lay::kTmemCols);
   }
 }
 
-// Joins the partial results of the spans that CTAs share: one CTA for every
-// CTA of the attention kernel (which had to begin the span) and row.  The
-// references first, then the channels, dealt over the partial results.
-constexpr int kMaxCtas = 1024;  // of the attention kernel (their factors fit shared memory)
+// Joins the partial results of the spans that CTAs share: for every CTA of the
+// attention kernel (which had to begin the span) one CTA per kPer rows.  First
+// a row's largest reference and sum, then its channels, four a lane, all
+// results' loads independent of one another.  A row is one warp's (kPer = 8),
+// or eight warps take every eighth result of it (kPer = 1): that is for spans
+// over so many CTAs that a warp's loads in a row would take longer than the
+// launch of seven more CTAs (one row of 131071 columns, 57 results: 10 -> 6 us).
+constexpr int kJoinThreads = 256;
+constexpr int kJoinMany = 16;  // results of a span from which on
 
-template <int D, int kRows, bool kSel, bool kScores>
-__global__ void __launch_bounds__(kThreads)
+template <int D, int kRows, int kPer, bool kSel, bool kScores>
+__global__ void __launch_bounds__(kJoinThreads)
     kv4_join_kernel(const __grid_constant__ Kv4AttnParams p) {
-  __shared__ float factor[kMaxCtas];
-  __shared__ float red[kWarps * 2];
-  __shared__ float4 sums[kThreads];
+  __shared__ float4 sums[kPer == 1 ? 8 : 1][D / 4];
   grid_dependency_wait();
-  const int cta = blockIdx.x / kRows, row = blockIdx.x % kRows;
+  constexpr int kSets = kRows / kPer;
+  const int cta = blockIdx.x / kSets;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = kPer == 1 ? blockIdx.x % kSets : (blockIdx.x % kSets) * 8 + warp;
   const int4 sp = p.spans[cta];
   if (sp.x < 0) return;
   const int grp = sp.x, ht = sp.y, n = sp.z - cta + 1;
   const int row0 = (ht % p.row_tiles) * kRows;
   const int nrows = kSel ? p.heads : p.heads * p.next_n;
   if (!kScores && row0 + row >= nrows) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   auto part_of = [&](int i) {
-    return static_cast<int64_t>(cta + i) * 2 + (i == 0 ? sp.w : 0);
+    return (static_cast<int64_t>(cta + i) * 2 + (i == 0 ? sp.w : 0)) * kRows + row;
   };
+  auto ml_of = [&](int i) { return *reinterpret_cast<const float2*>(p.part_ml + part_of(i) * 2); };
   float M = -INFINITY;
-  for (int i = threadIdx.x; i < n; i += kThreads)
-    M = fmaxf(M, p.part_ml[(part_of(i) * kRows + row) * 2]);
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, ml_of(i).x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) red[warp] = M;
-  __syncthreads();
-  M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
   const float z = M == -INFINITY ? 0.f : M;
   float L = 0.f;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (part_of(i) * kRows + row) * 2);
-    const float f = ex2(ml.x - z);
-    factor[i] = f;
-    L = fmaf(ml.y, f, L);
+  for (int i = lane; i < n; i += 32) {
+    const float2 ml = ml_of(i);
+    L = fmaf(ml.y, ex2(ml.x - z), L);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  if (lane == 0) red[kWarps + warp] = L;
-  __syncthreads();
-  L = (red[kWarps] + red[kWarps + 1]) + (red[kWarps + 2] + red[kWarps + 3]);
-  constexpr int kQuads = D / 4, kDeal = kThreads / kQuads;
-  const int q = threadIdx.x % kQuads;
+  constexpr int kQuads = D / 4, kHalves = 32 / kQuads, kDeal = (kPer == 1 ? 8 : 1) * kHalves;
+  const int q = lane % kQuads;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = threadIdx.x / kQuads; i < n; i += kDeal) {
-    const float4 x =
-        *reinterpret_cast<const float4*>(p.part_o + (part_of(i) * kRows + row) * D + q * 4);
-    const float f = factor[i];
+#pragma unroll 8
+  for (int i = (kPer == 1 ? warp * kHalves : 0) + lane / kQuads; i < n; i += kDeal) {
+    const float4 x = *reinterpret_cast<const float4*>(p.part_o + part_of(i) * D + q * 4);
+    const float f = ex2(ml_of(i).x - z);
     a.x = fmaf(x.x, f, a.x), a.y = fmaf(x.y, f, a.y);
     a.z = fmaf(x.z, f, a.z), a.w = fmaf(x.w, f, a.w);
   }
-  sums[threadIdx.x] = a;
-  __syncthreads();
-  if (threadIdx.x >= kQuads) return;
-#pragma unroll
-  for (int i = 1; i < kDeal; ++i) {
-    const float4 x = sums[i * kQuads + q];
-    a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+  if constexpr (kHalves == 2) {
+    a.x += __shfl_xor_sync(0xffffffffu, a.x, 16), a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
+    a.z += __shfl_xor_sync(0xffffffffu, a.z, 16), a.w += __shfl_xor_sync(0xffffffffu, a.w, 16);
   }
-  write_row<D, kRows, kSel, kScores>(p, grp, ht, row0, nrows, row, q * 4, true, 0, M, L, a);
+  if constexpr (kPer == 1) {
+    if (lane < kQuads) sums[warp][q] = a;
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int w = 1; w < 8; ++w) {
+      const float4 x = sums[w][q];
+      a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+    }
+  }
+  if (lane < kQuads)
+    write_row<D, kRows, kSel, kScores>(p, grp, ht, row0, nrows, row, q * 4, true, 0, M, L, a);
 }
 
 // A column's attention weight, summed over heads and rows in one fixed order:
@@ -1841,15 +1847,17 @@ cudaError_t launch_rows(const Kv4AttnParams& p, cudaStream_t s) {
   if (e == cudaSuccess && p.spans) {
     // Launched while the attention kernel still runs (it waits inside).
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.ctas) * kRows);
-    cfg.blockDim = dim3(kThreads);
+    const bool many = p.ctas >= static_cast<int64_t>(p.groups) * p.Hkv * p.row_tiles * kJoinMany;
+    cfg.gridDim = dim3(static_cast<unsigned>(p.ctas) * (many ? kRows : kRows / 8));
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, kRows, kSel, kScores>, p);
+    e = many ? cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, kRows, 1, kSel, kScores>, p)
+             : cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, kRows, 8, kSel, kScores>, p);
   }
   if (e == cudaSuccess && kScores) {
     const int64_t grid = static_cast<int64_t>(p.groups) * ((p.cols + 255) / 256);
@@ -1899,9 +1907,8 @@ Kv4AttnPlan kv4_attn_plan(int B, int next_n, int Hq, int Hkv, int D, int64_t col
   const int64_t units = cols > 0 ? (cols + unit - 1) / unit : 1;
   const int64_t lanes = pl.groups * Hkv * pl.row_tiles;
   const int64_t places = static_cast<int64_t>(device_sm_count() > 0 ? device_sm_count() : 152) *
-                         (pl.rows <= 16 ? 3 : 2);
+                         (uses_tc(pl.rows) ? kTcCtas : kCtasPerSm);
   pl.ctas = static_cast<int>(units * lanes < places ? units * lanes : places);
-  if (pl.ctas > kMaxCtas) pl.ctas = kMaxCtas;
   pl.split = units > 1;
   int64_t off = 0;
   auto take = [&](int64_t bytes) {

@@ -41,11 +41,16 @@ __global__ void __launch_bounds__(256)
   const int L = clamp_len(lens[b], max_ctx);
   const int lo = starts[b], hi = ends[b];
   const int32_t* m = mid + static_cast<int64_t>(b) * room;
-  // Entries of the selection before its -1 padding (it ascends).
-  int n = 0, step = 1;
-  while (step <= room) step <<= 1;
-  for (step >>= 1; step > 0; step >>= 1)
-    if (n + step <= room && m[n + step - 1] >= 0) n += step;
+  // Entries of the selection before its -1 padding (it ascends): as many as
+  // fit, unless some weights could not be chosen; then the end is searched.
+  int n = min(room, hi - lo);
+  if (n > 0 && m[n - 1] < 0) {
+    int most = n, step = 1;
+    n = 0;
+    while (step <= most) step <<= 1;
+    for (step >>= 1; step > 0; step >>= 1)
+      if (n + step <= most && m[n + step - 1] >= 0) n += step;
+  }
   const int total = lo + n + (L - hi);
   const int i = blockIdx.x * 256 + threadIdx.x;
   if (i == 0) new_lens[b] = total;
@@ -59,13 +64,118 @@ __global__ void __launch_bounds__(256)
 
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 8;  // rows a thread holds per chunk
-constexpr int kSlice = 128;     // bytes of a row one CTA moves
-constexpr int kPartRows = 1024; // rows a CTA moves when pages are fresh
+constexpr int kSlice = 128;     // bytes of a row one CTA moves in place
+constexpr int kPartRows = 64;   // rows a CTA moves to fresh pages
 
-// Rows [i0, i1) of one slice (plane, byte range) of a cache.
-template <typename V, bool kInPlace>
+// To fresh pages: a CTA takes kPartRows rows of a request in every cache.
+// Their slots are looked up once; after that the copies are independent of one
+// another, eight a thread in flight.
+template <typename V>
+__device__ __forceinline__ void copy_rows(const CompactParams& p, const CompactParams::Cache& c,
+                                          const int2* slots, int n) {
+  const int vecs = c.row_bytes / static_cast<int>(sizeof(V));  // of a row
+  const int per_plane = n * vecs;
+  const int total = per_plane * c.planes;
+  const int mask = (1 << p.log_bs) - 1;
+  auto row_of = [&](int slot, int plane) {
+    return ((static_cast<int64_t>(slot >> p.log_bs) * c.planes + plane) << p.log_bs) +
+           (slot & mask);
+  };
+  for (int base = threadIdx.x; base < total; base += kMoveThreads * kMoveUnroll) {
+    V buf[kMoveUnroll];
+    uint8_t* dst[kMoveUnroll];
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u) {
+      const int e = base + u * kMoveThreads;
+      dst[u] = nullptr;
+      if (e >= total) continue;
+      const int plane = e / per_plane, in = e - plane * per_plane;
+      const int row = in / vecs, v = in - row * vecs;
+      const int2 s = slots[row];
+      if (s.x < 0) continue;
+      const int64_t at = static_cast<int64_t>(v) * sizeof(V);
+      buf[u] = __ldg(reinterpret_cast<const V*>(c.base + row_of(s.x, plane) * c.row_bytes + at));
+      dst[u] = c.base + row_of(s.y, plane) * c.row_bytes + at;
+    }
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u)
+      if (dst[u]) *reinterpret_cast<V*>(dst[u]) = buf[u];
+  }
+}
+
+__global__ void __launch_bounds__(kMoveThreads)
+    kv_move_kernel(const __grid_constant__ CompactParams p) {
+  __shared__ int2 slots[kPartRows];  // source and destination, or (-1, .)
+  const int b = blockIdx.y, part = blockIdx.x;
+  const int cap = p.max_blocks << p.log_bs;
+  const int old_len = clamp_len(__ldg(p.old_lens + b), cap);
+  int n = __ldg(p.new_lens + b);
+  if (n < 0 || n > p.budget) {
+    if (threadIdx.x == 0 && part == 0) record_error(p.err, kErrBadIndex);
+    n = n < 0 ? 0 : p.budget;
+  }
+  const int32_t* keep = p.keep + static_cast<int64_t>(b) * p.budget;
+  const int i0 = part * kPartRows;
+  if (p.weights) {
+    // The weights: one value a position, and zeros after the last kept one.
+    // Rewritten where they lie, they are one CTA's work.
+    const float* w = p.weights + static_cast<int64_t>(b) * p.ldw;
+    float* out = p.weights_out + static_cast<int64_t>(b) * p.ldw;
+    const bool alone = p.weights_out == p.weights;
+    if (!alone || part == 0) {
+      const int kept = min(n, cap);
+      const int w0 = alone ? 0 : i0, w1 = alone ? kept : min(kept, i0 + kPartRows);
+      for (int base = w0; base < w1; base += kMoveThreads) {
+        const int i = base + threadIdx.x;
+        float v = 0.f;
+        if (i < w1) {
+          const int pos = __ldg(keep + i);
+          if (pos >= 0 && pos < old_len) v = w[pos];
+        }
+        __syncthreads();
+        if (i < w1) out[i] = v;
+      }
+      __syncthreads();
+      const int parts = alone ? 1 : gridDim.x;
+      const int64_t rest = cap - kept;
+      const int64_t z0 = kept + rest * part / parts, z1 = kept + rest * (part + 1) / parts;
+      for (int64_t i = z0 + threadIdx.x; i < z1; i += kMoveThreads) out[i] = 0.f;
+    }
+  }
+  n = min(n, p.new_max_blocks << p.log_bs);
+  const int rows = min(n - i0, kPartRows);
+  if (rows <= 0) return;
+  if (threadIdx.x < rows) {
+    const int i = i0 + threadIdx.x;
+    const int pos = __ldg(keep + i);
+    int2 s = make_int2(-1, -1);
+    bool bad = pos < 0 || pos >= old_len;
+    if (!bad) {
+      const int from = __ldg(p.block_table + static_cast<int64_t>(b) * p.max_blocks +
+                             (pos >> p.log_bs));
+      const int to = __ldg(p.new_block_table + static_cast<int64_t>(b) * p.new_max_blocks +
+                           (i >> p.log_bs));
+      const int mask = (1 << p.log_bs) - 1;
+      bad = from < 0 || from >= p.num_blocks || to < 0 || to >= p.num_blocks;
+      if (!bad)
+        s = make_int2((from << p.log_bs) + (pos & mask), (to << p.log_bs) + (i & mask));
+    }
+    if (bad) record_error(p.err, kErrBadIndex);
+    slots[threadIdx.x] = s;
+  }
+  __syncthreads();
+  for (int c = 0; c < p.ncaches; ++c) {
+    const CompactParams::Cache cache = p.cache[c];
+    if (cache.row_bytes % 16 == 0) copy_rows<uint4>(p, cache, slots, rows);
+    else if (cache.row_bytes % 8 == 0) copy_rows<uint2>(p, cache, slots, rows);
+    else copy_rows<uint32_t>(p, cache, slots, rows);
+  }
+}
+
+// In place: rows [0, i1) of one slice (plane, byte range) of a cache.
+template <typename V>
 __device__ __forceinline__ void move_rows(const CompactParams& p, const CompactParams::Cache& c,
-                                          int plane, int at, int width, int b, int old_len, int i0,
+                                          int plane, int at, int width, int b, int old_len,
                                           int i1) {
   const int lanes = width / static_cast<int>(sizeof(V));
   const int sub = threadIdx.x % lanes;
@@ -76,8 +186,6 @@ __device__ __forceinline__ void move_rows(const CompactParams& p, const CompactP
   const int mask = (1 << p.log_bs) - 1;
   const int32_t* keep = p.keep + static_cast<int64_t>(b) * p.budget;
   const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.max_blocks;
-  const int32_t* dst_table =
-      kInPlace ? table : p.new_block_table + static_cast<int64_t>(b) * p.new_max_blocks;
   auto address = [&](const int32_t* tab, int pos) -> uint8_t* {
     const int block = __ldg(tab + (pos >> p.log_bs));
     if (block < 0 || block >= p.num_blocks) {
@@ -100,7 +208,7 @@ __device__ __forceinline__ void move_rows(const CompactParams& p, const CompactP
         record_error(p.err, kErrBadIndex);
         continue;
       }
-      if (kInPlace && pos == i) continue;
+      if (pos == i) continue;
       const uint8_t* src = address(table, pos);
       if (!src) continue;
       v[u] = *reinterpret_cast<const V*>(src);
@@ -111,41 +219,36 @@ __device__ __forceinline__ void move_rows(const CompactParams& p, const CompactP
 #pragma unroll
     for (int u = 0; u < kMoveUnroll; ++u) {
       if (!((ok >> u) & 1)) continue;
-      uint8_t* dst = address(dst_table, base + u * rows + row_in);
+      uint8_t* dst = address(table, base + u * rows + row_in);
       if (dst) *reinterpret_cast<V*>(dst) = v[u];
     }
   };
-  load(buf[0], got[0], i0);
-  for (int base = i0; base < i1; base += 2 * chunk) {
+  load(buf[0], got[0], 0);
+  for (int base = 0; base < i1; base += 2 * chunk) {
     // The next chunk's rows lie at or above its own first position, so
     // reading them does not wait for this chunk's stores; this chunk's stores
     // wait for every thread's reads of this chunk.
     load(buf[1], got[1], base + chunk);
-    if (kInPlace) __syncthreads();
+    __syncthreads();
     store(buf[0], got[0], base);
     load(buf[0], got[0], base + 2 * chunk);
-    if (kInPlace) __syncthreads();
+    __syncthreads();
     store(buf[1], got[1], base + chunk);
   }
 }
 
-template <bool kInPlace>
 __global__ void __launch_bounds__(kMoveThreads)
     kv_compact_kernel(const __grid_constant__ CompactParams p) {
-  const int b = blockIdx.z, unit = blockIdx.x, part = blockIdx.y;
+  const int b = blockIdx.y, unit = blockIdx.x;
   const int cap = p.max_blocks << p.log_bs;
   const int old_len = clamp_len(__ldg(p.old_lens + b), cap);
   int n = __ldg(p.new_lens + b);
   if (n < 0 || n > p.budget) {
-    if (threadIdx.x == 0) record_error(p.err, kErrBadIndex);
+    if (threadIdx.x == 0 && unit == 0) record_error(p.err, kErrBadIndex);
     n = n < 0 ? 0 : p.budget;
   }
-  if (!kInPlace) n = min(n, p.new_max_blocks << p.log_bs);
-  else n = min(n, cap);
+  n = min(n, cap);
   if (unit < p.units) {
-    const int i0 = kInPlace ? 0 : part * kPartRows;
-    const int i1 = kInPlace ? n : min(n, i0 + kPartRows);
-    if (i0 >= i1) return;
     int c = 0;
     while (unit >= p.first_unit[c + 1]) ++c;
     const CompactParams::Cache cache = p.cache[c];
@@ -154,36 +257,29 @@ __global__ void __launch_bounds__(kMoveThreads)
     const int plane = u / slices, at = (u % slices) * kSlice;
     const int width = min(kSlice, cache.row_bytes - at);
     if (width % 16 == 0 && cache.row_bytes % 16 == 0)
-      move_rows<uint4, kInPlace>(p, cache, plane, at, width, b, old_len, i0, i1);
+      move_rows<uint4>(p, cache, plane, at, width, b, old_len, n);
     else if (width % 8 == 0 && cache.row_bytes % 8 == 0)
-      move_rows<uint2, kInPlace>(p, cache, plane, at, width, b, old_len, i0, i1);
+      move_rows<uint2>(p, cache, plane, at, width, b, old_len, n);
     else
-      move_rows<uint32_t, kInPlace>(p, cache, plane, at, width, b, old_len, i0, i1);
+      move_rows<uint32_t>(p, cache, plane, at, width, b, old_len, n);
     return;
   }
   // The weights: one value a position, and zeros after the last kept one.
   const float* w = p.weights + static_cast<int64_t>(b) * p.ldw;
   float* out = p.weights_out + static_cast<int64_t>(b) * p.ldw;
-  // Rewritten where they lie, they are one CTA's work whatever the pages do.
-  const bool alone = p.weights_out == p.weights;
-  if (alone && part > 0) return;
-  const int i0 = alone ? 0 : part * kPartRows, i1 = alone ? n : min(n, i0 + kPartRows);
   const int32_t* keep = p.keep + static_cast<int64_t>(b) * p.budget;
-  for (int base = i0; base < i1; base += kMoveThreads) {
+  for (int base = 0; base < n; base += kMoveThreads) {
     const int i = base + threadIdx.x;
     float v = 0.f;
-    if (i < i1) {
+    if (i < n) {
       const int pos = __ldg(keep + i);
       if (pos >= 0 && pos < old_len) v = w[pos];
     }
     __syncthreads();
-    if (i < i1) out[i] = v;
+    if (i < n) out[i] = v;
   }
   __syncthreads();
-  const int parts = alone ? 1 : gridDim.y;
-  const int64_t rest = cap - n;
-  const int64_t z0 = n + rest * part / parts, z1 = n + rest * (part + 1) / parts;
-  for (int64_t i = z0 + threadIdx.x; i < z1; i += kMoveThreads) out[i] = 0.f;
+  for (int i = n + threadIdx.x; i < cap; i += kMoveThreads) out[i] = 0.f;
 }
 
 }  // namespace
@@ -211,12 +307,10 @@ int compact_units(const CompactParams::Cache& c) {
 cudaError_t launch_kv_compact(const CompactParams& p, cudaStream_t s) {
   const int units = p.units + (p.weights ? 1 : 0);
   if (units == 0 || p.B == 0) return cudaSuccess;
-  if (p.new_block_table) {
-    const dim3 grid(units, (p.budget + kPartRows - 1) / kPartRows, p.B);
-    kv_compact_kernel<false><<<grid, kMoveThreads, 0, s>>>(p);
-  } else {
-    kv_compact_kernel<true><<<dim3(units, 1, p.B), kMoveThreads, 0, s>>>(p);
-  }
+  if (p.new_block_table)
+    kv_move_kernel<<<dim3((p.budget + kPartRows - 1) / kPartRows, p.B), kMoveThreads, 0, s>>>(p);
+  else
+    kv_compact_kernel<<<dim3(units, p.B), kMoveThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
