@@ -169,7 +169,7 @@ struct Kv4AttnParams {
 // How a call is cut up, and the byte offsets of its workspace.
 struct Kv4AttnPlan {
   int64_t groups;
-  int heads, rows, row_tiles, tile, ctas;  // rows of a CTA; columns of a tile
+  int heads, rows, row_tiles, tile, unit, ctas;  // rows of a CTA; columns of a tile, of a unit
   bool split;
   int64_t part_o, part_ml, spans, scores, lse2, sel_weights, bytes;
 };

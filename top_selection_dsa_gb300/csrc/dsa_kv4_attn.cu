@@ -218,8 +218,8 @@ __device__ __forceinline__ Group group_of(const Kv4AttnParams& p, int g) {
 
 // The work of a call is a list of units of kUnit columns, by group, then head
 // and row tile, then column (a group without columns has one empty unit); CTA
-// i of P takes the units [T i / P, T (i + 1) / P) of the T there are, whatever
-// the requests' lengths.  A run of units of one group, head and row tile is a
+// i of P takes T / P of the T there are (the first T % P CTAs one more),
+// whatever the requests' lengths.  A run of units of one group, head and row tile is a
 // span; a CTA's spans are whole, but for its first and its last, which may be
 // shared with its neighbours.
 // The walk lives in shared memory (its state would cost every thread a dozen
@@ -235,12 +235,12 @@ struct Span {
 
 template <bool kSel, int kUnit>
 struct Walk {
-  int64_t t, t1, total;
-  int64_t P;       // CTAs that have work
-  int64_t base;    // units before group g
+  uint32_t t, t1;        // units left: [t, t1)
+  uint32_t each, more;   // every CTA has `each` units, the first `more` one more
+  uint32_t base;         // units before group g
   int g;
   bool first;
-  Span span;       // the one in work
+  Span span;             // the one in work
 
   __device__ static int units_of(int cols) { return cols > 0 ? (cols + kUnit - 1) / kUnit : 1; }
 
@@ -249,35 +249,30 @@ struct Walk {
   __device__ __forceinline__ explicit Walk(const Kv4AttnParams& p) {
     const int per = p.Hkv * p.row_tiles;
     const int lane = threadIdx.x & 31;
-    const int64_t i = blockIdx.x;
     first = true;
     if constexpr (kSel) {
-      const int64_t upg = static_cast<int64_t>(units_of(p.sel_k)) * per;
-      total = upg * p.groups;
-      share(i);
+      const uint32_t upg = static_cast<uint32_t>(units_of(p.sel_k)) * per;
+      share(upg * p.groups);
       g = static_cast<int>(t / upg);
       base = g * upg;
       if (blockIdx.x == 0)
         for (int b = lane; b < p.groups / p.next_n; b += 32) context_len(p, b, true);
     } else {
       const bool report = blockIdx.x == 0;
-      int64_t mine = 0;
+      uint32_t mine = 0;
       for (int b = lane; b < p.groups; b += 32)
         mine += units_of(context_len(p, b, report));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-      total = mine * per;
-      share(i);
+      share(__reduce_add_sync(0xffffffffu, mine) * per);
       base = 0;
       g = 0;
       for (int b0 = 0; b0 < p.groups; b0 += 32) {
-        const int64_t v =
+        const uint32_t v =
             b0 + lane < p.groups
-                ? static_cast<int64_t>(units_of(context_len(p, b0 + lane))) * per : 0;
-        int64_t incl = v;
+                ? static_cast<uint32_t>(units_of(context_len(p, b0 + lane))) * per : 0;
+        uint32_t incl = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+          const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
           if (lane >= o) incl += y;
         }
         const uint32_t past = __ballot_sync(0xffffffffu, t < base + incl);
@@ -291,10 +286,11 @@ struct Walk {
       }
     }
   }
-  __device__ __forceinline__ void share(int64_t i) {
-    P = total < gridDim.x ? total : gridDim.x;
-    t = i < P ? total * i / P : total;
-    t1 = i < P ? total * (i + 1) / P : total;
+  __device__ __forceinline__ void share(uint32_t total) {
+    each = total / gridDim.x;
+    more = total - each * gridDim.x;
+    t = blockIdx.x * each + min(blockIdx.x, more);
+    t1 = t + each + (blockIdx.x < more ? 1 : 0);
   }
   // Thread 0: the next span; the one it begins and does not end is noted for
   // the join: .x group; .y head and row tile; .z the last CTA of the span; .w
@@ -309,11 +305,9 @@ struct Walk {
     s.gr = group_of<kSel>(p, g);
     s.g = g;
     s.units = units_of(s.gr.cols);
-    const int64_t at = t - base;
-    s.ht = static_cast<int>(at / s.units);
-    s.u0 = static_cast<int>(at - static_cast<int64_t>(s.ht) * s.units);
-    const int64_t left = t1 - t;
-    s.u1 = left < s.units - s.u0 ? s.u0 + static_cast<int>(left) : s.units;
+    s.ht = static_cast<int>((t - base) / s.units);
+    s.u0 = static_cast<int>(t - base) - s.ht * s.units;
+    s.u1 = min(s.u0 + static_cast<int>(t1 - t), s.units);
     s.first = first;
     first = false;
     t += s.u1 - s.u0;
@@ -326,8 +320,9 @@ struct Walk {
     span = s;
   }
   // The CTA that takes unit x.
-  __device__ __forceinline__ int cta_of(int64_t x) const {
-    return static_cast<int>(((x + 1) * P - 1) / total);
+  __device__ __forceinline__ int cta_of(uint32_t x) const {
+    const uint32_t ahead = more * (each + 1);
+    return static_cast<int>(x < ahead ? x / (each + 1) : more + (x - ahead) / each);
   }
 };
 
@@ -1903,7 +1898,7 @@ Kv4AttnPlan kv4_attn_plan(int B, int next_n, int Hq, int Hkv, int D, int64_t col
   pl.row_tiles = (rows + pl.rows - 1) / pl.rows;
   pl.tile = uses_tc(pl.rows) ? kTcTile : kTile;
   // As many CTAs as the device holds, or as there can be units of work.
-  const int64_t unit = uses_tc(pl.rows) ? kTcTile : kTile * kWarps;
+  const int64_t unit = pl.unit = uses_tc(pl.rows) ? kTcTile : kTile * kWarps;
   const int64_t units = cols > 0 ? (cols + unit - 1) / unit : 1;
   const int64_t lanes = pl.groups * Hkv * pl.row_tiles;
   const int64_t places = static_cast<int64_t>(device_sm_count() > 0 ? device_sm_count() : 152) *

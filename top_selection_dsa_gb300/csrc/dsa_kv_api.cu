@@ -78,7 +78,9 @@ dsa_status_t run_attention(const AttnArgs& a, bool selected, dsa_stream_t stream
   const Kv4AttnPlan pl =
       kv4_attn_plan(a.B, a.next_n, a.Hq, a.Hkv, a.D, cols, selected, weights);
   const int64_t lanes = static_cast<int64_t>(a.Hkv) * pl.row_tiles;
-  if (pl.groups * lanes >= (int64_t(1) << 31) || pl.groups * ((cols + 255) / 256) >= (int64_t(1) << 31) ||
+  // Units of work are counted in 32 bits.
+  const int64_t units = cols / pl.unit + 1;
+  if (pl.groups * lanes >= (int64_t(1) << 31) / units || pl.groups * ((cols + 255) / 256) >= (int64_t(1) << 31) ||
       (weights && lanes * pl.rows * 4 > 48 * 1024))
     return DSA_ERR_UNSUPPORTED;
   if (pl.bytes > 0 && (!a.workspace || !aligned(a.workspace, 256) ||
