@@ -129,6 +129,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
                : "memory");
   return r;
 }
+// The two low bytes of w as bf16 numbers 2^(byte - 127).
+__device__ __forceinline__ uint32_t e8m0x2_to_bf16x2(uint32_t w) {
+  return ((w & 0xFFu) << 7) | ((w & 0xFF00u) << 15);
+}
+
 // Non-zero when a byte of w is 255.
 __device__ __forceinline__ uint32_t has_ff(uint32_t w) {
   return (~w - 0x01010101u) & w & 0x80808080u;
@@ -180,6 +185,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t x) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
 }
 __device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
@@ -407,6 +415,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   }
   const int per_split = p.Hkv * p.row_tiles;
   const int nrows = kSel ? p.heads : p.heads * p.next_n;
+  // The products' fragments.  One row tile: S^T = K q^T and O^T = V^T P, keys
+  // and channels as the 16 rows, query rows as the 8 columns: this lane has
+  // query rows 2t and 2t + 1, S in two tiles of 16 keys a half tile, O in two
+  // of 16 channels a scale block.  Two row tiles: S = q K^T and O = P V, the
+  // query rows as the 16 rows: this lane has rows r and r + 8, S in four tiles
+  // of 8 keys, O in four of 8 channels a block.
+  constexpr int kOut = 2 * NT * G, kPerBlock = 2 * NT;
+  auto row_of = [&](int i) { return NT == 1 ? 2 * t + i : r + 8 * i; };
+  auto row_ix = [](int j) { return NT == 1 ? j & 1 : j >> 1; };  // of a fragment's element j
   auto* const walk = reinterpret_cast<Walk<kSel, kTile * kWarps>*>(smem + Lay::kWalk);
   if (warp == 0) begin_walk(walk, p);
   launch_dependents();
@@ -527,12 +544,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   }
 
   // ---------------------------------------------------------------- queries
-  // B fragments: lane (r, t) holds row r's elements 32 g + 8 t .. + 7, times
-  // the softmax scale's sign.
-  // One row tile: every warp keeps the fragments in registers.  Two: warps 0
-  // and 1 prepare one each, and all read them from shared memory.
+  // Lane (r, t) has row r's elements 32 g + 8 t .. + 7, times the softmax
+  // scale's sign.  One row tile: the lane's B fragments, which every warp keeps
+  // in registers.  Two: the A fragments' rows r and r + 8, prepared by warps 0
+  // and 1, which all read from shared memory.
   uint32_t qf[NT == 1 ? G : 1][4];
-  float f[NT][2];    // base-2 logit = f * accumulator (f > 0), rows 2t and 2t + 1
+  float f[2];        // base-2 logit = f * accumulator (f > 0), of this lane's rows
   const bool zero = p.scale_log2e == 0.f;
   const float sign = zero ? 0.f : (p.scale_log2e < 0.f ? -1.f : 1.f);
   const uint32_t q_at = smem_u32(smem) + Lay::kQueries + lane * 16;
@@ -576,36 +593,36 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
         for (int i = 0; i < 4; ++i) qf[g][i] = h[i];
       } else {
-        sts128(q_at + (nt * G + g) * 512, h[0], h[1], h[2], h[3]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t at = q_at + (g * 2 + i) * 512 + nt * 4;
+          sts32(at, h[2 * i]);
+          sts32(at + 8, h[2 * i + 1]);
+        }
       }
     }
     const float fr = zero ? 1.f : ldexpf(fabsf(p.scale_log2e), E);
     if constexpr (NT == 1) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) f[0][i] = __shfl_sync(0xffffffffu, fr, (2 * t + i) * 4);
+      for (int i = 0; i < 2; ++i) f[i] = __shfl_sync(0xffffffffu, fr, (2 * t + i) * 4);
     } else if (t == 0) {
       f_s[nt * 8 + r] = fr;
     }
   }
   __syncthreads();
   if constexpr (NT > 1) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) f[nt][i] = f_s[nt * 8 + 2 * t + i];
+    f[0] = f_s[r], f[1] = f_s[r + 8];
   }
-  // Columns that query row 2t + i of row tile nt sees (asked for in the tiles
-  // where some row does not see all of them).
-  auto limit = [&](int nt, int i) { return limit_s[nt * 8 + 2 * t + i]; };
+  // Columns that this lane's row i sees (asked for in the tiles where some row
+  // does not see all of them).
+  auto limit = [&](int i) { return limit_s[row_of(i)]; };
   const int all_see = kSel ? gr.cols : gr.L - p.next_n + 1;  // columns every row sees
 
-  float o[NT][2 * G][4];
+  float o[kOut][4];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int x = 0; x < kOut; ++x)
 #pragma unroll
-    for (int i = 0; i < 2 * G; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) o[x][j] = 0.f;
   // m: reference of a row's accumulators, weight = 2^(f (accumulator - m)).  It
   // is raised to the running maximum only when a logit passes it by kSlack
   // (base 2), that is when an accumulator passes thr, so most tiles need no
@@ -613,11 +630,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   // which fp16 and fp32 hold as well as 1.  thr = -inf: the row has seen no
   // column.
   constexpr float kSlack = 8.f;
-  float thr[NT][2], m[NT][2], l[NT][2];
+  float thr[2], m[2], l[2];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) thr[nt][i] = -INFINITY, m[nt][i] = l[nt][i] = 0.f;
+  for (int i = 0; i < 2; ++i) thr[i] = -INFINITY, m[i] = l[i] = 0.f;
   float unit = 0.f, inv_unit = 0.f;  // o is in units of the largest value scale so far
 
   // Lane addresses that do not change from tile to tile: the key chunk of
@@ -700,16 +715,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
               from &= from - 1;
               const uint32_t word = __shfl_sync(0xffffffffu, vw[i], src);
               const int col = col0 + __shfl_sync(0xffffffffu, key[i], src);
+              const bool sees[2] = {col < limit(0), col < limit(1)};
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
+              for (int g = 0; g < G; ++g)
+                if (((word >> (8 * g)) & 255u) == 255u)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                  for (int x = 0; x < kPerBlock; ++x)
 #pragma unroll
-                  for (int g = 0; g < G; ++g)
-                    if (((word >> (8 * g)) & 255u) == 255u && col < limit(nt, h)) {
-                      o[nt][2 * g][h] = o[nt][2 * g][2 + h] = __uint_as_float(0x7FC00000u);
-                      o[nt][2 * g + 1][h] = o[nt][2 * g + 1][2 + h] = __uint_as_float(0x7FC00000u);
-                    }
+                    for (int j = 0; j < 4; ++j)
+                      if (sees[row_ix(j)]) o[kPerBlock * g + x][j] = __uint_as_float(0x7FC00000u);
             }
           }
           top = 0;
@@ -728,16 +742,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           unit = up;
           inv_unit = 1.f / up;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int x = 0; x < kOut; ++x)
 #pragma unroll
-            for (int i = 0; i < 2 * G; ++i)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) o[nt][i][j] *= down;
+            for (int j = 0; j < 4; ++j) o[x][j] *= down;
         }
         if constexpr (NT == 1) {
           // The key scales as fp32, where rows r of a group of eight find
-          // them side by side.  (With two row tiles there is no room for
-          // them: the scale words are unpacked where they are used.)
+          // them side by side.
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint32_t at = ks_at + (r * 8 + 2 * t + i) * (4 * G);
@@ -747,6 +758,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             else
               sts64(at, e8m0_bits<0>(kw[i]), e8m0_bits<1>(kw[i]));
           }
+        } else {
+          // The pair's key scales as bf16, in the place of the scale words
+          // (read above): a lane's two keys of an eight-key tile side by side.
+          if constexpr (D == 128)
+            sts128(sbase + lane * 16, e8m0x2_to_bf16x2(kw[0]), e8m0x2_to_bf16x2(kw[0] >> 16),
+                   e8m0x2_to_bf16x2(kw[1]), e8m0x2_to_bf16x2(kw[1] >> 16));
+          else
+            sts64(sbase + lane * 8, e8m0x2_to_bf16x2(kw[0]), e8m0x2_to_bf16x2(kw[1]));
         }
         uint32_t fac[G];
 #pragma unroll
@@ -763,142 +782,161 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         const uint32_t hbase = base + half * 32 * D;
-        // ---------------------------------------------------------- S^T = K q^T
-        float sacc[2][NT][4];
+        // ------------------------------------------------------------- S = q K^T
+        float sacc[2 * NT][4];
+        if constexpr (NT == 1) {
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          uint32_t kw[2][G];
-          float ks[2][G];
+          for (int mt = 0; mt < 2; ++mt) {
+            uint32_t kw[2][G];
+            float ks[2][G];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t at = hbase + (mt * 16 + h * 8) * D + k_at;
-            if constexpr (D == 128) {
-              const uint4 u = lds128(at);
-              kw[h][0] = u.x, kw[h][1] = u.y, kw[h][2] = u.z, kw[h][3] = u.w;
-            } else {
-              const uint2 u = lds64(at);
-              kw[h][0] = u.x, kw[h][1] = u.y;
-            }
-            if constexpr (NT == 1) {
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t at = hbase + (mt * 16 + h * 8) * D + k_at;
               const uint32_t sat = ks_at + (half * 32 + mt * 16 + h * 8 + r) * (4 * G);
               if constexpr (D == 128) {
-                const uint4 v = lds128(sat);
+                const uint4 u = lds128(at), v = lds128(sat);
+                kw[h][0] = u.x, kw[h][1] = u.y, kw[h][2] = u.z, kw[h][3] = u.w;
                 ks[h][0] = __uint_as_float(v.x), ks[h][1] = __uint_as_float(v.y);
                 ks[h][2] = __uint_as_float(v.z), ks[h][3] = __uint_as_float(v.w);
               } else {
-                const uint2 v = lds64(sat);
+                const uint2 u = lds64(at), v = lds64(sat);
+                kw[h][0] = u.x, kw[h][1] = u.y;
                 ks[h][0] = __uint_as_float(v.x), ks[h][1] = __uint_as_float(v.y);
               }
-            } else {
-              const uint32_t w = lds32(sbase + (half * 32 + mt * 16 + h * 8 + prow) * Lay::kSc);
-              ks[h][0] = __uint_as_float(e8m0_bits<0>(w));
-              ks[h][1] = __uint_as_float(e8m0_bits<1>(w));
-              if constexpr (D == 128) {
-                ks[h][2] = __uint_as_float(e8m0_bits<2>(w));
-                ks[h][3] = __uint_as_float(e8m0_bits<3>(w));
-              }
             }
-          }
 #pragma unroll
-          for (int g = 0; g < G; ++g) {
-            const uint32_t a0 = e2m1x2_to_f16x2<0>(kw[0][g]), a1 = e2m1x2_to_f16x2<0>(kw[1][g]);
-            const uint32_t a2 = e2m1x2_to_f16x2<1>(kw[0][g]), a3 = e2m1x2_to_f16x2<1>(kw[1][g]);
-            const uint32_t b0 = e2m1x2_to_f16x2<2>(kw[0][g]), b1 = e2m1x2_to_f16x2<2>(kw[1][g]);
-            const uint32_t b2 = e2m1x2_to_f16x2<3>(kw[0][g]), b3 = e2m1x2_to_f16x2<3>(kw[1][g]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int g = 0; g < G; ++g) {
+              const uint32_t a0 = e2m1x2_to_f16x2<0>(kw[0][g]), a1 = e2m1x2_to_f16x2<0>(kw[1][g]);
+              const uint32_t a2 = e2m1x2_to_f16x2<1>(kw[0][g]), a3 = e2m1x2_to_f16x2<1>(kw[1][g]);
+              const uint32_t b0 = e2m1x2_to_f16x2<2>(kw[0][g]), b1 = e2m1x2_to_f16x2<2>(kw[1][g]);
+              const uint32_t b2 = e2m1x2_to_f16x2<3>(kw[0][g]), b3 = e2m1x2_to_f16x2<3>(kw[1][g]);
               float c[4];
-              uint4 q;
-              if constexpr (NT == 1) q = make_uint4(qf[g][0], qf[g][1], qf[g][2], qf[g][3]);
-              else q = lds128(q_at + (nt * G + g) * 512);
-              mma16816_zero(c, a0, a1, a2, a3, q.x, q.y);
-              mma16816(c, b0, b1, b2, b3, q.z, q.w);
+              mma16816_zero(c, a0, a1, a2, a3, qf[g][0], qf[g][1]);
+              mma16816(c, b0, b1, b2, b3, qf[g][2], qf[g][3]);
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                sacc[mt][nt][j] =
-                    g == 0 ? c[j] * ks[j >> 1][g] : fmaf(c[j], ks[j >> 1][g], sacc[mt][nt][j]);
+                sacc[mt][j] = g == 0 ? c[j] * ks[j >> 1][g] : fmaf(c[j], ks[j >> 1][g], sacc[mt][j]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int np = 0; np < 2; ++np) {  // pairs of eight-key tiles share the query fragments
+            uint32_t kw[2][G], ks[2][G];    // ks: key a's scales by two blocks, then key b's
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t at = hbase + (np * 16 + h * 8) * D + k_at;
+              const uint32_t sat = sbase + ((half * 4 + np * 2 + h) * 4 + t) * (4 * G);
+              if constexpr (D == 128) {
+                const uint4 u = lds128(at), v = lds128(sat);
+                kw[h][0] = u.x, kw[h][1] = u.y, kw[h][2] = u.z, kw[h][3] = u.w;
+                ks[h][0] = v.x, ks[h][1] = v.y, ks[h][2] = v.z, ks[h][3] = v.w;
+              } else {
+                const uint2 u = lds64(at), v = lds64(sat);
+                kw[h][0] = u.x, kw[h][1] = u.y, ks[h][0] = v.x, ks[h][1] = v.y;
+              }
+            }
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              const uint4 qa = lds128(q_at + (g * 2) * 512), qb = lds128(q_at + (g * 2 + 1) * 512);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float c[4];
+                mma16816_zero(c, qa.x, qa.y, qa.z, qa.w, e2m1x2_to_f16x2<0>(kw[h][g]),
+                              e2m1x2_to_f16x2<1>(kw[h][g]));
+                mma16816(c, qb.x, qb.y, qb.z, qb.w, e2m1x2_to_f16x2<2>(kw[h][g]),
+                         e2m1x2_to_f16x2<3>(kw[h][g]));
+                const uint32_t wa = ks[h][g / 2], wb = ks[h][G / 2 + g / 2];
+                const float sc[2] = {__uint_as_float(g % 2 ? wa & 0xFFFF0000u : wa << 16),
+                                     __uint_as_float(g % 2 ? wb & 0xFFFF0000u : wb << 16)};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  sacc[np * 2 + h][j] =
+                      g == 0 ? c[j] * sc[j & 1] : fmaf(c[j], sc[j & 1], sacc[np * 2 + h][j]);
+              }
             }
           }
         }
         // ------------------------------------------------------------- softmax
+        // Key of element j of S tile x, within the half.
+        auto key_of = [&](int x, int j) {
+          return NT == 1 ? x * 16 + (j >> 1) * 8 + prow : x * 8 + v_row[j & 1];
+        };
         if (!clean) {
           const uint32_t hlive = half ? live.y : live.x, hnan = half ? nan.y : nan.x;
+          const int sees[2] = {limit(0) - col0 - half * 32, limit(1) - col0 - half * 32};
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
+          for (int x = 0; x < 2 * NT; ++x)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int key = mt * 16 + h * 8 + prow;
-              const bool here = (hlive >> key) & 1, bad = (hnan >> key) & 1;
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  if (bad) sacc[mt][nt][2 * h + i] = __uint_as_float(0x7FC00000u);
-                  if (!here || (!kSel && col0 + half * 32 + key >= limit(nt, i)))
-                    sacc[mt][nt][2 * h + i] = -INFINITY;
-                }
+            for (int j = 0; j < 4; ++j) {
+              const int key = key_of(x, j);
+              if ((hnan >> key) & 1) sacc[x][j] = __uint_as_float(0x7FC00000u);
+              if (!((hlive >> key) & 1) || (!kSel && key >= sees[row_ix(j)]))
+                sacc[x][j] = -INFINITY;
             }
         }
         if constexpr (kScores) {
           float* dst = p.scores + (static_cast<int64_t>(grp) * per_split + ht) * p.cols * kRows;
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
+          for (int x = 0; x < 2 * NT; ++x)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int col = col0 + half * 32 + mt * 16 + h * 8 + prow;
+            for (int j = 0; j < 4; j += NT == 1 ? 2 : 1) {
+              const int col = col0 + half * 32 + key_of(x, j);
               if (col < c1) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                  *reinterpret_cast<float2*>(dst + static_cast<int64_t>(col) * kRows + nt * 8 +
-                                             2 * t) =
-                      make_float2(sacc[mt][nt][2 * h] * f[nt][0],
-                                  sacc[mt][nt][2 * h + 1] * f[nt][1]);
+                float* at = dst + static_cast<int64_t>(col) * kRows + row_of(row_ix(j));
+                if constexpr (NT == 1)
+                  *reinterpret_cast<float2*>(at) =
+                      make_float2(sacc[x][j] * f[0], sacc[x][j + 1] * f[1]);
+                else
+                  *at = sacc[x][j] * f[row_ix(j)];
               }
             }
         }
-        float x[NT][2];
-        bool up = false;
+        float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int x = 0; x < 2 * NT; ++x)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) top[row_ix(j)] = fmaxf(top[row_ix(j)], sacc[x][j]);
+        if (__any_sync(0xffffffffu, top[0] > thr[0] || top[1] > thr[1])) {
+          float a[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            x[nt][i] = fmaxf(fmaxf(sacc[0][nt][i], sacc[0][nt][2 + i]),
-                             fmaxf(sacc[1][nt][i], sacc[1][nt][2 + i]));
-            up |= x[nt][i] > thr[nt][i];
-          }
-        if (__any_sync(0xffffffffu, up)) {
+            float v = top[i];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float v = fmaxf(x[nt][i], __shfl_xor_sync(0xffffffffu, x[nt][i], 4));
-              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-              if (v > thr[nt][i]) {
-                const float a = thr[nt][i] == -INFINITY ? 0.f : ex2((m[nt][i] - v) * f[nt][i]);
-                m[nt][i] = v;
-                thr[nt][i] = v + kSlack / f[nt][i];
-                l[nt][i] *= a;
-#pragma unroll
-                for (int j = 0; j < 2 * G; ++j) o[nt][j][i] *= a, o[nt][j][2 + i] *= a;
-              }
+            for (int x = NT == 1 ? 4 : 1; x < (NT == 1 ? 32 : 4); x <<= 1)
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
+            a[i] = 1.f;
+            if (v > thr[i]) {
+              a[i] = thr[i] == -INFINITY ? 0.f : ex2((m[i] - v) * f[i]);
+              m[i] = v;
+              thr[i] = v + kSlack / f[i];
+              l[i] *= a[i];
             }
-        }
-        uint32_t pf[2][NT][2];  // P as B fragments: row r, keys 2t, 2t+1 (+ 8)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
-            const float p0 = ex2((sacc[mt][nt][0] - m[nt][0]) * f[nt][0]);
-            const float p1 = ex2((sacc[mt][nt][1] - m[nt][1]) * f[nt][1]);
-            const float p2 = ex2((sacc[mt][nt][2] - m[nt][0]) * f[nt][0]);
-            const float p3 = ex2((sacc[mt][nt][3] - m[nt][1]) * f[nt][1]);
-            l[nt][0] += p0 + p2;
-            l[nt][1] += p1 + p3;
-            pf[mt][nt][0] = transpose8x8(pack_f16(p0, p1));
-            pf[mt][nt][1] = transpose8x8(pack_f16(p2, p3));
           }
-        // ---------------------------------------------------------- O^T += V^T P
+#pragma unroll
+          for (int x = 0; x < kOut; ++x)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[x][j] *= a[row_ix(j)];
+        }
+        // P: one row tile, B fragments (row r, keys 2t, 2t+1, then + 8); two, A
+        // fragments (rows r and r + 8, those keys).  Of 16 keys each.
+        uint32_t pf[2][2 * NT];
+#pragma unroll
+        for (int x = 0; x < 2 * NT; ++x) {
+          float e[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            e[j] = ex2((sacc[x][j] - m[row_ix(j)]) * f[row_ix(j)]);
+            l[row_ix(j)] += e[j];
+          }
+          if constexpr (NT == 1) {
+            pf[x][0] = transpose8x8(pack_f16(e[0], e[1]));
+            pf[x][1] = transpose8x8(pack_f16(e[2], e[3]));
+          } else {
+            pf[x / 2][(x % 2) * 2] = pack_f16(e[0], e[1]);
+            pf[x / 2][(x % 2) * 2 + 1] = pack_f16(e[2], e[3]);
+          }
+        }
+        // --------------------------------------------------------------- O += P V
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
           // lo/hi: the even/odd codes of this lane's units for the key pairs
@@ -928,32 +966,39 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           }
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            // Channels 32 g + 4 r + {0, 1} (first tile) and + {2, 3} (second).
-            const uint32_t l0 = lo[0][g / 2], h0 = hi[0][g / 2];
-            const uint32_t l1 = lo[1][g / 2], h1 = hi[1][g / 2];
-            uint32_t a[2][4];
-            if (g % 2 == 0) {
-              a[0][0] = e2m1x2_to_f16x2<0>(l0), a[0][1] = e2m1x2_to_f16x2<0>(h0);
-              a[0][2] = e2m1x2_to_f16x2<0>(l1), a[0][3] = e2m1x2_to_f16x2<0>(h1);
-              a[1][0] = e2m1x2_to_f16x2<1>(l0), a[1][1] = e2m1x2_to_f16x2<1>(h0);
-              a[1][2] = e2m1x2_to_f16x2<1>(l1), a[1][3] = e2m1x2_to_f16x2<1>(h1);
-            } else {
-              a[0][0] = e2m1x2_to_f16x2<2>(l0), a[0][1] = e2m1x2_to_f16x2<2>(h0);
-              a[0][2] = e2m1x2_to_f16x2<2>(l1), a[0][3] = e2m1x2_to_f16x2<2>(h1);
-              a[1][0] = e2m1x2_to_f16x2<3>(l0), a[1][1] = e2m1x2_to_f16x2<3>(h0);
-              a[1][2] = e2m1x2_to_f16x2<3>(l1), a[1][3] = e2m1x2_to_f16x2<3>(h1);
-            }
+            // v[i][h]: channel 32 g + 4 r + i of the keys 2t, 2t+1 (+ 8 h).
+            uint32_t v[4][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint32_t b0 = mul_f16x2(pf[mt][nt][0], fac[0][g]);
-              const uint32_t b1 = mul_f16x2(pf[mt][nt][1], fac[1][g]);
-              mma16816(o[nt][2 * g], a[0][0], a[0][1], a[0][2], a[0][3], b0, b1);
-              mma16816(o[nt][2 * g + 1], a[1][0], a[1][1], a[1][2], a[1][3], b0, b1);
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t wl = lo[h][g / 2], wh = hi[h][g / 2];
+              if (g % 2 == 0) {
+                v[0][h] = e2m1x2_to_f16x2<0>(wl), v[1][h] = e2m1x2_to_f16x2<0>(wh);
+                v[2][h] = e2m1x2_to_f16x2<1>(wl), v[3][h] = e2m1x2_to_f16x2<1>(wh);
+              } else {
+                v[0][h] = e2m1x2_to_f16x2<2>(wl), v[1][h] = e2m1x2_to_f16x2<2>(wh);
+                v[2][h] = e2m1x2_to_f16x2<3>(wl), v[3][h] = e2m1x2_to_f16x2<3>(wh);
+              }
+            }
+            if constexpr (NT == 1) {
+              const uint32_t b0 = mul_f16x2(pf[mt][0], fac[0][g]);
+              const uint32_t b1 = mul_f16x2(pf[mt][1], fac[1][g]);
+              mma16816(o[2 * g], v[0][0], v[1][0], v[0][1], v[1][1], b0, b1);
+              mma16816(o[2 * g + 1], v[2][0], v[3][0], v[2][1], v[3][1], b0, b1);
+            } else {
+              const uint32_t a0 = mul_f16x2(pf[mt][0], fac[0][g]);
+              const uint32_t a1 = mul_f16x2(pf[mt][1], fac[0][g]);
+              const uint32_t a2 = mul_f16x2(pf[mt][2], fac[1][g]);
+              const uint32_t a3 = mul_f16x2(pf[mt][3], fac[1][g]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                mma16816(o[4 * g + i], a0, a1, a2, a3, v[i][0], v[i][1]);
             }
           }
         }
       }
     }
+    if (NT == 2 && !kSel)  // the key scales written above make way for a copy
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     const uint2 c = fetch(s, tile + kStages * kWarps);
 #pragma unroll
@@ -974,25 +1019,32 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   float* so = reinterpret_cast<float*>(smem);              // [warp][row][D]
   float* sml = so + kWarps * kRows * D;                    // [warp][row][2]
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int i = 0; i < 2; ++i) {
+    float sum = l[i];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float x = l[nt][i];
-      x += __shfl_xor_sync(0xffffffffu, x, 4);
-      x += __shfl_xor_sync(0xffffffffu, x, 8);
-      x += __shfl_xor_sync(0xffffffffu, x, 16);
-      const int row = nt * 8 + 2 * t + i;
-      if (r == 0) {
-        sml[(warp * kRows + row) * 2] = thr[nt][i] == -INFINITY ? -INFINITY : m[nt][i] * f[nt][i];
-        sml[(warp * kRows + row) * 2 + 1] = x;
-      }
-      float* dst = so + (warp * kRows + row) * D;
-#pragma unroll
-      for (int g = 0; g < G; ++g)
-        *reinterpret_cast<float4*>(dst + 32 * g + 4 * r) =
-            make_float4(o[nt][2 * g][i] * unit, o[nt][2 * g][2 + i] * unit,
-                        o[nt][2 * g + 1][i] * unit, o[nt][2 * g + 1][2 + i] * unit);
+    for (int x = NT == 1 ? 4 : 1; x < (NT == 1 ? 32 : 4); x <<= 1)
+      sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    const int row = row_of(i);
+    if (NT == 1 ? r == 0 : t == 0) {
+      sml[(warp * kRows + row) * 2] = thr[i] == -INFINITY ? -INFINITY : m[i] * f[i];
+      sml[(warp * kRows + row) * 2 + 1] = sum;
     }
+    float* dst = so + (warp * kRows + row) * D;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if constexpr (NT == 1) {
+        *reinterpret_cast<float4*>(dst + 32 * g + 4 * r) =
+            make_float4(o[2 * g][i] * unit, o[2 * g][2 + i] * unit, o[2 * g + 1][i] * unit,
+                        o[2 * g + 1][2 + i] * unit);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)  // columns 2t and 2t + 1 of the four tiles
+          *reinterpret_cast<float4*>(dst + 32 * g + 8 * t + 4 * c) =
+              make_float4(o[4 * g][2 * i + c] * unit, o[4 * g + 1][2 * i + c] * unit,
+                          o[4 * g + 2][2 * i + c] * unit, o[4 * g + 3][2 * i + c] * unit);
+      }
+    }
+  }
   __syncthreads();
   const int64_t part = static_cast<int64_t>(blockIdx.x) * 2 + (span.first ? 0 : 1);
   for (int e = threadIdx.x; e < kRows * D / 4; e += kThreads) {
