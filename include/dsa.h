@@ -465,7 +465,8 @@ dsa_status_t dsa_k_norm_quant_insert(const void* k, const float* ln_weight, cons
  *
  * Shared by the calls below: D is 64 or 128, block_size a power of two in
  * [8, 128] (else DSA_ERR_UNSUPPORTED), cache and scales 16-byte aligned;
- * num_blocks * block_size * Hkv < 2^32.  Slots are block * block_size + row,
+ * num_blocks * block_size * Hkv < 2^32; an insert or gather takes
+ * T * Hkv < 2^30 records (else DSA_ERR_UNSUPPORTED).  Slots are block * block_size + row,
  * as in dsa_k_norm_quant_insert; the index cache and this one can share a
  * block table.  Once a call has run on a device its calls can be captured
  * into a CUDA graph.

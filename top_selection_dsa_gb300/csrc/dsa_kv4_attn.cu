@@ -1825,6 +1825,7 @@ __global__ void __launch_bounds__(256) kv4_weight_kernel(const __grid_constant__
     if (pos < 0 || pos >= gr.limit) pos = -1;
   }
   if (pos >= 0) {
+#pragma unroll 4
     for (int ht = 0; ht < per_split; ++ht) {
       const float4* src = reinterpret_cast<const float4*>(
           p.scores + ((static_cast<int64_t>(grp) * per_split + ht) * p.cols + col) * kRows);

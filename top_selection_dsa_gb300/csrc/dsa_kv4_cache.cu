@@ -11,7 +11,9 @@
 //
 // Both are memory-bound: one lane moves eight elements (16 bytes of bf16), a
 // record takes D/4 lanes (the key's, then the value's), and a lane has
-// kRecords records in flight.
+// kRecords records in flight.  A lane's eight value codes belong to two rows of
+// the record four bytes apart; it exchanges half of them with the lane of the
+// neighbouring block, so that a record is one 4-byte access a lane.
 #include "dsa_internal.h"
 #include "dsa_kv4.cuh"
 
@@ -28,7 +30,7 @@ struct CacheParams {
   uint16_t* k_out;    // gather: [T, Hkv, D], dense
   uint16_t* v_out;
   const int64_t* slots;
-  int64_t items;      // T * Hkv
+  uint32_t items;     // T * Hkv
   int Hkv, log_bs;
   int64_t capacity;
   uint8_t* cache;
@@ -43,35 +45,59 @@ __device__ __forceinline__ int64_t record_of(const CacheParams& p, int64_t slot,
   return ((block * p.Hkv + head) << p.log_bs) + at;
 }
 
+// Where lane `sub` of a record's D/4 lanes keeps its codes.
+template <int D>
+struct Lane {
+  static constexpr int G = D / kMxBlock;
+  bool is_v;
+  int e8, g, t;   // its eight elements 8 e8 .., their block and place in it
+  int word;       // its 4-byte word of the record
+  __device__ explicit Lane(int sub) {
+    is_v = sub >= D / 8;
+    e8 = sub % (D / 8);
+    g = e8 / 4, t = e8 % 4;
+    // Value: units 2t (even blocks) or 2t + 1 (odd) of its block and the
+    // neighbouring one.
+    word = is_v ? D / 8 + ((2 * t + g % 2) * G + (g & ~1)) / 2 : t * G + g;
+  }
+  // A lane's eight codes <-> the word it accesses (the exchange is its own
+  // inverse; executed by whole warps).
+  __device__ uint32_t exchange(uint32_t w) const {
+    const bool odd = g % 2;
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w : w >> 16, 4);
+    const uint32_t mixed = odd ? (got & 0xFFFFu) | (w & 0xFFFF0000u) : (w & 0xFFFFu) | (got << 16);
+    return is_v ? mixed : w;
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads) kv4_insert_kernel(const __grid_constant__ CacheParams p) {
   constexpr int G = D / kMxBlock;
   constexpr int kLanes = D / 4;  // D/8 for the key row, D/8 for the value row
-  constexpr int kPerCta = kThreads / kLanes;
+  constexpr uint32_t kPerCta = kThreads / kLanes;
   const int sub = threadIdx.x % kLanes;
-  const bool is_v = sub >= kLanes / 2;
-  const int e8 = sub % (kLanes / 2);  // this lane's eight elements: 8 e8 ..
-  const int g = e8 / 4, t = e8 % 4;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kPerCta;
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * kPerCta + threadIdx.x / kLanes;
-       base - threadIdx.x / kLanes < p.items; base += step * kRecords) {
+  const Lane<D> lane(sub);
+  const uint16_t* const src = lane.is_v ? p.v : p.k;
+  const int64_t src_stride = lane.is_v ? p.v_stride : p.k_stride;
+  const uint32_t step = gridDim.x * kPerCta;
+  const uint32_t first = blockIdx.x * kPerCta;
+  for (uint32_t base = first; base < p.items; base += step * kRecords) {
     uint4 raw[kRecords];
     int64_t rec[kRecords];
 #pragma unroll
     for (int i = 0; i < kRecords; ++i) {
-      const int64_t item = base + i * step;
+      const uint32_t item = base + threadIdx.x / kLanes + i * step;
       rec[i] = -1;
       raw[i] = make_uint4(0u, 0u, 0u, 0u);
       if (item < p.items) {
-        const int64_t tok = item / p.Hkv;
+        const uint32_t tok = item / static_cast<uint32_t>(p.Hkv);
         const int head = static_cast<int>(item - tok * p.Hkv);
         const int64_t slot = __ldg(p.slots + tok);
+        raw[i] = __ldg(reinterpret_cast<const uint4*>(src + tok * src_stride + head * D) + lane.e8);
         if (slot >= p.capacity) {
           if (sub == 0 && head == 0) record_error(p.err, kErrBadIndex);
         } else if (slot >= 0) {
           rec[i] = record_of(p, slot, head);
-          const uint16_t* src = is_v ? p.v + tok * p.v_stride : p.k + tok * p.k_stride;
-          raw[i] = __ldg(reinterpret_cast<const uint4*>(src + head * D) + e8);
         }
       }
     }
@@ -96,18 +122,11 @@ __global__ void __launch_bounds__(kThreads) kv4_insert_kernel(const __grid_const
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         codes |= f32x2_to_e2m1x2(bf16_lo(w[j]) * inv, bf16_hi(w[j]) * inv) << (8 * j);
-      if (bad) codes = 0;
+      codes = lane.exchange(bad ? 0u : codes);
       if (rec[i] < 0) continue;
-      uint8_t* dst = p.cache + rec[i] * D;
-      if (!is_v) {
-        *reinterpret_cast<uint32_t*>(dst + (t * G + g) * 4) = codes;
-      } else {
-        uint16_t* half = reinterpret_cast<uint16_t*>(dst + D / 2);
-        half[(2 * t) * G + g] = static_cast<uint16_t>(codes);
-        half[(2 * t + 1) * G + g] = static_cast<uint16_t>(codes >> 16);
-      }
-      if (t == 0)
-        p.scales[rec[i] * (D / 16) + (is_v ? G : 0) + g] =
+      *(reinterpret_cast<uint32_t*>(p.cache + rec[i] * D) + lane.word) = codes;
+      if (lane.t == 0)
+        p.scales[rec[i] * (D / 16) + (lane.is_v ? G : 0) + lane.g] =
             bad ? 255 : static_cast<uint8_t>(e + 127);
     }
   }
@@ -117,57 +136,50 @@ template <int D>
 __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const __grid_constant__ CacheParams p) {
   constexpr int G = D / kMxBlock;
   constexpr int kLanes = D / 4;
-  constexpr int kPerCta = kThreads / kLanes;
+  constexpr uint32_t kPerCta = kThreads / kLanes;
   const int sub = threadIdx.x % kLanes;
-  const bool is_v = sub >= kLanes / 2;
-  const int e8 = sub % (kLanes / 2);
-  const int g = e8 / 4, t = e8 % 4;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kPerCta;
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * kPerCta + threadIdx.x / kLanes;
-       base < p.items; base += step * kRecords) {
+  const Lane<D> lane(sub);
+  uint16_t* const out = lane.is_v ? p.v_out : p.k_out;
+  const uint32_t step = gridDim.x * kPerCta;
+  const uint32_t first = blockIdx.x * kPerCta;
+  for (uint32_t base = first; base < p.items; base += step * kRecords) {
     uint32_t codes[kRecords];
     uint32_t sc[kRecords];
 #pragma unroll
     for (int i = 0; i < kRecords; ++i) {
-      const int64_t item = base + i * step;
+      const uint32_t item = base + threadIdx.x / kLanes + i * step;
       codes[i] = 0;
       sc[i] = 127;
       if (item < p.items) {
-        const int64_t tok = item / p.Hkv;
+        const uint32_t tok = item / static_cast<uint32_t>(p.Hkv);
         const int head = static_cast<int>(item - tok * p.Hkv);
         const int64_t slot = __ldg(p.slots + tok);
         if (slot >= p.capacity) {
           if (sub == 0 && head == 0) record_error(p.err, kErrBadIndex);
         } else if (slot >= 0) {
           const int64_t rec = record_of(p, slot, head);
-          const uint8_t* src = p.cache + rec * D;
-          if (!is_v) {
-            codes[i] = *reinterpret_cast<const uint32_t*>(src + (t * G + g) * 4);
-          } else {
-            const uint16_t* half = reinterpret_cast<const uint16_t*>(src + D / 2);
-            codes[i] = half[(2 * t) * G + g] |
-                       (static_cast<uint32_t>(half[(2 * t + 1) * G + g]) << 16);
-          }
-          sc[i] = p.scales[rec * (D / 16) + (is_v ? G : 0) + g];
+          codes[i] = *(reinterpret_cast<const uint32_t*>(p.cache + rec * D) + lane.word);
+          sc[i] = p.scales[rec * (D / 16) + (lane.is_v ? G : 0) + lane.g];
         }
       }
     }
 #pragma unroll
     for (int i = 0; i < kRecords; ++i) {
-      const int64_t item = base + i * step;
-      if (item >= p.items) break;
+      const uint32_t item = base + threadIdx.x / kLanes + i * step;
+      const uint32_t c = lane.exchange(codes[i]);
+      if (item >= p.items) continue;
       const float s = sc[i] == 255 ? __uint_as_float(0x7FC00000u)
                                    : ldexpf(1.f, static_cast<int>(sc[i]) - 127);
-      const uint32_t h[4] = {e2m1x2_to_f16x2<0>(codes[i]), e2m1x2_to_f16x2<1>(codes[i]),
-                             e2m1x2_to_f16x2<2>(codes[i]), e2m1x2_to_f16x2<3>(codes[i])};
+      const uint32_t h[4] = {e2m1x2_to_f16x2<0>(c), e2m1x2_to_f16x2<1>(c), e2m1x2_to_f16x2<2>(c),
+                             e2m1x2_to_f16x2<3>(c)};
       uint32_t o[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
         o[j] = pack_bf16(f.x * s, f.y * s);
       }
-      uint16_t* dst = (is_v ? p.v_out : p.k_out) + item * D;
-      *(reinterpret_cast<uint4*>(dst) + e8) = make_uint4(o[0], o[1], o[2], o[3]);
+      *(reinterpret_cast<uint4*>(out + static_cast<int64_t>(item) * D) + lane.e8) =
+          make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
@@ -197,14 +209,14 @@ cudaError_t launch_kv4_insert(const void* k, int64_t k_stride, const void* v, in
   p.k_stride = k_stride;
   p.v_stride = v_stride;
   p.slots = slots;
-  p.items = static_cast<int64_t>(T) * Hkv;
+  p.items = static_cast<uint32_t>(T) * static_cast<uint32_t>(Hkv);
   p.Hkv = Hkv;
   p.log_bs = log2_of(block_size);
   p.capacity = static_cast<int64_t>(num_blocks) * block_size;
   p.cache = static_cast<uint8_t*>(cache);
   p.scales = static_cast<uint8_t*>(scales);
   p.err = err;
-  if (p.items <= 0) return cudaSuccess;
+  if (p.items == 0) return cudaSuccess;
   if (D == 128)
     kv4_insert_kernel<128><<<cache_grid(p.items, D), kThreads, 0, s>>>(p);
   else
@@ -219,14 +231,14 @@ cudaError_t launch_kv4_gather(const void* cache, const void* scales, const int64
   p.k_out = static_cast<uint16_t*>(k);
   p.v_out = static_cast<uint16_t*>(v);
   p.slots = slots;
-  p.items = static_cast<int64_t>(T) * Hkv;
+  p.items = static_cast<uint32_t>(T) * static_cast<uint32_t>(Hkv);
   p.Hkv = Hkv;
   p.log_bs = log2_of(block_size);
   p.capacity = static_cast<int64_t>(num_blocks) * block_size;
   p.cache = static_cast<uint8_t*>(const_cast<void*>(cache));
   p.scales = static_cast<uint8_t*>(const_cast<void*>(scales));
   p.err = err;
-  if (p.items <= 0) return cudaSuccess;
+  if (p.items == 0) return cudaSuccess;
   if (D == 128)
     kv4_gather_kernel<128><<<cache_grid(p.items, D), kThreads, 0, s>>>(p);
   else

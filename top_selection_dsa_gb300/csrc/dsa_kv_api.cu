@@ -171,6 +171,7 @@ dsa_status_t dsa_kv4_insert(const void* k, int64_t k_stride, const void* v, int6
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slot_mapping, 8) || k_stride % 8 != 0 ||
       v_stride % 8 != 0 || (T > 1 && (k_stride < row || v_stride < row)))
     return DSA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(T) * Hkv >= (int64_t(1) << 30)) return DSA_ERR_UNSUPPORTED;
   if (T == 0) return DSA_OK;
   uint32_t* err = error_word();
   if (!err) return DSA_ERR_CUDA;
@@ -186,6 +187,7 @@ dsa_status_t dsa_kv4_gather(const void* cache, const uint8_t* scales, int num_bl
   dsa_status_t st = check_cache(cache, scales, num_blocks, block_size, Hkv, D);
   if (st != DSA_OK) return st;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8)) return DSA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(T) * Hkv >= (int64_t(1) << 30)) return DSA_ERR_UNSUPPORTED;
   if (T == 0) return DSA_OK;
   uint32_t* err = error_word();
   if (!err) return DSA_ERR_CUDA;
