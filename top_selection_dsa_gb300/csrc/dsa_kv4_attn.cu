@@ -1163,6 +1163,28 @@ __device__ __forceinline__ float unorder_f32(uint32_t u) {
   return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
 }
 
+// mbar_wait_bounded for waits that are long as a rule: every try suspends the
+// thread for up to a microsecond, so that a waiting warp takes no issue slots.
+__device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity,
+                                               volatile uint32_t* abort,
+                                               uint64_t timeout_ns = kWaitTimeoutNs) {
+  uint64_t t0 = 0;
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000u)
+        : "memory");
+    if (ok) return true;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if ((abort && *abort) || now - t0 > timeout_ns) return false;
+  }
+}
+
 // Barrier of the four warps of one kind, with an OR of their votes.
 __device__ __forceinline__ bool kind_barrier_or(int id, bool vote) {
   uint32_t r;
@@ -1332,7 +1354,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
   {
     constexpr int kPer = D / 16;
     const int sub = tid % kPer;
-#pragma unroll 1
+#pragma unroll 2
     for (int n = tid / kPer; n < N; n += kTcThreads / kPer) {  // whole warps
       uint4 raw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
       if (row0 + n < nrows) {
@@ -1368,7 +1390,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
       }
       if (sub == 0) {
         row_f[n] = zero ? 1.f : ldexpf(fabsf(p.scale_log2e), E);
-        fz[n] = make_float2(0.f, kUnseen);
+        fz[n] = make_float2(1.f, kUnseen);
         limit[n] = kSel ? gr.cols
                         : gr.L - p.next_n + min((row0 + n) / p.heads, p.next_n - 1) + 1;
         nan_rows[n] = 0;
@@ -1402,7 +1424,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
       __syncthreads();
       valid = here[0];
     } else {
-      if (!mbar_wait_bounded(&full[s], (done / kTcStages) & 1, abort_flag)) fail = true;
+      if (!mbar_wait_long(&full[s], (done / kTcStages) & 1, abort_flag)) fail = true;
       valid = col < c1;
     }
     const uint32_t base = sb + Lay::kTiles + s * Lay::kTileBytes;
@@ -1519,17 +1541,31 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
       }
       __syncwarp();
       // P's buffer is free once the last tile's products are done.
-      if (tile > 0 && !mbar_wait_bounded(o_done, (done - 1) & 1, abort_flag)) fail = true;
+      if (tile > 0 && !mbar_wait_long(o_done, (done - 1) & 1, abort_flag)) fail = true;
     } else {
-      if (tile > 0 && !mbar_wait_bounded(o_done, (done - 1) & 1, abort_flag)) fail = true;
+      if (tile > 0 && !mbar_wait_long(o_done, (done - 1) & 1, abort_flag)) fail = true;
       again = passes;
       put_values();
     }
-    if (!mbar_wait_bounded(s_done, done & 1, abort_flag)) fail = true;
+    if (!mbar_wait_long(s_done, done & 1, abort_flag)) fail = true;
     tc_fence_after_sync();
     // ---------------------------------------------------------------- softmax
     const bool clean = c0 + (tile + 1) * kTcTile <= min(c1, all_see) && (!kSel || valid);
-    const bool dirty = __any_sync(0xffffffffu, !clean);
+    if (__any_sync(0xffffffffu, !clean)) {
+      // Columns that are not there, or that a row does not see: -inf, written
+      // back (their weight is zero whatever the reference).
+#pragma unroll 1
+      for (int c = 0; c < kHalf; c += 8) {
+        float x[8];
+        tmem_load8(lanes + Lay::kTmemS + n0 + c, x);
+        uint32_t r[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          r[j] = !valid || (!kSel && col >= limit[n0 + c + j]) ? 0xFF800000u : __float_as_uint(x[j]);
+        tmem_store8(lanes + Lay::kTmemS + n0 + c, r);
+      }
+      tmem_wait_st();
+    }
     float pr[kHalf];
     // Once, but for the rare cases below, which need one round more.
     for (int round = 0;; ++round) {
@@ -1538,19 +1574,10 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
       for (int c = 0; c < kHalf; c += 8) {
         float x[8];
         tmem_load8(lanes + Lay::kTmemS + n0 + c, x);
-        if (dirty) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (!valid || (!kSel && col >= limit[n0 + c + j])) x[j] = -INFINITY;
-        }
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
           const float4 f = *reinterpret_cast<const float4*>(&fz[n0 + c + j]);
-          float e0 = (x[j] - f.y) * f.x, e1 = (x[j + 1] - f.w) * f.z;
-          if (dirty) {  // no reference makes an absent column's weight other than zero
-            if (x[j] == -INFINITY) e0 = -INFINITY;
-            if (x[j + 1] == -INFINITY) e1 = -INFINITY;
-          }
+          const float e0 = (x[j] - f.y) * f.x, e1 = (x[j + 1] - f.w) * f.z;
           mx = fmaxf(mx, fmaxf(e0, e1));
           pr[c + j] = ex2(e0), pr[c + j + 1] = ex2(e1);
         }
@@ -1590,8 +1617,8 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int n = n0 + c + j;
-          float v = valid && (kSel || col < limit[n]) ? x[j] : -INFINITY;
-          if (!(v == v)) v = -INFINITY;  // a NaN stays one without a reference
+          // A NaN stays one without a reference.
+          const float v = x[j] == x[j] ? x[j] : -INFINITY;
           const uint32_t w = __reduce_max_sync(0xffffffffu, order_f32(v));
           if (lane == 0) part[(warp & 3) * N + n] = w;
         }
@@ -1635,7 +1662,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
         tmem_load8(lanes + Lay::kTmemS + n0 + c, v);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          v[j] = valid && (kSel || col < limit[n0 + c + j]) ? v[j] * fz[n0 + c + j].x : -INFINITY;
+          v[j] *= fz[n0 + c + j].x;
         if (col < c1) {
           *reinterpret_cast<float4*>(dst + c) = make_float4(v[0], v[1], v[2], v[3]);
           *reinterpret_cast<float4*>(dst + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
@@ -1664,16 +1691,16 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
     here[kTcStages - 1] = h;
   }
   if (ok && tiles > 0) {
-    if (!mbar_wait_bounded(o_done, (done - 1) & 1, abort_flag)) ok = false;
+    if (!mbar_wait_long(o_done, (done - 1) & 1, abort_flag)) ok = false;
   } else if (!ok) {
     // A copy or a product never came: report, and give what is in flight its
     // time.
     if (tid == 0) record_error(p.err, kErrTimeout);
     if (!kSel)
       for (int i = 0; i < kTcStages; ++i)
-        mbar_wait_bounded(&full[(done + i) % kTcStages], ((done + i) / kTcStages) & 1, nullptr);
-    mbar_wait_bounded(s_done, done & 1, nullptr, 1000000);
-    mbar_wait_bounded(o_done, done & 1, nullptr, 1000000);
+        mbar_wait_long(&full[(done + i) % kTcStages], ((done + i) / kTcStages) & 1, nullptr);
+    mbar_wait_long(s_done, done & 1, nullptr, 1000000);
+    mbar_wait_long(o_done, done & 1, nullptr, 1000000);
   }
   cp_async_wait<0>();
   tc_fence_after_sync();
@@ -1698,13 +1725,26 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
     }
     tc_fence_before_sync();
     float* const lp = reinterpret_cast<float*>(part);
+    // Sums over the warp's lanes: halves of the rows change sides until a lane
+    // has one row (or lanes share it).
 #pragma unroll
-    for (int n = 0; n < kHalf; ++n) {
-      float v = l[n];
+    for (int x = 1, w = kHalf / 2; x < 32; x <<= 1, w >>= 1) {
+      if (w > 0) {
+        const bool high = lane & x;
 #pragma unroll
-      for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
-      if (lane == 0) lp[(warp & 3) * N + n0 + n] = v;
+        for (int n = 0; n < w; ++n) {
+          const float give = high ? l[n] : l[n + w], keep = high ? l[n + w] : l[n];
+          l[n] = keep + __shfl_xor_sync(0xffffffffu, give, x);
+        }
+      } else {
+        l[0] += __shfl_xor_sync(0xffffffffu, l[0], x);
+      }
     }
+    // Lane bit b chose between halves of width kHalf >> (b + 1).
+    int mine = 0;
+#pragma unroll
+    for (int x = 1, w = kHalf / 2; w > 0; x <<= 1, w >>= 1) mine += lane & x ? w : 0;
+    if (lane < kHalf) lp[(warp & 3) * N + n0 + mine] = l[0];
   }
   __syncthreads();
   const int64_t pt = static_cast<int64_t>(blockIdx.x) * 2 + (span.first ? 0 : 1);
@@ -1893,10 +1933,11 @@ cudaError_t launch_rows(const Kv4AttnParams& p, cudaStream_t s) {
                TcLayout<D, kRows>::kBytes);
   }
   if (e == cudaSuccess && p.spans) {
+    const bool many = p.ctas >= static_cast<int64_t>(p.groups) * p.Hkv * p.row_tiles * kJoinMany;
+    const unsigned grid = static_cast<unsigned>(p.ctas) * (many ? kRows : kRows / 8);
     // Launched while the attention kernel still runs (it waits inside).
     cudaLaunchConfig_t cfg = {};
-    const bool many = p.ctas >= static_cast<int64_t>(p.groups) * p.Hkv * p.row_tiles * kJoinMany;
-    cfg.gridDim = dim3(static_cast<unsigned>(p.ctas) * (many ? kRows : kRows / 8));
+    cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(256)
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 8;  // rows a thread holds per chunk
 constexpr int kSlice = 128;     // bytes of a row one CTA moves in place
-constexpr int kPartRows = 64;   // rows a CTA moves to fresh pages
+constexpr int kPartRows = 32;   // rows a CTA moves to fresh pages
 
 // To fresh pages: a CTA takes kPartRows rows of a request in every cache.
 // Their slots are looked up once; after that the copies are independent of one
@@ -74,36 +74,49 @@ template <typename V>
 __device__ __forceinline__ void copy_rows(const CompactParams& p, const CompactParams::Cache& c,
                                           const int2* slots, int n) {
   const int vecs = c.row_bytes / static_cast<int>(sizeof(V));  // of a row
-  const int per_plane = n * vecs;
-  const int total = per_plane * c.planes;
+  const int lanes = min(vecs, kMoveThreads);
+  const int sub = threadIdx.x % lanes, step = kMoveThreads / lanes;
+  if (static_cast<int>(threadIdx.x) >= lanes * step) return;
   const int mask = (1 << p.log_bs) - 1;
-  auto row_of = [&](int slot, int plane) {
-    return ((static_cast<int64_t>(slot >> p.log_bs) * c.planes + plane) << p.log_bs) +
-           (slot & mask);
+  auto at = [&](int slot, int plane, int v) {
+    const int64_t row = ((static_cast<int64_t>(slot >> p.log_bs) * c.planes + plane) << p.log_bs) +
+                        (slot & mask);
+    return reinterpret_cast<V*>(c.base + row * c.row_bytes) + v;
   };
-  for (int base = threadIdx.x; base < total; base += kMoveThreads * kMoveUnroll) {
-    V buf[kMoveUnroll];
-    uint8_t* dst[kMoveUnroll];
+  for (int v = sub; v < vecs; v += lanes) {
+    // Rows of all planes in one sequence, `step` apart.
+    int plane = 0, row = threadIdx.x / lanes;
+    auto settle = [&]() {
+      while (row >= n) row -= n, ++plane;
+    };
+    settle();
+    while (plane < c.planes) {
+      V buf[kMoveUnroll];
+      uint32_t has = 0;
+      int pl = plane, rw = row;
 #pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) {
-      const int e = base + u * kMoveThreads;
-      dst[u] = nullptr;
-      if (e >= total) continue;
-      const int plane = e / per_plane, in = e - plane * per_plane;
-      const int row = in / vecs, v = in - row * vecs;
-      const int2 s = slots[row];
-      if (s.x < 0) continue;
-      const int64_t at = static_cast<int64_t>(v) * sizeof(V);
-      buf[u] = __ldg(reinterpret_cast<const V*>(c.base + row_of(s.x, plane) * c.row_bytes + at));
-      dst[u] = c.base + row_of(s.y, plane) * c.row_bytes + at;
+      for (int u = 0; u < kMoveUnroll; ++u) {
+        if (plane < c.planes) {
+          const int2 s = slots[row];
+          if (s.x >= 0) {
+            buf[u] = __ldg(at(s.x, plane, v));
+            has |= 1u << u;
+          }
+        }
+        row += step;
+        settle();
+      }
+#pragma unroll
+      for (int u = 0; u < kMoveUnroll; ++u) {
+        if ((has >> u) & 1) *at(slots[rw].y, pl, v) = buf[u];
+        rw += step;
+        while (rw >= n) rw -= n, ++pl;
+      }
     }
-#pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u)
-      if (dst[u]) *reinterpret_cast<V*>(dst[u]) = buf[u];
   }
 }
 
-__global__ void __launch_bounds__(kMoveThreads)
+__global__ void __launch_bounds__(kMoveThreads, 4)
     kv_move_kernel(const __grid_constant__ CompactParams p) {
   __shared__ int2 slots[kPartRows];  // source and destination, or (-1, .)
   const int b = blockIdx.y, part = blockIdx.x;
