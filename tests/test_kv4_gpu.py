@@ -555,3 +555,38 @@ def test_a_decode_step_in_a_graph(api):
         eager = step()
         for x, y in zip(got, [t for pair in eager for t in pair] + [acc]):
             assert torch.equal(x, y)
+
+
+# ------------------------------------------- sizes on either side of a variant
+
+
+@pytest.mark.parametrize("B,ctx", [(2, 32768), (2, 32769), (40, 33000), (1, 131072)])
+def test_evict_select_on_either_side_of_the_one_kernel_path(api, B, ctx):
+    rng = np.random.default_rng(ctx)
+    lens = [ctx] + [int(x) for x in rng.integers(1, ctx, size=B - 1)]
+    w = np.exp(3 * rng.standard_normal((B, ctx))).astype(np.float32)
+    w[:, ::7] = 0.0
+    w[0, 100:5000] = 1.0                        # thousands of ties across the bound
+    w[:, 11] = -0.0
+    budget, sink, recent = 3000, 4, 100
+    keep, n = api.kv_evict_select(dev(w), dev(np.array(lens, np.int32)), budget, sink=sink,
+                                  recent=recent)
+    for b, L in enumerate(lens):
+        want = ref.evict(w[b], L, budget, sink, recent)
+        assert int(n[b]) == len(want)
+        assert keep[b].tolist() == want + [-1] * (budget - len(want))
+
+
+@pytest.mark.parametrize("values", ["equal", "two", "zero", "negative"])
+@pytest.mark.parametrize("room", [0, 1, 31, 500])
+def test_evict_select_few_distinct_weights(api, values, room):
+    L = 1500
+    w = np.full((1, L), {"equal": 2.5, "two": 1.0, "zero": 0.0, "negative": -3.0}[values],
+                np.float32)
+    if values == "two":
+        w[0, 700:730] = 9.0
+    if values == "negative":
+        w[0, 3::5] = -1.0
+    keep, n = api.kv_evict_select(dev(w), dev(np.array([L], np.int32)), room + 7, sink=3, recent=4)
+    want = ref.evict(w[0], L, room + 7, 3, 4)
+    assert n.tolist() == [len(want)] and keep[0].tolist() == want

@@ -263,6 +263,9 @@ dsa_status_t dsa_kv_evict_select(const float* key_weights, int64_t ldw,
   cudaStream_t st = as_stream(stream);
   uint32_t* err = error_word();
   if (!err) return DSA_ERR_CUDA;
+  if (evict_small(max_ctx))
+    return from_cuda(launch_evict_small(key_weights, ldw, context_lens, B, max_ctx, budget, sink,
+                                        recent, keep, new_lens, err, st));
   cudaError_t e =
       launch_evict_ranges(context_lens, B, max_ctx, sink, recent, starts, ends, err, st);
   if (e == cudaSuccess && room > 0) {
