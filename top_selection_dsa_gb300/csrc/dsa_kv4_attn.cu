@@ -51,7 +51,7 @@ constexpr int kStages = 2;
 constexpr int kCtasPerSm = 3;   // registers (168 a thread) and shared memory
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+  asm volatile("{.reg .b64 pol;\n\tcreatepolicy.fractional.L2::evict_first.b64 pol, 1.0;\n\tcp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, pol;}" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
 template <int kBytes>

@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4)
   }
   n = min(n, p.new_max_blocks << p.log_bs);
   const int rows = min(n - i0, kPartRows);
-  if (rows <= 0) return;
+  if (rows <= 0 || p.ncaches == 0) return;
   if (threadIdx.x < rows) {
     const int i = i0 + threadIdx.x;
     const int pos = __ldg(keep + i);
