@@ -32,17 +32,35 @@ struct CacheParams {
   const int64_t* slots;
   uint32_t items;     // T * Hkv
   int Hkv, log_bs;
+  uint32_t div_mul;   // item / Hkv = (item * div_mul) >> div_shift, for items < 2^30
+  int div_shift;
   int64_t capacity;
   uint8_t* cache;
   uint8_t* scales;
   uint32_t* err;
 };
 
-// Record number of (slot, head): ((slot / bs) * Hkv + head) * bs + slot % bs.
-__device__ __forceinline__ int64_t record_of(const CacheParams& p, int64_t slot, int head) {
-  const int64_t block = slot >> p.log_bs;
-  const int64_t at = slot & ((int64_t(1) << p.log_bs) - 1);
-  return ((block * p.Hkv + head) << p.log_bs) + at;
+__device__ __forceinline__ uint32_t token_of(const CacheParams& p, uint32_t item) {
+  return static_cast<uint32_t>((static_cast<uint64_t>(item) * p.div_mul) >> p.div_shift);
+}
+
+// Record number of (slot, head), a slot of the cache: ((slot / bs) * Hkv +
+// head) * bs + slot % bs, below 2^32 as all record numbers are.
+__device__ __forceinline__ uint32_t record_of(const CacheParams& p, uint32_t slot, uint32_t head) {
+  const uint32_t block = slot >> p.log_bs;
+  return ((block * p.Hkv + head) << p.log_bs) + (slot & ((1u << p.log_bs) - 1u));
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // Where lane `sub` of a record's D/4 lanes keeps its codes.
@@ -83,21 +101,22 @@ __global__ void __launch_bounds__(kThreads) kv4_insert_kernel(const __grid_const
   const uint32_t first = blockIdx.x * kPerCta;
   for (uint32_t base = first; base < p.items; base += step * kRecords) {
     uint4 raw[kRecords];
-    int64_t rec[kRecords];
+    uint32_t rec[kRecords], ok = 0;
 #pragma unroll
     for (int i = 0; i < kRecords; ++i) {
       const uint32_t item = base + threadIdx.x / kLanes + i * step;
-      rec[i] = -1;
+      rec[i] = 0;
       raw[i] = make_uint4(0u, 0u, 0u, 0u);
       if (item < p.items) {
-        const uint32_t tok = item / static_cast<uint32_t>(p.Hkv);
-        const int head = static_cast<int>(item - tok * p.Hkv);
+        const uint32_t tok = token_of(p, item);
+        const uint32_t head = item - tok * p.Hkv;
         const int64_t slot = __ldg(p.slots + tok);
         raw[i] = __ldg(reinterpret_cast<const uint4*>(src + tok * src_stride + head * D) + lane.e8);
         if (slot >= p.capacity) {
           if (sub == 0 && head == 0) record_error(p.err, kErrBadIndex);
         } else if (slot >= 0) {
-          rec[i] = record_of(p, slot, head);
+          rec[i] = record_of(p, static_cast<uint32_t>(slot), head);
+          ok |= 1u << i;
         }
       }
     }
@@ -106,27 +125,30 @@ __global__ void __launch_bounds__(kThreads) kv4_insert_kernel(const __grid_const
       const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
       // The largest magnitude as bits: a NaN's or an infinity's are above
       // every finite value's, so one integer maximum finds either.
-      uint32_t amax = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        amax = max(amax, max((w[j] << 16) & 0x7FFF0000u, w[j] & 0x7FFF0000u));
-      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      uint32_t mag = max_u16x2(max_u16x2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                               max_u16x2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+      mag = max_u16x2(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
+      mag = max_u16x2(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
+      const uint32_t amax = max(mag & 0xFFFFu, mag >> 16);  // bf16 bits
       // 6 * 2^e = 1.5 * 2^(e+2): compare the mantissa with 1.5.
-      const int E = static_cast<int>(amax >> 23);
-      int e = E - 127 - 2 + ((amax & 0x7FFFFFu) > 0x400000u ? 1 : 0);
-      e = amax == 0 ? 0 : (e < -126 ? -126 : e);
-      const bool bad = amax >= 0x7F800000u;
-      const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      int e = static_cast<int>(amax >> 7) - 127 - 2 + ((amax & 0x7Fu) > 0x40u ? 1 : 0);
+      e = amax == 0 ? 0 : max(e, -126);
+      const bool bad = amax >= 0x7F80u;
+      // x / 2^e: exact where it matters (what it rounds, below 2^-126, is
+      // far below half of the smallest code).
+      const uint32_t inv = static_cast<uint32_t>(127 - e) << 7;
       uint32_t codes = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        codes |= f32x2_to_e2m1x2(bf16_lo(w[j]) * inv, bf16_hi(w[j]) * inv) << (8 * j);
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t y = mul_bf16x2(w[j], inv | (inv << 16));
+        codes |= f32x2_to_e2m1x2(bf16_lo(y), bf16_hi(y)) << (8 * j);
+      }
       codes = lane.exchange(bad ? 0u : codes);
-      if (rec[i] < 0) continue;
-      *(reinterpret_cast<uint32_t*>(p.cache + rec[i] * D) + lane.word) = codes;
+      if (!((ok >> i) & 1)) continue;
+      *(reinterpret_cast<uint32_t*>(p.cache + static_cast<uint64_t>(rec[i]) * D) + lane.word) =
+          codes;
       if (lane.t == 0)
-        p.scales[rec[i] * (D / 16) + (lane.is_v ? G : 0) + lane.g] =
+        p.scales[static_cast<uint64_t>(rec[i]) * (D / 16) + (lane.is_v ? G : 0) + lane.g] =
             bad ? 255 : static_cast<uint8_t>(e + 127);
     }
   }
@@ -151,13 +173,13 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const __grid_const
       codes[i] = 0;
       sc[i] = 127;
       if (item < p.items) {
-        const uint32_t tok = item / static_cast<uint32_t>(p.Hkv);
-        const int head = static_cast<int>(item - tok * p.Hkv);
+        const uint32_t tok = token_of(p, item);
+        const uint32_t head = item - tok * p.Hkv;
         const int64_t slot = __ldg(p.slots + tok);
         if (slot >= p.capacity) {
           if (sub == 0 && head == 0) record_error(p.err, kErrBadIndex);
         } else if (slot >= 0) {
-          const int64_t rec = record_of(p, slot, head);
+          const uint64_t rec = record_of(p, static_cast<uint32_t>(slot), head);
           codes[i] = *(reinterpret_cast<const uint32_t*>(p.cache + rec * D) + lane.word);
           sc[i] = p.scales[rec * (D / 16) + (lane.is_v ? G : 0) + lane.g];
         }
@@ -168,8 +190,7 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const __grid_const
       const uint32_t item = base + threadIdx.x / kLanes + i * step;
       const uint32_t c = lane.exchange(codes[i]);
       if (item >= p.items) continue;
-      const float s = sc[i] == 255 ? __uint_as_float(0x7FC00000u)
-                                   : ldexpf(1.f, static_cast<int>(sc[i]) - 127);
+      const float s = __uint_as_float(sc[i] == 255 ? 0x7FC00000u : sc[i] << 23);
       const uint32_t h[4] = {e2m1x2_to_f16x2<0>(c), e2m1x2_to_f16x2<1>(c), e2m1x2_to_f16x2<2>(c),
                              e2m1x2_to_f16x2<3>(c)};
       uint32_t o[4];
@@ -197,6 +218,15 @@ int log2_of(int x) {
   return l;
 }
 
+// Division by Hkv of numbers below 2^30, by a multiplication: with l the
+// exponent of the power of two at or above Hkv, floor(2^(30+l) / Hkv) + 1 is
+// close enough to 2^(30+l) / Hkv.
+void set_division(CacheParams* p) {
+  const int l = log2_of(p->Hkv);
+  p->div_shift = 30 + l;
+  p->div_mul = static_cast<uint32_t>((uint64_t(1) << (30 + l)) / p->Hkv + 1);
+}
+
 }  // namespace
 
 cudaError_t launch_kv4_insert(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
@@ -211,6 +241,7 @@ cudaError_t launch_kv4_insert(const void* k, int64_t k_stride, const void* v, in
   p.slots = slots;
   p.items = static_cast<uint32_t>(T) * static_cast<uint32_t>(Hkv);
   p.Hkv = Hkv;
+  set_division(&p);
   p.log_bs = log2_of(block_size);
   p.capacity = static_cast<int64_t>(num_blocks) * block_size;
   p.cache = static_cast<uint8_t*>(cache);
@@ -233,6 +264,7 @@ cudaError_t launch_kv4_gather(const void* cache, const void* scales, const int64
   p.slots = slots;
   p.items = static_cast<uint32_t>(T) * static_cast<uint32_t>(Hkv);
   p.Hkv = Hkv;
+  set_division(&p);
   p.log_bs = log2_of(block_size);
   p.capacity = static_cast<int64_t>(num_blocks) * block_size;
   p.cache = static_cast<uint8_t*>(const_cast<void*>(cache));
