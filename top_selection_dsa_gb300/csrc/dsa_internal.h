@@ -159,7 +159,8 @@ struct Kv4AttnParams {
   float* part_o;           // [ctas, 2, rows, D]: partial results
   float* part_ml;          // [ctas, 2, rows, 2]
   int4* spans;             // [ctas]: what to join, or null when nothing can be split
-  float* scores;           // [groups, Hkv*row_tiles, cols, rows]: base-2 logits, for the weights
+  float* scores;           // [groups, Hkv*row_tiles, cols, score_rows]: base-2 logits, for the
+  int score_rows;          // weights
   float* lse2;             // [groups, Hkv*row_tiles, rows]
   float* sel_weights;      // [B*next_n, sel_k] or null
   float* key_weights;      // [B, ldw] or null
@@ -169,7 +170,7 @@ struct Kv4AttnParams {
 // How a call is cut up, and the byte offsets of its workspace.
 struct Kv4AttnPlan {
   int64_t groups;
-  int heads, rows, row_tiles, tile, unit, ctas;  // rows of a CTA; columns of a tile, of a unit
+  int heads, rows, score_rows, row_tiles, tile, unit, ctas;  // rows of a CTA; columns of a tile, of a unit
   bool split;
   int64_t part_o, part_ml, spans, scores, lse2, sel_weights, bytes;
 };

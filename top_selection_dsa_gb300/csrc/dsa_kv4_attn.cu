@@ -875,14 +875,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             }
         }
         if constexpr (kScores) {
-          float* dst = p.scores + (static_cast<int64_t>(grp) * per_split + ht) * p.cols * kRows;
+          float* dst =
+              p.scores + (static_cast<int64_t>(grp) * per_split + ht) * p.cols * p.score_rows;
 #pragma unroll
           for (int x = 0; x < 2 * NT; ++x)
 #pragma unroll
             for (int j = 0; j < 4; j += NT == 1 ? 2 : 1) {
               const int col = col0 + half * 32 + key_of(x, j);
-              if (col < c1) {
-                float* at = dst + static_cast<int64_t>(col) * kRows + row_of(row_ix(j));
+              if (col < c1 && row_of(row_ix(j)) < p.score_rows) {
+                float* at = dst + static_cast<int64_t>(col) * p.score_rows + row_of(row_ix(j));
                 if constexpr (NT == 1)
                   *reinterpret_cast<float2*>(at) =
                       make_float2(sacc[x][j] * f[0], sacc[x][j + 1] * f[1]);
@@ -1654,8 +1655,8 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
     }
     if (!ok) break;
     if constexpr (kScores) {
-      float* dst = p.scores +
-                   ((static_cast<int64_t>(grp) * per_split + ht) * p.cols + col) * N + n0;
+      float* dst =
+          p.scores + ((static_cast<int64_t>(grp) * per_split + ht) * p.cols + col) * p.score_rows;
 #pragma unroll 1
       for (int c = 0; c < kHalf; c += 8) {
         float v[8];
@@ -1663,10 +1664,11 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           v[j] *= fz[n0 + c + j].x;
-        if (col < c1) {
-          *reinterpret_cast<float4*>(dst + c) = make_float4(v[0], v[1], v[2], v[3]);
-          *reinterpret_cast<float4*>(dst + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
-        }
+        const int n = n0 + c;
+        if (col < c1 && n < p.score_rows)
+          *reinterpret_cast<float4*>(dst + n) = make_float4(v[0], v[1], v[2], v[3]);
+        if (col < c1 && n + 4 < p.score_rows)
+          *reinterpret_cast<float4*>(dst + n + 4) = make_float4(v[4], v[5], v[6], v[7]);
         __syncwarp();
       }
     }
@@ -1868,10 +1870,11 @@ __global__ void __launch_bounds__(256) kv4_weight_kernel(const __grid_constant__
 #pragma unroll 4
     for (int ht = 0; ht < per_split; ++ht) {
       const float4* src = reinterpret_cast<const float4*>(
-          p.scores + ((static_cast<int64_t>(grp) * per_split + ht) * p.cols + col) * kRows);
+          p.scores + ((static_cast<int64_t>(grp) * per_split + ht) * p.cols + col) * p.score_rows);
       const float4* z = reinterpret_cast<const float4*>(lse_s + ht * kRows);
 #pragma unroll
       for (int i = 0; i < kRows / 4; ++i) {
+        if (4 * i >= p.score_rows) break;
         const float4 x = __ldg(src + i), y = z[i];
         w += ex2(x.x - y.x) + ex2(x.y - y.y) + ex2(x.z - y.z) + ex2(x.w - y.w);
       }
@@ -2009,7 +2012,9 @@ Kv4AttnPlan kv4_attn_plan(int B, int next_n, int Hq, int Hkv, int D, int64_t col
   pl.part_o = take(parts * D * 4);
   pl.part_ml = take(parts * 8);
   pl.spans = take(pl.split ? static_cast<int64_t>(pl.ctas) * 16 : 0);
-  pl.scores = take(weights ? lanes * cols * pl.rows * 4 : 0);
+  // Logits kept for the weights: of the rows there are, by fours.
+  pl.score_rows = pl.row_tiles > 1 ? pl.rows : (rows + 3) / 4 * 4;
+  pl.scores = take(weights ? lanes * cols * pl.score_rows * 4 : 0);
   pl.lse2 = take(weights ? lanes * pl.rows * 4 : 0);
   pl.sel_weights = take(weights && selected && next_n > 1 ? pl.groups * cols * 4 : 0);
   pl.bytes = off;

@@ -117,6 +117,7 @@ dsa_status_t run_attention(const AttnArgs& a, bool selected, dsa_stream_t stream
   p.part_ml = reinterpret_cast<float*>(ws + pl.part_ml);
   p.spans = pl.split ? reinterpret_cast<int4*>(ws + pl.spans) : nullptr;
   p.scores = reinterpret_cast<float*>(ws + pl.scores);
+  p.score_rows = pl.score_rows;
   p.lse2 = reinterpret_cast<float*>(ws + pl.lse2);
   // Several tokens a request: the scatter reads the rows' weights, so they
   // are written out even when the caller does not ask for them.
