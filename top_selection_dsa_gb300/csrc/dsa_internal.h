@@ -158,7 +158,8 @@ struct Kv4AttnParams {
   float* lse;              // [B*next_n, Hq] or null
   float* part_o;           // [ctas, 2, rows, D]: partial results
   float* part_ml;          // [ctas, 2, rows, 2]
-  int4* spans;             // [ctas]: what to join, or null when nothing can be split
+  int4* spans;             // [groups, Hkv*row_tiles]: what to join, or null when nothing can be
+                           // split
   float* scores;           // [groups, Hkv*row_tiles, cols, score_rows]: base-2 logits, for the
   int score_rows;          // weights
   float* lse2;             // [groups, Hkv*row_tiles, rows]

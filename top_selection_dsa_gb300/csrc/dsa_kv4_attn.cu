@@ -300,10 +300,9 @@ struct Walk {
     t = blockIdx.x * each + min(blockIdx.x, more);
     t1 = t + each + (blockIdx.x < more ? 1 : 0);
   }
-  // Thread 0: the next span; the one it begins and does not end is noted for
-  // the join: .x group; .y head and row tile; .z the last CTA of the span; .w
-  // which of this CTA's two partial results it is (the others' are their
-  // first).
+  // Thread 0: the next span.  Where its group, head and row tile begin is noted
+  // for the join: .x this CTA; .y how many CTAs share them; .z which of this
+  // CTA's two partial results is theirs (the others' are their first).
   __device__ __forceinline__ void next(const Kv4AttnParams& p) {
     if (t >= t1) {
       span.g = -1;
@@ -319,8 +318,9 @@ struct Walk {
     s.first = first;
     first = false;
     t += s.u1 - s.u0;
-    if (s.u0 == 0 && s.u1 < s.units)
-      p.spans[blockIdx.x] = make_int4(s.g, s.ht, cta_of(t + s.units - s.u1 - 1), s.first ? 0 : 1);
+    if (s.u0 == 0 && p.spans)
+      p.spans[static_cast<int64_t>(s.g) * p.Hkv * p.row_tiles + s.ht] =
+          make_int4(blockIdx.x, cta_of(t + s.units - s.u1 - 1) - blockIdx.x + 1, s.first ? 0 : 1, 0);
     if (s.u1 == s.units && s.ht == p.Hkv * p.row_tiles - 1) {
       ++g;
       base = t;
@@ -338,10 +338,7 @@ struct Walk {
 template <class W>
 __device__ __forceinline__ void begin_walk(W* walk, const Kv4AttnParams& p) {
   const W w(p);
-  if (threadIdx.x == 0) {
-    *walk = w;
-    if (p.spans) p.spans[blockIdx.x] = make_int4(-1, 0, 0, 0);
-  }
+  if (threadIdx.x == 0) *walk = w;
 }
 
 __device__ __forceinline__ void launch_dependents() {
@@ -1773,15 +1770,15 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
   }
 }
 
-// Joins the partial results of the spans that CTAs share: for every CTA of the
-// attention kernel (which had to begin the span) one CTA per kPer rows.  First
-// a row's largest reference and sum, then its channels, four a lane, all
-// results' loads independent of one another.  A row is one warp's (kPer = 8),
-// or eight warps take every eighth result of it (kPer = 1): that is for spans
-// over so many CTAs that a warp's loads in a row would take longer than the
-// launch of seven more CTAs (one row of 131071 columns, 57 results: 10 -> 6 us).
+// Joins the partial results of a group, head and row tile that CTAs share: one
+// CTA per kPer rows of each.  First a row's largest reference and sum, then its
+// channels, four a lane, all results' loads independent of one another.  A row
+// is one warp's (kPer = 8), or eight warps take every eighth result of it
+// (kPer = 1): that is for so many results a row that one warp would wait for
+// its loads several times over (a request of 131071 columns, 57 results: 10 ->
+// 6 us).
 constexpr int kJoinThreads = 256;
-constexpr int kJoinMany = 16;  // results of a span from which on
+constexpr int kJoinMany = 16;  // results a row, on average, from which on
 
 template <int D, int kRows, int kPer, bool kSel, bool kScores>
 __global__ void __launch_bounds__(kJoinThreads)
@@ -1789,17 +1786,18 @@ __global__ void __launch_bounds__(kJoinThreads)
   __shared__ float4 sums[kPer == 1 ? 8 : 1][D / 4];
   grid_dependency_wait();
   constexpr int kSets = kRows / kPer;
-  const int cta = blockIdx.x / kSets;
+  const int item = blockIdx.x / kSets, per_split = p.Hkv * p.row_tiles;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = kPer == 1 ? blockIdx.x % kSets : (blockIdx.x % kSets) * 8 + warp;
-  const int4 sp = p.spans[cta];
-  if (sp.x < 0) return;
-  const int grp = sp.x, ht = sp.y, n = sp.z - cta + 1;
+  const int4 sp = p.spans[item];
+  const int cta = sp.x, n = sp.y;
+  if (n <= 1) return;  // written by the CTA that had all of it
+  const int grp = item / per_split, ht = item % per_split;
   const int row0 = (ht % p.row_tiles) * kRows;
   const int nrows = kSel ? p.heads : p.heads * p.next_n;
   if (!kScores && row0 + row >= nrows) return;
   auto part_of = [&](int i) {
-    return (static_cast<int64_t>(cta + i) * 2 + (i == 0 ? sp.w : 0)) * kRows + row;
+    return (static_cast<int64_t>(cta + i) * 2 + (i == 0 ? sp.z : 0)) * kRows + row;
   };
   auto ml_of = [&](int i) { return *reinterpret_cast<const float2*>(p.part_ml + part_of(i) * 2); };
   float M = -INFINITY;
@@ -1936,8 +1934,9 @@ cudaError_t launch_rows(const Kv4AttnParams& p, cudaStream_t s) {
                TcLayout<D, kRows>::kBytes);
   }
   if (e == cudaSuccess && p.spans) {
-    const bool many = p.ctas >= static_cast<int64_t>(p.groups) * p.Hkv * p.row_tiles * kJoinMany;
-    const unsigned grid = static_cast<unsigned>(p.ctas) * (many ? kRows : kRows / 8);
+    const int64_t items = static_cast<int64_t>(p.groups) * p.Hkv * p.row_tiles;
+    const bool many = p.ctas >= items * kJoinMany;
+    const unsigned grid = static_cast<unsigned>(items * (many ? kRows : kRows / 8));
     // Launched while the attention kernel still runs (it waits inside).
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
@@ -2011,7 +2010,7 @@ Kv4AttnPlan kv4_attn_plan(int B, int next_n, int Hq, int Hkv, int D, int64_t col
   const int64_t parts = pl.split ? static_cast<int64_t>(pl.ctas) * 2 * pl.rows : 0;
   pl.part_o = take(parts * D * 4);
   pl.part_ml = take(parts * 8);
-  pl.spans = take(pl.split ? static_cast<int64_t>(pl.ctas) * 16 : 0);
+  pl.spans = take(pl.split ? lanes * 16 : 0);
   // Logits kept for the weights: of the rows there are, by fours.
   pl.score_rows = pl.row_tiles > 1 ? pl.rows : (rows + 3) / 4 * 4;
   pl.scores = take(weights ? lanes * cols * pl.score_rows * 4 : 0);
