@@ -439,6 +439,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   const int c0 = span.u0 * (kTile * kWarps);
   const int c1 = min(gr.cols, span.u1 * (kTile * kWarps));
 
+  // The query rows: one row tile's every warp reads, and before the tiles'
+  // copies, behind which it would wait; two tiles' warps 0 and 1 read, later
+  // (their other warps' registers are not theirs to fill).
+  const bool has_q = NT == 1 || warp < NT;
+  const int q_row = row0 + (NT == 1 ? 0 : warp * 8) + r;
+  uint4 raw[G];
+  auto read_queries = [&]() {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      raw[g] = make_uint4(0u, 0u, 0u, 0u);
+      if (q_row < nrows)
+        raw[g] = __ldg(reinterpret_cast<const uint4*>(
+            p.q + head_row<kSel>(p, grp, head, q_row) * D + g * 32 + t * 8));
+    }
+  };
+  if (NT == 1) read_queries();
+
   // ------------------------------------------------------------------ loads
   // Tiles of this warp: columns c0 + 64 (warp + 4 i), in stage i % kStages.
   const int tiles = (c1 - c0 + kTile - 1) / kTile;
@@ -457,31 +474,36 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   // i-th run of `rows` tokens.  Selected: a lane has the columns `lane` and
   // `lane + 32`, their positions read one tile before their pages.
   const int rows = min(1 << p.log_bs, kTile);
-  int pos[2] = {-1, -1}, next_pos[2] = {-1, -1}, block[2] = {0, 0};
-  auto read_columns = [&](int tile) {  // selected: this lane's positions of `tile`
+  constexpr int kMine = kSel ? 2 : 1;  // columns (runs) of a tile a lane looks after
+  int pos[kMine], next_pos[kMine], block[kMine];
+  auto read_columns = [&](int tile, int (&to)[kMine]) {  // selected: positions of `tile`
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kMine; ++i) {
       const int col = c0 + tile * kTile + lane + 32 * i;
-      next_pos[i] = col < c1 ? __ldg(p.sel + static_cast<int64_t>(grp) * p.sel_k + col) : -1;
+      to[i] = col < c1 ? __ldg(p.sel + static_cast<int64_t>(grp) * p.sel_k + col) : -1;
+    }
+  };
+  auto read_pages = [&](int tile, int (&at)[kMine], int (&page)[kMine]) {
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      if constexpr (kSel) {
+        if (at[i] < -1 || at[i] >= gr.limit) {
+          record_error(p.err, kErrBadIndex);
+          at[i] = -1;
+        }
+      } else {
+        at[i] = c0 + tile * kTile + lane * rows;
+        if (lane * rows >= kTile || at[i] >= c1) at[i] = -1;
+      }
+      page[i] = at[i] >= 0 ? __ldg(table + (at[i] >> p.log_bs)) : 0;
     }
   };
   auto locate = [&](int tile) {
-    if constexpr (kSel) {
+    if constexpr (kSel)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        pos[i] = next_pos[i];
-        if (pos[i] < -1 || pos[i] >= gr.limit) {
-          record_error(p.err, kErrBadIndex);
-          pos[i] = -1;
-        }
-        if (pos[i] >= 0) block[i] = __ldg(table + (pos[i] >> p.log_bs));
-      }
-      read_columns(tile + kWarps);
-    } else {
-      pos[0] = c0 + tile * kTile + lane * rows;
-      if (lane * rows >= kTile || pos[0] >= c1) pos[0] = -1;
-      else block[0] = __ldg(table + (pos[0] >> p.log_bs));
-    }
+      for (int i = 0; i < kMine; ++i) pos[i] = next_pos[i];
+    read_pages(tile, pos, block);
+    if constexpr (kSel) read_columns(tile + kWarps, next_pos);
   };
   // Starts the copies of the located tile into stage s; returns which columns
   // of a selected tile there are (.x: columns 0 .. 31).
@@ -533,11 +555,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   };
 
   uint2 cols[kStages];  // oldest first
-  if (kSel) read_columns(warp);
+  {
+    // The first tiles' positions, and their pages, read at once.
+    int at[kStages][kMine], page[kStages][kMine];
+    if constexpr (kSel) {
 #pragma unroll
-  for (int i = 0; i < kStages; ++i) {
-    locate(warp + i * kWarps);
-    cols[i] = fetch((s + i) % kStages, warp + i * kWarps);
+      for (int i = 0; i < kStages; ++i) read_columns(warp + i * kWarps, at[i]);
+      read_columns(warp + kStages * kWarps, next_pos);
+    }
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) read_pages(warp + i * kWarps, at[i], page[i]);
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) {
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) pos[j] = at[i][j], block[j] = page[i][j];
+      cols[i] = fetch((s + i) % kStages, warp + i * kWarps);
+    }
   }
 
   // ---------------------------------------------------------------- queries
@@ -557,17 +590,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
              : gr.L - p.next_n +
                    min((row0 + static_cast<int>(threadIdx.x)) / p.heads, p.next_n - 1) + 1;
   float* const f_s = reinterpret_cast<float*>(smem + Lay::kFactorF);
-  if (NT == 1 || warp < NT) {
+  if (has_q) {
+    if (NT > 1) read_queries();
     const int nt = NT == 1 ? 0 : warp;
-    const int n = row0 + nt * 8 + r;
-    uint4 raw[G];
     uint32_t amax = 0;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      raw[g] = make_uint4(0u, 0u, 0u, 0u);
-      if (n < nrows)
-        raw[g] = __ldg(reinterpret_cast<const uint4*>(
-            p.q + head_row<kSel>(p, grp, head, n) * D + g * 32 + t * 8));
       const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
