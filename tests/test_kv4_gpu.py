@@ -200,6 +200,13 @@ SHAPES = [  # lens, next_n, Hq, Hkv, D, block
     ([1300], 1, 4, 1, 128, 64),                # several chunks
     ([2100, 700, 5], 2, 8, 2, 64, 64),
     ([513, 300], 5, 24, 2, 128, 8),            # 60 rows
+    ([300, 77], 2, 16, 2, 64, 16),             # 16 rows, D = 64
+    ([300, 1], 1, 24, 1, 64, 32),              # 24 rows, D = 64
+    ([520, 3], 2, 32, 1, 64, 64),              # 64 rows, D = 64
+    ([200, 129], 2, 96, 2, 128, 64),           # 96 rows: two tiles of 64
+    ([6000, 40], 1, 40, 1, 128, 64),           # 40 rows over many CTAs
+    ([300] * 40, 1, 2, 1, 64, 16),             # more requests than a warp has lanes
+    ([1000, 0, 2, 4000], 3, 11, 1, 128, 32),   # 33 rows, some of which see nothing
 ]
 
 
@@ -590,3 +597,49 @@ def test_evict_select_few_distinct_weights(api, values, room):
     keep, n = api.kv_evict_select(dev(w), dev(np.array([L], np.int32)), room + 7, sink=3, recent=4)
     want = ref.evict(w[0], L, room + 7, 3, 4)
     assert n.tolist() == [len(want)] and keep[0].tolist() == want
+
+
+@pytest.mark.parametrize("Hq", [4, 16, 24])
+@pytest.mark.parametrize("scale", [0.0, -0.04])
+def test_zero_and_negative_softmax_scale(api, Hq, scale):
+    P = Problem([150], 1, Hq, 1, 128, 64, seed=21)
+    out, lse = api.kv4_attention(*P.gpu(), next_n=1, softmax_scale=scale)
+    K, V = P.kv(0)
+    want = ref.attention(P.q[0], K, V, scale, 150)
+    check(out[0].double().cpu().numpy(), lse[0].double().cpu().numpy(), want, V, scale)
+
+
+@pytest.mark.parametrize("Hq", [4, 16, 24])
+@pytest.mark.parametrize("scale", [1e4, 1e8, 1e12])
+def test_huge_logits_pick_the_largest(api, Hq, scale):
+    """Logits far apart: the output is one value row, nothing overflows."""
+    P = Problem([150], 1, Hq, 1, 128, 64, seed=22, spread=0)
+    out, lse = api.kv4_attention(*P.gpu(), next_n=1, softmax_scale=scale)
+    K, V = P.kv(0)
+    S = np.einsum("hd,ld->hl", P.q[0], K[:, 0])
+    best = S.argmax(1)
+    second = np.sort(S, 1)[:, -2]
+    # the row is alone where the gap is far above the logits' rounding (2^-19 of
+    # sum |q||k|) and above 20 in the exponent
+    B = (np.abs(P.q[0]) @ np.abs(K[:, 0]).T).max(1)
+    alone = (S.max(1) - second > 2.0 ** -17 * B) & ((S.max(1) - second) * scale > 20)
+    assert alone.sum() >= 1
+    assert torch.isfinite(out.float()).all() and torch.isfinite(lse).all()
+    got = out[0].double().cpu().numpy()
+    for h in np.nonzero(alone)[0]:
+        assert np.abs(got[h] - V[best[h], 0]).max() <= 2.0 ** -8 * np.abs(V[best[h], 0]).max()
+
+
+@pytest.mark.parametrize("Hq", [4, 16, 24])
+def test_infinite_and_nan_queries_stay_in_their_rows(api, Hq):
+    P = Problem([100], 1, Hq, 1, 128, 64, seed=23)
+    q, rec, sc, table, cl = P.gpu()
+    q[0, 1, 5] = float("nan")
+    q[0, 3, 9] = float("inf")
+    out, lse = api.kv4_attention(q, rec, sc, table, cl, next_n=1, softmax_scale=P.scale)
+    assert torch.isnan(out[0, 1].float()).all() and torch.isnan(lse[0, 1])
+    K, V = P.kv(0)
+    want = ref.attention(P.q[0], K, V, P.scale, 100)
+    keep = [h for h in range(Hq) if h not in (1, 3)]
+    check(out[0, keep].double().cpu().numpy(), lse[0, keep].double().cpu().numpy(),
+          (want[0][keep], want[1][keep], want[2], (want[3][0][keep], want[3][1][keep])), V, "rows")
