@@ -205,11 +205,11 @@ constexpr int kCopyUnroll = 4;  // copies a thread has in flight there
 
 // To fresh pages: a CTA takes kPartRows rows of a request in every cache.
 // Where they are is looked up once; after that the copies are independent of
-// one another and cost two additions of an address each. Four of 16 bytes in
-// flight a thread and six CTAs an SM: 185 us for 32 requests of 8192 rows in
-// three caches (748 MB read and written, 4.0 TB/s); eight in flight and four
-// CTAs 205 us, and with the rows' numbers turned into addresses copy by copy
-// 225 us.
+// one another and cost two additions of an address each.  Bound by the
+// latency of reading single rows.  Selection and move of 64 requests that keep
+// 4096 positions each, 8 heads of 128 and an indexer's keys: 185 us, 4.0 TB/s
+// (four copies in flight a thread, six CTAs an SM); eight and four 205 us, and
+// with the rows' numbers turned into addresses copy by copy 225 us.
 struct RowMove {
   const uint8_t* from;  // in plane 0; null: not moved
   uint8_t* to;
@@ -288,8 +288,9 @@ __global__ void __launch_bounds__(kMoveThreads, 6)
       }
       __syncthreads();
       const int parts = alone ? 1 : static_cast<int>(gridDim.x);
-      const int share = (cap - kept + parts - 1) / parts;
-      const int z0 = kept + share * part, z1 = min(cap, z0 + share);
+      const int64_t share = (cap - kept + parts - 1) / parts;
+      const int z0 = static_cast<int>(min(static_cast<int64_t>(cap), kept + share * part));
+      const int z1 = static_cast<int>(min(static_cast<int64_t>(cap), z0 + share));
       for (int i = z0 + threadIdx.x; i < z1; i += kMoveThreads) out[i] = 0.f;
     }
   }
