@@ -9,11 +9,16 @@
 // NaN.  Reading back is exact in bf16 (two significant bits times a power of
 // two).
 //
-// Both are memory-bound: one lane moves eight elements (16 bytes of bf16), a
-// record takes D/4 lanes (the key's, then the value's), and a lane has
-// kRecords records in flight.  A lane's eight value codes belong to two rows of
-// the record four bytes apart; it exchanges half of them with the lane of the
-// neighbouring block, so that a record is one 4-byte access a lane.
+// A lane moves sixteen elements: the same eighth-of-32 of two neighbouring scale
+// blocks (two 16-byte pieces of bf16).  Their key codes are 8 contiguous bytes
+// of the record; their value codes are two units in each of two rows of units
+// (with two blocks a record these are contiguous; with four, the lanes of the
+// two pairs exchange half of them).  A record takes D/8 lanes (the key's, then
+// the value's), and a lane has kRecords records in flight.
+// Memory-bound next to its instructions: 65536 tokens of 8 heads of 128 written
+// and read back in 69 us, 5.0 TB/s (two records in flight; four 73 us; and one
+// 16-byte piece a lane, which pays for addresses, maxima and exchanges twice as
+// often, 90 us).
 #include "dsa_internal.h"
 #include "dsa_kv4.cuh"
 
@@ -21,7 +26,7 @@ namespace dsa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRecords = 4;
+constexpr int kRecords = 2;
 
 struct CacheParams {
   const uint16_t* k;  // insert: [T, Hkv, D], rows k_stride / v_stride elements apart
@@ -63,35 +68,47 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Where lane `sub` of a record's D/4 lanes keeps its codes.
+// Where lane `sub` of a record's D/8 lanes keeps its codes.
 template <int D>
 struct Lane {
   static constexpr int G = D / kMxBlock;
   bool is_v;
-  int e8, g, t;   // its eight elements 8 e8 .., their block and place in it
-  int word;       // its 4-byte word of the record
+  int g, t;   // its blocks, g and g + 1, and place in them
+  int word;   // its two 4-byte words of the record: the first
   __device__ explicit Lane(int sub) {
-    is_v = sub >= D / 8;
-    e8 = sub % (D / 8);
-    g = e8 / 4, t = e8 % 4;
-    // Value: units 2t (even blocks) or 2t + 1 (odd) of its block and the
-    // neighbouring one.
-    word = is_v ? D / 8 + ((2 * t + g % 2) * G + (g & ~1)) / 2 : t * G + g;
+    is_v = sub >= D / 16;
+    g = 2 * (sub % (D / 16) / 4), t = sub % 4;
+    // Value: rows 2t and 2t + 1 of units, G/2 words each; with four blocks the
+    // first pair's lane keeps the one and the second's the other.
+    word = !is_v ? t * G + g : D / 8 + (G == 2 ? 2 * t : 4 * t + g);
   }
-  // A lane's eight codes <-> the word it accesses (the exchange is its own
-  // inverse; executed by whole warps).
-  __device__ uint32_t exchange(uint32_t w) const {
-    const bool odd = g % 2;
-    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w : w >> 16, 4);
-    const uint32_t mixed = odd ? (got & 0xFFFFu) | (w & 0xFFFF0000u) : (w & 0xFFFFu) | (got << 16);
-    return is_v ? mixed : w;
+  __device__ int e16(int b) const { return 4 * (g + b) + t; }  // its 16-byte pieces of a row
+  // Codes of its eight elements of either block -> the words it stores (whole
+  // warps).
+  __device__ uint2 pack(uint2 c) const {
+    const uint2 v = make_uint2(__byte_perm(c.x, c.y, 0x5410), __byte_perm(c.x, c.y, 0x7632));
+    const uint2 x = G == 4 ? swap(v) : v;
+    return is_v ? x : c;
+  }
+  // The words it loaded -> codes of its elements (whole warps).
+  __device__ uint2 unpack(uint2 w) const {
+    uint2 v = G == 4 ? swap(w) : w;
+    v = make_uint2(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632));
+    return is_v ? v : w;
+  }
+
+ private:
+  // Of a 2 x 2 block of words in two lanes, the transpose.
+  __device__ uint2 swap(uint2 v) const {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, g ? v.x : v.y, 4);
+    return g ? make_uint2(got, v.y) : make_uint2(v.x, got);
   }
 };
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) kv4_insert_kernel(const __grid_constant__ CacheParams p) {
   constexpr int G = D / kMxBlock;
-  constexpr int kLanes = D / 4;  // D/8 for the key row, D/8 for the value row
+  constexpr int kLanes = D / 8;  // D/16 for the key row, D/16 for the value row
   constexpr uint32_t kPerCta = kThreads / kLanes;
   const int sub = threadIdx.x % kLanes;
   const Lane<D> lane(sub);
@@ -100,18 +117,20 @@ __global__ void __launch_bounds__(kThreads) kv4_insert_kernel(const __grid_const
   const uint32_t step = gridDim.x * kPerCta;
   const uint32_t first = blockIdx.x * kPerCta;
   for (uint32_t base = first; base < p.items; base += step * kRecords) {
-    uint4 raw[kRecords];
+    uint4 raw[kRecords][2];
     uint32_t rec[kRecords], ok = 0;
 #pragma unroll
     for (int i = 0; i < kRecords; ++i) {
       const uint32_t item = base + threadIdx.x / kLanes + i * step;
       rec[i] = 0;
-      raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      raw[i][0] = raw[i][1] = make_uint4(0u, 0u, 0u, 0u);
       if (item < p.items) {
         const uint32_t tok = token_of(p, item);
         const uint32_t head = item - tok * p.Hkv;
         const int64_t slot = __ldg(p.slots + tok);
-        raw[i] = __ldg(reinterpret_cast<const uint4*>(src + tok * src_stride + head * D) + lane.e8);
+        const uint4* row = reinterpret_cast<const uint4*>(src + tok * src_stride + head * D);
+        raw[i][0] = __ldg(row + lane.e16(0));
+        raw[i][1] = __ldg(row + lane.e16(1));
         if (slot >= p.capacity) {
           if (sub == 0 && head == 0) record_error(p.err, kErrBadIndex);
         } else if (slot >= 0) {
@@ -122,34 +141,48 @@ __global__ void __launch_bounds__(kThreads) kv4_insert_kernel(const __grid_const
     }
 #pragma unroll
     for (int i = 0; i < kRecords; ++i) {
-      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-      // The largest magnitude as bits: a NaN's or an infinity's are above
-      // every finite value's, so one integer maximum finds either.
-      uint32_t mag = max_u16x2(max_u16x2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
-                               max_u16x2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+      // The largest magnitudes as bits: a NaN's or an infinity's are above
+      // every finite value's, so one integer maximum finds either.  The two
+      // blocks' share a word.
+      uint32_t m[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const uint4 w = raw[i][b];
+        m[b] = max_u16x2(max_u16x2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                         max_u16x2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+      }
+      uint32_t mag = max_u16x2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
       mag = max_u16x2(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
       mag = max_u16x2(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
-      const uint32_t amax = max(mag & 0xFFFFu, mag >> 16);  // bf16 bits
-      // 6 * 2^e = 1.5 * 2^(e+2): compare the mantissa with 1.5.
-      int e = static_cast<int>(amax >> 7) - 127 - 2 + ((amax & 0x7Fu) > 0x40u ? 1 : 0);
-      e = amax == 0 ? 0 : max(e, -126);
-      const bool bad = amax >= 0x7F80u;
-      // x / 2^e: exact where it matters (what it rounds, below 2^-126, is
-      // far below half of the smallest code).
-      const uint32_t inv = static_cast<uint32_t>(127 - e) << 7;
-      uint32_t codes = 0;
+      uint32_t codes[2], scale[2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t y = mul_bf16x2(w[j], inv | (inv << 16));
-        codes |= f32x2_to_e2m1x2(bf16_lo(y), bf16_hi(y)) << (8 * j);
+      for (int b = 0; b < 2; ++b) {
+        const uint32_t w[4] = {raw[i][b].x, raw[i][b].y, raw[i][b].z, raw[i][b].w};
+        const uint32_t amax = b == 0 ? mag & 0xFFFFu : mag >> 16;  // bf16 bits
+        // 6 * 2^e = 1.5 * 2^(e+2): biased, the exponent of amax less two, and
+        // one more for a mantissa above 1.5 (whose addition carries).
+        int e = static_cast<int>((amax + 0x3Fu) >> 7) - 2;
+        e = amax == 0 ? 127 : max(e, 1);
+        const bool bad = amax >= 0x7F80u;
+        // x / 2^(e - 127): exact where it matters (what it rounds, below
+        // 2^-126, is far below half of the smallest code).
+        const uint32_t inv = static_cast<uint32_t>(254 - e) * 0x00800080u;
+        uint32_t c = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t y = mul_bf16x2(w[j], inv);
+          c |= f32x2_to_e2m1x2(bf16_lo(y), bf16_hi(y)) << (8 * j);
+        }
+        codes[b] = bad ? 0u : c;
+        scale[b] = bad ? 255u : static_cast<uint32_t>(e);
       }
-      codes = lane.exchange(bad ? 0u : codes);
+      const uint2 out = lane.pack(make_uint2(codes[0], codes[1]));
       if (!((ok >> i) & 1)) continue;
-      *(reinterpret_cast<uint32_t*>(p.cache + static_cast<uint64_t>(rec[i]) * D) + lane.word) =
-          codes;
+      *reinterpret_cast<uint2*>(p.cache + static_cast<uint64_t>(rec[i]) * D + lane.word * 4) = out;
       if (lane.t == 0)
-        p.scales[static_cast<uint64_t>(rec[i]) * (D / 16) + (lane.is_v ? G : 0) + lane.g] =
-            bad ? 255 : static_cast<uint8_t>(e + 127);
+        *reinterpret_cast<uint16_t*>(p.scales + static_cast<uint64_t>(rec[i]) * (D / 16) +
+                                     (lane.is_v ? G : 0) + lane.g) =
+            static_cast<uint16_t>(scale[0] | (scale[1] << 8));
     }
   }
 }
@@ -157,7 +190,7 @@ __global__ void __launch_bounds__(kThreads) kv4_insert_kernel(const __grid_const
 template <int D>
 __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const __grid_constant__ CacheParams p) {
   constexpr int G = D / kMxBlock;
-  constexpr int kLanes = D / 4;
+  constexpr int kLanes = D / 8;
   constexpr uint32_t kPerCta = kThreads / kLanes;
   const int sub = threadIdx.x % kLanes;
   const Lane<D> lane(sub);
@@ -165,13 +198,13 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const __grid_const
   const uint32_t step = gridDim.x * kPerCta;
   const uint32_t first = blockIdx.x * kPerCta;
   for (uint32_t base = first; base < p.items; base += step * kRecords) {
-    uint32_t codes[kRecords];
+    uint2 codes[kRecords];
     uint32_t sc[kRecords];
 #pragma unroll
     for (int i = 0; i < kRecords; ++i) {
       const uint32_t item = base + threadIdx.x / kLanes + i * step;
-      codes[i] = 0;
-      sc[i] = 127;
+      codes[i] = make_uint2(0u, 0u);
+      sc[i] = 0x7F7Fu;
       if (item < p.items) {
         const uint32_t tok = token_of(p, item);
         const uint32_t head = item - tok * p.Hkv;
@@ -180,33 +213,39 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const __grid_const
           if (sub == 0 && head == 0) record_error(p.err, kErrBadIndex);
         } else if (slot >= 0) {
           const uint64_t rec = record_of(p, static_cast<uint32_t>(slot), head);
-          codes[i] = *(reinterpret_cast<const uint32_t*>(p.cache + rec * D) + lane.word);
-          sc[i] = p.scales[rec * (D / 16) + (lane.is_v ? G : 0) + lane.g];
+          codes[i] = *reinterpret_cast<const uint2*>(p.cache + rec * D + lane.word * 4);
+          sc[i] = *reinterpret_cast<const uint16_t*>(p.scales + rec * (D / 16) +
+                                                     (lane.is_v ? G : 0) + lane.g);
         }
       }
     }
 #pragma unroll
     for (int i = 0; i < kRecords; ++i) {
       const uint32_t item = base + threadIdx.x / kLanes + i * step;
-      const uint32_t c = lane.exchange(codes[i]);
+      const uint2 both = lane.unpack(codes[i]);
       if (item >= p.items) continue;
-      const float s = __uint_as_float(sc[i] == 255 ? 0x7FC00000u : sc[i] << 23);
-      const uint32_t h[4] = {e2m1x2_to_f16x2<0>(c), e2m1x2_to_f16x2<1>(c), e2m1x2_to_f16x2<2>(c),
-                             e2m1x2_to_f16x2<3>(c)};
-      uint32_t o[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-        o[j] = pack_bf16(f.x * s, f.y * s);
+      for (int b = 0; b < 2; ++b) {
+        const uint32_t c = b == 0 ? both.x : both.y;
+        const uint32_t e = b == 0 ? sc[i] & 0xFFu : sc[i] >> 8;
+        const float s = __uint_as_float(e == 255 ? 0x7FC00000u : e << 23);
+        const uint32_t h[4] = {e2m1x2_to_f16x2<0>(c), e2m1x2_to_f16x2<1>(c),
+                               e2m1x2_to_f16x2<2>(c), e2m1x2_to_f16x2<3>(c)};
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+          o[j] = pack_bf16(f.x * s, f.y * s);
+        }
+        *(reinterpret_cast<uint4*>(out + static_cast<int64_t>(item) * D) + lane.e16(b)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
       }
-      *(reinterpret_cast<uint4*>(out + static_cast<int64_t>(item) * D) + lane.e8) =
-          make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
 
 int cache_grid(int64_t items, int D) {
-  const int64_t per = static_cast<int64_t>(kThreads / (D / 4)) * kRecords;
+  const int64_t per = static_cast<int64_t>(kThreads / (D / 8)) * kRecords;
   const int64_t need = (items + per - 1) / per;
   const int64_t cap = static_cast<int64_t>(device_sm_count() > 0 ? device_sm_count() : 1) * 16;
   return static_cast<int>(need < cap ? need : cap);
