@@ -567,6 +567,22 @@ def test_a_decode_step_in_a_graph(api):
 # ------------------------------------------- sizes on either side of a variant
 
 
+@pytest.mark.parametrize("B", [152, 153, 400])
+def test_evict_select_of_more_requests_than_sms(api, B):
+    rng = np.random.default_rng(B)
+    ctx, budget, sink, recent = 900, 200, 4, 30
+    lens = [0, 1, 200, 201, ctx] + [int(x) for x in rng.integers(1, ctx, size=B - 5)]
+    w = np.exp(3 * rng.standard_normal((B, ctx))).astype(np.float32)
+    w[:, ::7] = 0.0
+    keep, n = api.kv_evict_select(dev(w), dev(np.array(lens, np.int32)), budget, sink=sink,
+                                  recent=recent)
+    keep = keep.cpu().numpy()
+    for b, L in enumerate(lens):
+        want = ref.evict(w[b], L, budget, sink, recent)
+        assert int(n[b]) == len(want)
+        assert keep[b].tolist() == want + [-1] * (budget - len(want))
+
+
 @pytest.mark.parametrize("B,ctx", [(2, 32768), (2, 32769), (40, 33000), (1, 131072)])
 def test_evict_select_on_either_side_of_the_one_kernel_path(api, B, ctx):
     rng = np.random.default_rng(ctx)

@@ -181,7 +181,7 @@ cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int D, int rows, bool s
                                  cudaStream_t s);
 
 // Eviction (dsa_kv_evict.cu).
-bool evict_small(int max_ctx);  // one kernel, no workspace
+bool evict_small(int B, int max_ctx);  // one kernel, no workspace
 cudaError_t launch_evict_small(const float* weights, int64_t ldw, const int32_t* lens, int B,
                                int max_ctx, int budget, int sink, int recent, int32_t* keep,
                                int32_t* new_lens, uint32_t* err, cudaStream_t s);

@@ -5,24 +5,44 @@
 //   S[n,c] = scale * q[n] . K[c]       for the columns c that row n sees
 //   lse[n] = log sum_c exp S[n,c]      out[n] = sum_c exp(S[n,c] - lse[n]) V[c]
 //
-// One warp walks tiles of 64 columns of one key/value head for up to 16 query
-// rows (the rows of the head's group, all tokens of the request): cp.async
-// brings the tile's records and scales into the warp's own two-stage ring,
-// and everything after that stays in registers.
-//   S^T = K q^T   mma m16n8k16 with the keys as the 16-row operand: its fp16
-//                 elements are the E2M1 codes' values themselves (exact); the
-//                 four blocks of 32 elements accumulate apart and are summed
-//                 in fp32 with their power-of-two scales.  q is divided by a
-//                 power of two per row so that its largest element is in
-//                 [1, 2): bf16's eight bits fit fp16 exactly, and elements
-//                 below 2^-24 of the row's largest vanish.
-//   softmax       one pass: running maximum m and sum l per row (base 2, in
-//                 fp32), the accumulated output rescaled when m rises.
-//   O^T += V^T P  keys as the contraction: V's elements again the codes'
-//                 values, one 16-row tile per half block of channels, and the
-//                 value scales multiplied into P (fp16) once per block of 32
-//                 channels, relative to the largest scale met so far, 2^x:
-//                 P 2^(e - x) <= 1, and terms below 2^-24 of that vanish.
+// The query rows of a key/value head (its group's heads, of all tokens of the
+// request, or of one token on a selection) share one reading of its records;
+// two kernels take them:
+//
+// Up to 16 rows: kv4_attn_kernel.  One warp walks tiles of 64 columns: TMA
+// (dense) or cp.async (selected) brings the tile's records and scales into the
+// warp's own two-stage ring, and everything after that stays in registers.
+//   S     mma m16n8k16.  Up to 8 rows the keys are the 16-row operand, S^T =
+//         K q^T; from 9 on the query rows are, S = q K^T, with q's fragments
+//         in shared memory.  The keys' fp16 elements are the E2M1 codes'
+//         values themselves (exact); the blocks of 32 elements accumulate
+//         apart and are summed in fp32 with their power-of-two scales.  q is
+//         divided by a power of two per row so that its largest element is in
+//         [1, 2): bf16's eight bits fit fp16 exactly, and elements below 2^-24
+//         of the row's largest vanish.
+//   softmax  one pass: running maximum m and sum l per row (base 2, in fp32);
+//         m lags by up to a slack, so that the accumulated output is rescaled
+//         seldom.
+//   O     += V^T P (O += P V): V's elements again the codes' values, and the
+//         value scales multiplied into P (fp16) once per block of 32 channels,
+//         relative to the largest scale met so far, 2^x: P 2^(e - x) <= 1, and
+//         terms below 2^-24 of that vanish.
+// More rows: kv4_attn_tc_kernel, the same on the tensor cores' tcgen05 form
+// (further down).
+//
+// Times of one GB300 (copy bandwidth 6.68 TB/s), calls with their joins:
+//   64 requests of 4096 to 131072 keys, 8 key/value heads of 128 (2.55 GB):
+//     8 rows a head    405 us, 6.3 TB/s: bound by memory
+//     16 rows          586 us, 4.4 TB/s: bound by issue and latency (52 % of
+//                      the issue slots, ALU and tensor pipes 45 % each, three
+//                      warps a scheduler is what the registers leave)
+//   one request of 131071 keys, 8 rows   40 us, 3.5 TB/s: start and join
+//   2048 selected of each of 128 rows    106 us the kernel, 4.2 TB/s of DRAM:
+//     single records of 128 bytes and scales of 8 from all over 2.5 GB (a
+//     plain gather of those took 71 us)
+// Tried and slower: tiles of 32 columns in three stages; 8 warps with 254
+// registers for 16 rows (637 to 716 us); tcgen05 for 16 rows (856); TMA gathers
+// of selected records (103.5 against cp.async's 98.4).
 // Rounding P to fp16 costs 2^-12 of each term (the output's bf16 rounding is
 // 2^-9); l sums the unrounded weights.
 //
@@ -357,7 +377,18 @@ __device__ __forceinline__ int64_t head_row(const Kv4AttnParams& p, int g, int h
   return row * p.Hq + head * p.heads + (n - j * p.heads);
 }
 
-// Which kernel takes a CTA's rows (padded to 8, 16, 32 or 64).
+// Which kernel takes a CTA's rows (padded to 8, 16, 32 or 64).  Measured, us:
+//   rows of 64 requests of 4096 to 131072 keys, D = 128
+//     16 (4 key/value heads)      mma.sync 303, tcgen05 in tiles of 32 rows 542
+//     16 as two tiles of 8 rows   406
+//     32 (2 heads; 1)             mma.sync in tiles of 16 302; 162, tcgen05 283; 151
+//     64 (2 heads; 1)             583; 301, tcgen05 340; 184
+//   32, 64 rows of one request of 131071 keys: 61, 50 against 32, 38
+//   32, 64 rows on 2048 selected keys each of 64 requests, 8 heads: 180, 335
+//     against 163, 296
+// Where everything is small or D = 64, mma.sync would be faster still: 32 rows
+// of 64 requests of up to 16384 keys at D = 64, 29 against 36; 64 rows of 16
+// requests with key weights 92 against 107; single short calls by 1 us.
 constexpr bool uses_tc(int rows) { return rows > 16; }
 
 // One row's four channels d .. d + 3: the result, when the columns summed are
@@ -1097,6 +1128,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   }
 }
 
+// --------------------------------------------- more than 16 rows: tcgen05.mma
+//
+// Tiles of 128 columns by N = 32 or 64 query rows, two products a tile:
+//   S [128 x N]  = K' q^T    K' = K 2^-ref in TMEM, a key a lane: warps 0-3, one
+//                            key a thread
+//   O^T [D x N] += V'^T P    V' = V 2^-ref and P in shared memory, one row per
+//                            column: warps 4-7 make V', both kinds P, half of
+//                            the query rows each
+// One scale reference for a CTA's keys and one for its values, raised when a
+// scale passes it by 2^kSlack; references of the weights likewise lag behind
+// the rows' maxima.  Raising any is rare and costs one more round of the tile.
+// 64 requests of up to 16384 keys, 64 rows on one head: 54 us for 50 MB (0.9
+// TB/s).  Bound by the chain of a tile's steps (decode, product, softmax,
+// product) with two CTAs an SM to overlap them, which shared memory and TMEM
+// allow: issue 31 %, tensor pipe 12 %, and the stalls spread over copies,
+// barriers and instruction fetch.
 constexpr int kTcTile = 128;    // columns of a tile: one TMEM lane each
 constexpr int kTcThreads = 256; // warps 0-3: keys; warps 4-7: values; both: softmax
 constexpr int kTcStages = 2;
@@ -1807,6 +1854,9 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
 // 6 us).
 constexpr int kJoinThreads = 256;
 constexpr int kJoinMany = 16;  // results a row, on average, from which on
+// (whole calls, one warp a row against eight: 131071 columns 49 and 40 us, 32768
+// columns 32 and 24, 8192 columns 19.7 and 16.9; but for 512 items of 1 to 3
+// results 405 and 411, 22.1 and 23.8).
 
 template <int D, int kRows, int kPer, bool kSel, bool kScores>
 __global__ void __launch_bounds__(kJoinThreads)
@@ -1871,7 +1921,9 @@ __global__ void __launch_bounds__(kJoinThreads)
 // A column's attention weight, summed over heads and rows in one fixed order:
 // w = sum exp2(S - lse).  Dense: added to key_weights.  Selected: written to
 // sel_weights, and (one token a request) added to key_weights at the column's
-// position.
+// position.  One read of the logits, which lie in L2 where they fit: 11 us for
+// 16 requests of up to 32768 columns and 32 heads, 15 us for 128 rows of 2048
+// selected columns and 64 heads (67 MB, 4.5 TB/s).
 template <int NT, bool kSel>
 __global__ void __launch_bounds__(256) kv4_weight_kernel(const __grid_constant__ Kv4AttnParams p) {
   constexpr int kRows = 8 * NT;

@@ -80,7 +80,8 @@ dsa_status_t run_attention(const AttnArgs& a, bool selected, dsa_stream_t stream
   const int64_t lanes = static_cast<int64_t>(a.Hkv) * pl.row_tiles;
   // Units of work are counted in 32 bits.
   const int64_t units = cols / pl.unit + 1;
-  if (pl.groups * lanes >= (int64_t(1) << 31) / (units > pl.rows ? units : pl.rows) || pl.groups * ((cols + 255) / 256) >= (int64_t(1) << 31) ||
+  if (pl.groups * lanes >= (int64_t(1) << 31) / (units > pl.rows ? units : pl.rows) ||
+      pl.groups * ((cols + 255) / 256) >= (int64_t(1) << 31) ||
       (weights && lanes * pl.rows * 4 > 48 * 1024))
     return DSA_ERR_UNSUPPORTED;
   if (pl.bytes > 0 && (!a.workspace || !aligned(a.workspace, 256) ||
@@ -264,7 +265,7 @@ dsa_status_t dsa_kv_evict_select(const float* key_weights, int64_t ldw,
   cudaStream_t st = as_stream(stream);
   uint32_t* err = error_word();
   if (!err) return DSA_ERR_CUDA;
-  if (evict_small(max_ctx))
+  if (evict_small(B, max_ctx))
     return from_cuda(launch_evict_small(key_weights, ldw, context_lens, B, max_ctx, budget, sink,
                                         recent, keep, new_lens, err, st));
   cudaError_t e =

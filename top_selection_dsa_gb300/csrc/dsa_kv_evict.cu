@@ -5,11 +5,10 @@
 //             middle with the largest weight (ties to the lower position) and
 //             the last `recent`, ascending
 //
-// Up to kSmallCtx positions one CTA per request does all of it, its weights in
-// registers (evict_small_kernel).  Beyond that the middle's selection is the
+// Few requests of up to kSmallCtx positions: one CTA each does all of it, its
+// weights in registers (evict_small_kernel).  Else the middle's selection is the
 // library's masked top-k on the weights, and two small kernels make its row
-// ranges and put the three parts together: six launches, which is what a
-// request of 32768 positions would spend most of its time on (35 us against 17).
+// ranges and put the three parts together.
 // Compaction then moves row keep[b][i] of every cache to position i: to fresh
 // pages, or in place.  Because keep ascends, keep[i] >= i: in place, a CTA
 // that owns one request's slice of bytes goes through the rows in chunks and
@@ -438,7 +437,13 @@ __global__ void __launch_bounds__(kMoveThreads)
 
 }  // namespace
 
-bool evict_small(int max_ctx) { return max_ctx <= kSmallCtx; }
+// Short contexts, and no more requests than there are SMs, for one fills one:
+// selecting and moving 1024 of up to 32768 positions takes, with the one kernel
+// and with the general path, 53 and 68 us (1 request), 49 and 69 (8), 70 and 70
+// (64), 104 and 105 (128), but 154 and 145 (192) and 190 and 182 (256).
+bool evict_small(int B, int max_ctx) {
+  return max_ctx <= kSmallCtx && B <= device_sm_count();
+}
 
 cudaError_t launch_evict_small(const float* weights, int64_t ldw, const int32_t* lens, int B,
                                int max_ctx, int budget, int sink, int recent, int32_t* keep,
