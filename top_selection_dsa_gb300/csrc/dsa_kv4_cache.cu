@@ -14,11 +14,12 @@
 // of the record; their value codes are two units in each of two rows of units
 // (with two blocks a record these are contiguous; with four, the lanes of the
 // two pairs exchange half of them).  A record takes D/8 lanes (the key's, then
-// the value's), and a lane has kRecords records in flight.
-// Memory-bound next to its instructions: 65536 tokens of 8 heads of 128 written
-// and read back in 69 us, 5.0 TB/s (two records in flight; four 73 us; and one
-// 16-byte piece a lane, which pays for addresses, maxima and exchanges twice as
-// often, 90 us).
+// the value's).
+// Memory-bound next to its instructions: 32768 tokens of 8 heads of 128 written
+// and read back in 66 us, 5.1 TB/s, 100000 in 182 us, 5.7 TB/s.  More records in
+// flight a lane were slower (two 69 us, four 73 us), and so was one 16-byte
+// piece a lane, which pays for addresses, maxima and exchanges twice as often
+// (90 us).
 #include "dsa_internal.h"
 #include "dsa_kv4.cuh"
 
@@ -26,7 +27,6 @@ namespace dsa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRecords = 2;
 
 struct CacheParams {
   const uint16_t* k;  // insert: [T, Hkv, D], rows k_stride / v_stride elements apart
@@ -114,76 +114,63 @@ __global__ void __launch_bounds__(kThreads) kv4_insert_kernel(const __grid_const
   const Lane<D> lane(sub);
   const uint16_t* const src = lane.is_v ? p.v : p.k;
   const int64_t src_stride = lane.is_v ? p.v_stride : p.k_stride;
-  const uint32_t step = gridDim.x * kPerCta;
-  const uint32_t first = blockIdx.x * kPerCta;
-  for (uint32_t base = first; base < p.items; base += step * kRecords) {
-    uint4 raw[kRecords][2];
-    uint32_t rec[kRecords], ok = 0;
-#pragma unroll
-    for (int i = 0; i < kRecords; ++i) {
-      const uint32_t item = base + threadIdx.x / kLanes + i * step;
-      rec[i] = 0;
-      raw[i][0] = raw[i][1] = make_uint4(0u, 0u, 0u, 0u);
-      if (item < p.items) {
-        const uint32_t tok = token_of(p, item);
-        const uint32_t head = item - tok * p.Hkv;
-        const int64_t slot = __ldg(p.slots + tok);
-        const uint4* row = reinterpret_cast<const uint4*>(src + tok * src_stride + head * D);
-        raw[i][0] = __ldg(row + lane.e16(0));
-        raw[i][1] = __ldg(row + lane.e16(1));
-        if (slot >= p.capacity) {
-          if (sub == 0 && head == 0) record_error(p.err, kErrBadIndex);
-        } else if (slot >= 0) {
-          rec[i] = record_of(p, static_cast<uint32_t>(slot), head);
-          ok |= 1u << i;
-        }
-      }
+  for (uint32_t base = blockIdx.x * kPerCta; base < p.items; base += gridDim.x * kPerCta) {
+    const uint32_t item = base + threadIdx.x / kLanes;
+    uint4 raw[2];
+    raw[0] = raw[1] = make_uint4(0u, 0u, 0u, 0u);
+    uint32_t rec = 0;
+    bool ok = false;
+    if (item < p.items) {
+      const uint32_t tok = token_of(p, item);
+      const uint32_t head = item - tok * p.Hkv;
+      const int64_t slot = __ldg(p.slots + tok);
+      const uint4* row = reinterpret_cast<const uint4*>(src + tok * src_stride + head * D);
+      raw[0] = __ldg(row + lane.e16(0));
+      raw[1] = __ldg(row + lane.e16(1));
+      ok = slot >= 0 && slot < p.capacity;
+      if (ok) rec = record_of(p, static_cast<uint32_t>(slot), head);
+      else if (slot >= 0 && sub == 0 && head == 0) record_error(p.err, kErrBadIndex);
     }
+    // The largest magnitudes as bits: a NaN's or an infinity's are above every
+    // finite value's, so one integer maximum finds either.  The two blocks'
+    // share a word.
+    uint32_t m[2];
 #pragma unroll
-    for (int i = 0; i < kRecords; ++i) {
-      // The largest magnitudes as bits: a NaN's or an infinity's are above
-      // every finite value's, so one integer maximum finds either.  The two
-      // blocks' share a word.
-      uint32_t m[2];
+    for (int b = 0; b < 2; ++b)
+      m[b] = max_u16x2(max_u16x2(raw[b].x & 0x7FFF7FFFu, raw[b].y & 0x7FFF7FFFu),
+                       max_u16x2(raw[b].z & 0x7FFF7FFFu, raw[b].w & 0x7FFF7FFFu));
+    uint32_t mag = max_u16x2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
+    mag = max_u16x2(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
+    mag = max_u16x2(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
+    uint32_t codes[2], scale[2];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const uint4 w = raw[i][b];
-        m[b] = max_u16x2(max_u16x2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
-                         max_u16x2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+    for (int b = 0; b < 2; ++b) {
+      const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
+      const uint32_t amax = b == 0 ? mag & 0xFFFFu : mag >> 16;  // bf16 bits
+      // 6 * 2^e = 1.5 * 2^(e+2): biased, the exponent of amax less two, and one
+      // more for a mantissa above 1.5 (whose addition carries).
+      int e = static_cast<int>((amax + 0x3Fu) >> 7) - 2;
+      e = amax == 0 ? 127 : max(e, 1);
+      const bool bad = amax >= 0x7F80u;
+      // x / 2^(e - 127): exact where it matters (what it rounds, below 2^-126,
+      // is far below half of the smallest code).
+      const uint32_t inv = static_cast<uint32_t>(254 - e) * 0x00800080u;
+      uint32_t c = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t y = mul_bf16x2(w[j], inv);
+        c |= f32x2_to_e2m1x2(bf16_lo(y), bf16_hi(y)) << (8 * j);
       }
-      uint32_t mag = max_u16x2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
-      mag = max_u16x2(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
-      mag = max_u16x2(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
-      uint32_t codes[2], scale[2];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const uint32_t w[4] = {raw[i][b].x, raw[i][b].y, raw[i][b].z, raw[i][b].w};
-        const uint32_t amax = b == 0 ? mag & 0xFFFFu : mag >> 16;  // bf16 bits
-        // 6 * 2^e = 1.5 * 2^(e+2): biased, the exponent of amax less two, and
-        // one more for a mantissa above 1.5 (whose addition carries).
-        int e = static_cast<int>((amax + 0x3Fu) >> 7) - 2;
-        e = amax == 0 ? 127 : max(e, 1);
-        const bool bad = amax >= 0x7F80u;
-        // x / 2^(e - 127): exact where it matters (what it rounds, below
-        // 2^-126, is far below half of the smallest code).
-        const uint32_t inv = static_cast<uint32_t>(254 - e) * 0x00800080u;
-        uint32_t c = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t y = mul_bf16x2(w[j], inv);
-          c |= f32x2_to_e2m1x2(bf16_lo(y), bf16_hi(y)) << (8 * j);
-        }
-        codes[b] = bad ? 0u : c;
-        scale[b] = bad ? 255u : static_cast<uint32_t>(e);
-      }
-      const uint2 out = lane.pack(make_uint2(codes[0], codes[1]));
-      if (!((ok >> i) & 1)) continue;
-      *reinterpret_cast<uint2*>(p.cache + static_cast<uint64_t>(rec[i]) * D + lane.word * 4) = out;
-      if (lane.t == 0)
-        *reinterpret_cast<uint16_t*>(p.scales + static_cast<uint64_t>(rec[i]) * (D / 16) +
-                                     (lane.is_v ? G : 0) + lane.g) =
-            static_cast<uint16_t>(scale[0] | (scale[1] << 8));
+      codes[b] = bad ? 0u : c;
+      scale[b] = bad ? 255u : static_cast<uint32_t>(e);
     }
+    const uint2 out = lane.pack(make_uint2(codes[0], codes[1]));
+    if (!ok) continue;
+    *reinterpret_cast<uint2*>(p.cache + static_cast<uint64_t>(rec) * D + lane.word * 4) = out;
+    if (lane.t == 0)
+      *reinterpret_cast<uint16_t*>(p.scales + static_cast<uint64_t>(rec) * (D / 16) +
+                                   (lane.is_v ? G : 0) + lane.g) =
+          static_cast<uint16_t>(scale[0] | (scale[1] << 8));
   }
 }
 
@@ -195,57 +182,46 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const __grid_const
   const int sub = threadIdx.x % kLanes;
   const Lane<D> lane(sub);
   uint16_t* const out = lane.is_v ? p.v_out : p.k_out;
-  const uint32_t step = gridDim.x * kPerCta;
-  const uint32_t first = blockIdx.x * kPerCta;
-  for (uint32_t base = first; base < p.items; base += step * kRecords) {
-    uint2 codes[kRecords];
-    uint32_t sc[kRecords];
-#pragma unroll
-    for (int i = 0; i < kRecords; ++i) {
-      const uint32_t item = base + threadIdx.x / kLanes + i * step;
-      codes[i] = make_uint2(0u, 0u);
-      sc[i] = 0x7F7Fu;
-      if (item < p.items) {
-        const uint32_t tok = token_of(p, item);
-        const uint32_t head = item - tok * p.Hkv;
-        const int64_t slot = __ldg(p.slots + tok);
-        if (slot >= p.capacity) {
-          if (sub == 0 && head == 0) record_error(p.err, kErrBadIndex);
-        } else if (slot >= 0) {
-          const uint64_t rec = record_of(p, static_cast<uint32_t>(slot), head);
-          codes[i] = *reinterpret_cast<const uint2*>(p.cache + rec * D + lane.word * 4);
-          sc[i] = *reinterpret_cast<const uint16_t*>(p.scales + rec * (D / 16) +
-                                                     (lane.is_v ? G : 0) + lane.g);
-        }
+  for (uint32_t base = blockIdx.x * kPerCta; base < p.items; base += gridDim.x * kPerCta) {
+    const uint32_t item = base + threadIdx.x / kLanes;
+    uint2 codes = make_uint2(0u, 0u);
+    uint32_t scales = 0x7F7Fu;
+    if (item < p.items) {
+      const uint32_t tok = token_of(p, item);
+      const uint32_t head = item - tok * p.Hkv;
+      const int64_t slot = __ldg(p.slots + tok);
+      if (slot >= p.capacity) {
+        if (sub == 0 && head == 0) record_error(p.err, kErrBadIndex);
+      } else if (slot >= 0) {
+        const uint64_t rec = record_of(p, static_cast<uint32_t>(slot), head);
+        codes = *reinterpret_cast<const uint2*>(p.cache + rec * D + lane.word * 4);
+        scales = *reinterpret_cast<const uint16_t*>(p.scales + rec * (D / 16) +
+                                                    (lane.is_v ? G : 0) + lane.g);
       }
     }
+    codes = lane.unpack(codes);
+    if (item >= p.items) continue;
 #pragma unroll
-    for (int i = 0; i < kRecords; ++i) {
-      const uint32_t item = base + threadIdx.x / kLanes + i * step;
-      const uint2 both = lane.unpack(codes[i]);
-      if (item >= p.items) continue;
+    for (int b = 0; b < 2; ++b) {
+      const uint32_t c = b == 0 ? codes.x : codes.y;
+      const uint32_t e = b == 0 ? scales & 0xFFu : scales >> 8;
+      const float s = __uint_as_float(e == 255 ? 0x7FC00000u : e << 23);
+      const uint32_t h[4] = {e2m1x2_to_f16x2<0>(c), e2m1x2_to_f16x2<1>(c),
+                             e2m1x2_to_f16x2<2>(c), e2m1x2_to_f16x2<3>(c)};
+      uint32_t o[4];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const uint32_t c = b == 0 ? both.x : both.y;
-        const uint32_t e = b == 0 ? sc[i] & 0xFFu : sc[i] >> 8;
-        const float s = __uint_as_float(e == 255 ? 0x7FC00000u : e << 23);
-        const uint32_t h[4] = {e2m1x2_to_f16x2<0>(c), e2m1x2_to_f16x2<1>(c),
-                               e2m1x2_to_f16x2<2>(c), e2m1x2_to_f16x2<3>(c)};
-        uint32_t o[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-          o[j] = pack_bf16(f.x * s, f.y * s);
-        }
-        *(reinterpret_cast<uint4*>(out + static_cast<int64_t>(item) * D) + lane.e16(b)) =
-            make_uint4(o[0], o[1], o[2], o[3]);
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+        o[j] = pack_bf16(f.x * s, f.y * s);
       }
+      *(reinterpret_cast<uint4*>(out + static_cast<int64_t>(item) * D) + lane.e16(b)) =
+          make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
 
 int cache_grid(int64_t items, int D) {
-  const int64_t per = static_cast<int64_t>(kThreads / (D / 8)) * kRecords;
+  const int64_t per = kThreads / (D / 8);
   const int64_t need = (items + per - 1) / per;
   const int64_t cap = static_cast<int64_t>(device_sm_count() > 0 ? device_sm_count() : 1) * 16;
   return static_cast<int>(need < cap ? need : cap);
