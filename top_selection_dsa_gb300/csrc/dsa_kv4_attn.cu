@@ -37,9 +37,9 @@
 //                      the issue slots, ALU and tensor pipes 45 % each, three
 //                      warps a scheduler is what the registers leave)
 //   one request of 131071 keys, 8 rows   40 us, 3.5 TB/s: start and join
-//   2048 selected of each of 128 rows    106 us the kernel, 4.2 TB/s of DRAM:
-//     single records of 128 bytes and scales of 8 from all over 2.5 GB (a
-//     plain gather of those took 71 us)
+//   2048 selected of each of 128 rows    82 us: single records of 128 bytes and
+//     scales of 8 from all over 2.5 GB (a plain gather of those took 71 us;
+//     DRAM is read by 64 bytes, which makes it 400 MB); 108 us with weights
 // Tried and slower: tiles of 32 columns in three stages; 8 warps with 254
 // registers for 16 rows (637 to 716 us); tcgen05 for 16 rows (856); TMA gathers
 // of selected records (103.5 against cp.async's 98.4).
@@ -68,7 +68,14 @@ constexpr int kTile = 64;       // columns a warp takes at a time
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 2;
-constexpr int kCtasPerSm = 3;   // registers (168 a thread) and shared memory
+// Three fill an SM's registers (168 a thread) and shared memory.  On a selection
+// that leaves the L1, through which the gathers of single records go, 28 KB, and
+// two CTAs' fewer copies in flight are faster: 128 rows of 2048 selected keys, 8
+// heads, 82 us against 97 (with weights 108 against 131), 4 requests' 18
+// against 22; but two CTAs of three stages, which fill the shared memory again,
+// 107.  Dense copies do not pass through it: 64 requests 404 us with three CTAs,
+// 456 with two.
+constexpr int ctas_per_sm(bool sel) { return sel ? 2 : 3; }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("{.reg .b64 pol;\n\tcreatepolicy.fractional.L2::evict_first.b64 pol, 1.0;\n\tcp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, pol;}" ::"r"(dst), "l"(src), "r"(bytes)
@@ -420,7 +427,7 @@ __device__ __forceinline__ void write_row(const Kv4AttnParams& p, int grp, int h
 }
 
 template <int D, int NT, bool kSel, bool kScores>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(kSel))
     kv4_attn_kernel(const __grid_constant__ Kv4AttnParams p) {
   using Lay = Layout<D, NT>;
   constexpr int G = Lay::G;
@@ -2078,7 +2085,7 @@ Kv4AttnPlan kv4_attn_plan(int B, int next_n, int Hq, int Hkv, int D, int64_t col
   const int64_t units = cols > 0 ? (cols + unit - 1) / unit : 1;
   const int64_t lanes = pl.groups * Hkv * pl.row_tiles;
   const int64_t places = static_cast<int64_t>(device_sm_count() > 0 ? device_sm_count() : 152) *
-                         (uses_tc(pl.rows) ? kTcCtas : kCtasPerSm);
+                         (uses_tc(pl.rows) ? kTcCtas : ctas_per_sm(selected));
   pl.ctas = static_cast<int>(units * lanes < places ? units * lanes : places);
   pl.split = units > 1;
   int64_t off = 0;
