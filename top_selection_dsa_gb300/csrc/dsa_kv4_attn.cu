@@ -391,11 +391,14 @@ __device__ __forceinline__ int64_t head_row(const Kv4AttnParams& p, int g, int h
 //     32 (2 heads; 1)             mma.sync in tiles of 16 302; 162, tcgen05 283; 151
 //     64 (2 heads; 1)             583; 301, tcgen05 340; 184
 //   32, 64 rows of one request of 131071 keys: 61, 50 against 32, 38
-//   32, 64 rows on 2048 selected keys each of 64 requests, 8 heads: 180, 335
-//     against 163, 296
-// Where everything is small or D = 64, mma.sync would be faster still: 32 rows
-// of 64 requests of up to 16384 keys at D = 64, 29 against 36; 64 rows of 16
-// requests with key weights 92 against 107; single short calls by 1 us.
+//   32, 64 rows on 2048 selected keys of 128 rows, 8 heads: 191, 360 against
+//     164, 246
+// Where everything is small or D = 64 mma.sync would be faster still (32 rows of
+// 64 requests of up to 16384 keys at D = 64, 29 against 36; single short calls
+// by 1 us), and with weights, where the logits' writes count (64 rows: 92
+// against 107 for 16 requests of up to 32768 keys, 565 against 551 for the 64
+// above, 278 against 298 on 64 selections); but whether the weights are asked
+// for does not change the output.
 constexpr bool uses_tc(int rows) { return rows > 16; }
 
 // One row's four channels d .. d + 3: the result, when the columns summed are
