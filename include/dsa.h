@@ -494,8 +494,8 @@ dsa_status_t dsa_kv4_insert(const void* k, int64_t k_stride, const void* v, int6
 /*
  * Reads slots back as the values they stand for: k, v [T, Hkv, D] bf16 out,
  * dense, 16-byte aligned (exact: two significant bits times a power of two;
- * scale code 255 reads as NaN).  Slots as dsa_kv4_insert; a skipped one gives
- * zeros.
+ * scale code 255 reads as NaN, and code 0, which no insert writes, as zero).
+ * Slots as dsa_kv4_insert; a skipped one gives zeros.
  */
 dsa_status_t dsa_kv4_gather(const void* cache, const uint8_t* scales, int num_blocks,
                             int block_size, const int64_t* slots, int T, int Hkv, int D, void* k,
