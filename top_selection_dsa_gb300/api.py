@@ -729,6 +729,14 @@ def kv4_attention_topk(q, cache, scales, block_table, context_lens, topk_idx, *,
 
 @functools.lru_cache(maxsize=4096)
 def kv_evict_workspace_bytes(B, max_ctx, budget) -> int:
+    """Workspace of kv_evict_select over key_weights [B, max_ctx], on the current
+    device."""
+    return _evict_workspace(torch.cuda.current_device() if torch.cuda.is_available() else -1,
+                            B, max_ctx, budget)
+
+
+@functools.lru_cache(maxsize=4096)
+def _evict_workspace(device, B, max_ctx, budget):
     n = lib.dsa_kv_evict_workspace_bytes(B, max_ctx, budget)
     if n == ctypes.c_size_t(-1).value:
         raise ValueError("dsa_kv_evict_workspace_bytes: bad arguments")
@@ -752,8 +760,8 @@ def kv_evict_select(key_weights, context_lens, budget, *, sink=0, recent=0, keep
     _shape(context_lens, "context_lens", (B,))
     _shape(keep, "keep", (B, budget))
     _shape(new_lens, "new_lens", (B,))
-    nbytes = kv_evict_workspace_bytes(B, ldw, budget)
     with _on(dev):
+        nbytes = _evict_workspace(dev.index, B, ldw, budget)
         ws = _workspace(nbytes, dev, workspace)
         st = lib.dsa_kv_evict_select(_addr(key_weights), ldw, _addr(context_lens), B, ldw, budget,
                                      sink, recent, _addr(keep), _addr(new_lens), _addr(ws), nbytes,
