@@ -78,8 +78,11 @@ constexpr int kStages = 2;
 constexpr int ctas_per_sm(bool sel) { return sel ? 2 : 3; }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("{.reg .b64 pol;\n\tcreatepolicy.fractional.L2::evict_first.b64 pol, 1.0;\n\tcp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, pol;}" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
+  asm volatile(
+      "{\n\t.reg .b64 pol;\n\tcreatepolicy.fractional.L2::evict_first.b64 pol, 1.0;\n\t"
+      "cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, pol;\n\t}" ::"r"(dst),
+      "l"(src), "r"(bytes)
+      : "memory");
 }
 template <int kBytes>
 __device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, uint32_t bytes) {
