@@ -1,0 +1,120 @@
+"""The 4-bit cache's attention where sizes, scales and masks are far apart:
+long contexts, scales that grow along them, and what rows do not see, against
+the formulas in 64 bits (torch, on the GPU).
+
+Tolerances are those of test_kv4_gpu.py's first lines, with B = |scale| max_c
+sum_d |q_d||k_d| of a row and dS = (2^-19 + 2^-24) B:
+  weights  e^(error of the logits) on the numerator and in the log-sum-exp, ex2
+           within 2^-21, fp32 sums: relative 2 dS + 2^-18; then one fp32
+           addition a row: 2^-24 of the sum for each.
+"""
+import numpy as np
+import pytest
+import torch
+
+import kv4_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def api():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from top_selection_dsa_gb300 import api as _api
+    return _api
+
+
+@pytest.fixture(autouse=True)
+def clean_error_word(api):
+    yield
+    assert api.last_device_error() == api.DSA_OK
+
+
+class Cache:
+    """Random codes under given scale codes: key_codes, value_codes [L, Hkv,
+    D/32] of each request; pages in random order."""
+
+    def __init__(self, lens, nn, Hq, Hkv, D, bs, key_codes, value_codes, q, seed=0):
+        rng = np.random.default_rng(seed)
+        nblk = [max(-(-L // bs), 1) for L in lens]
+        total = sum(nblk)
+        perm = rng.permutation(total).astype(np.int32)
+        table = np.zeros((len(lens), max(nblk)), np.int32)
+        self.rec = rng.integers(0, 256, size=(total, Hkv, bs, D), dtype=np.uint8)
+        self.sc = np.full((total, Hkv, bs, D // 16), 127, np.uint8)
+        self.K, self.V = [], []
+        at = 0
+        for b, L in enumerate(lens):
+            table[b, :nblk[b]] = perm[at:at + nblk[b]]
+            at += nblk[b]
+            pos = np.arange(L)
+            page, row = table[b, pos // bs], pos % bs
+            self.sc[page, :, row] = np.concatenate([key_codes[b], value_codes[b]], -1)
+            k, v = ref.decode(self.rec[page, :, row], self.sc[page, :, row]) if L else \
+                (np.zeros((0, Hkv, D)),) * 2
+            self.K.append(torch.from_numpy(k).cuda())
+            self.V.append(torch.from_numpy(v).cuda())
+        self.lens, self.nn, self.Hq, self.Hkv, self.D, self.bs = lens, nn, Hq, Hkv, D, bs
+        self.table = table
+        self.q = torch.as_tensor(q).float().bfloat16().cuda().reshape(len(lens) * nn, Hq, D)
+        self.args = (self.q, torch.from_numpy(self.rec).cuda(), torch.from_numpy(self.sc).cuda(),
+                     torch.from_numpy(table).cuda(),
+                     torch.tensor(lens, dtype=torch.int32, device="cuda"))
+
+    def row(self, b, j, scale):
+        """Row j of request b in 64 bits: (out [Hq, D], lse [Hq], weights [Hq,
+        L], sum p |V| [Hq, D], B [Hq])."""
+        L, G = self.lens[b], self.Hq // self.Hkv
+        n = max(L - self.nn + j + 1, 0)
+        q = self.q[b * self.nn + j].double()
+        K = self.K[b][:n].repeat_interleave(G, 1)            # [n, Hq, D]
+        V = self.V[b][:n].repeat_interleave(G, 1)
+        S = scale * torch.einsum("hd,nhd->hn", q, K)
+        B = abs(scale) * torch.einsum("hd,nhd->hn", q.abs(), K.abs()).amax(1)
+        lse = torch.logsumexp(S, 1)
+        p = torch.exp(S - lse[:, None])
+        w = torch.zeros(self.Hq, L, dtype=torch.float64, device="cuda")
+        w[:, :n] = p
+        return (torch.einsum("hn,nhd->hd", p, V), lse, w,
+                torch.einsum("hn,nhd->hd", p, V.abs()), B)
+
+
+def rel_of(B):
+    return 2 * (2.0 ** -19 + 2.0 ** -24) * float(B.max()) + 2.0 ** -18
+
+
+# --------------------------------------------------------- every key's weight
+
+
+@pytest.mark.parametrize("rows", [24, 40, 64])
+def test_weights_over_many_tiles_of_growing_keys(api, rows):
+    """131071 keys whose scales grow by 2^9 along the context: each call's
+    weights are those in 64 bits and of the same keys selected, and those of
+    every other call to the bit."""
+    L, D = 131071, 128
+    rng = np.random.default_rng(rows)
+    grow = (np.arange(L) * 10 // L)[:, None, None]
+    kc = 118 + grow + rng.integers(-1, 2, size=(L, 1, 4))
+    vc = rng.integers(125, 129, size=(L, 1, 4))
+    scale = 0.02
+    c = Cache([L], 1, rows, 1, D, 64, [kc], [vc], rng.standard_normal((rows, D)), seed=rows)
+    out, lse, p, A, B = c.row(0, 0, scale)
+    want = p.sum(0)
+    rel = rel_of(B)
+    width = c.table.shape[1] * 64
+    first = None
+    for _ in range(20):
+        acc = torch.zeros(1, width, device="cuda")
+        api.kv4_attention(*c.args, next_n=1, softmax_scale=scale, key_weights=acc)
+        if first is None:
+            first = acc
+        assert torch.equal(acc, first)
+    got = first[0, :L].double()
+    tol = (rel + rows * 2.0 ** -24) * want
+    assert ((got - want).abs() <= tol).all(), float(((got - want).abs() / want).max())
+    assert (first[0, L:] == 0).all()
+    sel = torch.arange(L, dtype=torch.int32, device="cuda")[None]
+    sw = torch.empty(1, L, device="cuda")
+    api.kv4_attention_topk(*c.args, sel, next_n=1, softmax_scale=scale, sel_weights=sw)
+    assert ((sw[0].double() - want).abs() <= tol).all()

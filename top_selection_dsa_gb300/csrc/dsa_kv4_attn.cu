@@ -1510,6 +1510,10 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
       __syncthreads();
       valid = here[0];
     } else {
+      // The last tile's logits were read, for the weights, after its last
+      // barrier: what follows writes over them (S) and what they were read
+      // with (fz).
+      if constexpr (kScores) __syncthreads();
       if (!mbar_wait_long(&full[s], (done / kTcStages) & 1, abort_flag)) fail = true;
       valid = col < c1;
     }
@@ -1756,6 +1760,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
           *reinterpret_cast<float4*>(dst + n + 4) = make_float4(v[4], v[5], v[6], v[7]);
         __syncwarp();
       }
+      tc_fence_before_sync();
     }
 #pragma unroll
     for (int n = 0; n < kHalf; ++n) l[n] += pr[n];
