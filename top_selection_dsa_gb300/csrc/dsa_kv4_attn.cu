@@ -60,6 +60,7 @@
 
 #include "dsa_internal.h"
 #include "dsa_kv4.cuh"
+#include "dsa_kv4_span.h"
 
 namespace dsa {
 namespace {
@@ -1887,7 +1888,8 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int row = kPer == 1 ? blockIdx.x % kSets : (blockIdx.x % kSets) * 8 + warp;
   const int4 sp = p.spans[item];
   const int cta = sp.x, n = sp.y;
-  if (n <= 1) return;  // written by the CTA that had all of it
+  if (!span_noted(cta, n, sp.z, p.ctas)) return;  // a wait gave up, and that is recorded
+  if (n == 1) return;                             // written by the CTA that had all of it
   const int grp = item / per_split, ht = item % per_split;
   const int row0 = (ht % p.row_tiles) * kRows;
   const int nrows = kSel ? p.heads : p.heads * p.next_n;
