@@ -143,10 +143,9 @@ __global__ void __launch_bounds__(kSmallThreads)
   valid = block_sum(valid, slots[turn]);
   uint32_t bound = 1, taken = valid;  // at or above `bound`: `taken` weights
   if (valid > room) {
-    if (lane == 0) ties[warp] = __reduce_or_sync(0xffffffffu, any);
-    else __reduce_or_sync(0xffffffffu, any);
-    if (lane == 0) above[warp] = __reduce_and_sync(0xffffffffu, all);
-    else __reduce_and_sync(0xffffffffu, all);
+    any = __reduce_or_sync(0xffffffffu, any);
+    all = __reduce_and_sync(0xffffffffu, all);
+    if (lane == 0) ties[warp] = any, above[warp] = all;
     __syncthreads();
     any = __reduce_or_sync(0xffffffffu, ties[lane]);
     all = __reduce_and_sync(0xffffffffu, above[lane]);
