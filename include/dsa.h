@@ -608,7 +608,10 @@ typedef struct {
  *                    a page that block_table names; or NULL: in place (the
  *                    pages past new_lens are then free).  A page in place must
  *                    belong to one request only.
- *   context_lens     [B] lengths before, new_lens [B] after (at most budget)
+ *   context_lens     [B] lengths before, new_lens [B] after: at most budget, and
+ *                    what the request's row of the table moved to (in place:
+ *                    of block_table) has room for; rows past either are left
+ *                    out, their weights too, and recorded
  *   keep             [B, budget] int32, ascending; entries outside
  *                    [0, context_lens[b]) below new_lens[b], and pages outside
  *                    the cache, are skipped and recorded

@@ -118,3 +118,42 @@ def test_weights_over_many_tiles_of_growing_keys(api, rows):
     sw = torch.empty(1, L, device="cuda")
     api.kv4_attention_topk(*c.args, sel, next_n=1, softmax_scale=scale, sel_weights=sw)
     assert ((sw[0].double() - want).abs() <= tol).all()
+
+
+# ------------------------------------------------------------------ compaction
+
+
+@pytest.mark.parametrize("alone", [False, True])
+def test_a_new_table_too_short_for_the_kept_rows_is_reported(api, alone):
+    """12 rows kept, pages for 8: the first 8 move, with their weights, the rest
+    are zeros and the call is reported."""
+    bs = 8
+    g = torch.arange(4 * bs, dtype=torch.int32, device="cuda").reshape(4, bs).clone()
+    before = g.clone()
+    keep = torch.arange(2, 14, dtype=torch.int32, device="cuda")[None]
+    cl = torch.tensor([16], dtype=torch.int32, device="cuda")
+    table = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda")
+    fresh = torch.tensor([[3]], dtype=torch.int32, device="cuda")
+    n = torch.tensor([12], dtype=torch.int32, device="cuda")
+    w = torch.arange(1, 17, dtype=torch.float32, device="cuda")[None].clone()
+    out = w if alone else torch.full_like(w, 5.0)
+    api.kv_compact([g], keep, cl, table, fresh, new_lens=n, key_weights=w, key_weights_out=out)
+    assert api.last_device_error() == api.DSA_ERR_INVALID_ARG
+    before[3] = torch.arange(2, 10, dtype=torch.int32)
+    assert torch.equal(g, before)
+    assert out[0].tolist() == list(range(3, 11)) + [0.0] * 8
+
+
+def test_more_rows_than_the_table_has_room_for_in_place_are_reported(api):
+    bs = 8
+    g = torch.arange(4 * bs, dtype=torch.int32, device="cuda").reshape(4, bs).clone()
+    before = g.clone()
+    keep = torch.arange(20, dtype=torch.int32, device="cuda")[None]
+    cl = torch.tensor([16], dtype=torch.int32, device="cuda")
+    table = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda")
+    n = torch.tensor([20], dtype=torch.int32, device="cuda")
+    w = torch.arange(1, 17, dtype=torch.float32, device="cuda")[None].clone()
+    w0 = w.clone()
+    api.kv_compact([g], keep, cl, table, new_lens=n, key_weights=w)
+    assert api.last_device_error() == api.DSA_ERR_INVALID_ARG
+    assert torch.equal(g, before) and torch.equal(w, w0)

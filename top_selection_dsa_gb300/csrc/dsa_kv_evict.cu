@@ -201,6 +201,15 @@ constexpr int kSlice = 128;     // bytes of a row one CTA moves in place
 constexpr int kPartRows = 32;   // rows a CTA moves to fresh pages
 constexpr int kCopyUnroll = 4;  // copies a thread has in flight there
 
+// Rows a request keeps: new_lens, within the lists of `keep` and the `places`
+// its pages have; more are recorded, and left out.
+__device__ __forceinline__ int rows_to_keep(const CompactParams& p, int b, int places,
+                                            bool report) {
+  const int n = __ldg(p.new_lens + b), most = min(p.budget, places);
+  if (report && threadIdx.x == 0 && (n < 0 || n > most)) record_error(p.err, kErrBadIndex);
+  return n < 0 ? 0 : min(n, most);
+}
+
 // To fresh pages: a CTA takes kPartRows rows of a request in every cache.
 // Where they are is looked up once; after that the copies are independent of
 // one another and cost two additions of an address each.  Bound by the
@@ -258,11 +267,7 @@ __global__ void __launch_bounds__(kMoveThreads, 6)
   const int b = blockIdx.y, part = blockIdx.x;
   const int cap = p.max_blocks << p.log_bs;
   const int old_len = clamp_len(__ldg(p.old_lens + b), cap);
-  int n = __ldg(p.new_lens + b);
-  if (n < 0 || n > p.budget) {
-    if (threadIdx.x == 0 && part == 0) record_error(p.err, kErrBadIndex);
-    n = n < 0 ? 0 : p.budget;
-  }
+  const int n = rows_to_keep(p, b, min(cap, p.new_max_blocks << p.log_bs), part == 0);
   const int32_t* keep = p.keep + static_cast<int64_t>(b) * p.budget;
   const int i0 = part * kPartRows;
   if (p.weights) {
@@ -272,8 +277,7 @@ __global__ void __launch_bounds__(kMoveThreads, 6)
     float* out = p.weights_out + static_cast<int64_t>(b) * p.ldw;
     const bool alone = p.weights_out == p.weights;
     if (!alone || part == 0) {
-      const int kept = min(n, cap);
-      const int w0 = alone ? 0 : i0, w1 = alone ? kept : min(kept, i0 + kPartRows);
+      const int w0 = alone ? 0 : i0, w1 = alone ? n : min(n, i0 + kPartRows);
       for (int base = w0; base < w1; base += kMoveThreads) {
         const int i = base + threadIdx.x;
         float v = 0.f;
@@ -286,13 +290,12 @@ __global__ void __launch_bounds__(kMoveThreads, 6)
       }
       __syncthreads();
       const int parts = alone ? 1 : static_cast<int>(gridDim.x);
-      const int64_t share = (cap - kept + parts - 1) / parts;
-      const int z0 = static_cast<int>(min(static_cast<int64_t>(cap), kept + share * part));
+      const int64_t share = (cap - n + parts - 1) / parts;
+      const int z0 = static_cast<int>(min(static_cast<int64_t>(cap), n + share * part));
       const int z1 = static_cast<int>(min(static_cast<int64_t>(cap), z0 + share));
       for (int i = z0 + threadIdx.x; i < z1; i += kMoveThreads) out[i] = 0.f;
     }
   }
-  n = min(n, p.new_max_blocks << p.log_bs);
   const int rows = min(n - i0, kPartRows);
   if (rows <= 0 || p.ncaches == 0) return;
   if (threadIdx.x < rows) {
@@ -394,12 +397,7 @@ __global__ void __launch_bounds__(kMoveThreads)
   const int b = blockIdx.y, unit = blockIdx.x;
   const int cap = p.max_blocks << p.log_bs;
   const int old_len = clamp_len(__ldg(p.old_lens + b), cap);
-  int n = __ldg(p.new_lens + b);
-  if (n < 0 || n > p.budget) {
-    if (threadIdx.x == 0 && unit == 0) record_error(p.err, kErrBadIndex);
-    n = n < 0 ? 0 : p.budget;
-  }
-  n = min(n, cap);
+  const int n = rows_to_keep(p, b, cap, unit == 0);
   if (unit < p.units) {
     int c = 0;
     while (unit >= p.first_unit[c + 1]) ++c;
