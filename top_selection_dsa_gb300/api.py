@@ -727,7 +727,6 @@ def kv4_attention_topk(q, cache, scales, block_table, context_lens, topk_idx, *,
                           softmax_scale, out, lse, sel_weights, key_weights, workspace)
 
 
-@functools.lru_cache(maxsize=4096)
 def kv_evict_workspace_bytes(B, max_ctx, budget) -> int:
     """Workspace of kv_evict_select over key_weights [B, max_ctx], on the current
     device."""
