@@ -157,3 +157,25 @@ def test_more_rows_than_the_table_has_room_for_in_place_are_reported(api):
     api.kv_compact([g], keep, cl, table, new_lens=n, key_weights=w)
     assert api.last_device_error() == api.DSA_ERR_INVALID_ARG
     assert torch.equal(g, before) and torch.equal(w, w0)
+
+
+# ------------------------------------------------------------------ no requests
+
+
+def test_calls_without_requests_return_what_there_is(api):
+    """An empty batch: outputs of no rows, nothing touched."""
+    cache, scales = api.kv4_cache(2, 2, 8, 64)
+    q = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    table = torch.empty(0, 3, dtype=torch.int32, device="cuda")
+    lens = torch.empty(0, dtype=torch.int32, device="cuda")
+    out, lse = api.kv4_attention(q, cache, scales, table, lens, next_n=2)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    sel = torch.empty(0, 5, dtype=torch.int32, device="cuda")
+    acc = torch.empty(0, 24, device="cuda")
+    out, lse = api.kv4_attention_topk(q, cache, scales, table, lens, sel, next_n=2,
+                                      key_weights=acc)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    keep, n = api.kv_evict_select(acc, lens, 4)
+    assert keep.shape == (0, 4) and n.shape == (0,)
+    api.kv_compact([cache, scales], keep, lens, table, key_weights=acc)
+    assert (cache == 0).all() and (scales == 0).all()

@@ -677,6 +677,8 @@ def _kv4_attention(q, cache, scales, block_table, context_lens, topk_idx, next_n
             raise ValueError(f"key_weights must be [{B}, >= {max_blocks * bs}], got "
                              f"{tuple(key_weights.shape)}")
         ldw = key_weights.shape[1]
+    if B == 0:
+        return out, lse
     scale = D ** -0.5 if softmax_scale is None else softmax_scale
     with _on(dev):
         if topk_idx is None:
@@ -759,6 +761,8 @@ def kv_evict_select(key_weights, context_lens, budget, *, sink=0, recent=0, keep
     _shape(context_lens, "context_lens", (B,))
     _shape(keep, "keep", (B, budget))
     _shape(new_lens, "new_lens", (B,))
+    if B == 0:
+        return keep, new_lens
     with _on(dev):
         nbytes = _evict_workspace(dev.index, B, ldw, budget)
         ws = _workspace(nbytes, dev, workspace)
@@ -824,6 +828,8 @@ def kv_compact(caches, keep, context_lens, block_table, new_block_table=None, *,
         ldw = key_weights.shape[1]
         _shape(key_weights, "key_weights", (B, ldw))
         _shape(key_weights_out, "key_weights_out", (B, ldw))
+    if B == 0:
+        return caches
     with _on(dev):
         st = lib.dsa_kv_compact(rows, len(caches), num_blocks, block_size, _addr(block_table),
                                 max_blocks, _addr(new_block_table),
