@@ -179,3 +179,62 @@ def test_calls_without_requests_return_what_there_is(api):
     assert keep.shape == (0, 4) and n.shape == (0,)
     api.kv_compact([cache, scales], keep, lens, table, key_weights=acc)
     assert (cache == 0).all() and (scales == 0).all()
+
+
+# ------------------------------------------------- what a row does not see
+
+
+def check_row(c, out, lse, b, j, scale, under=2.0 ** -24):
+    """Row j of request b: output within fp16 weights' rounding (2^-11), the
+    logits', bf16's (2^-8), and the sums of what fp16 cannot hold, `under` of the
+    32-channel block's largest visible value each; its log-sum-exp."""
+    want, wlse, w, A, B = c.row(b, j, scale)
+    n = max(c.lens[b] - c.nn + j + 1, 0)
+    dS = (2.0 ** -19 + 2.0 ** -24) * B
+    G = c.Hq // c.Hkv
+    top = c.V[b][:n].abs().reshape(n, c.Hkv, c.D // 32, 32).amax((0, 3))
+    top = top.repeat_interleave(G, 0).repeat_interleave(32, 1)
+    tol = A * (2.0 ** -11 + 2 * dS + 2.0 ** -18)[:, None] + n * under * top + 2.0 ** -8 * want.abs()
+    r = b * c.nn + j
+    err = (out[r].double() - want).abs()
+    assert (err <= tol).all(), (b, j, float((err / tol).max()))
+    err = (lse[r].double() - wlse).abs()
+    assert (err <= 2 * dS + 2.0 ** -18 + 2.0 ** -22 * wlse.abs()).all(), (b, j, float(err.max()))
+
+
+@pytest.mark.parametrize("far", [20, 60, 100])
+@pytest.mark.parametrize("Hq,nn", [(4, 2), (8, 2), (16, 2), (32, 2), (16, 4), (10, 3)])
+def test_finite_keys_of_later_tokens_do_not_reach_a_row(api, Hq, nn, far):
+    """The request's new tokens after a row's own have key scales up to 2^far of
+    the others': the row stays as exact as without them."""
+    lens, D = [200, 129, 3], 128
+    rng = np.random.default_rng(far + Hq)
+    kc = [rng.integers(126, 129, size=(L, 1, 4)) for L in lens]
+    vc = [rng.integers(126, 129, size=(L, 1, 4)) for L in lens]
+    for b, L in enumerate(lens):
+        for j in range(1, nn):
+            if L - nn + j >= 0:
+                kc[b][L - nn + j, 0, j % 4] += far * j // (nn - 1)
+    c = Cache(lens, nn, Hq, 1, D, 64, kc, vc, rng.standard_normal((len(lens) * nn * Hq, D)),
+              seed=far)
+    out, lse = api.kv4_attention(*c.args, next_n=nn, softmax_scale=0.05)
+    assert torch.isfinite(out.float()).all()
+    for b, L in enumerate(lens):
+        if L - nn + 1 > 0:
+            check_row(c, out, lse, b, 0, 0.05)
+
+
+@pytest.mark.parametrize("rows", [8, 16, 24, 64])
+@pytest.mark.parametrize("step", [1, -1])
+def test_key_scales_far_apart_within_a_context(api, rows, step):
+    """Keys whose scales rise (or fall) by 2^40 along the context, and by 2^10
+    between the blocks of one: the logits are the formula's."""
+    L, D = 700, 128
+    rng = np.random.default_rng(rows)
+    at = np.arange(L)[::step]
+    kc = (107 + at * 40 // L)[:, None, None] + rng.integers(-5, 6, size=(L, 1, 4))
+    vc = rng.integers(126, 129, size=(L, 1, 4))
+    scale = 2.0 ** -17
+    c = Cache([L], 1, rows, 1, D, 64, [kc], [vc], rng.standard_normal((rows, D)), seed=rows)
+    out, lse = api.kv4_attention(*c.args, next_n=1, softmax_scale=scale)
+    check_row(c, out, lse, 0, 0, scale)

@@ -1145,14 +1145,17 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kSel))
 // --------------------------------------------- more than 16 rows: tcgen05.mma
 //
 // Tiles of 128 columns by N = 32 or 64 query rows, two products a tile:
-//   S [128 x N]  = K' q^T    K' = K 2^-ref in TMEM, a key a lane: warps 0-3, one
+//   S [128 x N]  = K' q^T    K' = K / 2^k in TMEM, a key a lane: warps 0-3, one
 //                            key a thread
 //   O^T [D x N] += V'^T P    V' = V 2^-ref and P in shared memory, one row per
 //                            column: warps 4-7 make V', both kinds P, half of
 //                            the query rows each
-// One scale reference for a CTA's keys and one for its values, raised when a
-// scale passes it by 2^kSlack; references of the weights likewise lag behind
-// the rows' maxima.  Raising any is rare and costs one more round of the tile.
+// A key is scaled by itself: 2^k is its largest block's scale less kKeyRoom, so
+// that fp16 holds its blocks exactly down to 2^-35 of that, and every key's
+// thread multiplies its logits by 2^k.  The values have one reference for a CTA,
+// raised when a scale passes it by 2^kSlack; references of the weights likewise
+// lag behind the rows' maxima.  Raising any is rare and costs one more round of
+// the tile.
 // 64 requests of up to 16384 keys, 64 rows on one head: 54 us for 50 MB (0.9
 // TB/s).  Bound by the chain of a tile's steps (decode, product, softmax,
 // product) with two CTAs an SM to overlap them, which shared memory and TMEM
@@ -1162,7 +1165,10 @@ constexpr int kTcTile = 128;    // columns of a tile: one TMEM lane each
 constexpr int kTcThreads = 256; // warps 0-3: keys; warps 4-7: values; both: softmax
 constexpr int kTcStages = 2;
 constexpr int kTcCtas = 2;      // an SM holds
-constexpr float kUnseen = -3e38f;  // reference of a row that has seen no column
+constexpr int kKeyRoom = 12;    // a key's largest elements are up to 6 * 2^kKeyRoom in fp16
+// Reference of a row that has seen no column.  Its factor F is 1 until then, so
+// that any logit is far above it.
+constexpr float kUnseen = -3e38f;
 
 // Shared memory of a CTA (1024-byte aligned).
 template <int D, int N>
@@ -1183,7 +1189,7 @@ struct TcLayout {
   static constexpr int kAlpha = kLimit + N * 4;
   static constexpr int kNan = kAlpha + N * 4;
   static constexpr int kPart = kNan + N * 4;       // [4][row] of a reduction over warps
-  static constexpr int kRed = kPart + 4 * N * 4;   // [4]: maxima of the warps of one kind, twice
+  static constexpr int kRed = kPart + 4 * N * 4;   // [4]: maxima of the value warps; O's factor
   static constexpr int kBars = (kRed + 32 + 7) / 8 * 8;
   static constexpr int kSlot = kBars + 8 * (kTcStages + 2);
   static constexpr int kWalk = kSlot + 16;
@@ -1272,17 +1278,7 @@ __device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity,
   }
 }
 
-// Barrier of the four warps of one kind, with an OR of their votes.
-__device__ __forceinline__ bool kind_barrier_or(int id, bool vote) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\t"
-      "barrier.cta.red.or.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(static_cast<uint32_t>(vote))
-      : "memory");
-  return r != 0;
-}
+// Barrier of the four warps of one kind.
 __device__ __forceinline__ void kind_barrier(int id) {
   asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory");
 }
@@ -1493,8 +1489,8 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
   float l[kHalf];  // the key lane's share of their sums
 #pragma unroll
   for (int n = 0; n < kHalf; ++n) l[n] = 0.f;
-  // Reference of this kind's scales (E8M0 bits as fp32): raised to the largest
-  // so far when one passes it by 2^kSlack.
+  // Value warps: reference of the scales (E8M0 bits as fp32), raised to the
+  // largest so far when one passes it by 2^kSlack.
   float ref = -1.f, ref_inv = 0.f;
 
   constexpr uint32_t kIdescS = mma_idesc(0, 128, N);
@@ -1520,58 +1516,69 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
     }
     const uint32_t base = sb + Lay::kTiles + s * Lay::kTileBytes;
     // ---------------------------------------------------------------- scales
-    uint32_t sw;  // of the key, or of the value
+    uint32_t kw, vw;  // of the key, and of the value
     {
       const uint32_t at = sb + Lay::kScales + (s * kTcTile + key) * Lay::kSc;
       if constexpr (D == 128) {
-        sw = lds32(at + (is_v ? 4 : 0));
+        const uint2 u = lds64(at);
+        kw = u.x, vw = u.y;
       } else {
         const uint32_t u = lds32(at);
-        sw = is_v ? u >> 16 : u & 0xFFFFu;
+        kw = u & 0xFFFFu, vw = u >> 16;
       }
-      if (!valid) sw = 0u;
+      if (!valid) kw = vw = 0u;
     }
-    uint32_t sf[G];
-    sf[0] = e8m0_bits<0>(sw), sf[1] = e8m0_bits<1>(sw);
-    if constexpr (D == 128) sf[2] = e8m0_bits<2>(sw), sf[3] = e8m0_bits<3>(sw);
-    bool k_nan = false;
-    if (has_ff(sw)) {
-      // NaN scales (rare): a key's makes its logits NaN, a value's makes its
-      // 32 channels of every row that sees the column NaN at the end.
-      k_nan = !is_v;
+    // A logit is ks times the product.  NaN scales (rare) take no part in the
+    // products: a key's makes its logits NaN, a value's makes its 32 channels of
+    // every row that sees the column NaN at the end.
+    const bool k_nan = has_ff(kw);
+    auto bits_of = [](uint32_t w, uint32_t (&f)[G]) {
+      f[0] = e8m0_bits<0>(w), f[1] = e8m0_bits<1>(w);
+      if constexpr (D == 128) f[2] = e8m0_bits<2>(w), f[3] = e8m0_bits<3>(w);
+      if (has_ff(w))
 #pragma unroll
-      for (int g = 0; g < G; ++g)
-        if (sf[g] == 0x7F800000u) {
-          sf[g] = 0u;
-          if (is_v)
+        for (int g = 0; g < G; ++g)
+          if (f[g] == 0x7F800000u) f[g] = 0u;
+    };
+    auto top_of = [](const uint32_t (&f)[G]) {
+      uint32_t t = f[0];
+#pragma unroll
+      for (int g = 1; g < G; ++g) t = max(t, f[g]);
+      return t;
+    };
+    uint32_t sf[G];
+    bits_of(kw, sf);
+    // 2^kKeyRoom / its inverse and it are normal numbers from here on.
+    const uint32_t k_top = max(top_of(sf), static_cast<uint32_t>(kKeyRoom + 1) << 23);
+    const float ks = __uint_as_float(k_top - (static_cast<uint32_t>(kKeyRoom) << 23));
+    if (is_v) {
+      bits_of(vw, sf);
+      if (has_ff(vw))
+        for (int g = 0; g < G; ++g)
+          if (((vw >> (8 * g)) & 255u) == 255u)
             for (int n = 0; n < N; ++n)
               if (col < limit[n]) atomicOr(&nan_rows[n], 1u << g);
-        }
     }
-    uint32_t top = sf[0];
-#pragma unroll
-    for (int g = 1; g < G; ++g) top = max(top, sf[g]);
-    const bool passes = valid && __uint_as_float(top) > ref * 256.f;
-    // The largest scale of this kind in the tile (rare: a new reference).
+    const uint32_t top = top_of(sf);
+    // Value warps: the largest scale in the tile (rare: a new reference).
     auto new_ref = [&]() {
       const uint32_t t = __reduce_max_sync(0xffffffffu, top);
-      if (lane == 0) red[warp] = t;
-      kind_barrier(is_v ? 2 : 1);
-      const uint32_t* r = red + (is_v ? 4 : 0);
+      if (lane == 0) red[warp & 3] = t;
+      kind_barrier(2);
       return fmaxf(fmaxf(ref, 1.17549435e-38f),
-                   __uint_as_float(max(max(r[0], r[1]), max(r[2], r[3]))));
+                   __uint_as_float(max(max(red[0], red[1]), max(red[2], red[3]))));
     };
     uint32_t fac[G];
-    auto factors = [&]() {
+    auto factors = [&](float inv) {
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const float x = __uint_as_float(sf[g]) * ref_inv;
-        fac[g] = k_nan ? 0x7E007E00u : pack_f16(x, x);
+        const float x = __uint_as_float(sf[g]) * inv;
+        fac[g] = pack_f16(x, x);
       }
     };
     // V' = V 2^-ref, one channel-major row per key.
     auto put_values = [&]() {
-      factors();
+      factors(ref_inv);
 #pragma unroll
       for (int c = 0; c < kChunks / 2; ++c) {
         const uint4 u = lds128(base + Layout<D, 1>::chunk_at(key, kChunks / 2 + c));
@@ -1589,20 +1596,13 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
         }
       }
     };
-    bool again = false;  // this kind's reference is new: what it went into is done once more
+    bool again = false;  // the values' reference is too low: they are written once more
     if (!is_v) {
-      // ------------------------------------------- K' = K 2^-ref to TMEM, S = K' q^T
-      if (kind_barrier_or(1, passes)) {
-        const float r = new_ref();
-        if (tid < N) {
-          const float m = fz[tid].y;  // an accumulator value: in the new unit
-          fz[tid] = make_float2(row_f[tid] * r, m == kUnseen ? m : m * (ref / r));
-        }
-        ref = r;
-        ref_inv = 1.f / r;
-        again = true;
-      }
-      factors();
+      // ------------------------------------------- K' = K / 2^k to TMEM, S = K' q^T
+      factors(__uint_as_float(0x7F000000u + (static_cast<uint32_t>(kKeyRoom) << 23) - k_top));
+      if (k_nan)
+#pragma unroll
+        for (int g = 0; g < G; ++g) fac[g] = 0x7E007E00u;
 #pragma unroll
       for (int c = 0; c < kChunks / 2; ++c) {
         const uint4 u = lds128(base + Layout<D, 1>::chunk_at(key, c));
@@ -1635,7 +1635,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
       if (tile > 0 && !mbar_wait_long(o_done, (done - 1) & 1, abort_flag)) fail = true;
     } else {
       if (tile > 0 && !mbar_wait_long(o_done, (done - 1) & 1, abort_flag)) fail = true;
-      again = passes;
+      again = valid && __uint_as_float(top) > ref * 256.f;
       put_values();
     }
     if (!mbar_wait_long(s_done, done & 1, abort_flag)) fail = true;
@@ -1668,7 +1668,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
           const float4 f = *reinterpret_cast<const float4*>(&fz[n0 + c + j]);
-          const float e0 = (x[j] - f.y) * f.x, e1 = (x[j + 1] - f.w) * f.z;
+          const float e0 = fmaf(x[j], ks, -f.y) * f.x, e1 = fmaf(x[j + 1], ks, -f.w) * f.z;
           mx = fmaxf(mx, fmaxf(e0, e1));
           pr[c + j] = ex2(e0), pr[c + j + 1] = ex2(e1);
         }
@@ -1693,7 +1693,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
       tc_fence_after_sync();
       if (is_v) {
         const float r = new_ref();
-        if (tid == 128) red[0] = __float_as_uint(r == ref ? 1.f : ref / r);
+        if (tid == 128) red[4] = __float_as_uint(r == ref ? 1.f : ref / r);
         if (r != ref) {
           ref = r;
           ref_inv = 1.f / r;
@@ -1709,13 +1709,13 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
         for (int j = 0; j < 8; ++j) {
           const int n = n0 + c + j;
           // A NaN stays one without a reference.
-          const float v = x[j] == x[j] ? x[j] : -INFINITY;
+          const float v = x[j] == x[j] ? x[j] * ks : -INFINITY;
           const uint32_t w = __reduce_max_sync(0xffffffffu, order_f32(v));
           if (lane == 0) part[(warp & 3) * N + n] = w;
         }
       }
       __syncthreads();
-      const float down = __uint_as_float(red[0]);
+      const float down = __uint_as_float(red[4]);
       if (tid < N) {
         const float2 f = fz[tid];
         const float m = unorder_f32(max(max(part[tid], part[N + tid]),
@@ -1723,7 +1723,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
         float a = 1.f;
         if (m > f.y && (f.y == kUnseen || (m - f.y) * f.x > kSlack)) {
           a = f.y == kUnseen ? 0.f : ex2((f.y - m) * f.x);
-          fz[tid].y = m;
+          fz[tid] = make_float2(row_f[tid], m);
         }
         alpha[tid] = a;
       }
@@ -1753,7 +1753,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
         tmem_load8(lanes + Lay::kTmemS + n0 + c, v);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          v[j] *= fz[n0 + c + j].x;
+          v[j] = v[j] * ks * fz[n0 + c + j].x;
         const int n = n0 + c;
         if (col < c1 && n < p.score_rows)
           *reinterpret_cast<float4*>(dst + n) = make_float4(v[0], v[1], v[2], v[3]);
