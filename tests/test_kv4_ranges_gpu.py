@@ -238,3 +238,64 @@ def test_key_scales_far_apart_within_a_context(api, rows, step):
     c = Cache([L], 1, rows, 1, D, 64, [kc], [vc], rng.standard_normal((rows, D)), seed=rows)
     out, lse = api.kv4_attention(*c.args, next_n=1, softmax_scale=scale)
     check_row(c, out, lse, 0, 0, scale)
+
+
+@pytest.mark.parametrize("far", [6, 20, 60, 100])
+@pytest.mark.parametrize("Hq,nn", [(4, 2), (8, 2), (16, 2), (32, 2), (16, 4), (10, 3), (1, 40)])
+def test_finite_values_of_later_tokens_do_not_reach_a_row(api, Hq, nn, far):
+    """The new tokens' value scales rise to 2^far of the others': every row is as
+    exact as the values that it sees allow, block by block, and so are the keys'
+    weights."""
+    lens, D = [200, 129, 64, 300, 3], 128
+    rng = np.random.default_rng(far + Hq)
+    kc = [rng.integers(126, 129, size=(L, 1, 4)) for L in lens]
+    vc = [rng.integers(126, 129, size=(L, 1, 4)) for L in lens]
+    for b, L in enumerate(lens):
+        for j in range(1, nn):
+            if L - nn + j >= 0:
+                vc[b][L - nn + j, 0, [j % 4, (j + b) % 4]] += far * j // (nn - 1)
+    c = Cache(lens, nn, Hq, 1, D, 64, kc, vc, rng.standard_normal((len(lens) * nn * Hq, D)),
+              seed=far)
+    out, lse = api.kv4_attention(*c.args, next_n=nn, softmax_scale=0.05)
+    acc = torch.zeros(len(lens), c.table.shape[1] * 64, device="cuda")
+    out2, lse2 = api.kv4_attention(*c.args, next_n=nn, softmax_scale=0.05, key_weights=acc)
+    assert torch.equal(out.view(torch.int16), out2.view(torch.int16)) and torch.equal(lse, lse2)
+    for b, L in enumerate(lens):
+        want, most = torch.zeros(L, dtype=torch.float64, device="cuda"), 0.0
+        for j in range(nn):
+            if L - nn + j + 1 <= 0:
+                assert (out[b * nn + j] == 0).all() and (lse[b * nn + j] == -torch.inf).all()
+                continue
+            check_row(c, out, lse, b, j, 0.05)
+            row = c.row(b, j, 0.05)
+            want += row[2].sum(0)
+            most = max(most, rel_of(row[4]))
+        tol = (most + nn * Hq * 2.0 ** -24) * want
+        assert ((acc[b, :L].double() - want).abs() <= tol).all(), b
+        assert (acc[b, L:] == 0).all()
+
+
+@pytest.mark.parametrize("rows", [8, 16, 24, 64])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kind", ["blocks", "rise", "fall", "keys"])
+def test_value_scales_far_apart(api, rows, D, kind):
+    """Value scales 2^+-18 apart between the blocks of a head (each is as exact as
+    alone), rising or falling by 2^60 along the context, or 2^+-18 at random."""
+    L, G = 700, D // 32
+    rng = np.random.default_rng(rows)
+    kc = rng.integers(126, 129, size=(L, 1, G))
+    vc = rng.integers(126, 129, size=(L, 1, G))
+    if kind == "blocks":
+        vc += (np.arange(G) * 37 // G - 18)[None, None]
+    elif kind == "keys":
+        vc += rng.integers(-18, 19, size=(L, 1, G))
+    else:
+        vc += (np.arange(L)[::1 if kind == "rise" else -1] * 60 // L - 30)[:, None, None]
+    c = Cache([L], 1, rows, 1, D, 64, [kc], [vc], rng.standard_normal((rows, D)), seed=rows)
+    for call in ("every", "selected"):
+        if call == "every":
+            out, lse = api.kv4_attention(*c.args, next_n=1, softmax_scale=0.1)
+        else:
+            sel = torch.randperm(L, dtype=torch.int32, device="cuda")[None]
+            out, lse = api.kv4_attention_topk(*c.args, sel, next_n=1, softmax_scale=0.1)
+        check_row(c, out, lse, 0, 0, 0.1)

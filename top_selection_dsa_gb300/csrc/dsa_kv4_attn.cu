@@ -24,9 +24,12 @@
 //         m lags by up to a slack, so that the accumulated output is rescaled
 //         seldom.
 //   O     += V^T P (O += P V): V's elements again the codes' values, and the
-//         value scales multiplied into P (fp16) once per block of 32 channels,
-//         relative to the largest scale met so far, 2^x: P 2^(e - x) <= 1, and
-//         terms below 2^-24 of that vanish.
+//         value scales multiplied into P (fp16), by block of 32 channels
+//         relative to the largest scale met so far, 2^x, which lags behind by up
+//         to kValueMost; terms below 2^-24 of 2^x vanish.  A request's new tokens do
+//         not all see one another: a later one's larger scale is met in a
+//         window of columns of its own, after those that every row sees, and
+//         rows that do not see it keep their 2^x.
 // More rows: kv4_attn_tc_kernel, the same on the tensor cores' tcgen05 form
 // (further down).
 //
@@ -69,6 +72,7 @@ constexpr int kTile = 64;       // columns a warp takes at a time
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 2;
+constexpr float kValueMost = 4.f;  // a value scale over its reference, which lags behind the largest
 // Three fill an SM's registers (168 a thread) and shared memory.  On a selection
 // that leaves the L1, through which the gathers of single records go, 28 KB, and
 // two CTAs' fewer copies in flight are faster: 128 rows of 2048 selected keys, 8
@@ -174,8 +178,8 @@ __device__ __forceinline__ uint32_t has_ff(uint32_t w) {
 // the swizzle is a function of the address; there is no static shared memory,
 // so the block begins so aligned), then by warp the tiles' scales, what the
 // tile in work needs of them -- 2^e of every key's blocks (fp32), and the
-// value factors as fp16 pairs in the order of P's fragments -- and the ring's
-// barriers.
+// value factors as fp16 pairs in the order of P's fragments -- the ring's
+// barriers, and the value scales' references.
 template <int D, int NT>
 struct Layout {
   static constexpr int G = D / kMxBlock;        // scale blocks of a row
@@ -189,7 +193,11 @@ struct Layout {
   static constexpr int kKeyScales = kScales + kStages * kScaleBytes;
   static constexpr int kFactors = kKeyScales + (NT > 1 ? 0 : kTile * G * 4);
   static constexpr int kBarriers = kFactors + kTile * G * 2;
-  static constexpr int kWarpRest = (kBarriers + 8 * kStages + 15) / 16 * 16;
+  static constexpr int kInvUnit = kBarriers + 8 * kStages;    // 2^-x by block
+  static constexpr int kRowUnits = kInvUnit + 16;             // every row's x, E8M0 by block
+  static constexpr int kNext = kRowUnits + NT * 8 * 4;        // where the tile's next window begins
+  static constexpr int kWarpRest = kNext + 16;
+  static_assert(kInvUnit % 16 == 0 && kWarpRest % 16 == 0, "");
   // Then, with two row tiles, the query fragments and their factors.
   static constexpr int kQueries = kWarps * (kWarpTiles + kWarpRest);
   static constexpr int kFactorF = kQueries + (NT > 1 ? NT * G * 32 * 16 : 0);
@@ -703,7 +711,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kSel))
   float thr[2], m[2], l[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) thr[i] = -INFINITY, m[i] = l[i] = 0.f;
-  float unit = 0.f, inv_unit = 0.f;  // o is in units of the largest value scale so far
+  // o is in units of its block's largest value scale so far.
+  const uint32_t inv_at = rest + Lay::kInvUnit, row_units_at = rest + Lay::kRowUnits;
+  if (lane < 4) sts32(inv_at + lane * 4, 0x7E800000u);  // 2^126
+  if (lane < kRows) sts32(row_units_at + lane * 4, 0x01010101u);
+  const uint32_t next_at = rest + Lay::kNext;  // 0: the tile has no other window
+  if (lane == 0) sts32(next_at, 0u);
+  __syncwarp();
 
   // Lane addresses that do not change from tile to tile: the key chunk of
   // rows pi(r) (+ 8, + 16 ..), the value units of rows 2t and (2t+1)^4.
@@ -718,10 +732,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kSel))
                        : Lay::chunk_at(v_row[i], 2 + (r >> 2)) + (r & 3) * 4;
   const uint32_t ks_at = rest + Lay::kKeyScales, fac_at = rest + Lay::kFactors;
 
-  for (int tile = warp; tile < tiles; tile += kWarps) {
+  for (int tile = warp; tile < tiles;) {
     locate(tile + kStages * kWarps);  // what it reads returns under this tile's work
     const int col0 = c0 + tile * kTile;
-    uint2 live;  // columns of this tile
+    const bool tail = !kSel && col0 + kTile > all_see;  // not every row sees all of it
+    const int first = tail ? static_cast<int>(lds32(next_at)) : 0;  // of the window
+    uint2 live;  // columns of this tile, and window
     if constexpr (kSel) {
       cp_async_wait<kStages - 1>();
       __syncwarp();
@@ -735,6 +751,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kSel))
       const int n = c1 - col0;
       live.x = n >= 32 ? 0xffffffffu : (1u << n) - 1u;
       live.y = n >= 64 ? 0xffffffffu : (n > 32 ? (1u << (n - 32)) - 1u : 0u);
+      if (first > 0) {
+        live.x &= first >= 32 ? 0u : ~0u << first;
+        live.y &= first > 32 ? ~0u << (first - 32) : ~0u;
+        __syncwarp();
+        if (lane == 0) sts32(next_at, 0u);
+      }
     }
     const uint32_t base = ring + s * Lay::kTileBytes;
     const uint32_t sbase = rest + Lay::kScales + s * Lay::kScaleBytes;
@@ -744,10 +766,23 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kSel))
       // Lane 4 q8 + t takes the keys of rows 2t and 2t + 1 of the q8-th group
       // of eight: one fragment pair.
       {
-        uint32_t kw[2], vw[2], vf[2][G];
+        uint32_t kw[2], vw[2];
+        float inv[G], vs[2][G];  // references' inverses; value scales over their references
         int key[2];
-        uint32_t top = 0;  // scales order as their bits
-        bool bad = false;
+        if constexpr (D == 128) {
+          const uint4 u = lds128(inv_at);
+          inv[0] = __uint_as_float(u.x), inv[1] = __uint_as_float(u.y);
+          inv[2] = __uint_as_float(u.z), inv[3] = __uint_as_float(u.w);
+        } else {
+          const uint2 u = lds64(inv_at);
+          inv[0] = __uint_as_float(u.x), inv[1] = __uint_as_float(u.y);
+        }
+        auto value_scales = [&](uint32_t w, float (&f)[G]) {
+          f[0] = __uint_as_float(e8m0_bits<0>(w)), f[1] = __uint_as_float(e8m0_bits<1>(w));
+          if constexpr (D == 128)
+            f[2] = __uint_as_float(e8m0_bits<2>(w)), f[3] = __uint_as_float(e8m0_bits<3>(w));
+        };
+        bool rare = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           key[i] = r * 8 + v_row[i];
@@ -758,63 +793,124 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kSel))
             const uint32_t u = lds32(sbase + key[i] * 4);
             kw[i] = u & 0xFFFFu, vw[i] = u >> 16;
           }
-          if (!(((r >= 4 ? live.y : live.x) >> (key[i] & 31)) & 1)) kw[i] = vw[i] = 0u;
-          bad |= has_ff(kw[i]) != 0;
-          vf[i][0] = e8m0_bits<0>(vw[i]), vf[i][1] = e8m0_bits<1>(vw[i]);
-          if constexpr (D == 128) vf[i][2] = e8m0_bits<2>(vw[i]), vf[i][3] = e8m0_bits<3>(vw[i]);
-#pragma unroll
-          for (int g = 0; g < G; ++g) top = max(top, vf[i][g]);
-        }
-        if (__any_sync(0xffffffffu, bad || top == 0x7F800000u)) {
-          // NaN scales (code 255; rare).  A key's makes its logits NaN below;
-          // a value's makes its 32 channels of every row that sees the column
-          // NaN, here, and takes no part in the products.
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t from = __ballot_sync(0xffffffffu, has_ff(kw[i]) != 0);
-            while (from) {
-              const int src = __ffs(from) - 1;
-              from &= from - 1;
-              const int k = __shfl_sync(0xffffffffu, key[i], src);
-              if (k < 32) nan.x |= 1u << k;
-              else nan.y |= 1u << (k - 32);
-            }
-            from = __ballot_sync(0xffffffffu, has_ff(vw[i]) != 0);
-            while (from) {
-              const int src = __ffs(from) - 1;
-              from &= from - 1;
-              const uint32_t word = __shfl_sync(0xffffffffu, vw[i], src);
-              const int col = col0 + __shfl_sync(0xffffffffu, key[i], src);
-              const bool sees[2] = {col < limit(0), col < limit(1)};
-#pragma unroll
-              for (int g = 0; g < G; ++g)
-                if (((word >> (8 * g)) & 255u) == 255u)
-#pragma unroll
-                  for (int x = 0; x < kPerBlock; ++x)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                      if (sees[row_ix(j)]) o[kPerBlock * g + x][j] = __uint_as_float(0x7FC00000u);
+          if constexpr (NT > 1 && !kSel) {
+            // A later window: the words made way for the first one's factors.
+            if (first > 0 && col0 + key[i] < c1) {
+              const int col = col0 + key[i];
+              const uint8_t* at = p.scales +
+                                  ((static_cast<int64_t>(page_of(__ldg(table + (col >> p.log_bs))))
+                                    << p.log_bs) + (col & bs_mask)) * Lay::kSc;
+              if constexpr (D == 128) {
+                const uint2 u = *reinterpret_cast<const uint2*>(at);
+                kw[i] = u.x, vw[i] = u.y;
+              } else {
+                const uint32_t u = *reinterpret_cast<const uint32_t*>(at);
+                kw[i] = u & 0xFFFFu, vw[i] = u >> 16;
+              }
             }
           }
-          top = 0;
+          if (!(((r >= 4 ? live.y : live.x) >> (key[i] & 31)) & 1)) kw[i] = vw[i] = 0u;
+          rare |= has_ff(kw[i]) != 0;
+          value_scales(vw[i], vs[i]);
+          float most = 0.f;
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            vs[i][g] *= inv[g];
+            most = fmaxf(most, vs[i][g]);
+          }
+          rare |= most > kValueMost;
+        }
+        if (__any_sync(0xffffffffu, rare)) {
+          if (__any_sync(0xffffffffu, has_ff(kw[0]) | has_ff(kw[1]) | has_ff(vw[0]) |
+                                          has_ff(vw[1]))) {
+            // NaN scales (code 255).  A key's makes its logits NaN below; a
+            // value's makes its 32 channels of every row that sees the column
+            // NaN, here, and takes no part in the products.
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t from = __ballot_sync(0xffffffffu, has_ff(kw[i]) != 0);
+              while (from) {
+                const int src = __ffs(from) - 1;
+                from &= from - 1;
+                const int k = __shfl_sync(0xffffffffu, key[i], src);
+                if (k < 32) nan.x |= 1u << k;
+                else nan.y |= 1u << (k - 32);
+              }
+              from = __ballot_sync(0xffffffffu, has_ff(vw[i]) != 0);
+              while (from) {
+                const int src = __ffs(from) - 1;
+                from &= from - 1;
+                const uint32_t word = __shfl_sync(0xffffffffu, vw[i], src);
+                const int col = col0 + __shfl_sync(0xffffffffu, key[i], src);
+                const bool sees[2] = {col < limit(0), col < limit(1)};
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+                  if (((word >> (8 * g)) & 255u) == 255u)
+#pragma unroll
+                    for (int x = 0; x < kPerBlock; ++x)
+#pragma unroll
+                      for (int j = 0; j < 4; ++j)
+                        if (sees[row_ix(j)]) o[kPerBlock * g + x][j] = __uint_as_float(0x7FC00000u);
+              }
+#pragma unroll
+              for (int g = 0; g < G; ++g)
+                if (((vw[i] >> (8 * g)) & 255u) == 255u) vw[i] &= ~(255u << (8 * g));
+            }
+          }
+          // New references: the largest scales of the columns before w0, which
+          // the same rows see.  The first column from w0 on whose scale is above
+          // them ends the window.
+          const int w0 = tail ? max(all_see - col0, first + 1) : kTile;
+          float up[G];
+          value_scales(vw[0], vs[0]), value_scales(vw[1], vs[1]);
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const uint32_t top = __reduce_max_sync(
+                0xffffffffu, max(key[0] < w0 ? __float_as_uint(vs[0][g]) : 0u,
+                                 key[1] < w0 ? __float_as_uint(vs[1][g]) : 0u));
+            up[g] = fminf(inv[g], __uint_as_float(max(0x7F000000u - top, 0x00800000u)));
+          }
+          if (tail) {
+            int past = kTile;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int g = 0; g < G; ++g)
+                if (key[i] >= w0 && vs[i][g] * up[g] > kValueMost) past = min(past, key[i]);
+            past = __reduce_min_sync(0xffffffffu, past);
+            if (past < kTile) {
+              if (lane == 0) sts32(next_at, past);
+              live.x &= past >= 32 ? ~0u : (1u << past) - 1u;
+              live.y &= past > 32 ? (1u << (past - 32)) - 1u : 0u;
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (key[i] >= past) {
+                  kw[i] = 0u;
+#pragma unroll
+                  for (int g = 0; g < G; ++g) vs[i][g] = 0.f;
+                }
+            }
+          }
+          const bool sees[2] = {kSel || limit(0) > col0 + first, kSel || limit(1) > col0 + first};
+          uint32_t units = 0;
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const float down = up[g] * __uint_as_float(0x7F000000u - __float_as_uint(inv[g]));
+            units |= (254u - (__float_as_uint(up[g]) >> 23)) << (8 * g);
+            vs[0][g] *= up[g], vs[1][g] *= up[g];
+#pragma unroll
+            for (int x = 0; x < kPerBlock; ++x)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (sees[row_ix(j)]) o[kPerBlock * g + x][j] *= down;
+          }
+          __syncwarp();
 #pragma unroll
           for (int i = 0; i < 2; ++i)
+            if (sees[i] && (NT == 1 ? r == 0 : t == 0)) sts32(row_units_at + row_of(i) * 4, units);
+          if (lane == 0)
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-              if (vf[i][g] == 0x7F800000u) vf[i][g] = 0u;
-              top = max(top, vf[i][g]);
-            }
-        }
-        top = __reduce_max_sync(0xffffffffu, top);
-        if (top > __float_as_uint(unit)) {
-          const float up = __uint_as_float(top);
-          const float down = unit == 0.f ? 0.f : unit / up;
-          unit = up;
-          inv_unit = 1.f / up;
-#pragma unroll
-          for (int x = 0; x < kOut; ++x)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[x][j] *= down;
+            for (int g = 0; g < G; ++g) sts32(inv_at + g * 4, __float_as_uint(up[g]));
         }
         if constexpr (NT == 1) {
           // The key scales as fp32, where rows r of a group of eight find
@@ -840,8 +936,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kSel))
         uint32_t fac[G];
 #pragma unroll
         for (int g = 0; g < G; ++g)
-          fac[g] = pack_f16(__uint_as_float(vf[0][g]) * inv_unit,
-                            __uint_as_float(vf[1][g]) * inv_unit);
+          fac[g] = pack_f16(vs[0][g], vs[1][g]);
         if constexpr (D == 128) sts128(fac_at + lane * 16, fac[0], fac[1], fac[2], fac[3]);
         else sts64(fac_at + lane * 8, fac[0], fac[1]);
         __syncwarp();
@@ -952,7 +1047,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kSel))
 #pragma unroll
             for (int j = 0; j < 4; j += NT == 1 ? 2 : 1) {
               const int col = col0 + half * 32 + key_of(x, j);
-              if (col < c1 && row_of(row_ix(j)) < p.score_rows) {
+              if ((((half ? live.y : live.x) >> key_of(x, j)) & 1) &&
+                  row_of(row_ix(j)) < p.score_rows) {
                 float* at = dst + static_cast<int64_t>(col) * p.score_rows + row_of(row_ix(j));
                 if constexpr (NT == 1)
                   *reinterpret_cast<float2*>(at) =
@@ -1068,6 +1164,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kSel))
         }
       }
     }
+    if (tail && lds32(next_at) > 0) {  // the tile's next window
+      __syncwarp();
+      continue;
+    }
     if (NT == 2 && !kSel)  // the key scales written above make way for a copy
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
@@ -1077,6 +1177,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kSel))
     cols[kStages - 1] = c;
     s = s + 1 == kStages ? 0 : s + 1;
     phase ^= s == 0;
+    tile += kWarps;
   }
   if (!kSel && !ok) {
     // A copy never came: report, and give the others their time to land.
@@ -1087,6 +1188,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kSel))
   // ------------------------------------------- join the four warps, write out
   cp_async_wait<0>();
   __syncthreads();
+  const uint32_t row_units_of[2] = {lds32(row_units_at + row_of(0) * 4),
+                                    lds32(row_units_at + row_of(1) * 4)};
   float* so = reinterpret_cast<float*>(smem);              // [warp][row][D]
   float* sml = so + kWarps * kRows * D;                    // [warp][row][2]
 #pragma unroll
@@ -1101,8 +1204,16 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kSel))
       sml[(warp * kRows + row) * 2 + 1] = sum;
     }
     float* dst = so + (warp * kRows + row) * D;
+    float units[G];
+    {
+      const uint32_t w = row_units_of[i];
+      units[0] = __uint_as_float(e8m0_bits<0>(w)), units[1] = __uint_as_float(e8m0_bits<1>(w));
+      if constexpr (D == 128)
+        units[2] = __uint_as_float(e8m0_bits<2>(w)), units[3] = __uint_as_float(e8m0_bits<3>(w));
+    }
 #pragma unroll
     for (int g = 0; g < G; ++g) {
+      const float unit = units[g];
       if constexpr (NT == 1) {
         *reinterpret_cast<float4*>(dst + 32 * g + 4 * r) =
             make_float4(o[2 * g][i] * unit, o[2 * g][2 + i] * unit, o[2 * g + 1][i] * unit,
@@ -1152,10 +1263,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kSel))
 //                            the query rows each
 // A key is scaled by itself: 2^k is its largest block's scale less kKeyRoom, so
 // that fp16 holds its blocks exactly down to 2^-35 of that, and every key's
-// thread multiplies its logits by 2^k.  The values have one reference for a CTA,
-// raised when a scale passes it by 2^kSlack; references of the weights likewise
-// lag behind the rows' maxima.  Raising any is rare and costs one more round of
-// the tile.
+// thread multiplies its logits by 2^k.  The values have a reference for each
+// block of 32 channels, raised when a scale passes it by 2^8 (V' is then 6 *
+// 2^kTcValueRoom at most, and exact down to 2^-28 of that scale); references of the
+// weights likewise lag behind the rows' maxima.  Raising any is rare and costs one
+// more round of the tile.  As above, a later token's scale that would raise the
+// values' is met in a window of its own, and rows that do not see it keep theirs.
 // 64 requests of up to 16384 keys, 64 rows on one head: 54 us for 50 MB (0.9
 // TB/s).  Bound by the chain of a tile's steps (decode, product, softmax,
 // product) with two CTAs an SM to overlap them, which shared memory and TMEM
@@ -1166,6 +1279,8 @@ constexpr int kTcThreads = 256; // warps 0-3: keys; warps 4-7: values; both: sof
 constexpr int kTcStages = 2;
 constexpr int kTcCtas = 2;      // an SM holds
 constexpr int kKeyRoom = 12;    // a key's largest elements are up to 6 * 2^kKeyRoom in fp16
+constexpr int kTcValueRoom = 5;   // V' at a new reference
+constexpr float kTcValueMost = 8192.f;  // a scale over its reference: 2^(kTcValueRoom + 8)
 // Reference of a row that has seen no column.  Its factor F is 1 until then, so
 // that any logit is far above it.
 constexpr float kUnseen = -3e38f;
@@ -1189,8 +1304,12 @@ struct TcLayout {
   static constexpr int kAlpha = kLimit + N * 4;
   static constexpr int kNan = kAlpha + N * 4;
   static constexpr int kPart = kNan + N * 4;       // [4][row] of a reduction over warps
-  static constexpr int kRed = kPart + 4 * N * 4;   // [4]: maxima of the value warps; O's factor
-  static constexpr int kBars = (kRed + 32 + 7) / 8 * 8;
+  static constexpr int kRowUnits = kPart + 4 * N * 4;  // [row]: O's units, E8M0 by block
+  static constexpr int kInvUnit = kRowUnits + N * 4;   // [4]: 1 / the values' references
+  // Maxima by block of the value warps; O's factors and the new references'
+  // inverses by block; a window's end.
+  static constexpr int kRed = kInvUnit + 16;
+  static constexpr int kBars = kRed + 25 * 4 + 4;
   static constexpr int kSlot = kBars + 8 * (kTcStages + 2);
   static constexpr int kWalk = kSlot + 16;
   static constexpr int kBytes = kWalk + 128;
@@ -1310,7 +1429,12 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
   float* const alpha = reinterpret_cast<float*>(smem + Lay::kAlpha);
   uint32_t* const nan_rows = reinterpret_cast<uint32_t*>(smem + Lay::kNan);
   uint32_t* const part = reinterpret_cast<uint32_t*>(smem + Lay::kPart);
+  uint32_t* const row_units = reinterpret_cast<uint32_t*>(smem + Lay::kRowUnits);
+  float* const inv_unit = reinterpret_cast<float*>(smem + Lay::kInvUnit);
   uint32_t* const red = reinterpret_cast<uint32_t*>(smem + Lay::kRed);
+  float* const down = reinterpret_cast<float*>(red + 16);
+  float* const new_inv = down + 4;
+  int* const window_end = reinterpret_cast<int*>(red + 24);
 
   if (tid == 0) {
     for (int s = 0; s < kTcStages; ++s) mbar_init(&full[s], 1);
@@ -1328,7 +1452,8 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
   tc_fence_after_sync();
   const uint32_t tmem = *slot;
   const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);  // this warp's 32 lanes
-  uint32_t done = 0;  // tiles so far: their stages and phases
+  uint32_t done = 0;   // tiles so far: their stages and phases
+  uint32_t prods = 0;  // pairs of products so far: their phases
   bool ok = true;
   for (;;) {
   if (tid == 0) walk->next(p);
@@ -1477,8 +1602,10 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
         limit[n] = kSel ? gr.cols
                         : gr.L - p.next_n + min((row0 + n) / p.heads, p.next_n - 1) + 1;
         nan_rows[n] = 0;
+        row_units[n] = 0x01010101u;
       }
     }
+    if (tid < 4) inv_unit[tid] = __uint_as_float(0x7E800000u);  // 2^126
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();
@@ -1489,31 +1616,30 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
   float l[kHalf];  // the key lane's share of their sums
 #pragma unroll
   for (int n = 0; n < kHalf; ++n) l[n] = 0.f;
-  // Value warps: reference of the scales (E8M0 bits as fp32), raised to the
-  // largest so far when one passes it by 2^kSlack.
-  float ref = -1.f, ref_inv = 0.f;
-
+  bool started = false;  // there are products of this span
   constexpr uint32_t kIdescS = mma_idesc(0, 128, N);
   constexpr uint32_t kIdescO = mma_idesc(0, 128, N) | (1u << 15) | (1u << 16);
   constexpr uint32_t kModeP = N == 16 ? 6 : (N == 32 ? 4 : 2);
   for (int tile = 0; tile < tiles; ++tile, ++done) {
     const int s = done % kTcStages;
     locate(tile + kTcStages);
-    const int col = c0 + tile * kTcTile + key;
-    bool valid, fail = false;  // fail: a wait gave up (votes carry it to every thread)
+    const int col0 = c0 + tile * kTcTile, col = col0 + key;
+    bool there, fail = false;  // fail: a wait gave up (votes carry it to every thread)
     if constexpr (kSel) {
       cp_async_wait<kTcStages - 1>();
       // The value warps read scales that the key warps copied.
       __syncthreads();
-      valid = here[0];
+      there = here[0];
     } else {
-      // The last tile's logits were read, for the weights, after its last
-      // barrier: what follows writes over them (S) and what they were read
-      // with (fz).
-      if constexpr (kScores) __syncthreads();
       if (!mbar_wait_long(&full[s], (done / kTcStages) & 1, abort_flag)) fail = true;
-      valid = col < c1;
+      there = col < c1;
     }
+    // Windows of the tile's columns: one, but where a later token's value scale
+    // ends it.
+    for (int lo = 0;;) {
+    // The last tile's logits were read, for the weights, after its last barrier:
+    // what follows writes over them (S) and what they were read with (fz).
+    if constexpr (kScores && !kSel) __syncthreads();
     const uint32_t base = sb + Lay::kTiles + s * Lay::kTileBytes;
     // ---------------------------------------------------------------- scales
     uint32_t kw, vw;  // of the key, and of the value
@@ -1526,7 +1652,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
         const uint32_t u = lds32(at);
         kw = u & 0xFFFFu, vw = u >> 16;
       }
-      if (!valid) kw = vw = 0u;
+      if (!there || key < lo) kw = vw = 0u;
     }
     // A logit is ks times the product.  NaN scales (rare) take no part in the
     // products: a key's makes its logits NaN, a value's makes its 32 channels of
@@ -1559,26 +1685,63 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
             for (int n = 0; n < N; ++n)
               if (col < limit[n]) atomicOr(&nan_rows[n], 1u << g);
     }
-    const uint32_t top = top_of(sf);
-    // Value warps: the largest scale in the tile (rare: a new reference).
-    auto new_ref = [&]() {
-      const uint32_t t = __reduce_max_sync(0xffffffffu, top);
-      if (lane == 0) red[warp & 3] = t;
-      kind_barrier(2);
-      return fmaxf(fmaxf(ref, 1.17549435e-38f),
-                   __uint_as_float(max(max(red[0], red[1]), max(red[2], red[3]))));
+    auto references = [&](float (&inv)[G]) {
+#pragma unroll
+      for (int g = 0; g < G; ++g) inv[g] = inv_unit[g];
     };
-    uint32_t fac[G];
-    auto factors = [&](float inv) {
+    // Value warps: the largest scales of the keys for which `of`, as the warps
+    // put them in `red`; and the references (inverses) that go with them.
+    auto put_tops = [&](bool of) {
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const float x = __uint_as_float(sf[g]) * inv;
-        fac[g] = pack_f16(x, x);
+        const uint32_t t = __reduce_max_sync(0xffffffffu, of ? sf[g] : 0u);
+        if (lane == 0) red[4 * g + (warp & 3)] = t;
       }
     };
-    // V' = V 2^-ref, one channel-major row per key.
-    auto put_values = [&]() {
-      factors(ref_inv);
+    auto top_in = [&](int g) {
+      return max(max(red[4 * g], red[4 * g + 1]), max(red[4 * g + 2], red[4 * g + 3]));
+    };
+    auto raised = [&](float inv, uint32_t t) {
+      constexpr uint32_t kRoom = static_cast<uint32_t>(kTcValueRoom) << 23;
+      return fminf(inv, __uint_as_float(0x7F000000u + kRoom - max(t, kRoom + 0x00800000u)));
+    };
+    // Columns that not every row sees begin new windows: those of [lo, w0) are
+    // seen by the same rows, and raise references; the first one from w0 on that
+    // would ends the window.
+    int hi = kTcTile, w0 = kTcTile;
+    if (!kSel && min(c1, col0 + kTcTile) > all_see) {
+      w0 = max(all_see - col0, lo + 1);
+      if (is_v) put_tops(key < w0);
+      if (tid == 0) *window_end = kTcTile;
+      __syncthreads();
+      if (is_v) {
+        float inv[G];
+        references(inv);
+        bool passes = false, ends = false;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          passes |= __uint_as_float(top_in(g)) * inv[g] > kTcValueMost;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          ends |= __uint_as_float(sf[g]) * (passes ? raised(inv[g], top_in(g)) : inv[g]) >
+                  kTcValueMost;
+        if (key >= w0 && ends) atomicMin(window_end, key);
+      }
+      __syncthreads();
+      hi = *window_end;
+      if (is_v && key >= hi)
+#pragma unroll
+        for (int g = 0; g < G; ++g) sf[g] = 0u;
+    }
+    const bool valid = there && key >= lo && key < hi;
+    // V' = V over the references, one channel-major row per key.
+    auto put_values = [&](const float (&inv)[G]) {
+      uint32_t fac[G];
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const float x = __uint_as_float(sf[g]) * inv[g];
+        fac[g] = pack_f16(x, x);
+      }
 #pragma unroll
       for (int c = 0; c < kChunks / 2; ++c) {
         const uint4 u = lds128(base + Layout<D, 1>::chunk_at(key, kChunks / 2 + c));
@@ -1599,10 +1762,14 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
     bool again = false;  // the values' reference is too low: they are written once more
     if (!is_v) {
       // ------------------------------------------- K' = K / 2^k to TMEM, S = K' q^T
-      factors(__uint_as_float(0x7F000000u + (static_cast<uint32_t>(kKeyRoom) << 23) - k_top));
-      if (k_nan)
+      const float inv =
+          __uint_as_float(0x7F000000u + (static_cast<uint32_t>(kKeyRoom) << 23) - k_top);
+      uint32_t fac[G];
 #pragma unroll
-        for (int g = 0; g < G; ++g) fac[g] = 0x7E007E00u;
+      for (int g = 0; g < G; ++g) {
+        const float x = __uint_as_float(sf[g]) * inv;
+        fac[g] = k_nan ? 0x7E007E00u : pack_f16(x, x);
+      }
 #pragma unroll
       for (int c = 0; c < kChunks / 2; ++c) {
         const uint4 u = lds128(base + Layout<D, 1>::chunk_at(key, c));
@@ -1632,16 +1799,20 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
       }
       __syncwarp();
       // P's buffer is free once the last tile's products are done.
-      if (tile > 0 && !mbar_wait_long(o_done, (done - 1) & 1, abort_flag)) fail = true;
+      if (started && !mbar_wait_long(o_done, (prods - 1) & 1, abort_flag)) fail = true;
     } else {
-      if (tile > 0 && !mbar_wait_long(o_done, (done - 1) & 1, abort_flag)) fail = true;
-      again = valid && __uint_as_float(top) > ref * 256.f;
-      put_values();
+      if (started && !mbar_wait_long(o_done, (prods - 1) & 1, abort_flag)) fail = true;
+      float inv[G];
+      references(inv);
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        again |= key < w0 && __uint_as_float(sf[g]) * inv[g] > kTcValueMost;
+      put_values(inv);
     }
-    if (!mbar_wait_long(s_done, done & 1, abort_flag)) fail = true;
+    if (!mbar_wait_long(s_done, prods & 1, abort_flag)) fail = true;
     tc_fence_after_sync();
     // ---------------------------------------------------------------- softmax
-    const bool clean = c0 + (tile + 1) * kTcTile <= min(c1, all_see) && (!kSel || valid);
+    const bool clean = col0 + kTcTile <= min(c1, all_see) && (!kSel || valid);
     if (__any_sync(0xffffffffu, !clean)) {
       // Columns that are not there, or that a row does not see: -inf, written
       // back (their weight is zero whatever the reference).
@@ -1692,13 +1863,19 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
       }
       tc_fence_after_sync();
       if (is_v) {
-        const float r = new_ref();
-        if (tid == 128) red[4] = __float_as_uint(r == ref ? 1.f : ref / r);
-        if (r != ref) {
-          ref = r;
-          ref_inv = 1.f / r;
-          put_values();
+        put_tops(key < w0);
+        kind_barrier(2);
+        float inv[G];
+        references(inv);
+        bool moved = false;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const float up = raised(inv[g], top_in(g));
+          if (tid == 128) down[g] = up / inv[g], new_inv[g] = up;
+          moved |= up != inv[g];
+          inv[g] = up;
         }
+        if (moved) put_values(inv);
       }
       again = false;
 #pragma unroll 1
@@ -1715,7 +1892,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
         }
       }
       __syncthreads();
-      const float down = __uint_as_float(red[4]);
+      if (tid >= 128 && tid < 128 + G) inv_unit[tid - 128] = new_inv[tid - 128];
       if (tid < N) {
         const float2 f = fz[tid];
         const float m = unorder_f32(max(max(part[tid], part[N + tid]),
@@ -1728,16 +1905,27 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
         alpha[tid] = a;
       }
       __syncthreads();
+      if (tid < N && limit[tid] > col0 + lo) {
+        uint32_t units = 0;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          units |= (254u - (__float_as_uint(inv_unit[g]) >> 23)) << (8 * g);
+        row_units[tid] = units;
+      }
 #pragma unroll
       for (int n = 0; n < kHalf; ++n) l[n] *= alpha[n0 + n];
-      if (tile > 0) {
+      if (started) {
+        const float by = down[(key / 4) % G];  // of this lane's channel
 #pragma unroll 1
         for (int c = 0; c < kHalf; c += 8) {
           float o[8];
           tmem_load8(lanes + Lay::kTmemO + n0 + c, o);
           uint32_t r[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(o[j] * (alpha[n0 + c + j] * down));
+          for (int j = 0; j < 8; ++j) {
+            const int n = n0 + c + j;
+            r[j] = __float_as_uint(o[j] * alpha[n] * (limit[n] > col0 + lo ? by : 1.f));
+          }
           tmem_store8(lanes + Lay::kTmemO + n0 + c, r);
         }
         tmem_wait_st();
@@ -1755,9 +1943,9 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
         for (int j = 0; j < 8; ++j)
           v[j] = v[j] * ks * fz[n0 + c + j].x;
         const int n = n0 + c;
-        if (col < c1 && n < p.score_rows)
+        if ((kSel ? col < c1 : valid) && n < p.score_rows)
           *reinterpret_cast<float4*>(dst + n) = make_float4(v[0], v[1], v[2], v[3]);
-        if (col < c1 && n + 4 < p.score_rows)
+        if ((kSel ? col < c1 : valid) && n + 4 < p.score_rows)
           *reinterpret_cast<float4*>(dst + n + 4) = make_float4(v[4], v[5], v[6], v[7]);
         __syncwarp();
       }
@@ -1774,17 +1962,26 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
                       mn_major_desc(sb + Lay::kValues + k * 2048, D == 128 ? kTcTile * 128 : 0,
                                     1024, 2),
                       mn_major_desc(sb + Lay::kP + k * (32 * N), 16, 16 * N, kModeP), kIdescO,
-                      tile > 0 || k > 0);
+                      started || k > 0);
       mma_commit(o_done);
     }
     __syncwarp();
+    started = true;
+    ++prods;
+    if (kSel || hi == kTcTile) break;
+    lo = hi;
+    }
+    if (!ok) break;
     const bool h = fetch(s, tile + kTcStages);
 #pragma unroll
     for (int i = 0; i + 1 < kTcStages; ++i) here[i] = here[i + 1];
     here[kTcStages - 1] = h;
   }
   if (ok && tiles > 0) {
-    if (!mbar_wait_long(o_done, (done - 1) & 1, abort_flag)) ok = false;
+    if (!mbar_wait_long(o_done, (prods - 1) & 1, abort_flag)) {
+      record_error(p.err, kErrTimeout);
+      ok = false;
+    }
   } else if (!ok) {
     // A copy or a product never came: report, and give what is in flight its
     // time.
@@ -1792,8 +1989,8 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
     if (!kSel)
       for (int i = 0; i < kTcStages; ++i)
         mbar_wait_long(&full[(done + i) % kTcStages], ((done + i) / kTcStages) & 1, nullptr);
-    mbar_wait_long(s_done, done & 1, nullptr, 1000000);
-    mbar_wait_long(o_done, done & 1, nullptr, 1000000);
+    mbar_wait_long(s_done, prods & 1, nullptr, 1000000);
+    mbar_wait_long(o_done, prods & 1, nullptr, 1000000);
   }
   cp_async_wait<0>();
   tc_fence_after_sync();
@@ -1801,10 +1998,8 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
   // -------------------------------------------------------------- write out
   // O^T's lane m holds channel 32 g + 4 r + i, m = (r G + g) 4 + i.
   float* const so = reinterpret_cast<float*>(smem + Lay::kValues);  // [row][D]
-  if (tid == 128) alpha[0] = ref;                                  // the values' unit
   __syncthreads();
   if (tiles > 0) {
-    const float unit = alpha[0];
     const int g = (key / 4) % G, r = key / (4 * G), d = 32 * g + 4 * r + key % 4;
 #pragma unroll 1
     for (int c = 0; c < kHalf; c += 8) {
@@ -1812,7 +2007,10 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
       tmem_load8(lanes + Lay::kTmemO + n0 + c, o);
       if (key < D) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) so[(n0 + c + j) * D + d] = o[j] * unit;
+        for (int j = 0; j < 8; ++j) {
+          const int n = n0 + c + j;
+          so[n * D + d] = o[j] * __uint_as_float(((row_units[n] >> (8 * g)) & 255u) << 23);
+        }
       }
       __syncwarp();
     }
