@@ -299,3 +299,27 @@ def test_value_scales_far_apart(api, rows, D, kind):
             sel = torch.randperm(L, dtype=torch.int32, device="cuda")[None]
             out, lse = api.kv4_attention_topk(*c.args, sel, next_n=1, softmax_scale=0.1)
         check_row(c, out, lse, 0, 0, 0.1)
+
+
+@pytest.mark.parametrize("rows", [4, 16, 24, 64])
+@pytest.mark.parametrize("scale", [1e-42, -1e-42])
+def test_a_factor_below_the_smallest_number_leaves_masked_columns_out(api, rows, scale):
+    """Queries of 2^-30 under a subnormal softmax scale: all logits are zero to
+    any precision, and the columns that are not there still have no weight."""
+    L, D = 150, 128
+    rng = np.random.default_rng(rows)
+    kc = rng.integers(126, 129, size=(L, 1, 4))
+    vc = rng.integers(126, 129, size=(L, 1, 4))
+    q = rng.standard_normal((2 * rows // 2, D)) * 2.0 ** -30
+    c = Cache([L], 2, rows // 2, 1, D, 64, [kc], [vc], q, seed=rows)
+    out, lse = api.kv4_attention(*c.args, next_n=2, softmax_scale=scale)
+    for j in range(2):
+        check_row(c, out, lse, 0, j, scale)
+    sel = torch.randperm(L - 1, dtype=torch.int32, device="cuda")[None].repeat(2, 1)
+    sel[:, 5::7] = -1
+    out, lse = api.kv4_attention_topk(*c.args, sel, next_n=2, softmax_scale=scale)
+    keep = sel[0][sel[0] >= 0].long()
+    want = c.V[0][keep, 0].mean(0)
+    top = c.V[0][keep, 0].abs().mean(0)
+    assert ((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -10 * top).all()
+    assert ((lse.double() - np.log(len(keep))).abs() <= 2.0 ** -18 + 2.0 ** -20).all()

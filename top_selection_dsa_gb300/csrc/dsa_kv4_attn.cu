@@ -396,6 +396,13 @@ __device__ __forceinline__ int64_t head_row(const Kv4AttnParams& p, int g, int h
   return row * p.Hq + head * p.heads + (n - j * p.heads);
 }
 
+// What an accumulator of a query row that was divided by 2^E counts in its
+// base-2 logit.  Never 0, which a masked column's -inf would make NaN.
+__device__ __forceinline__ float row_factor(const Kv4AttnParams& p, int E) {
+  if (p.scale_log2e == 0.f) return 1.f;
+  return fmaxf(ldexpf(fabsf(p.scale_log2e), E), 1.4012985e-45f);
+}
+
 // Which kernel takes a CTA's rows (padded to 8, 16, 32 or 64).  Measured, us:
 //   rows of 64 requests of 4096 to 131072 keys, D = 128
 //     16 (4 key/value heads)      mma.sync 303, tcgen05 in tiles of 32 rows 542
@@ -679,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kSel))
         }
       }
     }
-    const float fr = zero ? 1.f : ldexpf(fabsf(p.scale_log2e), E);
+    const float fr = row_factor(p, E);
     if constexpr (NT == 1) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) f[i] = __shfl_sync(0xffffffffu, fr, (2 * t + i) * 4);
@@ -1597,7 +1604,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
                pack_f16(bf16_lo(w[3]) * down, bf16_hi(w[3]) * down));
       }
       if (sub == 0) {
-        row_f[n] = zero ? 1.f : ldexpf(fabsf(p.scale_log2e), E);
+        row_f[n] = row_factor(p, E);
         fz[n] = make_float2(1.f, kUnseen);
         limit[n] = kSel ? gr.cols
                         : gr.L - p.next_n + min((row0 + n) / p.heads, p.next_n - 1) + 1;
