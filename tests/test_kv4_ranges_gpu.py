@@ -35,13 +35,13 @@ class Cache:
     """Random codes under given scale codes: key_codes, value_codes [L, Hkv,
     D/32] of each request; pages in random order."""
 
-    def __init__(self, lens, nn, Hq, Hkv, D, bs, key_codes, value_codes, q, seed=0):
+    def __init__(self, lens, nn, Hq, Hkv, D, bs, key_codes, value_codes, q, seed=0, codes=255):
         rng = np.random.default_rng(seed)
         nblk = [max(-(-L // bs), 1) for L in lens]
         total = sum(nblk)
         perm = rng.permutation(total).astype(np.int32)
         table = np.zeros((len(lens), max(nblk)), np.int32)
-        self.rec = rng.integers(0, 256, size=(total, Hkv, bs, D), dtype=np.uint8)
+        self.rec = rng.integers(0, 256, size=(total, Hkv, bs, D), dtype=np.uint8) & codes
         self.sc = np.full((total, Hkv, bs, D // 16), 127, np.uint8)
         self.K, self.V = [], []
         at = 0
@@ -323,3 +323,21 @@ def test_a_factor_below_the_smallest_number_leaves_masked_columns_out(api, rows,
     top = c.V[0][keep, 0].abs().mean(0)
     assert ((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -10 * top).all()
     assert ((lse.double() - np.log(len(keep))).abs() <= 2.0 ** -18 + 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("rows", [8, 16, 24, 64])
+@pytest.mark.parametrize("L", [90, 700, 5000])
+def test_the_mean_of_values_whose_sum_is_no_number(api, rows, L):
+    """Positive values around 2^123: their weighted sum overflows fp32, their
+    mean does not."""
+    D = 128
+    rng = np.random.default_rng(rows)
+    kc = rng.integers(124, 127, size=(L, 1, 4))
+    vc = rng.integers(246, 249, size=(L, 1, 4))
+    q = rng.standard_normal((rows, D))
+    c = Cache([L], 1, rows, 1, D, 64, [kc], [vc], q, seed=rows, codes=0x77)
+    out, lse = api.kv4_attention(*c.args, next_n=1, softmax_scale=0.05)
+    check_row(c, out, lse, 0, 0, 0.05)
+    sel = torch.randperm(L, dtype=torch.int32, device="cuda")[None]
+    out, lse = api.kv4_attention_topk(*c.args, sel, next_n=1, softmax_scale=0.05)
+    check_row(c, out, lse, 0, 0, 0.05)

@@ -156,8 +156,8 @@ struct Kv4AttnParams {
   int cols;                // columns at most (max context, or sel_k)
   uint16_t* out;           // [B*next_n, Hq, D] bf16
   float* lse;              // [B*next_n, Hq] or null
-  float* part_o;           // [ctas, 2, rows, D]: partial results
-  float* part_ml;          // [ctas, 2, rows, 2]
+  float* part_o;           // [ctas, 2, rows, D]: partial results, each divided by its sum
+  float* part_ml;          // [ctas, 2, rows, 2]: reference and sum of its weights
   int4* spans;             // [groups, Hkv*row_tiles]: what to join, or null when nothing can be
                            // split
   float* scores;           // [groups, Hkv*row_tiles, cols, score_rows]: base-2 logits, for the

@@ -420,9 +420,18 @@ __device__ __forceinline__ float row_factor(const Kv4AttnParams& p, int E) {
 // for does not change the output.
 constexpr bool uses_tc(int rows) { return rows > 16; }
 
+// One over a sum of weights, 0 for that of no columns.  Weighted values are
+// divided by it before they leave the units of their scales: the mean of the
+// values is finite where their sum may not be.
+__device__ __forceinline__ float inverse_sum(float l) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(l));  // within 2^-23
+  return l == 0.f ? 0.f : r;
+}
+
 // One row's four channels d .. d + 3: the result, when the columns summed are
-// all of the row's, else the partial sums `part` (M: reference of the weights,
-// base 2; L: their sum; a: the weighted values).
+// all of the row's, else the partial result `part` (M: reference of the weights,
+// base 2; L: their sum; a: the values' mean under them).
 template <int D, int kRows, bool kSel, bool kScores>
 __device__ __forceinline__ void write_row(const Kv4AttnParams& p, int grp, int ht, int row0,
                                           int nrows, int row, int d, bool whole, int64_t part,
@@ -431,12 +440,11 @@ __device__ __forceinline__ void write_row(const Kv4AttnParams& p, int grp, int h
   const int head = ht / p.row_tiles;
   const int n = row0 + row;
   if (whole) {
-    const float inv = L == 0.f ? 0.f : 1.f / L;
     const float lse2 = M + log2f(L);
     if (n < nrows) {
       const int64_t hr = head_row<kSel>(p, grp, head, n);
       *reinterpret_cast<uint2*>(p.out + hr * D + d) =
-          make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+          make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
       if (d == 0 && p.lse) p.lse[hr] = L == 0.f ? -INFINITY : lse2 * 0.69314718055994531f;
     }
     if (kScores && d == 0)
@@ -1211,6 +1219,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kSel))
       sml[(warp * kRows + row) * 2 + 1] = sum;
     }
     float* dst = so + (warp * kRows + row) * D;
+    const float inv = inverse_sum(sum);
     float units[G];
     {
       const uint32_t w = row_units_of[i];
@@ -1223,14 +1232,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kSel))
       const float unit = units[g];
       if constexpr (NT == 1) {
         *reinterpret_cast<float4*>(dst + 32 * g + 4 * r) =
-            make_float4(o[2 * g][i] * unit, o[2 * g][2 + i] * unit, o[2 * g + 1][i] * unit,
-                        o[2 * g + 1][2 + i] * unit);
+            make_float4(o[2 * g][i] * inv * unit, o[2 * g][2 + i] * inv * unit,
+                        o[2 * g + 1][i] * inv * unit, o[2 * g + 1][2 + i] * inv * unit);
       } else {
 #pragma unroll
         for (int c = 0; c < 2; ++c)  // columns 2t and 2t + 1 of the four tiles
           *reinterpret_cast<float4*>(dst + 32 * g + 8 * t + 4 * c) =
-              make_float4(o[4 * g][2 * i + c] * unit, o[4 * g + 1][2 * i + c] * unit,
-                          o[4 * g + 2][2 * i + c] * unit, o[4 * g + 3][2 * i + c] * unit);
+              make_float4(o[4 * g][2 * i + c] * inv * unit, o[4 * g + 1][2 * i + c] * inv * unit,
+                          o[4 * g + 2][2 * i + c] * inv * unit,
+                          o[4 * g + 3][2 * i + c] * inv * unit);
       }
     }
   }
@@ -1242,12 +1252,17 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kSel))
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sml[(w * kRows + row) * 2]);
     const float z0 = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
+    float share[kWarps], L = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      share[w] = sml[(w * kRows + row) * 2 + 1] * ex2(sml[(w * kRows + row) * 2] - z0);
+      L += share[w];
+    }
+    const float inv = inverse_sum(L);
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = ex2(sml[(w * kRows + row) * 2] - z0);
-      L = fmaf(sml[(w * kRows + row) * 2 + 1], f, L);
+      const float f = share[w] * inv;
       const float4 x = *reinterpret_cast<const float4*>(so + (w * kRows + row) * D + d);
       a.x = fmaf(x.x, f, a.x), a.y = fmaf(x.y, f, a.y);
       a.z = fmaf(x.z, f, a.z), a.w = fmaf(x.w, f, a.w);
@@ -2005,24 +2020,8 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
   // -------------------------------------------------------------- write out
   // O^T's lane m holds channel 32 g + 4 r + i, m = (r G + g) 4 + i.
   float* const so = reinterpret_cast<float*>(smem + Lay::kValues);  // [row][D]
-  __syncthreads();
+  float* const lp = reinterpret_cast<float*>(part);
   if (tiles > 0) {
-    const int g = (key / 4) % G, r = key / (4 * G), d = 32 * g + 4 * r + key % 4;
-#pragma unroll 1
-    for (int c = 0; c < kHalf; c += 8) {
-      float o[8];
-      tmem_load8(lanes + Lay::kTmemO + n0 + c, o);
-      if (key < D) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int n = n0 + c + j;
-          so[n * D + d] = o[j] * __uint_as_float(((row_units[n] >> (8 * g)) & 255u) << 23);
-        }
-      }
-      __syncwarp();
-    }
-    tc_fence_before_sync();
-    float* const lp = reinterpret_cast<float*>(part);
     // Sums over the warp's lanes: halves of the rows change sides until a lane
     // has one row (or lanes share it).
 #pragma unroll
@@ -2045,14 +2044,38 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
     if (lane < kHalf) lp[(warp & 3) * N + n0 + mine] = l[0];
   }
   __syncthreads();
+  if (tiles > 0) {
+    // Every row's sum, in the place of the first part, and its inverse.
+    if (tid < N) {
+      lp[tid] = (lp[tid] + lp[N + tid]) + (lp[2 * N + tid] + lp[3 * N + tid]);
+      alpha[tid] = inverse_sum(lp[tid]);
+    }
+    __syncthreads();
+    const int g = (key / 4) % G, r = key / (4 * G), d = 32 * g + 4 * r + key % 4;
+#pragma unroll 1
+    for (int c = 0; c < kHalf; c += 8) {
+      float o[8];
+      tmem_load8(lanes + Lay::kTmemO + n0 + c, o);
+      if (key < D) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int n = n0 + c + j;
+          so[n * D + d] =
+              o[j] * alpha[n] * __uint_as_float(((row_units[n] >> (8 * g)) & 255u) << 23);
+        }
+      }
+      __syncwarp();
+    }
+    tc_fence_before_sync();
+  }
+  __syncthreads();
   const int64_t pt = static_cast<int64_t>(blockIdx.x) * 2 + (span.first ? 0 : 1);
   for (int e = tid; e < N * D / 4; e += kTcThreads) {
     const int row = e / (D / 4), d = (e % (D / 4)) * 4;
-    const float* lp = reinterpret_cast<const float*>(part);
     float L = 0.f, M = -INFINITY;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     if (tiles > 0) {
-      L = (lp[row] + lp[N + row]) + (lp[2 * N + row] + lp[3 * N + row]);
+      L = lp[row];
       a = *reinterpret_cast<const float4*>(so + row * D + d);
       if (fz[row].y != kUnseen) M = fz[row].y * fz[row].x;
       if ((nan_rows[row] >> (d / 32)) & 1)
@@ -2115,13 +2138,15 @@ __global__ void __launch_bounds__(kJoinThreads)
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  const float inv = inverse_sum(L);
   constexpr int kQuads = D / 4, kHalves = 32 / kQuads, kDeal = (kPer == 1 ? 8 : 1) * kHalves;
   const int q = lane % kQuads;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
   for (int i = (kPer == 1 ? warp * kHalves : 0) + lane / kQuads; i < n; i += kDeal) {
     const float4 x = *reinterpret_cast<const float4*>(p.part_o + part_of(i) * D + q * 4);
-    const float f = ex2(ml_of(i).x - z);
+    const float2 ml = ml_of(i);
+    const float f = ml.y * ex2(ml.x - z) * inv;
     a.x = fmaf(x.x, f, a.x), a.y = fmaf(x.y, f, a.y);
     a.z = fmaf(x.z, f, a.z), a.w = fmaf(x.w, f, a.w);
   }
