@@ -341,3 +341,35 @@ def test_the_mean_of_values_whose_sum_is_no_number(api, rows, L):
     sel = torch.randperm(L, dtype=torch.int32, device="cuda")[None]
     out, lse = api.kv4_attention_topk(*c.args, sel, next_n=1, softmax_scale=0.05)
     check_row(c, out, lse, 0, 0, 0.05)
+
+
+@pytest.mark.parametrize("rows", [1, 8, 16, 24, 64])
+@pytest.mark.parametrize("what", ["every", "selected"])
+def test_many_small_weights_beside_large_ones(api, rows, what):
+    """Four keys (one in each warp's first tile) take nearly all the weight and
+    have small values; the output is the other 32764 keys', each at 2^-25.2 of
+    one's weight.  What fp16 cannot hold of a term, two half steps of 2^-24 in
+    units of 2^-5 of the largest weight, is 2^-28 of that and the largest value,
+    and the sum of the weights is 4.  300 requests on the same pages, so that a
+    CTA has long runs of columns."""
+    L, D, B = 32768, 128, 300
+    rng = np.random.default_rng(rows)
+    kc = np.full((L, 1, 4), 107)
+    vc = np.full((L, 1, 4), 127)
+    big = [0, 64, 128, 192]
+    kc[big], vc[big] = 127, 100
+    q = 1 + 2.0 ** -6 * rng.standard_normal((rows, D))
+    c = Cache([L], 1, rows, 1, D, 64, [kc], [vc], q, seed=rows, codes=0x77)
+    for pos in big:
+        c.args[1][int(c.table[0, pos // 64]), 0, pos % 64, :D // 2] = 0x22    # every element 1
+        c.K[0][pos] = 1.0
+    scale = 25.2 * np.log(2) / 128
+    qs, rec, sc, table, lens = c.args
+    args = (qs.repeat(B, 1, 1), rec, sc, table.repeat(B, 1), lens.repeat(B))
+    if what == "every":
+        out, lse = api.kv4_attention(*args, next_n=1, softmax_scale=scale)
+    else:
+        sel = torch.arange(L, dtype=torch.int32, device="cuda")[None].repeat(B, 1)
+        out, lse = api.kv4_attention_topk(*args, sel, next_n=1, softmax_scale=scale)
+    for b in (0, 1, 2, 150, 299):
+        check_row(c, out[b:b + 1], lse[b:b + 1], 0, 0, scale, under=2.0 ** -30)

@@ -72,7 +72,12 @@ constexpr int kTile = 64;       // columns a warp takes at a time
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 2;
-constexpr float kValueMost = 4.f;  // a value scale over its reference, which lags behind the largest
+// A weight's largest value is 2^(kSlack + kRoom), a value scale's over its
+// reference kValueMost; fp16 holds their product.  What is below 2^-24 of 1
+// vanishes: the room keeps the sum of many small weights beside a large one.
+constexpr float kSlack = 8.f;
+constexpr float kRoom = 5.f;
+constexpr float kValueMost = 4.f;
 // Three fill an SM's registers (168 a thread) and shared memory.  On a selection
 // that leaves the L1, through which the gathers of single records go, 28 KB, and
 // two CTAs' fewer copies in flight are faster: 128 rows of 2048 selected keys, 8
@@ -720,9 +725,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kSel))
   // is raised to the running maximum only when a logit passes it by kSlack
   // (base 2), that is when an accumulator passes thr, so most tiles need no
   // maximum across lanes and no rescaling; weights are then at most 2^kSlack,
-  // which fp16 and fp32 hold as well as 1.  thr = -inf: the row has seen no
-  // column.
-  constexpr float kSlack = 8.f;
+  // which fp16 and fp32 hold as well as 1, times 2^kRoom.  thr = -inf: the row
+  // has seen no column.
   float thr[2], m[2], l[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) thr[i] = -INFINITY, m[i] = l[i] = 0.f;
@@ -1107,7 +1111,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kSel))
           float e[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            e[j] = ex2((sacc[x][j] - m[row_ix(j)]) * f[row_ix(j)]);
+            e[j] = ex2(fmaf(sacc[x][j] - m[row_ix(j)], f[row_ix(j)], kRoom));
             l[row_ix(j)] += e[j];
           }
           if constexpr (NT == 1) {
@@ -1215,7 +1219,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kSel))
       sum += __shfl_xor_sync(0xffffffffu, sum, x);
     const int row = row_of(i);
     if (NT == 1 ? r == 0 : t == 0) {
-      sml[(warp * kRows + row) * 2] = thr[i] == -INFINITY ? -INFINITY : m[i] * f[i];
+      sml[(warp * kRows + row) * 2] = thr[i] == -INFINITY ? -INFINITY : m[i] * f[i] - kRoom;
       sml[(warp * kRows + row) * 2 + 1] = sum;
     }
     float* dst = so + (warp * kRows + row) * D;
@@ -1301,6 +1305,7 @@ constexpr int kTcThreads = 256; // warps 0-3: keys; warps 4-7: values; both: sof
 constexpr int kTcStages = 2;
 constexpr int kTcCtas = 2;      // an SM holds
 constexpr int kKeyRoom = 12;    // a key's largest elements are up to 6 * 2^kKeyRoom in fp16
+constexpr float kTcRoom = 7.f;    // as kRoom: the values' scales are not in the weights here
 constexpr int kTcValueRoom = 5;   // V' at a new reference
 constexpr float kTcValueMost = 8192.f;  // a scale over its reference: 2^(kTcValueRoom + 8)
 // Reference of a row that has seen no column.  Its factor F is 1 until then, so
@@ -1431,7 +1436,6 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
   constexpr int G = Lay::G;
   constexpr int kChunks = D / 16;
   constexpr int kHalf = N / 2;  // rows of a warp's share of the softmax
-  constexpr float kSlack = 8.f;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool is_v = warp >= 4;   // value warps
@@ -1861,7 +1865,8 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
           const float4 f = *reinterpret_cast<const float4*>(&fz[n0 + c + j]);
-          const float e0 = fmaf(x[j], ks, -f.y) * f.x, e1 = fmaf(x[j + 1], ks, -f.w) * f.z;
+          const float e0 = fmaf(fmaf(x[j], ks, -f.y), f.x, kTcRoom);
+          const float e1 = fmaf(fmaf(x[j + 1], ks, -f.w), f.z, kTcRoom);
           mx = fmaxf(mx, fmaxf(e0, e1));
           pr[c + j] = ex2(e0), pr[c + j + 1] = ex2(e1);
         }
@@ -1874,7 +1879,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       tc_fence_before_sync();
       if (fail) *abort_flag = 1;
-      if (!__syncthreads_or(mx > kSlack || again || fail) || round == 3) break;
+      if (!__syncthreads_or(mx > kSlack + kTcRoom || again || fail) || round == 3) break;
       // Rare.  A larger value scale than the reference allows for: a new
       // reference, the values once more, O in the new unit.  A logit far above
       // its row's reference: rows' maxima over the tile, new references, sums
@@ -2077,7 +2082,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
     if (tiles > 0) {
       L = lp[row];
       a = *reinterpret_cast<const float4*>(so + row * D + d);
-      if (fz[row].y != kUnseen) M = fz[row].y * fz[row].x;
+      if (fz[row].y != kUnseen) M = fz[row].y * fz[row].x - kTcRoom;
       if ((nan_rows[row] >> (d / 32)) & 1)
         a.x = a.y = a.z = a.w = __uint_as_float(0x7FC00000u);
     }
