@@ -373,3 +373,83 @@ def test_many_small_weights_beside_large_ones(api, rows, what):
         out, lse = api.kv4_attention_topk(*args, sel, next_n=1, softmax_scale=scale)
     for b in (0, 1, 2, 150, 299):
         check_row(c, out[b:b + 1], lse[b:b + 1], 0, 0, scale, under=2.0 ** -30)
+
+
+# ------------------------------------------------------------------- NaN scales
+
+
+@pytest.mark.parametrize("Hq,nn", [(8, 1), (16, 1), (24, 1), (64, 1), (12, 2), (32, 2)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bad", ["value", "key", "last"])
+def test_nan_scales_reach_the_rows_that_see_them(api, Hq, nn, D, bad):
+    """A value block's NaN scale is its 32 channels' of every row that sees the
+    token, a key block's all of the row's; other rows, channels and keys' weights
+    are as exact as without."""
+    L, G = 400, D // 32
+    rng = np.random.default_rng(Hq + D)
+    kc = rng.integers(126, 129, size=(L, 1, G))
+    vc = rng.integers(126, 129, size=(L, 1, G))
+    q = rng.standard_normal((nn * Hq, D))
+    block = G - 1
+    pos = L - 1 if bad == "last" else 137
+    if bad == "value":
+        vc[pos, 0, block] = 255
+    else:
+        kc[pos, 0, block] = 255
+        vc[pos, 0, 0] = 255
+    c = Cache([L], nn, Hq, 1, D, 16, [kc], [vc], q, seed=Hq)
+    acc = torch.zeros(1, L, device="cuda")
+    out, lse = api.kv4_attention(*c.args, next_n=nn, softmax_scale=0.05, key_weights=acc)
+    c.V[0] = torch.nan_to_num(c.V[0])
+    clean, want = [], torch.zeros(L, dtype=torch.float64, device="cuda")
+    for j in range(nn):
+        if bad == "value":
+            lane = torch.zeros(D, dtype=torch.bool, device="cuda")
+            lane[32 * block:32 * block + 32] = True
+            assert torch.isnan(out[j][:, lane]).all() and torch.isfinite(lse[j]).all()
+            o = torch.where(lane, c.row(0, j, 0.05)[0], out[j].double())
+            check_row(c, torch.stack([o] * nn), lse, 0, j, 0.05)
+            clean.append(j)
+        elif bad == "last" and j < nn - 1:
+            check_row(c, out, lse, 0, j, 0.05)
+            clean.append(j)
+        else:
+            assert torch.isnan(out[j]).all() and torch.isnan(lse[j]).all()
+    if len(clean) == nn:
+        rows = [c.row(0, j, 0.05) for j in range(nn)]
+        want = sum(r[2].sum(0) for r in rows)
+        rel = max(rel_of(r[4]) for r in rows)
+        assert ((acc[0].double() - want).abs() <= (rel + nn * Hq * 2.0 ** -24) * want).all()
+    else:
+        assert torch.isnan(acc[0]).all()
+    c.V[0] = torch.nan_to_num(c.V[0])
+    sel = torch.randperm(L - nn + 1, dtype=torch.int32, device="cuda")[None].repeat(nn, 1)
+    sel = sel[:, :300].contiguous()
+    sel = torch.where(sel == pos, torch.full_like(sel, -1), sel)
+    out, lse = api.kv4_attention_topk(*c.args, sel, next_n=nn, softmax_scale=0.05)
+    assert torch.isfinite(out.float()).all() and torch.isfinite(lse).all()
+
+
+# --------------------------------------------------------------------- eviction
+
+
+@pytest.mark.parametrize("B,ctx", [(3, 900), (160, 900), (3, 40000)])
+def test_weights_that_are_no_numbers_are_never_chosen(api, B, ctx):
+    """On both of the selection's paths: NaN and -inf in the middle, more and
+    fewer numbers left than there is room for; sink and recent stay."""
+    rng = np.random.default_rng(ctx)
+    w = np.exp(rng.standard_normal((B, ctx))).astype(np.float32)
+    lens = rng.integers(1, ctx + 1, size=B)
+    lens[:3] = ctx, ctx // 2, ctx // 3
+    for b in range(B):
+        share = (0.1, 0.95, 1.0)[b % 3]
+        odd = rng.random(ctx) < share
+        w[b, odd] = np.where(rng.random(odd.sum()) < 0.5, np.nan, -np.inf)
+    budget, sink, recent = 300, 5, 20
+    lens_d = torch.from_numpy(lens.astype(np.int32)).cuda()
+    keep, n = api.kv_evict_select(torch.from_numpy(w).cuda(), lens_d, budget, sink=sink,
+                                  recent=recent)
+    for b in range(B):
+        want = ref.evict(w[b], int(lens[b]), budget, sink, recent)
+        assert int(n[b]) == len(want), b
+        assert keep[b].tolist() == want + [-1] * (budget - len(want)), b
