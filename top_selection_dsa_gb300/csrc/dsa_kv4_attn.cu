@@ -1315,6 +1315,7 @@ constexpr float kUnseen = -3e38f;
 // Shared memory of a CTA (1024-byte aligned).
 template <int D, int N>
 struct TcLayout {
+  static_assert(N == 32 || N == 64, "");
   static constexpr int G = D / kMxBlock;
   static constexpr int kTileBytes = kTcTile * D;
   static constexpr int kSc = D / 16;
@@ -1344,6 +1345,7 @@ struct TcLayout {
   static constexpr int kTmemS = D / 2;
   static constexpr int kTmemO = kTmemS + N;
   static constexpr int kTmemCols = kTmemO + N <= 128 ? 128 : 256;
+  static_assert(kTmemO + N <= kTmemCols && kTmemCols * kTcCtas <= 512, "");
 };
 
 __device__ __forceinline__ void tmem_store8(uint32_t taddr, const uint32_t (&r)[8]) {
@@ -1376,7 +1378,7 @@ __device__ __forceinline__ void mma_ts_f16(uint32_t d_tmem, uint32_t a_tmem, uin
 
 // Shared-memory descriptor of an operand stored M- (or N-) major: rows of 2^s
 // bytes along M, one row per k, swizzled over the row (mode 2: 128 bytes, 4:
-// 64, 6: 32); `lead` bytes between row-wide blocks along M, eight k rows `row8`
+// 64); `lead` bytes between row-wide blocks along M, eight k rows `row8`
 // bytes apart.
 __device__ __forceinline__ uint64_t mn_major_desc(uint32_t saddr, uint32_t lead, uint32_t row8,
                                                   uint32_t mode) {
@@ -1645,7 +1647,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
   bool started = false;  // there are products of this span
   constexpr uint32_t kIdescS = mma_idesc(0, 128, N);
   constexpr uint32_t kIdescO = mma_idesc(0, 128, N) | (1u << 15) | (1u << 16);
-  constexpr uint32_t kModeP = N == 16 ? 6 : (N == 32 ? 4 : 2);
+  constexpr uint32_t kModeP = N == 32 ? 4 : 2;
   for (int tile = 0; tile < tiles; ++tile, ++done) {
     const int s = done % kTcStages;
     locate(tile + kTcStages);
@@ -1871,7 +1873,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtas)
           pr[c + j] = ex2(e0), pr[c + j + 1] = ex2(e1);
         }
         const int ch = (n0 + c) / 8;
-        const int fl = N == 16 ? (key >> 2) & 1 : (N == 32 ? (key >> 1) & 3 : key & 7);
+        const int fl = N == 32 ? (key >> 1) & 3 : key & 7;
         sts128(sb + Lay::kP + key * (2 * N) + ((ch ^ fl) << 4), pack_f16(pr[c], pr[c + 1]),
                pack_f16(pr[c + 2], pr[c + 3]), pack_f16(pr[c + 4], pr[c + 5]),
                pack_f16(pr[c + 6], pr[c + 7]));
