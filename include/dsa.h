@@ -457,6 +457,8 @@ dsa_status_t dsa_k_norm_quant_insert(const void* k, const float* ln_weight, cons
  *           key/value head is D/2 bytes of key codes, then D/2 of value codes
  *   scales  [num_blocks, Hkv, block_size, D/16] bytes: D/32 of the key's
  *           scales, then D/32 of the value's
+ *           (codes 1 to 254 are 2^(code - 127), 255 is NaN; code 0, which an
+ *           empty cache holds and no insert writes, reads as zero)
  * Order of the codes in a record (that of the attention kernel's matrix
  * fragments), with G = D/32: the key's 4-byte word t*G + g (t < 4, g < G)
  * holds elements 32g + 8t .. + 7, the value's 2-byte unit r*G + g (r < 8)
@@ -493,8 +495,8 @@ dsa_status_t dsa_kv4_insert(const void* k, int64_t k_stride, const void* v, int6
 
 /*
  * Reads slots back as the values they stand for: k, v [T, Hkv, D] bf16 out,
- * dense, 16-byte aligned (exact: two significant bits times a power of two;
- * scale code 255 reads as NaN, and code 0, which no insert writes, as zero).
+ * dense, 16-byte aligned (exact: two significant bits times a power of two; what
+ * passes bf16's range, 2^128 and more, reads as infinity).
  * Slots as dsa_kv4_insert; a skipped one gives zeros.
  */
 dsa_status_t dsa_kv4_gather(const void* cache, const uint8_t* scales, int num_blocks,

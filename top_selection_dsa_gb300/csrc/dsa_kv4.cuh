@@ -3,8 +3,12 @@
 //
 // One token of one key/value head is a record of D bytes: D/2 bytes of packed
 // E2M1 key codes, then D/2 bytes of packed E2M1 value codes; next to it, in an
-// array of its own, D/16 bytes of E8M0 scales (value 2^(code - 127), one per
-// 32 consecutive elements): D/32 of the key, then D/32 of the value.
+// array of its own, D/16 bytes of E8M0 scales (one per 32 consecutive elements):
+// D/32 of the key, then D/32 of the value.  A scale is 2^(code - 127) for the
+// codes 1 to 253 that an insert writes (and for 254), NaN for 255.  Code 0,
+// which E8M0 gives 2^-127, is what an empty cache holds, and reads as zero:
+// telling it from zero costs the 16-row attention 4 % (600 -> 624 us) for
+// values below 2^-124.
 //   records [num_blocks, Hkv, block_size, D], scales [num_blocks, Hkv,
 //   block_size, D/16] -- a page's tokens of one head are contiguous.
 // The codes of a record are ordered the way the attention kernel's matrix
