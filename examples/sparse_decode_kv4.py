@@ -79,8 +79,9 @@ class SparseDecoder:
         api.kv_compact([self.cache, self.scales, self.index_keys], keep, self.context_lens,
                        self.table, new_lens=new_lens, key_weights=self.key_weights)
         self.context_lens = new_lens
-        for b, L in enumerate(self.lens):
-            self.lens[b] = min(L, self.budget)
+        # A request keeps fewer than it could where weights are not numbers.
+        self.lens = new_lens.tolist()
+        for b in range(len(self.lens)):
             used = -(-self.lens[b] // self.block_size)
             self.free += self.pages[b][used:]
             del self.pages[b][used:]

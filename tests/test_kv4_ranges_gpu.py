@@ -8,6 +8,9 @@ sum_d |q_d||k_d| of a row and dS = (2^-19 + 2^-24) B:
            within 2^-21, fp32 sums: relative 2 dS + 2^-18; then one fp32
            addition a row: 2^-24 of the sum for each.
 """
+import importlib.util
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -15,6 +18,8 @@ import torch
 import kv4_reference as ref
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -453,3 +458,32 @@ def test_weights_that_are_no_numbers_are_never_chosen(api, B, ctx):
         want = ref.evict(w[b], int(lens[b]), budget, sink, recent)
         assert int(n[b]) == len(want), b
         assert keep[b].tolist() == want + [-1] * (budget - len(want)), b
+
+
+# ------------------------------------------------------------------ the example
+
+
+def test_the_example_counts_what_an_eviction_kept(api):
+    """A request whose weights are no numbers keeps its sink and recent tokens
+    only; the host's lengths and pages are the device's."""
+    spec = importlib.util.spec_from_file_location(
+        "sparse_decode_kv4", os.path.join(ROOT, "examples", "sparse_decode_kv4.py"))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    d = m.SparseDecoder(2, num_blocks=10, block_size=16, heads=8, kv_heads=2, topk=24, limit=64,
+                        budget=40, sink=2, recent=8)
+
+    def rand(*shape):
+        return torch.randn(*shape, device="cuda").bfloat16()
+
+    evicted = False
+    for step in range(80):
+        if step == 63:
+            d.key_weights[1] = float("nan")
+        d.step(rand(2, 64, 128), torch.rand(2, 64, device="cuda"), rand(2, 128), rand(2, 8, 128),
+               rand(2, 2, 128), rand(2, 2, 128))
+        assert d.lens == d.context_lens.tolist()
+        assert [len(p) for p in d.pages] == [-(-L // 16) for L in d.lens]
+        evicted |= d.lens == [40, 10]
+    assert evicted
+    assert sorted(d.free + [x for p in d.pages for x in p]) == list(range(10))
