@@ -531,7 +531,7 @@ dsa_status_t dsa_kv4_gather(const void* cache, const uint8_t* scales, int num_bl
  * values enter exactly (with more than 16 rows a key/value head, a key's blocks
  * down to 2^-35 of its largest), q after division by a power of two per row (its
  * elements below 2^-24 of the row's largest vanish), the weights rounded to
- * fp16 (2^-12 relative; contributions below 2^-29 of the largest weight times the
+ * fp16 (2^-11 relative; contributions below 2^-29 of the largest weight times the
  * largest value scale of their 32 channels that the row sees vanish).  Sums, the softmax's maximum and
  * sum, and the weights are fp32.
  * Every sum runs in one fixed order: results are the same from call to call.

@@ -26,28 +26,30 @@
 //   O     += V^T P (O += P V): V's elements again the codes' values, and the
 //         value scales multiplied into P (fp16), by block of 32 channels
 //         relative to the largest scale met so far, 2^x, which lags behind by up
-//         to kValueMost; terms below 2^-24 of 2^x vanish.  A request's new tokens do
-//         not all see one another: a later one's larger scale is met in a
-//         window of columns of its own, after those that every row sees, and
-//         rows that do not see it keep their 2^x.
+//         to kValueMost; terms below 2^-24 of 2^x in units of 2^-kRoom vanish.
+//         A request's new tokens do not all see one another: a later one's
+//         larger scale is met in a window of columns of its own, after those
+//         that every row sees, and rows that do not see it keep their 2^x.
 // More rows: kv4_attn_tc_kernel, the same on the tensor cores' tcgen05 form
 // (further down).
 //
 // Times of one GB300 (copy bandwidth 6.68 TB/s), calls with their joins:
 //   64 requests of 4096 to 131072 keys, 8 key/value heads of 128 (2.55 GB):
-//     8 rows a head    405 us, 6.3 TB/s: bound by memory
-//     16 rows          586 us, 4.4 TB/s: bound by issue and latency (52 % of
+//     8 rows a head    412 us, 6.2 TB/s: bound by memory
+//     16 rows          597 us, 4.3 TB/s: bound by issue and latency (53 % of
 //                      the issue slots, ALU and tensor pipes 45 % each, three
 //                      warps a scheduler is what the registers leave)
 //   one request of 131071 keys, 8 rows   40 us, 3.5 TB/s: start and join
-//   2048 selected of each of 128 rows    82 us: single records of 128 bytes and
+//   2048 selected of each of 128 rows    80 us: single records of 128 bytes and
 //     scales of 8 from all over 2.5 GB (a plain gather of those took 71 us;
-//     DRAM is read by 64 bytes, which makes it 400 MB); 108 us with weights
+//     DRAM is read by 64 bytes, which makes it 400 MB); 105 us with weights
 // Tried and slower: tiles of 32 columns in three stages; 8 warps with 254
 // registers for 16 rows (637 to 716 us); tcgen05 for 16 rows (856); TMA gathers
 // of selected records (103.5 against cp.async's 98.4).
-// Rounding P to fp16 costs 2^-12 of each term (the output's bf16 rounding is
-// 2^-9); l sums the unrounded weights.
+// Rounding P to fp16 costs up to 2^-11 of each term (the output's bf16 rounding
+// up to 2^-8); l sums the unrounded weights.  A reference by block and windows
+// instead of one reference for all columns and channels: 8 rows 405 -> 412 us, 16
+// rows 590 -> 597.
 //
 // Rows of the m16 operand are permuted within each group of eight (odd rows
 // exchange halves, row i holds key i ^ 4): with the records' 16-byte chunks
@@ -408,21 +410,22 @@ __device__ __forceinline__ float row_factor(const Kv4AttnParams& p, int E) {
   return fmaxf(ldexpf(fabsf(p.scale_log2e), E), 1.4012985e-45f);
 }
 
-// Which kernel takes a CTA's rows (padded to 8, 16, 32 or 64).  Measured, us:
-//   rows of 64 requests of 4096 to 131072 keys, D = 128
-//     16 (4 key/value heads)      mma.sync 303, tcgen05 in tiles of 32 rows 542
-//     16 as two tiles of 8 rows   406
-//     32 (2 heads; 1)             mma.sync in tiles of 16 302; 162, tcgen05 283; 151
-//     64 (2 heads; 1)             583; 301, tcgen05 340; 184
-//   32, 64 rows of one request of 131071 keys: 61, 50 against 32, 38
-//   32, 64 rows on 2048 selected keys of 128 rows, 8 heads: 191, 360 against
-//     164, 246
-// Where everything is small or D = 64 mma.sync would be faster still (32 rows of
-// 64 requests of up to 16384 keys at D = 64, 29 against 36; single short calls
-// by 1 us), and with weights, where the logits' writes count (64 rows: 92
-// against 107 for 16 requests of up to 32768 keys, 565 against 551 for the 64
-// above, 278 against 298 on 64 selections); but whether the weights are asked
-// for does not change the output.
+// Which kernel takes a CTA's rows (padded to 8, 16, 32 or 64).  Measured, us,
+// mma.sync in tiles of 16 rows against tcgen05, D = 128:
+//   64 requests of 4096 to 131072 keys
+//     16 rows (4 key/value heads)  303 against 542 (in tiles of 32 rows); as two
+//                                  tiles of 8 rows 406
+//     32 rows (2 heads; 1)         303; 162 against 301; 161
+//     64 rows (2 heads; 1)         588; 303 against 357; 192
+//   2048 selected keys of 128 rows, 8 heads, 32 and 64 rows: 185, 350 against
+//     165, 230
+//   64 requests of 1024 to 16384 keys, 32 and 64 rows on one head: 41, 69 against
+//     45, 55 (D = 64: 30, 48 against 37, 46)
+//   one request of 131071 keys, 32 and 64 rows on one head: 34, 38 against 42, 46
+// So mma.sync is faster still with few columns for every CTA, and with weights,
+// where the logits' writes count (64 rows: 90 against 97 for 16 requests of up
+// to 32768 keys, 547 against 506 for the 64 above, 270 against 285 on 64
+// selections); but whether the weights are asked for does not change the output.
 constexpr bool uses_tc(int rows) { return rows > 16; }
 
 // One over a sum of weights, 0 for that of no columns.  Weighted values are
@@ -1290,16 +1293,19 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kSel))
 // A key is scaled by itself: 2^k is its largest block's scale less kKeyRoom, so
 // that fp16 holds its blocks exactly down to 2^-35 of that, and every key's
 // thread multiplies its logits by 2^k.  The values have a reference for each
-// block of 32 channels, raised when a scale passes it by 2^8 (V' is then 6 *
-// 2^kTcValueRoom at most, and exact down to 2^-28 of that scale); references of the
-// weights likewise lag behind the rows' maxima.  Raising any is rare and costs one
-// more round of the tile.  As above, a later token's scale that would raise the
-// values' is met in a window of its own, and rows that do not see it keep theirs.
-// 64 requests of up to 16384 keys, 64 rows on one head: 54 us for 50 MB (0.9
-// TB/s).  Bound by the chain of a tile's steps (decode, product, softmax,
-// product) with two CTAs an SM to overlap them, which shared memory and TMEM
-// allow: issue 31 %, tensor pipe 12 %, and the stalls spread over copies,
-// barriers and instruction fetch.
+// block of 32 channels: the largest scale is 2^kTcValueRoom of it when it is set,
+// V' exact down to 2^-28 of that scale, and it is raised when a scale passes
+// kTcValueMost.  References of the weights likewise lag behind the rows' maxima.
+// Raising any is rare and costs one more round of the tile.  As above, a later
+// token's scale that would raise the values' is met in a window of its own, and
+// rows that do not see it keep theirs (64 rows of 2 heads of the 64 requests
+// above 341 -> 358 us; a key scaled by itself instead of by a reference made
+// attend_shared_head of perf/operators.py 53 -> 51).
+// 64 requests of up to 16384 keys, 64 rows on one head: 55 us for 50 MB (0.9
+// TB/s), 119 us with every key's weight.  Bound by the chain of a tile's steps
+// (decode, product, softmax, product) with two CTAs an SM to overlap them, which
+// shared memory and TMEM allow: issue 35 %, tensor pipe 12 %, and the stalls
+// spread over copies, barriers and the chain itself.
 constexpr int kTcTile = 128;    // columns of a tile: one TMEM lane each
 constexpr int kTcThreads = 256; // warps 0-3: keys; warps 4-7: values; both: softmax
 constexpr int kTcStages = 2;
