@@ -528,12 +528,13 @@ dsa_status_t dsa_kv4_gather(const void* cache, const uint8_t* scales, int num_bl
  *                 aligned; NULL where that is 0.  It is sized for the current
  *                 device.
  * Products run on the tensor cores in fp16 with fp32 accumulation: keys and
- * values enter exactly (with more than 16 rows a key/value head, a key's blocks
- * down to 2^-35 of its largest), q after division by a power of two per row (its
- * elements below 2^-24 of the row's largest vanish), the weights rounded to
- * fp16 (2^-11 relative; contributions below 2^-29 of the largest weight times the
- * largest value scale of their 32 channels that the row sees vanish).  Sums, the softmax's maximum and
- * sum, and the weights are fp32.
+ * values enter exactly (with more than 16 rows a key/value head: a key's blocks
+ * down to 2^-35 of its largest, values down to 2^-28 of the largest scale of
+ * their 32 channels that the row sees), q after division by a power of two per
+ * row (its elements below 2^-24 of the row's largest vanish), the weights rounded
+ * to fp16 (2^-11 relative; contributions below 2^-29 of the largest weight times
+ * that largest scale vanish).  Sums, the softmax's maximum and sum, and the
+ * weights are fp32, its exponentials within 2^-21.
  * Every sum runs in one fixed order: results are the same from call to call.
  */
 dsa_status_t dsa_kv4_attention(const void* q, const void* cache, const uint8_t* scales,
