@@ -1,4 +1,6 @@
 """The Python binding of the 4-bit cache's calls, as far as it needs no GPU."""
+import ctypes
+
 import pytest
 
 
@@ -23,3 +25,15 @@ def test_workspace_sizes_are_asked_for_by_device(api, monkeypatch, name):
         monkeypatch.setattr(api.torch.cuda, "current_device", lambda: device)
         assert getattr(api, name)(*args) == device
     assert asked == [5, 6, 5]
+
+
+@pytest.mark.parametrize("planes,row", [(1 << 20, 1 << 19), (1 << 24, 1 << 15), (3, (1 << 31) - 4),
+                                        ((1 << 31) - 1, 4)])
+def test_compaction_counts_its_work_past_32_bits(api, planes, row):
+    """Caches of more slices than a launch takes are refused, also where 32 bits
+    would count them to none.  (3 planes of one row of 2 GB are within it.)"""
+    A = ctypes.c_void_p(0x10000)
+    caches = (api.PagedRows * 1)(api.PagedRows(0x10000, planes, row))
+    st = api.lib.dsa_kv_compact(caches, 1, 4, 8, A, 1, None, 0, A, A, A, 0, 8, None, None, 0, None)
+    slices = planes * (-(-row // 128))
+    assert st == (api.DSA_ERR_UNSUPPORTED if slices > 1 << 30 else api.DSA_OK)

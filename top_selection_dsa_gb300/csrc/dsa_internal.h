@@ -211,6 +211,6 @@ struct CompactParams {
 };
 cudaError_t launch_kv_compact(const CompactParams& p, cudaStream_t s);
 // Units (plane, slice of bytes) of a cache.
-int compact_units(const CompactParams::Cache& c);
+int64_t compact_units(const CompactParams::Cache& c);
 
 }  // namespace dsa

@@ -466,8 +466,9 @@ cudaError_t launch_evict_keep(const int32_t* lens, const int32_t* starts, const 
   return cudaGetLastError();
 }
 
-int compact_units(const CompactParams::Cache& c) {
-  return c.planes * ((c.row_bytes + kSlice - 1) / kSlice);
+int64_t compact_units(const CompactParams::Cache& c) {
+  const int64_t slices = (static_cast<int64_t>(c.row_bytes) + kSlice - 1) / kSlice;
+  return c.planes * slices;
 }
 
 cudaError_t launch_kv_compact(const CompactParams& p, cudaStream_t s) {
