@@ -487,3 +487,19 @@ def test_the_example_counts_what_an_eviction_kept(api):
         evicted |= d.lens == [40, 10]
     assert evicted
     assert sorted(d.free + [x for p in d.pages for x in p]) == list(range(10))
+
+
+@pytest.mark.parametrize("rows", [1, 8, 16, 24, 64])
+@pytest.mark.parametrize("lens", [[131071], [65536, 30001, 1]])
+def test_outputs_over_long_contexts(api, rows, lens):
+    """Every channel of contexts up to 131071 keys; what fp16 cannot hold of a
+    term is 2^-28 of the largest weight and value."""
+    D = 128
+    rng = np.random.default_rng(rows)
+    kc = [rng.integers(125, 129, size=(L, 1, 4)) for L in lens]
+    vc = [rng.integers(124, 129, size=(L, 1, 4)) for L in lens]
+    q = rng.standard_normal((len(lens) * rows, D))
+    c = Cache(lens, 1, rows, 1, D, 64, kc, vc, q, seed=rows)
+    out, lse = api.kv4_attention(*c.args, next_n=1, softmax_scale=0.1)
+    for b in range(len(lens)):
+        check_row(c, out, lse, b, 0, 0.1, under=2.0 ** -28)
