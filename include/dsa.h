@@ -577,6 +577,115 @@ size_t dsa_kv4_attention_workspace_bytes(int B, int next_n, int Hq, int Hkv, int
                                          int selected, int weights);
 
 /*
+ * --------------------------------------------------------------------------
+ * The 16-bit key/value cache: keys and values as bf16, paged like the others
+ * (kv_compact moves it too, with planes = Hkv and row_bytes = 2 D).
+ *
+ *   k_cache, v_cache  [num_blocks, Hkv, block_size, D] bf16 each, 16-byte aligned
+ *
+ * Shared by the calls below: D is 64 or 128, block_size a power of two in
+ * [8, 128], num_blocks * block_size * Hkv < 2^31 (else DSA_ERR_UNSUPPORTED).
+ * Rows of several tokens (q, k, v) are [T, H, D] bf16, 16-byte aligned, heads
+ * and elements dense, tokens a stride of elements apart (a multiple of 8, at
+ * least H * D), as slices of one projection are.  Once a call has run on a
+ * device its calls can be captured into a CUDA graph.
+ * --------------------------------------------------------------------------
+ */
+
+/*
+ * A norm of every query and key head and its rotation by position, in one
+ * pass.  For a head's row x at position p:
+ *   y = x / sqrt(mean(x^2) + eps) * weight         (no weight: y = x)
+ *   the first `rotary` = 2 F elements of y, in pairs (y_i, y_{i+F}), or
+ *   interleaved (y_{2i}, y_{2i+1}), turned by the angle p f_i:
+ *     rope_scale (a cos - b sin),  rope_scale (a sin + b cos)
+ *   the others as they are.  Computed in fp32, rounded to bf16 once.
+ *
+ *   q, k          [T, Hq, D], [T, Hk, D]; k may be NULL (then Hk = 0, k_out NULL)
+ *   positions     [T] int32, any value
+ *   turns         [rotary / 2] uint64: f_i / (2 pi) in units of 2^-64 turns,
+ *                 rounded (modulo 2^64).  The angle is reduced exactly, so its
+ *                 error is below 2^-31 turns at every position.
+ *   rotary        0 (positions and turns may then be NULL) .. D, a multiple of
+ *                 16 (other even ones: DSA_ERR_UNSUPPORTED)
+ *   q_weight, k_weight  [D] fp32, or NULL: that side is not normalised
+ *   q_out, k_out  [T, H, D] dense, 16-byte aligned; may be q or k where those
+ *                 are dense
+ *   Hq, Hk <= 4096 (else DSA_ERR_UNSUPPORTED)
+ */
+dsa_status_t dsa_qk_norm_rope(const void* q, int64_t q_stride, int Hq, const void* k,
+                              int64_t k_stride, int Hk, int T, int D, const int32_t* positions,
+                              const uint64_t* turns, int rotary, int interleaved,
+                              float rope_scale, const float* q_weight, const float* k_weight,
+                              float eps, void* q_out, void* k_out, dsa_stream_t stream);
+
+/*
+ * Writes new keys and values into their slots, the keys normalised and rotated
+ * on the way (as dsa_qk_norm_rope does), the values as they are; with q, its
+ * rows become q_out in the same launch.
+ *
+ *   slot_mapping  [T] int64, distinct: a slot below 0 is skipped; one past the
+ *                 cache is skipped and reported by dsa_get_last_device_error
+ *                 as DSA_ERR_INVALID_ARG (the token's query is written either way)
+ *   q             [T, Hq, D], or NULL (then Hq = 0, q_weight and q_out NULL)
+ *   the others    as dsa_qk_norm_rope; rotary = 0 for keys already rotated
+ */
+dsa_status_t dsa_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           const int64_t* slot_mapping, int T, int Hkv, int D,
+                           const int32_t* positions, const uint64_t* turns, int rotary,
+                           int interleaved, float rope_scale, const float* k_weight, float eps,
+                           void* k_cache, void* v_cache, int num_blocks, int block_size,
+                           const void* q, int64_t q_stride, int Hq, const float* q_weight,
+                           void* q_out, dsa_stream_t stream);
+
+/*
+ * Attention of every request's new tokens over its pages: from one token a
+ * request (decode) to whole prompts, mixed in one call.  Request b's tokens are
+ * the rows query_starts[b] .. query_starts[b+1] of q, n of them, the last n
+ * positions of its context of L_b tokens (which are in the cache already).
+ * The token at position p sees the keys c <= p and, with a window, of those
+ * only c > p - window and c < sink:
+ *   S[t,h,c] = softmax_scale * q[t,h] . K[c, h / (Hq/Hkv)]
+ *   lse[t,h] = log sum_c exp S[t,h,c]
+ *   out[t,h] = sum_c exp(S[t,h,c] - lse[t,h]) V[c, h / (Hq/Hkv)]
+ * A token that sees nothing (a position below 0: L_b < n) gives out = 0 and
+ * lse = -inf.  Values of keys that a token does not see never reach it,
+ * whatever they hold.  Rows of no request are left as they were.
+ *
+ *   q             [T, Hq, D]; Hq a multiple of Hkv, Hq / Hkv <= 128
+ *   block_table   [B, max_blocks] int32; context_lens [B] int32, counting the
+ *                 new tokens: bad entries as in dsa_indexer_logits_paged (block
+ *                 0 in their place, lengths clamped, both recorded)
+ *   query_starts  [B + 1] int32, ascending, in [0, T]: entries outside or
+ *                 descending are clamped and recorded alike
+ *   softmax_scale in [2^-64, 2^64]
+ *   window        0: none; else a token sees that many keys, itself among them
+ *   sink          the first keys that stay visible behind the window
+ *   out           [T, Hq, D] bf16 dense, 16-byte aligned
+ *   lse           [T, Hq] fp32 (natural logarithm) or NULL
+ *   workspace     dsa_kv_attention_workspace_bytes(T, Hq, Hkv, D) bytes (for the
+ *                 current device), 256-byte aligned.  Calls that may overlap
+ *                 need one each.
+ *   B <= 2048, max_blocks * block_size < 2^30, T < 2^30 (else
+ *   DSA_ERR_UNSUPPORTED; also where (T Hq / (256 Hkv) + B) times the tiles of
+ *   128 keys of the longest context pass 2^31)
+ * Products run on the tensor cores on the bf16 inputs with fp32 accumulation;
+ * the weights exp(S - max) are rounded to bf16 for the second one (2^-8 relative),
+ * their sum and the maximum are fp32.  Every sum runs in one fixed order: results
+ * are the same from call to call.
+ */
+dsa_status_t dsa_kv_attention(const void* q, int64_t q_stride, const void* k_cache,
+                              const void* v_cache, int num_blocks, const int32_t* block_table,
+                              int max_blocks, const int32_t* context_lens,
+                              const int32_t* query_starts, int T, int B, int block_size, int Hq,
+                              int Hkv, int D, float softmax_scale, int window, int sink, void* out,
+                              float* lse, void* workspace, size_t ws_bytes, dsa_stream_t stream);
+
+/* Scratch bytes of dsa_kv_attention on the current device; (size_t)-1 for bad
+ * arguments. */
+size_t dsa_kv_attention_workspace_bytes(int T, int Hq, int Hkv, int D);
+
+/*
  * Which tokens of every request a budget keeps: its first `sink` positions,
  * its last `recent`, and of those between the budget - sink - recent with the
  * largest accumulated weight (ties to the lower position; -inf and NaN are

@@ -11,7 +11,9 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import fractions
 import functools
+import math
 import os
 
 import torch
@@ -36,7 +38,8 @@ EXPORTS = (
     "dsa_indexer_logits_mxfp4", "dsa_indexer_topk_mxfp4", "dsa_topk_merge_ranks",
     "dsa_topk_dcp_candidates", "dsa_kv4_insert", "dsa_kv4_gather", "dsa_kv4_attention",
     "dsa_kv4_attention_topk", "dsa_kv4_attention_workspace_bytes", "dsa_kv_evict_select",
-    "dsa_kv_evict_workspace_bytes", "dsa_kv_compact",
+    "dsa_kv_evict_workspace_bytes", "dsa_kv_compact", "dsa_qk_norm_rope", "dsa_kv_append",
+    "dsa_kv_attention", "dsa_kv_attention_workspace_bytes",
 )
 
 
@@ -97,6 +100,15 @@ def _load():
     lib.dsa_kv_evict_workspace_bytes.restype = SZ
     lib.dsa_kv_compact.argtypes = [ctypes.POINTER(PagedRows), I, I, I, P, I, P, I, P, P, P, I, I,
                                    P, P, I64, P]
+    lib.dsa_qk_norm_rope.argtypes = [P, I64, I, P, I64, I, I, I, P, P, I, I, F, P, P, F, P, P, P]
+    lib.dsa_kv_append.argtypes = [P, I64, P, I64, P, I, I, I, P, P, I, I, F, P, F, P, P, I, I, P,
+                                  I64, I, P, P, P]
+    lib.dsa_kv_attention.argtypes = [P, I64, P, P, I, P, I, P, P, I, I, I, I, I, I, F, I, I, P, P,
+                                     P, SZ, P]
+    lib.dsa_kv_attention_workspace_bytes.argtypes = [I, I, I, I]
+    lib.dsa_kv_attention_workspace_bytes.restype = SZ
+    for name in ("dsa_qk_norm_rope", "dsa_kv_append", "dsa_kv_attention"):
+        getattr(lib, name).restype = I
     for name in ("dsa_kv4_insert", "dsa_kv4_gather", "dsa_kv4_attention",
                  "dsa_kv4_attention_topk", "dsa_kv_evict_select", "dsa_kv_compact"):
         getattr(lib, name).restype = I
@@ -727,6 +739,222 @@ def kv4_attention_topk(q, cache, scales, block_table, context_lens, topk_idx, *,
         raise ValueError("topk_idx [B*next_n, k] expected")
     return _kv4_attention(q, cache, scales, block_table, context_lens, topk_idx, next_n,
                           softmax_scale, out, lse, sel_weights, key_weights, workspace)
+
+
+def rope_frequencies(rotary, base=10000.0, *, factor=1.0, scaling=None, original_context=None,
+                     beta_fast=32.0, beta_slow=1.0):
+    """Angles per position of the `rotary` rotated elements of a head, and the
+    factor on them (rope_scale): (float64 [rotary/2] on the host, float).
+
+    base^(-2i/rotary), and for contexts stretched by `factor`:
+      scaling="linear"  all of them divided by factor
+      scaling="yarn"    those that turn more than beta_fast times within
+                        original_context kept, those that turn less than
+                        beta_slow times divided by factor, between them a linear
+                        ramp over i; the factor on the elements is
+                        0.1 log(factor) + 1
+    """
+    if rotary < 2 or rotary % 2 or not base > 1 or not factor >= 1:
+        raise ValueError("rotary a positive even number, base > 1 and factor >= 1 expected")
+    i = torch.arange(rotary // 2, dtype=torch.float64)
+    freq = float(base) ** (-2 * i / rotary)
+    if scaling is None:
+        if factor != 1.0:
+            raise ValueError("factor needs scaling='linear' or 'yarn'")
+        return freq, 1.0
+    if scaling == "linear":
+        return freq / factor, 1.0
+    if scaling != "yarn":
+        raise ValueError(f"scaling must be None, 'linear' or 'yarn', got {scaling!r}")
+    if not original_context or not beta_fast > beta_slow > 0:
+        raise ValueError("yarn needs original_context and beta_fast > beta_slow > 0")
+
+    def element(turns):  # the (real) i that turns so often within original_context
+        return rotary * math.log(original_context / (2 * math.pi * turns)) / (2 * math.log(base))
+
+    lo = max(math.floor(element(beta_fast)), 0)
+    hi = min(math.ceil(element(beta_slow)), rotary - 1)
+    ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+    return freq * (1 - ramp) + freq / factor * ramp, 0.1 * math.log(factor) + 1.0
+
+
+# 2 pi to 120 bits and more: a position multiplies the rounding of the table.
+_TWO_PI = fractions.Fraction(2 * 31415926535897932384626433832795028841971693993751, 10 ** 49)
+
+
+def rope_turns(freq, device="cuda"):
+    """The table qk_norm_rope and kv_append read: angles per position (float64,
+    radians, magnitude below 2^31) as int64 [F], units of 2^-64 turns."""
+    freq = torch.as_tensor(freq, dtype=torch.float64)
+    if freq.dim() != 1 or not bool((freq.abs() < 2.0 ** 31).all()):
+        raise ValueError("freq must be one row of finite angles below 2^31")
+    turns = []
+    for f in freq.tolist():
+        n = round(fractions.Fraction(f) / _TWO_PI * 2 ** 64) % 2 ** 64
+        turns.append(n - 2 ** 64 if n >= 2 ** 63 else n)
+    return torch.tensor(turns, dtype=torch.int64, device=device)
+
+
+def _rotation(dev, T, D, positions, turns, q_weight, k_weight):
+    """Checks of the rotation's tensors; how many elements are rotated."""
+    _need_all(dev, ((positions, "positions", torch.int32), (turns, "turns", torch.int64),
+                    (q_weight, "q_weight", torch.float32), (k_weight, "k_weight", torch.float32)))
+    if (positions is None) != (turns is None):
+        raise ValueError("positions and turns go together")
+    _shape(positions, "positions", (T,))
+    _shape(q_weight, "q_weight", (D,))
+    _shape(k_weight, "k_weight", (D,))
+    return 0 if turns is None else 2 * turns.numel()
+
+
+def _rows_of(t, name, dev):
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, H, D], got {tuple(t.shape)}")
+    return _token_rows(t, name, dev, t.shape)
+
+
+def qk_norm_rope(q, k, positions, turns, *, q_weight=None, k_weight=None, eps=1e-6,
+                 interleaved=False, rope_scale=1.0, q_out=None, k_out=None):
+    """Queries [T, Hq, D] and keys [T, Hk, D] (bf16; tokens may be strided;
+    k may be None) normalised per head (where there is a weight, [D] fp32) and
+    rotated by positions [T] int32, in one pass: (q_out, k_out), dense.
+    `turns` is rope_turns(...); None (and positions None): only the norm."""
+    dev = q.device
+    T, Hq, D = q.shape if q.dim() == 3 else (0, 0, 0)
+    qs = _rows_of(q, "q", dev)
+    ks = hk = 0
+    if k is not None:
+        ks, hk = _rows_of(k, "k", dev), k.shape[1]
+        _shape(k, "k", (T, hk, D))
+        if k_out is None:
+            k_out = torch.empty((T, hk, D), dtype=torch.bfloat16, device=dev)
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("k_out and k_weight need k")
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    rotary = _rotation(dev, T, D, positions, turns, q_weight, k_weight)
+    _need_all(dev, ((q_out, "q_out", torch.bfloat16), (k_out, "k_out", torch.bfloat16)))
+    _shape(q_out, "q_out", (T, Hq, D))
+    _shape(k_out, "k_out", (T, hk, D))
+    if T == 0:
+        return q_out, k_out
+    with _on(dev):
+        st = lib.dsa_qk_norm_rope(_addr(q), qs, Hq, _addr(k), ks, hk, T, D, _addr(positions),
+                                  _addr(turns), rotary, bool(interleaved), rope_scale,
+                                  _addr(q_weight), _addr(k_weight), eps, _addr(q_out),
+                                  _addr(k_out), _raw_stream(dev))
+    _check(st, "dsa_qk_norm_rope")
+    return q_out, k_out
+
+
+def kv_cache(num_blocks, num_kv_heads, block_size, head_dim, device="cuda"):
+    """An empty 16-bit key/value cache: (k_cache, v_cache), each [num_blocks,
+    Hkv, block_size, D] bf16."""
+    shape = (num_blocks, num_kv_heads, block_size, head_dim)
+    return (torch.zeros(shape, dtype=torch.bfloat16, device=device),
+            torch.zeros(shape, dtype=torch.bfloat16, device=device))
+
+
+def _kv_shape(k_cache, v_cache, dev):
+    _need_all(dev, ((k_cache, "k_cache", torch.bfloat16), (v_cache, "v_cache", torch.bfloat16)))
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache [num_blocks, Hkv, block_size, D] expected, got "
+                         f"{tuple(k_cache.shape)}")
+    _shape(v_cache, "v_cache", k_cache.shape)
+    return k_cache.shape
+
+
+def kv_append(k, v, slot_mapping, k_cache, v_cache, *, positions=None, turns=None, k_weight=None,
+              eps=1e-6, interleaved=False, rope_scale=1.0, q=None, q_weight=None, q_out=None):
+    """New keys and values [T, Hkv, D] (bf16; tokens may be strided) into their
+    slots of the 16-bit cache, in place; the keys normalised and rotated on the
+    way as by qk_norm_rope, and with q [T, Hq, D] the queries beside them.
+    Returns (k_cache, v_cache, q_out), q_out None without q."""
+    dev = k_cache.device
+    nb, hkv, bs, D = _kv_shape(k_cache, v_cache, dev)
+    _need_all(dev, ((slot_mapping, "slot_mapping", torch.int64),))
+    T = slot_mapping.numel()
+    ks = _token_rows(k, "k", dev, (T, hkv, D))
+    vs = _token_rows(v, "v", dev, (T, hkv, D))
+    qs = hq = 0
+    if q is not None:
+        qs, hq = _rows_of(q, "q", dev), q.shape[1]
+        _shape(q, "q", (T, hq, D))
+        if q_out is None:
+            q_out = torch.empty((T, hq, D), dtype=torch.bfloat16, device=dev)
+        _need_all(dev, ((q_out, "q_out", torch.bfloat16),))
+        _shape(q_out, "q_out", (T, hq, D))
+    elif q_out is not None or q_weight is not None:
+        raise ValueError("q_out and q_weight need q")
+    rotary = _rotation(dev, T, D, positions, turns, q_weight, k_weight)
+    if T == 0:
+        return k_cache, v_cache, q_out
+    with _on(dev):
+        st = lib.dsa_kv_append(_addr(k), ks, _addr(v), vs, _addr(slot_mapping), T, hkv, D,
+                               _addr(positions), _addr(turns), rotary, bool(interleaved),
+                               rope_scale, _addr(k_weight), eps, _addr(k_cache), _addr(v_cache),
+                               nb, bs, _addr(q), qs, hq, _addr(q_weight), _addr(q_out),
+                               _raw_stream(dev))
+    _check(st, "dsa_kv_append")
+    return k_cache, v_cache, q_out
+
+
+def kv_attention_workspace_bytes(T, Hq, Hkv, D) -> int:
+    """Workspace of kv_attention over T tokens, on the current device."""
+    return _kv_attn_workspace(torch.cuda.current_device() if torch.cuda.is_available() else -1,
+                              T, Hq, Hkv, D)
+
+
+@functools.lru_cache(maxsize=4096)
+def _kv_attn_workspace(device, T, Hq, Hkv, D):
+    n = lib.dsa_kv_attention_workspace_bytes(T, Hq, Hkv, D)
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("dsa_kv_attention_workspace_bytes: bad arguments")
+    return int(n)
+
+
+def kv_attention(q, k_cache, v_cache, block_table, context_lens, query_starts, *,
+                 softmax_scale=None, window=0, sink=0, out=None, lse=None, workspace=None):
+    """Attention of every request's new tokens over the 16-bit paged cache: q
+    [T, Hq, D] (bf16; tokens may be strided) holds request b's tokens in rows
+    query_starts[b] .. query_starts[b+1] (int32 [B+1]), the last positions of
+    its context of context_lens[b].  Each sees the keys up to its own position;
+    with a window, the last `window` of them and the first `sink`.  Returns
+    (out [T, Hq, D], lse [T, Hq] fp32).  softmax_scale defaults to D^-0.5."""
+    dev = q.device
+    nb, hkv, bs, D = _kv_shape(k_cache, v_cache, dev)
+    qs = _rows_of(q, "q", dev)
+    T, Hq, Dq = q.shape
+    if Dq != D:
+        raise ValueError(f"q must be [T, Hq, {D}], got {tuple(q.shape)}")
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table must be [B, max_blocks], got {tuple(block_table.shape)}")
+    B, max_blocks = block_table.shape
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    _need_all(dev, ((block_table, "block_table", torch.int32),
+                    (context_lens, "context_lens", torch.int32),
+                    (query_starts, "query_starts", torch.int32), (out, "out", torch.bfloat16),
+                    (lse, "lse", torch.float32)))
+    _shape(context_lens, "context_lens", (B,))
+    _shape(query_starts, "query_starts", (B + 1,))
+    _shape(out, "out", (T, Hq, D))
+    _shape(lse, "lse", (T, Hq))
+    if T == 0 or B == 0:
+        return out, lse
+    scale = D ** -0.5 if softmax_scale is None else softmax_scale
+    with _on(dev):
+        nbytes = _kv_attn_workspace(dev.index, T, Hq, hkv, D)
+        ws = _workspace(nbytes, dev, workspace)
+        st = lib.dsa_kv_attention(_addr(q), qs, _addr(k_cache), _addr(v_cache), nb,
+                                  _addr(block_table), max_blocks, _addr(context_lens),
+                                  _addr(query_starts), T, B, bs, Hq, hkv, D, scale, int(window),
+                                  int(sink), _addr(out), _addr(lse), _addr(ws), nbytes,
+                                  _raw_stream(dev))
+    _check(st, "dsa_kv_attention")
+    return out, lse
 
 
 def kv_evict_workspace_bytes(B, max_ctx, budget) -> int:

@@ -180,6 +180,66 @@ Kv4AttnPlan kv4_attn_plan(int B, int next_n, int Hq, int Hkv, int D, int64_t col
 cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int D, int rows, bool scores,
                                  cudaStream_t s);
 
+// ------------------------------------------------ the 16-bit key/value cache
+// Tiled map over bf16 values, innermost dimension first (strides in bytes, of
+// the outer ones), boxes of 64 elements innermost, swizzled over 128 bytes.
+bool encode_bf16_boxes(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                       const uint64_t* strides, const uint32_t* box);
+
+// Norm, rotation and append (dsa_rope.cu); D is 64 or 128.
+struct RopeParams {
+  const uint16_t* q;      // [T, Hq, D], tokens q_stride elements apart
+  const uint16_t* k;      // [T, Hk, D], k_stride
+  const uint16_t* v;      // [T, Hv, D], v_stride
+  int64_t q_stride, k_stride, v_stride;
+  int T, Hq, Hk, Hv;      // heads, 0 for what there is none of
+  const int32_t* positions;  // [T] or null (with rotary = 0)
+  const uint64_t* turns;     // [rotary / 2] or null
+  int rotary;             // elements of a head that are rotated
+  float rope_scale;
+  const float* q_weight;  // [D] or null: no norm
+  const float* k_weight;
+  float eps;
+  uint16_t* q_out;        // [T, Hq, D]
+  uint16_t* k_out;        // [T, Hk, D], or [num_blocks, Hk, block_size, D] with slots
+  uint16_t* v_out;        // [num_blocks, Hv, block_size, D]
+  const int64_t* slots;   // [T] or null
+  int64_t capacity;       // slots of the cache
+  int log_bs;
+  uint32_t* err;
+};
+cudaError_t launch_rope(const RopeParams& p, int D, bool interleaved, cudaStream_t s);
+
+// Attention of chunks of new tokens (dsa_kv_attn.cu).
+struct KvAttnParams {
+  CUtensorMap tmap_q;         // q as {D, Hq, T}, boxes of one row tile
+  CUtensorMap tmap_k, tmap_v;  // the caches as {D, num_blocks*Hkv*block_size}, boxes of one page
+  const uint16_t* v;          // [num_blocks, Hkv, block_size, D]
+  const int32_t* block_table;   // [B, max_blocks]
+  const int32_t* context_lens;  // [B]
+  const int32_t* starts;        // [B + 1]: first token of each request, and the end
+  int T, B, Hq, Hkv, G, tpt;  // G query heads a key/value head; tokens of a row tile
+  int max_blocks, num_blocks, log_bs;
+  int window, sink;           // window 0: none
+  float scale_log2e;          // softmax scale times log2(e)
+  float lazy;                 // growth of a logit maximum that moves a row's reference
+  uint16_t* out;              // [T, Hq, D]
+  float* lse;                 // [T, Hq] or null
+  int ctas, slot_rows;
+  int4* notes;                // [ctas, 2]: what each CTA left unfinished
+  float2* part_ml;            // [ctas, 2, slot_rows]: base-2 reference and sum of weights
+  float* part_o;              // [ctas, 2, slot_rows, D]
+  uint32_t* err;
+};
+struct KvAttnPlan {
+  int tpt, ctas, slot_rows;
+  int64_t part_ml, part_o, bytes;  // offsets of the workspace, and its size
+};
+KvAttnPlan kv_attn_plan(int T, int G, int D);
+// Bound on one head's units of work.
+int64_t kv_attn_units(int T, int B, int G, int64_t max_ctx);
+cudaError_t launch_kv_attention(const KvAttnParams& p, int D, cudaStream_t s);
+
 // Eviction (dsa_kv_evict.cu).
 bool evict_small(int B, int max_ctx);  // one kernel, no workspace
 cudaError_t launch_evict_small(const float* weights, int64_t ldw, const int32_t* lens, int B,

@@ -1,0 +1,1011 @@
+// dsa_kv_attn.cu -- attention of chunks of new tokens over the 16-bit paged
+// key/value cache (sm_103a).
+//
+// Request b's n tokens stand at the end of its context of L; the one at
+// position p sees the keys c <= p, with a window W only c > p - W or c < sink:
+//   S = scale q . k,  lse = log sum exp S,  out = sum exp(S - lse) v
+//
+// Rows.  The query heads of one key/value head share their keys, so a row of
+// the products is a (token, head of the group) pair: 128 rows hold
+// tpt = floor(128 / G) whole tokens.  Two such row tiles, A and B, run at a
+// time, each with a warpgroup of its own for the softmax (a thread a row):
+// while one is exponentiated, the tensor cores work on the other.
+//   tall  more than tpt tokens: A and B are neighbouring rows on the same keys
+//   short no more: A takes the even key tiles and B the odd ones of the same
+//         rows, and their results are joined at the end, so that a single
+//         token's long axis keeps both halves busy too
+//
+// Work.  A unit is one tile of 128 keys (tall) or two (short).  The units of
+// all heads, requests and row tiles, in that order, are cut into equal runs,
+// one for each CTA; a tile that a cut goes through leaves its parts (maximum,
+// sum, unscaled output, all fp32) in the workspace, and a second kernel joins
+// them in their fixed order.  Lengths are read on the device, so a captured
+// graph serves every step, and one long request fills the GPU as evenly as
+// many short ones.
+//
+// Roles: warps 0-3 softmax of A, 4-7 of B, 8 TMA (queries, then a ring of key
+// and value tiles fetched page by page), 9 tcgen05.mma, 10-11 the check of
+// values that some row does not see.  S = Q K^T goes to TMEM; P overwrites it
+// as bf16 and is the A operand of O += P V straight from TMEM.  A row's
+// reference maximum is only moved, and O rescaled, when the maximum grows by
+// more than 2^8: P stays below 2^8 and sums are fp32, so nothing is lost.
+// P is rounded to bf16 (2^-8 relative each, on average below what the output's own
+// rounding adds once a few weights are summed); all else is fp32.
+//
+// Values that a row does not see never reach it, whatever they hold: in tiles
+// that are not wholly seen, infinities and NaN among the values are replaced
+// by zeros before the product (0 * inf would be NaN), and rows that do see
+// them have them added at the end.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include <atomic>
+
+#include "dsa_common.cuh"
+#include "dsa_internal.h"
+
+namespace dsa {
+namespace {
+
+constexpr int kTile = 128;    // keys of a tile, rows of a row tile
+constexpr int kThreads = 384;
+constexpr int kMaxStages = 12;
+// Registers a thread: 168 at launch, shifted to the softmax (8 warps at 200 and
+// 4 at 96 are 63488 of the block's 64512).
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 96;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
+
+template <int D>
+struct AttnCfg {
+  static constexpr int HALVES = D / 64;               // 128-byte columns of a row
+  static constexpr int HALF_BYTES = kTile * 128;      // one column of a tile
+  static constexpr int TILE_BYTES = HALVES * HALF_BYTES;
+  static constexpr int NST = D == 128 ? 5 : 12;       // what shared memory has room for
+  static constexpr int RING = 2 * TILE_BYTES;
+  static constexpr int MISC = RING + NST * TILE_BYTES;
+  static constexpr int XML = 0;                       // float2[2][128]
+  static constexpr int BARS = 2048;
+  static constexpr int SLOT = BARS + 8 * (3 * kMaxStages + 12);
+  static constexpr int SMEM = MISC + (SLOT + 16 + 127) / 128 * 128;
+  static constexpr uint32_t S_COL = 0, O_COL = 256;   // TMEM: S/P of A, of B; O of A, of B
+  static constexpr uint32_t IDESC_S = mma_idesc(1u, 128, 128);
+  static constexpr uint32_t IDESC_O = mma_idesc(1u, 128, D) | (1u << 16);  // V: N-major
+  static_assert(SMEM <= 232448, "shared memory");
+  static_assert((kMaxPagedRequests + 1) * 4 <= NST * TILE_BYTES, "prefix sums in the ring");
+};
+
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void tma_load_box3(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                              int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// Descriptor of a [keys, 64-element columns] tile read along its elements
+// (N-major B operand): 8-key atoms 1024 bytes apart, columns `column` bytes.
+__device__ __forceinline__ uint64_t sw128_nmajor_desc(uint32_t saddr, uint32_t column) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(column >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], one elected thread.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// ------------------------------------------------------------------- the work
+
+// One request: its first token, tokens and context, all inside the buffers.
+struct Req {
+  int b, s0, n, L;
+};
+
+__device__ __forceinline__ Req req_of(const KvAttnParams& p, int b, uint32_t* err = nullptr) {
+  const int a = __ldg(p.starts + b), e = __ldg(p.starts + b + 1), L = __ldg(p.context_lens + b);
+  const int cap = p.max_blocks << p.log_bs;
+  Req r;
+  r.b = b;
+  r.s0 = min(max(a, 0), p.T);
+  r.n = min(max(e, r.s0), p.T) - r.s0;
+  r.L = min(max(L, 0), cap);
+  if (err && (a < 0 || e < a || e > p.T || L < 0 || L > cap)) record_error(err, kErrBadIndex);
+  return r;
+}
+
+__device__ __forceinline__ int tiles_of(const KvAttnParams& p, const Req& r) {
+  return (r.n + 2 * p.tpt - 1) / (2 * p.tpt);
+}
+
+// One tile of rows: its tokens, their positions, and the key tiles that any of
+// them sees: the first `nsink`, then those from `first` on, `keys` in all (one
+// when none is seen, so that the rows' empty results are written).
+struct Tile {
+  int tok0, ntok, p0, nsink, first, keys, units;
+  bool tall;
+  __device__ int key_tile(int j) const { return j < nsink ? j : first + (j - nsink); }
+  // The i-th key tile of group g from unit j on.
+  __device__ int key_of(int j, int i, int g) const {
+    return key_tile(tall ? j + i : 2 * (j + i) + g);
+  }
+  __device__ int last() const { return p0 + ntok - 1; }
+};
+
+__device__ __forceinline__ Tile tile_of(const KvAttnParams& p, const Req& r, int qt) {
+  Tile t;
+  const int at = qt * 2 * p.tpt;
+  t.ntok = min(2 * p.tpt, r.n - at);
+  t.tall = t.ntok > p.tpt;
+  t.tok0 = r.s0 + at;
+  t.p0 = r.L - r.n + at;
+  const int end = max(t.last() + 1, 0);
+  t.first = p.window > 0 ? max(t.p0 - p.window + 1, 0) / kTile : 0;
+  t.nsink = min((min(p.sink, end) + kTile - 1) / kTile, t.first);
+  t.keys = max(t.nsink + (end + kTile - 1) / kTile - t.first, 1);
+  t.units = t.tall ? t.keys : (t.keys + 1) / 2;
+  return t;
+}
+
+// Whether every row of the tile sees all keys of key tile kt.
+__device__ __forceinline__ bool all_seen(const KvAttnParams& p, const Tile& t, int kt) {
+  const int c0 = kt * kTile;
+  return c0 + kTile - 1 <= t.p0 &&
+         (p.window == 0 || c0 > t.last() - p.window || c0 + kTile <= p.sink);
+}
+
+// A run of units and where it stands; every role walks it by itself.
+struct Walk {
+  Req r;
+  int h, qt, j;
+  int64_t left;
+  __device__ void next(const KvAttnParams& p, int taken) {
+    left -= taken;
+    j = 0;
+    if (left <= 0) return;
+    if (++qt < tiles_of(p, r)) return;
+    qt = 0;
+    do {
+      if (r.b + 1 < p.B) {
+        r = req_of(p, r.b + 1);
+      } else {
+        ++h;
+        r = req_of(p, 0);
+      }
+    } while (r.n == 0);
+  }
+};
+
+// Units of one request's row tiles for one head, summed by one thread.
+__device__ __forceinline__ int units_by_thread(const KvAttnParams& p, const Req& r, int nt) {
+  int u = 0;
+  for (int qt = 0; qt < nt; ++qt) u += tile_of(p, r, qt).units;
+  return u;
+}
+
+// This CTA's run.  Called by all threads; `pfx` is B + 1 ints of scratch.
+__device__ Walk find_run(const KvAttnParams& p, int* pfx) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // Requests of few row tiles are summed by a thread each, others by a warp.
+  constexpr int kFew = 4;
+  uint32_t* err = blockIdx.x == 0 ? p.err : nullptr;
+  for (int b = tid; b < p.B; b += kThreads) {
+    const Req r = req_of(p, b, err);
+    const int nt = tiles_of(p, r);
+    pfx[b + 1] = nt <= kFew ? units_by_thread(p, r, nt) : -1;
+  }
+  __syncthreads();
+  for (int b = warp; b < p.B; b += kThreads / 32) {
+    if (pfx[b + 1] >= 0) continue;
+    const Req r = req_of(p, b);
+    const int nt = tiles_of(p, r);
+    int u = 0;
+    for (int qt = lane; qt < nt; qt += 32) u += tile_of(p, r, qt).units;
+    u = __reduce_add_sync(0xffffffffu, u);
+    __syncwarp();
+    if (lane == 0) pfx[b + 1] = u;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int carry = 0;
+    if (lane == 0) pfx[0] = 0;
+    for (int at = 0; at < p.B; at += 32) {
+      int v = at + lane < p.B ? pfx[at + lane + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+      }
+      if (at + lane < p.B) pfx[at + lane + 1] = carry + v;
+      carry += __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+  __syncthreads();
+  const int U = pfx[p.B];
+  const int64_t total = static_cast<int64_t>(U) * p.Hkv;
+  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
+  Walk w = {};
+  if (static_cast<int64_t>(blockIdx.x) < ctas) {
+    const int64_t u0 = blockIdx.x * total / ctas;
+    w.left = (blockIdx.x + 1) * total / ctas - u0;
+    w.h = static_cast<int>(u0 / U);
+    int at = static_cast<int>(u0 - static_cast<int64_t>(w.h) * U);
+    int lo = 0, hi = p.B;  // the request: pfx[lo] <= at < pfx[lo + 1]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pfx[mid] <= at) lo = mid; else hi = mid;
+    }
+    at -= pfx[lo];
+    w.r = req_of(p, lo);
+    const int nt = tiles_of(p, w.r);
+    for (int base = 0; base < nt; base += 32) {
+      const int u = base + lane < nt ? tile_of(p, w.r, base + lane).units : 0;
+      int incl = u;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, incl > at);
+      if (past) {
+        const int k = __ffs(past) - 1;
+        w.qt = base + k;
+        w.j = at - __shfl_sync(0xffffffffu, incl - u, k);
+        break;
+      }
+      at -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  // The scratch is the ring that TMA writes next.
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncthreads();
+  return w;
+}
+
+// Key tiles that A and B take of `take` units from j on.
+struct Shares {
+  int a, b;
+};
+__device__ __forceinline__ Shares shares(const Tile& t, int j, int take) {
+  return {take, t.tall || 2 * (j + take) <= t.keys ? take : take - 1};
+}
+
+// Where a role stands in the ring of stages.
+template <int N>
+struct Ring {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ void step() {
+    if (++st == N) {
+      st = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
+// Zeroes the infinities and NaN of a tile in shared memory (64 threads) and
+// says so in *flag.
+template <int BYTES>
+__device__ __forceinline__ void clear_nonfinite(uint8_t* tile, int me, volatile uint32_t* flag) {
+  uint4* v = reinterpret_cast<uint4*>(tile);
+  uint32_t top = 0;
+#pragma unroll 8
+  for (int k = me; k < BYTES / 16; k += 64) {
+    const uint4 x = v[k];
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                                 __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+  }
+  if ((top & 0xFFFFu) < 0x7F80u && (top >> 16) < 0x7F80u) return;
+  uint16_t* e = reinterpret_cast<uint16_t*>(v);
+  for (int k = me; k < BYTES / 16; k += 64)
+    for (int q = 0; q < 8; ++q)
+      if ((e[8 * k + q] & 0x7F80u) == 0x7F80u) e[8 * k + q] = 0;
+  *flag = 1;
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Bits below x of a 32-bit word.
+__device__ __forceinline__ uint32_t below(int x) {
+  return x <= 0 ? 0u : x >= 32 ? 0xFFFFFFFFu : (1u << x) - 1u;
+}
+
+// What a row sees, relative to a key tile: columns <= hi that are >= lo or < sk.
+struct Sight {
+  int hi, lo, sk;
+  __device__ bool all() const { return hi >= kTile - 1 && (lo <= 0 || sk >= kTile); }
+  __device__ uint32_t word(int k) const {
+    return below(hi + 1 - 32 * k) & (~below(lo - 32 * k) | below(sk - 32 * k));
+  }
+  __device__ bool sees(int c) const { return c <= hi && (c >= lo || c < sk); }
+};
+
+__device__ __forceinline__ Sight sight_of(const KvAttnParams& p, int pos, int c0) {
+  return {pos - c0, p.window > 0 ? pos - p.window + 1 - c0 : 0, p.sink - c0};
+}
+
+__device__ __forceinline__ int page_of(const KvAttnParams& p, const Req& r, int c) {
+  const int used = (r.L + (1 << p.log_bs) - 1) >> p.log_bs;
+  const int lb = min(c >> p.log_bs, used - 1);
+  if (lb < 0) return 0;
+  const int page = __ldg(p.block_table + static_cast<int64_t>(r.b) * p.max_blocks + lb);
+  if (page < 0 || page >= p.num_blocks) {
+    record_error(p.err, kErrBadIndex);
+    return 0;
+  }
+  return page;
+}
+
+// Infinities and NaN among the values that a row sees in tiles that are not
+// wholly seen, which the products left out, added to elements d0 .. of its
+// output.
+template <int D, int N>
+__device__ __forceinline__ void add_nonfinite(const KvAttnParams& p, const Walk& w, const Tile& t,
+                                              int take, int pos, int d0, float (&o)[N]) {
+  const int j0 = t.tall ? w.j : 2 * w.j;
+  const int j1 = min(t.tall ? w.j + take : 2 * (w.j + take), t.keys);
+  for (int j = j0; j < j1; ++j) {
+    const int kt = t.key_tile(j);
+    if (all_seen(p, t, kt)) continue;
+    const Sight s = sight_of(p, pos, kt * kTile);
+    for (int c = 0; c < kTile; ++c) {
+      if (!s.sees(c)) continue;
+      const int key = kt * kTile + c;
+      const int64_t row = ((static_cast<int64_t>(page_of(p, w.r, key)) * p.Hkv + w.h)
+                           << p.log_bs) + (key & ((1 << p.log_bs) - 1));
+      const uint16_t* v = p.v + row * D + d0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint32_t x = v[i];
+        if ((x & 0x7F80u) == 0x7F80u) o[i] += __uint_as_float(x << 16);
+      }
+    }
+  }
+}
+
+// N elements of an output row: bf16 to `out`, or fp32 to a part.
+template <int N>
+__device__ __forceinline__ void store_out(uint16_t* out, const float (&o)[N], float f) {
+#pragma unroll
+  for (int i = 0; i < N; i += 8) {
+    uint32_t v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(o[i + 2 * k] * f, o[i + 2 * k + 1] * f);
+      v[k] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+    *reinterpret_cast<uint4*>(out + i) = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_part(float* out, const float (&o)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4)
+    *reinterpret_cast<float4*>(out + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+}
+
+__device__ __forceinline__ float lse_of(float m2, float l) {
+  return l == 0.f ? -INFINITY : (m2 + log2f(l)) * 0.69314718055994531f;
+}
+
+// ----------------------------------------------------------------- the kernel
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv_attn_kernel(const __grid_constant__ KvAttnParams p) {
+  using C = AttnCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* ring = smem + C::RING;
+  uint8_t* misc = smem + C::MISC;
+  float2* xml = reinterpret_cast<float2*>(misc + C::XML);
+  uint64_t* full = reinterpret_cast<uint64_t*>(misc + C::BARS);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* clean = empty + kMaxStages;
+  uint64_t* qfull = clean + kMaxStages;
+  uint64_t* qempty = qfull + 1;
+  uint64_t* sfull = qempty + 1;  // [2] S is in TMEM
+  uint64_t* pfull = sfull + 2;   // [2] P is in TMEM, O rescaled
+  uint64_t* ofull = pfull + 2;   // [2] a piece's last product is done
+  uint64_t* xbar = ofull + 2;    // [2] short pieces: sums exchanged; both outputs read
+  uint64_t* drained = xbar + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + C::SLOT);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  volatile uint32_t* nonfinite = tmem_slot + 2;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  launch_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < C::NST; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 3);  // the products, and the two warps of the check
+      mbar_init(&clean[i], 64);
+    }
+    mbar_init(qfull, 1);
+    mbar_init(qempty, 1);
+    mbar_init(drained, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sfull[i], 1);
+      mbar_init(&pfull[i], 4);
+      mbar_init(&ofull[i], 1);
+      mbar_init(&xbar[i], 256);
+    }
+    tmem_slot[1] = 0;
+    tmem_slot[2] = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9) tmem_alloc(tmem_slot, 512);
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&p.tmap_q);
+    tma_prefetch_desc(&p.tmap_k);
+    tma_prefetch_desc(&p.tmap_v);
+  }
+  tc_fence_before_sync();
+  Walk w = find_run(p, reinterpret_cast<int*>(ring));
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  if (tid == 0) p.notes[2 * blockIdx.x] = p.notes[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+
+  bool ok = true;
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 8) {
+      // ------------------------------------------------------------- producer
+      Ring<C::NST> at;
+      int pieces = 0, loads = 0;
+      const int per_tile = kTile >> p.log_bs;
+      auto page = [&](int kt) {
+        return lane < per_tile ? page_of(p, w.r, kt * kTile + (lane << p.log_bs)) : 0;
+      };
+      auto load = [&](const CUtensorMap* map, int pg) {
+        if (ok && lane == 0) ok = mbar_wait_bounded(&empty[at.st], at.ph ^ 1u, abort_flag);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) return;
+        if (lane == 0) mbar_arrive_expect_tx(&full[at.st], C::TILE_BYTES);
+        __syncwarp();
+        if (lane < per_tile) {
+          uint8_t* dst = ring + at.st * C::TILE_BYTES + ((lane * 128) << p.log_bs);
+          const int row = (pg * p.Hkv + w.h) << p.log_bs;
+#pragma unroll
+          for (int a = 0; a < C::HALVES; ++a)
+            tma_load_2d(dst + a * C::HALF_BYTES, map, &full[at.st], a * 64, row);
+        }
+        at.step();
+        ++loads;
+      };
+      while (ok && w.left > 0) {
+        const Tile t = tile_of(p, w.r, w.qt);
+        const int take = static_cast<int>(min(static_cast<int64_t>(t.units - w.j), w.left));
+        const Shares n = shares(t, w.j, take);
+        // Pages of the tiles whose values are loaded next, and of those after.
+        int pa = page(t.key_of(w.j, 0, 0)), pb = !t.tall && n.b > 0 ? page(t.key_of(w.j, 0, 1)) : 0;
+        int na = 0, nb = 0;
+        if (lane == 0)
+          ok = mbar_wait_bounded(qempty, (static_cast<uint32_t>(pieces) & 1u) ^ 1u, abort_flag);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
+        if (lane == 0) {
+          const int nq = t.tall ? 2 : 1;
+          mbar_arrive_expect_tx(qfull, nq * C::HALVES * p.tpt * p.G * 128);
+          for (int q = 0; q < nq; ++q)
+#pragma unroll
+            for (int a = 0; a < C::HALVES; ++a)
+              tma_load_box3(smem + q * C::TILE_BYTES + a * C::HALF_BYTES, &p.tmap_q, qfull, a * 64,
+                            w.h * p.G, t.tok0 + q * p.tpt);
+        }
+        __syncwarp();
+        ++pieces;
+        load(&p.tmap_k, pa);
+        if (!t.tall && n.b > 0) load(&p.tmap_k, pb);
+#pragma unroll 1
+        for (int i = 0; ok && i < n.a; ++i) {
+          if (i + 1 < n.a) na = page(t.key_of(w.j, i + 1, 0));
+          if (!t.tall && i + 1 < n.b) nb = page(t.key_of(w.j, i + 1, 1));
+          load(&p.tmap_v, pa);
+          pa = na;
+          if (i + 1 < n.a) load(&p.tmap_k, pa);
+          if (t.tall || i >= n.b) continue;
+          load(&p.tmap_v, pb);
+          pb = nb;
+          if (i + 1 < n.b) load(&p.tmap_k, pb);
+        }
+        w.next(p, take);
+      }
+      if (!ok && lane == 0) {
+        // Let the copies already in flight land before the CTA retires.
+        for (int i = loads > C::NST ? loads - C::NST : 0; i < loads; ++i)
+          mbar_wait_bounded(&full[i % C::NST], static_cast<uint32_t>(i / C::NST) & 1u, nullptr,
+                            100000000ull);
+        if (pieces > 0)
+          mbar_wait_bounded(qfull, static_cast<uint32_t>(pieces - 1) & 1u, nullptr, 100000000ull);
+      }
+    } else if (warp == 9) {
+      // ----------------------------------------------------------- MMA issuer
+      if (lane == 0) {
+        Ring<C::NST> at;
+        int pieces = 0, ks = 0;
+        uint32_t pn = 0, cleaned = 0;  // phases of pfull (a bit a group) and of clean (a bit a stage)
+        const uint32_t q_addr = smem_u32(smem), r_addr = smem_u32(ring);
+        auto take_stage = [&]() {
+          if (ok) ok = mbar_wait_bounded(&full[at.st], at.ph, abort_flag);
+          const int st = at.st;
+          at.step();
+          return st;
+        };
+        // S of group g: its queries times the keys in the next stage (tall: in
+        // the stage that both groups share).
+        auto s_mma = [&](bool tall, int g) {
+          if (!tall || g == 0) ks = take_stage();
+          if (!ok) return;
+          tc_fence_after_sync();
+          const uint32_t qa = q_addr + (tall ? g : 0) * C::TILE_BYTES;
+          const uint32_t ka = r_addr + ks * C::TILE_BYTES;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k / 4) * C::HALF_BYTES + (k % 4) * 32;
+            mma_ss<false>(tmem + C::S_COL + g * 128, sw128_kmajor_desc(qa + off),
+                          sw128_kmajor_desc(ka + off), C::IDESC_S, k > 0 ? 1u : 0u);
+          }
+          mma_commit(&sfull[g]);
+          if (!tall || g == 1) mma_commit(&empty[ks]);
+        };
+#pragma unroll 1
+        while (ok && w.left > 0) {
+          const Tile t = tile_of(p, w.r, w.qt);
+          const int take = static_cast<int>(min(static_cast<int64_t>(t.units - w.j), w.left));
+          const Shares n = shares(t, w.j, take);
+          ok = mbar_wait_bounded(qfull, static_cast<uint32_t>(pieces) & 1u, abort_flag);
+          ++pieces;
+#pragma unroll 1
+          for (int g = 0; ok && g < (n.b > 0 ? 2 : 1); ++g) s_mma(t.tall, g);
+          if (ok && take == 1) mma_commit(qempty);
+          int vs = 0;
+#pragma unroll 1
+          for (int i = 0; ok && i < n.a; ++i) {
+#pragma unroll 1
+            for (int g = 0; ok && g < (i < n.b ? 2 : 1); ++g) {
+              if (!t.tall || g == 0) {
+                vs = take_stage();
+                if (!all_seen(p, t, t.key_of(w.j, i, g))) {
+                  if (ok) ok = mbar_wait_bounded(&clean[vs], cleaned >> vs & 1u, abort_flag);
+                  cleaned ^= 1u << vs;
+                }
+              }
+              if (ok) ok = mbar_wait_bounded(&pfull[g], pn >> g & 1u, abort_flag);
+              pn ^= 1u << g;
+              if (!ok) break;
+              tc_fence_after_sync();
+              const uint32_t va = r_addr + vs * C::TILE_BYTES;
+#pragma unroll
+              for (int k = 0; k < kTile / 16; ++k)
+                mma_ts(tmem + C::O_COL + g * D, tmem + C::S_COL + g * 128 + k * 8,
+                       sw128_nmajor_desc(va + k * 2048, C::HALF_BYTES), C::IDESC_O,
+                       k > 0 || i > 0 ? 1u : 0u);
+              if (!t.tall || g == 1) mma_commit(&empty[vs]);
+              // S of the next tile overwrites P: the tensor core takes the
+              // products of one thread in their order.
+              if (i + 1 < (g ? n.b : n.a))
+                s_mma(t.tall, g);
+              else
+                mma_commit(&ofull[g]);
+            }
+            if (ok && i + 2 == take) mma_commit(qempty);  // the piece's last S is issued
+          }
+          if (!ok) break;
+          w.next(p, take);
+        }
+        // All products of this CTA are done before its TMEM is given back.
+        mma_commit(drained);
+        mbar_wait_bounded(drained, 0, nullptr, 100000000ull);
+      }
+      __syncwarp();
+    } else {
+      // ---------------------------------------------- values that some row does not see
+      Ring<C::NST> at;
+      const int me = tid - 320;
+      // Every stage is waited for and given back, looked at or not: a phase
+      // that is skipped could be taken for another one.
+      auto pass = [&](bool look) {
+        if (ok) ok = mbar_wait_bounded(&full[at.st], at.ph, abort_flag);
+        if (ok && look) {
+          clear_nonfinite<C::TILE_BYTES>(ring + at.st * C::TILE_BYTES, me, nonfinite);
+          mbar_arrive(&clean[at.st]);
+        }
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&empty[at.st]);
+        at.step();
+      };
+#pragma unroll 1
+      while (ok && w.left > 0) {
+        const Tile t = tile_of(p, w.r, w.qt);
+        const int take = static_cast<int>(min(static_cast<int64_t>(t.units - w.j), w.left));
+        const Shares n = shares(t, w.j, take);
+        pass(false);  // the first keys
+        if (!t.tall && n.b > 0) pass(false);
+#pragma unroll 1
+        for (int i = 0; ok && i < n.a; ++i) {
+#pragma unroll 1
+          for (int g = 0; ok && g < (!t.tall && i < n.b ? 2 : 1); ++g) {
+            pass(!all_seen(p, t, t.key_of(w.j, i, g)));
+            if (i + 1 < (g ? n.b : n.a)) pass(false);  // keys
+          }
+        }
+        w.next(p, take);
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int g = warp >> 2, row = tid & 127;
+    const uint32_t quarter = static_cast<uint32_t>(warp & 3) << 21;  // 32 lanes, << 16
+    const uint32_t s_addr = tmem + quarter + C::S_COL + g * 128;
+    const uint32_t o_addr = tmem + quarter + C::O_COL;
+    const float sc = p.scale_log2e;
+    uint32_t sn = 0, xn = 0, on = 0;  // parities of the phases waited for (ofull: a bit a group)
+    while (ok && w.left > 0) {
+      const Tile t = tile_of(p, w.r, w.qt);
+      const int take = static_cast<int>(min(static_cast<int64_t>(t.units - w.j), w.left));
+      const Shares n = shares(t, w.j, take);
+      const int tok = row / p.G + (t.tall ? g * p.tpt : 0);
+      const bool mine = row < p.tpt * p.G && tok < t.ntok;
+      const int pos = t.p0 + tok;
+      const bool busy = __any_sync(0xffffffffu, mine);
+      float m = -INFINITY, l = 0.f;
+      const int steps = g ? n.b : n.a;
+      for (int i = 0; i < steps; ++i) {
+        const int kt = t.key_of(w.j, i, g);
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait_bounded(&sfull[g], sn, abort_flag) ? 1 : 0);
+        sn ^= 1u;
+        if (!ok) break;
+        if (busy) {
+          tc_fence_after_sync();
+          uint32_t s[4][32];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tmem_ld32_async(s_addr + 32 * k, s[k]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tmem_wait_ld(s[k]);
+          const Sight see = sight_of(p, pos, kt * kTile);
+          if (__any_sync(0xffffffffu, mine && !see.all())) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t word = see.word(k);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(word >> c & 1u)) s[k][c] = 0xFF800000u;
+            }
+          }
+          float mx[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            mx[k] = __uint_as_float(s[k][0]);
+#pragma unroll
+            for (int c = 1; c < 32; ++c) mx[k] = fmaxf(mx[k], __uint_as_float(s[k][c]));
+          }
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          if (__any_sync(0xffffffffu, top > m + p.lazy)) {
+            const float mn = fmaxf(m, top);
+            const float f = m == -INFINITY ? 0.f : ex2((m - mn) * sc);
+            m = mn;
+            l *= f;
+            if (i > 0) {
+#pragma unroll
+              for (int d = 0; d < D; d += 16) {
+                float o[16];
+                tmem_load16(o_addr + g * D + d, o);
+                uint32_t r[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(o[k] * f);
+                tmem_st16(o_addr + g * D + d, r);
+              }
+            }
+          }
+          const float ref = m == -INFINITY ? 0.f : -m * sc;
+          const float2 ref2 = make_float2(ref, ref), sc2 = make_float2(sc, sc);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              const float2 x = __ffma2_rn(
+                  make_float2(__uint_as_float(s[k][c]), __uint_as_float(s[k][c + 1])), sc2, ref2);
+              const float2 e = make_float2(ex2(x.x), ex2(x.y));
+              sum[c >> 1 & 1] = __fadd2_rn(sum[c >> 1 & 1], e);
+              const __nv_bfloat162 y = __floats2bfloat162_rn(e.x, e.y);
+              pk[c >> 1] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            tmem_st16(s_addr + 16 * k, pk);
+          }
+          const float2 both = __fadd2_rn(sum[0], sum[1]);
+          l += both.x + both.y;
+          tmem_wait_st();
+          tc_fence_before_sync();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[g]);
+      }
+      // The piece's outputs.
+      auto wait_o = [&](int k) {
+        if ((k ? n.b : n.a) == 0) return;
+        if (ok)
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait_bounded(&ofull[k], on >> k & 1u, abort_flag) ? 1 : 0);
+        on ^= 1u << k;
+      };
+      wait_o(g);
+      if (!t.tall) wait_o(1 - g);
+      if (!ok) break;
+      tc_fence_after_sync();
+      const bool whole = w.j == 0 && take == t.units;
+      const int64_t at =
+          static_cast<int64_t>(t.tok0 + tok) * p.Hq + w.h * p.G + (row - row / p.G * p.G);
+      const int64_t part = static_cast<int64_t>(2 * blockIdx.x + (w.j == 0 ? 1 : 0)) * p.slot_rows +
+                           (t.tall ? g * kTile : 0) + row;
+      const bool bad = *nonfinite != 0;
+      const float m2 = m * sc;
+      if (t.tall) {
+        const float f = l == 0.f ? 0.f : 1.f / l;
+        if (busy) {
+#pragma unroll
+          for (int d = 0; d < D; d += 32) {
+            float o[32];
+            tmem_load32(o_addr + g * D + d, o);
+            if (mine) {
+              if (bad) add_nonfinite<D>(p, w, t, take, pos, d, o);
+              if (whole)
+                store_out(p.out + at * D + d, o, f);
+              else
+                store_part(p.part_o + part * D + d, o);
+            }
+            __syncwarp();
+          }
+        }
+        if (mine) {
+          if (!whole)
+            p.part_ml[part] = make_float2(m2, l);
+          else if (p.lse)
+            p.lse[at] = lse_of(m2, l);
+        }
+        wait_o(1 - g);  // no phase is skipped
+        if (!ok) break;
+      } else {
+        // A and B hold two halves of the same rows' keys: each group joins one
+        // half of the elements.
+        xml[g * 128 + row] = make_float2(m2, l);
+        mbar_arrive(&xbar[0]);
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&xbar[0], xn, abort_flag) ? 1 : 0);
+        if (!ok) break;
+        const float2 a = xml[row], b = n.b > 0 ? xml[128 + row] : make_float2(-INFINITY, 0.f);
+        const float top = fmaxf(a.x, b.x);
+        const float fa = a.x == -INFINITY ? 0.f : ex2(a.x - top);
+        const float fb = b.x == -INFINITY ? 0.f : ex2(b.x - top);
+        const float sum = a.y * fa + b.y * fb;
+        const float f = sum == 0.f ? 0.f : 1.f / sum;
+        if (busy) {
+#pragma unroll
+          for (int d = 0; d < D / 2; d += 32) {
+            const int d0 = g * (D / 2) + d;
+            float o[32];
+            tmem_load32(o_addr + d0, o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] *= fa;
+            if (n.b > 0) {
+              float o2[32];
+              tmem_load32(o_addr + D + d0, o2);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = fmaf(o2[k], fb, o[k]);
+            }
+            if (mine) {
+              if (bad) add_nonfinite<D>(p, w, t, take, pos, d0, o);
+              if (whole)
+                store_out(p.out + at * D + d0, o, f);
+              else
+                store_part(p.part_o + part * D + d0, o);
+            }
+            __syncwarp();
+          }
+        }
+        if (mine && g == 0) {
+          if (!whole)
+            p.part_ml[part] = make_float2(top, sum);
+          else if (p.lse)
+            p.lse[at] = lse_of(top, sum);
+        }
+        tc_fence_before_sync();
+        mbar_arrive(&xbar[1]);
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&xbar[1], xn, abort_flag) ? 1 : 0);
+        xn ^= 1u;
+        if (!ok) break;
+        tc_fence_after_sync();
+      }
+      if (!whole && tid == 0) {
+        // Slot 1 starts a tile, slot 0 goes on with one that an earlier CTA
+        // started (and, with 2, ends it).
+        if (w.j == 0)
+          p.notes[2 * blockIdx.x + 1] = make_int4(1, w.r.b, w.qt, w.h);
+        else
+          p.notes[2 * blockIdx.x] = make_int4(w.j + take == t.units ? 2 : 1, 0, 0, 0);
+      }
+      w.next(p, take);
+    }
+  }
+  if (!ok) {
+    *abort_flag = 1;
+    record_error(p.err, kErrTimeout);
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------- the join
+
+constexpr int kJoinWarps = 8;
+
+// The parts of each cut tile, a warp a row: CTA blockIdx.x started the tile,
+// the next ones went on with it.
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(
+    const __grid_constant__ KvAttnParams p) {
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int cta = blockIdx.x;
+  const int4 note = p.notes[2 * cta + 1];
+  if (note.x == 0) return;
+  const Req r = req_of(p, note.y);
+  const Tile t = tile_of(p, r, note.z);
+  const int rows = t.ntok * p.G;
+  if (blockIdx.y * kJoinWarps + warp >= rows) return;
+  // How many CTAs went on with the tile.
+  int more = 0;
+  for (int at = cta + 1; at < p.ctas; at += 32) {
+    const bool ends = at + lane < p.ctas && p.notes[2 * (at + lane)].x == 2;
+    const uint32_t vote = __ballot_sync(0xffffffffu, ends);
+    if (vote) {
+      more += __ffs(vote);
+      break;
+    }
+    more += 32;
+  }
+  more = min(more, p.ctas - 1 - cta);
+  constexpr int N = D / 32;
+  for (int i = blockIdx.y * kJoinWarps + warp; i < rows; i += gridDim.y * kJoinWarps) {
+    const int tok = i / p.G, g = i - tok * p.G;
+    const int row = tok / p.tpt * kTile + (tok % p.tpt) * p.G + g;
+    auto part = [&](int k) {
+      return static_cast<int64_t>(k == 0 ? 2 * cta + 1 : 2 * (cta + k)) * p.slot_rows + row;
+    };
+    float top = -INFINITY;
+    for (int k = lane; k <= more; k += 32) top = fmaxf(top, p.part_ml[part(k)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float sum = 0.f, acc[N] = {};
+#pragma unroll 4
+    for (int k = 0; k <= more; ++k) {
+      const int64_t at = part(k);
+      const float2 ml = p.part_ml[at];
+      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+      sum = fmaf(ml.y, f, sum);
+      float v[N];
+      if constexpr (N == 4) {
+        const float4 x = reinterpret_cast<const float4*>(p.part_o + at * D)[lane];
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+      } else {
+        const float2 x = reinterpret_cast<const float2*>(p.part_o + at * D)[lane];
+        v[0] = x.x; v[1] = x.y;
+      }
+#pragma unroll
+      for (int q = 0; q < N; ++q) acc[q] = f == 0.f ? acc[q] : fmaf(v[q], f, acc[q]);
+    }
+    const float f = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t at = static_cast<int64_t>(t.tok0 + tok) * p.Hq + note.w * p.G + g;
+    uint32_t v[N / 2];
+#pragma unroll
+    for (int q = 0; q < N / 2; ++q) {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(acc[2 * q] * f, acc[2 * q + 1] * f);
+      v[q] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+    if constexpr (N == 4)
+      reinterpret_cast<uint2*>(p.out + at * D)[lane] = make_uint2(v[0], v[1]);
+    else
+      reinterpret_cast<uint32_t*>(p.out + at * D)[lane] = v[0];
+    if (lane == 0 && p.lse) p.lse[at] = lse_of(top, sum);
+  }
+}
+
+template <int D>
+cudaError_t launch_d(const KvAttnParams& p, cudaStream_t s) {
+  using C = AttnCfg<D>;
+  // The attribute is set once a device (devices past 64: every time).
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kv_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::SMEM);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  kv_attn_kernel<D><<<p.ctas, kThreads, C::SMEM, s>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // Launched while the attention kernel still runs (it waits inside).
+  const int64_t rows = static_cast<int64_t>(p.T) * p.G;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.ctas, ((rows < p.slot_rows ? static_cast<int>(rows) : p.slot_rows) +
+                              kJoinWarps - 1) / kJoinWarps);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D>, p);
+}
+
+int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+KvAttnPlan kv_attn_plan(int T, int G, int D) {
+  KvAttnPlan pl = {};
+  pl.tpt = kTile / G;
+  pl.ctas = device_sm_count() > 0 ? device_sm_count() : 1;
+  pl.slot_rows = T > pl.tpt ? 2 * kTile : kTile;
+  const int64_t rows = static_cast<int64_t>(pl.ctas) * 2 * pl.slot_rows;
+  pl.part_ml = up256(static_cast<int64_t>(pl.ctas) * 2 * 16);
+  pl.part_o = pl.part_ml + up256(rows * 8);
+  pl.bytes = pl.part_o + up256(rows * D * 4);
+  return pl;
+}
+
+int64_t kv_attn_units(int T, int B, int G, int64_t max_ctx) {
+  return (static_cast<int64_t>(T) / (2 * (kTile / G)) + B) * ((max_ctx + kTile - 1) / kTile + 1);
+}
+
+cudaError_t launch_kv_attention(const KvAttnParams& p, int D, cudaStream_t s) {
+  return D == 64 ? launch_d<64>(p, s) : launch_d<128>(p, s);
+}
+
+}  // namespace dsa
