@@ -14,11 +14,11 @@
 // whole turns), whatever the position: no table over positions, no 64-bit
 // floating point, and an error below 2^-31 turns at every position of 32 bits.
 //
-// Every element needs only its own and its partner's input:
-//   out_i = rstd (x_i A_i + x_partner B_i),  A = w_i m cos,  B = +-w_partner m sin
-// so a CTA writes A and B of its tokens to shared memory once and applies them
-// to all heads.  D / 8 lanes take a row, 16 bytes each; the partner's elements
-// come by shuffles.  The pass is memory-bound.
+// A CTA writes the cosines and sines of its tokens to shared memory once; D / 8
+// lanes take a row, each the elements of whole pairs (two groups of four that
+// lie F apart, or eight neighbours), so nothing but the norm's sum crosses
+// lanes, and they keep the products of weights, cosines and sines while their
+// rows stay with one token and kind.  The pass is memory-bound.
 #include <cuda_bf16.h>
 
 #include "dsa_common.cuh"
@@ -28,176 +28,205 @@ namespace dsa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 8;  // of a CTA
-constexpr int kAhead = 4;      // rows whose loads a lane has in flight
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxTokens = 16;  // of a CTA
+constexpr int kAhead = 4;       // rows whose loads a lane has in flight
 
+// A CTA takes `tasks` of the tasks of each of `tokens` tokens (blockIdx.y says
+// which); a task is up to kAhead rows a lane group of one token's queries, keys
+// or values, and goes to one warp.
 struct RopeShape {
-  int tokens;  // of a CTA
-  int rows;    // of one token that a CTA takes (blockIdx.y: which)
+  int tokens, tasks;
 };
 
-__device__ __forceinline__ void unpack8(const uint4 u, float (&x)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+__device__ __forceinline__ float2 unpack2(uint32_t u) {
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ uint32_t pack2(const float2 v) {
+  const __nv_bfloat162 o = __floats2bfloat162_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&o);
 }
 
 template <int D, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p, const RopeShape sh) {
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p, const RopeShape sh) {
   constexpr int kLanes = D / 8;
-  constexpr int kGroups = kThreads / kLanes;
-  // A and B of every element, for queries and for keys of each token.
-  __shared__ float2 ab[kMaxTokens][2][D];
-  const int tid = threadIdx.x, sub = tid % kLanes, group = tid / kLanes;
-  const int heads = p.Hq + p.Hk + p.Hv;
-  const int h0 = blockIdx.y * sh.rows;
-  const int hn = min(sh.rows, heads - h0);  // rows of one token here
+  constexpr int kGroups = 32 / kLanes;      // rows of a warp at a time
+  constexpr int kRows = kGroups * kAhead;   // of a task
+  // Cosine and sine of every pair, by token; pairs four by four, cosines first.
+  __shared__ float4 turn[kMaxTokens][D / 4];
+  const int tid = threadIdx.x, warp = tid >> 5, sub = tid % kLanes, group = tid % 32 / kLanes;
   const int t0 = blockIdx.x * sh.tokens;
   const int nt = min(sh.tokens, p.T - t0);
-  const int rows = nt * hn;
-
-  // Row `i` of this CTA: what it is, and where it comes from.
-  struct Row {
-    int t, h, kind;  // kind 0 query, 1 key, 2 value
-  };
-  auto row_of = [&](int i) {
-    Row r;
-    const int tt = i / hn;
-    const int h = h0 + (i - tt * hn);
-    r.t = t0 + tt;
-    r.kind = h < p.Hq ? 0 : h < p.Hq + p.Hk ? 1 : 2;
-    r.h = r.kind == 0 ? h : r.kind == 1 ? h - p.Hq : h - p.Hq - p.Hk;
-    return r;
-  };
-  auto fetch = [&](int i) {
-    if (i >= rows) return make_uint4(0u, 0u, 0u, 0u);
-    const Row r = row_of(i);
-    const uint16_t* src = r.kind == 0   ? p.q + r.t * p.q_stride
-                          : r.kind == 1 ? p.k + r.t * p.k_stride
-                                        : p.v + r.t * p.v_stride;
-    return *(reinterpret_cast<const uint4*>(src + r.h * D) + sub);
-  };
-  uint4 raw[kAhead];
-#pragma unroll
-  for (int a = 0; a < kAhead; ++a) raw[a] = fetch(group + a * kGroups);
-
+  const int nq = (p.Hq + kRows - 1) / kRows, nk = (p.Hk + kRows - 1) / kRows,
+            nv = (p.Hv + kRows - 1) / kRows;
+  const int first = blockIdx.y * sh.tasks;
+  const int per = min(sh.tasks, nq + nk + nv - first);  // of one token here
   const int F = p.rotary / 2;
-  for (int i = tid; i < nt * 2 * D; i += kThreads) {
-    const int e = i % D, which = i / D & 1, tt = i / (2 * D);
-    if ((which == 0 ? p.Hq : p.Hk) == 0) continue;
-    const float* weight = which == 0 ? p.q_weight : p.k_weight;
-    float2 c = make_float2(weight ? __ldg(weight + e) : 1.f, 0.f);
-    if (e < p.rotary) {
-      const int f = kInterleaved ? e >> 1 : e < F ? e : e - F;
-      const bool second = kInterleaved ? (e & 1) != 0 : e >= F;
-      const int partner = kInterleaved ? e ^ 1 : second ? e - F : e + F;
-      const uint64_t angle =
-          __ldg(p.turns + f) * static_cast<uint64_t>(static_cast<int64_t>(__ldg(p.positions + t0 + tt)));
-      float sn, cs;
-      // Half turns in [-1, 1).
-      sincospif(static_cast<float>(static_cast<int32_t>(angle >> 32)) * 0x1p-31f, &sn, &cs);
-      c.x *= cs * p.rope_scale;
-      c.y = (weight ? __ldg(weight + partner) : 1.f) * (sn * p.rope_scale);
-      if (!second) c.y = -c.y;
-    }
-    ab[tt][which][e] = c;
-  }
-  __syncthreads();
+  // This lane's elements: four from e0, four from e1.  Half layout: pairs
+  // (e0 + i, e1 + i) for the first F / 4 lanes, eight neighbours for the rest.
+  const bool turned = kInterleaved ? 8 * sub < p.rotary : 4 * sub < F;
+  const int e0 = kInterleaved ? 8 * sub : turned ? 4 * sub : 2 * F + 8 * (sub - F / 4);
+  const int e1 = !kInterleaved && turned ? e0 + F : e0 + 4;
+  const int first_pair = kInterleaved ? e0 / 2 : e0;  // of four
 
-  const bool turned = sub * 8 < p.rotary;  // whole lanes: rotary is a multiple of 16
-  const int other = kInterleaved ? sub : sub * 8 < F ? sub + F / 8 : sub - F / 8;
-  for (int base = group; base - group < rows; base += kAhead * kGroups) {
+  for (int i = tid; i < nt * F; i += kThreads) {
+    const int tt = i / F, f = i - tt * F;
+    const uint64_t angle = __ldg(p.turns + f) *
+                           static_cast<uint64_t>(static_cast<int64_t>(__ldg(p.positions + t0 + tt)));
+    float sn, cs;
+    // Half turns in [-1, 1).
+    sincospif(static_cast<float>(static_cast<int32_t>(angle >> 32)) * 0x1p-31f, &sn, &cs);
+    float* to = reinterpret_cast<float*>(&turn[tt][f / 4 * 2]) + f % 4;
+    to[0] = cs * p.rope_scale;
+    to[4] = sn * p.rope_scale;
+  }
+  bool ready = false;  // the table: waited for with the first rows' loads in flight
+
+  for (int task = warp; task < nt * per || !ready; task += kWarps) {
+    const bool none = task >= nt * per;
+    const int tt = none ? 0 : task / per;
+    const int c = first + (none ? 0 : task - tt * per);
+    const int64_t t = t0 + tt;
+    // What the task takes: kind 0 queries, 1 keys, 2 values.
+    const int kind = c < nq ? 0 : c < nq + nk ? 1 : 2;
+    const int h0 = (kind == 0 ? c : kind == 1 ? c - nq : c - nq - nk) * kRows + group;
+    const int H = none ? 0 : kind == 0 ? p.Hq : kind == 1 ? p.Hk : p.Hv;
+    const uint16_t* src = (kind == 0   ? p.q + t * p.q_stride
+                           : kind == 1 ? p.k + t * p.k_stride
+                                       : p.v + t * p.v_stride) + h0 * D;
+    uint4 raw[kAhead];
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const int i = base + a * kGroups;
-      if (i - group >= rows) break;  // the same for every group
-      const uint4 u = raw[a];
-      raw[a] = fetch(i + kAhead * kGroups);
-      uint4 pu = u;
-      if constexpr (!kInterleaved) {
-        pu.x = __shfl_sync(0xffffffffu, u.x, other, kLanes);
-        pu.y = __shfl_sync(0xffffffffu, u.y, other, kLanes);
-        pu.z = __shfl_sync(0xffffffffu, u.z, other, kLanes);
-        pu.w = __shfl_sync(0xffffffffu, u.w, other, kLanes);
-      }
-      float x[8], y[8];
-      unpack8(u, x);
-      unpack8(pu, y);
-      float ss = 0.f;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) ss = fmaf(x[q], x[q], ss);
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (i >= rows) continue;
-      const Row r = row_of(i);
-      uint16_t* dst;
-      if (r.kind == 0) {
-        dst = p.q_out + (static_cast<int64_t>(r.t) * p.Hq + r.h) * D;
-      } else {
-        const int H = r.kind == 1 ? p.Hk : p.Hv;
-        uint16_t* out = r.kind == 1 ? p.k_out : p.v_out;
-        if (p.slots) {
-          const int64_t slot = __ldg(p.slots + r.t);
-          if (slot < 0) continue;
-          if (slot >= p.capacity) {
-            if (sub == 0) record_error(p.err, kErrBadIndex);
-            continue;
-          }
-          dst = out + ((((slot >> p.log_bs) * H + r.h) << p.log_bs) +
-                       (slot & ((1 << p.log_bs) - 1))) * D;
+    for (int i = 0; i < kAhead; ++i) {
+      raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (h0 + i * kGroups < H) {
+        if constexpr (kInterleaved) {
+          raw[i] = *reinterpret_cast<const uint4*>(src + i * kGroups * D + e0);
         } else {
-          dst = out + (static_cast<int64_t>(r.t) * H + r.h) * D;
+          const uint2 a = *reinterpret_cast<const uint2*>(src + i * kGroups * D + e0);
+          const uint2 b = *reinterpret_cast<const uint2*>(src + i * kGroups * D + e1);
+          raw[i] = make_uint4(a.x, a.y, b.x, b.y);
         }
       }
-      if (r.kind == 2) {
-        *(reinterpret_cast<uint4*>(dst) + sub) = u;
-        continue;
+    }
+    // Where it goes: rows `pitch` elements apart.
+    uint16_t* dst = kind == 0 ? p.q_out : kind == 1 ? p.k_out : p.v_out;
+    int64_t pitch = D;
+    bool skip = none;
+    if (kind > 0 && p.slots) {
+      const int64_t slot = __ldg(p.slots + t);
+      const bool past = slot >= p.capacity;
+      if (past && (tid & 31) == 0 && !none) record_error(p.err, kErrBadIndex);
+      skip = skip || slot < 0 || past;
+      dst += (((slot >> p.log_bs) * H << p.log_bs) + (slot & ((1 << p.log_bs) - 1))) * D;
+      pitch = static_cast<int64_t>(D) << p.log_bs;
+    } else {
+      dst += t * H * D;
+    }
+    dst += h0 * pitch;
+    if (!ready) {
+      __syncthreads();
+      ready = true;
+    }
+    if (skip) continue;
+    auto store = [&](int i, const uint4 u) {
+      uint16_t* to = dst + i * kGroups * pitch;
+      if constexpr (kInterleaved) {
+        *reinterpret_cast<uint4*>(to + e0) = u;
+      } else {
+        *reinterpret_cast<uint2*>(to + e0) = make_uint2(u.x, u.y);
+        *reinterpret_cast<uint2*>(to + e1) = make_uint2(u.z, u.w);
       }
-      const float4* c4 = reinterpret_cast<const float4*>(&ab[r.t - t0][r.kind][8 * sub]);
-      const bool norm = (r.kind == 0 ? p.q_weight : p.k_weight) != nullptr;
-      const float rstd = norm ? rsqrtf(ss * (1.f / D) + p.eps) : 1.f;
-      uint32_t w[4];
+    };
+    if (kind == 2) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (h0 + i * kGroups < H) store(i, raw[i]);
+      continue;
+    }
+    // out = rstd (x A + partner B), in pairs of neighbouring elements.
+    const float* weight = kind == 0 ? p.q_weight : p.k_weight;
+    float2 A[4], B[4];
+    {
+      float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (turned) {
+        cs = turn[tt][first_pair / 2];
+        sn = turn[tt][first_pair / 2 + 1];
+      }
+      float4 w0 = make_float4(1.f, 1.f, 1.f, 1.f), w1 = w0;
+      if (weight) {  // aligned to 4 bytes only
+        w0 = make_float4(__ldg(weight + e0), __ldg(weight + e0 + 1), __ldg(weight + e0 + 2),
+                         __ldg(weight + e0 + 3));
+        w1 = make_float4(__ldg(weight + e1), __ldg(weight + e1 + 1), __ldg(weight + e1 + 2),
+                         __ldg(weight + e1 + 3));
+      }
+      if constexpr (kInterleaved) {  // pairs (x, y) of a float2
+        A[0] = make_float2(w0.x * cs.x, w0.y * cs.x);
+        A[1] = make_float2(w0.z * cs.y, w0.w * cs.y);
+        A[2] = make_float2(w1.x * cs.z, w1.y * cs.z);
+        A[3] = make_float2(w1.z * cs.w, w1.w * cs.w);
+        B[0] = make_float2(-w0.y * sn.x, w0.x * sn.x);
+        B[1] = make_float2(-w0.w * sn.y, w0.z * sn.y);
+        B[2] = make_float2(-w1.y * sn.z, w1.x * sn.z);
+        B[3] = make_float2(-w1.w * sn.w, w1.z * sn.w);
+      } else {  // pairs (x[q], x[q + 2])
+        A[0] = make_float2(w0.x * cs.x, w0.y * cs.y);
+        A[1] = make_float2(w0.z * cs.z, w0.w * cs.w);
+        A[2] = make_float2(w1.x * cs.x, w1.y * cs.y);
+        A[3] = make_float2(w1.z * cs.z, w1.w * cs.w);
+        B[0] = make_float2(-w1.x * sn.x, -w1.y * sn.y);
+        B[1] = make_float2(-w1.z * sn.z, -w1.w * sn.w);
+        B[2] = make_float2(w0.x * sn.x, w0.y * sn.y);
+        B[3] = make_float2(w0.z * sn.z, w0.w * sn.w);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (h0 - group + i * kGroups >= H) break;  // the whole warp
+      float2 x[4] = {unpack2(raw[i].x), unpack2(raw[i].y), unpack2(raw[i].z), unpack2(raw[i].w)};
+      float2 y[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const float4 c = c4[q];  // A, B of elements 2q and 2q + 1
-        const float pa = kInterleaved ? x[2 * q + 1] : y[2 * q];
-        const float pb = kInterleaved ? x[2 * q] : y[2 * q + 1];
-        float oa = x[2 * q] * c.x, ob = x[2 * q + 1] * c.z;
-        if (turned) {
-          oa = fmaf(pa, c.y, oa);
-          ob = fmaf(pb, c.w, ob);
-        }
-        const __nv_bfloat162 o = __floats2bfloat162_rn(oa * rstd, ob * rstd);
-        w[q] = *reinterpret_cast<const uint32_t*>(&o);
+        y[q] = __fmul2_rn(x[q], A[q]);
+        if (turned)
+          y[q] = __ffma2_rn(kInterleaved ? make_float2(x[q].y, x[q].x) : x[q ^ 2], B[q], y[q]);
       }
-      *(reinterpret_cast<uint4*>(dst) + sub) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (weight) {
+        float2 ss = __fmul2_rn(x[0], x[0]);
+#pragma unroll
+        for (int q = 1; q < 4; ++q) ss = __ffma2_rn(x[q], x[q], ss);
+        float sum = ss.x + ss.y;
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float rstd = rsqrtf(sum * (1.f / D) + p.eps);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) y[q] = __fmul2_rn(y[q], make_float2(rstd, rstd));
+      }
+      if (h0 + i * kGroups < H)
+        store(i, make_uint4(pack2(y[0]), pack2(y[1]), pack2(y[2]), pack2(y[3])));
     }
   }
 }
 
 template <int D>
 cudaError_t launch_d(const RopeParams& p, bool interleaved, cudaStream_t s) {
-  const int heads = p.Hq + p.Hk + p.Hv;
-  if (p.T <= 0 || heads <= 0) return cudaSuccess;
+  constexpr int kRows = 32 / (D / 8) * kAhead;
+  if (p.T <= 0) return cudaSuccess;
+  const int per = (p.Hq + kRows - 1) / kRows + (p.Hk + kRows - 1) / kRows + (p.Hv + kRows - 1) / kRows;
   const int sms = device_sm_count() > 0 ? device_sm_count() : 1;
-  constexpr int kGroups = kThreads / (D / 8);
-  // A CTA takes about kAhead rows a lane group, all of them in flight at once:
-  // several tokens of few heads, or a share of one token's heads; fewer rows
-  // where that leaves SMs without work.
+  // A CTA takes up to four tasks a warp: several tokens, or a share of one
+  // token's tasks; fewer where that leaves SMs without work.
   RopeShape sh;
-  int target = kAhead * kGroups;
-  while (target > kGroups &&
-         static_cast<int64_t>(p.T) * heads < static_cast<int64_t>(2) * sms * target)
+  int target = 4 * kWarps;
+  while (target > kWarps / 2 &&
+         static_cast<int64_t>(p.T) * per < static_cast<int64_t>(8) * sms * target)
     target /= 2;
-  const int chunks = (heads + target - 1) / target;
-  sh.rows = (heads + chunks - 1) / chunks;
-  sh.tokens = target / sh.rows;
+  const int chunks = (per + target - 1) / target;
+  sh.tasks = (per + chunks - 1) / chunks;
+  sh.tokens = target / sh.tasks;
   if (sh.tokens < 1) sh.tokens = 1;
   if (sh.tokens > kMaxTokens) sh.tokens = kMaxTokens;
-  const dim3 grid((p.T + sh.tokens - 1) / sh.tokens, (heads + sh.rows - 1) / sh.rows);
+  const dim3 grid((p.T + sh.tokens - 1) / sh.tokens, (per + sh.tasks - 1) / sh.tasks);
   if (interleaved)
     rope_kernel<D, true><<<grid, kThreads, 0, s>>>(p, sh);
   else
