@@ -797,20 +797,40 @@ def rope_turns(freq, device="cuda"):
 
 def _rotation(dev, T, D, positions, turns, q_weight, k_weight):
     """Checks of the rotation's tensors; how many elements are rotated."""
-    _need_all(dev, ((positions, "positions", torch.int32), (turns, "turns", torch.int64),
-                    (q_weight, "q_weight", torch.float32), (k_weight, "k_weight", torch.float32)))
-    if (positions is None) != (turns is None):
+    if q_weight is not None or k_weight is not None:
+        _need_all(dev, ((q_weight, "q_weight", torch.float32),
+                        (k_weight, "k_weight", torch.float32)))
+        _shape(q_weight, "q_weight", (D,))
+        _shape(k_weight, "k_weight", (D,))
+    if turns is None and positions is None:
+        return 0
+    if positions is None or turns is None:
         raise ValueError("positions and turns go together")
+    _need_all(dev, ((positions, "positions", torch.int32), (turns, "turns", torch.int64)))
     _shape(positions, "positions", (T,))
-    _shape(q_weight, "q_weight", (D,))
-    _shape(k_weight, "k_weight", (D,))
-    return 0 if turns is None else 2 * turns.numel()
+    return 2 * turns.numel()
 
 
 def _rows_of(t, name, dev):
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [T, H, D], got {tuple(t.shape)}")
-    return _token_rows(t, name, dev, t.shape)
+    """Shape and token stride of a [T, H, D] bf16 tensor whose heads and
+    elements are dense."""
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [T, H, D], got {tuple(shape)}")
+    s0, s1, s2 = t.stride()
+    if t.dtype is torch.bfloat16 and t.device == dev and s2 == 1 and s1 == shape[2] and \
+            shape[0] > 1 and dev.type == "cuda":
+        return shape, s0
+    return shape, _token_rows(t, name, dev, shape)
+
+
+def _bf16_out(t, name, shape, dev):
+    """The caller's output, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    _need_all(dev, ((t, name, torch.bfloat16),))
+    _shape(t, name, shape)
+    return t
 
 
 def qk_norm_rope(q, k, positions, turns, *, q_weight=None, k_weight=None, eps=1e-6,
@@ -820,22 +840,19 @@ def qk_norm_rope(q, k, positions, turns, *, q_weight=None, k_weight=None, eps=1e
     rotated by positions [T] int32, in one pass: (q_out, k_out), dense.
     `turns` is rope_turns(...); None (and positions None): only the norm."""
     dev = q.device
-    T, Hq, D = q.shape if q.dim() == 3 else (0, 0, 0)
-    qs = _rows_of(q, "q", dev)
+    shape, qs = _rows_of(q, "q", dev)
+    T, Hq, D = shape
     ks = hk = 0
     if k is not None:
-        ks, hk = _rows_of(k, "k", dev), k.shape[1]
-        _shape(k, "k", (T, hk, D))
-        if k_out is None:
-            k_out = torch.empty((T, hk, D), dtype=torch.bfloat16, device=dev)
+        k_shape, ks = _rows_of(k, "k", dev)
+        hk = k_shape[1]
+        if k_shape[0] != T or k_shape[2] != D:
+            raise ValueError(f"k must be [{T}, Hk, {D}], got {tuple(k_shape)}")
+        k_out = _bf16_out(k_out, "k_out", k_shape, dev)
     elif k_out is not None or k_weight is not None:
         raise ValueError("k_out and k_weight need k")
-    if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    q_out = _bf16_out(q_out, "q_out", shape, dev)
     rotary = _rotation(dev, T, D, positions, turns, q_weight, k_weight)
-    _need_all(dev, ((q_out, "q_out", torch.bfloat16), (k_out, "k_out", torch.bfloat16)))
-    _shape(q_out, "q_out", (T, Hq, D))
-    _shape(k_out, "k_out", (T, hk, D))
     if T == 0:
         return q_out, k_out
     with _on(dev):
@@ -874,16 +891,17 @@ def kv_append(k, v, slot_mapping, k_cache, v_cache, *, positions=None, turns=Non
     nb, hkv, bs, D = _kv_shape(k_cache, v_cache, dev)
     _need_all(dev, ((slot_mapping, "slot_mapping", torch.int64),))
     T = slot_mapping.numel()
-    ks = _token_rows(k, "k", dev, (T, hkv, D))
-    vs = _token_rows(v, "v", dev, (T, hkv, D))
+    k_shape, ks = _rows_of(k, "k", dev)
+    v_shape, vs = _rows_of(v, "v", dev)
+    if k_shape != (T, hkv, D) or v_shape != (T, hkv, D):
+        raise ValueError(f"k and v must be {(T, hkv, D)}, got {tuple(k_shape)}, {tuple(v_shape)}")
     qs = hq = 0
     if q is not None:
-        qs, hq = _rows_of(q, "q", dev), q.shape[1]
-        _shape(q, "q", (T, hq, D))
-        if q_out is None:
-            q_out = torch.empty((T, hq, D), dtype=torch.bfloat16, device=dev)
-        _need_all(dev, ((q_out, "q_out", torch.bfloat16),))
-        _shape(q_out, "q_out", (T, hq, D))
+        q_shape, qs = _rows_of(q, "q", dev)
+        hq = q_shape[1]
+        if q_shape[0] != T or q_shape[2] != D:
+            raise ValueError(f"q must be [{T}, Hq, {D}], got {tuple(q_shape)}")
+        q_out = _bf16_out(q_out, "q_out", q_shape, dev)
     elif q_out is not None or q_weight is not None:
         raise ValueError("q_out and q_weight need q")
     rotary = _rotation(dev, T, D, positions, turns, q_weight, k_weight)
@@ -923,25 +941,23 @@ def kv_attention(q, k_cache, v_cache, block_table, context_lens, query_starts, *
     (out [T, Hq, D], lse [T, Hq] fp32).  softmax_scale defaults to D^-0.5."""
     dev = q.device
     nb, hkv, bs, D = _kv_shape(k_cache, v_cache, dev)
-    qs = _rows_of(q, "q", dev)
-    T, Hq, Dq = q.shape
+    shape, qs = _rows_of(q, "q", dev)
+    T, Hq, Dq = shape
     if Dq != D:
-        raise ValueError(f"q must be [T, Hq, {D}], got {tuple(q.shape)}")
+        raise ValueError(f"q must be [T, Hq, {D}], got {tuple(shape)}")
     if block_table.dim() != 2:
         raise ValueError(f"block_table must be [B, max_blocks], got {tuple(block_table.shape)}")
     B, max_blocks = block_table.shape
-    if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-    if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
     _need_all(dev, ((block_table, "block_table", torch.int32),
                     (context_lens, "context_lens", torch.int32),
-                    (query_starts, "query_starts", torch.int32), (out, "out", torch.bfloat16),
-                    (lse, "lse", torch.float32)))
+                    (query_starts, "query_starts", torch.int32), (lse, "lse", torch.float32)))
     _shape(context_lens, "context_lens", (B,))
     _shape(query_starts, "query_starts", (B + 1,))
-    _shape(out, "out", (T, Hq, D))
-    _shape(lse, "lse", (T, Hq))
+    out = _bf16_out(out, "out", shape, dev)
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    else:
+        _shape(lse, "lse", (T, Hq))
     if T == 0 or B == 0:
         return out, lse
     scale = D ** -0.5 if softmax_scale is None else softmax_scale
@@ -950,8 +966,8 @@ def kv_attention(q, k_cache, v_cache, block_table, context_lens, query_starts, *
         ws = _workspace(nbytes, dev, workspace)
         st = lib.dsa_kv_attention(_addr(q), qs, _addr(k_cache), _addr(v_cache), nb,
                                   _addr(block_table), max_blocks, _addr(context_lens),
-                                  _addr(query_starts), T, B, bs, Hq, hkv, D, scale, int(window),
-                                  int(sink), _addr(out), _addr(lse), _addr(ws), nbytes,
+                                  _addr(query_starts), T, B, bs, Hq, hkv, D, scale, window, sink,
+                                  _addr(out), _addr(lse), _addr(ws), nbytes,
                                   _raw_stream(dev))
     _check(st, "dsa_kv_attention")
     return out, lse

@@ -226,7 +226,7 @@ struct KvAttnParams {
   uint16_t* out;              // [T, Hq, D]
   float* lse;                 // [T, Hq] or null
   int ctas, slot_rows;
-  int4* notes;                // [ctas, 2]: what each CTA left unfinished
+  int4* notes;                // [ctas]: the tile each CTA started and did not end
   float2* part_ml;            // [ctas, 2, slot_rows]: base-2 reference and sum of weights
   float* part_o;              // [ctas, 2, slot_rows, D]
   uint32_t* err;

@@ -194,7 +194,7 @@ __device__ __forceinline__ bool all_seen(const KvAttnParams& p, const Tile& t, i
 struct Walk {
   Req r;
   int h, qt, j;
-  int64_t left;
+  int64_t left, total;  // units to go, and of the whole call
   __device__ void next(const KvAttnParams& p, int taken) {
     left -= taken;
     j = 0;
@@ -261,6 +261,7 @@ __device__ Walk find_run(const KvAttnParams& p, int* pfx) {
   const int64_t total = static_cast<int64_t>(U) * p.Hkv;
   const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
   Walk w = {};
+  w.total = total;
   if (static_cast<int64_t>(blockIdx.x) < ctas) {
     const int64_t u0 = blockIdx.x * total / ctas;
     w.left = (blockIdx.x + 1) * total / ctas - u0;
@@ -478,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Walk w = find_run(p, reinterpret_cast<int*>(ring));
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  if (tid == 0) p.notes[2 * blockIdx.x] = p.notes[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+  if (tid == 0) p.notes[blockIdx.x] = make_int4(0, 0, 0, 0);
 
   bool ok = true;
   if (warp >= 8) {
@@ -774,6 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = w.j == 0 && take == t.units;
       const int64_t at =
           static_cast<int64_t>(t.tok0 + tok) * p.Hq + w.h * p.G + (row - row / p.G * p.G);
+      // Slot 1 starts a tile, slot 0 goes on with one that an earlier CTA started.
       const int64_t part = static_cast<int64_t>(2 * blockIdx.x + (w.j == 0 ? 1 : 0)) * p.slot_rows +
                            (t.tall ? g * kTile : 0) + row;
       const bool bad = *nonfinite != 0;
@@ -853,13 +855,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after_sync();
       }
-      if (!whole && tid == 0) {
-        // Slot 1 starts a tile, slot 0 goes on with one that an earlier CTA
-        // started (and, with 2, ends it).
-        if (w.j == 0)
-          p.notes[2 * blockIdx.x + 1] = make_int4(1, w.r.b, w.qt, w.h);
-        else
-          p.notes[2 * blockIdx.x] = make_int4(w.j + take == t.units ? 2 : 1, 0, 0, 0);
+      if (!whole && w.j == 0 && tid == 0) {
+        // The join's note: the tile, and how many CTAs go on with it (CTA c has
+        // the units from floor(c total / ctas) on).
+        const int64_t ctas = min(static_cast<int64_t>(gridDim.x), w.total);
+        const int64_t end = (blockIdx.x + 1) * w.total / ctas - w.left + t.units;
+        p.notes[blockIdx.x] = make_int4(t.tok0, t.ntok, w.h,
+                                        static_cast<int>((end * ctas - 1) / w.total) -
+                                            static_cast<int>(blockIdx.x));
       }
       w.next(p, take);
     }
@@ -880,32 +883,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 constexpr int kJoinWarps = 8;
 
-// The parts of each cut tile, a warp a row: CTA blockIdx.x started the tile,
-// the next ones went on with it.
+// The parts of each cut tile, a warp a row.  CTA blockIdx.x started the tile
+// (its slot 1), the next ones went on with it (their slots 0).
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(
     const __grid_constant__ KvAttnParams p) {
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int cta = blockIdx.x;
-  const int4 note = p.notes[2 * cta + 1];
-  if (note.x == 0) return;
-  const Req r = req_of(p, note.y);
-  const Tile t = tile_of(p, r, note.z);
-  const int rows = t.ntok * p.G;
-  if (blockIdx.y * kJoinWarps + warp >= rows) return;
-  // How many CTAs went on with the tile.
-  int more = 0;
-  for (int at = cta + 1; at < p.ctas; at += 32) {
-    const bool ends = at + lane < p.ctas && p.notes[2 * (at + lane)].x == 2;
-    const uint32_t vote = __ballot_sync(0xffffffffu, ends);
-    if (vote) {
-      more += __ffs(vote);
-      break;
-    }
-    more += 32;
-  }
-  more = min(more, p.ctas - 1 - cta);
+  const int4 note = p.notes[cta];  // first token, tokens, head, CTAs that went on
+  const int rows = note.y * p.G, more = note.w;
   constexpr int N = D / 32;
   for (int i = blockIdx.y * kJoinWarps + warp; i < rows; i += gridDim.y * kJoinWarps) {
     const int tok = i / p.G, g = i - tok * p.G;
@@ -936,7 +923,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(
       for (int q = 0; q < N; ++q) acc[q] = f == 0.f ? acc[q] : fmaf(v[q], f, acc[q]);
     }
     const float f = sum == 0.f ? 0.f : 1.f / sum;
-    const int64_t at = static_cast<int64_t>(t.tok0 + tok) * p.Hq + note.w * p.G + g;
+    const int64_t at = static_cast<int64_t>(note.x + tok) * p.Hq + note.z * p.G + g;
     uint32_t v[N / 2];
 #pragma unroll
     for (int q = 0; q < N / 2; ++q) {
@@ -994,7 +981,7 @@ KvAttnPlan kv_attn_plan(int T, int G, int D) {
   pl.ctas = device_sm_count() > 0 ? device_sm_count() : 1;
   pl.slot_rows = T > pl.tpt ? 2 * kTile : kTile;
   const int64_t rows = static_cast<int64_t>(pl.ctas) * 2 * pl.slot_rows;
-  pl.part_ml = up256(static_cast<int64_t>(pl.ctas) * 2 * 16);
+  pl.part_ml = up256(static_cast<int64_t>(pl.ctas) * 16);
   pl.part_o = pl.part_ml + up256(rows * 8);
   pl.bytes = pl.part_o + up256(rows * D * 4);
   return pl;
