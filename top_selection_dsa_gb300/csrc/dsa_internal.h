@@ -222,7 +222,6 @@ struct KvAttnParams {
   int max_blocks, num_blocks, log_bs;
   int window, sink;           // window 0: none
   float scale_log2e;          // softmax scale times log2(e)
-  float lazy;                 // growth of a logit maximum that moves a row's reference
   uint16_t* out;              // [T, Hq, D]
   float* lse;                 // [T, Hq] or null
   int ctas, slot_rows;

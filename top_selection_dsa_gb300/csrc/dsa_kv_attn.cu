@@ -49,30 +49,15 @@ namespace {
 
 constexpr int kTile = 128;    // keys of a tile, rows of a row tile
 constexpr int kThreads = 384;
+constexpr int kProducer = 8;  // warps: 0-7 softmax, then the producer, the issuer, the check
+constexpr int kIssuer = 9;
 constexpr int kMaxStages = 12;
-// Registers a thread: 168 at launch, shifted to the softmax (8 warps at 200 and
-// 4 at 96 are 63488 of the block's 64512).
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 96;
+// A row's weights of one tile add to no more than this, or its reference moves.
+constexpr float kMostSum = 65536.f;
+// Registers a thread: 168 at launch, shifted to the softmax (8 warps at 208 and
+// 4 at 88 are the block's 64512).
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
-
-template <int D>
-struct AttnCfg {
-  static constexpr int HALVES = D / 64;               // 128-byte columns of a row
-  static constexpr int HALF_BYTES = kTile * 128;      // one column of a tile
-  static constexpr int TILE_BYTES = HALVES * HALF_BYTES;
-  static constexpr int NST = D == 128 ? 5 : 12;       // what shared memory has room for
-  static constexpr int RING = 2 * TILE_BYTES;
-  static constexpr int MISC = RING + NST * TILE_BYTES;
-  static constexpr int XML = 0;                       // float2[2][128]
-  static constexpr int BARS = 2048;
-  static constexpr int SLOT = BARS + 8 * (3 * kMaxStages + 12);
-  static constexpr int SMEM = MISC + (SLOT + 16 + 127) / 128 * 128;
-  static constexpr uint32_t S_COL = 0, O_COL = 256;   // TMEM: S/P of A, of B; O of A, of B
-  static constexpr uint32_t IDESC_S = mma_idesc(1u, 128, 128);
-  static constexpr uint32_t IDESC_O = mma_idesc(1u, 128, D) | (1u << 16);  // V: N-major
-  static_assert(SMEM <= 232448, "shared memory");
-  static_assert((kMaxPagedRequests + 1) * 4 <= NST * TILE_BYTES, "prefix sums in the ring");
-};
 
 __device__ __forceinline__ void launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -131,6 +116,15 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// One lane of a converged warp (the same one each time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 // ------------------------------------------------------------------- the work
 
 // One request: its first token, tokens and context, all inside the buffers.
@@ -160,11 +154,6 @@ __device__ __forceinline__ int tiles_of(const KvAttnParams& p, const Req& r) {
 struct Tile {
   int tok0, ntok, p0, nsink, first, keys, units;
   bool tall;
-  __device__ int key_tile(int j) const { return j < nsink ? j : first + (j - nsink); }
-  // The i-th key tile of group g from unit j on.
-  __device__ int key_of(int j, int i, int g) const {
-    return key_tile(tall ? j + i : 2 * (j + i) + g);
-  }
   __device__ int last() const { return p0 + ntok - 1; }
 };
 
@@ -183,14 +172,31 @@ __device__ __forceinline__ Tile tile_of(const KvAttnParams& p, const Req& r, int
   return t;
 }
 
+// What a CTA does next of a tile: `take` of its units from j on.  The producer
+// writes it to shared memory, every other role reads it there.
+struct Piece {
+  int tok0, ntok, p0, last, nsink, first, keys, tall;  // of the tile; last: its last position
+  int j, take;   // take 0: no more pieces
+  int a, b;      // key tiles that A and B take
+  int h, req, L;
+  int whole;     // the piece is the whole tile
+  int more;      // CTAs that go on with the tile (where the piece starts it)
+  // The i-th key tile of group g.
+  __device__ int key_of(int i, int g) const {
+    const int k = tall ? j + i : 2 * (j + i) + g;
+    return k < nsink ? k : first + (k - nsink);
+  }
+};
+constexpr int kPieces = 4;  // published ahead
+
 // Whether every row of the tile sees all keys of key tile kt.
-__device__ __forceinline__ bool all_seen(const KvAttnParams& p, const Tile& t, int kt) {
+__device__ __forceinline__ bool all_seen(const KvAttnParams& p, const Piece& t, int kt) {
   const int c0 = kt * kTile;
   return c0 + kTile - 1 <= t.p0 &&
-         (p.window == 0 || c0 > t.last() - p.window || c0 + kTile <= p.sink);
+         (p.window == 0 || c0 > t.last - p.window || c0 + kTile <= p.sink);
 }
 
-// A run of units and where it stands; every role walks it by itself.
+// A run of units and where it stands.
 struct Walk {
   Req r;
   int h, qt, j;
@@ -215,27 +221,32 @@ struct Walk {
 // Units of one request's row tiles for one head, summed by one thread.
 __device__ __forceinline__ int units_by_thread(const KvAttnParams& p, const Req& r, int nt) {
   int u = 0;
+#pragma unroll 1
   for (int qt = 0; qt < nt; ++qt) u += tile_of(p, r, qt).units;
   return u;
 }
 
-// This CTA's run.  Called by all threads; `pfx` is B + 1 ints of scratch.
+// This CTA's run, for the producer's warp.  Called by all threads; `pfx` is
+// B + 1 ints of scratch.
 __device__ Walk find_run(const KvAttnParams& p, int* pfx) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // Requests of few row tiles are summed by a thread each, others by a warp.
   constexpr int kFew = 4;
   uint32_t* err = blockIdx.x == 0 ? p.err : nullptr;
+#pragma unroll 1
   for (int b = tid; b < p.B; b += kThreads) {
     const Req r = req_of(p, b, err);
     const int nt = tiles_of(p, r);
     pfx[b + 1] = nt <= kFew ? units_by_thread(p, r, nt) : -1;
   }
   __syncthreads();
+#pragma unroll 1
   for (int b = warp; b < p.B; b += kThreads / 32) {
     if (pfx[b + 1] >= 0) continue;
     const Req r = req_of(p, b);
     const int nt = tiles_of(p, r);
     int u = 0;
+#pragma unroll 1
     for (int qt = lane; qt < nt; qt += 32) u += tile_of(p, r, qt).units;
     u = __reduce_add_sync(0xffffffffu, u);
     __syncwarp();
@@ -245,6 +256,7 @@ __device__ Walk find_run(const KvAttnParams& p, int* pfx) {
   if (warp == 0) {
     int carry = 0;
     if (lane == 0) pfx[0] = 0;
+#pragma unroll 1
     for (int at = 0; at < p.B; at += 32) {
       int v = at + lane < p.B ? pfx[at + lane + 1] : 0;
 #pragma unroll
@@ -262,12 +274,13 @@ __device__ Walk find_run(const KvAttnParams& p, int* pfx) {
   const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
   Walk w = {};
   w.total = total;
-  if (static_cast<int64_t>(blockIdx.x) < ctas) {
+  if (warp == kProducer && static_cast<int64_t>(blockIdx.x) < ctas) {
     const int64_t u0 = blockIdx.x * total / ctas;
     w.left = (blockIdx.x + 1) * total / ctas - u0;
     w.h = static_cast<int>(u0 / U);
     int at = static_cast<int>(u0 - static_cast<int64_t>(w.h) * U);
     int lo = 0, hi = p.B;  // the request: pfx[lo] <= at < pfx[lo + 1]
+#pragma unroll 1
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (pfx[mid] <= at) lo = mid; else hi = mid;
@@ -275,6 +288,7 @@ __device__ Walk find_run(const KvAttnParams& p, int* pfx) {
     at -= pfx[lo];
     w.r = req_of(p, lo);
     const int nt = tiles_of(p, w.r);
+#pragma unroll 1
     for (int base = 0; base < nt; base += 32) {
       const int u = base + lane < nt ? tile_of(p, w.r, base + lane).units : 0;
       int incl = u;
@@ -297,14 +311,6 @@ __device__ Walk find_run(const KvAttnParams& p, int* pfx) {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();
   return w;
-}
-
-// Key tiles that A and B take of `take` units from j on.
-struct Shares {
-  int a, b;
-};
-__device__ __forceinline__ Shares shares(const Tile& t, int j, int take) {
-  return {take, t.tall || 2 * (j + take) <= t.keys ? take : take - 1};
 }
 
 // Where a role stands in the ring of stages.
@@ -360,11 +366,12 @@ __device__ __forceinline__ Sight sight_of(const KvAttnParams& p, int pos, int c0
   return {pos - c0, p.window > 0 ? pos - p.window + 1 - c0 : 0, p.sink - c0};
 }
 
-__device__ __forceinline__ int page_of(const KvAttnParams& p, const Req& r, int c) {
-  const int used = (r.L + (1 << p.log_bs) - 1) >> p.log_bs;
+// The page of key c of a request whose context is L.
+__device__ __forceinline__ int page_of(const KvAttnParams& p, int req, int L, int c) {
+  const int used = (L + (1 << p.log_bs) - 1) >> p.log_bs;
   const int lb = min(c >> p.log_bs, used - 1);
   if (lb < 0) return 0;
-  const int page = __ldg(p.block_table + static_cast<int64_t>(r.b) * p.max_blocks + lb);
+  const int page = __ldg(p.block_table + static_cast<int64_t>(req) * p.max_blocks + lb);
   if (page < 0 || page >= p.num_blocks) {
     record_error(p.err, kErrBadIndex);
     return 0;
@@ -373,27 +380,32 @@ __device__ __forceinline__ int page_of(const KvAttnParams& p, const Req& r, int 
 }
 
 // Infinities and NaN among the values that a row sees in tiles that are not
-// wholly seen, which the products left out, added to elements d0 .. of its
-// output.
-template <int D, int N>
-__device__ __forceinline__ void add_nonfinite(const KvAttnParams& p, const Walk& w, const Tile& t,
-                                              int take, int pos, int d0, float (&o)[N]) {
-  const int j0 = t.tall ? w.j : 2 * w.j;
-  const int j1 = min(t.tall ? w.j + take : 2 * (w.j + take), t.keys);
-  for (int j = j0; j < j1; ++j) {
-    const int kt = t.key_tile(j);
+// wholly seen, which the products left out, added to `n` elements from d0 on of
+// its output as this thread stored it: bf16 at `out`, or fp32 at `part`.
+template <int D>
+__device__ __noinline__ void add_nonfinite(const KvAttnParams& p, const Piece& t, int pos, int d0,
+                                           int n, uint16_t* out, float* part) {
+#pragma unroll 1
+  for (int i = 0; i < t.a + (t.tall ? 0 : t.b); ++i) {
+    const int kt = t.tall ? t.key_of(i, 0) : t.key_of(i / 2, i % 2);
     if (all_seen(p, t, kt)) continue;
     const Sight s = sight_of(p, pos, kt * kTile);
+#pragma unroll 1
     for (int c = 0; c < kTile; ++c) {
       if (!s.sees(c)) continue;
       const int key = kt * kTile + c;
-      const int64_t row = ((static_cast<int64_t>(page_of(p, w.r, key)) * p.Hkv + w.h)
-                           << p.log_bs) + (key & ((1 << p.log_bs) - 1));
-      const uint16_t* v = p.v + row * D + d0;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const uint32_t x = v[i];
-        if ((x & 0x7F80u) == 0x7F80u) o[i] += __uint_as_float(x << 16);
+      const int64_t row = ((static_cast<int64_t>(page_of(p, t.req, t.L, key)) * p.Hkv + t.h) << p.log_bs) +
+                          (key & ((1 << p.log_bs) - 1));
+#pragma unroll 1
+      for (int d = d0; d < d0 + n; ++d) {
+        const uint32_t x = p.v[row * D + d];
+        if ((x & 0x7F80u) != 0x7F80u) continue;
+        const float v = __uint_as_float(x << 16);
+        if (part)
+          part[d] += v;
+        else
+          out[d] = __bfloat16_as_ushort(
+              __float2bfloat16_rn(__uint_as_float(static_cast<uint32_t>(out[d]) << 16) + v));
       }
     }
   }
@@ -414,10 +426,11 @@ __device__ __forceinline__ void store_out(uint16_t* out, const float (&o)[N], fl
   }
 }
 template <int N>
-__device__ __forceinline__ void store_part(float* out, const float (&o)[N]) {
+__device__ __forceinline__ void store_part(float* out, const float (&o)[N], float f) {
 #pragma unroll
   for (int i = 0; i < N; i += 4)
-    *reinterpret_cast<float4*>(out + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+    *reinterpret_cast<float4*>(out + i) =
+        make_float4(o[i] * f, o[i + 1] * f, o[i + 2] * f, o[i + 3] * f);
 }
 
 __device__ __forceinline__ float lse_of(float m2, float l) {
@@ -425,6 +438,26 @@ __device__ __forceinline__ float lse_of(float m2, float l) {
 }
 
 // ----------------------------------------------------------------- the kernel
+
+template <int D>
+struct AttnCfg {
+  static constexpr int HALVES = D / 64;               // 128-byte columns of a row
+  static constexpr int HALF_BYTES = kTile * 128;      // one column of a tile
+  static constexpr int TILE_BYTES = HALVES * HALF_BYTES;
+  static constexpr int NST = D == 128 ? 5 : 12;       // what shared memory has room for
+  static constexpr int RING = 2 * TILE_BYTES;
+  static constexpr int MISC = RING + NST * TILE_BYTES;
+  static constexpr int XML = 0;                       // float2[2][128]
+  static constexpr int BARS = 2048;
+  static constexpr int SLOT = BARS + 8 * (3 * kMaxStages + 12 + 2 * kPieces);
+  static constexpr int PIECES = SLOT + 16;
+  static constexpr int SMEM = MISC + (PIECES + kPieces * static_cast<int>(sizeof(Piece)) + 127) / 128 * 128;
+  static constexpr uint32_t S_COL = 0, O_COL = 256;   // TMEM: S/P of A, of B; O of A, of B
+  static constexpr uint32_t IDESC_S = mma_idesc(1u, 128, 128);
+  static constexpr uint32_t IDESC_O = mma_idesc(1u, 128, D) | (1u << 16);  // V: N-major
+  static_assert(SMEM <= 232448, "shared memory");
+  static_assert((kMaxPagedRequests + 1) * 4 <= NST * TILE_BYTES, "prefix sums in the ring");
+};
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -444,9 +477,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* ofull = pfull + 2;   // [2] a piece's last product is done
   uint64_t* xbar = ofull + 2;    // [2] short pieces: sums exchanged; both outputs read
   uint64_t* drained = xbar + 2;
+  uint64_t* told = drained + 1;       // [kPieces] a piece is published
+  uint64_t* done = told + kPieces;    // [kPieces] and read by all
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + C::SLOT);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   volatile uint32_t* nonfinite = tmem_slot + 2;
+  Piece* pieces = reinterpret_cast<Piece*>(misc + C::PIECES);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   launch_dependents();
@@ -465,12 +501,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ofull[i], 1);
       mbar_init(&xbar[i], 256);
     }
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(&told[i], 1);
+      mbar_init(&done[i], 11);  // every warp but the producer's
+    }
     tmem_slot[1] = 0;
     tmem_slot[2] = 0;
     fence_barrier_init();
+    p.notes[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
-  if (warp == 9) tmem_alloc(tmem_slot, 512);
-  if (warp == 8 && lane == 0) {
+  if (warp == kIssuer) tmem_alloc(tmem_slot, 512);
+  if (warp == kProducer && lane == 0) {
     tma_prefetch_desc(&p.tmap_q);
     tma_prefetch_desc(&p.tmap_k);
     tma_prefetch_desc(&p.tmap_v);
@@ -479,22 +520,37 @@ __global__ void __launch_bounds__(kThreads, 1)
   Walk w = find_run(p, reinterpret_cast<int*>(ring));
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  if (tid == 0) p.notes[blockIdx.x] = make_int4(0, 0, 0, 0);
 
   bool ok = true;
+  // Waits of a whole warp; after one that gave up the others pass at once.
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag) ? 1 : 0);
+  };
+  // The next piece, and its return once nothing of it is read any more.
+  Ring<kPieces> next;
+  auto piece = [&]() -> const Piece& {
+    wait(&told[next.st], next.ph);
+    return pieces[next.st];
+  };
+  auto piece_done = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&done[next.st]);
+    next.step();
+  };
+
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 8) {
+    if (warp == kProducer) {
       // ------------------------------------------------------------- producer
       Ring<C::NST> at;
-      int pieces = 0, loads = 0;
+      int queries = 0, loads = 0;
       const int per_tile = kTile >> p.log_bs;
+      const CUtensorMap* const maps[2] = {&p.tmap_k, &p.tmap_v};
       auto page = [&](int kt) {
-        return lane < per_tile ? page_of(p, w.r, kt * kTile + (lane << p.log_bs)) : 0;
+        return lane < per_tile ? page_of(p, w.r.b, w.r.L, kt * kTile + (lane << p.log_bs)) : 0;
       };
-      auto load = [&](const CUtensorMap* map, int pg) {
-        if (ok && lane == 0) ok = mbar_wait_bounded(&empty[at.st], at.ph ^ 1u, abort_flag);
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      auto load = [&](int which, int pg) {
+        wait(&empty[at.st], at.ph ^ 1u);
         if (!ok) return;
         if (lane == 0) mbar_arrive_expect_tx(&full[at.st], C::TILE_BYTES);
         __syncwarp();
@@ -503,136 +559,177 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row = (pg * p.Hkv + w.h) << p.log_bs;
 #pragma unroll
           for (int a = 0; a < C::HALVES; ++a)
-            tma_load_2d(dst + a * C::HALF_BYTES, map, &full[at.st], a * 64, row);
+            tma_load_2d(dst + a * C::HALF_BYTES, maps[which], &full[at.st], a * 64, row);
         }
         at.step();
         ++loads;
       };
-      while (ok && w.left > 0) {
-        const Tile t = tile_of(p, w.r, w.qt);
-        const int take = static_cast<int>(min(static_cast<int64_t>(t.units - w.j), w.left));
-        const Shares n = shares(t, w.j, take);
+#pragma unroll 1
+      while (true) {
+        wait(&done[next.st], next.ph ^ 1u);
+        if (!ok) break;
+        Piece t = {};
+        if (w.left > 0) {
+          const Tile tile = tile_of(p, w.r, w.qt);
+          const int64_t ctas = min(static_cast<int64_t>(gridDim.x), w.total);
+          // CTA c has the units from floor(c total / ctas) on: who has the last one.
+          const int64_t end = (blockIdx.x + 1) * w.total / ctas - w.left - w.j + tile.units;
+          t.tok0 = tile.tok0;
+          t.ntok = tile.ntok;
+          t.p0 = tile.p0;
+          t.last = tile.last();
+          t.nsink = tile.nsink;
+          t.first = tile.first;
+          t.keys = tile.keys;
+          t.tall = tile.tall;
+          t.j = w.j;
+          t.take = static_cast<int>(min(static_cast<int64_t>(tile.units - w.j), w.left));
+          t.a = t.take;
+          t.b = t.tall || 2 * (t.j + t.take) <= t.keys ? t.take : t.take - 1;
+          t.h = w.h;
+          t.req = w.r.b;
+          t.L = w.r.L;
+          t.whole = t.j == 0 && t.take == tile.units;
+          t.more = static_cast<int>((end * ctas - 1) / w.total) - static_cast<int>(blockIdx.x);
+        }
+        if (lane == 0) {
+          pieces[next.st] = t;
+          mbar_arrive(&told[next.st]);
+        }
+        __syncwarp();
+        next.step();
+        if (t.take == 0) break;
+        const bool two = !t.tall;  // A and B have key tiles of their own
         // Pages of the tiles whose values are loaded next, and of those after.
-        int pa = page(t.key_of(w.j, 0, 0)), pb = !t.tall && n.b > 0 ? page(t.key_of(w.j, 0, 1)) : 0;
-        int na = 0, nb = 0;
-        if (lane == 0)
-          ok = mbar_wait_bounded(qempty, (static_cast<uint32_t>(pieces) & 1u) ^ 1u, abort_flag);
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        int pa = page(t.key_of(0, 0)), pb = two && t.b > 0 ? page(t.key_of(0, 1)) : 0;
+        wait(qempty, (static_cast<uint32_t>(queries) & 1u) ^ 1u);
         if (!ok) break;
         if (lane == 0) {
-          const int nq = t.tall ? 2 : 1;
+          const int nq = two ? 1 : 2;
           mbar_arrive_expect_tx(qfull, nq * C::HALVES * p.tpt * p.G * 128);
           for (int q = 0; q < nq; ++q)
 #pragma unroll
             for (int a = 0; a < C::HALVES; ++a)
               tma_load_box3(smem + q * C::TILE_BYTES + a * C::HALF_BYTES, &p.tmap_q, qfull, a * 64,
-                            w.h * p.G, t.tok0 + q * p.tpt);
+                            t.h * p.G, t.tok0 + q * p.tpt);
         }
         __syncwarp();
-        ++pieces;
-        load(&p.tmap_k, pa);
-        if (!t.tall && n.b > 0) load(&p.tmap_k, pb);
+        ++queries;
+        // Keys of the first tiles, then the values of a tile and the keys of
+        // its group's next one, in the order of the products.
+        load(0, pa);
+        if (two && t.b > 0) load(0, pb);
 #pragma unroll 1
-        for (int i = 0; ok && i < n.a; ++i) {
-          if (i + 1 < n.a) na = page(t.key_of(w.j, i + 1, 0));
-          if (!t.tall && i + 1 < n.b) nb = page(t.key_of(w.j, i + 1, 1));
-          load(&p.tmap_v, pa);
-          pa = na;
-          if (i + 1 < n.a) load(&p.tmap_k, pa);
-          if (t.tall || i >= n.b) continue;
-          load(&p.tmap_v, pb);
-          pb = nb;
-          if (i + 1 < n.b) load(&p.tmap_k, pb);
+        for (int s = 0; ok && s < (two ? 2 * t.a : t.a); ++s) {
+          const int i = two ? s >> 1 : s, g = two ? s & 1 : 0;
+          if (g == 1 && i >= t.b) break;
+          const bool more = i + 1 < (g ? t.b : t.a);
+          const int now = g ? pb : pa;
+          const int pg = more ? page(t.key_of(i + 1, g)) : 0;
+          if (g) pb = pg; else pa = pg;
+          load(1, now);
+          if (more) load(0, pg);
         }
-        w.next(p, take);
+        w.next(p, t.take);
       }
       if (!ok && lane == 0) {
         // Let the copies already in flight land before the CTA retires.
         for (int i = loads > C::NST ? loads - C::NST : 0; i < loads; ++i)
           mbar_wait_bounded(&full[i % C::NST], static_cast<uint32_t>(i / C::NST) & 1u, nullptr,
                             100000000ull);
-        if (pieces > 0)
-          mbar_wait_bounded(qfull, static_cast<uint32_t>(pieces - 1) & 1u, nullptr, 100000000ull);
+        if (queries > 0)
+          mbar_wait_bounded(qfull, static_cast<uint32_t>(queries - 1) & 1u, nullptr, 100000000ull);
       }
-    } else if (warp == 9) {
+      __syncwarp();
+    } else if (warp == kIssuer) {
       // ----------------------------------------------------------- MMA issuer
-      if (lane == 0) {
-        Ring<C::NST> at;
-        int pieces = 0, ks = 0;
-        uint32_t pn = 0, cleaned = 0;  // phases of pfull (a bit a group) and of clean (a bit a stage)
-        const uint32_t q_addr = smem_u32(smem), r_addr = smem_u32(ring);
-        auto take_stage = [&]() {
-          if (ok) ok = mbar_wait_bounded(&full[at.st], at.ph, abort_flag);
-          const int st = at.st;
-          at.step();
-          return st;
-        };
-        // S of group g: its queries times the keys in the next stage (tall: in
-        // the stage that both groups share).
-        auto s_mma = [&](bool tall, int g) {
-          if (!tall || g == 0) ks = take_stage();
-          if (!ok) return;
-          tc_fence_after_sync();
-          const uint32_t qa = q_addr + (tall ? g : 0) * C::TILE_BYTES;
-          const uint32_t ka = r_addr + ks * C::TILE_BYTES;
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k / 4) * C::HALF_BYTES + (k % 4) * 32;
-            mma_ss<false>(tmem + C::S_COL + g * 128, sw128_kmajor_desc(qa + off),
-                          sw128_kmajor_desc(ka + off), C::IDESC_S, k > 0 ? 1u : 0u);
-          }
-          mma_commit(&sfull[g]);
-          if (!tall || g == 1) mma_commit(&empty[ks]);
-        };
+      // The whole warp walks, so that descriptors are uniform values, and one
+      // lane issues: with one lane's own values each instruction waited for its
+      // operands' way into uniform registers, 107 cycles a product of 64.
+      Ring<C::NST> at;
+      int ks = 0;
+      uint32_t pn = 0, cleaned = 0;  // phases of pfull (a bit a group) and of clean (a bit a stage)
+      uint32_t qn = 0;
+      const uint32_t q_addr = smem_u32(smem), r_addr = smem_u32(ring);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      auto take_stage = [&]() {
+        wait(&full[at.st], at.ph);
+        const int st = at.st;
+        at.step();
+        return __shfl_sync(0xffffffffu, st, 0);
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) mma_commit(bar);
+        __syncwarp();
+      };
 #pragma unroll 1
-        while (ok && w.left > 0) {
-          const Tile t = tile_of(p, w.r, w.qt);
-          const int take = static_cast<int>(min(static_cast<int64_t>(t.units - w.j), w.left));
-          const Shares n = shares(t, w.j, take);
-          ok = mbar_wait_bounded(qfull, static_cast<uint32_t>(pieces) & 1u, abort_flag);
-          ++pieces;
+      while (true) {
+        const Piece& t = piece();
+        if (!ok || t.take == 0) break;
+        const bool tall = t.tall;
+        const int na = t.a, nb = t.b;
+        wait(qfull, qn);
+        qn ^= 1u;
+        // Step s: the product with the values of group g's tile i, then S of
+        // its next tile; before the first of each group only S.
+        int vs = 0;
 #pragma unroll 1
-          for (int g = 0; ok && g < (n.b > 0 ? 2 : 1); ++g) s_mma(t.tall, g);
-          if (ok && take == 1) mma_commit(qempty);
-          int vs = 0;
-#pragma unroll 1
-          for (int i = 0; ok && i < n.a; ++i) {
-#pragma unroll 1
-            for (int g = 0; ok && g < (i < n.b ? 2 : 1); ++g) {
-              if (!t.tall || g == 0) {
-                vs = take_stage();
-                if (!all_seen(p, t, t.key_of(w.j, i, g))) {
-                  if (ok) ok = mbar_wait_bounded(&clean[vs], cleaned >> vs & 1u, abort_flag);
-                  cleaned ^= 1u << vs;
-                }
+        for (int s = -2; ok && s < 2 * na; ++s) {
+          const int i = s >> 1, g = s & 1, n = g ? nb : na;
+          if (i >= n) continue;
+          if (i >= 0) {
+            if (!tall || g == 0) {
+              vs = take_stage();
+              if (!all_seen(p, t, t.key_of(i, g))) {
+                wait(&clean[vs], cleaned >> vs & 1u);
+                cleaned ^= 1u << vs;
               }
-              if (ok) ok = mbar_wait_bounded(&pfull[g], pn >> g & 1u, abort_flag);
-              pn ^= 1u << g;
-              if (!ok) break;
-              tc_fence_after_sync();
-              const uint32_t va = r_addr + vs * C::TILE_BYTES;
+            }
+            wait(&pfull[g], pn >> g & 1u);
+            pn ^= 1u << g;
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint32_t va = r_addr + vs * C::TILE_BYTES;
+            const uint32_t pt = tm + C::S_COL + g * 128, ot = tm + C::O_COL + g * D;
+            if (elect_one()) {
 #pragma unroll
               for (int k = 0; k < kTile / 16; ++k)
-                mma_ts(tmem + C::O_COL + g * D, tmem + C::S_COL + g * 128 + k * 8,
-                       sw128_nmajor_desc(va + k * 2048, C::HALF_BYTES), C::IDESC_O,
+                mma_ts(ot, pt + k * 8, sw128_nmajor_desc(va + k * 2048, C::HALF_BYTES), C::IDESC_O,
                        k > 0 || i > 0 ? 1u : 0u);
-              if (!t.tall || g == 1) mma_commit(&empty[vs]);
-              // S of the next tile overwrites P: the tensor core takes the
-              // products of one thread in their order.
-              if (i + 1 < (g ? n.b : n.a))
-                s_mma(t.tall, g);
-              else
-                mma_commit(&ofull[g]);
+              if (!tall || g == 1) mma_commit(&empty[vs]);
+              if (i + 1 == n) mma_commit(&ofull[g]);
             }
-            if (ok && i + 2 == take) mma_commit(qempty);  // the piece's last S is issued
+            __syncwarp();
           }
-          if (!ok) break;
-          w.next(p, take);
+          if (i + 1 < n) {
+            // S overwrites P: the tensor core takes one thread's products in
+            // their order.  Tall tiles: both groups share the keys' stage.
+            if (!tall || g == 0) ks = take_stage();
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint32_t qa = q_addr + (tall ? g : 0) * C::TILE_BYTES;
+            const uint32_t ka = r_addr + ks * C::TILE_BYTES, st = tm + C::S_COL + g * 128;
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = (k / 4) * C::HALF_BYTES + (k % 4) * 32;
+                mma_ss<false>(st, sw128_kmajor_desc(qa + off), sw128_kmajor_desc(ka + off),
+                              C::IDESC_S, k > 0 ? 1u : 0u);
+              }
+              mma_commit(&sfull[g]);
+              if (!tall || g == 1) mma_commit(&empty[ks]);
+            }
+            __syncwarp();
+          }
+          // The piece's last S is issued: its queries may go.
+          if (g == 1 && i + 2 == na) commit(qempty);
         }
-        // All products of this CTA are done before its TMEM is given back.
-        mma_commit(drained);
-        mbar_wait_bounded(drained, 0, nullptr, 100000000ull);
+        if (!ok) break;
+        piece_done();
       }
+      // All products of this CTA are done before its TMEM is given back.
+      commit(drained);
+      mbar_wait_bounded(drained, 0, nullptr, 100000000ull);
       __syncwarp();
     } else {
       // ---------------------------------------------- values that some row does not see
@@ -641,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Every stage is waited for and given back, looked at or not: a phase
       // that is skipped could be taken for another one.
       auto pass = [&](bool look) {
-        if (ok) ok = mbar_wait_bounded(&full[at.st], at.ph, abort_flag);
+        wait(&full[at.st], at.ph);
         if (ok && look) {
           clear_nonfinite<C::TILE_BYTES>(ring + at.st * C::TILE_BYTES, me, nonfinite);
           mbar_arrive(&clean[at.st]);
@@ -651,46 +748,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         at.step();
       };
 #pragma unroll 1
-      while (ok && w.left > 0) {
-        const Tile t = tile_of(p, w.r, w.qt);
-        const int take = static_cast<int>(min(static_cast<int64_t>(t.units - w.j), w.left));
-        const Shares n = shares(t, w.j, take);
-        pass(false);  // the first keys
-        if (!t.tall && n.b > 0) pass(false);
+      while (true) {
+        const Piece& t = piece();
+        if (!ok || t.take == 0) break;
+        const bool tall = t.tall;
+        const int na = t.a, nb = tall ? 0 : t.b;
+        // The stages' order is the producer's: two (or one) of keys first.
 #pragma unroll 1
-        for (int i = 0; ok && i < n.a; ++i) {
-#pragma unroll 1
-          for (int g = 0; ok && g < (!t.tall && i < n.b ? 2 : 1); ++g) {
-            pass(!all_seen(p, t, t.key_of(w.j, i, g)));
-            if (i + 1 < (g ? n.b : n.a)) pass(false);  // keys
-          }
+        for (int s = -2; ok && s < 2 * na; ++s) {
+          const int i = s >> 1, g = s & 1, n = g ? nb : na;
+          if (i >= n) continue;
+          if (i >= 0) pass(!all_seen(p, t, t.key_of(i, g)));
+          if (i + 1 < n) pass(false);
         }
-        w.next(p, take);
+        piece_done();
       }
     }
   } else {
     // -------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int g = warp >> 2, row = tid & 127;
+    const int row_tok = row / p.G, row_head = row - row_tok * p.G;
     const uint32_t quarter = static_cast<uint32_t>(warp & 3) << 21;  // 32 lanes, << 16
     const uint32_t s_addr = tmem + quarter + C::S_COL + g * 128;
     const uint32_t o_addr = tmem + quarter + C::O_COL;
     const float sc = p.scale_log2e;
     uint32_t sn = 0, xn = 0, on = 0;  // parities of the phases waited for (ofull: a bit a group)
-    while (ok && w.left > 0) {
-      const Tile t = tile_of(p, w.r, w.qt);
-      const int take = static_cast<int>(min(static_cast<int64_t>(t.units - w.j), w.left));
-      const Shares n = shares(t, w.j, take);
-      const int tok = row / p.G + (t.tall ? g * p.tpt : 0);
-      const bool mine = row < p.tpt * p.G && tok < t.ntok;
-      const int pos = t.p0 + tok;
+#pragma unroll 1
+    while (true) {
+      const Piece& t = piece();
+      if (!ok || t.take == 0) break;
+      const int tok = row_tok + (t.tall ? g * p.tpt : 0);
+      const bool mine = row_tok < p.tpt && tok < t.ntok;
       const bool busy = __any_sync(0xffffffffu, mine);
+      const int pos = t.p0 + tok;
       float m = -INFINITY, l = 0.f;
-      const int steps = g ? n.b : n.a;
+      const int steps = g ? t.b : t.a;
+#pragma unroll 1
       for (int i = 0; i < steps; ++i) {
-        const int kt = t.key_of(w.j, i, g);
-        ok = __all_sync(0xffffffffu,
-                        mbar_wait_bounded(&sfull[g], sn, abort_flag) ? 1 : 0);
+        wait(&sfull[g], sn);
         sn ^= 1u;
         if (!ok) break;
         if (busy) {
@@ -698,10 +794,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t s[4][32];
 #pragma unroll
           for (int k = 0; k < 4; ++k) tmem_ld32_async(s_addr + 32 * k, s[k]);
+          const Sight see = sight_of(p, pos, t.key_of(i, g) * kTile);
+          const bool masked = __any_sync(0xffffffffu, mine && !see.all());
 #pragma unroll
           for (int k = 0; k < 4; ++k) tmem_wait_ld(s[k]);
-          const Sight see = sight_of(p, pos, kt * kTile);
-          if (__any_sync(0xffffffffu, mine && !see.all())) {
+          if (masked) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t word = see.word(k);
@@ -710,50 +807,65 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(word >> c & 1u)) s[k][c] = 0xFF800000u;
             }
           }
-          float mx[4];
+          // Weights by the present reference, in place of S.
+          float add = 0.f;
+          bool fresh = i == 0;
+#pragma unroll 1
+          while (true) {
+            if (fresh) {
+              float mx[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            mx[k] = __uint_as_float(s[k][0]);
+              for (int k = 0; k < 8; ++k) {
+                mx[k] = __uint_as_float(s[k / 2][k % 2 * 16]);
 #pragma unroll
-            for (int c = 1; c < 32; ++c) mx[k] = fmaxf(mx[k], __uint_as_float(s[k][c]));
-          }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          if (__any_sync(0xffffffffu, top > m + p.lazy)) {
-            const float mn = fmaxf(m, top);
-            const float f = m == -INFINITY ? 0.f : ex2((m - mn) * sc);
-            m = mn;
-            l *= f;
-            if (i > 0) {
+                for (int c = 1; c < 16; ++c)
+                  mx[k] = fmaxf(mx[k], __uint_as_float(s[k / 2][k % 2 * 16 + c]));
+              }
+              const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                      fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+              const float mn = fmaxf(m, top);
+              const float f = m == -INFINITY ? 0.f : ex2((m - mn) * sc);
+              m = mn;
+              l *= f;
+              if (i > 0) {
+#pragma unroll 1
+                for (int d = 0; d < D; d += 16) {
+                  float o[16];
+                  tmem_load16(o_addr + g * D + d, o);
+                  uint32_t r[16];
 #pragma unroll
-              for (int d = 0; d < D; d += 16) {
-                float o[16];
-                tmem_load16(o_addr + g * D + d, o);
-                uint32_t r[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(o[k] * f);
-                tmem_st16(o_addr + g * D + d, r);
+                  for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(o[k] * f);
+                  tmem_st16(o_addr + g * D + d, r);
+                }
               }
             }
-          }
-          const float ref = m == -INFINITY ? 0.f : -m * sc;
-          const float2 ref2 = make_float2(ref, ref), sc2 = make_float2(sc, sc);
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            const float ref = m == -INFINITY ? 0.f : -m * sc;
+            const float2 ref2 = make_float2(ref, ref), sc2 = make_float2(sc, sc);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t pk[16];
+            for (int k = 0; k < 4; ++k) {
+              uint32_t pk[16];
 #pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              const float2 x = __ffma2_rn(
-                  make_float2(__uint_as_float(s[k][c]), __uint_as_float(s[k][c + 1])), sc2, ref2);
-              const float2 e = make_float2(ex2(x.x), ex2(x.y));
-              sum[c >> 1 & 1] = __fadd2_rn(sum[c >> 1 & 1], e);
-              const __nv_bfloat162 y = __floats2bfloat162_rn(e.x, e.y);
-              pk[c >> 1] = *reinterpret_cast<const uint32_t*>(&y);
+              for (int c = 0; c < 32; c += 2) {
+                const float2 x = __ffma2_rn(
+                    make_float2(__uint_as_float(s[k][c]), __uint_as_float(s[k][c + 1])), sc2, ref2);
+                const float2 e = make_float2(ex2(x.x), ex2(x.y));
+                sum[c >> 1 & 1] = __fadd2_rn(sum[c >> 1 & 1], e);
+                const __nv_bfloat162 y = __floats2bfloat162_rn(e.x, e.y);
+                pk[c >> 1] = *reinterpret_cast<const uint32_t*>(&y);
+              }
+              tmem_st16(s_addr + 16 * k, pk);
             }
-            tmem_st16(s_addr + 16 * k, pk);
+            const float2 both = __fadd2_rn(sum[0], sum[1]);
+            add = both.x + both.y;
+            // A new reference: the first tile, rows that have seen nothing yet,
+            // and where the old one lets the weights grow (or they are NaN).
+            if (fresh ||
+                !__any_sync(0xffffffffu, mine && (m == -INFINITY || !(add <= kMostSum))))
+              break;
+            fresh = true;
           }
-          const float2 both = __fadd2_rn(sum[0], sum[1]);
-          l += both.x + both.y;
+          l += add;
           tmem_wait_st();
           tc_fence_before_sync();
         }
@@ -762,109 +874,85 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // The piece's outputs.
       auto wait_o = [&](int k) {
-        if ((k ? n.b : n.a) == 0) return;
-        if (ok)
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait_bounded(&ofull[k], on >> k & 1u, abort_flag) ? 1 : 0);
+        if ((k ? t.b : t.a) == 0) return;
+        wait(&ofull[k], on >> k & 1u);
         on ^= 1u << k;
       };
       wait_o(g);
       if (!t.tall) wait_o(1 - g);
       if (!ok) break;
       tc_fence_after_sync();
-      const bool whole = w.j == 0 && take == t.units;
-      const int64_t at =
-          static_cast<int64_t>(t.tok0 + tok) * p.Hq + w.h * p.G + (row - row / p.G * p.G);
+      const bool whole = t.whole;
+      const int64_t at = static_cast<int64_t>(t.tok0 + tok) * p.Hq + t.h * p.G + row_head;
       // Slot 1 starts a tile, slot 0 goes on with one that an earlier CTA started.
-      const int64_t part = static_cast<int64_t>(2 * blockIdx.x + (w.j == 0 ? 1 : 0)) * p.slot_rows +
+      const int64_t part = static_cast<int64_t>(2 * blockIdx.x + (t.j == 0 ? 1 : 0)) * p.slot_rows +
                            (t.tall ? g * kTile : 0) + row;
-      const bool bad = *nonfinite != 0;
-      const float m2 = m * sc;
-      if (t.tall) {
-        const float f = l == 0.f ? 0.f : 1.f / l;
-        if (busy) {
-#pragma unroll
-          for (int d = 0; d < D; d += 32) {
-            float o[32];
-            tmem_load32(o_addr + g * D + d, o);
-            if (mine) {
-              if (bad) add_nonfinite<D>(p, w, t, take, pos, d, o);
-              if (whole)
-                store_out(p.out + at * D + d, o, f);
-              else
-                store_part(p.part_o + part * D + d, o);
-            }
-            __syncwarp();
-          }
-        }
-        if (mine) {
-          if (!whole)
-            p.part_ml[part] = make_float2(m2, l);
-          else if (p.lse)
-            p.lse[at] = lse_of(m2, l);
-        }
-        wait_o(1 - g);  // no phase is skipped
-        if (!ok) break;
-      } else {
-        // A and B hold two halves of the same rows' keys: each group joins one
-        // half of the elements.
-        xml[g * 128 + row] = make_float2(m2, l);
+      // Tall: this group's rows.  Short: A and B hold two halves of the same
+      // rows' keys, and each group joins one half of the elements.
+      float top = m * sc, sum = l, fa = 1.f, fb = 0.f;
+      int d0 = 0, d1 = D;
+      uint32_t from = o_addr + g * D;
+      if (!t.tall) {
+        xml[g * 128 + row] = make_float2(top, l);
         mbar_arrive(&xbar[0]);
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&xbar[0], xn, abort_flag) ? 1 : 0);
+        wait(&xbar[0], xn);
         if (!ok) break;
-        const float2 a = xml[row], b = n.b > 0 ? xml[128 + row] : make_float2(-INFINITY, 0.f);
-        const float top = fmaxf(a.x, b.x);
-        const float fa = a.x == -INFINITY ? 0.f : ex2(a.x - top);
-        const float fb = b.x == -INFINITY ? 0.f : ex2(b.x - top);
-        const float sum = a.y * fa + b.y * fb;
-        const float f = sum == 0.f ? 0.f : 1.f / sum;
-        if (busy) {
+        const float2 a = xml[row], b = t.b > 0 ? xml[128 + row] : make_float2(-INFINITY, 0.f);
+        top = fmaxf(a.x, b.x);
+        fa = a.x == -INFINITY ? 0.f : ex2(a.x - top);
+        fb = b.x == -INFINITY ? 0.f : ex2(b.x - top);
+        sum = a.y * fa + b.y * fb;
+        d0 = g * (D / 2);
+        d1 = d0 + D / 2;
+        from = o_addr;
+      }
+      const float f = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+      const bool second = !t.tall && t.b > 0;
+      if (busy) {
+#pragma unroll 1
+        for (int d = d0; d < d1; d += 32) {
+          float o[32];
+          tmem_load32(from + d, o);
+          if (second) {
+            float o2[32];
+            tmem_load32(o_addr + D + d, o2);
 #pragma unroll
-          for (int d = 0; d < D / 2; d += 32) {
-            const int d0 = g * (D / 2) + d;
-            float o[32];
-            tmem_load32(o_addr + d0, o);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] *= fa;
-            if (n.b > 0) {
-              float o2[32];
-              tmem_load32(o_addr + D + d0, o2);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = fmaf(o2[k], fb, o[k]);
-            }
-            if (mine) {
-              if (bad) add_nonfinite<D>(p, w, t, take, pos, d0, o);
-              if (whole)
-                store_out(p.out + at * D + d0, o, f);
-              else
-                store_part(p.part_o + part * D + d0, o);
-            }
-            __syncwarp();
+            for (int k = 0; k < 32; ++k) o[k] = fmaf(o2[k], fb, o[k] * fa);
           }
+          if (mine) {
+            if (whole)
+              store_out(p.out + at * D + d, o, second ? f : f * fa);
+            else
+              store_part(p.part_o + part * D + d, o, second ? 1.f : fa);
+          }
+          __syncwarp();
         }
-        if (mine && g == 0) {
+      }
+      if (mine) {
+        if (*nonfinite)
+          add_nonfinite<D>(p, t, pos, d0, d1 - d0, p.out + at * D,
+                           whole ? nullptr : p.part_o + part * D);
+        if (d0 == 0) {
           if (!whole)
             p.part_ml[part] = make_float2(top, sum);
           else if (p.lse)
             p.lse[at] = lse_of(top, sum);
         }
+      }
+      __syncwarp();
+      if (!whole && t.j == 0 && tid == 0)
+        p.notes[blockIdx.x] = make_int4(t.tok0, t.ntok, t.h, t.more);
+      if (t.tall) {
+        wait_o(1 - g);  // no phase is skipped
+      } else {
         tc_fence_before_sync();
         mbar_arrive(&xbar[1]);
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&xbar[1], xn, abort_flag) ? 1 : 0);
+        wait(&xbar[1], xn);
         xn ^= 1u;
-        if (!ok) break;
         tc_fence_after_sync();
       }
-      if (!whole && w.j == 0 && tid == 0) {
-        // The join's note: the tile, and how many CTAs go on with it (CTA c has
-        // the units from floor(c total / ctas) on).
-        const int64_t ctas = min(static_cast<int64_t>(gridDim.x), w.total);
-        const int64_t end = (blockIdx.x + 1) * w.total / ctas - w.left + t.units;
-        p.notes[blockIdx.x] = make_int4(t.tok0, t.ntok, w.h,
-                                        static_cast<int>((end * ctas - 1) / w.total) -
-                                            static_cast<int>(blockIdx.x));
-      }
-      w.next(p, take);
+      if (!ok) break;
+      piece_done();
     }
   }
   if (!ok) {
@@ -873,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kIssuer) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
   }
