@@ -677,39 +677,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = -2; ok && s < 2 * na; ++s) {
           const int i = s >> 1, g = s & 1, n = g ? nb : na;
           if (i >= n) continue;
-          if (i >= 0) {
-            if (!tall || g == 0) {
-              vs = take_stage();
-              if (!all_seen(p, t, t.key_of(i, g))) {
-                wait(&clean[vs], cleaned >> vs & 1u);
-                cleaned ^= 1u << vs;
-              }
+          // The stages are waited for first: the products then follow the
+          // weights without a pause.
+          const bool more = i + 1 < n;
+          if (i >= 0 && (!tall || g == 0)) {
+            vs = take_stage();
+            if (!all_seen(p, t, t.key_of(i, g))) {
+              wait(&clean[vs], cleaned >> vs & 1u);
+              cleaned ^= 1u << vs;
             }
+          }
+          if (more && (!tall || g == 0)) ks = take_stage();
+          if (i >= 0) {
             wait(&pfull[g], pn >> g & 1u);
             pn ^= 1u << g;
-            if (!ok) break;
-            tc_fence_after_sync();
-            const uint32_t va = r_addr + vs * C::TILE_BYTES;
-            const uint32_t pt = tm + C::S_COL + g * 128, ot = tm + C::O_COL + g * D;
-            if (elect_one()) {
+          }
+          if (!ok) break;
+          tc_fence_after_sync();
+          const uint32_t va = r_addr + vs * C::TILE_BYTES, ka = r_addr + ks * C::TILE_BYTES;
+          const uint32_t qa = q_addr + (tall ? g : 0) * C::TILE_BYTES;
+          const uint32_t st = tm + C::S_COL + g * 128, ot = tm + C::O_COL + g * D;
+          if (elect_one()) {
+            if (i >= 0) {
 #pragma unroll
               for (int k = 0; k < kTile / 16; ++k)
-                mma_ts(ot, pt + k * 8, sw128_nmajor_desc(va + k * 2048, C::HALF_BYTES), C::IDESC_O,
+                mma_ts(ot, st + k * 8, sw128_nmajor_desc(va + k * 2048, C::HALF_BYTES), C::IDESC_O,
                        k > 0 || i > 0 ? 1u : 0u);
               if (!tall || g == 1) mma_commit(&empty[vs]);
-              if (i + 1 == n) mma_commit(&ofull[g]);
+              if (!more) mma_commit(&ofull[g]);
             }
-            __syncwarp();
-          }
-          if (i + 1 < n) {
             // S overwrites P: the tensor core takes one thread's products in
             // their order.  Tall tiles: both groups share the keys' stage.
-            if (!tall || g == 0) ks = take_stage();
-            if (!ok) break;
-            tc_fence_after_sync();
-            const uint32_t qa = q_addr + (tall ? g : 0) * C::TILE_BYTES;
-            const uint32_t ka = r_addr + ks * C::TILE_BYTES, st = tm + C::S_COL + g * 128;
-            if (elect_one()) {
+            if (more) {
 #pragma unroll
               for (int k = 0; k < D / 16; ++k) {
                 const uint32_t off = (k / 4) * C::HALF_BYTES + (k % 4) * 32;
@@ -719,8 +718,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_commit(&sfull[g]);
               if (!tall || g == 1) mma_commit(&empty[ks]);
             }
-            __syncwarp();
           }
+          __syncwarp();
           // The piece's last S is issued: its queries may go.
           if (g == 1 && i + 2 == na) commit(qempty);
         }
@@ -786,6 +785,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int steps = g ? t.b : t.a;
 #pragma unroll 1
       for (int i = 0; i < steps; ++i) {
+        const Sight see = sight_of(p, pos, t.key_of(i, g) * kTile);
+        const bool masked = __any_sync(0xffffffffu, mine && !see.all());
         wait(&sfull[g], sn);
         sn ^= 1u;
         if (!ok) break;
@@ -794,8 +795,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t s[4][32];
 #pragma unroll
           for (int k = 0; k < 4; ++k) tmem_ld32_async(s_addr + 32 * k, s[k]);
-          const Sight see = sight_of(p, pos, t.key_of(i, g) * kTile);
-          const bool masked = __any_sync(0xffffffffu, mine && !see.all());
 #pragma unroll
           for (int k = 0; k < 4; ++k) tmem_wait_ld(s[k]);
           if (masked) {
