@@ -16,8 +16,8 @@
 //         token's long axis keeps both halves busy too
 //
 // Work.  A unit is one tile of 128 keys (tall) or two (short).  The units of
-// all heads, requests and row tiles, in that order, are cut into equal runs,
-// one for each CTA; a tile that a cut goes through leaves its parts (maximum,
+// all heads, requests and row tiles, in that order, and what each tile costs
+// besides, are cut into equal runs, one for each CTA; a tile that a cut goes through leaves its parts (maximum,
 // sum, unscaled output, all fp32) in the workspace, and a second kernel joins
 // them in their fixed order.  Lengths are read on the device, so a captured
 // graph serves every step, and one long request fills the GPU as evenly as
@@ -70,6 +70,24 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// mbar_wait_bounded with the clock read only after many tries: the read takes
+// longer than most waits here.
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity,
+                                             volatile uint32_t* abort,
+                                             uint64_t timeout_ns = kWaitTimeoutNs) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 255u) == 0) {
+      if (abort && *abort) return false;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > timeout_ns) return false;
+    }
+  }
 }
 
 __device__ __forceinline__ void tma_load_box3(void* dst, const CUtensorMap* map, uint64_t* bar,
@@ -181,29 +199,27 @@ struct Piece {
   int h, req, L;
   int whole;     // the piece is the whole tile
   int more;      // CTAs that go on with the tile (where the piece starts it)
+  // Key tiles that every row sees whole: those below `seen`, of these in a
+  // window the ones from `behind` on and the first `kept`.
+  int seen, behind, kept;
+  __device__ bool all_seen(int kt) const { return kt < seen && (kt >= behind || kt < kept); }
   // The i-th key tile of group g.
   __device__ int key_of(int i, int g) const {
     const int k = tall ? j + i : 2 * (j + i) + g;
     return k < nsink ? k : first + (k - nsink);
   }
 };
-constexpr int kPieces = 4;  // published ahead
+constexpr int kPieces = 4;    // published ahead
+constexpr int kTileCost = 2;  // units that a tile's start and end take (about 8000 cycles)
 
-// Whether every row of the tile sees all keys of key tile kt.
-__device__ __forceinline__ bool all_seen(const KvAttnParams& p, const Piece& t, int kt) {
-  const int c0 = kt * kTile;
-  return c0 + kTile - 1 <= t.p0 &&
-         (p.window == 0 || c0 > t.last - p.window || c0 + kTile <= p.sink);
-}
-
-// A run of units and where it stands.
+// A CTA's run of the work and where it stands.
 struct Walk {
   Req r;
-  int h, qt, j;
-  int64_t left, total;  // units to go, and of the whole call
+  int h, qt, at;        // at: how much of the tile's cost lies behind
+  int64_t left, total;  // cost to go, and of the whole call
   __device__ void next(const KvAttnParams& p, int taken) {
     left -= taken;
-    j = 0;
+    at = 0;
     if (left <= 0) return;
     if (++qt < tiles_of(p, r)) return;
     qt = 0;
@@ -218,12 +234,11 @@ struct Walk {
   }
 };
 
-// Units of one request's row tiles for one head, summed by one thread.
-__device__ __forceinline__ int units_by_thread(const KvAttnParams& p, const Req& r, int nt) {
-  int u = 0;
-#pragma unroll 1
-  for (int qt = 0; qt < nt; ++qt) u += tile_of(p, r, qt).units;
-  return u;
+// What a tile counts in the division of the work: its units, and what starting
+// and ending it costs in units (queries, the first logits, the outputs), as if
+// that came first.
+__device__ __forceinline__ int cost_of(const KvAttnParams& p, const Req& r, int qt) {
+  return kTileCost + tile_of(p, r, qt).units;
 }
 
 // This CTA's run, for the producer's warp.  Called by all threads; `pfx` is
@@ -237,7 +252,13 @@ __device__ Walk find_run(const KvAttnParams& p, int* pfx) {
   for (int b = tid; b < p.B; b += kThreads) {
     const Req r = req_of(p, b, err);
     const int nt = tiles_of(p, r);
-    pfx[b + 1] = nt <= kFew ? units_by_thread(p, r, nt) : -1;
+    int u = -1;
+    if (nt <= kFew) {
+      u = 0;
+#pragma unroll 1
+      for (int qt = 0; qt < nt; ++qt) u += cost_of(p, r, qt);
+    }
+    pfx[b + 1] = u;
   }
   __syncthreads();
 #pragma unroll 1
@@ -247,7 +268,7 @@ __device__ Walk find_run(const KvAttnParams& p, int* pfx) {
     const int nt = tiles_of(p, r);
     int u = 0;
 #pragma unroll 1
-    for (int qt = lane; qt < nt; qt += 32) u += tile_of(p, r, qt).units;
+    for (int qt = lane; qt < nt; qt += 32) u += cost_of(p, r, qt);
     u = __reduce_add_sync(0xffffffffu, u);
     __syncwarp();
     if (lane == 0) pfx[b + 1] = u;
@@ -290,7 +311,7 @@ __device__ Walk find_run(const KvAttnParams& p, int* pfx) {
     const int nt = tiles_of(p, w.r);
 #pragma unroll 1
     for (int base = 0; base < nt; base += 32) {
-      const int u = base + lane < nt ? tile_of(p, w.r, base + lane).units : 0;
+      const int u = base + lane < nt ? cost_of(p, w.r, base + lane) : 0;
       int incl = u;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -301,7 +322,7 @@ __device__ Walk find_run(const KvAttnParams& p, int* pfx) {
       if (past) {
         const int k = __ffs(past) - 1;
         w.qt = base + k;
-        w.j = at - __shfl_sync(0xffffffffu, incl - u, k);
+        w.at = at - __shfl_sync(0xffffffffu, incl - u, k);
         break;
       }
       at -= __shfl_sync(0xffffffffu, incl, 31);
@@ -388,7 +409,7 @@ __device__ __noinline__ void add_nonfinite(const KvAttnParams& p, const Piece& t
 #pragma unroll 1
   for (int i = 0; i < t.a + (t.tall ? 0 : t.b); ++i) {
     const int kt = t.tall ? t.key_of(i, 0) : t.key_of(i / 2, i % 2);
-    if (all_seen(p, t, kt)) continue;
+    if (t.all_seen(kt)) continue;
     const Sight s = sight_of(p, pos, kt * kTile);
 #pragma unroll 1
     for (int c = 0; c < kTile; ++c) {
@@ -524,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool ok = true;
   // Waits of a whole warp; after one that gave up the others pass at once.
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag) ? 1 : 0);
+    if (ok) ok = __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag) ? 1 : 0);
   };
   // The next piece, and its return once nothing of it is read any more.
   Ring<kPieces> next;
@@ -569,11 +590,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(&done[next.st], next.ph ^ 1u);
         if (!ok) break;
         Piece t = {};
-        if (w.left > 0) {
+        int taken = 0;
+        while (w.left > 0) {
           const Tile tile = tile_of(p, w.r, w.qt);
+          const int cost = kTileCost + tile.units;
+          taken = static_cast<int>(min(static_cast<int64_t>(cost - w.at), w.left));
+          t.j = max(w.at - kTileCost, 0);
+          t.take = max(w.at + taken - kTileCost, 0) - t.j;
+          if (t.take == 0) {  // a cut in what starts the tile: the next CTA's
+            w.next(p, taken);
+            continue;
+          }
           const int64_t ctas = min(static_cast<int64_t>(gridDim.x), w.total);
-          // CTA c has the units from floor(c total / ctas) on: who has the last one.
-          const int64_t end = (blockIdx.x + 1) * w.total / ctas - w.left - w.j + tile.units;
+          // CTA c has the cost from floor(c total / ctas) on: who has the tile's end.
+          const int64_t end = (blockIdx.x + 1) * w.total / ctas - w.left - w.at + cost;
           t.tok0 = tile.tok0;
           t.ntok = tile.ntok;
           t.p0 = tile.p0;
@@ -582,8 +612,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           t.first = tile.first;
           t.keys = tile.keys;
           t.tall = tile.tall;
-          t.j = w.j;
-          t.take = static_cast<int>(min(static_cast<int64_t>(tile.units - w.j), w.left));
+          t.seen = max(t.p0 + 1, 0) / kTile;
+          t.behind = p.window > 0 ? max(t.last - p.window + kTile, 0) / kTile : 0;
+          t.kept = p.sink / kTile;
           t.a = t.take;
           t.b = t.tall || 2 * (t.j + t.take) <= t.keys ? t.take : t.take - 1;
           t.h = w.h;
@@ -591,6 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           t.L = w.r.L;
           t.whole = t.j == 0 && t.take == tile.units;
           t.more = static_cast<int>((end * ctas - 1) / w.total) - static_cast<int>(blockIdx.x);
+          break;
         }
         if (lane == 0) {
           pieces[next.st] = t;
@@ -630,15 +662,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           load(1, now);
           if (more) load(0, pg);
         }
-        w.next(p, t.take);
+        w.next(p, taken);
       }
       if (!ok && lane == 0) {
         // Let the copies already in flight land before the CTA retires.
         for (int i = loads > C::NST ? loads - C::NST : 0; i < loads; ++i)
-          mbar_wait_bounded(&full[i % C::NST], static_cast<uint32_t>(i / C::NST) & 1u, nullptr,
+          wait_bounded(&full[i % C::NST], static_cast<uint32_t>(i / C::NST) & 1u, nullptr,
                             100000000ull);
         if (queries > 0)
-          mbar_wait_bounded(qfull, static_cast<uint32_t>(queries - 1) & 1u, nullptr, 100000000ull);
+          wait_bounded(qfull, static_cast<uint32_t>(queries - 1) & 1u, nullptr, 100000000ull);
       }
       __syncwarp();
     } else if (warp == kIssuer) {
@@ -664,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
 #pragma unroll 1
       while (true) {
-        const Piece& t = piece();
+        const Piece t = piece();
         if (!ok || t.take == 0) break;
         const bool tall = t.tall;
         const int na = t.a, nb = t.b;
@@ -682,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool more = i + 1 < n;
           if (i >= 0 && (!tall || g == 0)) {
             vs = take_stage();
-            if (!all_seen(p, t, t.key_of(i, g))) {
+            if (!t.all_seen(t.key_of(i, g))) {
               wait(&clean[vs], cleaned >> vs & 1u);
               cleaned ^= 1u << vs;
             }
@@ -728,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // All products of this CTA are done before its TMEM is given back.
       commit(drained);
-      mbar_wait_bounded(drained, 0, nullptr, 100000000ull);
+      wait_bounded(drained, 0, nullptr, 100000000ull);
       __syncwarp();
     } else {
       // ---------------------------------------------- values that some row does not see
@@ -757,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = -2; ok && s < 2 * na; ++s) {
           const int i = s >> 1, g = s & 1, n = g ? nb : na;
           if (i >= n) continue;
-          if (i >= 0) pass(!all_seen(p, t, t.key_of(i, g)));
+          if (i >= 0) pass(!t.all_seen(t.key_of(i, g)));
           if (i + 1 < n) pass(false);
         }
         piece_done();
@@ -1075,7 +1107,7 @@ KvAttnPlan kv_attn_plan(int T, int G, int D) {
 }
 
 int64_t kv_attn_units(int T, int B, int G, int64_t max_ctx) {
-  return (static_cast<int64_t>(T) / (2 * (kTile / G)) + B) * ((max_ctx + kTile - 1) / kTile + 1);
+  return (static_cast<int64_t>(T) / (2 * (kTile / G)) + B) * ((max_ctx + kTile - 1) / kTile + 1 + kTileCost);
 }
 
 cudaError_t launch_kv_attention(const KvAttnParams& p, int D, cudaStream_t s) {
