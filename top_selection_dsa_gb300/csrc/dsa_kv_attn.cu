@@ -72,22 +72,20 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// mbar_wait_bounded with the clock read only after many tries: the read takes
-// longer than most waits here.
+// A wait for the phase of `bar` with the given parity that gives up after
+// kMaxTries (of at least some 20 ns each, and more where the hardware suspends
+// the warp) or once another role did.  A try counter instead of a clock: its
+// code is a few instructions, and there is a copy at every wait.
+constexpr uint32_t kMaxTries = 1u << 24, kDrainTries = 1u << 20;
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity,
                                              volatile uint32_t* abort,
-                                             uint64_t timeout_ns = kWaitTimeoutNs) {
-  uint64_t t0 = 0;
+                                             uint32_t tries = kMaxTries) {
 #pragma unroll 1
-  for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 255u) == 0) {
-      if (abort && *abort) return false;
-      const uint64_t now = globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > timeout_ns) return false;
-    }
+  for (uint32_t it = tries; it != 0; --it) {
+    if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
+    if ((it & 1023u) == 0 && *abort) return false;
   }
+  return false;
 }
 
 __device__ __forceinline__ void tma_load_box3(void* dst, const CUtensorMap* map, uint64_t* bar,
@@ -666,11 +664,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok && lane == 0) {
         // Let the copies already in flight land before the CTA retires.
+        volatile uint32_t never = 0;
         for (int i = loads > C::NST ? loads - C::NST : 0; i < loads; ++i)
-          wait_bounded(&full[i % C::NST], static_cast<uint32_t>(i / C::NST) & 1u, nullptr,
-                            100000000ull);
+          wait_bounded(&full[i % C::NST], static_cast<uint32_t>(i / C::NST) & 1u, &never,
+                            kDrainTries);
         if (queries > 0)
-          wait_bounded(qfull, static_cast<uint32_t>(queries - 1) & 1u, nullptr, 100000000ull);
+          wait_bounded(qfull, static_cast<uint32_t>(queries - 1) & 1u, &never, kDrainTries);
       }
       __syncwarp();
     } else if (warp == kIssuer) {
@@ -714,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool more = i + 1 < n;
           if (i >= 0 && (!tall || g == 0)) {
             vs = take_stage();
-            if (!t.all_seen(t.key_of(i, g))) {
+            if (__builtin_expect(!t.all_seen(t.key_of(i, g)), 0)) {
               wait(&clean[vs], cleaned >> vs & 1u);
               cleaned ^= 1u << vs;
             }
@@ -760,7 +759,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // All products of this CTA are done before its TMEM is given back.
       commit(drained);
-      wait_bounded(drained, 0, nullptr, 100000000ull);
+      volatile uint32_t never = 0;
+      wait_bounded(drained, 0, &never, kDrainTries);
       __syncwarp();
     } else {
       // ---------------------------------------------- values that some row does not see
@@ -829,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 4; ++k) tmem_ld32_async(s_addr + 32 * k, s[k]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) tmem_wait_ld(s[k]);
-          if (masked) {
+          if (__builtin_expect(masked, 0)) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t word = see.word(k);
@@ -843,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool fresh = i == 0;
 #pragma unroll 1
           while (true) {
-            if (fresh) {
+            if (__builtin_expect(fresh, 0)) {
               float mx[8];
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
