@@ -24,8 +24,8 @@
 // many short ones.
 //
 // Roles: warps 0-3 softmax of A, 4-7 of B, 8 TMA (queries, then a ring of key
-// and value tiles fetched page by page), 9 tcgen05.mma, 10-11 the check of
-// values that some row does not see.  S = Q K^T goes to TMEM; P overwrites it
+// and value tiles fetched page by page), 9 and 10 tcgen05.mma of A and of B, 11
+// the check of values that some row does not see.  S = Q K^T goes to TMEM; P overwrites it
 // as bf16 and is the A operand of O += P V straight from TMEM.  A row's
 // reference maximum is only moved, and O rescaled, when the maximum grows by
 // more than 2^8: P stays below 2^8 and sums are fp32, so nothing is lost.
@@ -49,8 +49,8 @@ namespace {
 
 constexpr int kTile = 128;    // keys of a tile, rows of a row tile
 constexpr int kThreads = 384;
-constexpr int kProducer = 8;  // warps: 0-7 softmax, then the producer, the issuer, the check
-constexpr int kIssuer = 9;
+// Warps: 0-7 softmax, then these (an issuer for A, one for B).
+constexpr int kProducer = 8, kIssuer = 9, kCheck = 11;
 constexpr int kMaxStages = 12;
 // A row's weights of one tile add to no more than this, or its reference moves.
 constexpr float kMostSum = 65536.f;
@@ -345,21 +345,21 @@ struct Ring {
   }
 };
 
-// Zeroes the infinities and NaN of a tile in shared memory (64 threads) and
+// Zeroes the infinities and NaN of a tile in shared memory (one warp) and
 // says so in *flag.
 template <int BYTES>
 __device__ __forceinline__ void clear_nonfinite(uint8_t* tile, int me, volatile uint32_t* flag) {
   uint4* v = reinterpret_cast<uint4*>(tile);
   uint32_t top = 0;
 #pragma unroll 8
-  for (int k = me; k < BYTES / 16; k += 64) {
+  for (int k = me; k < BYTES / 16; k += 32) {
     const uint4 x = v[k];
     top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
                                  __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
   }
   if ((top & 0xFFFFu) < 0x7F80u && (top >> 16) < 0x7F80u) return;
   uint16_t* e = reinterpret_cast<uint16_t*>(v);
-  for (int k = me; k < BYTES / 16; k += 64)
+  for (int k = me; k < BYTES / 16; k += 32)
     for (int q = 0; q < 8; ++q)
       if ((e[8 * k + q] & 0x7F80u) == 0x7F80u) e[8 * k + q] = 0;
   *flag = 1;
@@ -508,12 +508,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < C::NST; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 3);  // the products, and the two warps of the check
-      mbar_init(&clean[i], 64);
+      mbar_init(&empty[i], 3);  // both groups' products, and the check
+      mbar_init(&clean[i], 32);
     }
     mbar_init(qfull, 1);
-    mbar_init(qempty, 1);
-    mbar_init(drained, 1);
+    mbar_init(qempty, 2);
+    mbar_init(drained, 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfull[i], 1);
       mbar_init(&pfull[i], 4);
@@ -672,73 +672,74 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_bounded(qfull, static_cast<uint32_t>(queries - 1) & 1u, &never, kDrainTries);
       }
       __syncwarp();
-    } else if (warp == kIssuer) {
-      // ----------------------------------------------------------- MMA issuer
-      // The whole warp walks, so that descriptors are uniform values, and one
-      // lane issues: with one lane's own values each instruction waited for its
-      // operands' way into uniform registers, 107 cycles a product of 64.
+    } else if (warp < kCheck) {
+      // --------------------------------------------------- MMA issuers, one a group
+      // The products read shared memory at its full rate, and every barrier
+      // that a warp looks at then takes some 250 cycles: with a warp a group,
+      // one looks while the other's products run.  The whole warp walks, so
+      // that descriptors are uniform values, and one lane issues: with one
+      // lane's own values each instruction waited for its operands' way into
+      // uniform registers, 107 cycles a product of 64.
+      const int g = warp - kIssuer;
       Ring<C::NST> at;
-      int ks = 0;
-      uint32_t pn = 0, cleaned = 0;  // phases of pfull (a bit a group) and of clean (a bit a stage)
-      uint32_t qn = 0;
+      uint32_t pn = 0, qn = 0, cleaned = 0;  // parities of pfull, qfull and clean (a bit a stage)
       const uint32_t q_addr = smem_u32(smem), r_addr = smem_u32(ring);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      auto take_stage = [&]() {
+      const uint32_t st = tm + C::S_COL + g * 128, ot = tm + C::O_COL + g * D;
+      // The next stage; both issuers wait for each, and give back those of the
+      // other group alone at once.
+      auto take_stage = [&](bool mine) {
         wait(&full[at.st], at.ph);
-        const int st = at.st;
+        const int k = at.st;
         at.step();
-        return __shfl_sync(0xffffffffu, st, 0);
-      };
-      auto commit = [&](uint64_t* bar) {
-        if (elect_one()) mma_commit(bar);
-        __syncwarp();
+        if (!mine && ok && elect_one()) mbar_arrive(&empty[k]);
+        return __shfl_sync(0xffffffffu, k, 0);
       };
 #pragma unroll 1
       while (true) {
         const Piece t = piece();
         if (!ok || t.take == 0) break;
         const bool tall = t.tall;
-        const int na = t.a, nb = t.b;
+        const int n = g ? t.b : t.a;  // this group's key tiles
+        const uint32_t qa = q_addr + (tall ? g : 0) * C::TILE_BYTES;
         wait(qfull, qn);
         qn ^= 1u;
-        // Step s: the product with the values of group g's tile i, then S of
-        // its next tile; before the first of each group only S.
-        int vs = 0;
+        // Stages come as the values of a tile and the keys of its group's next
+        // one (before the first, only keys); tall: one tile for both groups.
 #pragma unroll 1
-        for (int s = -2; ok && s < 2 * na; ++s) {
-          const int i = s >> 1, g = s & 1, n = g ? nb : na;
-          if (i >= n) continue;
-          // The stages are waited for first: the products then follow the
-          // weights without a pause.
-          const bool more = i + 1 < n;
-          if (i >= 0 && (!tall || g == 0)) {
-            vs = take_stage();
-            if (__builtin_expect(!t.all_seen(t.key_of(i, g)), 0)) {
-              wait(&clean[vs], cleaned >> vs & 1u);
+        for (int s = tall ? -1 : -2; ok && s < (tall ? t.a : 2 * t.a); ++s) {
+          const int i = tall ? s : s >> 1, whose = tall ? g : s & 1;
+          const int all = whose ? t.b : t.a;
+          if (i >= all) continue;
+          const bool mine = whose == g, more = i + 1 < all;
+          int vs = 0, ks = 0;
+          if (i >= 0) {
+            vs = take_stage(mine);
+            if (__builtin_expect(!t.all_seen(t.key_of(i, whose)), 0)) {
+              if (mine) wait(&clean[vs], cleaned >> vs & 1u);
               cleaned ^= 1u << vs;
             }
           }
-          if (more && (!tall || g == 0)) ks = take_stage();
+          if (more) ks = take_stage(mine);
+          if (!mine) continue;
           if (i >= 0) {
-            wait(&pfull[g], pn >> g & 1u);
-            pn ^= 1u << g;
+            wait(&pfull[g], pn);
+            pn ^= 1u;
           }
           if (!ok) break;
           tc_fence_after_sync();
           const uint32_t va = r_addr + vs * C::TILE_BYTES, ka = r_addr + ks * C::TILE_BYTES;
-          const uint32_t qa = q_addr + (tall ? g : 0) * C::TILE_BYTES;
-          const uint32_t st = tm + C::S_COL + g * 128, ot = tm + C::O_COL + g * D;
           if (elect_one()) {
             if (i >= 0) {
 #pragma unroll
               for (int k = 0; k < kTile / 16; ++k)
                 mma_ts(ot, st + k * 8, sw128_nmajor_desc(va + k * 2048, C::HALF_BYTES), C::IDESC_O,
                        k > 0 || i > 0 ? 1u : 0u);
-              if (!tall || g == 1) mma_commit(&empty[vs]);
+              mma_commit(&empty[vs]);
               if (!more) mma_commit(&ofull[g]);
             }
             // S overwrites P: the tensor core takes one thread's products in
-            // their order.  Tall tiles: both groups share the keys' stage.
+            // their order.
             if (more) {
 #pragma unroll
               for (int k = 0; k < D / 16; ++k) {
@@ -747,31 +748,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                               C::IDESC_S, k > 0 ? 1u : 0u);
               }
               mma_commit(&sfull[g]);
-              if (!tall || g == 1) mma_commit(&empty[ks]);
+              mma_commit(&empty[ks]);
+              if (i + 2 == n) mma_commit(qempty);  // the queries' last use
             }
           }
           __syncwarp();
-          // The piece's last S is issued: its queries may go.
-          if (g == 1 && i + 2 == na) commit(qempty);
         }
         if (!ok) break;
+        if (n == 0) {
+          if (elect_one()) mbar_arrive(qempty);
+          __syncwarp();
+        }
         piece_done();
       }
       // All products of this CTA are done before its TMEM is given back.
-      commit(drained);
+      if (elect_one()) mma_commit(drained);
+      __syncwarp();
       volatile uint32_t never = 0;
       wait_bounded(drained, 0, &never, kDrainTries);
       __syncwarp();
     } else {
       // ---------------------------------------------- values that some row does not see
       Ring<C::NST> at;
-      const int me = tid - 320;
       // Every stage is waited for and given back, looked at or not: a phase
       // that is skipped could be taken for another one.
       auto pass = [&](bool look) {
         wait(&full[at.st], at.ph);
         if (ok && look) {
-          clear_nonfinite<C::TILE_BYTES>(ring + at.st * C::TILE_BYTES, me, nonfinite);
+          clear_nonfinite<C::TILE_BYTES>(ring + at.st * C::TILE_BYTES, lane, nonfinite);
           mbar_arrive(&clean[at.st]);
         }
         __syncwarp();
@@ -780,17 +784,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
 #pragma unroll 1
       while (true) {
-        const Piece& t = piece();
+        const Piece t = piece();
         if (!ok || t.take == 0) break;
         const bool tall = t.tall;
-        const int na = t.a, nb = tall ? 0 : t.b;
-        // The stages' order is the producer's: two (or one) of keys first.
 #pragma unroll 1
-        for (int s = -2; ok && s < 2 * na; ++s) {
-          const int i = s >> 1, g = s & 1, n = g ? nb : na;
-          if (i >= n) continue;
-          if (i >= 0) pass(!t.all_seen(t.key_of(i, g)));
-          if (i + 1 < n) pass(false);
+        for (int s = tall ? -1 : -2; ok && s < (tall ? t.a : 2 * t.a); ++s) {
+          const int i = tall ? s : s >> 1, whose = tall ? 0 : s & 1;
+          const int all = whose ? t.b : t.a;
+          if (i >= all) continue;
+          if (i >= 0) pass(!t.all_seen(t.key_of(i, whose)));
+          if (i + 1 < all) pass(false);
         }
         piece_done();
       }
