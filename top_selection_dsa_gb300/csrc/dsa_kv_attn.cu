@@ -24,8 +24,8 @@
 // many short ones.
 //
 // Roles: warps 0-3 softmax of A, 4-7 of B, 8 TMA (queries, then a ring of key
-// and value tiles fetched page by page), 9 and 10 tcgen05.mma of A and of B, 11
-// the check of values that some row does not see.  S = Q K^T goes to TMEM; P overwrites it
+// and value tiles fetched page by page), 9 tcgen05.mma, 10 and 11
+// watch the ring.  S = Q K^T goes to TMEM; P overwrites it
 // as bf16 and is the A operand of O += P V straight from TMEM.  A row's
 // reference maximum is only moved, and O rescaled, when the maximum grows by
 // more than 2^8: P stays below 2^8 and sums are fp32, so nothing is lost.
@@ -49,8 +49,8 @@ namespace {
 
 constexpr int kTile = 128;    // keys of a tile, rows of a row tile
 constexpr int kThreads = 384;
-// Warps: 0-7 softmax, then these (an issuer for A, one for B).
-constexpr int kProducer = 8, kIssuer = 9, kCheck = 11;
+// Warps: 0-7 softmax, then these (two watchers).
+constexpr int kProducer = 8, kIssuer = 9, kWatch = 10;
 constexpr int kMaxStages = 12;
 // A row's weights of one tile add to no more than this, or its reference moves.
 constexpr float kMostSum = 65536.f;
@@ -345,21 +345,21 @@ struct Ring {
   }
 };
 
-// Zeroes the infinities and NaN of a tile in shared memory (one warp) and
+// Zeroes the infinities and NaN of a tile in shared memory (64 threads) and
 // says so in *flag.
 template <int BYTES>
 __device__ __forceinline__ void clear_nonfinite(uint8_t* tile, int me, volatile uint32_t* flag) {
   uint4* v = reinterpret_cast<uint4*>(tile);
   uint32_t top = 0;
 #pragma unroll 8
-  for (int k = me; k < BYTES / 16; k += 32) {
+  for (int k = me; k < BYTES / 16; k += 64) {
     const uint4 x = v[k];
     top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
                                  __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
   }
   if ((top & 0xFFFFu) < 0x7F80u && (top >> 16) < 0x7F80u) return;
   uint16_t* e = reinterpret_cast<uint16_t*>(v);
-  for (int k = me; k < BYTES / 16; k += 32)
+  for (int k = me; k < BYTES / 16; k += 64)
     for (int q = 0; q < 8; ++q)
       if ((e[8 * k + q] & 0x7F80u) == 0x7F80u) e[8 * k + q] = 0;
   *flag = 1;
@@ -468,7 +468,7 @@ struct AttnCfg {
   static constexpr int MISC = RING + NST * TILE_BYTES;
   static constexpr int XML = 0;                       // float2[2][128]
   static constexpr int BARS = 2048;
-  static constexpr int SLOT = BARS + 8 * (3 * kMaxStages + 12 + 2 * kPieces);
+  static constexpr int SLOT = BARS + 8 * (2 * kMaxStages + 12 + 2 * kPieces);
   static constexpr int PIECES = SLOT + 16;
   static constexpr int SMEM = MISC + (PIECES + kPieces * static_cast<int>(sizeof(Piece)) + 127) / 128 * 128;
   static constexpr uint32_t S_COL = 0, O_COL = 256;   // TMEM: S/P of A, of B; O of A, of B
@@ -488,11 +488,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   float2* xml = reinterpret_cast<float2*>(misc + C::XML);
   uint64_t* full = reinterpret_cast<uint64_t*>(misc + C::BARS);
   uint64_t* empty = full + kMaxStages;
-  uint64_t* clean = empty + kMaxStages;
-  uint64_t* qfull = clean + kMaxStages;
+  uint64_t* qfull = empty + kMaxStages;
   uint64_t* qempty = qfull + 1;
   uint64_t* sfull = qempty + 1;  // [2] S is in TMEM
-  uint64_t* pfull = sfull + 2;   // [2] P is in TMEM, O rescaled
+  uint64_t* pfull = sfull + 2;   // [2] P is in TMEM, O rescaled; the stages have arrived
   uint64_t* ofull = pfull + 2;   // [2] a piece's last product is done
   uint64_t* xbar = ofull + 2;    // [2] short pieces: sums exchanged; both outputs read
   uint64_t* drained = xbar + 2;
@@ -508,15 +507,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < C::NST; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 3);  // both groups' products, and the check
-      mbar_init(&clean[i], 32);
+      mbar_init(&empty[i], 3);  // the products, and both watchers
     }
     mbar_init(qfull, 1);
-    mbar_init(qempty, 2);
-    mbar_init(drained, 2);
+    mbar_init(qempty, 1);
+    mbar_init(drained, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfull[i], 1);
-      mbar_init(&pfull[i], 4);
+      mbar_init(&pfull[i], 6);  // four warps' weights, both watchers
       mbar_init(&ofull[i], 1);
       mbar_init(&xbar[i], 256);
     }
@@ -672,27 +670,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_bounded(qfull, static_cast<uint32_t>(queries - 1) & 1u, &never, kDrainTries);
       }
       __syncwarp();
-    } else if (warp < kCheck) {
-      // --------------------------------------------------- MMA issuers, one a group
-      // The products read shared memory at its full rate, and every barrier
-      // that a warp looks at then takes some 250 cycles: with a warp a group,
-      // one looks while the other's products run.  The whole warp walks, so
+    } else if (warp == kIssuer) {
+      // ----------------------------------------------------------- MMA issuer
+      // The products read shared memory at its full rate, and a look at a
+      // barrier then takes some 250 cycles, as long as the products still in
+      // the tensor core's queue.  So there is one look a step: pfull counts the
+      // weights and, from the watchers, the stages.  The whole warp walks, so
       // that descriptors are uniform values, and one lane issues: with one
       // lane's own values each instruction waited for its operands' way into
       // uniform registers, 107 cycles a product of 64.
-      const int g = warp - kIssuer;
       Ring<C::NST> at;
-      uint32_t pn = 0, qn = 0, cleaned = 0;  // parities of pfull, qfull and clean (a bit a stage)
+      uint32_t pn = 0, qn = 0;  // parities of pfull (a bit a group) and qfull
       const uint32_t q_addr = smem_u32(smem), r_addr = smem_u32(ring);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      const uint32_t st = tm + C::S_COL + g * 128, ot = tm + C::O_COL + g * D;
-      // The next stage; both issuers wait for each, and give back those of the
-      // other group alone at once.
-      auto take_stage = [&](bool mine) {
-        wait(&full[at.st], at.ph);
+      auto take_stage = [&]() {
         const int k = at.st;
         at.step();
-        if (!mine && ok && elect_one()) mbar_arrive(&empty[k]);
         return __shfl_sync(0xffffffffu, k, 0);
       };
 #pragma unroll 1
@@ -700,42 +693,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Piece t = piece();
         if (!ok || t.take == 0) break;
         const bool tall = t.tall;
-        const int n = g ? t.b : t.a;  // this group's key tiles
-        const uint32_t qa = q_addr + (tall ? g : 0) * C::TILE_BYTES;
+        int vs = 0, ks = 0;
         wait(qfull, qn);
         qn ^= 1u;
-        // Stages come as the values of a tile and the keys of its group's next
-        // one (before the first, only keys); tall: one tile for both groups.
+        // Step s: the product with the values of group g's tile i, then S of
+        // its next tile; before the first of each group only S.
 #pragma unroll 1
-        for (int s = tall ? -1 : -2; ok && s < (tall ? t.a : 2 * t.a); ++s) {
-          const int i = tall ? s : s >> 1, whose = tall ? g : s & 1;
-          const int all = whose ? t.b : t.a;
-          if (i >= all) continue;
-          const bool mine = whose == g, more = i + 1 < all;
-          int vs = 0, ks = 0;
-          if (i >= 0) {
-            vs = take_stage(mine);
-            if (__builtin_expect(!t.all_seen(t.key_of(i, whose)), 0)) {
-              if (mine) wait(&clean[vs], cleaned >> vs & 1u);
-              cleaned ^= 1u << vs;
-            }
+        for (int s = -2; ok && s < 2 * t.a; ++s) {
+          const int i = s >> 1, g = s & 1, n = g ? t.b : t.a;
+          if (i >= n) continue;
+          const bool more = i + 1 < n;
+          // Tall tiles: both groups share the stages.
+          if (!tall || g == 0) {
+            if (i < 0) wait(&full[at.st], at.ph);
+            if (i >= 0) vs = take_stage();
+            if (more) ks = take_stage();
           }
-          if (more) ks = take_stage(mine);
-          if (!mine) continue;
           if (i >= 0) {
-            wait(&pfull[g], pn);
-            pn ^= 1u;
+            wait(&pfull[g], pn >> g & 1u);
+            pn ^= 1u << g;
           }
           if (!ok) break;
           tc_fence_after_sync();
           const uint32_t va = r_addr + vs * C::TILE_BYTES, ka = r_addr + ks * C::TILE_BYTES;
+          const uint32_t qa = q_addr + (tall ? g : 0) * C::TILE_BYTES;
+          const uint32_t st = tm + C::S_COL + g * 128, ot = tm + C::O_COL + g * D;
           if (elect_one()) {
             if (i >= 0) {
 #pragma unroll
               for (int k = 0; k < kTile / 16; ++k)
                 mma_ts(ot, st + k * 8, sw128_nmajor_desc(va + k * 2048, C::HALF_BYTES), C::IDESC_O,
                        k > 0 || i > 0 ? 1u : 0u);
-              mma_commit(&empty[vs]);
+              if (!tall || g == 1) mma_commit(&empty[vs]);
               if (!more) mma_commit(&ofull[g]);
             }
             // S overwrites P: the tensor core takes one thread's products in
@@ -748,17 +737,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                               C::IDESC_S, k > 0 ? 1u : 0u);
               }
               mma_commit(&sfull[g]);
-              mma_commit(&empty[ks]);
-              if (i + 2 == n) mma_commit(qempty);  // the queries' last use
+              if (!tall || g == 1) mma_commit(&empty[ks]);
             }
+            // The piece's last S is issued: its queries may go.
+            if (g == (t.b == t.a ? 1 : 0) && i + 2 == t.a) mma_commit(qempty);
           }
           __syncwarp();
         }
         if (!ok) break;
-        if (n == 0) {
-          if (elect_one()) mbar_arrive(qempty);
-          __syncwarp();
-        }
         piece_done();
       }
       // All products of this CTA are done before its TMEM is given back.
@@ -768,16 +754,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait_bounded(drained, 0, &never, kDrainTries);
       __syncwarp();
     } else {
-      // ---------------------------------------------- values that some row does not see
+      // ------------------------------------------------------------- watchers
+      // They see every stage arrive, clear what some row must not see of the
+      // values in it, and tell the issuer when a step has its stages.
       Ring<C::NST> at;
-      // Every stage is waited for and given back, looked at or not: a phase
-      // that is skipped could be taken for another one.
+      uint32_t pn = 0, any = 0;  // parity of pfull's phase to come and whether there was one
+      const int me = tid - 32 * kWatch;
+      // A stage is given back beside the products' own return.
       auto pass = [&](bool look) {
         wait(&full[at.st], at.ph);
-        if (ok && look) {
-          clear_nonfinite<C::TILE_BYTES>(ring + at.st * C::TILE_BYTES, lane, nonfinite);
-          mbar_arrive(&clean[at.st]);
-        }
+        if (ok && look)
+          clear_nonfinite<C::TILE_BYTES>(ring + at.st * C::TILE_BYTES, me, nonfinite);
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(&empty[at.st]);
         at.step();
@@ -788,12 +775,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok || t.take == 0) break;
         const bool tall = t.tall;
 #pragma unroll 1
-        for (int s = tall ? -1 : -2; ok && s < (tall ? t.a : 2 * t.a); ++s) {
-          const int i = tall ? s : s >> 1, whose = tall ? 0 : s & 1;
-          const int all = whose ? t.b : t.a;
-          if (i >= all) continue;
-          if (i >= 0) pass(!t.all_seen(t.key_of(i, whose)));
-          if (i + 1 < all) pass(false);
+        for (int s = -2; ok && s < 2 * t.a; ++s) {
+          const int i = s >> 1, g = s & 1, n = g ? t.b : t.a;
+          if (i >= n) continue;
+          if (!tall || g == 0) {
+            if (i >= 0) pass(!t.all_seen(t.key_of(i, g)));
+            if (i + 1 < n) pass(false);
+          }
+          if (i < 0) continue;
+          // An arrival ahead of the step before would be counted with it.
+          if (any >> g & 1u) wait(&pfull[g], (pn >> g & 1u) ^ 1u);
+          if (ok && lane == 0) mbar_arrive(&pfull[g]);
+          any |= 1u << g;
+          pn ^= 1u << g;
         }
         piece_done();
       }
@@ -1023,7 +1017,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(
       return static_cast<int64_t>(k == 0 ? 2 * cta + 1 : 2 * (cta + k)) * p.slot_rows + row;
     };
     float top = -INFINITY;
-    for (int k = lane; k <= more; k += 32) top = fmaxf(top, p.part_ml[part(k)].x);
+    for (int k = lane; k <= more; k += 64) top = fmaxf(top, p.part_ml[part(k)].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     float sum = 0.f, acc[N] = {};
