@@ -24,8 +24,8 @@
 // many short ones.
 //
 // Roles: warps 0-3 softmax of A, 4-7 of B, 8 TMA (queries, then a ring of key
-// and value tiles fetched page by page), 9 tcgen05.mma, 10 and 11
-// watch the ring.  S = Q K^T goes to TMEM; P overwrites it
+// and value tiles fetched page by page), 9 and 10 tcgen05.mma
+// of A and of B, 11 watches the ring.  S = Q K^T goes to TMEM; P overwrites it
 // as bf16 and is the A operand of O += P V straight from TMEM.  A row's
 // reference maximum is only moved, and O rescaled, when the maximum grows by
 // more than 2^8: P stays below 2^8 and sums are fp32, so nothing is lost.
@@ -49,8 +49,8 @@ namespace {
 
 constexpr int kTile = 128;    // keys of a tile, rows of a row tile
 constexpr int kThreads = 384;
-// Warps: 0-7 softmax, then these (two watchers).
-constexpr int kProducer = 8, kIssuer = 9, kWatch = 10;
+// Warps: 0-7 softmax, then these (an issuer for A, one for B).
+constexpr int kProducer = 8, kIssuer = 9, kWatch = 11;
 constexpr int kMaxStages = 12;
 // A row's weights of one tile add to no more than this, or its reference moves.
 constexpr float kMostSum = 65536.f;
@@ -73,19 +73,23 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // A wait for the phase of `bar` with the given parity that gives up after
-// kMaxTries (of at least some 20 ns each, and more where the hardware suspends
-// the warp) or once another role did.  A try counter instead of a clock: its
-// code is a few instructions, and there is a copy at every wait.
-constexpr uint32_t kMaxTries = 1u << 24, kDrainTries = 1u << 20;
+// timeout_ns or once another role did.  mbar_wait_bounded reads the clock at its
+// first failure, which takes longer than most waits here.
+constexpr uint64_t kDrainNs = 100000000ull;
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity,
                                              volatile uint32_t* abort,
-                                             uint32_t tries = kMaxTries) {
+                                             uint64_t timeout_ns = kWaitTimeoutNs) {
+  uint64_t t0 = 0;
 #pragma unroll 1
-  for (uint32_t it = tries; it != 0; --it) {
+  for (uint32_t it = 1;; ++it) {
     if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
-    if ((it & 1023u) == 0 && *abort) return false;
+    if ((it & 255u) == 0) {
+      if (abort && *abort) return false;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > timeout_ns) return false;
+    }
   }
-  return false;
 }
 
 __device__ __forceinline__ void tma_load_box3(void* dst, const CUtensorMap* map, uint64_t* bar,
@@ -345,21 +349,21 @@ struct Ring {
   }
 };
 
-// Zeroes the infinities and NaN of a tile in shared memory (64 threads) and
+// Zeroes the infinities and NaN of a tile in shared memory (one warp) and
 // says so in *flag.
 template <int BYTES>
 __device__ __forceinline__ void clear_nonfinite(uint8_t* tile, int me, volatile uint32_t* flag) {
   uint4* v = reinterpret_cast<uint4*>(tile);
   uint32_t top = 0;
 #pragma unroll 8
-  for (int k = me; k < BYTES / 16; k += 64) {
+  for (int k = me; k < BYTES / 16; k += 32) {
     const uint4 x = v[k];
     top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
                                  __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
   }
   if ((top & 0xFFFFu) < 0x7F80u && (top >> 16) < 0x7F80u) return;
   uint16_t* e = reinterpret_cast<uint16_t*>(v);
-  for (int k = me; k < BYTES / 16; k += 64)
+  for (int k = me; k < BYTES / 16; k += 32)
     for (int q = 0; q < 8; ++q)
       if ((e[8 * k + q] & 0x7F80u) == 0x7F80u) e[8 * k + q] = 0;
   *flag = 1;
@@ -468,7 +472,7 @@ struct AttnCfg {
   static constexpr int MISC = RING + NST * TILE_BYTES;
   static constexpr int XML = 0;                       // float2[2][128]
   static constexpr int BARS = 2048;
-  static constexpr int SLOT = BARS + 8 * (2 * kMaxStages + 12 + 2 * kPieces);
+  static constexpr int SLOT = BARS + 8 * (2 * kMaxStages + 14 + 2 * kPieces);
   static constexpr int PIECES = SLOT + 16;
   static constexpr int SMEM = MISC + (PIECES + kPieces * static_cast<int>(sizeof(Piece)) + 127) / 128 * 128;
   static constexpr uint32_t S_COL = 0, O_COL = 256;   // TMEM: S/P of A, of B; O of A, of B
@@ -491,8 +495,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* qfull = empty + kMaxStages;
   uint64_t* qempty = qfull + 1;
   uint64_t* sfull = qempty + 1;  // [2] S is in TMEM
-  uint64_t* pfull = sfull + 2;   // [2] P is in TMEM, O rescaled; the stages have arrived
-  uint64_t* ofull = pfull + 2;   // [2] a piece's last product is done
+  uint64_t* pfull = sfull + 2;   // [2] P is in TMEM, O rescaled; the stages arrived, its turn
+  uint64_t* kfirst = pfull + 2;  // [2] the first keys of a piece have arrived
+  uint64_t* ofull = kfirst + 2;   // [2] a piece's last product is done
   uint64_t* xbar = ofull + 2;    // [2] short pieces: sums exchanged; both outputs read
   uint64_t* drained = xbar + 2;
   uint64_t* told = drained + 1;       // [kPieces] a piece is published
@@ -507,14 +512,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < C::NST; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 3);  // the products, and both watchers
+      mbar_init(&empty[i], 3);  // both issuers' products, and the watcher
     }
     mbar_init(qfull, 1);
-    mbar_init(qempty, 1);
-    mbar_init(drained, 1);
+    mbar_init(qempty, 2);
+    mbar_init(drained, 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfull[i], 1);
-      mbar_init(&pfull[i], 6);  // four warps' weights, both watchers
+      mbar_init(&pfull[i], 6);  // four warps' weights, the watcher, the turn
+      mbar_init(&kfirst[i], 1);
       mbar_init(&ofull[i], 1);
       mbar_init(&xbar[i], 256);
     }
@@ -662,27 +668,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok && lane == 0) {
         // Let the copies already in flight land before the CTA retires.
-        volatile uint32_t never = 0;
         for (int i = loads > C::NST ? loads - C::NST : 0; i < loads; ++i)
-          wait_bounded(&full[i % C::NST], static_cast<uint32_t>(i / C::NST) & 1u, &never,
-                            kDrainTries);
+          wait_bounded(&full[i % C::NST], static_cast<uint32_t>(i / C::NST) & 1u, nullptr,
+                            kDrainNs);
         if (queries > 0)
-          wait_bounded(qfull, static_cast<uint32_t>(queries - 1) & 1u, &never, kDrainTries);
+          wait_bounded(qfull, static_cast<uint32_t>(queries - 1) & 1u, nullptr, kDrainNs);
       }
       __syncwarp();
-    } else if (warp == kIssuer) {
-      // ----------------------------------------------------------- MMA issuer
+    } else if (warp < kWatch) {
+      // --------------------------------------------------- MMA issuers, one a group
       // The products read shared memory at its full rate, and a look at a
       // barrier then takes some 250 cycles, as long as the products still in
-      // the tensor core's queue.  So there is one look a step: pfull counts the
-      // weights and, from the watchers, the stages.  The whole warp walks, so
-      // that descriptors are uniform values, and one lane issues: with one
-      // lane's own values each instruction waited for its operands' way into
-      // uniform registers, 107 cycles a product of 64.
+      // the tensor core's queue.  So there is one look a step -- pfull counts
+      // the weights, the stages (from the watcher) and the turn (from the other
+      // issuer) -- and it is taken while the other group's products run.  Turns
+      // keep the groups half a step apart: the products of one beside the
+      // softmax of the other.  The whole warp walks, so that descriptors are
+      // uniform values, and one lane issues: with one lane's own values each
+      // instruction waited for its operands' way into uniform registers, 107
+      // cycles a product of 64.
+      const int g = warp - kIssuer;
       Ring<C::NST> at;
-      uint32_t pn = 0, qn = 0;  // parities of pfull (a bit a group) and qfull
+      uint32_t pn = 0, qn = 0, kn = 0;  // parities of pfull, qfull and kfirst
+      uint32_t an = 0;                  // B: of A's pfull
+      bool any = false;                 // B: whether that had a phase
       const uint32_t q_addr = smem_u32(smem), r_addr = smem_u32(ring);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t st = tm + C::S_COL + g * 128, ot = tm + C::O_COL + g * D;
       auto take_stage = [&]() {
         const int k = at.st;
         at.step();
@@ -693,78 +705,118 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Piece t = piece();
         if (!ok || t.take == 0) break;
         const bool tall = t.tall;
-        int vs = 0, ks = 0;
+        const int n = g ? t.b : t.a, other = g ? t.a : t.b;  // key tiles of both groups
+        const uint32_t qa = q_addr + (tall ? g : 0) * C::TILE_BYTES;
         wait(qfull, qn);
         qn ^= 1u;
-        // Step s: the product with the values of group g's tile i, then S of
-        // its next tile; before the first of each group only S.
+        // Step i: the product with the values of the group's tile i, then S of
+        // its next tile; before the first only S.  The stages of the other
+        // group's steps are passed by (tall: both use the same).
 #pragma unroll 1
-        for (int s = -2; ok && s < 2 * t.a; ++s) {
-          const int i = s >> 1, g = s & 1, n = g ? t.b : t.a;
-          if (i >= n) continue;
+        for (int i = n > 0 ? -1 : 0; ok && i < n; ++i) {
           const bool more = i + 1 < n;
-          // Tall tiles: both groups share the stages.
-          if (!tall || g == 0) {
-            if (i < 0) wait(&full[at.st], at.ph);
+          int vs = 0, ks = 0;
+          if (tall || g == 0) {
+            if (i >= 0) vs = take_stage();
+            if (more) ks = take_stage();
+            if (!tall && i < other) {
+              if (i >= 0) at.step();
+              if (i + 1 < other) at.step();
+            }
+          } else {
+            if (i >= 0) at.step();
+            if (i + 1 < other) at.step();
             if (i >= 0) vs = take_stage();
             if (more) ks = take_stage();
           }
-          if (i >= 0) {
-            wait(&pfull[g], pn >> g & 1u);
-            pn ^= 1u << g;
+          if (i < 0) {
+            wait(&kfirst[g], kn);
+            kn ^= 1u;
+          } else {
+            wait(&pfull[g], pn);
+            pn ^= 1u;
           }
           if (!ok) break;
           tc_fence_after_sync();
           const uint32_t va = r_addr + vs * C::TILE_BYTES, ka = r_addr + ks * C::TILE_BYTES;
-          const uint32_t qa = q_addr + (tall ? g : 0) * C::TILE_BYTES;
-          const uint32_t st = tm + C::S_COL + g * 128, ot = tm + C::O_COL + g * D;
+          // S overwrites P: the tensor core takes one thread's products in
+          // their order.
+          auto s_mma = [&](int from, int to) {
+#pragma unroll
+            for (int k = from; k < to; ++k) {
+              const uint32_t off = (k / 4) * C::HALF_BYTES + (k % 4) * 32;
+              mma_ss<false>(st, sw128_kmajor_desc(qa + off), sw128_kmajor_desc(ka + off),
+                            C::IDESC_S, k > 0 ? 1u : 0u);
+            }
+          };
           if (elect_one()) {
             if (i >= 0) {
 #pragma unroll
               for (int k = 0; k < kTile / 16; ++k)
                 mma_ts(ot, st + k * 8, sw128_nmajor_desc(va + k * 2048, C::HALF_BYTES), C::IDESC_O,
                        k > 0 || i > 0 ? 1u : 0u);
-              if (!tall || g == 1) mma_commit(&empty[vs]);
+              mma_commit(&empty[vs]);
+              if (!tall) mma_commit(&empty[vs]);  // for the other issuer
               if (!more) mma_commit(&ofull[g]);
             }
-            // S overwrites P: the tensor core takes one thread's products in
-            // their order.
+            if (more) s_mma(0, D / 32);
+            // The turn of B's same step, or of A's next.
+            if (g == 0 && i >= 0 && i < other) mbar_arrive(&pfull[1]);
+            if (g == 1 && i >= 0 && i + 1 < other) mbar_arrive(&pfull[0]);
             if (more) {
-#pragma unroll
-              for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = (k / 4) * C::HALF_BYTES + (k % 4) * 32;
-                mma_ss<false>(st, sw128_kmajor_desc(qa + off), sw128_kmajor_desc(ka + off),
-                              C::IDESC_S, k > 0 ? 1u : 0u);
-              }
+              s_mma(D / 32, D / 16);
               mma_commit(&sfull[g]);
-              if (!tall || g == 1) mma_commit(&empty[ks]);
+              mma_commit(&empty[ks]);
+              if (!tall) mma_commit(&empty[ks]);
+              if (i + 2 == n) mma_commit(qempty);  // the queries' last use
             }
-            // The piece's last S is issued: its queries may go.
-            if (g == (t.b == t.a ? 1 : 0) && i + 2 == t.a) mma_commit(qempty);
           }
           __syncwarp();
+          if (g == 1 && i < 0) {
+            // A's first turn; its last step of the piece before is awaited, that
+            // this is not counted there.
+            if (any) wait(&pfull[0], an ^ 1u);
+            if (ok && elect_one()) mbar_arrive(&pfull[0]);
+            __syncwarp();
+          }
         }
         if (!ok) break;
+        if (g == 1) {
+          if (n == 0) {
+            // No step of its own: the stages passed by, the queries given back,
+            // A's one turn.
+            at.step();
+            at.step();
+            if (any) wait(&pfull[0], an ^ 1u);
+            if (ok && elect_one()) {
+              mbar_arrive(qempty);
+              mbar_arrive(&pfull[0]);
+            }
+            __syncwarp();
+          } else if (!tall && n < other) {
+            at.step();  // A's last values
+          }
+          any = true;
+          an ^= other & 1u;
+        }
         piece_done();
       }
       // All products of this CTA are done before its TMEM is given back.
       if (elect_one()) mma_commit(drained);
       __syncwarp();
-      volatile uint32_t never = 0;
-      wait_bounded(drained, 0, &never, kDrainTries);
+      wait_bounded(drained, 0, nullptr, kDrainNs);
       __syncwarp();
     } else {
-      // ------------------------------------------------------------- watchers
-      // They see every stage arrive, clear what some row must not see of the
-      // values in it, and tell the issuer when a step has its stages.
+      // -------------------------------------------------------------- watcher
+      // It sees every stage arrive, clears what some row must not see of the
+      // values in it, and tells the issuers when a step has its stages.
       Ring<C::NST> at;
-      uint32_t pn = 0, any = 0;  // parity of pfull's phase to come and whether there was one
-      const int me = tid - 32 * kWatch;
+      uint32_t pn = 0, any = 0;  // a bit a group: parity of pfull's phase to come, was there one
       // A stage is given back beside the products' own return.
       auto pass = [&](bool look) {
         wait(&full[at.st], at.ph);
         if (ok && look)
-          clear_nonfinite<C::TILE_BYTES>(ring + at.st * C::TILE_BYTES, me, nonfinite);
+          clear_nonfinite<C::TILE_BYTES>(ring + at.st * C::TILE_BYTES, lane, nonfinite);
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(&empty[at.st]);
         at.step();
@@ -782,9 +834,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i >= 0) pass(!t.all_seen(t.key_of(i, g)));
             if (i + 1 < n) pass(false);
           }
-          if (i < 0) continue;
           // An arrival ahead of the step before would be counted with it.
           if (any >> g & 1u) wait(&pfull[g], (pn >> g & 1u) ^ 1u);
+          if (i < 0) {
+            if (ok && n > 0 && lane == 0) mbar_arrive(&kfirst[g]);
+            continue;
+          }
           if (ok && lane == 0) mbar_arrive(&pfull[g]);
           any |= 1u << g;
           pn ^= 1u << g;
@@ -1017,7 +1072,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(
       return static_cast<int64_t>(k == 0 ? 2 * cta + 1 : 2 * (cta + k)) * p.slot_rows + row;
     };
     float top = -INFINITY;
-    for (int k = lane; k <= more; k += 64) top = fmaxf(top, p.part_ml[part(k)].x);
+    for (int k = lane; k <= more; k += 32) top = fmaxf(top, p.part_ml[part(k)].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     float sum = 0.f, acc[N] = {};
