@@ -876,25 +876,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         if (busy) {
           tc_fence_after_sync();
-          uint32_t s[4][32];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) tmem_ld32_async(s_addr + 32 * k, s[k]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) tmem_wait_ld(s[k]);
-          if (__builtin_expect(masked, 0)) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t word = see.word(k);
-#pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (!(word >> c & 1u)) s[k][c] = 0xFF800000u;
-            }
-          }
-          // Weights by the present reference, in place of S.
+          // Weights by the present reference.  S stays in TMEM until they serve,
+          // so that registers hold it only up to its exponential: kept beside
+          // them for a second try, it took the exponentials their overlap (1250
+          // cycles a tile, against 720).
+          uint32_t pk[4][16];
           float add = 0.f;
           bool fresh = i == 0;
 #pragma unroll 1
           while (true) {
+            uint32_t s[4][32];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tmem_ld32_async(s_addr + 32 * k, s[k]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tmem_wait_ld(s[k]);
+            if (__builtin_expect(masked, 0)) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t word = see.word(k);
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (!(word >> c & 1u)) s[k][c] = 0xFF800000u;
+              }
+            }
             if (__builtin_expect(fresh, 0)) {
               float mx[8];
 #pragma unroll
@@ -927,7 +931,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              uint32_t pk[16];
 #pragma unroll
               for (int c = 0; c < 32; c += 2) {
                 const float2 x = __ffma2_rn(
@@ -935,9 +938,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float2 e = make_float2(ex2(x.x), ex2(x.y));
                 sum[c >> 1 & 1] = __fadd2_rn(sum[c >> 1 & 1], e);
                 const __nv_bfloat162 y = __floats2bfloat162_rn(e.x, e.y);
-                pk[c >> 1] = *reinterpret_cast<const uint32_t*>(&y);
+                pk[k][c >> 1] = *reinterpret_cast<const uint32_t*>(&y);
               }
-              tmem_st16(s_addr + 16 * k, pk);
             }
             const float2 both = __fadd2_rn(sum[0], sum[1]);
             add = both.x + both.y;
@@ -948,6 +950,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             fresh = true;
           }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tmem_st16(s_addr + 16 * k, pk[k]);
           l += add;
           tmem_wait_st();
           tc_fence_before_sync();
