@@ -212,7 +212,7 @@ struct Piece {
   }
 };
 constexpr int kPieces = 4;    // published ahead
-constexpr int kTileCost = 2;  // units that a tile's start and end take (about 8000 cycles)
+constexpr int kTileCost = 4;  // units that a tile's start and end take (about 11000 cycles)
 
 // A CTA's run of the work and where it stands.
 struct Walk {
@@ -434,26 +434,43 @@ __device__ __noinline__ void add_nonfinite(const KvAttnParams& p, const Piece& t
   }
 }
 
-// N elements of an output row: bf16 to `out`, or fp32 to a part.
+// 32 bytes to one row.  A warp's lanes write 32 rows, so that a store costs the
+// same whatever its width: half as many of these as of 16 bytes.
+__device__ __forceinline__ void store32(void* to, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// N elements of an output row times f: bf16 to `out` (16-byte aligned, `wide`: 32),
+// or fp32 to a part.
 template <int N>
-__device__ __forceinline__ void store_out(uint16_t* out, const float (&o)[N], float f) {
+__device__ __forceinline__ void store_out(uint16_t* out, const float (&o)[N], float f, bool wide) {
 #pragma unroll
-  for (int i = 0; i < N; i += 8) {
-    uint32_t v[4];
+  for (int i = 0; i < N; i += 16) {
+    uint32_t v[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 8; ++k) {
       const __nv_bfloat162 x = __floats2bfloat162_rn(o[i + 2 * k] * f, o[i + 2 * k + 1] * f);
       v[k] = *reinterpret_cast<const uint32_t*>(&x);
     }
-    *reinterpret_cast<uint4*>(out + i) = make_uint4(v[0], v[1], v[2], v[3]);
+    if (wide) {
+      store32(out + i, v);
+    } else {
+      *reinterpret_cast<uint4*>(out + i) = make_uint4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<uint4*>(out + i + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+    }
   }
 }
 template <int N>
 __device__ __forceinline__ void store_part(float* out, const float (&o)[N], float f) {
 #pragma unroll
-  for (int i = 0; i < N; i += 4)
-    *reinterpret_cast<float4*>(out + i) =
-        make_float4(o[i] * f, o[i + 1] * f, o[i + 2] * f, o[i + 3] * f);
+  for (int i = 0; i < N; i += 8) {
+    uint32_t v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[i + k] * f);
+    store32(out + i, v);
+  }
 }
 
 __device__ __forceinline__ float lse_of(float m2, float l) {
@@ -1038,6 +1055,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float f = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
       const bool second = !t.tall && t.b > 0;
+      const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
       if (busy) {
 #pragma unroll 1
         for (int d = d0; d < d1; d += 32) {
@@ -1051,7 +1069,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (mine) {
             if (whole)
-              store_out(p.out + at * D + d, o, second ? f : f * fa);
+              store_out(p.out + at * D + d, o, second ? f : f * fa, wide);
             else
               store_part(p.part_o + part * D + d, o, second ? 1.f : fa);
           }
