@@ -661,7 +661,8 @@ dsa_status_t dsa_kv_append(const void* k, int64_t k_stride, const void* v, int64
  *   softmax_scale in [2^-64, 2^64]
  *   window        0: none; else a token sees that many keys, itself among them
  *   sink          the first keys that stay visible behind the window
- *   out           [T, Hq, D] bf16 dense, 16-byte aligned
+ *   out           [T, Hq, D] bf16 dense, 16-byte aligned (32 is faster); apart
+ *                 from the inputs
  *   lse           [T, Hq] fp32 (natural logarithm) or NULL
  *   workspace     dsa_kv_attention_workspace_bytes(T, Hq, Hkv, D) bytes (for the
  *                 current device), 256-byte aligned.  Calls that may overlap
@@ -671,8 +672,9 @@ dsa_status_t dsa_kv_append(const void* k, int64_t k_stride, const void* v, int64
  *   128 keys of the longest context pass 2^31)
  * Products run on the tensor cores on the bf16 inputs with fp32 accumulation;
  * the weights exp(S - max) are rounded to bf16 for the second one (2^-8 relative),
- * their sum and the maximum are fp32.  Every sum runs in one fixed order: results
- * are the same from call to call.
+ * their sum and the maximum are fp32.  A row's weights are divided by their sum at
+ * the end: sums of values beyond 2^90 may pass fp32's range.  Every sum runs in one
+ * fixed order: results are the same from call to call.
  */
 dsa_status_t dsa_kv_attention(const void* q, int64_t q_stride, const void* k_cache,
                               const void* v_cache, int num_blocks, const int32_t* block_table,
@@ -759,7 +761,7 @@ const char* dsa_status_string(dsa_status_t status);
  * kernel's bounded wait gave up since the last call, DSA_ERR_INVALID_ARG when
  * a paged call met a block id or context length out of range (or
  * dsa_topk_sort_by_score an index outside its row, or
- * dsa_k_norm_quant_insert a slot past the cache; the key/value cache's calls
+ * dsa_k_norm_quant_insert a slot past the cache; the key/value caches' calls
  * likewise), DSA_ERR_CUDA
  * when the synchronisation itself failed, else DSA_OK.
  */

@@ -554,9 +554,14 @@ def _need_all(dev, specs):
 _NO_GUARD = contextlib.nullcontext()
 
 
+# The current device without the check that CUDA is initialised: a CUDA tensor is
+# at hand wherever this is asked.
+_device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _on(dev):
     """The device of a call made current (a no-op when it is)."""
-    return _NO_GUARD if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    return _NO_GUARD if _device_now() == dev.index else torch.cuda.device(dev)
 
 
 def _addr(t):
