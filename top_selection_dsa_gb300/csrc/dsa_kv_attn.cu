@@ -236,6 +236,15 @@ struct Walk {
   }
 };
 
+// a * b / c, rounded down: 32-bit arithmetic where it serves (a 64-bit
+// division takes some 400 cycles).
+__device__ __forceinline__ int64_t muldiv(int64_t a, int64_t b, int64_t c) {
+  const uint64_t ab = static_cast<uint64_t>(a * b);
+  if ((ab | static_cast<uint64_t>(c)) >> 32 == 0)
+    return static_cast<uint32_t>(ab) / static_cast<uint32_t>(c);
+  return static_cast<int64_t>(ab / static_cast<uint64_t>(c));
+}
+
 // What a tile counts in the division of the work: its units, and what starting
 // and ending it costs in units (queries, the first logits, the outputs), as if
 // that came first.
@@ -298,9 +307,9 @@ __device__ Walk find_run(const KvAttnParams& p, int* pfx) {
   Walk w = {};
   w.total = total;
   if (warp == kProducer && static_cast<int64_t>(blockIdx.x) < ctas) {
-    const int64_t u0 = blockIdx.x * total / ctas;
-    w.left = (blockIdx.x + 1) * total / ctas - u0;
-    w.h = static_cast<int>(u0 / U);
+    const int64_t u0 = muldiv(blockIdx.x, total, ctas);
+    w.left = muldiv(blockIdx.x + 1, total, ctas) - u0;
+    w.h = static_cast<int>(muldiv(u0, 1, U));
     int at = static_cast<int>(u0 - static_cast<int64_t>(w.h) * U);
     int lo = 0, hi = p.B;  // the request: pfx[lo] <= at < pfx[lo + 1]
 #pragma unroll 1
@@ -617,9 +626,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             w.next(p, taken);
             continue;
           }
-          const int64_t ctas = min(static_cast<int64_t>(gridDim.x), w.total);
-          // CTA c has the cost from floor(c total / ctas) on: who has the tile's end.
-          const int64_t end = (blockIdx.x + 1) * w.total / ctas - w.left - w.at + cost;
           t.tok0 = tile.tok0;
           t.ntok = tile.ntok;
           t.p0 = tile.p0;
@@ -637,7 +643,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           t.req = w.r.b;
           t.L = w.r.L;
           t.whole = t.j == 0 && t.take == tile.units;
-          t.more = static_cast<int>((end * ctas - 1) / w.total) - static_cast<int>(blockIdx.x);
+          if (t.j == 0 && !t.whole) {
+            // CTA c has the cost from floor(c total / ctas) on: who has the tile's end.
+            const int64_t ctas = min(static_cast<int64_t>(gridDim.x), w.total);
+            const int64_t end = muldiv(blockIdx.x + 1, w.total, ctas) - w.left - w.at + cost;
+            t.more = static_cast<int>(muldiv(end * ctas - 1, 1, w.total)) -
+                     static_cast<int>(blockIdx.x);
+          }
           break;
         }
         if (lane == 0) {
@@ -1136,27 +1148,43 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(
     auto part = [&](int k) {
       return static_cast<int64_t>(k == 0 ? 2 * cta + 1 : 2 * (cta + k)) * p.slot_rows + row;
     };
-    float top = -INFINITY;
-    for (int k = lane; k <= more; k += 32) top = fmaxf(top, p.part_ml[part(k)].x);
+    // Parts four at a time, one running maximum: a part's sum and values are
+    // read together.
+    float top = -INFINITY, sum = 0.f, acc[N] = {};
+#pragma unroll 1
+    for (int k0 = 0; k0 <= more; k0 += 4) {
+      float2 ml[4];
+      float v[4][N];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float sum = 0.f, acc[N] = {};
-#pragma unroll 4
-    for (int k = 0; k <= more; ++k) {
-      const int64_t at = part(k);
-      const float2 ml = p.part_ml[at];
-      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-      sum = fmaf(ml.y, f, sum);
-      float v[N];
-      if constexpr (N == 4) {
-        const float4 x = reinterpret_cast<const float4*>(p.part_o + at * D)[lane];
-        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-      } else {
-        const float2 x = reinterpret_cast<const float2*>(p.part_o + at * D)[lane];
-        v[0] = x.x; v[1] = x.y;
+      for (int k = 0; k < 4; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int q = 0; q < N; ++q) v[k][q] = 0.f;
+        if (k0 + k > more) continue;
+        const int64_t at = part(k0 + k);
+        ml[k] = p.part_ml[at];
+        if constexpr (N == 4) {
+          const float4 x = reinterpret_cast<const float4*>(p.part_o + at * D)[lane];
+          v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
+        } else {
+          const float2 x = reinterpret_cast<const float2*>(p.part_o + at * D)[lane];
+          v[k][0] = x.x; v[k][1] = x.y;
+        }
       }
+      const float was = top;
 #pragma unroll
-      for (int q = 0; q < N; ++q) acc[q] = f == 0.f ? acc[q] : fmaf(v[q], f, acc[q]);
+      for (int k = 0; k < 4; ++k) top = fmaxf(top, ml[k].x);
+      const float keep = was == -INFINITY ? 0.f : ex2(was - top);
+      sum *= keep;
+#pragma unroll
+      for (int q = 0; q < N; ++q) acc[q] = keep == 0.f ? 0.f : acc[q] * keep;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float f = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - top);
+        sum = fmaf(ml[k].y, f, sum);
+#pragma unroll
+        for (int q = 0; q < N; ++q) acc[q] = f == 0.f ? acc[q] : fmaf(v[k][q], f, acc[q]);
+      }
     }
     const float f = sum == 0.f ? 0.f : 1.f / sum;
     const int64_t at = static_cast<int64_t>(note.x + tok) * p.Hq + note.z * p.G + g;
