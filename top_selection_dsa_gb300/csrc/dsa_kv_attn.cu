@@ -40,6 +40,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "dsa_common.cuh"
 #include "dsa_internal.h"
@@ -1148,19 +1149,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(
     auto part = [&](int k) {
       return static_cast<int64_t>(k == 0 ? 2 * cta + 1 : 2 * (cta + k)) * p.slot_rows + row;
     };
-    // Parts four at a time, one running maximum: a part's sum and values are
+    // Parts k0 .. k0 + K - 1, one running maximum: their sums and values are
     // read together.
     float top = -INFINITY, sum = 0.f, acc[N] = {};
-#pragma unroll 1
-    for (int k0 = 0; k0 <= more; k0 += 4) {
-      float2 ml[4];
-      float v[4][N];
+    auto add = [&](auto count, int k0) {
+      constexpr int K = decltype(count)::value;
+      float2 ml[K];
+      float v[K][N];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < K; ++k) {
         ml[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
         for (int q = 0; q < N; ++q) v[k][q] = 0.f;
-        if (k0 + k > more) continue;
+        if (K > 2 && k0 + k > more) continue;
         const int64_t at = part(k0 + k);
         ml[k] = p.part_ml[at];
         if constexpr (N == 4) {
@@ -1173,18 +1174,24 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(
       }
       const float was = top;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) top = fmaxf(top, ml[k].x);
+      for (int k = 0; k < K; ++k) top = fmaxf(top, ml[k].x);
       const float keep = was == -INFINITY ? 0.f : ex2(was - top);
       sum *= keep;
 #pragma unroll
       for (int q = 0; q < N; ++q) acc[q] = keep == 0.f ? 0.f : acc[q] * keep;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < K; ++k) {
         const float f = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - top);
         sum = fmaf(ml[k].y, f, sum);
 #pragma unroll
         for (int q = 0; q < N; ++q) acc[q] = f == 0.f ? acc[q] : fmaf(v[k][q], f, acc[q]);
       }
+    };
+    if (more == 1) {  // most rows of prompts
+      add(std::integral_constant<int, 2>(), 0);
+    } else {
+#pragma unroll 1
+      for (int k0 = 0; k0 <= more; k0 += 4) add(std::integral_constant<int, 4>(), k0);
     }
     const float f = sum == 0.f ? 0.f : 1.f / sum;
     const int64_t at = static_cast<int64_t>(note.x + tok) * p.Hq + note.z * p.G + g;
