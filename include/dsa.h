@@ -611,7 +611,7 @@ size_t dsa_kv4_attention_workspace_bytes(int B, int next_n, int Hq, int Hkv, int
  *   q_weight, k_weight  [D] fp32, or NULL: that side is not normalised
  *   q_out, k_out  [T, H, D] dense, 16-byte aligned; may be q or k where those
  *                 are dense
- *   Hq, Hk <= 4096 (else DSA_ERR_UNSUPPORTED)
+ *   Hq, Hk <= 4096, T < 2^30 (else DSA_ERR_UNSUPPORTED)
  */
 dsa_status_t dsa_qk_norm_rope(const void* q, int64_t q_stride, int Hq, const void* k,
                               int64_t k_stride, int Hk, int T, int D, const int32_t* positions,
@@ -657,7 +657,8 @@ dsa_status_t dsa_kv_append(const void* k, int64_t k_stride, const void* v, int64
  *                 new tokens: bad entries as in dsa_indexer_logits_paged (block
  *                 0 in their place, lengths clamped, both recorded)
  *   query_starts  [B + 1] int32, ascending, in [0, T]: entries outside or
- *                 descending are clamped and recorded alike
+ *                 descending are clamped and recorded alike (nothing is
+ *                 computed where requests then overlap to more than T tokens)
  *   softmax_scale in [2^-64, 2^64]
  *   window        0: none; else a token sees that many keys, itself among them
  *   sink          the first keys that stay visible behind the window

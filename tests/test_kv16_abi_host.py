@@ -40,7 +40,8 @@ def test_norm_rope_refusals(api):
                 dict(turns=NUL), dict(pos=M2), dict(turns=M4), dict(qw=M2), dict(kw=M2),
                 dict(eps=-1.0), dict(eps=NAN), dict(eps=INF), dict(m=INF), dict(m=NAN)):
         assert rope(api, **bad) == E, bad
-    for bad in (dict(D=96), dict(D=256), dict(R=8), dict(R=120), dict(Hq=5000, qs=5000 * 128)):
+    for bad in (dict(D=96), dict(D=256), dict(R=8), dict(R=120), dict(Hq=5000, qs=5000 * 128),
+                dict(T=1 << 30)):
         assert rope(api, **bad) == U, bad
     assert rope(api, T=0) == api.DSA_OK
     assert rope(api, T=0, k=NUL, ko=NUL, Hk=0, kw=NUL) == api.DSA_OK
@@ -63,7 +64,7 @@ def test_append_refusals(api):
                 dict(eps=-1.0), dict(m=INF)):
         assert append(api, **bad) == E, bad
     for bad in (dict(D=96), dict(bs=4), dict(bs=48), dict(bs=256), dict(nb=1 << 25, bs=64),
-                dict(R=24)):
+                dict(R=24), dict(T=1 << 30)):
         assert append(api, **bad) == U, bad
     assert append(api, T=0) == api.DSA_OK
     assert append(api, T=0, q=NUL, qo=NUL, qw=NUL, Hq=0) == api.DSA_OK

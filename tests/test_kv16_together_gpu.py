@@ -113,3 +113,14 @@ def test_outputs_of_any_16_byte_alignment(api):
     lse = torch.empty(43, 8, device="cuda")
     call(api, s, out=out, lse=lse)
     check(s, out, lse)
+
+
+def test_requests_that_overlap_compute_nothing(api):
+    """Starts that go back and forth name more tokens than there are."""
+    s = make([1] * 40, [100] * 40, 8, 2, 128, 64, seed=8)
+    s["starts_d"].copy_(torch.tensor([0, 40] * 20 + [0]))
+    out = torch.full_like(s["q"], 7.0)
+    lse = torch.full(s["q"].shape[:2], 7.0, device="cuda")
+    call(api, s, out=out, lse=lse)
+    assert api.last_device_error() == api.DSA_ERR_INVALID_ARG
+    assert (out == 7).all() and (lse == 7).all()

@@ -71,7 +71,7 @@ dsa_status_t dsa_qk_norm_rope(const void* q, int64_t q_stride, int Hq, const voi
   dsa_status_t st =
       check_rotation(positions, turns, rotary, rope_scale, q_weight, k_weight, eps, D);
   if (st != DSA_OK) return st;
-  if (Hq > 4096 || Hk > 4096) return DSA_ERR_UNSUPPORTED;
+  if (Hq > 4096 || Hk > 4096 || T >= (1 << 30)) return DSA_ERR_UNSUPPORTED;
   if (T == 0) return DSA_OK;
   RopeParams p = {};
   p.q = static_cast<const uint16_t*>(q);
@@ -111,7 +111,7 @@ dsa_status_t dsa_kv_append(const void* k, int64_t k_stride, const void* v, int64
   if (q && (bad_rows(q, q_stride, T, Hq, D) || !aligned(q_out, 16))) return DSA_ERR_INVALID_ARG;
   st = check_rotation(positions, turns, rotary, rope_scale, q_weight, k_weight, eps, D);
   if (st != DSA_OK) return st;
-  if (Hq > 4096 || Hkv > 4096) return DSA_ERR_UNSUPPORTED;
+  if (Hq > 4096 || Hkv > 4096 || T >= (1 << 30)) return DSA_ERR_UNSUPPORTED;
   if (T == 0) return DSA_OK;
   RopeParams p = {};
   p.q = static_cast<const uint16_t*>(q);

@@ -17,20 +17,32 @@
 //
 // Work.  A unit is one tile of 128 keys (tall) or two (short).  The units of
 // all heads, requests and row tiles, in that order, and what each tile costs
-// besides, are cut into equal runs, one for each CTA; a tile that a cut goes through leaves its parts (maximum,
-// sum, unscaled output, all fp32) in the workspace, and a second kernel joins
-// them in their fixed order.  Lengths are read on the device, so a captured
-// graph serves every step, and one long request fills the GPU as evenly as
-// many short ones.
+// besides, are cut into equal runs, one for each CTA; a tile that a cut goes
+// through leaves its parts (reference, sum, unscaled output, all fp32) in the
+// workspace, and a second kernel joins them in their fixed order.  Lengths are
+// read on the device, so a captured graph serves every step, and one long
+// request fills the GPU as evenly as many short ones.
 //
 // Roles: warps 0-3 softmax of A, 4-7 of B, 8 TMA (queries, then a ring of key
-// and value tiles fetched page by page), 9 and 10 tcgen05.mma
-// of A and of B, 11 watches the ring.  S = Q K^T goes to TMEM; P overwrites it
-// as bf16 and is the A operand of O += P V straight from TMEM.  A row's
-// reference maximum is only moved, and O rescaled, when the maximum grows by
-// more than 2^8: P stays below 2^8 and sums are fp32, so nothing is lost.
-// P is rounded to bf16 (2^-8 relative each, on average below what the output's own
-// rounding adds once a few weights are summed); all else is fp32.
+// and value tiles fetched page by page), 9 and 10 tcgen05.mma of A and of B, 11
+// watches the ring.  S = Q K^T goes to TMEM; P overwrites it as bf16 and is the A
+// operand of O += P V straight from TMEM.  Weights are relative to a reference
+// that is a row's maximum at first and only moves, with O rescaled, when a tile's
+// weights add to more than 2^16: no tile but the first needs a maximum, and fp32
+// sums lose nothing by it.  P is rounded to bf16, 2^-8 relative each (the error of
+// the output's own rounding over again: 0.0017 becomes 0.0023 of its size); all
+// else is fp32.
+//
+// What bounds it (times at 64 query heads on 8 of 128, measured copy bandwidth
+// 6672 GB/s, bf16 products 1964 TFLOP/s, 1735 sustained):
+//   single tokens   memory: 64 contexts of 4096 to 131072 keys, 9.6 GB, 1.31 ms,
+//                   7.3 TB/s; one of 131071 90 us, 5.9 TB/s with its start and join
+//   prompts         a row tile's chain of product, softmax and product, about 2900
+//                   cycles a unit where the products alone take 2060 (S reads
+//                   both operands from shared memory at its full rate): 8192
+//                   tokens 0.78 ms, 1.41 PFLOP/s; 2048 in 65536 2.9 to 3.2 ms,
+//                   1.34 to 1.5, where power caps the clock
+//   in between      what starts and ends a tile, about 11000 cycles
 //
 // Values that a row does not see never reach it, whatever they hold: in tiles
 // that are not wholly seen, infinities and NaN among the values are replaced
@@ -260,9 +272,11 @@ __device__ Walk find_run(const KvAttnParams& p, int* pfx) {
   // Requests of few row tiles are summed by a thread each, others by a warp.
   constexpr int kFew = 4;
   uint32_t* err = blockIdx.x == 0 ? p.err : nullptr;
+  int descends = 0;
 #pragma unroll 1
   for (int b = tid; b < p.B; b += kThreads) {
     const Req r = req_of(p, b, err);
+    descends |= __ldg(p.starts + b + 1) < __ldg(p.starts + b);
     const int nt = tiles_of(p, r);
     int u = -1;
     if (nt <= kFew) {
@@ -272,7 +286,7 @@ __device__ Walk find_run(const KvAttnParams& p, int* pfx) {
     }
     pfx[b + 1] = u;
   }
-  __syncthreads();
+  descends = __syncthreads_or(descends);
 #pragma unroll 1
   for (int b = warp; b < p.B; b += kThreads / 32) {
     if (pfx[b + 1] >= 0) continue;
@@ -302,7 +316,14 @@ __device__ Walk find_run(const KvAttnParams& p, int* pfx) {
     }
   }
   __syncthreads();
-  const int U = pfx[p.B];
+  int U = pfx[p.B];
+  if (descends) {
+    // Requests that overlap can be more work than 32 bits count: none then.
+    int64_t tokens = 0;
+#pragma unroll 1
+    for (int b = 0; b < p.B; ++b) tokens += req_of(p, b).n;
+    if (tokens > p.T) U = 0;
+  }
   const int64_t total = static_cast<int64_t>(U) * p.Hkv;
   const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
   Walk w = {};
@@ -427,8 +448,8 @@ __device__ __noinline__ void add_nonfinite(const KvAttnParams& p, const Piece& t
     for (int c = 0; c < kTile; ++c) {
       if (!s.sees(c)) continue;
       const int key = kt * kTile + c;
-      const int64_t row = ((static_cast<int64_t>(page_of(p, entry_of(p, t.req, t.L, key))) * p.Hkv + t.h) << p.log_bs) +
-                          (key & ((1 << p.log_bs) - 1));
+      const int64_t page = page_of(p, entry_of(p, t.req, t.L, key));
+      const int64_t row = ((page * p.Hkv + t.h) << p.log_bs) + (key & ((1 << p.log_bs) - 1));
 #pragma unroll 1
       for (int d = d0; d < d0 + n; ++d) {
         const uint32_t x = p.v[row * D + d];
@@ -501,7 +522,8 @@ struct AttnCfg {
   static constexpr int BARS = 2048;
   static constexpr int SLOT = BARS + 8 * (2 * kMaxStages + 14 + 2 * kPieces);
   static constexpr int PIECES = SLOT + 16;
-  static constexpr int SMEM = MISC + (PIECES + kPieces * static_cast<int>(sizeof(Piece)) + 127) / 128 * 128;
+  static constexpr int END = PIECES + kPieces * static_cast<int>(sizeof(Piece));
+  static constexpr int SMEM = MISC + (END + 127) / 128 * 128;
   static constexpr uint32_t S_COL = 0, O_COL = 256;   // TMEM: S/P of A, of B; O of A, of B
   static constexpr uint32_t IDESC_S = mma_idesc(1u, 128, 128);
   static constexpr uint32_t IDESC_O = mma_idesc(1u, 128, D) | (1u << 16);  // V: N-major
@@ -601,7 +623,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // of B (tall: A alone).  Returns whether there is such a tile.
       auto entries = [&](const Piece& t, int i, int (&e)[2]) {
         const int g = lane_tile >> 1, k = i + (lane_tile & 1);
-        const bool here = k >= 0 && k < (g ? (t.tall ? 0 : t.b) : t.a) && (i >= 0 || (lane_tile & 1));
+        const bool here = k >= 0 && k < (g ? (t.tall ? 0 : t.b) : t.a) &&
+                          (i >= 0 || (lane_tile & 1));
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const int page = (lane & 7) + 8 * q;
@@ -1259,7 +1282,8 @@ KvAttnPlan kv_attn_plan(int T, int G, int D) {
 }
 
 int64_t kv_attn_units(int T, int B, int G, int64_t max_ctx) {
-  return (static_cast<int64_t>(T) / (2 * (kTile / G)) + B) * ((max_ctx + kTile - 1) / kTile + 1 + kTileCost);
+  return (static_cast<int64_t>(T) / (2 * (kTile / G)) + B) *
+         ((max_ctx + kTile - 1) / kTile + 1 + kTileCost);
 }
 
 cudaError_t launch_kv_attention(const KvAttnParams& p, int D, cudaStream_t s) {
