@@ -800,20 +800,14 @@ def rope_turns(freq, device="cuda"):
     return torch.tensor(turns, dtype=torch.int64, device=device)
 
 
-def _rotation(dev, T, D, positions, turns, q_weight, k_weight):
-    """Checks of the rotation's tensors; how many elements are rotated."""
-    if q_weight is not None or k_weight is not None:
-        _need_all(dev, ((q_weight, "q_weight", torch.float32),
-                        (k_weight, "k_weight", torch.float32)))
-        _shape(q_weight, "q_weight", (D,))
-        _shape(k_weight, "k_weight", (D,))
-    if turns is None and positions is None:
-        return 0
-    if positions is None or turns is None:
-        raise ValueError("positions and turns go together")
-    _need_all(dev, ((positions, "positions", torch.int32), (turns, "turns", torch.int64)))
-    _shape(positions, "positions", (T,))
-    return 2 * turns.numel()
+# The 16-bit cache's calls run once a layer and step as well: one expression sees
+# whether everything is as it should be, and only where it is not (or a case that
+# it leaves out) the checks above are gone through, which name what is wrong.
+_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+
+
+def _dense(t, dtype, index):
+    return t is None or (t.dtype is dtype and t.get_device() == index and t.is_contiguous())
 
 
 def _rows_of(t, name, dev):
@@ -823,19 +817,47 @@ def _rows_of(t, name, dev):
     if len(shape) != 3:
         raise ValueError(f"{name} must be [T, H, D], got {tuple(shape)}")
     s0, s1, s2 = t.stride()
-    if t.dtype is torch.bfloat16 and t.device == dev and s2 == 1 and s1 == shape[2] and \
-            shape[0] > 1 and dev.type == "cuda":
+    if t.dtype is _BF16 and t.get_device() == dev.index and s2 == 1 and s1 == shape[2] and \
+            shape[0] > 1:
         return shape, s0
     return shape, _token_rows(t, name, dev, shape)
+
+
+def _rotation(dev, T, D, positions, turns, q_weight, k_weight):
+    """Checks of the rotation's tensors; how many elements are rotated."""
+    index = dev.index
+    if not (_dense(q_weight, _F32, index) and _dense(k_weight, _F32, index) and
+            _dense(positions, _I32, index) and _dense(turns, _I64, index)):
+        _need_all(dev, ((positions, "positions", _I32), (turns, "turns", _I64),
+                        (q_weight, "q_weight", _F32), (k_weight, "k_weight", _F32)))
+    _shape(q_weight, "q_weight", (D,))
+    _shape(k_weight, "k_weight", (D,))
+    if turns is None and positions is None:
+        return 0
+    if positions is None or turns is None:
+        raise ValueError("positions and turns go together")
+    _shape(positions, "positions", (T,))
+    return 2 * turns.numel()
 
 
 def _bf16_out(t, name, shape, dev):
     """The caller's output, checked, or a new one."""
     if t is None:
-        return torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    _need_all(dev, ((t, name, torch.bfloat16),))
+        return torch.empty(shape, dtype=_BF16, device=dev)
+    _need_all(dev, ((t, name, _BF16),))
     _shape(t, name, shape)
     return t
+
+
+def _call(dev, fn, name, *args):
+    """A call of the library on the current stream of `dev`."""
+    if _device_now() == dev.index:
+        status = fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _raw_stream(dev))
+    if status != DSA_OK:
+        _check(status, name)
 
 
 def qk_norm_rope(q, k, positions, turns, *, q_weight=None, k_weight=None, eps=1e-6,
@@ -860,12 +882,9 @@ def qk_norm_rope(q, k, positions, turns, *, q_weight=None, k_weight=None, eps=1e
     rotary = _rotation(dev, T, D, positions, turns, q_weight, k_weight)
     if T == 0:
         return q_out, k_out
-    with _on(dev):
-        st = lib.dsa_qk_norm_rope(_addr(q), qs, Hq, _addr(k), ks, hk, T, D, _addr(positions),
-                                  _addr(turns), rotary, bool(interleaved), rope_scale,
-                                  _addr(q_weight), _addr(k_weight), eps, _addr(q_out),
-                                  _addr(k_out), _raw_stream(dev))
-    _check(st, "dsa_qk_norm_rope")
+    _call(dev, lib.dsa_qk_norm_rope, "dsa_qk_norm_rope", q.data_ptr(), qs, Hq, _addr(k), ks, hk, T,
+          D, _addr(positions), _addr(turns), rotary, bool(interleaved), rope_scale,
+          _addr(q_weight), _addr(k_weight), eps, q_out.data_ptr(), _addr(k_out))
     return q_out, k_out
 
 
@@ -878,12 +897,16 @@ def kv_cache(num_blocks, num_kv_heads, block_size, head_dim, device="cuda"):
 
 
 def _kv_shape(k_cache, v_cache, dev):
-    _need_all(dev, ((k_cache, "k_cache", torch.bfloat16), (v_cache, "v_cache", torch.bfloat16)))
-    if k_cache.dim() != 4:
+    index = dev.index
+    if not (_dense(k_cache, _BF16, index) and _dense(v_cache, _BF16, index)):
+        _need_all(dev, ((k_cache, "k_cache", _BF16), (v_cache, "v_cache", _BF16)))
+    shape = k_cache.shape
+    if len(shape) != 4:
         raise ValueError("k_cache [num_blocks, Hkv, block_size, D] expected, got "
-                         f"{tuple(k_cache.shape)}")
-    _shape(v_cache, "v_cache", k_cache.shape)
-    return k_cache.shape
+                         f"{tuple(shape)}")
+    if v_cache.shape != shape:
+        _shape(v_cache, "v_cache", shape)
+    return shape
 
 
 def kv_append(k, v, slot_mapping, k_cache, v_cache, *, positions=None, turns=None, k_weight=None,
@@ -912,13 +935,10 @@ def kv_append(k, v, slot_mapping, k_cache, v_cache, *, positions=None, turns=Non
     rotary = _rotation(dev, T, D, positions, turns, q_weight, k_weight)
     if T == 0:
         return k_cache, v_cache, q_out
-    with _on(dev):
-        st = lib.dsa_kv_append(_addr(k), ks, _addr(v), vs, _addr(slot_mapping), T, hkv, D,
-                               _addr(positions), _addr(turns), rotary, bool(interleaved),
-                               rope_scale, _addr(k_weight), eps, _addr(k_cache), _addr(v_cache),
-                               nb, bs, _addr(q), qs, hq, _addr(q_weight), _addr(q_out),
-                               _raw_stream(dev))
-    _check(st, "dsa_kv_append")
+    _call(dev, lib.dsa_kv_append, "dsa_kv_append", k.data_ptr(), ks, v.data_ptr(), vs,
+          slot_mapping.data_ptr(), T, hkv, D, _addr(positions), _addr(turns), rotary,
+          bool(interleaved), rope_scale, _addr(k_weight), eps, k_cache.data_ptr(),
+          v_cache.data_ptr(), nb, bs, _addr(q), qs, hq, _addr(q_weight), _addr(q_out))
     return k_cache, v_cache, q_out
 
 
@@ -930,7 +950,11 @@ def kv_attention_workspace_bytes(T, Hq, Hkv, D) -> int:
 
 @functools.lru_cache(maxsize=4096)
 def _kv_attn_workspace(device, T, Hq, Hkv, D):
-    n = lib.dsa_kv_attention_workspace_bytes(T, Hq, Hkv, D)
+    if 0 <= device != _device_now():
+        with torch.cuda.device(device):
+            n = lib.dsa_kv_attention_workspace_bytes(T, Hq, Hkv, D)
+    else:
+        n = lib.dsa_kv_attention_workspace_bytes(T, Hq, Hkv, D)
     if n == ctypes.c_size_t(-1).value:
         raise ValueError("dsa_kv_attention_workspace_bytes: bad arguments")
     return int(n)
@@ -950,31 +974,31 @@ def kv_attention(q, k_cache, v_cache, block_table, context_lens, query_starts, *
     T, Hq, Dq = shape
     if Dq != D:
         raise ValueError(f"q must be [T, Hq, {D}], got {tuple(shape)}")
-    if block_table.dim() != 2:
-        raise ValueError(f"block_table must be [B, max_blocks], got {tuple(block_table.shape)}")
-    B, max_blocks = block_table.shape
-    _need_all(dev, ((block_table, "block_table", torch.int32),
-                    (context_lens, "context_lens", torch.int32),
-                    (query_starts, "query_starts", torch.int32), (lse, "lse", torch.float32)))
+    index = dev.index
+    if not (_dense(block_table, _I32, index) and _dense(context_lens, _I32, index) and
+            _dense(query_starts, _I32, index) and _dense(lse, _F32, index)):
+        _need_all(dev, ((block_table, "block_table", _I32), (context_lens, "context_lens", _I32),
+                        (query_starts, "query_starts", _I32), (lse, "lse", _F32)))
+    table = block_table.shape
+    if len(table) != 2:
+        raise ValueError(f"block_table must be [B, max_blocks], got {tuple(table)}")
+    B, max_blocks = table
     _shape(context_lens, "context_lens", (B,))
     _shape(query_starts, "query_starts", (B + 1,))
     out = _bf16_out(out, "out", shape, dev)
     if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        lse = torch.empty((T, Hq), dtype=_F32, device=dev)
     else:
         _shape(lse, "lse", (T, Hq))
     if T == 0 or B == 0:
         return out, lse
-    scale = D ** -0.5 if softmax_scale is None else softmax_scale
-    with _on(dev):
-        nbytes = _kv_attn_workspace(dev.index, T, Hq, hkv, D)
-        ws = _workspace(nbytes, dev, workspace)
-        st = lib.dsa_kv_attention(_addr(q), qs, _addr(k_cache), _addr(v_cache), nb,
-                                  _addr(block_table), max_blocks, _addr(context_lens),
-                                  _addr(query_starts), T, B, bs, Hq, hkv, D, scale, window, sink,
-                                  _addr(out), _addr(lse), _addr(ws), nbytes,
-                                  _raw_stream(dev))
-    _check(st, "dsa_kv_attention")
+    nbytes = _kv_attn_workspace(index, T, Hq, hkv, D)
+    ws = _workspace(nbytes, dev, workspace)
+    _call(dev, lib.dsa_kv_attention, "dsa_kv_attention", q.data_ptr(), qs, k_cache.data_ptr(),
+          v_cache.data_ptr(), nb, block_table.data_ptr(), max_blocks, context_lens.data_ptr(),
+          query_starts.data_ptr(), T, B, bs, Hq, hkv, D,
+          D ** -0.5 if softmax_scale is None else softmax_scale, window, sink, out.data_ptr(),
+          lse.data_ptr(), ws.data_ptr(), nbytes)
     return out, lse
 
 

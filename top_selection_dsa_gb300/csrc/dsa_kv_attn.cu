@@ -1250,6 +1250,9 @@ cudaError_t launch_d(const KvAttnParams& p, cudaStream_t s) {
   kv_attn_kernel<D><<<p.ctas, kThreads, C::SMEM, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  // A tile of one unit is never cut.
+  const int64_t keys = ((static_cast<int64_t>(p.max_blocks) << p.log_bs) + kTile - 1) / kTile;
+  if ((p.slot_rows > kTile ? keys : (keys + 1) / 2) <= 1) return cudaSuccess;
   // Launched while the attention kernel still runs (it waits inside).
   const int64_t rows = static_cast<int64_t>(p.T) * p.G;
   cudaLaunchConfig_t cfg = {};
