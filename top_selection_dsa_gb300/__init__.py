@@ -16,6 +16,7 @@ __all__ = [
     "indexer_topk_paged", "workspace_bytes", "DSAError",
     "kv4_cache", "kv4_insert", "kv4_gather", "kv4_attention", "kv4_attention_topk",
     "kv_evict_select", "kv_compact",
+    "rope_frequencies", "rope_turns", "qk_norm_rope", "kv_cache", "kv_append", "kv_attention",
 ]
 
 
