@@ -221,6 +221,7 @@ struct KvAttnParams {
   int T, B, Hq, Hkv, G, tpt;  // G query heads a key/value head; tokens of a row tile
   int max_blocks, num_blocks, log_bs;
   int window, sink;           // window 0: none
+  int short_log;              // log2 of a short unit's cost in tall ones
   float scale_log2e;          // softmax scale times log2(e)
   uint16_t* out;              // [T, Hq, D]
   float* lse;                 // [T, Hq] or null
@@ -235,7 +236,7 @@ struct KvAttnPlan {
   int64_t part_ml, part_o, bytes;  // offsets of the workspace, and its size
 };
 KvAttnPlan kv_attn_plan(int T, int G, int D);
-// Bound on one head's units of work.
+// Bound on the cost of one head's work, in units of a key tile.
 int64_t kv_attn_units(int T, int B, int G, int64_t max_ctx);
 cudaError_t launch_kv_attention(const KvAttnParams& p, int D, cudaStream_t s);
 

@@ -205,6 +205,7 @@ dsa_status_t dsa_kv_attention(const void* q, int64_t q_stride, const void* k_cac
   // A window or sink past every context changes nothing more.
   p.window = window < max_ctx ? window : 0;
   p.sink = static_cast<int>(sink < max_ctx ? sink : max_ctx);
+  p.short_log = D == 128 ? 1 : 0;
   p.scale_log2e = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;

@@ -181,13 +181,21 @@ __device__ __forceinline__ int tiles_of(const KvAttnParams& p, const Req& r) {
   return (r.n + 2 * p.tpt - 1) / (2 * p.tpt);
 }
 
+// The cost of a tall tile's start and end in its units, about 3000 cycles each
+// (2, 3, 4: 782, 768, 774 us for an 8192-token prompt; 6 805).  A short tile's
+// unit costs 2^short_log, and so do its start and end: 2 at D = 128, where its
+// twice the keys are bound by memory, 1 at D = 64.
+constexpr int kTallCost = 3;
+
 // One tile of rows: its tokens, their positions, and the key tiles that any of
 // them sees: the first `nsink`, then those from `first` on, `keys` in all (one
 // when none is seen, so that the rows' empty results are written).
 struct Tile {
   int tok0, ntok, p0, nsink, first, keys, units;
+  int start, log;  // cost of its start and end, and of a unit (2^log)
   bool tall;
   __device__ int last() const { return p0 + ntok - 1; }
+  __device__ int cost() const { return start + (units << log); }
 };
 
 __device__ __forceinline__ Tile tile_of(const KvAttnParams& p, const Req& r, int qt) {
@@ -202,6 +210,8 @@ __device__ __forceinline__ Tile tile_of(const KvAttnParams& p, const Req& r, int
   t.nsink = min((min(p.sink, end) + kTile - 1) / kTile, t.first);
   t.keys = max(t.nsink + (end + kTile - 1) / kTile - t.first, 1);
   t.units = t.tall ? t.keys : (t.keys + 1) / 2;
+  t.log = t.tall ? 0 : p.short_log;
+  t.start = t.tall ? kTallCost : 1 << p.short_log;
   return t;
 }
 
@@ -225,7 +235,6 @@ struct Piece {
   }
 };
 constexpr int kPieces = 4;    // published ahead
-constexpr int kTileCost = 4;  // units that a tile's start and end take (about 11000 cycles)
 
 // A CTA's run of the work and where it stands.
 struct Walk {
@@ -258,11 +267,10 @@ __device__ __forceinline__ int64_t muldiv(int64_t a, int64_t b, int64_t c) {
   return static_cast<int64_t>(ab / static_cast<uint64_t>(c));
 }
 
-// What a tile counts in the division of the work: its units, and what starting
-// and ending it costs in units (queries, the first logits, the outputs), as if
-// that came first.
-__device__ __forceinline__ int cost_of(const KvAttnParams& p, const Req& r, int qt) {
-  return kTileCost + tile_of(p, r, qt).units;
+// CTAs that share the work: each has the cost of a short tile's unit at least, so
+// that none between a tile's first and last is without a unit of it.
+__device__ __forceinline__ int64_t ctas_of(const KvAttnParams& p, int64_t total) {
+  return min(static_cast<int64_t>(gridDim.x), total >> p.short_log);
 }
 
 // This CTA's run, for the producer's warp.  Called by all threads; `pfx` is
@@ -282,7 +290,7 @@ __device__ Walk find_run(const KvAttnParams& p, int* pfx) {
     if (nt <= kFew) {
       u = 0;
 #pragma unroll 1
-      for (int qt = 0; qt < nt; ++qt) u += cost_of(p, r, qt);
+      for (int qt = 0; qt < nt; ++qt) u += tile_of(p, r, qt).cost();
     }
     pfx[b + 1] = u;
   }
@@ -294,7 +302,7 @@ __device__ Walk find_run(const KvAttnParams& p, int* pfx) {
     const int nt = tiles_of(p, r);
     int u = 0;
 #pragma unroll 1
-    for (int qt = lane; qt < nt; qt += 32) u += cost_of(p, r, qt);
+    for (int qt = lane; qt < nt; qt += 32) u += tile_of(p, r, qt).cost();
     u = __reduce_add_sync(0xffffffffu, u);
     __syncwarp();
     if (lane == 0) pfx[b + 1] = u;
@@ -325,7 +333,7 @@ __device__ Walk find_run(const KvAttnParams& p, int* pfx) {
     if (tokens > p.T) U = 0;
   }
   const int64_t total = static_cast<int64_t>(U) * p.Hkv;
-  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
+  const int64_t ctas = ctas_of(p, total);
   Walk w = {};
   w.total = total;
   if (warp == kProducer && static_cast<int64_t>(blockIdx.x) < ctas) {
@@ -344,7 +352,7 @@ __device__ Walk find_run(const KvAttnParams& p, int* pfx) {
     const int nt = tiles_of(p, w.r);
 #pragma unroll 1
     for (int base = 0; base < nt; base += 32) {
-      const int u = base + lane < nt ? cost_of(p, w.r, base + lane) : 0;
+      const int u = base + lane < nt ? tile_of(p, w.r, base + lane).cost() : 0;
       int incl = u;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -642,10 +650,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         int taken = 0;
         while (w.left > 0) {
           const Tile tile = tile_of(p, w.r, w.qt);
-          const int cost = kTileCost + tile.units;
+          const int cost = tile.cost();
           taken = static_cast<int>(min(static_cast<int64_t>(cost - w.at), w.left));
-          t.j = max(w.at - kTileCost, 0);
-          t.take = max(w.at + taken - kTileCost, 0) - t.j;
+          t.j = max(w.at - tile.start, 0) >> tile.log;
+          t.take = (max(w.at + taken - tile.start, 0) >> tile.log) - t.j;
           if (t.take == 0) {  // a cut in what starts the tile: the next CTA's
             w.next(p, taken);
             continue;
@@ -669,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           t.whole = t.j == 0 && t.take == tile.units;
           if (t.j == 0 && !t.whole) {
             // CTA c has the cost from floor(c total / ctas) on: who has the tile's end.
-            const int64_t ctas = min(static_cast<int64_t>(gridDim.x), w.total);
+            const int64_t ctas = ctas_of(p, w.total);
             const int64_t end = muldiv(blockIdx.x + 1, w.total, ctas) - w.left - w.at + cost;
             t.more = static_cast<int>(muldiv(end * ctas - 1, 1, w.total)) -
                      static_cast<int>(blockIdx.x);
@@ -1286,7 +1294,7 @@ KvAttnPlan kv_attn_plan(int T, int G, int D) {
 
 int64_t kv_attn_units(int T, int B, int G, int64_t max_ctx) {
   return (static_cast<int64_t>(T) / (2 * (kTile / G)) + B) *
-         ((max_ctx + kTile - 1) / kTile + 1 + kTileCost);
+         ((max_ctx + kTile - 1) / kTile + 3 + kTallCost);
 }
 
 cudaError_t launch_kv_attention(const KvAttnParams& p, int D, cudaStream_t s) {

@@ -20,8 +20,8 @@
 // lanes.  A warp's task is some rows of one token and kind, all loaded at once,
 // and the products of weights, cosines and sines are made once for it.
 //
-// The pass is memory-bound: 16384 tokens of 64 + 8 heads of 128 with norms 103 us,
-// 5.9 TB/s (88 % of the measured copy bandwidth, 69 % of the issue slots); index
+// The pass is memory-bound: 16384 tokens of 64 + 8 heads of 128 with norms 98 us,
+// 6.1 TB/s (92 % of the measured copy bandwidth, 69 % of the issue slots); index
 // queries and key, 8191 tokens of 64 + 1 heads, half of them rotated, 45 us, 6.0;
 // 32768 tokens appended, 48 us, 5.6.  With pairs across lanes and heads stepped
 // one by one (194 instructions a warp's row instead of some 90) it was bound by
@@ -36,7 +36,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxTokens = 16;  // of a CTA
+constexpr int kMaxTokens = 32;  // of a CTA
 constexpr int kAhead = 4;       // rows whose loads a lane has in flight
 
 // A CTA takes `tasks` of the tasks of each of `tokens` tokens (blockIdx.y says
@@ -222,10 +222,10 @@ cudaError_t launch_d(const RopeParams& p, bool interleaved, cudaStream_t s) {
   const int per = (p.Hq + kRows - 1) / kRows + (p.Hk + kRows - 1) / kRows +
                   (p.Hv + kRows - 1) / kRows;
   const int sms = device_sm_count() > 0 ? device_sm_count() : 1;
-  // A CTA takes up to four tasks a warp: several tokens, or a share of one
+  // A CTA takes up to eight tasks a warp: several tokens, or a share of one
   // token's tasks; fewer where that leaves SMs without work.
   RopeShape sh;
-  int target = 4 * kWarps;
+  int target = 8 * kWarps;
   while (target > kWarps / 2 &&
          static_cast<int64_t>(p.T) * per < static_cast<int64_t>(8) * sms * target)
     target /= 2;
