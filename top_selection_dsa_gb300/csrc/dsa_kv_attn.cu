@@ -528,7 +528,7 @@ struct AttnCfg {
   static constexpr int MISC = RING + NST * TILE_BYTES;
   static constexpr int XML = 0;                       // float2[2][128]
   static constexpr int BARS = 2048;
-  static constexpr int SLOT = BARS + 8 * (2 * kMaxStages + 14 + 2 * kPieces);
+  static constexpr int SLOT = BARS + 8 * (2 * kMaxStages + 16 + 2 * kPieces);
   static constexpr int PIECES = SLOT + 16;
   static constexpr int END = PIECES + kPieces * static_cast<int>(sizeof(Piece));
   static constexpr int SMEM = MISC + (END + 127) / 128 * 128;
@@ -554,8 +554,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* sfull = qempty + 1;  // [2] S is in TMEM
   uint64_t* pfull = sfull + 2;   // [2] P is in TMEM, O rescaled; the stages arrived, its turn
   uint64_t* kfirst = pfull + 2;  // [2] the first keys of a piece have arrived
-  uint64_t* ofull = kfirst + 2;   // [2] a piece's last product is done
-  uint64_t* xbar = ofull + 2;    // [2] short pieces: sums exchanged; both outputs read
+  uint64_t* ofull = kfirst + 2;   // [2][2] a piece's last product is done: tall, short ones
+  uint64_t* xbar = ofull + 4;    // [2] short pieces: sums exchanged; both outputs read
   uint64_t* drained = xbar + 2;
   uint64_t* told = drained + 1;       // [kPieces] a piece is published
   uint64_t* done = told + kPieces;    // [kPieces] and read by all
@@ -579,6 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&pfull[i], 6);  // four warps' weights, the watcher, the turn
       mbar_init(&kfirst[i], 1);
       mbar_init(&ofull[i], 1);
+      mbar_init(&ofull[2 + i], 1);
       mbar_init(&xbar[i], 256);
     }
     for (int i = 0; i < kPieces; ++i) {
@@ -861,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        k > 0 || i > 0 ? 1u : 0u);
               mma_commit(&empty[vs]);
               if (!tall) mma_commit(&empty[vs]);  // for the other issuer
-              if (!more) mma_commit(&ofull[g]);
+              if (!more) mma_commit(&ofull[tall ? g : 2 + g]);
             }
             if (more) s_mma(0, D / 32);
             // The turn of B's same step, or of A's next.
@@ -960,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_addr = tmem + quarter + C::S_COL + g * 128;
     const uint32_t o_addr = tmem + quarter + C::O_COL;
     const float sc = p.scale_log2e;
-    uint32_t sn = 0, xn = 0, on = 0;  // parities of the phases waited for (ofull: a bit a group)
+    uint32_t sn = 0, xn = 0, on = 0;  // parities of the phases waited for (ofull: a bit each)
 #pragma unroll 1
     while (true) {
       const Piece& t = piece();
@@ -1064,13 +1065,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&pfull[g]);
       }
       // The piece's outputs.
+      // Tall pieces have barriers of their own, one group waiting on each, so
+      // that A need not wait for B's end and no phase goes unseen.
       auto wait_o = [&](int k) {
-        if ((k ? t.b : t.a) == 0) return;
         wait(&ofull[k], on >> k & 1u);
         on ^= 1u << k;
       };
-      wait_o(g);
-      if (!t.tall) wait_o(1 - g);
+      if (t.tall) {
+        wait_o(g);
+      } else {
+        wait_o(2);
+        if (t.b > 0) wait_o(3);
+      }
       if (!ok) break;
       tc_fence_after_sync();
       const bool whole = t.whole;
@@ -1134,9 +1140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (!whole && t.j == 0 && tid == 0)
         p.notes[blockIdx.x] = make_int4(t.tok0, t.ntok, t.h, t.more);
-      if (t.tall) {
-        wait_o(1 - g);  // no phase is skipped
-      } else {
+      if (!t.tall) {
         tc_fence_before_sync();
         mbar_arrive(&xbar[1]);
         wait(&xbar[1], xn);
