@@ -40,9 +40,9 @@
 //   prompts         a row tile's chain of product, softmax and product, about 2900
 //                   cycles a unit where the products alone take 2060 (S reads
 //                   both operands from shared memory at its full rate): 8192
-//                   tokens 0.78 ms, 1.41 PFLOP/s; 2048 in 65536 2.9 to 3.2 ms,
+//                   tokens 0.77 ms, 1.42 PFLOP/s; 2048 in 65536 2.9 to 3.2 ms,
 //                   1.34 to 1.5, where power caps the clock
-//   in between      what starts and ends a tile, about 11000 cycles
+//   in between      what starts and ends a tile, about 9000 cycles
 //
 // Values that a row does not see never reach it, whatever they hold: in tiles
 // that are not wholly seen, infinities and NaN among the values are replaced
