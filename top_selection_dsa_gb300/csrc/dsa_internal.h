@@ -221,7 +221,8 @@ struct KvAttnParams {
   int T, B, Hq, Hkv, G, tpt;  // G query heads a key/value head; tokens of a row tile
   int max_blocks, num_blocks, log_bs;
   int window, sink;           // window 0: none
-  int short_log;              // log2 of a short unit's cost in tall ones
+  int short_log;              // log2 of a short unit's cost (a tall one's: 1)
+  int tall_start, short_start;  // cost of a tile's start and end
   float scale_log2e;          // softmax scale times log2(e)
   uint16_t* out;              // [T, Hq, D]
   float* lse;                 // [T, Hq] or null
@@ -236,7 +237,7 @@ struct KvAttnPlan {
   int64_t part_ml, part_o, bytes;  // offsets of the workspace, and its size
 };
 KvAttnPlan kv_attn_plan(int T, int G, int D);
-// Bound on the cost of one head's work, in units of a key tile.
+// Bound on the cost of one head's work.
 int64_t kv_attn_units(int T, int B, int G, int64_t max_ctx);
 cudaError_t launch_kv_attention(const KvAttnParams& p, int D, cudaStream_t s);
 

@@ -205,7 +205,13 @@ dsa_status_t dsa_kv_attention(const void* q, int64_t q_stride, const void* k_cac
   // A window or sink past every context changes nothing more.
   p.window = window < max_ctx ? window : 0;
   p.sink = static_cast<int>(sink < max_ctx ? sink : max_ctx);
-  p.short_log = D == 128 ? 1 : 0;
+  // Cost, in halves of a tall unit (some 3000 cycles), as fitted to the SMs' times
+  // of 40 batches: D = 128, where a short unit's twice the keys are bound by
+  // memory, 4 a short unit, 5 and 2 a tile's start and end; D = 64 2, 4 and 3.
+  // (Starts of 6 and 4, 6 and 2 instead: 0.9 and 2.5 % slower over all.)
+  p.short_log = D == 128 ? 2 : 1;
+  p.tall_start = D == 128 ? 5 : 4;
+  p.short_start = D == 128 ? 2 : 3;
   p.scale_log2e = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;

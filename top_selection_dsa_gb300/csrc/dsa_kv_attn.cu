@@ -62,6 +62,7 @@ namespace {
 
 constexpr int kTile = 128;    // keys of a tile, rows of a row tile
 constexpr int kThreads = 384;
+constexpr int kTallLog = 1;   // log2 of a tall unit's cost: starts and ends count halves
 // Warps: 0-7 softmax, then these (an issuer for A, one for B).
 constexpr int kProducer = 8, kIssuer = 9, kWatch = 11;
 constexpr int kMaxStages = 12;
@@ -181,12 +182,6 @@ __device__ __forceinline__ int tiles_of(const KvAttnParams& p, const Req& r) {
   return (r.n + 2 * p.tpt - 1) / (2 * p.tpt);
 }
 
-// The cost of a tall tile's start and end in its units, about 3000 cycles each
-// (2, 3, 4: 782, 768, 774 us for an 8192-token prompt; 6 805).  A short tile's
-// unit costs 2^short_log, and so do its start and end: 2 at D = 128, where its
-// twice the keys are bound by memory, 1 at D = 64.
-constexpr int kTallCost = 3;
-
 // One tile of rows: its tokens, their positions, and the key tiles that any of
 // them sees: the first `nsink`, then those from `first` on, `keys` in all (one
 // when none is seen, so that the rows' empty results are written).
@@ -210,8 +205,8 @@ __device__ __forceinline__ Tile tile_of(const KvAttnParams& p, const Req& r, int
   t.nsink = min((min(p.sink, end) + kTile - 1) / kTile, t.first);
   t.keys = max(t.nsink + (end + kTile - 1) / kTile - t.first, 1);
   t.units = t.tall ? t.keys : (t.keys + 1) / 2;
-  t.log = t.tall ? 0 : p.short_log;
-  t.start = t.tall ? kTallCost : 1 << p.short_log;
+  t.log = t.tall ? kTallLog : p.short_log;
+  t.start = t.tall ? p.tall_start : p.short_start;
   return t;
 }
 
@@ -1297,8 +1292,9 @@ KvAttnPlan kv_attn_plan(int T, int G, int D) {
 }
 
 int64_t kv_attn_units(int T, int B, int G, int64_t max_ctx) {
+  // (the cost of a row tile is at most twice its tiles of keys and 5)
   return (static_cast<int64_t>(T) / (2 * (kTile / G)) + B) *
-         ((max_ctx + kTile - 1) / kTile + 3 + kTallCost);
+         (((max_ctx + kTile - 1) / kTile + 3) << kTallLog);
 }
 
 cudaError_t launch_kv_attention(const KvAttnParams& p, int D, cudaStream_t s) {
