@@ -534,7 +534,9 @@ struct AttnCfg {
   static_assert((kMaxPagedRequests + 1) * 4 <= NST * TILE_BYTES, "prefix sums in the ring");
 };
 
-template <int D>
+// kSmall: pages of 8 or 16 keys, whose copies one lane issues (in a kernel of
+// their own: that code beside the other roles' slowed these by a tenth).
+template <int D, bool kSmall>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_attn_kernel(const __grid_constant__ KvAttnParams p) {
   using C = AttnCfg<D>;
@@ -711,6 +713,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q = 0; q < 2; ++q)
             row[q] = here ? (page_of(p, e[q]) * p.Hkv + t.h) << p.log_bs : 0;
           here = entries(t, i + 1, e);  // read a step ahead
+          // Small pages of tile q of the step: the whole warp walks them and one
+          // lane issues eight at a time.  With a lane for each page the warp took
+          // 80 cycles a copy: decode over pages of 8 and 16 612 and 416 us (2.3 GB,
+          // heads of 128) against 352 and 340, an 8192-token prompt over pages of
+          // 16 1002 against 828.
+          auto copy_small = [&](int q, int st) {
+            const CUtensorMap* map = q & 1 ? &p.tmap_k : &p.tmap_v;
+#pragma unroll 1
+            for (int box = 0; box < per_tile; box += 8) {
+              int from[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                from[k] = __shfl_sync(0xffffffffu, box ? row[1] : row[0], 8 * q + k);
+              if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+#pragma unroll
+                  for (int a = 0; a < C::HALVES; ++a)
+                    tma_load_2d(ring + st * C::TILE_BYTES + a * C::HALF_BYTES +
+                                    (((box + k) * 128) << p.log_bs),
+                                map, &full[st], a * 64, from[k]);
+              }
+              __syncwarp();
+            }
+          };
           // This lane's pages of its tile, a box of 64 elements each.
           auto copy = [&](int st) {
 #pragma unroll
@@ -734,7 +761,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int st = at.st;
               if (lane == 0) mbar_arrive_expect_tx(&full[st], C::TILE_BYTES);
               __syncwarp();
-              if (lane_tile == q) copy(st);
+              if constexpr (kSmall)
+                copy_small(q, __shfl_sync(0xffffffffu, st, 0));
+              else if (lane_tile == q)
+                copy(st);
               __syncwarp();
               at.step();
               ++loads;
@@ -756,9 +786,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             if (mine && (lane & 7) == 0) mbar_arrive_expect_tx(&full[st], C::TILE_BYTES);
             __syncwarp();
-            if (mine) copy(st);
+            if (!kSmall && mine) copy(st);
             __syncwarp();
-            for (int q = __popc(tiles) >> 3; q > 0; --q) {
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              if (!(tiles >> 8 * q & 1u)) continue;
+              if constexpr (kSmall) copy_small(q, __shfl_sync(0xffffffffu, at.st, 0));
               at.step();
               ++loads;
             }
@@ -1239,7 +1272,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(
   }
 }
 
-template <int D>
+template <int D, bool kSmall>
 cudaError_t launch_d(const KvAttnParams& p, cudaStream_t s) {
   using C = AttnCfg<D>;
   // The attribute is set once a device (devices past 64: every time).
@@ -1249,12 +1282,12 @@ cudaError_t launch_d(const KvAttnParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(kv_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(kv_attn_kernel<D, kSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::SMEM);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  kv_attn_kernel<D><<<p.ctas, kThreads, C::SMEM, s>>>(p);
+  kv_attn_kernel<D, kSmall><<<p.ctas, kThreads, C::SMEM, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // A tile of one unit is never cut.
@@ -1298,7 +1331,8 @@ int64_t kv_attn_units(int T, int B, int G, int64_t max_ctx) {
 }
 
 cudaError_t launch_kv_attention(const KvAttnParams& p, int D, cudaStream_t s) {
-  return D == 64 ? launch_d<64>(p, s) : launch_d<128>(p, s);
+  if (p.log_bs < 5) return D == 64 ? launch_d<64, true>(p, s) : launch_d<128, true>(p, s);
+  return D == 64 ? launch_d<64, false>(p, s) : launch_d<128, false>(p, s);
 }
 
 }  // namespace dsa
