@@ -97,6 +97,15 @@ def test_pages(api, block):
     check(s, *call(api, s))
 
 
+@pytest.mark.parametrize("window,sink", [(0, 0), (300, 130)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("block", [8, 16])
+def test_small_pages(api, block, D, window, sink):
+    """Rings that go round many times, tiles cut between SMs, odd key tiles."""
+    s = make([1, 260, 37, 2], [9001, 2500, 1283, 8], 12, 3, D, block, seed=block + D)
+    check(s, *call(api, s, window=window, sink=sink), window=window, sink=sink)
+
+
 def test_positions_below_zero_see_nothing(api):
     """Contexts shorter than the new tokens: the first rows are empty."""
     s = make([20, 5, 90, 2], [7, 0, 60, 2], 8, 2, 128, 16, seed=3)
