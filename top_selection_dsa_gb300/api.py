@@ -179,6 +179,8 @@ def _workspace(nbytes, device, workspace):
         return workspace
     if workspace is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
     if workspace.numel() * workspace.element_size() < nbytes:
         raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} "
                          f"bytes, {nbytes} needed")
