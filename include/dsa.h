@@ -655,7 +655,9 @@ dsa_status_t dsa_kv_append(const void* k, int64_t k_stride, const void* v, int64
  *   q             [T, Hq, D]; Hq a multiple of Hkv, Hq / Hkv <= 128
  *   block_table   [B, max_blocks] int32; context_lens [B] int32, counting the
  *                 new tokens: bad entries as in dsa_indexer_logits_paged (block
- *                 0 in their place, lengths clamped, both recorded)
+ *                 0 in their place, lengths clamped, both recorded).  Entries of
+ *                 pages that no token of the request sees (behind a window, not
+ *                 among the first `sink` keys) are not read: any value serves
  *   query_starts  [B + 1] int32, ascending, in [0, T]: entries outside or
  *                 descending are clamped and recorded alike (nothing is
  *                 computed where requests then overlap to more than T tokens)

@@ -5,7 +5,8 @@ import math
 import pytest
 import torch
 
-from test_kv16_gpu import call, make
+import kv16_reference as ref
+from test_kv16_gpu import call, check, make
 
 pytestmark = pytest.mark.gpu
 
@@ -16,6 +17,40 @@ def api():
     assert _api.last_device_error() == _api.DSA_OK
     yield _api
     assert _api.last_device_error() == _api.DSA_OK
+
+
+@pytest.mark.parametrize("window,sink", [(1, 0), (100, 4), (300, 130), (257, 0)])
+@pytest.mark.parametrize("D,block", [(128, 8), (64, 8), (64, 16), (128, 32), (64, 64), (128, 128)])
+def test_entries_of_pages_that_no_token_sees(api, D, block, window, sink):
+    """Pages behind the window that a serving loop has freed."""
+    s = make([1, 200, 40, 1, 3, 1], [1500, 700, 2500, 90, 129, 9001], 8, 2, D, block,
+             seed=window + sink)
+    table = s["table"].clone()
+    gone = 0
+    for b, L in enumerate(s["lens"]):
+        seen = ref.sees(s["starts"][b + 1] - s["starts"][b], L, window, sink, "cuda").any(0)
+        for page in range(-(-L // block)):
+            if not seen[page * block:(page + 1) * block].any():
+                table[b, page] = -1 if page % 2 else 1 << 30
+                gone += 1
+    assert gone or block == 128
+    out, lse = call(api, dict(s, table=table), window=window, sink=sink)
+    assert api.last_device_error() == api.DSA_OK
+    check(s, out, lse, window=window, sink=sink)
+    # one that a token sees is recorded all the same
+    L = s["lens"][1]
+    table[1, (L - window) // block] = -1
+    call(api, dict(s, table=table), window=window, sink=sink)
+    assert api.last_device_error() == api.DSA_ERR_INVALID_ARG
+
+
+def test_positions_below_zero_look_up_no_page(api):
+    s = make([300, 5], [3, 0], 8, 2, 128, 16, seed=3)
+    table = s["table"].clone()
+    table[1] = -1
+    out, lse = call(api, dict(s, table=table))
+    assert api.last_device_error() == api.DSA_OK
+    check(s, out, lse)
 
 
 def spoil_tails(s):

@@ -968,7 +968,8 @@ def kv_attention(q, k_cache, v_cache, block_table, context_lens, query_starts, *
     [T, Hq, D] (bf16; tokens may be strided) holds request b's tokens in rows
     query_starts[b] .. query_starts[b+1] (int32 [B+1]), the last positions of
     its context of context_lens[b].  Each sees the keys up to its own position;
-    with a window, the last `window` of them and the first `sink`.  Returns
+    with a window, the last `window` of them and the first `sink`; the table's
+    entries of pages that none of them sees may hold anything.  Returns
     (out [T, Hq, D], lse [T, Hq] fp32).  softmax_scale defaults to D^-0.5."""
     dev = q.device
     nb, hkv, bs, D = _kv_shape(k_cache, v_cache, dev)

@@ -216,7 +216,7 @@ struct Piece {
   int tok0, ntok, p0, last, nsink, first, keys, tall;  // of the tile; last: its last position
   int j, take;   // take 0: no more pieces
   int a, b;      // key tiles that A and B take
-  int h, req, L;
+  int h, req;
   int whole;     // the piece is the whole tile
   int more;      // CTAs that go on with the tile (where the piece starts it)
   // Key tiles that every row sees whole: those below `seen`, of these in a
@@ -450,13 +450,27 @@ __device__ __forceinline__ Sight sight_of(const KvAttnParams& p, int pos, int c0
   return {pos - c0, p.window > 0 ? pos - p.window + 1 - c0 : 0, p.sink - c0};
 }
 
-// The block table's entry for key c of a request whose context is L, and the
-// page it stands for.
-__device__ __forceinline__ int entry_of(const KvAttnParams& p, int req, int L, int c) {
-  const int used = (L + (1 << p.log_bs) - 1) >> p.log_bs;
-  const int lb = min(c >> p.log_bs, used - 1);
-  return lb < 0 ? 0 : __ldg(p.block_table + static_cast<int64_t>(req) * p.max_blocks + lb);
+// A request's row of the block table and the pages of it that some row of a piece
+// sees: up to `last`, from `first` on or below `kept`.
+struct Pages {
+  const int32_t* row;
+  int first, last, kept;
+  // The entry of page k.  One that no row sees is not looked up, as the caller may
+  // have given it away: the last row's page stands in for it.
+  __device__ int entry(int k) const {
+    k = min(k, last);
+    if (k < first && k >= kept) k = last;
+    return k < 0 ? 0 : __ldg(row + k);
+  }
+};
+
+__device__ __forceinline__ Pages pages_of(const KvAttnParams& p, const Piece& t) {
+  return {p.block_table + static_cast<int64_t>(t.req) * p.max_blocks,
+          p.window > 0 ? max(t.p0 - p.window + 1, 0) >> p.log_bs : 0, t.last >> p.log_bs,
+          (p.sink + (1 << p.log_bs) - 1) >> p.log_bs};
 }
+
+// The page that an entry stands for.
 __device__ __forceinline__ int page_of(const KvAttnParams& p, int entry) {
   if (static_cast<uint32_t>(entry) < static_cast<uint32_t>(p.num_blocks)) return entry;
   record_error(p.err, kErrBadIndex);
@@ -470,6 +484,7 @@ __device__ __forceinline__ int page_of(const KvAttnParams& p, int entry) {
 template <int D>
 __device__ __noinline__ void add_nonfinite(const KvAttnParams& p, const Piece& t, int2 found,
                                            int pos, int d0, int n, uint16_t* out, float* part) {
+  const Pages pages = pages_of(p, t);
 #pragma unroll 1
   for (int i = 0; i < t.a + (t.tall ? 0 : t.b); ++i) {
     const int kt = t.tall ? t.key_of(i, 0) : t.key_of(i / 2, i % 2);
@@ -480,7 +495,7 @@ __device__ __noinline__ void add_nonfinite(const KvAttnParams& p, const Piece& t
     for (int c = max(found.x - kt * kTile, 0); c <= c1; ++c) {
       if (!s.sees(c)) continue;
       const int key = kt * kTile + c;
-      const int64_t page = page_of(p, entry_of(p, t.req, t.L, key));
+      const int64_t page = page_of(p, pages.entry(key >> p.log_bs));
       const int64_t row = ((page * p.Hkv + t.h) << p.log_bs) + (key & ((1 << p.log_bs) - 1));
 #pragma unroll 1
       for (int d = d0; d < d0 + n; d += 8) {
@@ -668,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The entries of this lane's pages (lane & 7, and 8 more) of the tiles of
       // step i: the values of A's tile i, the keys of its tile i + 1, the same
       // of B (tall: A alone).  Returns whether there is such a tile.
-      auto entries = [&](const Piece& t, int i, int (&e)[2]) {
+      auto entries = [&](const Piece& t, const Pages& pages, int i, int (&e)[2]) {
         const int g = lane_tile >> 1, k = i + (lane_tile & 1);
         const bool here = k >= 0 && k < (g ? (t.tall ? 0 : t.b) : t.a) &&
                           (i >= 0 || (lane_tile & 1));
@@ -676,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int q = 0; q < 2; ++q) {
           const int page = (lane & 7) + 8 * q;
           e[q] = here && page < per_tile
-                     ? entry_of(p, t.req, t.L, t.key_of(k, g) * kTile + (page << p.log_bs))
+                     ? pages.entry((t.key_of(k, g) * kTile >> p.log_bs) + page)
                      : 0;
         }
         return here;
@@ -712,7 +727,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           t.b = t.tall || 2 * (t.j + t.take) <= t.keys ? t.take : t.take - 1;
           t.h = w.h;
           t.req = w.r.b;
-          t.L = w.r.L;
           t.whole = t.j == 0 && t.take == tile.units;
           if (t.j == 0 && !t.whole) {
             // CTA c has the cost from floor(c total / ctas) on: who has the tile's end.
@@ -733,7 +747,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (t.take == 0) break;
         const bool two = !t.tall;  // A and B have key tiles of their own
         int e[2];
-        bool here = entries(t, -1, e);
+        const Pages pages = pages_of(p, t);
+        bool here = entries(t, pages, -1, e);
         wait(qempty, (static_cast<uint32_t>(queries) & 1u) ^ 1u);
         if (!ok) break;
         if (lane == 0) {
@@ -754,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int q = 0; q < 2; ++q)
             row[q] = here ? (page_of(p, e[q]) * p.Hkv + t.h) << p.log_bs : 0;
-          here = entries(t, i + 1, e);  // read a step ahead
+          here = entries(t, pages, i + 1, e);  // read a step ahead
           // Small pages of tile q of the step: the whole warp walks them and one
           // lane issues eight at a time.  With a lane for each page the warp took
           // 80 cycles a copy: decode over pages of 8 and 16 612 and 416 us (2.3 GB,
