@@ -650,7 +650,9 @@ dsa_status_t dsa_kv_append(const void* k, int64_t k_stride, const void* v, int64
  *   out[t,h] = sum_c exp(S[t,h,c] - lse[t,h]) V[c, h / (Hq/Hkv)]
  * A token that sees nothing (a position below 0: L_b < n) gives out = 0 and
  * lse = -inf.  Values of keys that a token does not see never reach it,
- * whatever they hold.  Rows of no request are left as they were.
+ * whatever they hold; an infinity or NaN that it sees makes that element of its
+ * output one of them (NaN where fp32 holds an infinity's weight as zero).  Rows
+ * of no request are left as they were.
  *
  *   q             [T, Hq, D]; Hq a multiple of Hkv, Hq / Hkv <= 128
  *   block_table   [B, max_blocks] int32; context_lens [B] int32, counting the

@@ -93,3 +93,39 @@ def test_values_that_no_row_sees_cost_no_time(api, news):
     assert torch.equal(kw["out"], want[0]) and torch.equal(kw["lse"], want[1])
     print(f"clean {clean:.1f} us, NaN behind the contexts {spoiled:.1f} us")
     assert spoiled < 1.5 * clean, (spoiled, clean)
+
+
+@pytest.mark.parametrize("news,L,high", [
+    (1, 200, 128), (1, 700, 600), (1, 20000, 600), (1, 20000, 19000), (40, 20000, 600),
+    (40, 20000, 19000), (100, 6000, 5000), (3, 131000, 130000)])
+def test_seen_values_that_are_no_numbers_and_weigh_nothing(api, news, L, high):
+    """Keys from `high` on have logits 200 above the others': what is not finite
+    among the values before them has weights of exp(-200), and shows, wherever
+    the work is cut."""
+    D = 128
+    s = make([news], [L], 8, 1, D, 64, seed=2)
+    s["q"].fill_(4.0)
+    table = s["table"][0].long()
+    c = torch.arange(L, device="cuda")
+    s["kc"].zero_()
+    s["kc"][table[c[high:] // 64], 0, c[high:] % 64] = 200 / (4 * D ** 0.5)
+
+    def put(key, d, x):
+        s["vc"][table[key // 64], 0, key % 64, d] = x
+
+    for key in (3, high // 2, high - 1):
+        put(key, 5 + key % 3, math.inf)
+    put(high // 3, 20, -math.inf)
+    put(high // 2, 21, math.nan)
+    put(7, 22, math.inf)
+    put(high - 2, 22, -math.inf)
+    out, lse = call(api, s)
+    o, z, tol, ltol = ref.attention(s["q"], s["kc"], s["vc"], s["table"], [L], s["starts"],
+                                    D ** -0.5)
+    out = out.double()
+    assert torch.equal(torch.isfinite(out), torch.isfinite(o))
+    fine = torch.isfinite(o)
+    assert ((out - o).abs() <= tol)[fine].all()
+    # an infinity times a weight that fp32 holds as zero is no number
+    assert (out.isnan() | (out == o) | fine).all()
+    assert ((lse.double() - z).abs() <= ltol).all()

@@ -1255,6 +1255,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 constexpr int kJoinWarps = 8;
 
+// A part's value times its weight: what is not finite shows where fp32 holds the
+// weight as zero too, as it does where a tile is not cut.
+__device__ __forceinline__ float weighted(float v, float f) {
+  return f != 0.f ? v * f : isfinite(v) ? 0.f : v;
+}
+
 // The parts of each cut tile, a warp a row.  CTA blockIdx.x started the tile
 // (its slot 1), the next ones went on with it (their slots 0).
 template <int D>
@@ -1301,13 +1307,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(
       const float keep = was == -INFINITY ? 0.f : ex2(was - top);
       sum *= keep;
 #pragma unroll
-      for (int q = 0; q < N; ++q) acc[q] = keep == 0.f ? 0.f : acc[q] * keep;
+      for (int q = 0; q < N; ++q) acc[q] = weighted(acc[q], keep);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const float f = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - top);
         sum = fmaf(ml[k].y, f, sum);
 #pragma unroll
-        for (int q = 0; q < N; ++q) acc[q] = f == 0.f ? acc[q] : fmaf(v[k][q], f, acc[q]);
+        for (int q = 0; q < N; ++q)
+          acc[q] = f == 0.f ? acc[q] + weighted(v[k][q], f) : fmaf(v[k][q], f, acc[q]);
       }
     };
     if (more == 1) {  // most rows of prompts
