@@ -678,7 +678,9 @@ dsa_status_t dsa_kv_append(const void* k, int64_t k_stride, const void* v, int64
  * Products run on the tensor cores on the bf16 inputs with fp32 accumulation;
  * the weights exp(S - max) are rounded to bf16 for the second one (2^-8 relative),
  * their sum and the maximum are fp32.  A row's weights are divided by their sum at
- * the end: sums of values beyond 2^90 may pass fp32's range.  Every sum runs in one
+ * the end: sums of values beyond 2^90 may pass fp32's range.  Logits count up to
+ * 2^27 in magnitude: out and lse are NaN where a row's largest one passes 2^28, and
+ * may be where it or the largest of 128 keys passes 2^27.  Every sum runs in one
  * fixed order: results are the same from call to call.
  */
 dsa_status_t dsa_kv_attention(const void* q, int64_t q_stride, const void* k_cache,

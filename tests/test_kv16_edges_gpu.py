@@ -129,3 +129,42 @@ def test_seen_values_that_are_no_numbers_and_weigh_nothing(api, news, L, high):
     # an infinity times a weight that fp32 holds as zero is no number
     assert (out.isnan() | (out == o) | fine).all()
     assert ((lse.double() - z).abs() <= ltol).all()
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 10, 1e5, 2.0 ** 18, 2.0 ** 21, 3e11, 2.0 ** 64])
+@pytest.mark.parametrize("D,news,lens", [(128, [1, 60], [3000, 500]), (64, [1, 200], [9001, 200])])
+def test_largest_scales(api, D, news, lens, scale):
+    """Logits up to 2^27 count; past 2^28 rows are no numbers, never wrong ones.
+    Whole numbers, whose products are exact: what is left is the scale."""
+    s = make(news, lens, 8, 2, D, 64, seed=5)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    for name in ("q", "kc"):
+        s[name].copy_(torch.randint(-3, 4, s[name].shape, generator=g, device="cuda"))
+    out, lse = call(api, s, softmax_scale=scale)
+    scale = torch.tensor(scale, dtype=torch.float32).double().item()
+    for b, L in enumerate(lens):
+        rows = slice(s["starts"][b], s["starts"][b + 1])
+        K, V = (ref.context(s[n], s["table"], b, L).double() for n in ("kc", "vc"))
+        ok = ref.sees(news[b], L, 0, 0, "cuda")
+        for h in range(8):
+            S = s["q"][rows, h].double() @ K[:, h // 4].T
+            most = torch.where(ok, S.abs(), 0.0).amax(-1) * scale
+            S = S.masked_fill(~ok, -math.inf)
+            top = S.amax(-1, keepdim=True)
+            w = ((S - top) * scale).exp()
+            l = w.sum(-1, keepdim=True)
+            want = w / l @ V[:, h // 4]
+            size = w / l @ V[:, h // 4].abs()
+            # a step of S is 1024 at least, so that weights are 0 or all alike: the
+            # output's half step, theirs, the sum's and the division's roundings
+            got = out[rows, h].double()
+            close = ((got - want).abs() <= ref.BF16 * want.abs() + 1e-38 +
+                     (ref.BF16 * (1 + ref.BF16) + (L + 40) * ref.F32) * size).all(-1)
+            z = (top * scale + l.log())[:, 0]
+            # the logit's product, log(2) and its inverse: a rounding each
+            close &= (lse[rows, h].double() - z).abs() <= 8 * ref.F32 * z.abs() + 1e-5
+            nan = got.isnan().all(-1) & lse[rows, h].isnan()
+            assert (close | nan).all()
+            assert close[most <= 2.0 ** 27].all()
+            assert nan[top[:, 0] * scale > 2.0 ** 28].all()
+    assert api.last_device_error() == api.DSA_OK

@@ -155,7 +155,7 @@ dsa_status_t dsa_kv_attention(const void* q, int64_t q_stride, const void* k_cac
                               float* lse, void* workspace, size_t ws_bytes, dsa_stream_t stream) {
   const CallRange range("dsa_kv_attention");
   if (!q || !block_table || !context_lens || !query_starts || !out) return DSA_ERR_INVALID_ARG;
-  // The scale's range keeps every product of it with a logit's bound finite.
+  // (Where the scaled logits leave the range that the weights serve, rows are NaN.)
   if (T < 0 || B < 0 || max_blocks < 1 || Hq < 1 || window < 0 || sink < 0 ||
       !(softmax_scale >= 0x1p-64f && softmax_scale <= 0x1p64f))
     return DSA_ERR_INVALID_ARG;

@@ -68,6 +68,11 @@ constexpr int kProducer = 8, kIssuer = 9, kWatch = 11;
 constexpr int kMaxStages = 12;
 // A row's weights of one tile add to no more than this, or its reference moves.
 constexpr float kMostSum = 65536.f;
+// A reference (times the scale) from here on is no number, and so are its row's
+// results: fp32 holds it to 16 only, and at 2^31 weights relative to it, which are all
+// off by the same factor then, would leave fp32's range.  (Taking the difference from
+// the maximum ahead of the scale has no such bound: a prompt 806 us against 774.)
+constexpr float kMostRef = 0x1p28f;
 // Registers a thread: 168 at launch, shifted to the softmax (8 warps at 208 and
 // 4 at 88 are the block's 64512).
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
@@ -1104,7 +1109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
               const float mn = fmaxf(m, top);
               const float f = m == -INFINITY ? 0.f : ex2((m - mn) * sc);
-              m = mn;
+              m = fabsf(mn * sc) < kMostRef || mn == -INFINITY ? mn : NAN;
               l *= f;
               if (i > 0) {
 #pragma unroll 1
