@@ -604,8 +604,10 @@ size_t dsa_kv4_attention_workspace_bytes(int B, int next_n, int Hq, int Hkv, int
  *   q, k          [T, Hq, D], [T, Hk, D]; k may be NULL (then Hk = 0, k_out NULL)
  *   positions     [T] int32, any value
  *   turns         [rotary / 2] uint64: f_i / (2 pi) in units of 2^-64 turns,
- *                 rounded (modulo 2^64).  The angle is reduced exactly, so its
- *                 error is below 2^-31 turns at every position.
+ *                 rounded (modulo 2^64).  The angle is reduced exactly and its
+ *                 distance from the nearest quarter turn rounded to fp32: off by
+ *                 2^-28 turns at most, and by the table's rounding times the
+ *                 position, 2^-34 at most
  *   rotary        0 (positions and turns may then be NULL) .. D, a multiple of
  *                 16 (other even ones: DSA_ERR_UNSUPPORTED)
  *   q_weight, k_weight  [D] fp32, or NULL: that side is not normalised

@@ -168,3 +168,27 @@ def test_largest_scales(api, D, news, lens, scale):
             assert close[most <= 2.0 ** 27].all()
             assert nan[top[:, 0] * scale > 2.0 ** 28].all()
     assert api.last_device_error() == api.DSA_OK
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_angles_near_quarter_turns(api, interleaved):
+    """The angle's error is at most 2^-28 turns where a cosine or sine is nearly
+    zero too: there it is all that the result consists of."""
+    F, D = 32, 64
+    near = [24, -24, 5, -5, 40, -100, 1001, -77777]          # units of 2^-32 turns
+    whole = [(q << 62) + (n << 32) + 12345 for q in range(4) for n in near]
+    turns = torch.tensor([w - 2 ** 64 if w >= 2 ** 63 else w for w in whole], device="cuda")
+    q = torch.zeros(1, 1, D)
+    q[..., 0::2 if interleaved else 1] = 1.0                 # pairs (1, 0)
+    if not interleaved:
+        q[..., F:] = 0.0
+    pos = torch.ones(1, dtype=torch.int32, device="cuda")
+    got, _ = api.qk_norm_rope(q.bfloat16().cuda(), None, pos, turns, interleaved=interleaved)
+    got = got[0, 0].double().cpu()
+    cos, sin = (got[0::2], got[1::2]) if interleaved else (got[:F], got[F:])
+    t = torch.tensor([2 * math.pi * w / 2 ** 64 for w in whole], dtype=torch.float64)
+    # half a step of bf16, sincospif's two steps and its products' roundings,
+    # and the angle's 2^-28 turns (2 pi / 2^64 in float64: 2^-50)
+    rel, angle = ref.BF16 + 8 * ref.F32, 2 * math.pi * 2.0 ** -28 + 2.0 ** -50
+    assert ((cos - t.cos()).abs() <= rel * t.cos().abs() + angle * t.sin().abs()).all()
+    assert ((sin - t.sin()).abs() <= rel * t.sin().abs() + angle * t.cos().abs()).all()

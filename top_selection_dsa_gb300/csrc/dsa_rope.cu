@@ -12,7 +12,8 @@
 // Angles.  f_i comes as `turns`, f_i / (2 pi) in units of 2^-64 turns: p times
 // it, modulo 2^64, is the angle's fraction of a turn exactly (integers wrap at
 // whole turns), whatever the position: no table over positions, no 64-bit
-// floating point, and an error below 2^-31 turns at every position of 32 bits.
+// floating point.  Its distance from the nearest quarter turn is rounded to fp32,
+// 2^-28 turns at most; the table's own rounding times the position is 2^-34 at most.
 //
 // A CTA writes the cosines and sines of its tokens to shared memory once; D / 8
 // lanes take a row, each the elements of whole pairs (two groups of four that
@@ -81,9 +82,15 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p, c
     const int tt = i / F, f = i - tt * F;
     const int64_t pos = __ldg(p.positions + t0 + tt);
     const uint64_t angle = __ldg(p.turns + f) * static_cast<uint64_t>(pos);
-    float sn, cs;
-    // Half turns in [-1, 1).
-    sincospif(static_cast<float>(static_cast<int32_t>(angle >> 32)) * 0x1p-31f, &sn, &cs);
+    // The nearest quarter turn, and what is left of an eighth turn at most, which fp32
+    // holds to 2^-28 turns (half turns for sincospif).
+    const uint64_t quarter = (angle + (uint64_t(1) << 61)) >> 62;
+    const float rest = __ll2float_rn(static_cast<int64_t>(angle - (quarter << 62))) * 0x1p-63f;
+    float s0, c0;
+    sincospif(rest, &s0, &c0);
+    const float s1 = quarter & 1 ? c0 : s0, c1 = quarter & 1 ? s0 : c0;
+    const float sn = quarter & 2 ? -s1 : s1;
+    const float cs = (quarter + 1) & 2 ? -c1 : c1;
     float* to = reinterpret_cast<float*>(&turn[tt][f / 4 * 2]) + f % 4;
     to[0] = cs * p.rope_scale;
     to[4] = sn * p.rope_scale;
