@@ -192,3 +192,16 @@ def test_angles_near_quarter_turns(api, interleaved):
     rel, angle = ref.BF16 + 8 * ref.F32, 2 * math.pi * 2.0 ** -28 + 2.0 ** -50
     assert ((cos - t.cos()).abs() <= rel * t.cos().abs() + angle * t.sin().abs()).all()
     assert ((sin - t.sin()).abs() <= rel * t.sin().abs() + angle * t.cos().abs()).all()
+
+
+def test_windows_past_32_bits(api):
+    """A window or first tokens of any size that Python holds."""
+    s = make([1, 40], [1500, 90], 8, 2, 128, 64, seed=9)
+    want = call(api, s)
+    for kw in (dict(window=2 ** 31), dict(window=2 ** 32 + 5), dict(window=2 ** 63),
+               dict(window=9, sink=2 ** 32 + 1), dict(window=9, sink=2 ** 40)):
+        got = call(api, s, **kw)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), kw
+    for kw in (dict(window=-1), dict(window=-2 ** 32), dict(window=9, sink=-2 ** 40)):
+        with pytest.raises(api.DSAError):
+            call(api, s, **kw)

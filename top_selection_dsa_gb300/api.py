@@ -806,6 +806,13 @@ def rope_turns(freq, device="cuda"):
 # whether everything is as it should be, and only where it is not (or a case that
 # it leaves out) the checks above are gone through, which name what is wrong.
 _BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+_MOST_INT = 2 ** 31 - 1
+
+
+def _to_int32(n):
+    """A count for a 32-bit argument, which ctypes would cut without a word: the
+    largest one past it, -1 (which the library refuses) below 0."""
+    return min(max(n, -1), _MOST_INT)
 
 
 def _dense(t, dtype, index):
@@ -1000,8 +1007,10 @@ def kv_attention(q, k_cache, v_cache, block_table, context_lens, query_starts, *
     _call(dev, lib.dsa_kv_attention, "dsa_kv_attention", q.data_ptr(), qs, k_cache.data_ptr(),
           v_cache.data_ptr(), nb, block_table.data_ptr(), max_blocks, context_lens.data_ptr(),
           query_starts.data_ptr(), T, B, bs, Hq, hkv, D,
-          D ** -0.5 if softmax_scale is None else softmax_scale, window, sink, out.data_ptr(),
-          lse.data_ptr(), ws.data_ptr(), nbytes)
+          D ** -0.5 if softmax_scale is None else softmax_scale,
+          window if -1 <= window <= _MOST_INT else _to_int32(window),
+          sink if -1 <= sink <= _MOST_INT else _to_int32(sink), out.data_ptr(), lse.data_ptr(),
+          ws.data_ptr(), nbytes)
     return out, lse
 
 
