@@ -675,8 +675,8 @@ dsa_status_t dsa_kv_append(const void* k, int64_t k_stride, const void* v, int64
  *                 current device), 256-byte aligned.  Calls that may overlap
  *                 need one each.
  *   B <= 2048, max_blocks * block_size < 2^30, T < 2^30 (else
- *   DSA_ERR_UNSUPPORTED; also where (T Hq / (256 Hkv) + B) times the tiles of
- *   128 keys of the longest context pass 2^30)
+ *   DSA_ERR_UNSUPPORTED; also where (floor(T / 2r) + B) (ceil(max_blocks * block_size
+ *   / 128) + 3) reaches 2^30, with r = floor(128 Hkv / Hq))
  * Products run on the tensor cores on the bf16 inputs with fp32 accumulation;
  * the weights exp(S - max) are rounded to bf16 for the second one (2^-8 relative),
  * their sum and the maximum are fp32.  A row's weights are divided by their sum at

@@ -2,7 +2,24 @@
 import pytest
 import torch
 
-from test_kv16_abi_host import api  # noqa: F401  (fixture)
+from test_kv16_abi_host import NUL, api, attend  # noqa: F401  (api: fixture)
+
+
+@pytest.mark.parametrize("G", [1, 4, 5, 65, 128])
+def test_most_work_of_a_call(api, G):
+    """(T / (2 floor(128 / G)) + B) (tiles + 3) < 2^30, tiles = the longest
+    context's of 128 keys."""
+    tiles = (1 << 22) * 64 // 128
+    fits = (1 << 30) // (tiles + 3)                      # row tiles
+    fits -= fits * (tiles + 3) == 1 << 30
+    per = 2 * (128 // G)
+    T = (fits - 2) * per
+    assert (T // per + 2) * (tiles + 3) < 1 << 30 <= (T // per + 3) * (tiles + 3)
+    kw = dict(Hq=G, Hkv=1, qs=G * 128, mb=1 << 22, bs=64, B=2)
+    # no workspace: refused for that, behind the limit's check
+    assert attend(api, T=T, ws=NUL, **kw) == api.DSA_ERR_INVALID_ARG
+    assert attend(api, T=T + per - 1, ws=NUL, **kw) == api.DSA_ERR_INVALID_ARG
+    assert attend(api, T=T + per, ws=NUL, **kw) == api.DSA_ERR_UNSUPPORTED
 
 
 def test_workspace_of_the_wrong_kind_is_refused(api):
