@@ -39,3 +39,12 @@ def test_workspace_of_the_wrong_kind_is_refused(api):
         api._workspace(500, host, torch.empty(499, dtype=torch.uint8))
     ok = torch.empty(125, dtype=torch.float32)
     assert api._workspace(500, host, ok) is ok
+
+
+def test_contexts_that_no_element_turns_in(api):
+    """An original context so short that even the first element turns less than
+    beta_slow times: all are divided."""
+    freq, _ = api.rope_frequencies(64, 1e4)
+    for kw in (dict(original_context=4), dict(original_context=60, beta_slow=10.0)):
+        yarn, _ = api.rope_frequencies(64, 1e4, scaling="yarn", factor=8.0, **kw)
+        assert torch.allclose(yarn, freq / 8, rtol=1e-14), kw

@@ -779,6 +779,8 @@ def rope_frequencies(rotary, base=10000.0, *, factor=1.0, scaling=None, original
     def element(turns):  # the (real) i that turns so often within original_context
         return rotary * math.log(original_context / (2 * math.pi * turns)) / (2 * math.log(base))
 
+    if element(beta_slow) < 0:  # all turn less often
+        return freq / factor, 0.1 * math.log(factor) + 1.0
     lo = max(math.floor(element(beta_fast)), 0)
     hi = min(math.ceil(element(beta_slow)), rotary - 1)
     ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
