@@ -1,4 +1,6 @@
 """Limits of the 16-bit cache's calls and the tables they read, on the CPU."""
+import math
+
 import pytest
 import torch
 
@@ -39,6 +41,29 @@ def test_workspace_of_the_wrong_kind_is_refused(api):
         api._workspace(500, host, torch.empty(499, dtype=torch.uint8))
     ok = torch.empty(125, dtype=torch.float32)
     assert api._workspace(500, host, ok) is ok
+
+
+def test_stretched_frequencies_between_the_ends(api):
+    """Every element from the formula, written out."""
+    for rotary, base, factor, ctx, fast, slow in ((64, 1e4, 40.0, 4096, 32, 1),
+                                                  (128, 1e6, 4.0, 32768, 32, 1),
+                                                  (16, 5e5, 8.0, 8192, 20, 2)):
+        freq, m = api.rope_frequencies(rotary, base, scaling="yarn", factor=factor,
+                                       original_context=ctx, beta_fast=fast, beta_slow=slow)
+
+        def at(turns):   # base^(-2 i / rotary) ctx / (2 pi) = turns, solved for i
+            return rotary / 2 * math.log(ctx / (2 * math.pi * turns), base)
+
+        lo, hi = math.floor(at(fast)), math.ceil(at(slow))
+        between = 0
+        for i in range(rotary // 2):
+            f = base ** (-2 * i / rotary)
+            share = min(max((i - lo) / (hi - lo), 0), 1)      # of the divided one
+            between += 0 < share < 1
+            want = f * (1 - share) + f / factor * share
+            assert abs(freq[i].item() - want) <= 1e-13 * want, (rotary, i)
+        # the ramp is rotary / 2 log(fast / slow) / log(base) wide: 1.4 elements at least
+        assert between >= 1 and abs(m - (1 + math.log(factor) / 10)) < 1e-15
 
 
 def test_contexts_that_no_element_turns_in(api):
