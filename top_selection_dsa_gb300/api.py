@@ -979,7 +979,11 @@ def kv_attention(q, k_cache, v_cache, block_table, context_lens, query_starts, *
     its context of context_lens[b].  Each sees the keys up to its own position;
     with a window, the last `window` of them and the first `sink`; the table's
     entries of pages that none of them sees may hold anything.  Returns
-    (out [T, Hq, D], lse [T, Hq] fp32).  softmax_scale defaults to D^-0.5."""
+    (out [T, Hq, D], lse [T, Hq] fp32).  softmax_scale defaults to D^-0.5.
+
+    Rows of no request (padding behind query_starts[B]; all of them without
+    requests) are not written: they hold what `out` and `lse` held, and nothing
+    in particular where the call makes these."""
     dev = q.device
     nb, hkv, bs, D = _kv_shape(k_cache, v_cache, dev)
     shape, qs = _rows_of(q, "q", dev)
