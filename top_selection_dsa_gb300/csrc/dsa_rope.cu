@@ -21,7 +21,7 @@
 // lanes.  A warp's task is some rows of one token and kind, all loaded at once,
 // and the products of weights, cosines and sines are made once for it.
 //
-// The pass is memory-bound: 16384 tokens of 64 + 8 heads of 128 with norms 98 us,
+// The pass is memory-bound: 16384 tokens of 64 + 8 heads of 128 with norms 99 us,
 // 6.1 TB/s (92 % of the measured copy bandwidth, 71 % of the issue slots); index
 // queries and key, 8191 tokens of 64 + 1 heads, half of them rotated, 45 us, 6.0;
 // 32768 tokens appended, 48 us, 5.6.  With pairs across lanes and heads stepped
